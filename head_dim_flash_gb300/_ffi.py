@@ -34,6 +34,13 @@ EXPORTS = (
     "ffpa_fwd_fp8_quantized",
     "ffpa_varlen_fp8_workspace_bytes",
     "ffpa_varlen_fwd_fp8",
+    "ffpa_kv4_cache_bytes",
+    "ffpa_kv4_write",
+    "ffpa_varlen_kv4_write",
+    "ffpa_kv4_read",
+    "ffpa_varlen_kv4_read",
+    "ffpa_decode_kv4_workspace_bytes",
+    "ffpa_decode_fwd_kv4",
     "ffpa_bwd_stages",
     "ffpa_bwd_noalloc",
     "ffpa_varlen_fwd",
@@ -63,6 +70,13 @@ class View(ctypes.Structure):
 
     _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
                 ("stride_n", ctypes.c_int64)]
+
+
+class Kv4Cache(ctypes.Structure):
+    """``ffpa_kv4_cache``: a paged 4-bit K/V cache and its block table."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int), ("block_stride", ctypes.c_int64)]
 
 
 def _declare(lib):
@@ -96,6 +110,20 @@ def _declare(lib):
     lib.ffpa_decode_workspace_bytes.restype = _sz
     lib.ffpa_decode_fwd.argtypes = [_i, View, View, View, View, _p, _p, _sz, _i, _i, _i, _i, _i, _i, _i, _f, _p]
     lib.ffpa_decode_fwd.restype = _i
+    lib.ffpa_kv4_cache_bytes.argtypes = [_i, _i, _i, _i]
+    lib.ffpa_kv4_cache_bytes.restype = _sz
+    lib.ffpa_kv4_write.argtypes = [_i, View, View, Kv4Cache, _p, _p, _i, _i, _i, _i, _p]
+    lib.ffpa_kv4_write.restype = _i
+    lib.ffpa_varlen_kv4_write.argtypes = [_i, _p, _p, Kv4Cache, _p, _p, _i, _i, _i, _i, _i, _p]
+    lib.ffpa_varlen_kv4_write.restype = _i
+    lib.ffpa_kv4_read.argtypes = [_i, Kv4Cache, View, View, _p, _p, _i, _i, _i, _i, _p]
+    lib.ffpa_kv4_read.restype = _i
+    lib.ffpa_varlen_kv4_read.argtypes = [_i, Kv4Cache, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p]
+    lib.ffpa_varlen_kv4_read.restype = _i
+    lib.ffpa_decode_kv4_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i]
+    lib.ffpa_decode_kv4_workspace_bytes.restype = _sz
+    lib.ffpa_decode_fwd_kv4.argtypes = [_i, View, Kv4Cache, _p, View, _p, _p, _sz, _i, _i, _i, _i, _i, _i, _f, _p]
+    lib.ffpa_decode_fwd_kv4.restype = _i
     lib.ffpa_bwd_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i]
     lib.ffpa_bwd_workspace_bytes.restype = _sz
     lib.ffpa_bwd.argtypes = [_i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _i, _i, _i, _i, _i, _i, _i, _f, _p]
@@ -222,6 +250,34 @@ def ffpa_decode_workspace_bytes(*args):
 
 def ffpa_decode_fwd(*args):
     return load().ffpa_decode_fwd(*args)
+
+
+def ffpa_kv4_cache_bytes(*args):
+    return load().ffpa_kv4_cache_bytes(*args)
+
+
+def ffpa_kv4_write(*args):
+    return load().ffpa_kv4_write(*args)
+
+
+def ffpa_varlen_kv4_write(*args):
+    return load().ffpa_varlen_kv4_write(*args)
+
+
+def ffpa_kv4_read(*args):
+    return load().ffpa_kv4_read(*args)
+
+
+def ffpa_varlen_kv4_read(*args):
+    return load().ffpa_varlen_kv4_read(*args)
+
+
+def ffpa_decode_kv4_workspace_bytes(*args):
+    return load().ffpa_decode_kv4_workspace_bytes(*args)
+
+
+def ffpa_decode_fwd_kv4(*args):
+    return load().ffpa_decode_fwd_kv4(*args)
 
 
 def ffpa_bwd_workspace_bytes(*args):

@@ -447,6 +447,178 @@ def varlen_attention(q, k, v, cu_seqlens_q, cu_seqlens_k=None, max_seqlen_q=None
     return (o, lse) if return_lse else o
 
 
+# ----------------------------------------------------------------- 4-bit K/V cache
+KV4_TILE = 576  # bytes of a cache tile: 16 tokens x 64 head dims, 512 of codes and 64 of scales
+
+
+def kv4_cache(num_pages: int, page_size: int, Hkv: int, D: int, device="cuda") -> torch.Tensor:
+    """A zeroed paged 4-bit K/V cache (ffpa_kv4_cache in include/ffpa.h): uint8
+    [num_pages, 2 (K, V), Hkv, page_size / 16, D / 64, 576]. page_size is a multiple
+    of 16 (tokens per page), D a multiple of 64 in [64, 1024]."""
+    if page_size <= 0 or page_size % 16 != 0:
+        raise ValueError(f"page_size {page_size} must be a positive multiple of 16")
+    if D % 64 != 0 or not 64 <= D <= 1024:
+        raise NotImplementedError(f"head dim {D}: the 4-bit cache takes multiples of 64 in [64, 1024]")
+    return torch.zeros((num_pages, 2, Hkv, page_size // 16, D // 64, KV4_TILE), dtype=torch.uint8, device=device)
+
+
+def _kv4(cache, block_table, B: int):
+    """The ffpa_kv4_cache of a cache tensor and a block table [B, max_blocks], with Hkv and D."""
+    if cache.dtype != torch.uint8 or cache.dim() != 6 or cache.shape[1] != 2 or cache.shape[5] != KV4_TILE:
+        raise ValueError(f"expected a cache of kv4_cache(), got {cache.dtype} {tuple(cache.shape)}")
+    if not cache.is_cuda or not cache.is_contiguous():
+        raise ValueError("the cache must be a contiguous tensor on a CUDA device")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"expected an int32 block_table [{B}, max_blocks], got {block_table.dtype} "
+                         f"{tuple(block_table.shape)}")
+    if block_table.device != cache.device:
+        raise ValueError("block_table and cache are on different devices")
+    blocks = block_table.shape[1]
+    if blocks > 1 and block_table.stride(1) != 1 or B > 1 and block_table.stride(0) < blocks:
+        raise ValueError(f"block_table's rows must be contiguous, got strides {block_table.stride()}")
+    stride = block_table.stride(0) if B > 1 else blocks
+    pages, _, Hkv, strips, chunks, _ = cache.shape
+    return _ffi.Kv4Cache(cache.data_ptr(), pages, 16 * strips, block_table.data_ptr(), blocks, stride), Hkv, 64 * chunks
+
+
+def _lengths(x, n: int, name: str, device) -> int | None:
+    """The address of an optional int32 [n] tensor of lengths on `device`."""
+    if x is None:
+        return None
+    if x.dtype != torch.int32 or tuple(x.shape) != (n,) or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on {device}, got {x.dtype} "
+                         f"{tuple(x.shape)} on {x.device}")
+    return x.data_ptr()
+
+
+def _kv4_pair(cache, k, v, dims: int, Hkv: int, D: int):
+    if k.dim() != dims or v.shape != k.shape or k.shape[1] != Hkv or k.shape[-1] != D:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not match a cache of Hkv={Hkv}, D={D}")
+    if k.device != cache.device or v.device != cache.device:
+        raise ValueError("k, v and the cache must be on one device")
+    if k.dtype != v.dtype:
+        raise ValueError(f"mixed dtypes {k.dtype} and {v.dtype}")
+
+
+def _stream_of(x: torch.Tensor) -> int:
+    return torch.cuda.current_stream(x.device).cuda_stream
+
+
+def kv4_write(cache, block_table, k, v, start=None, count=None) -> None:
+    """Quantises new tokens into the cache through ffpa_kv4_write (views, no copy):
+    row i of sequence b becomes cached token start[b] + i, for i < count[b].
+
+    k, v: [B, Hkv, N, D]; block_table: int32 [B, max_blocks]; start, count: int32 [B]
+    on the device (None: 0 and N)."""
+    B = k.shape[0]
+    c, Hkv, D = _kv4(cache, block_table, B)
+    _kv4_pair(cache, k, v, 4, Hkv, D)
+    k, v = _dense(k, v)
+    with torch.cuda.device(cache.device):
+        st = _ffi.ffpa_kv4_write(_dt(k), _view(k), _view(v), c, _lengths(start, B, "start", cache.device),
+                                 _lengths(count, B, "count", cache.device), B, Hkv, k.shape[2], D, _stream_of(cache))
+    _ffi.raise_for(st, "ffpa_kv4_write")
+
+
+def varlen_kv4_write(cache, block_table, k, v, cu_seqlens, max_seqlen: int, start=None) -> None:
+    """As kv4_write, for a packed batch: k, v [T, Hkv, D], sequence b's tokens the rows
+    [cu_seqlens[b], cu_seqlens[b + 1]) (int32 on the device), at most max_seqlen of them."""
+    B = cu_seqlens.numel() - 1
+    c, Hkv, D = _kv4(cache, block_table, B)
+    _kv4_pair(cache, k, v, 3, Hkv, D)
+    k, v = _prep(k, v)
+    with torch.cuda.device(cache.device):
+        st = _ffi.ffpa_varlen_kv4_write(_dt(k), k.data_ptr(), v.data_ptr(), c,
+                                        _lengths(cu_seqlens, B + 1, "cu_seqlens", cache.device),
+                                        _lengths(start, B, "start", cache.device), B, k.shape[0], int(max_seqlen), Hkv,
+                                        D, _stream_of(cache))
+    _ffi.raise_for(st, "ffpa_varlen_kv4_write")
+
+
+def kv4_read(cache, block_table, count, max_count: int | None = None, dtype=torch.bfloat16, start=None, k_out=None,
+             v_out=None):
+    """Reads cached tokens back through ffpa_kv4_read: token start[b] + i of sequence b to
+    row i, for i < count[b] (int32 [B] on the device). Returns (k, v) [B, Hkv, N, D].
+
+    With k_out and v_out given, N is theirs and rows at and past count[b] keep what they
+    hold; else N is max_count and those rows are zero."""
+    B = block_table.shape[0]
+    c, Hkv, D = _kv4(cache, block_table, B)
+    if (k_out is None) != (v_out is None) or (k_out is None) == (max_count is None):
+        raise ValueError("give either k_out and v_out or max_count")
+    if k_out is None:
+        k_out, v_out = (torch.zeros((B, Hkv, max_count, D), dtype=dtype, device=cache.device) for _ in range(2))
+    _kv4_pair(cache, k_out, v_out, 4, Hkv, D)
+    if k_out.shape[0] != B:
+        raise ValueError(f"k_out has {k_out.shape[0]} sequences, block_table {B}")
+    if count is None:
+        raise ValueError("count is required")
+    with torch.cuda.device(cache.device):
+        st = _ffi.ffpa_kv4_read(_dt(k_out), c, _view(k_out), _view(v_out), _lengths(start, B, "start", cache.device),
+                                _lengths(count, B, "count", cache.device), B, Hkv, k_out.shape[2], D,
+                                _stream_of(cache))
+    _ffi.raise_for(st, "ffpa_kv4_read")
+    return k_out, v_out
+
+
+def varlen_kv4_read(cache, block_table, cu_seqlens, max_seqlen: int, total: int | None = None, dtype=torch.bfloat16,
+                    start=None, k_out=None, v_out=None):
+    """As kv4_read, into packed tensors [T, Hkv, D] (what varlen_fwd takes as keys and
+    values): sequence b's tokens to the rows [cu_seqlens[b], cu_seqlens[b + 1]). T is
+    `total` or that of k_out and v_out."""
+    B = cu_seqlens.numel() - 1
+    c, Hkv, D = _kv4(cache, block_table, B)
+    if (k_out is None) != (v_out is None) or (k_out is None) == (total is None):
+        raise ValueError("give either k_out and v_out or total")
+    if k_out is None:
+        k_out, v_out = (torch.zeros((total, Hkv, D), dtype=dtype, device=cache.device) for _ in range(2))
+    _kv4_pair(cache, k_out, v_out, 3, Hkv, D)
+    if not k_out.is_contiguous() or not v_out.is_contiguous():
+        raise ValueError("k_out and v_out must be contiguous")
+    with torch.cuda.device(cache.device):
+        st = _ffi.ffpa_varlen_kv4_read(_dt(k_out), c, k_out.data_ptr(), v_out.data_ptr(),
+                                       _lengths(cu_seqlens, B + 1, "cu_seqlens", cache.device),
+                                       _lengths(start, B, "start", cache.device), B, k_out.shape[0], int(max_seqlen),
+                                       Hkv, D, _stream_of(cache))
+    _ffi.raise_for(st, "ffpa_varlen_kv4_read")
+    return k_out, v_out
+
+
+def decode_fwd_kv4(q, cache, block_table, seq_lens, causal: bool = False, scale: float | None = None, out=None,
+                   lse=None, workspace=None):
+    """Decode / short-query forward over the 4-bit cache through ffpa_decode_fwd_kv4: the
+    keys and values of sequence b are its first seq_lens[b] cached tokens (int32 [B] on
+    the device); causal is bottom-right per sequence. q [B, Hq, Nq, D]; returns (o, lse).
+
+    A long chunk of queries goes through varlen_kv4_read and varlen_fwd instead."""
+    if q.dim() != 4:
+        raise ValueError("expected q [B,Hq,Nq,D]")
+    B, Hq, Nq, D = q.shape
+    c, Hkv, Dc = _kv4(cache, block_table, B)
+    if D != Dc:
+        raise ValueError(f"q has head dim {D}, the cache {Dc}")
+    if q.device != cache.device:
+        raise ValueError("q and the cache are on different devices")
+    if seq_lens is None:
+        raise ValueError("seq_lens is required")
+    (q,) = _dense(q)
+    o = _out_like(q) if out is None else out
+    l = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
+    if o.shape != q.shape or o.dtype != q.dtype or o.device != q.device:
+        raise ValueError("out must have q's shape, dtype and device")
+    if not l.is_contiguous() or l.dtype != torch.float32 or l.shape != q.shape[:3] or l.device != q.device:
+        raise ValueError("lse must be a contiguous fp32 [B, Hq, Nq] tensor")
+    with torch.cuda.device(q.device):
+        if workspace is None:
+            n = int(_ffi.ffpa_decode_kv4_workspace_bytes(_dt(q), B, Hq, Hkv, Nq, D))
+            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+        st = _ffi.ffpa_decode_fwd_kv4(_dt(q), _view(q), c, _lengths(seq_lens, B, "seq_lens", q.device), _view(o),
+                                      l.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                      B, Hq, Hkv, Nq, D, int(bool(causal)), _scale(scale, D), _stream_of(q))
+    _ffi.raise_for(st, "ffpa_decode_fwd_kv4")
+    return o, l
+
+
 def get_status() -> None:
     """Synchronises the current stream and raises if a kernel reported a device time-out."""
     _ffi.raise_for(_ffi.ffpa_get_status(_stream()), "device status")

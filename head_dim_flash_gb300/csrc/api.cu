@@ -614,6 +614,157 @@ ffpa_status ffpa_varlen_fwd_fp8(ffpa_dtype dt, const void* q, const void* k, con
                          "fp8 varlen launch");
 }
 
+size_t ffpa_kv4_cache_bytes(int num_pages, int page_size, int Hkv, int D)
+{
+    if (num_pages < 0 || page_size <= 0 || page_size % 16 != 0 || Hkv < 0 || D < 64 || D > 1024 || D % 64 != 0) return 0;
+    return static_cast<size_t>(num_pages) * 2 * Hkv * (page_size / 16) * (D / 64) * ffpa::kKv4Tile;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Validation shared by the entry points over the 4-bit cache (`used`: the call reaches it).
+ffpa_status check_kv4_cache(const ffpa_kv4_cache& c, bool used, int Hkv, int D, ffpa::Kv4Cache* out)
+{
+    if (D % 64 != 0) return fail(FFPA_ERR_NOT_SUPPORTED, "4-bit cache: D=%d must be a multiple of 64", D);
+    if (c.page_size <= 0 || c.page_size % 16 != 0)
+        return fail(FFPA_ERR_INVALID_VALUE, "page_size=%d must be a positive multiple of 16", c.page_size);
+    if (c.num_pages < 0 || c.max_blocks < 0) return fail(FFPA_ERR_INVALID_VALUE, "negative num_pages or max_blocks");
+    if (c.block_stride < c.max_blocks)
+        return fail(FFPA_ERR_INVALID_VALUE, "block_stride=%lld is below max_blocks=%d", (long long)c.block_stride,
+                    c.max_blocks);
+    FFPA_TRY(check_ptr(c.data, used && c.num_pages > 0 && Hkv > 0, "cache data"));
+    if (used && c.max_blocks > 0 && !c.block_table) return fail(FFPA_ERR_INVALID_VALUE, "block_table is NULL");
+    if (reinterpret_cast<uintptr_t>(c.block_table) & 3u)
+        return fail(FFPA_ERR_INVALID_VALUE, "block_table must be 4-byte aligned");
+    out->data = static_cast<uint8_t*>(c.data);
+    out->num_pages = c.num_pages;
+    out->page_size = c.page_size;
+    out->table = c.block_table;
+    out->max_blocks = c.max_blocks;
+    out->table_stride = c.block_stride;
+    return FFPA_OK;
+}
+
+// Writes (read = false) or reads a batch; dense with views, packed with cu_seqlens.
+ffpa_status run_kv4_io(bool read, ffpa_dtype dt, const ffpa_view& k, const ffpa_view& v, const ffpa_kv4_cache& cache,
+                       const int* start, const int* count, const int* cu, int B, int total, int Hkv, int N, int D,
+                       ffpa_stream_t stream)
+{
+    FFPA_TRY(check_common(dt, Hkv, Hkv, D, 1.f));
+    if (B < 0 || N < 0 || total < 0) return fail(FFPA_ERR_INVALID_VALUE, "negative size B=%d N=%d total=%d", B, N, total);
+    if (static_cast<long long>(B) * Hkv > kMaxUnits)
+        return fail(FFPA_ERR_NOT_SUPPORTED, "B*Hkv=%lld exceeds the launch grid's %lld units", (long long)B * Hkv,
+                    kMaxUnits);
+    ffpa::Kv4Io a{};
+    const bool any = B > 0 && Hkv > 0 && N > 0 && (!cu || total > 0);
+    FFPA_TRY(check_kv4_cache(cache, any, Hkv, D, &a.cache));
+    if ((reinterpret_cast<uintptr_t>(start) & 3u) || (reinterpret_cast<uintptr_t>(count) & 3u) ||
+        (reinterpret_cast<uintptr_t>(cu) & 3u))
+        return fail(FFPA_ERR_INVALID_VALUE, "start, count and cu_seqlens must be 4-byte aligned");
+    const int ext_b = cu ? 1 : B, ext_n = cu ? total : N;
+    FFPA_TRY(check_view(k, any, "k", ext_b, Hkv, ext_n));
+    FFPA_TRY(check_view(v, any, "v", ext_b, Hkv, ext_n));
+    if (!any) return ok();
+    ffpa::DeviceCtl ctl;
+    FFPA_TRY(device_ctl(&ctl));
+    a.bf16 = dt == FFPA_BF16;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.N = N;
+    a.D = D;
+    a.k = k.data;
+    a.v = v.data;
+    a.vk = to_view(k);
+    a.vv = to_view(v);
+    a.start = start;
+    a.count = count;
+    a.cu = cu;
+    a.total = total;
+    a.status = ctl.status;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return read ? launch_result(ffpa::launch_kv4_read(a, s), "4-bit cache read launch")
+                : launch_result(ffpa::launch_kv4_write(a, s), "4-bit cache write launch");
+}
+
+ffpa_view packed_rows(void* p, int Hkv, int D) { return ffpa_view{p, 0, D, static_cast<int64_t>(Hkv) * D}; }
+
+}  // namespace
+
+extern "C" {
+
+ffpa_status ffpa_kv4_write(ffpa_dtype dt, ffpa_view k, ffpa_view v, ffpa_kv4_cache cache, const int* start,
+                           const int* count, int B, int Hkv, int N, int D, ffpa_stream_t stream)
+{
+    return run_kv4_io(false, dt, k, v, cache, start, count, nullptr, B, 0, Hkv, N, D, stream);
+}
+
+ffpa_status ffpa_kv4_read(ffpa_dtype dt, ffpa_kv4_cache cache, ffpa_view k, ffpa_view v, const int* start,
+                          const int* count, int B, int Hkv, int N, int D, ffpa_stream_t stream)
+{
+    return run_kv4_io(true, dt, k, v, cache, start, count, nullptr, B, 0, Hkv, N, D, stream);
+}
+
+ffpa_status ffpa_varlen_kv4_write(ffpa_dtype dt, const void* k, const void* v, ffpa_kv4_cache cache,
+                                  const int* cu_seqlens, const int* start, int batch, int total, int max_seqlen,
+                                  int Hkv, int D, ffpa_stream_t stream)
+{
+    if (batch > 0 && !cu_seqlens) return fail(FFPA_ERR_INVALID_VALUE, "cu_seqlens is NULL");
+    return run_kv4_io(false, dt, packed_rows(const_cast<void*>(k), Hkv, D), packed_rows(const_cast<void*>(v), Hkv, D),
+                      cache, start, nullptr, cu_seqlens, batch, total, Hkv, max_seqlen, D, stream);
+}
+
+ffpa_status ffpa_varlen_kv4_read(ffpa_dtype dt, ffpa_kv4_cache cache, void* k, void* v, const int* cu_seqlens,
+                                 const int* start, int batch, int total, int max_seqlen, int Hkv, int D,
+                                 ffpa_stream_t stream)
+{
+    if (batch > 0 && !cu_seqlens) return fail(FFPA_ERR_INVALID_VALUE, "cu_seqlens is NULL");
+    return run_kv4_io(true, dt, packed_rows(k, Hkv, D), packed_rows(v, Hkv, D), cache, start, nullptr, cu_seqlens,
+                      batch, total, Hkv, max_seqlen, D, stream);
+}
+
+size_t ffpa_decode_kv4_workspace_bytes(ffpa_dtype, int B, int Hq, int Hkv, int Nq, int D)
+{
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Nq <= 0 || D <= 0 || Hq % Hkv != 0) return 0;
+    return ffpa::kv4_decode_workspace_bytes(dense_problem(B, Hq, Hkv, Nq, 0, D, 0, 1.f));
+}
+
+ffpa_status ffpa_decode_fwd_kv4(ffpa_dtype dt, ffpa_view q, ffpa_kv4_cache cache, const int* seq_lens, ffpa_view o,
+                                float* lse, void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq,
+                                int D, int causal, float scale, ffpa_stream_t stream)
+{
+    FFPA_TRY(check_common(dt, Hq, Hkv, D, scale));
+    FFPA_TRY(check_dense_sizes(B, Hq, Nq, 0));
+    const long q_rows = static_cast<long>(B) * Hq * Nq;
+    if (q_rows > INT_MAX) return fail(FFPA_ERR_NOT_SUPPORTED, "B*Hq*Nq=%ld exceeds 2^31 - 1 query rows", q_rows);
+    ffpa::Kv4Decode a{};
+    FFPA_TRY(check_kv4_cache(cache, q_rows > 0, Hkv, D, &a.cache));
+    FFPA_TRY(check_view(q, q_rows > 0, "q", B, Hq, Nq));
+    FFPA_TRY(check_view(o, q_rows > 0, "o", B, Hq, Nq));
+    FFPA_TRY(check_ptr(lse, q_rows > 0, "lse"));
+    if (q_rows > 0 && !seq_lens) return fail(FFPA_ERR_INVALID_VALUE, "seq_lens is NULL");
+    if (reinterpret_cast<uintptr_t>(seq_lens) & 3u) return fail(FFPA_ERR_INVALID_VALUE, "seq_lens must be 4-byte aligned");
+    if (q_rows == 0) return ok();
+    ffpa::Problem pb = dense_problem(B, Hq, Hkv, Nq, 0, D, causal, scale);
+    pb.vq = to_view(q);
+    pb.vo = to_view(o);
+    const size_t need = ffpa::kv4_decode_workspace_bytes(pb);
+    if (workspace_bytes < need)
+        return fail(FFPA_ERR_INVALID_VALUE, "decode workspace too small: %zu < %zu bytes", workspace_bytes, need);
+    if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return fail(FFPA_ERR_INVALID_VALUE, "decode workspace must be non-NULL and 256-byte aligned");
+    a.f.pb = pb;
+    FFPA_TRY(device_ctl(&a.f.ctl));
+    a.f.bf16 = dt == FFPA_BF16;
+    a.f.q = q.data;
+    a.f.o = o.data;
+    a.f.lse = lse;
+    a.seq_lens = seq_lens;
+    return launch_result(ffpa::launch_decode_kv4(a, workspace, reinterpret_cast<cudaStream_t>(stream)),
+                         "4-bit decode launch");
+}
+
 size_t ffpa_bwd_workspace_bytes_ds(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int Nkv, int D, int causal)
 {
     const size_t small = ffpa_bwd_workspace_bytes(dt, B, Hq, Hkv, Nq, Nkv, D);
@@ -769,6 +920,13 @@ ffpa_status ffpa_get_status(ffpa_stream_t stream)
     cudaMemcpyToSymbol(g_ffpa_status_word, &zero, sizeof(zero));
     if ((word & 0xffu) == ffpa::DEV_TIMEOUT)
         return fail(FFPA_ERR_TIMEOUT, "a device wait timed out (site %u, block %u)", (word >> 8) & 0xffu, word >> 16);
+    const uint32_t site = (word >> 8) & 0xffu;
+    if ((word & 0xffu) == ffpa::DEV_INVALID && site >= ffpa::VS_KV4_WRITE && site <= ffpa::VS_KV4_DECODE)
+        return fail(FFPA_ERR_INVALID_VALUE,
+                    "4-bit cache: sequence %u breaks the contract of its lengths and block table (a negative length or "
+                    "start, tokens past max_blocks * page_size or past the tensor's rows, or a page outside "
+                    "[0, num_pages)); the outputs of that call are undefined for it (site 0x%02x)",
+                    word >> 16, site);
     if ((word & 0xffu) == ffpa::DEV_INVALID)
         return fail(FFPA_ERR_INVALID_VALUE,
                     "packed sequence %u breaks the varlen contract: its cu_seqlens entries are negative, decrease or "

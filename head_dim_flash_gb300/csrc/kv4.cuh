@@ -1,0 +1,163 @@
+// The 4-bit K/V cache: its format, and the device code that every kernel over
+// it shares.
+//
+// A value is an e2m1 code times the scale of its group of 16 along the head
+// dim. The scale byte holds five exponent bits (bias 15) and three bits of
+// mantissa, that is, the eight bits behind the sign of a 16-bit float, so
+// scale byte << 7 IS the scale as fp16. A code has two significant bits and a
+// scale four: every cached value has at most six and is exact in fp16 and in
+// bf16 (the largest, 6 x 10240, and the smallest, 2^-18, are fp16 numbers).
+// The matrix products over the cache therefore run on exact operands.
+//
+// Layout: pages of page_size tokens (a multiple of 16), in each page
+// [2 (K, V)][Hkv][page_size / 16][D / 64] tiles of 16 tokens x 64 head dims.
+// A tile is 512 bytes of codes and 64 scale bytes, in the order in which the
+// lanes of a warp hold the A operand of mma.m16n8k16, so that a lane's four
+// matrix steps are one 16-byte load without any exchange. With lane =
+// 4 g + t:
+//   K (A rows = tokens, k = head dims): bytes 16 lane + 8 hi hold token
+//     g + 8 hi, head dims 16 t .. 16 t + 15 (one group); its scale is byte
+//     512 + 2 lane + hi;
+//   V (A = V^T: rows = head dims, k = tokens): bytes 16 lane + 4 j hold token
+//     2 t + (j & 1) + 8 (j >> 1), head dims 8 g .. 8 g + 7 (half a group); the
+//     scale of head dims 16 p .. 16 p + 15 is byte 512 + 16 p + 4 t + j.
+// The even head dim of a pair is in a byte's low nibble.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "kernels.h"
+#include "ptx.cuh"
+#include "tile_common.cuh"
+
+namespace ffpa {
+
+__device__ __forceinline__ void kv4_invalid(uint32_t* status, uint32_t site, int b)
+{
+    atomicCAS(status, 0u, DEV_INVALID | (site << 8) | ((static_cast<uint32_t>(b) & 0xffffu) << 16));
+}
+
+// Byte offset of the first tile of strip `strip` (16 tokens) of a page.
+__device__ __forceinline__ size_t kv4_strip_offset(const Kv4Cache& c, int Hkv, int chunks, int page, int kv, int h,
+                                                   int strip)
+{
+    const size_t strips = static_cast<size_t>(c.page_size >> 4);
+    return (((static_cast<size_t>(page) * 2 + kv) * Hkv + h) * strips + strip) * (static_cast<size_t>(chunks) * kKv4Tile);
+}
+
+// One byte of codes -> two fp16 values (low nibble in the low half).
+__device__ __forceinline__ void kv4_decode8(uint32_t w, uint32_t (&h)[4])
+{
+    asm("{\n"
+        " .reg .b8 a, b, c, d;\n"
+        " mov.b32 {a, b, c, d}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, a;\n"
+        " cvt.rn.f16x2.e2m1x2 %1, b;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, c;\n"
+        " cvt.rn.f16x2.e2m1x2 %3, d;\n"
+        "}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A scale byte (the low byte of s) as a pair of fp16 scales.
+__device__ __forceinline__ uint32_t kv4_scale2(uint32_t s)
+{
+    const uint32_t h = (s & 0xffu) << 7;
+    return h | (h << 16);
+}
+
+// Eight codes (four bytes) times their scale, as four fp16 pairs (exact).
+__device__ __forceinline__ void kv4_dequant8(uint32_t w, uint32_t scale2, uint32_t (&h)[4])
+{
+    kv4_decode8(w, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = hmul2_u32(h[i], scale2);
+}
+
+// Scale byte of a group whose largest magnitude is amax (not NaN; values past
+// 61440 = 6 x 10240, infinity among them, count as 61440, so that every cached
+// value is a finite fp16 number): amax / 6 rounded to nearest even to three
+// bits of mantissa, steps of 2^-17 below 2^-14. The division is correctly
+// rounded, and amax has at most 11 significant bits: a quotient that is not on
+// a border between two scales is further than 2^-12 of itself away from it, so
+// the fp32 quotient rounds as the exact one does.
+__device__ __forceinline__ uint32_t kv4_scale_code(float amax)
+{
+    const float v = __fdiv_rn(fminf(amax, 61440.f), 6.f);
+    if (v < 6.103515625e-05f) return static_cast<uint32_t>(__float2int_rn(v * 131072.f));  // 2^-14, 2^17
+    uint32_t u = __float_as_uint(v);
+    u += 0x7ffffu + ((u >> 20) & 1u);
+    return (u >> 20) - ((127u - 15u) << 3);
+}
+
+__device__ __forceinline__ float kv4_scale_value(uint32_t code)
+{
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(code << 7)));
+}
+
+// Codes of eight values (four bytes) from their products with 1 / scale. The quotient of an
+// input (at most 11 significant bits) by a scale (4 bits) either is a border
+// between two codes or is at least 2^-11 of itself away from it, while the
+// product with the rounded reciprocal is 2^-23 off: rounding it to 16 bits
+// puts it back on a border that it belongs on and moves it across none, so
+// the ties of the conversion (nearest even, saturating) are the exact ones.
+__device__ __forceinline__ float kv4_snap(float q)
+{
+    return __uint_as_float((__float_as_uint(q) + 0x80u) & ~0xffu);
+}
+
+__device__ __forceinline__ uint32_t kv4_code8(const float (&x)[8], float rcp)
+{
+    uint32_t r;
+    asm("{\n"
+        " .reg .b8 a, b, c, d;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        " mov.b32 %0, {a, b, c, d};\n"
+        "}\n"
+        : "=r"(r)
+        : "f"(kv4_snap(x[0] * rcp)), "f"(kv4_snap(x[1] * rcp)), "f"(kv4_snap(x[2] * rcp)), "f"(kv4_snap(x[3] * rcp)),
+          "f"(kv4_snap(x[4] * rcp)), "f"(kv4_snap(x[5] * rcp)), "f"(kv4_snap(x[6] * rcp)), "f"(kv4_snap(x[7] * rcp)));
+    return r;
+}
+
+// Sequence range [p0, p0 + cnt) of cache positions and its first row in the
+// 16-bit tensor, from the device arrays. A range outside the cache's blocks or
+// the tensor's rows records DEV_INVALID and is not processed.
+__device__ __forceinline__ bool kv4_range(const Kv4Io& a, int b, uint32_t site, int& p0, int& cnt, long long& row0)
+{
+    long long s = a.start ? a.start[b] : 0, n, r = 0;
+    bool ok;
+    if (a.cu) {
+        r = a.cu[b];
+        n = static_cast<long long>(a.cu[b + 1]) - r;
+        ok = r >= 0 && n >= 0 && n <= a.N && r + n <= a.total;
+    } else {
+        n = a.count ? a.count[b] : a.N;
+        ok = n >= 0 && n <= a.N;
+    }
+    ok = ok && s >= 0 && s + n <= static_cast<long long>(a.cache.max_blocks) * a.cache.page_size && s + n <= 0x7fffffffLL;
+    if (!ok) {
+        if (threadIdx.x == 0) kv4_invalid(a.status, site, b);
+        return false;
+    }
+    p0 = static_cast<int>(s);
+    cnt = static_cast<int>(n);
+    row0 = r;
+    return true;
+}
+
+}  // namespace ffpa

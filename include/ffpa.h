@@ -196,6 +196,106 @@ FFPA_API ffpa_status ffpa_varlen_fwd_fp8(ffpa_dtype dt, const void* q, const voi
                                          int Hkv, int D, int causal, float scale, void* workspace,
                                          size_t workspace_bytes, ffpa_stream_t stream);
 
+/*
+ * 4-bit K/V cache: new tokens are quantised as they are written, the cached
+ * tokens can be read back to 16 bits, and ffpa_decode_fwd_kv4 attends over
+ * the cache itself (an extension: the FFPA pages have no cache; its attention
+ * is ffpa_decode_fwd's operation on the cached values).
+ *
+ * Format: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) in
+ * groups of 16 along the head dim, with one scale byte per group: five
+ * exponent bits of bias 15 and three bits of mantissa, i.e. the eight bits
+ * behind the sign of a 16-bit float. 4.5 bits per value.
+ *   scale = amax / 6 rounded to nearest even, amax the group's largest
+ *           magnitude, at most 61440 (infinities saturate to +-61440);
+ *   code  = x / scale rounded to nearest even, saturating (0 for scale 0).
+ * A NaN is stored as zero. A cached value is scale x code exactly; it is
+ * exact in bf16 and in fp16. Groups whose amax is below 6 x 2^-14 lose
+ * precision, below 6 x 2^-18 they are zero.
+ *
+ * data: device memory of ffpa_kv4_cache_bytes() bytes, 16-byte aligned, as
+ *   [num_pages][2 (K, V)][Hkv][page_size / 16][D / 64][576]: tiles of 16 tokens
+ *   x 64 head dims, 512 bytes of codes, then 64 scale bytes. With s the
+ *   token's place among the 16, x the head dim's among the 64 (even head dims
+ *   in the low nibble):
+ *     K  code   byte ((s % 8) * 4 + x / 16) * 16 + (s / 8) * 8 + (x % 16) / 2
+ *        scale  byte 512 + (s % 8) * 8 + (x / 16) * 2 + s / 8
+ *     V  code   byte ((x / 8) * 4 + (s % 8) / 2) * 16 + (s / 8) * 8 + (s % 2) * 4 + (x % 8) / 2
+ *        scale  byte 512 + (x / 16) * 16 + ((s % 8) / 2) * 4 + (s / 8) * 2 + s % 2
+ * page_size: tokens per page, a positive multiple of 16. One large page per
+ *   sequence makes a contiguous cache.
+ * block_table: device int32, B rows of max_blocks entries, block_stride
+ *   entries apart: tokens [j page_size, (j + 1) page_size) of sequence b are
+ *   in page block_table[b * block_stride + j]. Entries past a sequence's last
+ *   token are not read. Sequences may share pages that no call writes.
+ *
+ * Lengths and block tables live on the device and are checked there: a
+ * sequence whose range is negative or passes max_blocks * page_size (or the
+ * stated tensor sizes), or that names a page outside [0, num_pages), records
+ * the error in the device status word (ffpa_get_status returns
+ * FFPA_ERR_INVALID_VALUE) and its outputs are undefined; nothing is read or
+ * written outside the caller's tensors.
+ *
+ * D: a multiple of 64 in [64, 1024] (else FFPA_ERR_NOT_SUPPORTED).
+ */
+typedef struct ffpa_kv4_cache {
+    void* data;
+    int num_pages, page_size;
+    const int* block_table;
+    int max_blocks;
+    int64_t block_stride;
+} ffpa_kv4_cache;
+
+/* Bytes of a cache's data (0 for sizes outside the format). */
+FFPA_API size_t ffpa_kv4_cache_bytes(int num_pages, int page_size, int Hkv, int D);
+
+/*
+ * Writes new tokens: token i of sequence b becomes cached token start[b] + i,
+ * for i < count[b]. Cells of other tokens keep what they hold. Two tokens of
+ * one call must not share a cell.
+ *   k, v: [B, Hkv, N, D] views, dtype dt; rows at and past count[b] are not read.
+ *   start, count: device int32 [B]; NULL start is 0, NULL count is N.
+ */
+FFPA_API ffpa_status ffpa_kv4_write(ffpa_dtype dt, ffpa_view k, ffpa_view v, ffpa_kv4_cache cache, const int* start,
+                                    const int* count, int B, int Hkv, int N, int D, ffpa_stream_t stream);
+/* The same for a packed batch: k, v [total, Hkv, D] contiguous, sequence b's
+ * tokens are rows [cu_seqlens[b], cu_seqlens[b + 1]) (device int32 [batch + 1]),
+ * at most max_seqlen of them (it sizes the launch). */
+FFPA_API ffpa_status ffpa_varlen_kv4_write(ffpa_dtype dt, const void* k, const void* v, ffpa_kv4_cache cache,
+                                           const int* cu_seqlens, const int* start, int batch, int total,
+                                           int max_seqlen, int Hkv, int D, ffpa_stream_t stream);
+
+/*
+ * Reads cached tokens back: token start[b] + i of sequence b to row i, for
+ * i < count[b]. Rows at and past count[b] keep what they hold. Arguments as
+ * for the writes; k and v are written. A packed result (with cu_seqlens) is
+ * what ffpa_varlen_fwd takes as its keys and values.
+ */
+FFPA_API ffpa_status ffpa_kv4_read(ffpa_dtype dt, ffpa_kv4_cache cache, ffpa_view k, ffpa_view v, const int* start,
+                                   const int* count, int B, int Hkv, int N, int D, ffpa_stream_t stream);
+FFPA_API ffpa_status ffpa_varlen_kv4_read(ffpa_dtype dt, ffpa_kv4_cache cache, void* k, void* v,
+                                          const int* cu_seqlens, const int* start, int batch, int total,
+                                          int max_seqlen, int Hkv, int D, ffpa_stream_t stream);
+
+/*
+ * Decode / short-query forward over the cache: ffpa_decode_fwd's operation
+ * with the keys and values of sequence b its first seq_lens[b] cached tokens
+ * (device int32 [B]). Causal is bottom-right per sequence: query row i sees
+ * cached token j iff j <= i + seq_lens[b] - Nq. A sequence of length 0, and any
+ * row with no legal key, gives O = 0 and LSE = -inf.
+ *   q, o: [B, Hq, Nq, D] views; lse: contiguous fp32 [B, Hq, Nq].
+ *   workspace: device scratch of at least ffpa_decode_kv4_workspace_bytes()
+ *   bytes, 256-byte aligned, sized on the current device; one call at a time
+ *   per workspace.
+ * Meant for few query rows per kv head (Hq / Hkv * Nq); for a long chunk of
+ * queries, ffpa_varlen_kv4_read and ffpa_varlen_fwd.
+ */
+FFPA_API size_t ffpa_decode_kv4_workspace_bytes(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int D);
+FFPA_API ffpa_status ffpa_decode_fwd_kv4(ffpa_dtype dt, ffpa_view q, ffpa_kv4_cache cache, const int* seq_lens,
+                                         ffpa_view o, float* lse, void* workspace, size_t workspace_bytes, int B,
+                                         int Hq, int Hkv, int Nq, int D, int causal, float scale,
+                                         ffpa_stream_t stream);
+
 /* Workspace bytes ffpa_bwd needs for this problem (fp32 row statistics). */
 FFPA_API size_t ffpa_bwd_workspace_bytes(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int Nkv, int D);
 /*
@@ -377,8 +477,9 @@ FFPA_API ffpa_status ffpa_varlen_bwd(ffpa_dtype dt, const void* q, const void* k
  * Synchronises `stream`, then reports and clears the device status word:
  * FFPA_OK, FFPA_ERR_TIMEOUT (a bounded device wait ran out; the kernel
  * returned early and its outputs are undefined), FFPA_ERR_INVALID_VALUE (a
- * packed varlen sequence broke the cu_seqlens / max_seqlen contract; see
- * ffpa_varlen_fwd) or FFPA_ERR_CUDA (the stream reported an error).
+ * packed varlen sequence broke the cu_seqlens / max_seqlen contract, see
+ * ffpa_varlen_fwd, or a sequence of a 4-bit cache the contract of its lengths
+ * and block table, see ffpa_kv4_cache) or FFPA_ERR_CUDA (the stream reported an error).
  */
 FFPA_API ffpa_status ffpa_get_status(ffpa_stream_t stream);
 
