@@ -11,40 +11,43 @@
 //     The tiles are stored in A-fragment order, so a lane dequantises its own
 //     16 bytes (cvt.e2m1x2 and one fp16 product per pair, both exact) into the
 //     fragments of four matrix steps, with no ldmatrix and no 16-bit copy of the
-//     cache in shared memory. The operands of both products are fp16 for either
-//     element type: cached values and (power-of-two scaled) queries are exact.
-//   - a group of C warps owns a strip of tokens, each warp up to four 64-wide
-//     head-dim chunks of it: partial scores are exchanged through shared memory
-//     (none when C = 1), the softmax is computed by every warp, and O^T stays in
-//     registers. NG groups per CTA work on different strips; one CTA per SM.
-//   - strips arrive by bulk copies into a K ring and a V ring per group. The
-//     group's one barrier per step (after the exchange) also frees the K stage of
-//     the step and the V stage of the one before, so that every copy has a whole
-//     step to arrive.
+//     cache in shared memory. V's pairs run along tokens: the nibbles of two
+//     tokens are interleaved before the conversion, which costs half of what
+//     exchanging the converted halves would. The operands of both products are
+//     fp16 for either element type: cached values and (power-of-two scaled)
+//     queries are exact.
+//   - a group of C warps works on a strip of tokens, each warp on up to four
+//     64-wide head-dim chunks of it: partial scores are exchanged through shared
+//     memory (none when C = 1), the softmax is computed by every warp, and O^T
+//     stays in registers. One CTA per SM holds NG groups.
+//   - a producer warp, one lane per group, streams the strips by bulk copies into
+//     a K ring and a V ring per group.
 //   - the softmax keeps a reference instead of the running maximum: it moves (and
 //     O is rescaled) only when a score passes it by 2^14, so that the usual step
 //     is one vote. P <= 2^14 and its row's largest is >= 2^6 in fp16.
 //   - the strips of all (sequence, kv head, row block) units form one line, cut
-//     into equal ranges, one per CTA: lengths live on the device, so the cut is
-//     made there. A unit that a range covers alone is finished by its CTA, the
-//     parts of others go to the workspace (two at most per CTA) and a second
-//     kernel joins them in a fixed order. It is launched as a dependent, so its
-//     start overlaps the first kernel.
+//     into equal ranges, one per group: lengths live on the device, so the cut is
+//     made there. A unit counts kUnitCost strips more than it has, for its start
+//     and end. A group that covers a unit alone writes its outputs; parts of
+//     others go to the workspace, those that the groups of a CTA end with joined
+//     there first, and a second kernel joins the parts in a fixed order. It is
+//     launched as a dependent, so its start overlaps the first kernel.
 #include "kv4.cuh"
 
 namespace ffpa {
 namespace {
 
-constexpr int kMaxWarps = 10;      // per CTA: up to 200 registers each
-constexpr int kThreads = kMaxWarps * 32;
+constexpr int kComputeWarps = 11;  // at most, and one producer warp: 168 registers per thread
+constexpr int kThreads = (kComputeWarps + 1) * 32;
 constexpr int kMaxStages = 4;
-constexpr int kMaxGroups = kMaxWarps;
+constexpr int kMaxGroups = kComputeWarps;
 constexpr int kStepStrips = 2;     // strips of 16 tokens per step
+constexpr int kUnitCost = 4;       // strips' worth of a unit's start and end
 constexpr float kRefBelow = 6.f;   // the reference lies this far (log2) below the maximum it was taken from
 constexpr float kRefSpan = 14.f;   // and is kept until a score is this far above it
 constexpr float kLn2 = 0.693147180559945309f;
 
-enum Kv4Site : uint32_t { KS_K = 0x7b, KS_V, KS_DRAIN };
+enum Kv4Site : uint32_t { KS_K = 0x7b, KS_V, KS_PROD, KS_DRAIN };
 
 struct Kv4Geo {
     int chunks;      // D / 64
@@ -53,9 +56,9 @@ struct Kv4Geo {
     int rblocks;     // blocks of `rows` query rows per kv head's group of G * Nq
     int rows;        // 8 or 16
     int stages;
-    int ctas;
-    float* part;     // [ctas][2][rows][D] unnormalised partial O
-    float* ml;       // [ctas][2][rows][2] reference (log2) and sum
+    int workers;     // groups of the whole grid
+    float* part;     // [workers][2][rows][D] unnormalised partial O
+    float* ml;       // [workers][2][rows][2] reference (log2) and sum
 };
 
 // K or V of a step
@@ -72,8 +75,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -87,6 +89,21 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return r;
 }
 
+// Two words of eight codes (two tokens, the same head dims) -> the even and the odd head dims with the two tokens'
+// codes side by side in each byte (the first in the low nibble).
+__device__ __forceinline__ void interleave(uint32_t x, uint32_t y, uint32_t& even, uint32_t& odd)
+{
+    const uint32_t m = 0x0f0f0f0fu;
+    even = (x & m) | ((y << 4) & ~m);
+    odd = ((x >> 4) & m) | (y & ~m);
+}
+
+// The scales in bytes i and j of s, as an fp16 pair.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t s, int i, int j)
+{
+    return __byte_perm(s, 0, i | 0x40 | (j << 8) | 0x4000) << 7;
+}
+
 // Cached tokens of sequence b; 0 (and the status word) when the length is outside the block table.
 __device__ __forceinline__ int cached_len(const Kv4Decode& a, int b)
 {
@@ -98,57 +115,72 @@ __device__ __forceinline__ int cached_len(const Kv4Decode& a, int b)
     return len;
 }
 
-__device__ __forceinline__ long long strips_of(int len) { return (static_cast<long long>(len) + 15) >> 4; }
+__device__ __forceinline__ int strips_of(int len) { return (len >> 4) + ((len & 15) != 0); }
+// places of one unit on the line
+__device__ __forceinline__ int cost_of(int len) { return len > 0 ? strips_of(len) + kUnitCost : 0; }
 
-// Strips of all sequences before b (b = B: of all), by every thread of the block; `red`: a sum per warp.
-struct LineSums {
-    long long before, total;
-};
-__device__ __forceinline__ LineSums line_sums(const Kv4Decode& a, int b_end, long long (*red)[kMaxWarps])
-{
-    long long before = 0, total = 0;
-    for (int b = threadIdx.x; b < a.f.pb.B; b += blockDim.x) {
-        const long long n = strips_of(cached_len(a, b));
-        total += n;
-        before += b < b_end ? n : 0;
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        total += __shfl_xor_sync(0xffffffffu, total, d);
-        before += __shfl_xor_sync(0xffffffffu, before, d);
-    }
-    if ((threadIdx.x & 31) == 0) {
-        red[0][threadIdx.x >> 5] = total;
-        red[1][threadIdx.x >> 5] = before;
-    }
-    __syncthreads();
-    LineSums s{0, 0};
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
-        s.total += red[0][w];
-        s.before += red[1][w];
-    }
-    __syncthreads();
-    return s;
-}
-
-// First strip of CTA c's range of a line of `total` strips.
-__device__ __forceinline__ long long range_begin(long long total, int c, int ctas) { return total * c / ctas; }
-
-// A run of strips [s0, s1) of one unit within a CTA's range; w is its place on the line.
+// A run of strips [s0, s1) of one unit within a group's range [.., end) of the line; `unit` is the line place where
+// the unit begins, its first strip lies kUnitCost behind.
 struct Piece {
     int b, hk, rb, len;
     int s0, s1;
-    long long w;
+    long long unit, end;
 };
+
+__device__ __forceinline__ void piece_end(Piece& p)
+{
+    const int n = strips_of(p.len);
+    const long long left = p.end - p.unit - kUnitCost;
+    p.s1 = left < n ? static_cast<int>(left) : n;
+}
+
+// The run that begins at place `at` of the line, in sequence b whose units begin at place `b_at`; false when the
+// range holds no strip.
+__device__ __forceinline__ bool first_piece(const Kv4Decode& a, const Kv4Geo& gm, Piece& p, long long at, long long end,
+                                            int b, long long b_at)
+{
+    if (at >= end) return false;
+    p.b = b;
+    p.len = cached_len(a, b);
+    p.end = end;
+    const int cost = cost_of(p.len), u = static_cast<int>((at - b_at) / cost);
+    p.unit = b_at + static_cast<long long>(u) * cost;
+    p.hk = u / gm.rblocks;
+    p.rb = u - p.hk * gm.rblocks;
+    const int r = static_cast<int>(at - p.unit);
+    p.s0 = r > kUnitCost ? r - kUnitCost : 0;
+    piece_end(p);
+    return p.s1 > p.s0;
+}
+
+__device__ __forceinline__ bool next_piece(const Kv4Decode& a, const Kv4Geo& gm, Piece& p)
+{
+    p.unit += cost_of(p.len);
+    if (p.unit + kUnitCost >= p.end) return false;
+    if (++p.rb == gm.rblocks) {
+        p.rb = 0;
+        if (++p.hk == a.f.pb.Hkv) {
+            p.hk = 0;
+            do {  // places are left, so a later sequence has tokens
+                if (++p.b >= a.f.pb.B) return false;
+                p.len = cached_len(a, p.b);
+            } while (p.len == 0);
+        }
+    }
+    p.s0 = 0;
+    piece_end(p);
+    return p.s1 > 0;
+}
 
 struct __align__(16) DecShared {
     uint64_t full_k[kMaxGroups][kMaxStages], full_v[kMaxGroups][kMaxStages];
-    long long red[2][kMaxWarps];
-    long long first;   // strips of the sequences before the range's first one
-    int first_b;
+    uint64_t empty_k[kMaxGroups][kMaxStages], empty_v[kMaxGroups][kMaxStages];
+    long long sums[kThreads / 32];
+    long long first_at[kMaxGroups];   // place where the units of each group's first sequence begin
+    int first_b[kMaxGroups];
     int abort_flag;
-    float c2[16];                      // log2-domain score scale of each row
-    float ml[kMaxGroups][16][2];       // reference and sum of each group and row
+    int last[kMaxGroups][3];          // sequence (-1: none), kv head and row block of the part a group ends with
+    float ml[kMaxGroups][16][2];      // its references and sums
 };
 
 template <int CH, int NB, bool BF16>
@@ -157,494 +189,534 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
     pdl_trigger();
     const Problem& pb = a.f.pb;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int group = warp / gm.C, wg = warp % gm.C;  // my group, my place in it
+    const int warps = blockDim.x >> 5;
     const int G = pb.Hq / pb.Hkv, R = G * pb.Nq;
     const int units_b = pb.Hkv * gm.rblocks;          // units per sequence
     __shared__ DecShared sh;
     extern __shared__ __align__(128) uint8_t smem[];
 
-    // ---- my range of the line
-    const LineSums all = line_sums(a, 0, sh.red);
-    const long long total = all.total * units_b;
-    const long long w0 = range_begin(total, blockIdx.x, gm.ctas), w1 = range_begin(total, blockIdx.x + 1, gm.ctas);
-    if (w0 >= w1) return;
+    // ---- the line's length and the sequence in which each of my groups begins
+    long long chunk, total;
     {
-        long long base = 0;
-        for (int b0 = 0; b0 < pb.B; b0 += blockDim.x) {
-            const int b = b0 + threadIdx.x;
-            const long long n = b < pb.B ? strips_of(cached_len(a, b)) : 0;
-            long long incl = n;
+        const int per = (pb.B + blockDim.x - 1) / blockDim.x;
+        const int b0 = min(static_cast<int>(threadIdx.x) * per, pb.B), b1 = min(b0 + per, pb.B);
+        long long sum = 0;
+        for (int b = b0; b < b1; ++b) sum += cost_of(cached_len(a, b));
+        long long incl = sum;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const long long x = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += x;
-            }
-            if (lane == 31) sh.red[0][warp] = incl;
-            __syncthreads();
-            long long chunk = 0;
-            for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
-                if (w < warp) incl += sh.red[0][w];
-                chunk += sh.red[0][w];
-            }
-            if ((base + incl - n) * units_b <= w0 && w0 < (base + incl) * units_b) {
-                sh.first = base + incl - n;
-                sh.first_b = b;
-            }
-            base += chunk;
-            __syncthreads();
-            if (base * units_b > w0) break;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += x;
         }
+        if (lane == 31) sh.sums[warp] = incl;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < gm.NG; ++i)
+                for (int s = 0; s < gm.stages; ++s) {
+                    mbar_init(&sh.full_k[i][s], 1);
+                    mbar_init(&sh.full_v[i][s], 1);
+                    mbar_init(&sh.empty_k[i][s], gm.C);
+                    mbar_init(&sh.empty_v[i][s], gm.C);
+                }
+            sh.abort_flag = 0;
+            fence_barrier_init();
+        }
+        __syncthreads();
+        total = 0;
+        for (int w = 0; w < warps; ++w) {
+            if (w < warp) incl += sh.sums[w];
+            total += sh.sums[w];
+        }
+        total *= units_b;
+        chunk = (total + gm.workers - 1) / gm.workers;
+        const long long lo = (incl - sum) * units_b, hi = incl * units_b;
+        for (int i = 0; i < gm.NG; ++i) {
+            const long long at = (static_cast<long long>(blockIdx.x) * gm.NG + i) * chunk;
+            if (at < lo || at >= hi || at >= total) continue;
+            long long b_at = lo;
+            for (int b = b0; b < b1; ++b) {
+                const long long n = static_cast<long long>(cost_of(cached_len(a, b))) * units_b;
+                if (at < b_at + n) {
+                    sh.first_b[i] = b;
+                    sh.first_at[i] = b_at;
+                    break;
+                }
+                b_at += n;
+            }
+        }
+        __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < gm.NG; ++i)
-            for (int s = 0; s < gm.stages; ++s) {
-                mbar_init(&sh.full_k[i][s], 1);
-                mbar_init(&sh.full_v[i][s], 1);
-            }
-        sh.abort_flag = 0;
-        fence_barrier_init();
-    }
-    __syncthreads();
+    if (static_cast<long long>(blockIdx.x) * gm.NG * chunk >= total) return;
 
-    auto piece_end = [&](Piece& p) {
-        const long long n = strips_of(p.len), left = w1 - p.w;
-        p.s1 = static_cast<int>(n - p.s0 < left ? n : p.s0 + left);
+    const int st_bytes = stage_bytes(gm.chunks), strip_bytes = gm.chunks * kKv4Tile;
+    auto range = [&](int grp, Piece& p) {
+        const long long at = (static_cast<long long>(blockIdx.x) * gm.NG + grp) * chunk;
+        return first_piece(a, gm, p, at, min(at + chunk, total), sh.first_b[grp], sh.first_at[grp]);
     };
-    auto next_piece = [&](Piece& p) {
-        p.w += p.s1 - p.s0;
-        if (p.w >= w1) return false;
-        p.s0 = 0;
-        if (++p.rb == gm.rblocks) {
-            p.rb = 0;
-            if (++p.hk == pb.Hkv) {
-                p.hk = 0;
-                do {  // strips are left, so a later sequence has some
-                    if (++p.b >= pb.B) return false;
-                    p.len = cached_len(a, p.b);
-                } while (p.len == 0);
-            }
-        }
-        piece_end(p);
-        return true;
-    };
-    // strips per step: one where a piece has no more strips than there are groups
-    auto per_step = [&](const Piece& p) { return p.s1 - p.s0 <= gm.NG ? 1 : kStepStrips; };
 
-    Piece cur;
-    {
-        const long long off = w0 - sh.first * units_b;
-        cur.b = sh.first_b;
-        cur.len = cached_len(a, cur.b);
-        const long long n = strips_of(cur.len);
-        const int u = static_cast<int>(off / n);
-        cur.s0 = static_cast<int>(off - u * n);
-        cur.hk = u / gm.rblocks;
-        cur.rb = u % gm.rblocks;
-        cur.w = w0;
-        piece_end(cur);
-    }
-
-    // ---- shared memory: ring stages of every group, score exchange, then Q staging / the join
-    const int st_bytes = stage_bytes(gm.chunks);
-    const int strip_bytes = gm.chunks * kKv4Tile;
-    uint8_t* const ring_k = smem + static_cast<size_t>(group) * 2 * gm.stages * st_bytes;
-    uint8_t* const ring_v = ring_k + gm.stages * st_bytes;
-    float4* const after = reinterpret_cast<float4*>(smem + static_cast<size_t>(gm.NG) * 2 * gm.stages * st_bytes);
-    constexpr int kExch = kStepStrips * NB * 32;  // float4 per warp and buffer
-    float4* const exch = after + group * 2 * gm.C * kExch;
-    float4* const join = after + gm.NG * 2 * gm.C * kExch;
-    uint16_t* const qs = reinterpret_cast<uint16_t*>(join);  // [rows][D + 8]
-    uint64_t *const full_k = sh.full_k[group], *const full_v = sh.full_v[group];
-
-    // ---- loads: the group's first warp walks the group's steps ahead of the products
-    const int spp = a.cache.page_size >> 4;  // strips per page
-    const size_t v_off = static_cast<size_t>(pb.Hkv) * spp * strip_bytes;
-    Piece lp = cur;
-    int l_step = group;
-    int l_page0 = 0, l_page1 = 0;  // pages of the next step's strips, fetched one step ahead
-    bool l_more = true;
-    auto fetch = [&]() {
-        for (;;) {
-            const int per = per_step(lp);
-            const int s = lp.s0 + l_step * per;
-            if (s < lp.s1) {
-                const int* row = a.cache.table + lp.b * a.cache.table_stride;
-                l_page0 = row[s / spp];
-                l_page1 = per > 1 && s + 1 < lp.s1 ? row[(s + 1) / spp] : l_page0;
-                return;
-            }
-            if (!next_piece(lp)) {
-                l_more = false;
-                return;
-            }
-            l_step = group;
-        }
-    };
-    // K tiles of a step's strips (V lies v_off behind); n = 0: no step
-    struct Source {
-        const uint8_t *s0, *s1;
-        int n;
-        bool joint;  // the two strips are neighbours in one page
-    };
-    auto next_source = [&]() {
-        Source x{nullptr, nullptr, 0, false};
-        if (!l_more) return x;
-        const int per = per_step(lp), s = lp.s0 + l_step * per;
-        x.n = min(per, lp.s1 - s);
-        x.joint = x.n == 2 && s % spp + 1 < spp;
-        if (static_cast<unsigned>(l_page0) >= static_cast<unsigned>(a.cache.num_pages) ||
-            static_cast<unsigned>(l_page1) >= static_cast<unsigned>(a.cache.num_pages)) {
-            // the sequence's rows are undefined, but the copies stay inside the cache
-            if (lane == 0) kv4_invalid(a.f.ctl.status, VS_KV4_DECODE, lp.b);
-            l_page0 = l_page1 = 0;
-        }
-        x.s0 = a.cache.data + kv4_strip_offset(a.cache, pb.Hkv, gm.chunks, l_page0, 0, lp.hk, s % spp);
-        x.s1 = a.cache.data + kv4_strip_offset(a.cache, pb.Hkv, gm.chunks, l_page1, 0, lp.hk, (s + 1) % spp);
-        l_step += gm.NG;
-        fetch();
-        return x;
-    };
-    auto load = [&](const Source& x, size_t off, uint8_t* dst, uint64_t* bar) {
-        if (lane != 0 || x.n == 0) return;
-        mbar_arrive_expect_tx(bar, x.n * strip_bytes);
-        bulk_load(dst, x.s0 + off, (x.joint ? 2 : 1) * strip_bytes, bar);
-        if (x.n == 2 && !x.joint) bulk_load(dst + strip_bytes, x.s1 + off, strip_bytes, bar);
-    };
-    int k_loads = 0, v_loads = 0;  // steps whose K / V copies were issued, or that do not exist
-    Source last{nullptr, nullptr, 0, false};
-    // K of the next step, into the stage that is free; its V follows a step later
-    auto load_k = [&]() {
-        last = next_source();
-        const int slot = k_loads % gm.stages;
-        load(last, 0, ring_k + slot * st_bytes, &full_k[slot]);
-        k_loads += last.n > 0;
-    };
-    auto load_v = [&]() {
-        const int slot = v_loads % gm.stages;
-        load(last, v_off, ring_v + slot * st_bytes, &full_v[slot]);
-        v_loads += last.n > 0;
-    };
-    if (wg == 0) {
-        fetch();
-        for (int i = 0; i < gm.stages; ++i) {
-            load_k();
-            if (i + 1 < gm.stages) load_v();
-        }
-    }
-
-    // ---- state of the products
-    const int my = (gm.chunks - wg + gm.C - 1) / gm.C;  // my chunks: wg, wg + C, ...
-    int done = 0;    // steps of my group finished
-    int eb = 0;      // exchange buffer
-    bool ok = true;
-    uint32_t qf[NB][CH][4][2];
+    Piece cur{};
+    bool pending = false;  // my group's last part is still in its registers
+    const int group = warp / gm.C, wg = warp - group * gm.C;  // my group, my place in it
     float acc[CH][4][NB][4];
-    float m[NB][2], l[NB][2], c2[NB][2];
-    float s[kStepStrips][NB][4];
-    uint32_t pf[kStepStrips][NB][2];
+    float m[NB][2], l[NB][2];
 
-    auto group_sync = [&]() {
-        if (gm.C == 1)
-            __syncwarp();
-        else
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gm.C * 32) : "memory");
-    };
-
-    // Waits for a copy. One that runs out of time ends the warp's work, not its barriers; another sequence's error
-    // in the status word does not end it.
-    auto arrived = [&](uint64_t* bar, int k, uint32_t site) {
-        if (ok)
-            ok = __all_sync(0xffffffffu, mbar_wait(bar, static_cast<uint32_t>((k / gm.stages) & 1), &sh.abort_flag,
-                                                   a.f.ctl.status, a.f.ctl.limit_ns, site, false));
-    };
-
-    // S^T of a step over my chunks, left in s (C = 1) or in the exchange buffer
-    auto scores = [&](int ns, int k) {
-        const int slot = k % gm.stages;
-        arrived(&full_k[slot], k, KS_K);
-        const uint8_t* kb = ring_k + slot * st_bytes;
-#pragma unroll
-        for (int i = 0; i < kStepStrips; ++i) {
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
-            if (i >= ns || !ok) continue;
-#pragma unroll
-            for (int cc = 0; cc < CH; ++cc) {
-                if (cc >= my) break;
-                const uint8_t* tile = kb + i * strip_bytes + (wg + cc * gm.C) * kKv4Tile;
-                const uint4 w = *reinterpret_cast<const uint4*>(tile + lane * 16);
-                const uint32_t sc = *reinterpret_cast<const uint16_t*>(tile + 512 + lane * 2);
-                const uint32_t lo = kv4_scale2(sc), hi = kv4_scale2(sc >> 8);
-                uint32_t x[4], y[4], z[4], u[4];
-                kv4_dequant8(w.x, lo, x);
-                kv4_dequant8(w.y, lo, y);
-                kv4_dequant8(w.z, hi, z);
-                kv4_dequant8(w.w, hi, u);
-#pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    mma_f16_16816(s[i][n], x[0], z[0], x[1], z[1], qf[n][cc][0][0], qf[n][cc][0][1]);
-                    mma_f16_16816(s[i][n], x[2], z[2], x[3], z[3], qf[n][cc][1][0], qf[n][cc][1][1]);
-                    mma_f16_16816(s[i][n], y[0], u[0], y[1], u[1], qf[n][cc][2][0], qf[n][cc][2][1]);
-                    mma_f16_16816(s[i][n], y[2], u[2], y[3], u[3], qf[n][cc][3][0], qf[n][cc][3][1]);
+    if (warp == warps - 1) {
+        // ------------------------------------------------------------ producer: one lane per group
+        bool more = lane < gm.NG;
+        if (more) more = range(lane, cur);
+        uint8_t* const ring_k = smem + static_cast<size_t>(lane) * 2 * gm.stages * st_bytes;
+        uint8_t* const ring_v = ring_k + gm.stages * st_bytes;
+        const int spp = a.cache.page_size >> 4;  // strips per page
+        const size_t v_off = static_cast<size_t>(pb.Hkv) * spp * strip_bytes, page_bytes = 2 * v_off;
+        int s = cur.s0, slot = 0, loads = 0;     // next strip; steps whose K was issued, with ring slot and parity
+        uint32_t phase = 1;
+        bool v_next = false;                     // K of the step is issued, its V is not
+        const uint8_t *src0 = nullptr, *src1 = nullptr;
+        int ns = 0;
+        bool joint = false;                      // the two strips are neighbours in a page
+        uint64_t t0 = global_timer_ns();
+        while (__any_sync(0xffffffffu, more)) {
+            bool moved = false;
+            if (more) {
+                uint64_t* empty = v_next ? &sh.empty_v[lane][slot] : &sh.empty_k[lane][slot];
+                if (mbar_test(empty, phase)) {
+                    moved = true;
+                    uint64_t* bar = v_next ? &sh.full_v[lane][slot] : &sh.full_k[lane][slot];
+                    uint8_t* dst = (v_next ? ring_v : ring_k) + slot * st_bytes;
+                    if (!v_next) {
+                        const int* row = a.cache.table + cur.b * a.cache.table_stride;
+                        const int blk0 = s / spp, in0 = s - blk0 * spp;
+                        ns = min(kStepStrips, cur.s1 - s);
+                        joint = ns == 2 && in0 + 1 < spp;
+                        const int blk1 = ns == 2 && !joint ? blk0 + 1 : blk0, in1 = joint ? in0 + 1 : 0;
+                        int page0 = row[blk0], page1 = row[blk1];
+                        if (static_cast<unsigned>(page0) >= static_cast<unsigned>(a.cache.num_pages) ||
+                            static_cast<unsigned>(page1) >= static_cast<unsigned>(a.cache.num_pages)) {
+                            // the sequence's rows are undefined, but the copies stay inside the cache
+                            kv4_invalid(a.f.ctl.status, VS_KV4_DECODE, cur.b);
+                            page0 = page1 = 0;
+                        }
+                        const uint8_t* head = a.cache.data + static_cast<size_t>(cur.hk) * spp * strip_bytes;
+                        src0 = head + page0 * page_bytes + static_cast<size_t>(in0) * strip_bytes;
+                        src1 = head + page1 * page_bytes + static_cast<size_t>(in1) * strip_bytes;
+                    }
+                    const size_t off = v_next ? v_off : 0;
+                    mbar_arrive_expect_tx(bar, ns * strip_bytes);
+                    bulk_load(dst, src0 + off, (joint ? 2 : 1) * strip_bytes, bar);
+                    if (ns == 2 && !joint) bulk_load(dst + strip_bytes, src1 + off, strip_bytes, bar);
+                    if (!v_next) {
+                        ++loads;
+                    } else {
+                        s += ns;
+                        if (++slot == gm.stages) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
+                        if (s >= cur.s1) {
+                            more = next_piece(a, gm, cur);
+                            s = 0;
+                        }
+                    }
+                    v_next = !v_next;
                 }
             }
+            if (__any_sync(0xffffffffu, moved)) {
+                t0 = global_timer_ns();
+                continue;
+            }
+            __nanosleep(40);
+            bool stop = *reinterpret_cast<volatile int*>(&sh.abort_flag) != 0;
+            if (global_timer_ns() - t0 > a.f.ctl.limit_ns) {
+                stop = true;
+                if (lane == 0) atomicCAS(a.f.ctl.status, 0u, DEV_TIMEOUT | (KS_PROD << 8) | (blockIdx.x << 16));
+            }
+            if (__any_sync(0xffffffffu, stop)) {
+                // copies in flight end before the CTA does
+                sh.abort_flag = 1;
+                if (lane < gm.NG)
+                    for (int k = max(0, loads - gm.stages); k < loads; ++k) {
+                        const uint32_t ph = static_cast<uint32_t>((k / gm.stages) & 1);
+                        mbar_wait(&sh.full_k[lane][k % gm.stages], ph, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns,
+                                  KS_DRAIN, false);
+                        if (k + 1 < loads || !v_next)
+                            mbar_wait(&sh.full_v[lane][k % gm.stages], ph, &sh.abort_flag, a.f.ctl.status,
+                                      a.f.ctl.limit_ns, KS_DRAIN, false);
+                    }
+                break;
+            }
         }
-        if (gm.C > 1) {
+        if (lane < gm.NG) sh.last[lane][0] = -1;
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ compute warps
+        const uint8_t* const ring_k = smem + static_cast<size_t>(group) * 2 * gm.stages * st_bytes;
+        const uint8_t* const ring_v = ring_k + gm.stages * st_bytes;
+        constexpr int kExch = kStepStrips * NB * 32;  // float4 per warp and buffer
+        float4* const exch = reinterpret_cast<float4*>(smem + static_cast<size_t>(gm.NG) * 2 * gm.stages * st_bytes) +
+                             group * 2 * gm.C * kExch + lane;
+        int eb = 0;                      // exchange buffer
+        RingPos kpos, vpos;
+        bool ok = true;
+        uint32_t qf[NB][CH][4][2];
+        float c2[NB][2];                 // log2-domain scale of my partial scores
+        float s[kStepStrips][NB][4];
+        uint32_t pf[kStepStrips][NB][2];
+        int tile_at[CH];                 // byte offsets of my chunks (the last one again where I have fewer)
 #pragma unroll
-            for (int i = 0; i < kStepStrips; ++i)
+        for (int c = 0; c < CH; ++c) tile_at[c] = min(wg + c * gm.C, gm.chunks - 1) * kKv4Tile;
+
+        // Waits for a copy. One that runs out of time ends the warp's work, not its barriers; another sequence's
+        // error in the status word does not end it.
+        auto arrived = [&](uint64_t* bar, uint32_t phase, uint32_t site) {
+            if (ok)
+                ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns,
+                                                       site, false));
+        };
+
+        // S^T of a step over my chunks, scaled to log2 units: left in s (C = 1) or in the exchange buffer
+        auto scores = [&](int ns) {
+            arrived(&sh.full_k[group][kpos.slot], kpos.phase, KS_K);
+            const uint8_t* kb = ring_k + kpos.slot * st_bytes;
+#pragma unroll
+            for (int i = 0; i < kStepStrips; ++i) {
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
-                    exch[(eb * gm.C + wg) * kExch + (i * NB + n) * 32 + lane] =
-                        make_float4(s[i][n][0], s[i][n][1], s[i][n][2], s[i][n][3]);
-        }
-    };
-
-    // sums of the partial scores, mask, P^T fragments; tok: the step's first token
-    auto softmax = [&](int ns, int tok, int len) {
-        if (gm.C > 1) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+                if (i >= ns || !ok) continue;
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const uint8_t* tile = kb + i * strip_bytes + tile_at[c];
+                    const uint4 w = *reinterpret_cast<const uint4*>(tile + lane * 16);
+                    const uint32_t sc = *reinterpret_cast<const uint16_t*>(tile + 512 + lane * 2);
+                    const uint32_t lo = scale_pair(sc, 0, 0), hi = scale_pair(sc, 1, 1);
+                    uint32_t x[4], y[4], z[4], u[4];
+                    kv4_dequant8(w.x, lo, x);
+                    kv4_dequant8(w.y, lo, y);
+                    kv4_dequant8(w.z, hi, z);
+                    kv4_dequant8(w.w, hi, u);
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        mma_f16_16816(s[i][n], x[0], z[0], x[1], z[1], qf[n][c][0][0], qf[n][c][0][1]);
+                        mma_f16_16816(s[i][n], x[2], z[2], x[3], z[3], qf[n][c][1][0], qf[n][c][1][1]);
+                        mma_f16_16816(s[i][n], y[0], u[0], y[1], u[1], qf[n][c][2][0], qf[n][c][2][1]);
+                        mma_f16_16816(s[i][n], y[2], u[2], y[3], u[3], qf[n][c][3][0], qf[n][c][3][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.empty_k[group][kpos.slot]);
+            kpos.advance(gm.stages);
 #pragma unroll
             for (int i = 0; i < kStepStrips; ++i)
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    float4 v = exch[eb * gm.C * kExch + (i * NB + n) * 32 + lane];
-                    for (int w = 1; w < gm.C; ++w) {  // one order for every warp: all get the same bits
-                        const float4 x = exch[(eb * gm.C + w) * kExch + (i * NB + n) * 32 + lane];
-                        v.x += x.x;
-                        v.y += x.y;
-                        v.z += x.z;
-                        v.w += x.w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i][n][e] *= c2[n][e & 1];
+                    if (gm.C > 1)
+                        exch[(eb * gm.C + wg) * kExch + (i * NB + n) * 32] =
+                            make_float4(s[i][n][0], s[i][n][1], s[i][n][2], s[i][n][3]);
+                }
+        };
+
+        // sums of the partial scores, mask, P^T fragments; tok: the step's first token
+        auto softmax = [&](int ns, int tok) {
+            if (gm.C > 1) {
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gm.C * 32) : "memory");
+#pragma unroll
+                for (int i = 0; i < kStepStrips; ++i)
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        float4 v = exch[eb * gm.C * kExch + (i * NB + n) * 32];
+                        for (int w = 1; w < gm.C; ++w) {  // one order for every warp: all get the same bits
+                            const float4 x = exch[(eb * gm.C + w) * kExch + (i * NB + n) * 32];
+                            v.x += x.x;
+                            v.y += x.y;
+                            v.z += x.z;
+                            v.w += x.w;
+                        }
+                        s[i][n][0] = v.x;
+                        s[i][n][1] = v.y;
+                        s[i][n][2] = v.z;
+                        s[i][n][3] = v.w;
                     }
-                    s[i][n][0] = v.x;
-                    s[i][n][1] = v.y;
-                    s[i][n][2] = v.z;
-                    s[i][n][3] = v.w;
-                }
-            eb ^= 1;
-        }
-        const int least = pb.causal ? len - pb.Nq + 1 : len;  // first token that some row does not see
-        const bool mask = tok + 16 * ns > least || ns < kStepStrips;
-        bool up = false;
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                int lim = len;
-                if (mask && pb.causal) lim = min(len, least + (cur.rb * gm.rows + n * 8 + 2 * t + (e & 1)) % pb.Nq);
-#pragma unroll
-                for (int i = 0; i < kStepStrips; ++i) {
-                    float x = s[i][n][e] * c2[n][e & 1];
-                    if (mask) x = i < ns && tok + 16 * i + g + 8 * (e >> 1) < lim ? x : -INFINITY;
-                    s[i][n][e] = x;
-                    up |= x > m[n][e & 1] + kRefSpan;
-                }
+                eb ^= 1;
             }
-        if (__any_sync(0xffffffffu, up)) {
+            const int least = pb.causal ? cur.len - pb.Nq + 1 : cur.len;  // first token that some row does not see
+            if (tok + 16 * kStepStrips > least || ns < kStepStrips) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        int lim = cur.len;
+                        if (pb.causal) lim = min(lim, least + (cur.rb * gm.rows + n * 8 + 2 * t + q) % pb.Nq);
+#pragma unroll
+                        for (int i = 0; i < kStepStrips; ++i)
+#pragma unroll
+                            for (int hi = 0; hi < 2; ++hi)
+                                if (i >= ns || tok + 16 * i + g + 8 * hi >= lim) s[i][n][q + 2 * hi] = -INFINITY;
+                    }
+            }
+            bool up = false;
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    float mx = -INFINITY;
+                    const float top = m[n][q] + kRefSpan;
 #pragma unroll
-                    for (int i = 0; i < kStepStrips; ++i) mx = fmaxf(mx, fmaxf(s[i][n][q], s[i][n][q + 2]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float mn = fmaxf(m[n][q], mx - kRefBelow);
-                    const float al = m[n][q] == -INFINITY ? 0.f : ex2_approx(m[n][q] - mn);
-                    m[n][q] = mn;
-                    l[n][q] *= al;
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            acc[c][i][n][q] *= al;
-                            acc[c][i][n][q + 2] *= al;
-                        }
+                    for (int i = 0; i < kStepStrips; ++i) up |= s[i][n][q] > top || s[i][n][q + 2] > top;
                 }
-        }
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            float mu[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) mu[q] = m[n][q] == -INFINITY ? 0.f : m[n][q];
-#pragma unroll
-            for (int i = 0; i < kStepStrips; ++i) {
-                float p[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = ex2_approx(s[i][n][e] - mu[e & 1]);
-                l[n][0] += p[0] + p[2];
-                l[n][1] += p[1] + p[3];
-                // fp16 P: half a step of 2^-11, an eighth of what bf16 operands would cost
-                pf[i][n][0] = transpose8x8(pack2<false>(p[0], p[1]));
-                pf[i][n][1] = transpose8x8(pack2<false>(p[2], p[3]));
-            }
-        }
-    };
-
-    // O^T += V^T P^T over my chunks
-    auto values = [&](int ns, int tok, int len, int k) {
-        const int slot = k % gm.stages;
-        arrived(&full_v[slot], k, KS_V);
-        if (!ok) return;
-        const uint8_t* vb = ring_v + slot * st_bytes;
-#pragma unroll
-        for (int i = 0; i < kStepStrips; ++i) {
-            if (i >= ns) break;
-            uint32_t keep = 0xffffffffu;  // cells behind the last token hold anything: their scales count as zero
-            if (tok + 16 * i + 16 > len) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (tok + 16 * i + 2 * t + (j & 1) + 8 * (j >> 1) >= len) keep &= ~(0xffu << (8 * j));
-            }
-#pragma unroll
-            for (int cc = 0; cc < CH; ++cc) {
-                if (cc >= my) break;
-                const uint8_t* tile = vb + i * strip_bytes + (wg + cc * gm.C) * kKv4Tile;
-                const uint4 w = *reinterpret_cast<const uint4*>(tile + lane * 16);
-                const uint32_t sc = *reinterpret_cast<const uint32_t*>(tile + 512 + ((g >> 1) * 4 + t) * 4) & keep;
-                uint32_t x[4], y[4], z[4], u[4];
-                kv4_dequant8(w.x, kv4_scale2(sc), x);
-                kv4_dequant8(w.y, kv4_scale2(sc >> 8), y);
-                kv4_dequant8(w.z, kv4_scale2(sc >> 16), z);
-                kv4_dequant8(w.w, kv4_scale2(sc >> 24), u);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t a0 = __byte_perm(x[e], y[e], 0x5410), a1 = __byte_perm(x[e], y[e], 0x7632);
-                    const uint32_t a2 = __byte_perm(z[e], u[e], 0x5410), a3 = __byte_perm(z[e], u[e], 0x7632);
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) mma_f16_16816(acc[cc][e][n], a0, a1, a2, a3, pf[i][n][0], pf[i][n][1]);
-                }
-            }
-        }
-    };
-
-    for (bool more = true; more;) {
-        // ---- Q of the piece's rows: fp16, scaled by a power of two into its range (bf16 has the wider one)
-        const int r0 = cur.rb * gm.rows;
-        for (int r = warp; r < gm.rows; r += blockDim.x >> 5) {
-            uint4 v[4];
-            float amax = 0.f;
-            const bool row = r0 + r < R;
-            const int h = cur.hk * G + (r0 + r) / pb.Nq, i = (r0 + r) % pb.Nq;
-            const uint16_t* q = static_cast<const uint16_t*>(a.f.q) + cur.b * pb.vq.sb + h * pb.vq.sh + i * pb.vq.sn;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = make_uint4(0, 0, 0, 0);
-                const int d = e * 256 + lane * 8;
-                if (row && d < pb.D) v[e] = *reinterpret_cast<const uint4*>(q + d);
-            }
-            float mul = 1.f;
-            if (BF16) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = unpack2<true>(w[j]);
-                        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
-                }
-#pragma unroll
-                for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-                // largest magnitude to [2^14, 2^15); rows of zeros or with infinities stay as they are
-                const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-                if (amax > 0.f && e < 128) mul = __uint_as_float(static_cast<uint32_t>(min(14 - e, 126) + 127) << 23);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int d = e * 256 + lane * 8;
-                if (d >= pb.D) break;
-                if (BF16) {
-                    uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = unpack2<true>(w[j]);
-                        w[j] = pack2<false>(f.x * mul, f.y * mul);
-                    }
-                    v[e] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                *reinterpret_cast<uint4*>(qs + r * (pb.D + 8) + d) = v[e];
-            }
-            if (lane == 0) sh.c2[r] = pb.scale_log2 / mul;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-#pragma unroll
-            for (int cc = 0; cc < CH; ++cc) {
-                if (cc >= my) break;
-                const uint4* src = reinterpret_cast<const uint4*>(qs + (n * 8 + g) * (pb.D + 8) +
-                                                                  (wg + cc * gm.C) * 64 + t * 16);
-                const uint4 x = src[0], y = src[1];
-                qf[n][cc][0][0] = x.x;
-                qf[n][cc][0][1] = x.y;
-                qf[n][cc][1][0] = x.z;
-                qf[n][cc][1][1] = x.w;
-                qf[n][cc][2][0] = y.x;
-                qf[n][cc][2][1] = y.y;
-                qf[n][cc][3][0] = y.z;
-                qf[n][cc][3][1] = y.w;
-            }
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                c2[n][q] = sh.c2[n * 8 + 2 * t + q];
-                m[n][q] = -INFINITY;
-                l[n][q] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
+            if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[c][i][n][e] = 0.f;
-
-        // ---- my group's steps of the piece; the scores of a step are issued before the values of the last one
-        const int per = per_step(cur), steps = (cur.s1 - cur.s0 + per - 1) / per;
-        const int mine = group < steps ? (steps - group + gm.NG - 1) / gm.NG : 0;
-        auto first_strip = [&](int j) { return cur.s0 + (group + j * gm.NG) * per; };
-        if (mine > 0) scores(min(per, cur.s1 - first_strip(0)), done);
-        for (int j = 0; j < mine; ++j) {
-            group_sync();  // the exchange is written; K of this step and V of the one before are read by all
-            if (wg == 0 && ok) {
-                load_v();
-                load_k();
+                    for (int q = 0; q < 2; ++q) {
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < kStepStrips; ++i) mx = fmaxf(mx, fmaxf(s[i][n][q], s[i][n][q + 2]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float mn = fmaxf(m[n][q], mx - kRefBelow);
+                        const float al = m[n][q] == -INFINITY ? 0.f : ex2_approx(m[n][q] - mn);
+                        m[n][q] = mn;
+                        l[n][q] *= al;
+#pragma unroll
+                        for (int c = 0; c < CH; ++c)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                acc[c][i][n][q] *= al;
+                                acc[c][i][n][q + 2] *= al;
+                            }
+                    }
             }
-            const int s0 = first_strip(j), ns = min(per, cur.s1 - s0);
-            softmax(ns, s0 * 16, cur.len);
-            if (j + 1 < mine) scores(min(per, cur.s1 - first_strip(j + 1)), done + 1);
-            values(ns, s0 * 16, cur.len, done);
-            ++done;
-        }
-
-        // ---- join the groups: their references and sums, then O in turn (a fixed order)
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+            for (int n = 0; n < NB; ++n) {
+                float mu[2];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 4);
-                l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 8);
-                l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 16);
-                if (wg == 0 && lane < 4) {
-                    sh.ml[group][n * 8 + 2 * t + q][0] = m[n][q];
-                    sh.ml[group][n * 8 + 2 * t + q][1] = l[n][q];
+                for (int q = 0; q < 2; ++q) mu[q] = m[n][q] == -INFINITY ? 0.f : m[n][q];
+#pragma unroll
+                for (int i = 0; i < kStepStrips; ++i) {
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[e] = ex2_approx(s[i][n][e] - mu[e & 1]);
+                    l[n][0] += p[0] + p[2];
+                    l[n][1] += p[1] + p[3];
+                    // fp16 P: half a step of 2^-11, an eighth of what bf16 operands would cost
+                    pf[i][n][0] = transpose8x8(pack2<false>(p[0], p[1]));
+                    pf[i][n][1] = transpose8x8(pack2<false>(p[2], p[3]));
                 }
             }
-        __syncthreads();
-        const int active = min(steps, gm.NG);
+        };
+
+        // O^T += V^T P^T over my chunks
+        auto values = [&](int ns, int tok) {
+            arrived(&sh.full_v[group][vpos.slot], vpos.phase, KS_V);
+            const uint8_t* vb = ring_v + vpos.slot * st_bytes;
+#pragma unroll
+            for (int i = 0; i < kStepStrips; ++i) {
+                if (i >= ns || !ok) break;
+                uint32_t keep = 0xffffffffu;  // cells behind the last token hold anything: their scales count as zero
+                if (tok + 16 * i + 16 > cur.len) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (tok + 16 * i + 2 * t + (j & 1) + 8 * (j >> 1) >= cur.len) keep &= ~(0xffu << (8 * j));
+                }
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const uint8_t* tile = vb + i * strip_bytes + tile_at[c];
+                    const uint4 w = *reinterpret_cast<const uint4*>(tile + lane * 16);
+                    const uint32_t sc = *reinterpret_cast<const uint32_t*>(tile + 512 + ((g >> 1) * 4 + t) * 4) & keep;
+                    const uint32_t lo = scale_pair(sc, 0, 1), hi = scale_pair(sc, 2, 3);
+                    uint32_t even, odd, a0[4], a1[4], a2[4], a3[4];
+                    interleave(w.x, w.y, even, odd);
+                    kv4_dequant8(even, lo, a0);
+                    kv4_dequant8(odd, lo, a1);
+                    interleave(w.z, w.w, even, odd);
+                    kv4_dequant8(even, hi, a2);
+                    kv4_dequant8(odd, hi, a3);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+                            mma_f16_16816(acc[c][e][n], a0[e], a1[e], a2[e], a3[e], pf[i][n][0], pf[i][n][1]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.empty_v[group][vpos.slot]);
+            vpos.advance(gm.stages);
+        };
+
+        // a part of the piece's rows to a slot of the workspace
+        auto store_part = [&](size_t slot) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int r = n * 8 + 2 * t + q;
+                    if (cur.rb * gm.rows + r >= R) continue;
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        if (wg + c * gm.C >= gm.chunks) break;
+                        float4* o = reinterpret_cast<float4*>(gm.part + (slot * gm.rows + r) * pb.D +
+                                                              (wg + c * gm.C) * 64 + 8 * g);
+                        o[0] = make_float4(acc[c][0][n][q], acc[c][0][n][q + 2], acc[c][1][n][q], acc[c][1][n][q + 2]);
+                        o[1] = make_float4(acc[c][2][n][q], acc[c][2][n][q + 2], acc[c][3][n][q], acc[c][3][n][q + 2]);
+                    }
+                    if (wg == 0 && g == 0) {
+                        gm.ml[(slot * gm.rows + r) * 2] = m[n][q];
+                        gm.ml[(slot * gm.rows + r) * 2 + 1] = l[n][q];
+                    }
+                }
+        };
+        const size_t worker = static_cast<size_t>(blockIdx.x) * gm.NG + group;
+
+        bool more = range(group, cur);
+        while (more) {
+            // ---- Q of the piece's rows over my chunks, as B fragments: fp16, scaled by a power of two into its range
+            // (bf16 has the wider one). A lane holds query g, head dims 16 t .. 16 t + 15 of every chunk.
+            const int r0 = cur.rb * gm.rows;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const int r = r0 + n * 8 + g;
+                const int h = cur.hk * G + r / pb.Nq, i = r % pb.Nq;
+                const uint16_t* q = static_cast<const uint16_t*>(a.f.q) + cur.b * pb.vq.sb + h * pb.vq.sh + i * pb.vq.sn;
+                uint32_t amax = 0;  // magnitudes of 16-bit floats order as their bits do
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                    if (r < R && wg + c * gm.C < gm.chunks) {
+                        const uint4* src = reinterpret_cast<const uint4*>(q + (wg + c * gm.C) * 64 + t * 16);
+                        x = src[0];
+                        y = src[1];
+                    }
+                    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        qf[n][c][e >> 1][e & 1] = w[e];
+                        if (BF16) amax = max(amax, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+                    }
+                }
+                float mul = 1.f;
+                if (BF16) {
+                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                    // largest magnitude to [2^14, 2^15); rows of zeros or that are not finite stay as they are
+                    const int e = static_cast<int>(amax >> 7);
+                    if (amax > 0 && e < 255) mul = __uint_as_float(static_cast<uint32_t>(min(14 + 127 - e, 126) + 127) << 23);
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float2 f = unpack2<true>(qf[n][c][k >> 1][k & 1]);
+                            qf[n][c][k >> 1][k & 1] = pack2<false>(f.x * mul, f.y * mul);
+                        }
+                }
+                const float scale = pb.scale_log2 / mul;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    c2[n][e] = __shfl_sync(0xffffffffu, scale, (2 * t + e) * 4);
+                    m[n][e] = -INFINITY;
+                    l[n][e] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[c][i][n][e] = 0.f;
+
+            // ---- the scores of a step are issued before the values of the one before
+            scores(min(kStepStrips, cur.s1 - cur.s0));
+            for (int at = cur.s0; at < cur.s1; at += kStepStrips) {
+                const int ns = min(kStepStrips, cur.s1 - at);
+                softmax(ns, at * 16);
+                if (at + kStepStrips < cur.s1) scores(min(kStepStrips, cur.s1 - at - kStepStrips));
+                values(ns, at * 16);
+            }
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 4);
+                    l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 8);
+                    l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 16);
+                }
+
+            // ---- a whole unit's outputs, or a part of one
+            if (cur.s0 == 0 && cur.s1 == strips_of(cur.len)) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int r = r0 + n * 8 + 2 * t + q;
+                        if (r >= R) continue;
+                        const int h = cur.hk * G + r / pb.Nq, i = r % pb.Nq;
+                        const float inv = l[n][q] == 0.f ? 0.f : 1.f / l[n][q];
+                        uint16_t* o = static_cast<uint16_t*>(a.f.o) + cur.b * pb.vo.sb + h * pb.vo.sh + i * pb.vo.sn;
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            if (wg + c * gm.C >= gm.chunks) break;
+                            uint32_t x[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[e] = pack2<BF16>(acc[c][e][n][q] * inv, acc[c][e][n][q + 2] * inv);
+                            *reinterpret_cast<uint4*>(o + (wg + c * gm.C) * 64 + 8 * g) = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                        if (wg == 0 && g == 0)
+                            a.f.lse[(static_cast<long long>(cur.b) * pb.Hq + h) * pb.Nq + i] =
+                                l[n][q] == 0.f ? -INFINITY : (m[n][q] + lg2_approx(l[n][q])) * kLn2;
+                    }
+                more = next_piece(a, gm, cur);
+            } else {
+                Piece next = cur;
+                more = next_piece(a, gm, next);
+                if (more) {
+                    store_part(2 * worker);
+                    cur = next;
+                } else {
+                    pending = true;
+                }
+            }
+        }
+        if (pending && wg == 0) {
+            if (lane == 0) {
+                sh.last[group][1] = cur.hk;
+                sh.last[group][2] = cur.rb;
+            }
+            if (g == 0)
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        sh.ml[group][n * 8 + 2 * t + q][0] = m[n][q];
+                        sh.ml[group][n * 8 + 2 * t + q][1] = l[n][q];
+                    }
+        }
+    }
+    __syncthreads();  // every copy has been read: the rings are free
+    if (pending && wg == 0 && lane == 0) sh.last[group][0] = cur.b;
+    __syncthreads();
+    const bool compute = warp < warps - 1;
+
+    // ---- neighbouring groups that end in the same unit join their parts in shared memory, each group a share of it
+    int run0 = group, run1 = group;
+    if (compute && pending) {
+        auto same = [&](int i) {
+            return sh.last[i][0] == cur.b && sh.last[i][1] == cur.hk && sh.last[i][2] == cur.rb;
+        };
+        while (run0 > 0 && same(run0 - 1)) --run0;
+        while (run1 + 1 < gm.NG && same(run1 + 1)) ++run1;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int r = n * 8 + 2 * t + q;
                 float mx = -INFINITY, sum = 0.f;
-                for (int i = 0; i < active; ++i) mx = fmaxf(mx, sh.ml[i][r][0]);
+                for (int i = run0; i <= run1; ++i) mx = fmaxf(mx, sh.ml[i][r][0]);
                 const float mu = mx == -INFINITY ? 0.f : mx;
-                for (int i = 0; i < active; ++i) sum += sh.ml[i][r][1] * ex2_approx(sh.ml[i][r][0] - mu);
+                for (int i = run0; i <= run1; ++i) sum += sh.ml[i][r][1] * ex2_approx(sh.ml[i][r][0] - mu);
                 const float f = ex2_approx(m[n][q] - mu);
                 m[n][q] = mx;
                 l[n][q] = sum;
@@ -656,88 +728,53 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                         acc[c][i][n][q + 2] *= f;
                     }
             }
-        for (int turn = 0; turn < active; ++turn) {
-            if (turn == group) {
-                float4* buf = join + wg * (CH * 4 * NB * 32) + lane;
+    }
+    float4* const buf = reinterpret_cast<float4*>(smem) + lane;
+    constexpr int kRegs = CH * 4 * NB;  // float4 per lane
+    if (compute && pending) {
+        float4* mine = buf + static_cast<size_t>(warp) * kRegs * 32;
 #pragma unroll
-                for (int c = 0; c < CH; ++c)
+        for (int c = 0; c < CH; ++c)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int n = 0; n < NB; ++n) {
-                            float(&x)[4] = acc[c][i][n];
-                            float4* at = buf + ((c * 4 + i) * NB + n) * 32;
-                            if (turn > 0) {
-                                const float4 v = *at;
-                                x[0] += v.x;
-                                x[1] += v.y;
-                                x[2] += v.z;
-                                x[3] += v.w;
-                            }
-                            if (turn + 1 < active) *at = make_float4(x[0], x[1], x[2], x[3]);
-                        }
+                for (int n = 0; n < NB; ++n)
+                    mine[((c * 4 + i) * NB + n) * 32] =
+                        make_float4(acc[c][i][n][0], acc[c][i][n][1], acc[c][i][n][2], acc[c][i][n][3]);
+    }
+    __syncthreads();
+    if (!compute || !pending) return;
+    // the part goes to slot 1 of the run's last group
+    const size_t slot = 2 * (static_cast<size_t>(blockIdx.x) * gm.NG + run1) + 1;
+    const int r0 = cur.rb * gm.rows;
+    for (int e = group - run0; e < kRegs; e += run1 - run0 + 1) {
+        const int c = e / (4 * NB), i = e / NB % 4, n = e % NB;
+        if (wg + c * gm.C >= gm.chunks) break;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = run0; k <= run1; ++k) {
+            const float4 v = buf[(static_cast<size_t>(k * gm.C + wg) * kRegs + e) * 32];
+            x.x += v.x;
+            x.y += v.y;
+            x.z += v.z;
+            x.w += v.w;
+        }
+        const int r = n * 8 + 2 * t;
+        float* o = gm.part + (slot * gm.rows + r) * pb.D + (wg + c * gm.C) * 64 + 8 * g + 2 * i;
+        if (r0 + r < R) *reinterpret_cast<float2*>(o) = make_float2(x.x, x.z);
+        if (r0 + r + 1 < R) *reinterpret_cast<float2*>(o + pb.D) = make_float2(x.y, x.w);
+    }
+    if (group == run1 && wg == 0 && g == 0)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float* ml = gm.ml + (slot * gm.rows + n * 8 + 2 * t + q) * 2;
+                ml[0] = m[n][q];
+                ml[1] = l[n][q];
             }
-            __syncthreads();
-        }
-        if (group == active - 1) {
-            const bool whole = cur.s0 == 0 && cur.s1 == strips_of(cur.len);
-            const int slot = 2 * blockIdx.x + (cur.s0 > 0 ? 0 : 1);  // a unit that an earlier CTA began, or not
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int r = n * 8 + 2 * t + q;
-                    if (r0 + r >= R) continue;
-                    const int h = cur.hk * G + (r0 + r) / pb.Nq, i = (r0 + r) % pb.Nq;
-                    const float inv = l[n][q] == 0.f ? 0.f : 1.f / l[n][q];
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        if (c >= my) break;
-                        const int d = (wg + c * gm.C) * 64 + 8 * g;
-                        float x[8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[2 * e] = acc[c][e][n][q];
-                            x[2 * e + 1] = acc[c][e][n][q + 2];
-                        }
-                        if (whole) {
-                            uint16_t* o = static_cast<uint16_t*>(a.f.o) + cur.b * pb.vo.sb + h * pb.vo.sh + i * pb.vo.sn;
-                            *reinterpret_cast<uint4*>(o + d) =
-                                make_uint4(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv),
-                                           pack2<BF16>(x[4] * inv, x[5] * inv), pack2<BF16>(x[6] * inv, x[7] * inv));
-                        } else {
-                            float4* o = reinterpret_cast<float4*>(gm.part + (static_cast<size_t>(slot) * gm.rows + r) * pb.D + d);
-                            o[0] = make_float4(x[0], x[1], x[2], x[3]);
-                            o[1] = make_float4(x[4], x[5], x[6], x[7]);
-                        }
-                    }
-                    if (wg == 0 && g == 0) {
-                        if (whole) {
-                            a.f.lse[(static_cast<long long>(cur.b) * pb.Hq + h) * pb.Nq + i] =
-                                l[n][q] == 0.f ? -INFINITY : (m[n][q] + lg2_approx(l[n][q])) * kLn2;
-                        } else {
-                            float* ml = gm.ml + (static_cast<size_t>(slot) * gm.rows + r) * 2;
-                            ml[0] = m[n][q];
-                            ml[1] = l[n][q];
-                        }
-                    }
-                }
-        }
-        more = next_piece(cur);
-    }
-    // after a wait that ran out, copies may still be in flight: they end before the CTA does
-    if (wg == 0 && lane == 0 && !ok) {
-        auto drain = [&](uint64_t* full, int loads) {
-            for (int k = max(0, loads - gm.stages); k < loads; ++k)
-                mbar_wait(&full[k % gm.stages], static_cast<uint32_t>((k / gm.stages) & 1), &sh.abort_flag,
-                          a.f.ctl.status, a.f.ctl.limit_ns, KS_DRAIN, false);
-        };
-        drain(full_k, k_loads);
-        drain(full_v, v_loads);
-    }
 }
 
-// Joins the parts of units that several CTAs worked on; writes the rows of
+// Joins the parts of units that several groups worked on; writes the rows of
 // sequences without tokens. One CTA per query row and 128 head dims: its four
 // warps take parts in turn, four head dims per lane.
 constexpr int kJoinThreads = 128;
@@ -746,52 +783,73 @@ template <bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_kernel(const Kv4Decode a, const Kv4Geo gm)
 {
     const Problem& pb = a.f.pb;
-    __shared__ long long red[2][kMaxWarps];
-    __shared__ float4 sum[kJoinThreads];
-    extern __shared__ float weight[];  // [ctas]
+    __shared__ long long sums[2][kJoinThreads / 32];
+    __shared__ float4 acc[kJoinThreads];
+    extern __shared__ float weight[];  // [CTAs + 1], then the slots
+    int* const slots = reinterpret_cast<int*>(weight) + gm.workers / gm.NG + 1;
     const long long row = blockIdx.x;
     const int i = static_cast<int>(row % pb.Nq), h = static_cast<int>(row / pb.Nq % pb.Hq);
     const int b = static_cast<int>(row / (static_cast<long long>(pb.Nq) * pb.Hq));
     const int G = pb.Hq / pb.Hkv, r = (h % G) * pb.Nq + i, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int units_b = pb.Hkv * gm.rblocks;
-    const LineSums line = line_sums(a, b, red);
-    const long long total = line.total * units_b, n = strips_of(cached_len(a, b));
-    const long long u0 = line.before * units_b + ((h / G) * gm.rblocks + r / gm.rows) * n;
+    long long total = 0, before = 0;  // places of the line, and those before sequence b
+    for (int k = threadIdx.x; k < pb.B; k += kJoinThreads) {
+        const int c = cost_of(cached_len(a, k));
+        total += c;
+        before += k < b ? c : 0;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, d);
+        before += __shfl_xor_sync(0xffffffffu, before, d);
+    }
+    if (lane == 0) {
+        sums[0][warp] = total;
+        sums[1][warp] = before;
+    }
+    __syncthreads();
+    total = before = 0;
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+        total += sums[0][w];
+        before += sums[1][w];
+    }
+    total *= units_b;
+    const int len = cached_len(a, b), n = strips_of(len);
     const int d = blockIdx.y * 128 + lane * 4;
     uint16_t* o = static_cast<uint16_t*>(a.f.o) + b * pb.vo.sb + h * pb.vo.sh + i * pb.vo.sn + d;
-    pdl_wait();
     if (n == 0) {
+        pdl_wait();
         if (warp == 0 && d < pb.D) *reinterpret_cast<uint2*>(o) = make_uint2(0, 0);
         if (blockIdx.y == 0 && threadIdx.x == 0) a.f.lse[row] = -INFINITY;
         return;
     }
-    auto cta_of = [&](long long w) {  // the CTA whose range holds strip w
-        int c = static_cast<int>(static_cast<double>(w) * gm.ctas / static_cast<double>(total));
-        c = max(0, min(c, gm.ctas - 1));
-        while (range_begin(total, c, gm.ctas) > w) --c;
-        while (range_begin(total, c + 1, gm.ctas) <= w) ++c;
-        return c;
-    };
-    const int c0 = cta_of(u0), c1 = cta_of(u0 + n - 1);
-    if (c0 == c1) return;
-    // slot of the unit's part in CTA c: 0 when the unit began before the CTA's range
-    auto slot = [&](int c) { return 2 * c + (range_begin(total, c, gm.ctas) > u0 ? 0 : 1); };
-    auto has = [&](int c) { return range_begin(total, c, gm.ctas) < range_begin(total, c + 1, gm.ctas); };
+    // the unit's strips lie at [first, end) of the line; groups v0 .. v1 hold them
+    const long long first = before * units_b + static_cast<long long>((h / G) * gm.rblocks + r / gm.rows) * cost_of(len) + kUnitCost;
+    const long long end = first + n, chunk = (total + gm.workers - 1) / gm.workers;
+    const int v0 = static_cast<int>(first / chunk), v1 = static_cast<int>((end - 1) / chunk);
+    pdl_wait();
+    if (v0 == v1) return;  // written by its group
+    // v1 ends in this unit unless its range reaches strips of the next one; the parts that groups of a CTA end with
+    // are in slot 1 of the last of them, a part that is followed by another unit is in slot 0
+    const bool ends = min((v1 + 1LL) * chunk, total) <= end + kUnitCost;
+    const int vl = ends ? v1 : v1 - 1, c0 = v0 / gm.NG, parts = vl / gm.NG - c0 + 1 + (ends ? 0 : 1);
     float mx = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32)
-        if (has(c)) mx = fmaxf(mx, gm.ml[(static_cast<size_t>(slot(c)) * gm.rows + r % gm.rows) * 2]);
+    for (int k = lane; k < parts; k += 32) {
+        const bool tail = !ends && k == parts - 1;
+        const int s = tail ? 2 * v1 : 2 * min(vl, (c0 + k) * gm.NG + gm.NG - 1) + 1;
+        if (warp == 0) slots[k] = s;
+        mx = fmaxf(mx, gm.ml[(static_cast<size_t>(s) * gm.rows + r % gm.rows) * 2]);
+    }
 #pragma unroll
     for (int e = 16; e; e >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, e));
     const float mu = mx == -INFINITY ? 0.f : mx;
+    __syncthreads();
     float l = 0.f;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-        float w = 0.f;
-        if (has(c)) {
-            const float* ml = gm.ml + (static_cast<size_t>(slot(c)) * gm.rows + r % gm.rows) * 2;
-            w = ex2_approx(ml[0] - mu);
-            l += w * ml[1];
-        }
-        if (warp == 0) weight[c - c0] = w;
+    for (int k = lane; k < parts; k += 32) {
+        const float* ml = gm.ml + (static_cast<size_t>(slots[k]) * gm.rows + r % gm.rows) * 2;
+        const float w = ex2_approx(ml[0] - mu);
+        l += w * ml[1];
+        if (warp == 0) weight[k] = w;
     }
 #pragma unroll
     for (int e = 16; e; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
@@ -799,23 +857,22 @@ __global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_kernel(const Kv4
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (d < pb.D) {
 #pragma unroll 4
-        for (int c = c0 + warp; c <= c1; c += 4) {
-            if (!has(c)) continue;
-            const float w = weight[c - c0];
-            const float4 v =
-                *reinterpret_cast<const float4*>(gm.part + (static_cast<size_t>(slot(c)) * gm.rows + r % gm.rows) * pb.D + d);
+        for (int k = warp; k < parts; k += kJoinThreads / 32) {
+            const float w = weight[k];
+            const float4 v = *reinterpret_cast<const float4*>(
+                gm.part + (static_cast<size_t>(slots[k]) * gm.rows + r % gm.rows) * pb.D + d);
             x.x = fmaf(w, v.x, x.x);
             x.y = fmaf(w, v.y, x.y);
             x.z = fmaf(w, v.z, x.z);
             x.w = fmaf(w, v.w, x.w);
         }
     }
-    sum[threadIdx.x] = x;
+    acc[threadIdx.x] = x;
     __syncthreads();
     if (warp == 0 && d < pb.D) {
 #pragma unroll
-        for (int w = 1; w < 4; ++w) {
-            const float4 v = sum[w * 32 + lane];
+        for (int w = 1; w < kJoinThreads / 32; ++w) {
+            const float4 v = acc[w * 32 + lane];
             x.x += v.x;
             x.y += v.y;
             x.z += v.z;
@@ -829,6 +886,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_kernel(const Kv4
 
 struct Plan {
     Kv4Geo gm;
+    int ctas;
     int nb, ch;
     int smem;
     size_t part_floats, bytes;
@@ -849,18 +907,21 @@ Plan plan(const Problem& pb)
     const int most = p.nb == 1 ? 4 : 2;
     gm.C = (gm.chunks + most - 1) / most;
     p.ch = (gm.chunks + gm.C - 1) / gm.C;
-    gm.NG = kMaxGroups / gm.C;
-    const int exch = gm.NG * 2 * gm.C * kStepStrips * p.nb * 32 * 16;
-    const int join = gm.C * p.ch * 4 * p.nb * 32 * 16, q = gm.rows * (pb.D + 8) * 2;
-    const int fixed = exch + (join > q ? join : q), ring = gm.NG * 2 * stage_bytes(gm.chunks);
-    // at least two stages for every head dim: 184 KB of ring, 20 of exchange, 16 of join at D = 512
-    gm.stages = (kMaxSmem - 1024 - static_cast<int>(sizeof(DecShared)) - fixed) / ring;
+    // at least two stages for every head dim: five groups with 184 KB of rings and 20 of exchange at D = 512
+    for (gm.NG = kComputeWarps / gm.C; gm.NG > 1; --gm.NG) {
+        const int exch = gm.C > 1 ? gm.NG * 2 * gm.C * kStepStrips * p.nb * 32 * 16 : 0;
+        if (2 * gm.NG * 2 * stage_bytes(gm.chunks) + exch + 1024 + static_cast<int>(sizeof(DecShared)) <= kMaxSmem) break;
+    }
+    const int exch = gm.C > 1 ? gm.NG * 2 * gm.C * kStepStrips * p.nb * 32 * 16 : 0;
+    const int ring = gm.NG * 2 * stage_bytes(gm.chunks);
+    gm.stages = (kMaxSmem - 1024 - static_cast<int>(sizeof(DecShared)) - exch) / ring;
     if (gm.stages > kMaxStages) gm.stages = kMaxStages;
-    p.smem = fixed + gm.stages * ring;
+    p.smem = exch + gm.stages * ring;
     const int sms = num_sms();
-    gm.ctas = sms > 0 ? sms : 152;
-    p.part_floats = static_cast<size_t>(gm.ctas) * 2 * gm.rows * pb.D;
-    p.bytes = (p.part_floats + static_cast<size_t>(gm.ctas) * 2 * gm.rows * 2) * sizeof(float);
+    p.ctas = sms > 0 ? sms : 152;
+    gm.workers = p.ctas * gm.NG;
+    p.part_floats = static_cast<size_t>(gm.workers) * 2 * gm.rows * pb.D;
+    p.bytes = (p.part_floats + static_cast<size_t>(gm.workers) * 2 * gm.rows * 2) * sizeof(float);
     return p;
 }
 
@@ -870,7 +931,7 @@ cudaError_t launch_variant(const Kv4Decode& a, const Plan& p, cudaStream_t s)
     auto* kernel = a.f.bf16 ? decode_kv4_kernel<CH, NB, true> : decode_kv4_kernel<CH, NB, false>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
     if (e != cudaSuccess) return e;
-    kernel<<<p.gm.ctas, p.gm.NG * p.gm.C * 32, p.smem, s>>>(a, p.gm);
+    kernel<<<p.ctas, (p.gm.NG * p.gm.C + 1) * 32, p.smem, s>>>(a, p.gm);
     return cudaGetLastError();
 }
 
@@ -896,7 +957,7 @@ cudaError_t launch_decode_kv4(const Kv4Decode& a, void* workspace, cudaStream_t 
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(pb.B) * pb.Hq * pb.Nq), (pb.D + 127) / 128);
     cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = p.gm.ctas * sizeof(float);
+    cfg.dynamicSmemBytes = 2 * (p.ctas + 1) * sizeof(float);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
