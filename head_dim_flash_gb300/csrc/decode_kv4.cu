@@ -181,9 +181,10 @@ struct __align__(16) DecShared {
     int abort_flag;
     int last[kMaxGroups][3];          // sequence (-1: none), kv head and row block of the part a group ends with
     float ml[kMaxGroups][16][2];      // its references and sums
+    uint32_t qmax[kComputeWarps][16]; // largest query magnitudes over a warp's chunks
 };
 
-template <int CH, int NB, bool BF16>
+template <int CH, int NB, bool SPLIT, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode a, const Kv4Geo gm)
 {
     pdl_trigger();
@@ -256,6 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
     Piece cur{};
     bool pending = false;  // my group's last part is still in its registers
     const int group = warp / gm.C, wg = warp - group * gm.C;  // my group, my place in it
+    // my chunks are chunk0 .. chunk0 + CH - 1; those before wg * CH are another warp's too, here with queries of zero
+    const int chunk0 = min(wg * CH, gm.chunks - CH);
     float acc[CH][4][NB][4];
     float m[NB][2], l[NB][2];
 
@@ -357,13 +360,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
         RingPos kpos, vpos;
         bool ok = true;
         uint32_t qf[NB][CH][4][2];
-        float c2[NB][2];                 // log2-domain scale of my partial scores
+        float c2[NB][2];                 // log2-domain scale of the scores
         float s[kStepStrips][NB][4];
         uint32_t pf[kStepStrips][NB][2];
-        int tile_at[CH];                 // byte offsets of my chunks (the last one again where I have fewer)
-#pragma unroll
-        for (int c = 0; c < CH; ++c) tile_at[c] = min(wg + c * gm.C, gm.chunks - 1) * kKv4Tile;
-
+        int limits[NB][2];               // first token that my columns' rows do not see
+        int least = 0;                   // and that some row does not see
         // Waits for a copy. One that runs out of time ends the warp's work, not its barriers; another sequence's
         // error in the status word does not end it.
         auto arrived = [&](uint64_t* bar, uint32_t phase, uint32_t site) {
@@ -372,20 +373,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                                                        site, false));
         };
 
-        // S^T of a step over my chunks, scaled to log2 units: left in s (C = 1) or in the exchange buffer
-        auto scores = [&](int ns) {
+        // S^T of a step over my chunks: left in s, or in the exchange buffer. A step of one strip computes on what
+        // the second one's place holds, and masks it.
+        auto scores = [&]() {
             arrived(&sh.full_k[group][kpos.slot], kpos.phase, KS_K);
-            const uint8_t* kb = ring_k + kpos.slot * st_bytes;
+            const uint8_t* kb = ring_k + kpos.slot * st_bytes + chunk0 * kKv4Tile;
 #pragma unroll
             for (int i = 0; i < kStepStrips; ++i) {
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
-                if (i >= ns || !ok) continue;
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    const uint8_t* tile = kb + i * strip_bytes + tile_at[c];
+                    const uint8_t* tile = kb + i * strip_bytes + c * kKv4Tile;
                     const uint4 w = *reinterpret_cast<const uint4*>(tile + lane * 16);
                     const uint32_t sc = *reinterpret_cast<const uint16_t*>(tile + 512 + lane * 2);
                     const uint32_t lo = scale_pair(sc, 0, 0), hi = scale_pair(sc, 1, 1);
@@ -406,66 +407,70 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.empty_k[group][kpos.slot]);
             kpos.advance(gm.stages);
+            if (SPLIT) {
 #pragma unroll
-            for (int i = 0; i < kStepStrips; ++i)
+                for (int i = 0; i < kStepStrips; ++i)
 #pragma unroll
-                for (int n = 0; n < NB; ++n) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i][n][e] *= c2[n][e & 1];
-                    if (gm.C > 1)
+                    for (int n = 0; n < NB; ++n)
                         exch[(eb * gm.C + wg) * kExch + (i * NB + n) * 32] =
                             make_float4(s[i][n][0], s[i][n][1], s[i][n][2], s[i][n][3]);
-                }
+            }
         };
 
         // sums of the partial scores, mask, P^T fragments; tok: the step's first token
-        auto softmax = [&](int ns, int tok) {
-            if (gm.C > 1) {
+        auto softmax = [&](int ns, int tok, bool first) {
+            if (SPLIT) {
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gm.C * 32) : "memory");
+                const float4* x = exch + eb * gm.C * kExch;
 #pragma unroll
                 for (int i = 0; i < kStepStrips; ++i)
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
-                        float4 v = exch[eb * gm.C * kExch + (i * NB + n) * 32];
-                        for (int w = 1; w < gm.C; ++w) {  // one order for every warp: all get the same bits
-                            const float4 x = exch[(eb * gm.C + w) * kExch + (i * NB + n) * 32];
-                            v.x += x.x;
-                            v.y += x.y;
-                            v.z += x.z;
-                            v.w += x.w;
-                        }
-                        s[i][n][0] = v.x;
-                        s[i][n][1] = v.y;
-                        s[i][n][2] = v.z;
-                        s[i][n][3] = v.w;
+                        const float4 v0 = x[(i * NB + n) * 32], v1 = x[kExch + (i * NB + n) * 32];
+                        s[i][n][0] = v0.x + v1.x;
+                        s[i][n][1] = v0.y + v1.y;
+                        s[i][n][2] = v0.z + v1.z;
+                        s[i][n][3] = v0.w + v1.w;
                     }
+                for (int w = 2; w < gm.C; ++w) {  // one order for every warp: all get the same bits
+                    x += w == 2 ? 2 * kExch : kExch;
+#pragma unroll
+                    for (int i = 0; i < kStepStrips; ++i)
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            const float4 v = x[(i * NB + n) * 32];
+                            s[i][n][0] += v.x;
+                            s[i][n][1] += v.y;
+                            s[i][n][2] += v.z;
+                            s[i][n][3] += v.w;
+                        }
+                }
                 eb ^= 1;
             }
-            const int least = pb.causal ? cur.len - pb.Nq + 1 : cur.len;  // first token that some row does not see
+            // scores in log2 units above the reference; keys that a row does not see have none
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int i = 0; i < kStepStrips; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i][n][e] = fmaf(s[i][n][e], c2[n][e & 1], -m[n][e & 1]);
             if (tok + 16 * kStepStrips > least || ns < kStepStrips) {
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        int lim = cur.len;
-                        if (pb.causal) lim = min(lim, least + (cur.rb * gm.rows + n * 8 + 2 * t + q) % pb.Nq);
+                    for (int e = 0; e < 4; ++e)
 #pragma unroll
                         for (int i = 0; i < kStepStrips; ++i)
-#pragma unroll
-                            for (int hi = 0; hi < 2; ++hi)
-                                if (i >= ns || tok + 16 * i + g + 8 * hi >= lim) s[i][n][q + 2 * hi] = -INFINITY;
-                    }
+                            if (i >= ns || tok + 16 * i + g + 8 * (e >> 1) >= limits[n][e & 1]) s[i][n][e] = -INFINITY;
             }
-            bool up = false;
+            float top = -INFINITY;
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float top = m[n][q] + kRefSpan;
+                for (int i = 0; i < kStepStrips; ++i)
 #pragma unroll
-                    for (int i = 0; i < kStepStrips; ++i) up |= s[i][n][q] > top || s[i][n][q + 2] > top;
-                }
-            if (__any_sync(0xffffffffu, up)) {
+                    for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i][n][e]);
+            if (first || __any_sync(0xffffffffu, top > kRefSpan)) {
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -476,10 +481,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float mn = fmaxf(m[n][q], mx - kRefBelow);
-                        const float al = m[n][q] == -INFINITY ? 0.f : ex2_approx(m[n][q] - mn);
-                        m[n][q] = mn;
+                        // how far the reference moves; a row's keys come first, so one without any in the piece's first
+                        // step has none in the piece
+                        float up = mx - kRefBelow;
+                        if (first ? mx == -INFINITY : up < 0.f) up = 0.f;
+                        const float al = first ? 0.f : ex2_approx(-up);
+                        m[n][q] += up;
                         l[n][q] *= al;
+#pragma unroll
+                        for (int i = 0; i < kStepStrips; ++i) {
+                            s[i][n][q] -= up;
+                            s[i][n][q + 2] -= up;
+                        }
 #pragma unroll
                         for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -490,40 +503,39 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                     }
             }
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                float mu[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) mu[q] = m[n][q] == -INFINITY ? 0.f : m[n][q];
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int i = 0; i < kStepStrips; ++i) {
                     float p[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = ex2_approx(s[i][n][e] - mu[e & 1]);
+                    for (int e = 0; e < 4; ++e) p[e] = ex2_approx(s[i][n][e]);
                     l[n][0] += p[0] + p[2];
                     l[n][1] += p[1] + p[3];
                     // fp16 P: half a step of 2^-11, an eighth of what bf16 operands would cost
                     pf[i][n][0] = transpose8x8(pack2<false>(p[0], p[1]));
                     pf[i][n][1] = transpose8x8(pack2<false>(p[2], p[3]));
                 }
-            }
         };
 
         // O^T += V^T P^T over my chunks
         auto values = [&](int ns, int tok) {
             arrived(&sh.full_v[group][vpos.slot], vpos.phase, KS_V);
-            const uint8_t* vb = ring_v + vpos.slot * st_bytes;
+            const uint8_t* vb = ring_v + vpos.slot * st_bytes + chunk0 * kKv4Tile;
 #pragma unroll
             for (int i = 0; i < kStepStrips; ++i) {
-                if (i >= ns || !ok) break;
-                uint32_t keep = 0xffffffffu;  // cells behind the last token hold anything: their scales count as zero
-                if (tok + 16 * i + 16 > cur.len) {
+                // cells behind the last token hold anything, as does the place of a second strip that is not there:
+                // their scales count as zero
+                uint32_t keep = 0xffffffffu;
+                if (i >= ns) {
+                    keep = 0;
+                } else if (tok + 16 * i + 16 > cur.len) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (tok + 16 * i + 2 * t + (j & 1) + 8 * (j >> 1) >= cur.len) keep &= ~(0xffu << (8 * j));
                 }
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    const uint8_t* tile = vb + i * strip_bytes + tile_at[c];
+                    const uint8_t* tile = vb + i * strip_bytes + c * kKv4Tile;
                     const uint4 w = *reinterpret_cast<const uint4*>(tile + lane * 16);
                     const uint32_t sc = *reinterpret_cast<const uint32_t*>(tile + 512 + ((g >> 1) * 4 + t) * 4) & keep;
                     const uint32_t lo = scale_pair(sc, 0, 1), hi = scale_pair(sc, 2, 3);
@@ -556,9 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                     if (cur.rb * gm.rows + r >= R) continue;
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
-                        if (wg + c * gm.C >= gm.chunks) break;
-                        float4* o = reinterpret_cast<float4*>(gm.part + (slot * gm.rows + r) * pb.D +
-                                                              (wg + c * gm.C) * 64 + 8 * g);
+                        if (chunk0 + c < wg * CH) continue;
+                        float4* o = reinterpret_cast<float4*>(gm.part + (slot * gm.rows + r) * pb.D + (chunk0 + c) * 64 + 8 * g);
                         o[0] = make_float4(acc[c][0][n][q], acc[c][0][n][q + 2], acc[c][1][n][q], acc[c][1][n][q + 2]);
                         o[1] = make_float4(acc[c][2][n][q], acc[c][2][n][q + 2], acc[c][3][n][q], acc[c][3][n][q + 2]);
                     }
@@ -575,17 +586,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
             // ---- Q of the piece's rows over my chunks, as B fragments: fp16, scaled by a power of two into its range
             // (bf16 has the wider one). A lane holds query g, head dims 16 t .. 16 t + 15 of every chunk.
             const int r0 = cur.rb * gm.rows;
+            least = pb.causal ? cur.len - pb.Nq + 1 : cur.len;  // first token that some row does not see
+            uint32_t amax[NB];  // magnitudes of 16-bit floats order as their bits do
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 const int r = r0 + n * 8 + g;
                 const int h = cur.hk * G + r / pb.Nq, i = r % pb.Nq;
                 const uint16_t* q = static_cast<const uint16_t*>(a.f.q) + cur.b * pb.vq.sb + h * pb.vq.sh + i * pb.vq.sn;
-                uint32_t amax = 0;  // magnitudes of 16-bit floats order as their bits do
+                amax[n] = 0;
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                    if (r < R && wg + c * gm.C < gm.chunks) {
-                        const uint4* src = reinterpret_cast<const uint4*>(q + (wg + c * gm.C) * 64 + t * 16);
+                    if (r < R && chunk0 + c >= wg * CH) {
+                        const uint4* src = reinterpret_cast<const uint4*>(q + (chunk0 + c) * 64 + t * 16);
                         x = src[0];
                         y = src[1];
                     }
@@ -593,16 +606,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         qf[n][c][e >> 1][e & 1] = w[e];
-                        if (BF16) amax = max(amax, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+                        if (BF16) amax[n] = max(amax[n], max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
                     }
                 }
+                if (BF16) {
+                    amax[n] = max(amax[n], __shfl_xor_sync(0xffffffffu, amax[n], 1));
+                    amax[n] = max(amax[n], __shfl_xor_sync(0xffffffffu, amax[n], 2));
+                    if (SPLIT && t == 0) sh.qmax[warp][n * 8 + g] = amax[n];
+                }
+            }
+            // (the steps of a piece have this barrier too, so the last piece's maxima are read by now)
+            if (BF16 && SPLIT) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gm.C * 32) : "memory");
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
                 float mul = 1.f;
                 if (BF16) {
-                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                    if (SPLIT)
+                        for (int w = 0; w < gm.C; ++w) amax[n] = max(amax[n], sh.qmax[group * gm.C + w][n * 8 + g]);
                     // largest magnitude to [2^14, 2^15); rows of zeros or that are not finite stay as they are
-                    const int e = static_cast<int>(amax >> 7);
-                    if (amax > 0 && e < 255) mul = __uint_as_float(static_cast<uint32_t>(min(14 + 127 - e, 126) + 127) << 23);
+                    const int e = static_cast<int>(amax[n] >> 7);
+                    if (amax[n] > 0 && e < 255) mul = __uint_as_float(static_cast<uint32_t>(min(14 + 127 - e, 126) + 127) << 23);
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -615,7 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     c2[n][e] = __shfl_sync(0xffffffffu, scale, (2 * t + e) * 4);
-                    m[n][e] = -INFINITY;
+                    limits[n][e] = pb.causal ? min(cur.len, least + (r0 + n * 8 + 2 * t + e) % pb.Nq) : cur.len;
+                    m[n][e] = 0.f;
                     l[n][e] = 0.f;
                 }
             }
@@ -629,12 +653,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                         for (int e = 0; e < 4; ++e) acc[c][i][n][e] = 0.f;
 
             // ---- the scores of a step are issued before the values of the one before
-            scores(min(kStepStrips, cur.s1 - cur.s0));
-            for (int at = cur.s0; at < cur.s1; at += kStepStrips) {
-                const int ns = min(kStepStrips, cur.s1 - at);
-                softmax(ns, at * 16);
-                if (at + kStepStrips < cur.s1) scores(min(kStepStrips, cur.s1 - at - kStepStrips));
-                values(ns, at * 16);
+            for (int at = cur.s0;; at += kStepStrips) {
+                const bool in = at < cur.s1;
+                if (in) scores();
+                if (at > cur.s0) values(min(kStepStrips, cur.s1 - at + kStepStrips), (at - kStepStrips) * 16);
+                if (!in) break;
+                softmax(min(kStepStrips, cur.s1 - at), at * 16, at == cur.s0);
             }
 #pragma unroll
             for (int n = 0; n < NB; ++n)
@@ -643,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                     l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 4);
                     l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 8);
                     l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 16);
+                    if (l[n][q] == 0.f) m[n][q] = -INFINITY;  // no keys, no reference
                 }
 
             // ---- a whole unit's outputs, or a part of one
@@ -658,11 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                         uint16_t* o = static_cast<uint16_t*>(a.f.o) + cur.b * pb.vo.sb + h * pb.vo.sh + i * pb.vo.sn;
 #pragma unroll
                         for (int c = 0; c < CH; ++c) {
-                            if (wg + c * gm.C >= gm.chunks) break;
+                            if (chunk0 + c < wg * CH) continue;
                             uint32_t x[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) x[e] = pack2<BF16>(acc[c][e][n][q] * inv, acc[c][e][n][q + 2] * inv);
-                            *reinterpret_cast<uint4*>(o + (wg + c * gm.C) * 64 + 8 * g) = make_uint4(x[0], x[1], x[2], x[3]);
+                            *reinterpret_cast<uint4*>(o + (chunk0 + c) * 64 + 8 * g) = make_uint4(x[0], x[1], x[2], x[3]);
                         }
                         if (wg == 0 && g == 0)
                             a.f.lse[(static_cast<long long>(cur.b) * pb.Hq + h) * pb.Nq + i] =
@@ -749,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
     const int r0 = cur.rb * gm.rows;
     for (int e = group - run0; e < kRegs; e += run1 - run0 + 1) {
         const int c = e / (4 * NB), i = e / NB % 4, n = e % NB;
-        if (wg + c * gm.C >= gm.chunks) break;
+        if (chunk0 + c < wg * CH) continue;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = run0; k <= run1; ++k) {
             const float4 v = buf[(static_cast<size_t>(k * gm.C + wg) * kRegs + e) * 32];
@@ -759,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
             x.w += v.w;
         }
         const int r = n * 8 + 2 * t;
-        float* o = gm.part + (slot * gm.rows + r) * pb.D + (wg + c * gm.C) * 64 + 8 * g + 2 * i;
+        float* o = gm.part + (slot * gm.rows + r) * pb.D + (chunk0 + c) * 64 + 8 * g + 2 * i;
         if (r0 + r < R) *reinterpret_cast<float2*>(o) = make_float2(x.x, x.z);
         if (r0 + r + 1 < R) *reinterpret_cast<float2*>(o + pb.D) = make_float2(x.y, x.w);
     }
@@ -925,14 +950,28 @@ Plan plan(const Problem& pb)
     return p;
 }
 
-template <int CH, int NB>
+template <int CH, int NB, bool SPLIT>
 cudaError_t launch_variant(const Kv4Decode& a, const Plan& p, cudaStream_t s)
 {
-    auto* kernel = a.f.bf16 ? decode_kv4_kernel<CH, NB, true> : decode_kv4_kernel<CH, NB, false>;
+    auto* kernel = a.f.bf16 ? decode_kv4_kernel<CH, NB, SPLIT, true> : decode_kv4_kernel<CH, NB, SPLIT, false>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
     if (e != cudaSuccess) return e;
     kernel<<<p.ctas, (p.gm.NG * p.gm.C + 1) * 32, p.smem, s>>>(a, p.gm);
     return cudaGetLastError();
+}
+
+// The chunks per warp that plan() can give, for one warp per group and for several.
+cudaError_t launch_main(const Kv4Decode& a, const Plan& p, cudaStream_t s)
+{
+    if (p.nb == 1) {
+        if (p.gm.C > 1) return p.ch == 3 ? launch_variant<3, 1, true>(a, p, s) : launch_variant<4, 1, true>(a, p, s);
+        return p.ch == 1   ? launch_variant<1, 1, false>(a, p, s)
+               : p.ch == 2 ? launch_variant<2, 1, false>(a, p, s)
+               : p.ch == 3 ? launch_variant<3, 1, false>(a, p, s)
+                           : launch_variant<4, 1, false>(a, p, s);
+    }
+    if (p.gm.C > 1) return launch_variant<2, 2, true>(a, p, s);
+    return p.ch == 1 ? launch_variant<1, 2, false>(a, p, s) : launch_variant<2, 2, false>(a, p, s);
 }
 
 }  // namespace
@@ -944,14 +983,7 @@ cudaError_t launch_decode_kv4(const Kv4Decode& a, void* workspace, cudaStream_t 
     Plan p = plan(a.f.pb);
     p.gm.part = static_cast<float*>(workspace);
     p.gm.ml = p.gm.part + p.part_floats;
-    cudaError_t e;
-    if (p.nb == 1)
-        e = p.ch == 1   ? launch_variant<1, 1>(a, p, s)
-            : p.ch == 2 ? launch_variant<2, 1>(a, p, s)
-            : p.ch == 3 ? launch_variant<3, 1>(a, p, s)
-                        : launch_variant<4, 1>(a, p, s);
-    else
-        e = p.ch == 1 ? launch_variant<1, 2>(a, p, s) : launch_variant<2, 2>(a, p, s);
+    cudaError_t e = launch_main(a, p, s);
     if (e != cudaSuccess) return e;
     const Problem& pb = a.f.pb;
     cudaLaunchConfig_t cfg{};
