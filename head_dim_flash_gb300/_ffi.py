@@ -160,6 +160,8 @@ def _declare(lib):
 def load(path: str | None = None):
     """Loads (once) and returns the CUDA library; raises if it has not been built."""
     global _lib
+    if path is None and _lib is not None:
+        return _lib
     with _lock:
         if _lib is None or path is not None:
             p = path or LIB_PATH

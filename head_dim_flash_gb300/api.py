@@ -462,46 +462,82 @@ def kv4_cache(num_pages: int, page_size: int, Hkv: int, D: int, device="cuda") -
     return torch.zeros((num_pages, 2, Hkv, page_size // 16, D // 64, KV4_TILE), dtype=torch.uint8, device=device)
 
 
+# The 4-bit cache's calls run once per layer and token on tensors of a few
+# kilobytes, where the host's part is what a call costs: each property of a
+# tensor is read once, and the device is entered only when it is not current.
 def _kv4(cache, block_table, B: int):
-    """The ffpa_kv4_cache of a cache tensor and a block table [B, max_blocks], with Hkv and D."""
-    if cache.dtype != torch.uint8 or cache.dim() != 6 or cache.shape[1] != 2 or cache.shape[5] != KV4_TILE:
-        raise ValueError(f"expected a cache of kv4_cache(), got {cache.dtype} {tuple(cache.shape)}")
-    if not cache.is_cuda or not cache.is_contiguous():
+    """The ffpa_kv4_cache of a cache tensor and a block table [B, max_blocks], with Hkv, D and the device."""
+    shape, dev = cache.shape, cache.device
+    if cache.dtype is not torch.uint8 or len(shape) != 6 or shape[1] != 2 or shape[5] != KV4_TILE:
+        raise ValueError(f"expected a cache of kv4_cache(), got {cache.dtype} {tuple(shape)}")
+    if dev.type != "cuda" or not cache.is_contiguous():
         raise ValueError("the cache must be a contiguous tensor on a CUDA device")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"expected an int32 block_table [{B}, max_blocks], got {block_table.dtype} "
-                         f"{tuple(block_table.shape)}")
-    if block_table.device != cache.device:
+    rows, stride = block_table.shape, block_table.stride()
+    if block_table.dtype is not torch.int32 or len(rows) != 2 or rows[0] != B:
+        raise ValueError(f"expected an int32 block_table [{B}, max_blocks], got {block_table.dtype} {tuple(rows)}")
+    if block_table.device != dev:
         raise ValueError("block_table and cache are on different devices")
-    blocks = block_table.shape[1]
-    if blocks > 1 and block_table.stride(1) != 1 or B > 1 and block_table.stride(0) < blocks:
-        raise ValueError(f"block_table's rows must be contiguous, got strides {block_table.stride()}")
-    stride = block_table.stride(0) if B > 1 else blocks
-    pages, _, Hkv, strips, chunks, _ = cache.shape
-    return _ffi.Kv4Cache(cache.data_ptr(), pages, 16 * strips, block_table.data_ptr(), blocks, stride), Hkv, 64 * chunks
+    blocks = rows[1]
+    if blocks > 1 and stride[1] != 1 or B > 1 and stride[0] < blocks:
+        raise ValueError(f"block_table's rows must be contiguous, got strides {stride}")
+    c = _ffi.Kv4Cache(cache.data_ptr(), shape[0], 16 * shape[3], block_table.data_ptr(), blocks,
+                      stride[0] if B > 1 else blocks)
+    return c, shape[2], 64 * shape[4], dev
 
 
 def _lengths(x, n: int, name: str, device) -> int | None:
     """The address of an optional int32 [n] tensor of lengths on `device`."""
     if x is None:
         return None
-    if x.dtype != torch.int32 or tuple(x.shape) != (n,) or not x.is_contiguous() or x.device != device:
+    if x.dtype is not torch.int32 or x.shape != (n,) or not x.is_contiguous() or x.device != device:
         raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on {device}, got {x.dtype} "
                          f"{tuple(x.shape)} on {x.device}")
     return x.data_ptr()
 
 
-def _kv4_pair(cache, k, v, dims: int, Hkv: int, D: int):
-    if k.dim() != dims or v.shape != k.shape or k.shape[1] != Hkv or k.shape[-1] != D:
-        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not match a cache of Hkv={Hkv}, D={D}")
-    if k.device != cache.device or v.device != cache.device:
+def _kv4_pair(k, v, dims: int, Hkv: int, D: int, device):
+    """The shape of a k, v pair that fits a cache."""
+    shape = k.shape
+    if len(shape) != dims or v.shape != shape or shape[1] != Hkv or shape[-1] != D:
+        raise ValueError(f"k {tuple(shape)} and v {tuple(v.shape)} do not match a cache of Hkv={Hkv}, D={D}")
+    if k.device != device or v.device != device:
         raise ValueError("k, v and the cache must be on one device")
     if k.dtype != v.dtype:
         raise ValueError(f"mixed dtypes {k.dtype} and {v.dtype}")
+    return shape
 
 
-def _stream_of(x: torch.Tensor) -> int:
-    return torch.cuda.current_stream(x.device).cuda_stream
+def _view_or_none(x):
+    """The ffpa_view of a dense 4-D tensor, or None where it has none (as _viewable)."""
+    (B, H, N, _), (sb, sh, sn, sd), p = x.shape, x.stride(), x.data_ptr()
+    if sd != 1 or p & 15 or (sb | sh | sn) & 7 or sb < 0 or sh < 0 or sn < 0:
+        return None
+    if B > 1 and sb == 0 or H > 1 and sh == 0 or N > 1 and sn == 0:
+        return None
+    return _ffi.View(p, sb, sh, sn)
+
+
+def _in_view(x):
+    """(tensor, its ffpa_view) of an input, copied only where no view of it fits."""
+    w = _view_or_none(x)
+    if w is None:
+        x = x.contiguous()
+        w = _view(x)
+    return x, w
+
+
+def _out_view(x):
+    w = _view_or_none(x)
+    return _view(x) if w is None else w  # _view() says what is wrong
+
+
+def _on(device, call, *args) -> int:
+    """call(*args, stream) on `device` and its current stream."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        return call(*args, torch._C._cuda_getCurrentRawStream(i))
+    with torch.cuda.device(device):
+        return call(*args, torch._C._cuda_getCurrentRawStream(i))
 
 
 def kv4_write(cache, block_table, k, v, start=None, count=None) -> None:
@@ -511,12 +547,11 @@ def kv4_write(cache, block_table, k, v, start=None, count=None) -> None:
     k, v: [B, Hkv, N, D]; block_table: int32 [B, max_blocks]; start, count: int32 [B]
     on the device (None: 0 and N)."""
     B = k.shape[0]
-    c, Hkv, D = _kv4(cache, block_table, B)
-    _kv4_pair(cache, k, v, 4, Hkv, D)
-    k, v = _dense(k, v)
-    with torch.cuda.device(cache.device):
-        st = _ffi.ffpa_kv4_write(_dt(k), _view(k), _view(v), c, _lengths(start, B, "start", cache.device),
-                                 _lengths(count, B, "count", cache.device), B, Hkv, k.shape[2], D, _stream_of(cache))
+    c, Hkv, D, dev = _kv4(cache, block_table, B)
+    N = _kv4_pair(k, v, 4, Hkv, D, dev)[2]
+    (k, wk), (v, wv) = _in_view(k), _in_view(v)
+    st = _on(dev, _ffi.load().ffpa_kv4_write, _dt(k), wk, wv, c, _lengths(start, B, "start", dev),
+             _lengths(count, B, "count", dev), B, Hkv, N, D)
     _ffi.raise_for(st, "ffpa_kv4_write")
 
 
@@ -524,14 +559,12 @@ def varlen_kv4_write(cache, block_table, k, v, cu_seqlens, max_seqlen: int, star
     """As kv4_write, for a packed batch: k, v [T, Hkv, D], sequence b's tokens the rows
     [cu_seqlens[b], cu_seqlens[b + 1]) (int32 on the device), at most max_seqlen of them."""
     B = cu_seqlens.numel() - 1
-    c, Hkv, D = _kv4(cache, block_table, B)
-    _kv4_pair(cache, k, v, 3, Hkv, D)
-    k, v = _prep(k, v)
-    with torch.cuda.device(cache.device):
-        st = _ffi.ffpa_varlen_kv4_write(_dt(k), k.data_ptr(), v.data_ptr(), c,
-                                        _lengths(cu_seqlens, B + 1, "cu_seqlens", cache.device),
-                                        _lengths(start, B, "start", cache.device), B, k.shape[0], int(max_seqlen), Hkv,
-                                        D, _stream_of(cache))
+    c, Hkv, D, dev = _kv4(cache, block_table, B)
+    T = _kv4_pair(k, v, 3, Hkv, D, dev)[0]
+    k, v = k.contiguous(), v.contiguous()
+    st = _on(dev, _ffi.load().ffpa_varlen_kv4_write, _dt(k), k.data_ptr(), v.data_ptr(), c,
+             _lengths(cu_seqlens, B + 1, "cu_seqlens", dev), _lengths(start, B, "start", dev), B, T, int(max_seqlen),
+             Hkv, D)
     _ffi.raise_for(st, "ffpa_varlen_kv4_write")
 
 
@@ -543,20 +576,18 @@ def kv4_read(cache, block_table, count, max_count: int | None = None, dtype=torc
     With k_out and v_out given, N is theirs and rows at and past count[b] keep what they
     hold; else N is max_count and those rows are zero."""
     B = block_table.shape[0]
-    c, Hkv, D = _kv4(cache, block_table, B)
+    c, Hkv, D, dev = _kv4(cache, block_table, B)
     if (k_out is None) != (v_out is None) or (k_out is None) == (max_count is None):
         raise ValueError("give either k_out and v_out or max_count")
-    if k_out is None:
-        k_out, v_out = (torch.zeros((B, Hkv, max_count, D), dtype=dtype, device=cache.device) for _ in range(2))
-    _kv4_pair(cache, k_out, v_out, 4, Hkv, D)
-    if k_out.shape[0] != B:
-        raise ValueError(f"k_out has {k_out.shape[0]} sequences, block_table {B}")
     if count is None:
         raise ValueError("count is required")
-    with torch.cuda.device(cache.device):
-        st = _ffi.ffpa_kv4_read(_dt(k_out), c, _view(k_out), _view(v_out), _lengths(start, B, "start", cache.device),
-                                _lengths(count, B, "count", cache.device), B, Hkv, k_out.shape[2], D,
-                                _stream_of(cache))
+    if k_out is None:
+        k_out, v_out = (torch.zeros((B, Hkv, max_count, D), dtype=dtype, device=dev) for _ in range(2))
+    shape = _kv4_pair(k_out, v_out, 4, Hkv, D, dev)
+    if shape[0] != B:
+        raise ValueError(f"k_out has {shape[0]} sequences, block_table {B}")
+    st = _on(dev, _ffi.load().ffpa_kv4_read, _dt(k_out), c, _out_view(k_out), _out_view(v_out),
+             _lengths(start, B, "start", dev), _lengths(count, B, "count", dev), B, Hkv, shape[2], D)
     _ffi.raise_for(st, "ffpa_kv4_read")
     return k_out, v_out
 
@@ -567,21 +598,31 @@ def varlen_kv4_read(cache, block_table, cu_seqlens, max_seqlen: int, total: int 
     values): sequence b's tokens to the rows [cu_seqlens[b], cu_seqlens[b + 1]). T is
     `total` or that of k_out and v_out."""
     B = cu_seqlens.numel() - 1
-    c, Hkv, D = _kv4(cache, block_table, B)
+    c, Hkv, D, dev = _kv4(cache, block_table, B)
     if (k_out is None) != (v_out is None) or (k_out is None) == (total is None):
         raise ValueError("give either k_out and v_out or total")
     if k_out is None:
-        k_out, v_out = (torch.zeros((total, Hkv, D), dtype=dtype, device=cache.device) for _ in range(2))
-    _kv4_pair(cache, k_out, v_out, 3, Hkv, D)
+        k_out, v_out = (torch.zeros((total, Hkv, D), dtype=dtype, device=dev) for _ in range(2))
+    T = _kv4_pair(k_out, v_out, 3, Hkv, D, dev)[0]
     if not k_out.is_contiguous() or not v_out.is_contiguous():
         raise ValueError("k_out and v_out must be contiguous")
-    with torch.cuda.device(cache.device):
-        st = _ffi.ffpa_varlen_kv4_read(_dt(k_out), c, k_out.data_ptr(), v_out.data_ptr(),
-                                       _lengths(cu_seqlens, B + 1, "cu_seqlens", cache.device),
-                                       _lengths(start, B, "start", cache.device), B, k_out.shape[0], int(max_seqlen),
-                                       Hkv, D, _stream_of(cache))
+    st = _on(dev, _ffi.load().ffpa_varlen_kv4_read, _dt(k_out), c, k_out.data_ptr(), v_out.data_ptr(),
+             _lengths(cu_seqlens, B + 1, "cu_seqlens", dev), _lengths(start, B, "start", dev), B, T, int(max_seqlen),
+             Hkv, D)
     _ffi.raise_for(st, "ffpa_varlen_kv4_read")
     return k_out, v_out
+
+
+def decode_kv4_workspace(q, cache) -> torch.Tensor:
+    """Device scratch for decode_fwd_kv4 (uint8, 256-byte aligned by the allocator)."""
+    B, Hq, Nq, D = q.shape
+    with torch.cuda.device(q.device):
+        return _kv4_scratch(_dt(q), B, Hq, cache.shape[2], Nq, D, q.device)
+
+
+def _kv4_scratch(dt, B, Hq, Hkv, Nq, D, device):
+    n = _ffi.load().ffpa_decode_kv4_workspace_bytes(dt, B, Hq, Hkv, Nq, D)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
 def decode_fwd_kv4(q, cache, block_table, seq_lens, causal: bool = False, scale: float | None = None, out=None,
@@ -591,32 +632,41 @@ def decode_fwd_kv4(q, cache, block_table, seq_lens, causal: bool = False, scale:
     the device); causal is bottom-right per sequence. q [B, Hq, Nq, D]; returns (o, lse).
 
     A long chunk of queries goes through varlen_kv4_read and varlen_fwd instead."""
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("expected q [B,Hq,Nq,D]")
-    B, Hq, Nq, D = q.shape
-    c, Hkv, Dc = _kv4(cache, block_table, B)
+    B, Hq, Nq, D = shape
+    c, Hkv, Dc, dev = _kv4(cache, block_table, B)
     if D != Dc:
         raise ValueError(f"q has head dim {D}, the cache {Dc}")
-    if q.device != cache.device:
+    if q.device != dev:
         raise ValueError("q and the cache are on different devices")
     if seq_lens is None:
         raise ValueError("seq_lens is required")
-    (q,) = _dense(q)
-    o = _out_like(q) if out is None else out
-    l = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
-    if o.shape != q.shape or o.dtype != q.dtype or o.device != q.device:
+    q, wq = _in_view(q)
+    dt = _dt(q)
+    if out is None:
+        out = torch.empty_like(q)
+        wo = _view_or_none(out)
+        if wo is None:
+            out = torch.empty(shape, dtype=q.dtype, device=dev)
+            wo = _view(out)
+    elif out.shape != shape or out.dtype != q.dtype or out.device != dev:
         raise ValueError("out must have q's shape, dtype and device")
-    if not l.is_contiguous() or l.dtype != torch.float32 or l.shape != q.shape[:3] or l.device != q.device:
+    else:
+        wo = _out_view(out)
+    if lse is None:
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+    elif not lse.is_contiguous() or lse.dtype != torch.float32 or lse.shape != shape[:3] or lse.device != dev:
         raise ValueError("lse must be a contiguous fp32 [B, Hq, Nq] tensor")
-    with torch.cuda.device(q.device):
-        if workspace is None:
-            n = int(_ffi.ffpa_decode_kv4_workspace_bytes(_dt(q), B, Hq, Hkv, Nq, D))
-            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
-        st = _ffi.ffpa_decode_fwd_kv4(_dt(q), _view(q), c, _lengths(seq_lens, B, "seq_lens", q.device), _view(o),
-                                      l.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                      B, Hq, Hkv, Nq, D, int(bool(causal)), _scale(scale, D), _stream_of(q))
+    args = (B, Hq, Hkv, Nq, D)
+    if workspace is None:
+        workspace = _on(dev, lambda _: _kv4_scratch(dt, *args, dev))  # sized for the SMs of its device
+    st = _on(dev, _ffi.load().ffpa_decode_fwd_kv4, dt, wq, c, _lengths(seq_lens, B, "seq_lens", dev), wo,
+             lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), *args,
+             int(bool(causal)), _scale(scale, D))
     _ffi.raise_for(st, "ffpa_decode_fwd_kv4")
-    return o, l
+    return out, lse
 
 
 def get_status() -> None:

@@ -81,6 +81,14 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Bounded wait for a copy, kept out of the loop's code. A wait that runs out raises the CTA's abort flag, after
+// which no later one waits; another sequence's error in the status word does not end it.
+__device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t phase, volatile int* abort_flag, uint32_t* status,
+                                       uint64_t limit_ns, uint32_t site)
+{
+    if (*abort_flag == 0) mbar_wait(bar, phase, abort_flag, status, limit_ns, site, false);
+}
+
 // 8 x 8 matrix of 16-bit values held as an MMA fragment -> its transpose.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 {
@@ -210,17 +218,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
             if (lane >= d) incl += x;
         }
         if (lane == 31) sh.sums[warp] = incl;
-        if (threadIdx.x == 0) {
-            for (int i = 0; i < gm.NG; ++i)
-                for (int s = 0; s < gm.stages; ++s) {
-                    mbar_init(&sh.full_k[i][s], 1);
-                    mbar_init(&sh.full_v[i][s], 1);
-                    mbar_init(&sh.empty_k[i][s], gm.C);
-                    mbar_init(&sh.empty_v[i][s], gm.C);
-                }
-            sh.abort_flag = 0;
+        if (threadIdx.x < gm.NG * kMaxStages) {
+            uint64_t* bar = &sh.full_k[0][0] + threadIdx.x;
+            constexpr int kSet = kMaxGroups * kMaxStages;  // full_k, full_v, empty_k, empty_v
+            mbar_init(bar, 1);
+            mbar_init(bar + kSet, 1);
+            mbar_init(bar + 2 * kSet, gm.C);
+            mbar_init(bar + 3 * kSet, gm.C);
             fence_barrier_init();
         }
+        if (threadIdx.x == 0) sh.abort_flag = 0;
         __syncthreads();
         total = 0;
         for (int w = 0; w < warps; ++w) {
@@ -326,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                 t0 = global_timer_ns();
                 continue;
             }
-            __nanosleep(40);
+            __nanosleep(150);  // a copy has a whole step of slack
             bool stop = *reinterpret_cast<volatile int*>(&sh.abort_flag) != 0;
             if (global_timer_ns() - t0 > a.f.ctl.limit_ns) {
                 stop = true;
@@ -356,28 +363,30 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
         constexpr int kExch = kStepStrips * NB * 32;  // float4 per warp and buffer
         float4* const exch = reinterpret_cast<float4*>(smem + static_cast<size_t>(gm.NG) * 2 * gm.stages * st_bytes) +
                              group * 2 * gm.C * kExch + lane;
-        int eb = 0;                      // exchange buffer
-        RingPos kpos, vpos;
-        bool ok = true;
+        const int exch_size = gm.C * kExch;  // float4 of one of the two buffers
+        float4* ex = exch;               // the buffer in use
+        // ring places: byte offset of the stage, its barrier and the barrier's parity
+        const uint8_t *kp = ring_k, *vp = ring_v;
+        uint64_t *kb_full = sh.full_k[group], *vb_full = sh.full_v[group];
+        uint32_t k_phase = 0, v_phase = 0;
+        constexpr int kEmpty = 2 * kMaxGroups * kMaxStages;  // from a full barrier to its empty one
         uint32_t qf[NB][CH][4][2];
         float c2[NB][2];                 // log2-domain scale of the scores
         float s[kStepStrips][NB][4];
         uint32_t pf[kStepStrips][NB][2];
         int limits[NB][2];               // first token that my columns' rows do not see
         int least = 0;                   // and that some row does not see
-        // Waits for a copy. One that runs out of time ends the warp's work, not its barriers; another sequence's
-        // error in the status word does not end it.
         auto arrived = [&](uint64_t* bar, uint32_t phase, uint32_t site) {
-            if (ok)
-                ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns,
-                                                       site, false));
+            if (!mbar_try_wait(smem_u32(bar), phase))
+                wait_slow(bar, phase, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns, site);
+            __syncwarp();
         };
 
         // S^T of a step over my chunks: left in s, or in the exchange buffer. A step of one strip computes on what
         // the second one's place holds, and masks it.
         auto scores = [&]() {
-            arrived(&sh.full_k[group][kpos.slot], kpos.phase, KS_K);
-            const uint8_t* kb = ring_k + kpos.slot * st_bytes + chunk0 * kKv4Tile;
+            arrived(kb_full, k_phase, KS_K);
+            const uint8_t* kb = kp + chunk0 * kKv4Tile;
 #pragma unroll
             for (int i = 0; i < kStepStrips; ++i) {
 #pragma unroll
@@ -405,14 +414,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.empty_k[group][kpos.slot]);
-            kpos.advance(gm.stages);
+            if (lane == 0) mbar_arrive(kb_full + kEmpty);
+            kp += st_bytes;
+            ++kb_full;
+            if (kp == ring_v) {
+                kp = ring_k;
+                kb_full -= gm.stages;
+                k_phase ^= 1u;
+            }
             if (SPLIT) {
 #pragma unroll
                 for (int i = 0; i < kStepStrips; ++i)
 #pragma unroll
                     for (int n = 0; n < NB; ++n)
-                        exch[(eb * gm.C + wg) * kExch + (i * NB + n) * 32] =
+                        ex[wg * kExch + (i * NB + n) * 32] =
                             make_float4(s[i][n][0], s[i][n][1], s[i][n][2], s[i][n][3]);
             }
         };
@@ -421,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
         auto softmax = [&](int ns, int tok, bool first) {
             if (SPLIT) {
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gm.C * 32) : "memory");
-                const float4* x = exch + eb * gm.C * kExch;
+                const float4* x = ex;
 #pragma unroll
                 for (int i = 0; i < kStepStrips; ++i)
 #pragma unroll
@@ -445,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                             s[i][n][3] += v.w;
                         }
                 }
-                eb ^= 1;
+                ex = ex == exch ? exch + exch_size : exch;
             }
             // scores in log2 units above the reference; keys that a row does not see have none
 #pragma unroll
@@ -519,8 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
 
         // O^T += V^T P^T over my chunks
         auto values = [&](int ns, int tok) {
-            arrived(&sh.full_v[group][vpos.slot], vpos.phase, KS_V);
-            const uint8_t* vb = ring_v + vpos.slot * st_bytes + chunk0 * kKv4Tile;
+            arrived(vb_full, v_phase, KS_V);
+            const uint8_t* vb = vp + chunk0 * kKv4Tile;
 #pragma unroll
             for (int i = 0; i < kStepStrips; ++i) {
                 // cells behind the last token hold anything, as does the place of a second strip that is not there:
@@ -554,8 +569,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.empty_v[group][vpos.slot]);
-            vpos.advance(gm.stages);
+            if (lane == 0) mbar_arrive(vb_full + kEmpty);
+            vp += st_bytes;
+            ++vb_full;
+            if (vp == ring_v + gm.stages * st_bytes) {
+                vp = ring_v;
+                vb_full -= gm.stages;
+                v_phase ^= 1u;
+            }
         };
 
         // a part of the piece's rows to a slot of the workspace
