@@ -16,15 +16,18 @@
 //     exchanging the converted halves would. The operands of both products are
 //     fp16 for either element type: cached values and (power-of-two scaled)
 //     queries are exact.
-//   - a group of C warps works on a strip of tokens, each warp on up to four
-//     64-wide head-dim chunks of it: partial scores are exchanged through shared
-//     memory (none when C = 1), the softmax is computed by every warp, and O^T
-//     stays in registers. One CTA per SM holds NG groups.
-//   - a producer warp, one lane per group, streams the strips by bulk copies into
-//     a K ring and a V ring per group.
+//   - a group of C warps works on a step of C * SW strips of 16 tokens. For the
+//     scores each warp takes SW strips over the whole head dim, so a softmax is
+//     computed once and its scores are never exchanged; for the values it takes
+//     two 64-wide head-dim chunks over all strips, so O^T stays in registers
+//     (32 for eight rows: 16 warps per SM). Between the two, P goes through
+//     shared memory as ready operands. One barrier per step.
+//   - each warp loads the strips it scores, K and V, by bulk copies: K into a
+//     place of its own as soon as its scores are done, V when the step's barrier
+//     says that the last values are.
 //   - the softmax keeps a reference instead of the running maximum: it moves (and
-//     O is rescaled) only when a score passes it by 2^14, so that the usual step
-//     is one vote. P <= 2^14 and its row's largest is >= 2^6 in fp16.
+//     O is rescaled) only when a score passes it by 2^14. P <= 2^14 and its row's
+//     largest is >= 2^6 in fp16.
 //   - the strips of all (sequence, kv head, row block) units form one line, cut
 //     into equal ranges, one per group: lengths live on the device, so the cut is
 //     made there. A unit counts kUnitCost strips more than it has, for its start
@@ -37,17 +40,14 @@
 namespace ffpa {
 namespace {
 
-constexpr int kComputeWarps = 11;  // at most, and one producer warp: 168 registers per thread
-constexpr int kThreads = (kComputeWarps + 1) * 32;
-constexpr int kMaxStages = 4;
-constexpr int kMaxGroups = kComputeWarps;
-constexpr int kStepStrips = 2;     // strips of 16 tokens per step
+constexpr int kMaxWarps = 16;
+constexpr int kMaxDepth = 2;       // places per strip in the K and V buffers
 constexpr int kUnitCost = 4;       // strips' worth of a unit's start and end
 constexpr float kRefBelow = 6.f;   // the reference lies this far (log2) below the maximum it was taken from
 constexpr float kRefSpan = 14.f;   // and is kept until a score is this far above it
 constexpr float kLn2 = 0.693147180559945309f;
 
-enum Kv4Site : uint32_t { KS_K = 0x7b, KS_V, KS_PROD, KS_DRAIN };
+enum Kv4Site : uint32_t { KS_K = 0x7b, KS_V, KS_DRAIN };
 
 struct Kv4Geo {
     int chunks;      // D / 64
@@ -55,14 +55,12 @@ struct Kv4Geo {
     int NG;          // groups per CTA
     int rblocks;     // blocks of `rows` query rows per kv head's group of G * Nq
     int rows;        // 8 or 16
-    int stages;
+    int depth;       // places per strip
+    int group_bytes; // shared memory of one group
     int workers;     // groups of the whole grid
     float* part;     // [workers][2][rows][D] unnormalised partial O
     float* ml;       // [workers][2][rows][2] reference (log2) and sum
 };
-
-// K or V of a step
-__host__ __device__ inline int stage_bytes(int chunks) { return kStepStrips * chunks * kKv4Tile; }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
 {
@@ -83,10 +81,10 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
 
 // Bounded wait for a copy, kept out of the loop's code. A wait that runs out raises the CTA's abort flag, after
 // which no later one waits; another sequence's error in the status word does not end it.
-__device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t phase, volatile int* abort_flag, uint32_t* status,
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t phase, volatile int* abort_flag, uint32_t* status,
                                        uint64_t limit_ns, uint32_t site)
 {
-    if (*abort_flag == 0) mbar_wait(bar, phase, abort_flag, status, limit_ns, site, false);
+    return *abort_flag == 0 && mbar_wait(bar, phase, abort_flag, status, limit_ns, site, false);
 }
 
 // 8 x 8 matrix of 16-bit values held as an MMA fragment -> its transpose.
@@ -180,23 +178,95 @@ __device__ __forceinline__ bool next_piece(const Kv4Decode& a, const Kv4Geo& gm,
     return p.s1 > 0;
 }
 
-struct __align__(16) DecShared {
-    uint64_t full_k[kMaxGroups][kMaxStages], full_v[kMaxGroups][kMaxStages];
-    uint64_t empty_k[kMaxGroups][kMaxStages], empty_v[kMaxGroups][kMaxStages];
-    long long sums[kThreads / 32];
-    long long first_at[kMaxGroups];   // place where the units of each group's first sequence begin
-    int first_b[kMaxGroups];
-    int abort_flag;
-    int last[kMaxGroups][3];          // sequence (-1: none), kv head and row block of the part a group ends with
-    float ml[kMaxGroups][16][2];      // its references and sums
-    uint32_t qmax[kComputeWarps][16]; // largest query magnitudes over a warp's chunks
+// Strips [s, s + n) of a sequence's head: the head's K tiles in page 0, the block table's entry and the place in its
+// page of the first one. n = 0: none in this step, n < 0: no step.
+struct Strips {
+    const uint8_t* head;
+    const int* row;
+    int s, in, page, n;
 };
 
-template <int CH, int NB, bool SPLIT, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode a, const Kv4Geo gm)
+// What a warp's lane 0 keeps of its loads.
+struct Loader {
+    Piece piece;
+    Strips next, issued, loaded;  // of the next step; of the step whose K was issued last; whose V is next
+    bool more;
+    int step_blk, step_in;        // a step's strips in pages and strips
+    uint32_t k_armed, v_armed;    // parities of the uses of each place
+};
+
+struct __align__(16) DecShared {
+    uint64_t full_k[kMaxWarps][kMaxDepth];  // per warp
+    uint64_t full_v[kMaxWarps][kMaxDepth];  // per group
+    long long sums[kMaxWarps];
+    long long first_at[kMaxWarps];    // place where the units of each group's first sequence begin
+    int first_b[kMaxWarps];
+    Loader load[kMaxWarps];
+    int abort_flag;
+    int up[kMaxWarps][2];             // per group and step parity: the last step in which a score passed the reference
+    int last[kMaxWarps][3];           // sequence (-1: none), kv head and row block of the part a group ends with
+    float ml[kMaxWarps][16][2];       // its references and sums
+    float col[kMaxWarps][16];         // per warp and row: largest query magnitude or score
+    float sum[kMaxWarps][16];         // per warp and row: sum of its P
+};
+
+// A operands of a K tile: four matrix steps of 16 tokens x 16 head dims.
+__device__ __forceinline__ void k_tile(const uint8_t* tile, int lane, uint32_t (&a)[4][4])
+{
+    const uint4 w = *reinterpret_cast<const uint4*>(tile + lane * 16);
+    const uint32_t sc = *reinterpret_cast<const uint16_t*>(tile + 512 + lane * 2);
+    const uint32_t lo = scale_pair(sc, 0, 0), hi = scale_pair(sc, 1, 1);
+    uint32_t x[4], y[4];
+    kv4_dequant8(w.x, lo, x);
+    kv4_dequant8(w.z, hi, y);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        a[k][0] = x[2 * k];
+        a[k][1] = y[2 * k];
+        a[k][2] = x[2 * k + 1];
+        a[k][3] = y[2 * k + 1];
+    }
+    kv4_dequant8(w.y, lo, x);
+    kv4_dequant8(w.w, hi, y);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        a[2 + k][0] = x[2 * k];
+        a[2 + k][1] = y[2 * k];
+        a[2 + k][2] = x[2 * k + 1];
+        a[2 + k][3] = y[2 * k + 1];
+    }
+}
+
+// A operands of a V tile: four blocks of 16 head dims x 16 tokens. keep: bytes of the four tokens' scales that count.
+__device__ __forceinline__ void v_tile(const uint8_t* tile, int lane, uint32_t keep, uint32_t (&a)[4][4])
+{
+    const uint4 w = *reinterpret_cast<const uint4*>(tile + lane * 16);
+    const uint32_t sc = *reinterpret_cast<const uint32_t*>(tile + 512 + ((lane >> 3) * 4 + (lane & 3)) * 4) & keep;
+    const uint32_t lo = scale_pair(sc, 0, 1), hi = scale_pair(sc, 2, 3);
+    uint32_t even, odd, x[4];
+    interleave(w.x, w.y, even, odd);
+    kv4_dequant8(even, lo, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e][0] = x[e];
+    kv4_dequant8(odd, lo, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e][1] = x[e];
+    interleave(w.z, w.w, even, odd);
+    kv4_dequant8(even, hi, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e][2] = x[e];
+    kv4_dequant8(odd, hi, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e][3] = x[e];
+}
+
+// CH: chunks per warp; NB: blocks of eight query rows; SW: strips that a warp scores per step.
+template <int CH, int NB, int SW>
+__global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(const Kv4Decode a, const Kv4Geo gm)
 {
     pdl_trigger();
     const Problem& pb = a.f.pb;
+    const bool bf16 = a.f.bf16 != 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int warps = blockDim.x >> 5;
     const int G = pb.Hq / pb.Hkv, R = G * pb.Nq;
@@ -218,15 +288,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
             if (lane >= d) incl += x;
         }
         if (lane == 31) sh.sums[warp] = incl;
-        if (threadIdx.x < gm.NG * kMaxStages) {
-            uint64_t* bar = &sh.full_k[0][0] + threadIdx.x;
-            constexpr int kSet = kMaxGroups * kMaxStages;  // full_k, full_v, empty_k, empty_v
-            mbar_init(bar, 1);
-            mbar_init(bar + kSet, 1);
-            mbar_init(bar + 2 * kSet, gm.C);
-            mbar_init(bar + 3 * kSet, gm.C);
+        if (threadIdx.x < kMaxWarps * kMaxDepth) {
+            mbar_init(&sh.full_k[0][0] + threadIdx.x, 1);
+            mbar_init(&sh.full_v[0][0] + threadIdx.x, gm.C);
+            (&sh.up[0][0])[threadIdx.x] = 0;
             fence_barrier_init();
         }
+        if (threadIdx.x < kMaxWarps) sh.last[threadIdx.x][0] = -1;
         if (threadIdx.x == 0) sh.abort_flag = 0;
         __syncthreads();
         total = 0;
@@ -255,500 +323,530 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
     }
     if (static_cast<long long>(blockIdx.x) * gm.NG * chunk >= total) return;
 
-    const int st_bytes = stage_bytes(gm.chunks), strip_bytes = gm.chunks * kKv4Tile;
-    auto range = [&](int grp, Piece& p) {
-        const long long at = (static_cast<long long>(blockIdx.x) * gm.NG + grp) * chunk;
-        return first_piece(a, gm, p, at, min(at + chunk, total), sh.first_b[grp], sh.first_at[grp]);
-    };
-
-    Piece cur{};
-    bool pending = false;  // my group's last part is still in its registers
     const int group = warp / gm.C, wg = warp - group * gm.C;  // my group, my place in it
-    // my chunks are chunk0 .. chunk0 + CH - 1; those before wg * CH are another warp's too, here with queries of zero
+    const int steps = gm.C * SW;                              // strips per step
+    const int strip_bytes = gm.chunks * kKv4Tile;
+    // my chunks are chunk0 .. chunk0 + CH - 1; those before wg * CH are another warp's too and are not stored
     const int chunk0 = min(wg * CH, gm.chunks - CH);
-    float acc[CH][4][NB][4];
-    float m[NB][2], l[NB][2];
+    // shared memory of the group: K places [depth][strips], V places, Q operands [chunks][NB][2][32] of 16 bytes,
+    // P operands [2][strips][NB][32] of 8 bytes
+    uint8_t* const base = smem + static_cast<size_t>(group) * gm.group_bytes;
+    const int place_bytes = steps * strip_bytes;
+    uint8_t* const k_mem = base + wg * SW * strip_bytes;
+    uint8_t* const v_mem = base + gm.depth * place_bytes;
+    uint4* const q_mem = reinterpret_cast<uint4*>(v_mem + gm.depth * place_bytes) + lane;
+    uint2* const p_mem = reinterpret_cast<uint2*>(q_mem - lane + gm.chunks * NB * 64) + lane;
+    uint64_t *const full_k = sh.full_k[warp], *const full_v = sh.full_v[group];
 
-    if (warp == warps - 1) {
-        // ------------------------------------------------------------ producer: one lane per group
-        bool more = lane < gm.NG;
-        if (more) more = range(lane, cur);
-        uint8_t* const ring_k = smem + static_cast<size_t>(lane) * 2 * gm.stages * st_bytes;
-        uint8_t* const ring_v = ring_k + gm.stages * st_bytes;
-        const int spp = a.cache.page_size >> 4;  // strips per page
-        const size_t v_off = static_cast<size_t>(pb.Hkv) * spp * strip_bytes, page_bytes = 2 * v_off;
-        int s = cur.s0, slot = 0, loads = 0;     // next strip; steps whose K was issued, with ring slot and parity
-        uint32_t phase = 1;
-        bool v_next = false;                     // K of the step is issued, its V is not
-        const uint8_t *src0 = nullptr, *src1 = nullptr;
-        int ns = 0;
-        bool joint = false;                      // the two strips are neighbours in a page
-        uint64_t t0 = global_timer_ns();
-        while (__any_sync(0xffffffffu, more)) {
-            bool moved = false;
-            if (more) {
-                uint64_t* empty = v_next ? &sh.empty_v[lane][slot] : &sh.empty_k[lane][slot];
-                if (mbar_test(empty, phase)) {
-                    moved = true;
-                    uint64_t* bar = v_next ? &sh.full_v[lane][slot] : &sh.full_k[lane][slot];
-                    uint8_t* dst = (v_next ? ring_v : ring_k) + slot * st_bytes;
-                    if (!v_next) {
-                        const int* row = a.cache.table + cur.b * a.cache.table_stride;
-                        const int blk0 = s / spp, in0 = s - blk0 * spp;
-                        ns = min(kStepStrips, cur.s1 - s);
-                        joint = ns == 2 && in0 + 1 < spp;
-                        const int blk1 = ns == 2 && !joint ? blk0 + 1 : blk0, in1 = joint ? in0 + 1 : 0;
-                        int page0 = row[blk0], page1 = row[blk1];
-                        if (static_cast<unsigned>(page0) >= static_cast<unsigned>(a.cache.num_pages) ||
-                            static_cast<unsigned>(page1) >= static_cast<unsigned>(a.cache.num_pages)) {
-                            // the sequence's rows are undefined, but the copies stay inside the cache
-                            kv4_invalid(a.f.ctl.status, VS_KV4_DECODE, cur.b);
-                            page0 = page1 = 0;
-                        }
-                        const uint8_t* head = a.cache.data + static_cast<size_t>(cur.hk) * spp * strip_bytes;
-                        src0 = head + page0 * page_bytes + static_cast<size_t>(in0) * strip_bytes;
-                        src1 = head + page1 * page_bytes + static_cast<size_t>(in1) * strip_bytes;
-                    }
-                    const size_t off = v_next ? v_off : 0;
-                    mbar_arrive_expect_tx(bar, ns * strip_bytes);
-                    bulk_load(dst, src0 + off, (joint ? 2 : 1) * strip_bytes, bar);
-                    if (ns == 2 && !joint) bulk_load(dst + strip_bytes, src1 + off, strip_bytes, bar);
-                    if (!v_next) {
-                        ++loads;
-                    } else {
-                        s += ns;
-                        if (++slot == gm.stages) {
-                            slot = 0;
-                            phase ^= 1u;
-                        }
-                        if (s >= cur.s1) {
-                            more = next_piece(a, gm, cur);
-                            s = 0;
-                        }
-                    }
-                    v_next = !v_next;
-                }
-            }
-            if (__any_sync(0xffffffffu, moved)) {
-                t0 = global_timer_ns();
-                continue;
-            }
-            __nanosleep(150);  // a copy has a whole step of slack
-            bool stop = *reinterpret_cast<volatile int*>(&sh.abort_flag) != 0;
-            if (global_timer_ns() - t0 > a.f.ctl.limit_ns) {
-                stop = true;
-                if (lane == 0) atomicCAS(a.f.ctl.status, 0u, DEV_TIMEOUT | (KS_PROD << 8) | (blockIdx.x << 16));
-            }
-            if (__any_sync(0xffffffffu, stop)) {
-                // copies in flight end before the CTA does
-                sh.abort_flag = 1;
-                if (lane < gm.NG)
-                    for (int k = max(0, loads - gm.stages); k < loads; ++k) {
-                        const uint32_t ph = static_cast<uint32_t>((k / gm.stages) & 1);
-                        mbar_wait(&sh.full_k[lane][k % gm.stages], ph, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns,
-                                  KS_DRAIN, false);
-                        if (k + 1 < loads || !v_next)
-                            mbar_wait(&sh.full_v[lane][k % gm.stages], ph, &sh.abort_flag, a.f.ctl.status,
-                                      a.f.ctl.limit_ns, KS_DRAIN, false);
-                    }
-                break;
+    auto group_sync = [&]() {
+        if (SW == 4)  // groups of one warp
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gm.C * 32) : "memory");
+    };
+    Piece cur{};
+    bool more;
+    {
+        const long long at = (static_cast<long long>(blockIdx.x) * gm.NG + group) * chunk;
+        more = first_piece(a, gm, cur, at, min(at + chunk, total), sh.first_b[group], sh.first_at[group]);
+    }
+
+    // ---- loads of my strips, `depth` steps ahead (lane 0). The place of the next step's strips in the block table
+    // moves by steps without a division, and its page is fetched a step early.
+    const int spp = a.cache.page_size >> 4;  // strips per page
+    const size_t v_off = static_cast<size_t>(pb.Hkv) * spp * strip_bytes, page_bytes = 2 * v_off;
+    Loader& ld = sh.load[warp];
+    auto valid_page = [&](int page, int b) {
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.num_pages)) return page;
+        // the sequence's rows are undefined, but the copies stay inside the cache
+        kv4_invalid(a.f.ctl.status, VS_KV4_DECODE, b);
+        return 0;
+    };
+    auto begin_piece = [&]() {
+        ld.next.s = ld.piece.s0 + wg * SW;
+        const int blk = ld.next.s / spp;
+        ld.next.in = ld.next.s - blk * spp;
+        ld.next.row = a.cache.table + ld.piece.b * a.cache.table_stride + blk;
+        ld.next.head = a.cache.data + static_cast<size_t>(ld.piece.hk) * spp * strip_bytes;
+        if (ld.next.s < ld.piece.s1) ld.next.page = valid_page(*ld.next.row, ld.piece.b);
+    };
+    auto copy = [&](const Strips& x, size_t off, uint8_t* dst, uint64_t* bar) {
+        int run = SW == 1 ? 1 : min(x.n, spp - x.in);
+        bulk_load(dst, x.head + off + x.page * page_bytes + static_cast<size_t>(x.in) * strip_bytes, run * strip_bytes, bar);
+        if (SW > 1) {
+            const int* row = x.row;
+            for (int done = run; done < x.n; done += run) {
+                run = min(x.n - done, spp);
+                bulk_load(dst + done * strip_bytes, x.head + off + valid_page(*++row, ld.piece.b) * page_bytes,
+                          run * strip_bytes, bar);
             }
         }
-        if (lane < gm.NG) sh.last[lane][0] = -1;
-        __syncwarp();
-    } else {
-        // ------------------------------------------------------------ compute warps
-        const uint8_t* const ring_k = smem + static_cast<size_t>(group) * 2 * gm.stages * st_bytes;
-        const uint8_t* const ring_v = ring_k + gm.stages * st_bytes;
-        constexpr int kExch = kStepStrips * NB * 32;  // float4 per warp and buffer
-        float4* const exch = reinterpret_cast<float4*>(smem + static_cast<size_t>(gm.NG) * 2 * gm.stages * st_bytes) +
-                             group * 2 * gm.C * kExch + lane;
-        const int exch_size = gm.C * kExch;  // float4 of one of the two buffers
-        float4* ex = exch;               // the buffer in use
-        // ring places: byte offset of the stage, its barrier and the barrier's parity
-        const uint8_t *kp = ring_k, *vp = ring_v;
-        uint64_t *kb_full = sh.full_k[group], *vb_full = sh.full_v[group];
-        uint32_t k_phase = 0, v_phase = 0;
-        constexpr int kEmpty = 2 * kMaxGroups * kMaxStages;  // from a full barrier to its empty one
-        uint32_t qf[NB][CH][4][2];
-        float c2[NB][2];                 // log2-domain scale of the scores
-        float s[kStepStrips][NB][4];
-        uint32_t pf[kStepStrips][NB][2];
-        int limits[NB][2];               // first token that my columns' rows do not see
-        int least = 0;                   // and that some row does not see
-        auto arrived = [&](uint64_t* bar, uint32_t phase, uint32_t site) {
-            if (!mbar_try_wait(smem_u32(bar), phase))
-                wait_slow(bar, phase, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns, site);
-            __syncwarp();
-        };
+    };
+    // K of my strips of the next step
+    auto load_k = [&](int place) {
+        Strips x = ld.next;
+        x.n = ld.more ? max(0, min(SW, ld.piece.s1 - x.s)) : -1;
+        if (x.n > 0) {
+            ld.k_armed ^= 1u << place;
+            mbar_arrive_expect_tx(&full_k[place], x.n * strip_bytes);
+            copy(x, 0, k_mem + place * place_bytes, &full_k[place]);
+        }
+        ld.issued = x;
+        if (!ld.more) return;
+        x.s += steps;
+        if (x.s - wg * SW < ld.piece.s1) {
+            x.row += ld.step_blk;
+            x.in += ld.step_in;
+            if (x.in >= spp) {
+                x.in -= spp;
+                ++x.row;
+            }
+            if (x.s < ld.piece.s1) x.page = valid_page(*x.row, ld.piece.b);
+            ld.next = x;
+        } else {
+            ld.more = next_piece(a, gm, ld.piece);
+            if (ld.more) begin_piece();
+        }
+    };
+    // V of strips whose K was issued
+    auto load_v = [&](const Strips& x, int place) {
+        if (x.n < 0) return;
+        ld.v_armed ^= 1u << place;
+        mbar_arrive_expect_tx(&full_v[place], x.n * strip_bytes);
+        if (x.n > 0) copy(x, v_off, v_mem + place * place_bytes + wg * SW * strip_bytes, &full_v[place]);
+    };
+    if (lane == 0) {
+        ld.piece = cur;
+        ld.more = more;
+        ld.k_armed = ld.v_armed = 0;
+        ld.step_blk = steps / spp;
+        ld.step_in = steps - ld.step_blk * spp;
+        if (more) {
+            begin_piece();
+            for (int i = 0; i < gm.depth; ++i) {
+                load_k(i);
+                load_v(ld.issued, i);
+            }
+        }
+        ld.loaded.n = -1;
+    }
+    __syncwarp();
 
-        // S^T of a step over my chunks: left in s, or in the exchange buffer. A step of one strip computes on what
-        // the second one's place holds, and masks it.
-        auto scores = [&]() {
-            arrived(kb_full, k_phase, KS_K);
-            const uint8_t* kb = kp + chunk0 * kKv4Tile;
+    // Waits for a copy. After one that ran out of time no more are issued, the group's barriers go on.
+    auto arrived = [&](uint64_t* bar, uint32_t phase, uint32_t site) {
+        if (!mbar_try_wait(smem_u32(bar), phase) &&
+            !wait_slow(bar, phase, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns, site)) {
+            if (lane == 0) {
+                ld.more = false;
+                ld.loaded.n = ld.issued.n = -1;
+            }
+        }
+        __syncwarp();
+    };
+
+    bool pending = false;  // my group's last part is still in its registers
+    float acc[CH][4][NB][4];
+    float m[NB][2], l[NB][2];
+    int step = 0;                       // steps begun by my group
+    int k_place = 0, v_place = 0;
+    uint32_t k_used = 0, v_phase = 0;   // parities of my K places' uses; of the V places' round
+    float s[SW][NB][4], c2[NB][2];
+    int limits[NB][2], least = 0;       // first token that my columns' rows do not see, and that some row does not see
+
+    // S^T of my strips
+    auto scores = [&](int n) {
+        float sum[SW == 1 ? 2 : 1][SW][NB][4];  // two chains where there is one strip
 #pragma unroll
-            for (int i = 0; i < kStepStrips; ++i) {
+        for (int x = 0; x < (SW == 1 ? 2 : 1); ++x)
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
+            for (int i = 0; i < SW; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+                for (int k = 0; k < NB; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[x][i][k][e] = 0.f;
+        if (n > 0) {
+            arrived(&full_k[k_place], (k_used >> k_place) & 1u, KS_K);
+            const uint8_t* tile = k_mem + k_place * place_bytes;
+            const uint4* q = q_mem;
+            auto one = [&](float (&to)[SW][NB][4]) {
+                uint4 q0[NB], q1[NB];
+#pragma unroll
+                for (int k = 0; k < NB; ++k) {
+                    q0[k] = q[k * 64];
+                    q1[k] = q[k * 64 + 32];
+                }
+#pragma unroll
+                for (int i = 0; i < SW; ++i) {
+                    uint32_t x[4][4];
+                    k_tile(tile + i * strip_bytes, lane, x);
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) {
+                        mma_f16_16816(to[i][k], x[0][0], x[0][1], x[0][2], x[0][3], q0[k].x, q0[k].y);
+                        mma_f16_16816(to[i][k], x[1][0], x[1][1], x[1][2], x[1][3], q0[k].z, q0[k].w);
+                        mma_f16_16816(to[i][k], x[2][0], x[2][1], x[2][2], x[2][3], q1[k].x, q1[k].y);
+                        mma_f16_16816(to[i][k], x[3][0], x[3][1], x[3][2], x[3][3], q1[k].z, q1[k].w);
+                    }
+                }
+                tile += kKv4Tile;
+                q += NB * 64;
+            };
+            if (CH == 1) {
+                one(sum[0]);
+            } else {
+                int c = 0;
+                for (; c + 1 < gm.chunks; c += 2) {
+                    one(sum[0]);
+                    one(sum[SW == 1 ? 1 : 0]);
+                }
+                if (c < gm.chunks) one(sum[0]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < SW; ++i)
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[i][k][e] = SW == 1 ? sum[0][i][k][e] + sum[SW == 1 ? 1 : 0][i][k][e] : sum[0][i][k][e];
+    };
+    // P of my strips as operands to the step's buffer; their sums
+    float dl[NB][2];
+    auto store_p = [&]() {
+        uint2* p = p_mem + ((step & 1) * steps + wg * SW) * NB * 32;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) dl[k][0] = dl[k][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < SW; ++i)
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = ex2_approx(s[i][k][e]);
+                dl[k][0] += x[0] + x[2];
+                dl[k][1] += x[1] + x[3];
+                // fp16 P: half a step of 2^-11, an eighth of what bf16 operands would cost
+                p[(i * NB + k) * 32] = make_uint2(transpose8x8(pack2<false>(x[0], x[1])), transpose8x8(pack2<false>(x[2], x[3])));
+            }
+    };
+    // O^T += V^T P^T over my chunks, for the n strips of step `of`, whose first token is tok
+    auto values = [&](int n, int tok, int of) {
+        arrived(&full_v[v_place], v_phase, KS_V);
+        const uint8_t* tile = v_mem + v_place * place_bytes + chunk0 * kKv4Tile;
+        const uint2* p = p_mem + (of & 1) * steps * NB * 32;
+        // cells behind the last token hold anything: their scales count as zero
+        const int tail = cur.len - tok - 16 * (n - 1);
+        uint32_t last_keep = 0xffffffffu;
+        if (tail < 16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (2 * t + (j & 1) + 8 * (j >> 1) >= tail) last_keep &= ~(0xffu << (8 * j));
+        }
+#pragma unroll 2
+        for (int i = 0; i < n; ++i) {
+            uint2 pf[NB];
+#pragma unroll
+            for (int k = 0; k < NB; ++k) pf[k] = p[k * 32];
+            const uint32_t keep = i == n - 1 ? last_keep : 0xffffffffu;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                uint32_t x[4][4];
+                v_tile(tile + c * kKv4Tile, lane, keep, x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int k = 0; k < NB; ++k)
+                        mma_f16_16816(acc[c][e][k], x[e][0], x[e][1], x[e][2], x[e][3], pf[k].x, pf[k].y);
+            }
+            tile += strip_bytes;
+            p += NB * 32;
+        }
+        if (++v_place == gm.depth) {
+            v_place = 0;
+            v_phase ^= 1u;
+        }
+    };
+    // a part of the piece's rows to a slot of the workspace
+    auto store_part = [&](size_t slot) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int r = n * 8 + 2 * t + q;
+                if (cur.rb * gm.rows + r >= R) continue;
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    const uint8_t* tile = kb + i * strip_bytes + c * kKv4Tile;
-                    const uint4 w = *reinterpret_cast<const uint4*>(tile + lane * 16);
-                    const uint32_t sc = *reinterpret_cast<const uint16_t*>(tile + 512 + lane * 2);
-                    const uint32_t lo = scale_pair(sc, 0, 0), hi = scale_pair(sc, 1, 1);
-                    uint32_t x[4], y[4], z[4], u[4];
-                    kv4_dequant8(w.x, lo, x);
-                    kv4_dequant8(w.y, lo, y);
-                    kv4_dequant8(w.z, hi, z);
-                    kv4_dequant8(w.w, hi, u);
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        mma_f16_16816(s[i][n], x[0], z[0], x[1], z[1], qf[n][c][0][0], qf[n][c][0][1]);
-                        mma_f16_16816(s[i][n], x[2], z[2], x[3], z[3], qf[n][c][1][0], qf[n][c][1][1]);
-                        mma_f16_16816(s[i][n], y[0], u[0], y[1], u[1], qf[n][c][2][0], qf[n][c][2][1]);
-                        mma_f16_16816(s[i][n], y[2], u[2], y[3], u[3], qf[n][c][3][0], qf[n][c][3][1]);
-                    }
+                    if (chunk0 + c < wg * CH) continue;
+                    float4* o = reinterpret_cast<float4*>(gm.part + (slot * gm.rows + r) * pb.D + (chunk0 + c) * 64 + 8 * g);
+                    o[0] = make_float4(acc[c][0][n][q], acc[c][0][n][q + 2], acc[c][1][n][q], acc[c][1][n][q + 2]);
+                    o[1] = make_float4(acc[c][2][n][q], acc[c][2][n][q + 2], acc[c][3][n][q], acc[c][3][n][q + 2]);
+                }
+                if (wg == 0 && g == 0) {
+                    gm.ml[(slot * gm.rows + r) * 2] = m[n][q];
+                    gm.ml[(slot * gm.rows + r) * 2 + 1] = l[n][q];
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(kb_full + kEmpty);
-            kp += st_bytes;
-            ++kb_full;
-            if (kp == ring_v) {
-                kp = ring_k;
-                kb_full -= gm.stages;
-                k_phase ^= 1u;
-            }
-            if (SPLIT) {
-#pragma unroll
-                for (int i = 0; i < kStepStrips; ++i)
-#pragma unroll
-                    for (int n = 0; n < NB; ++n)
-                        ex[wg * kExch + (i * NB + n) * 32] =
-                            make_float4(s[i][n][0], s[i][n][1], s[i][n][2], s[i][n][3]);
-            }
-        };
+    };
 
-        // sums of the partial scores, mask, P^T fragments; tok: the step's first token
-        auto softmax = [&](int ns, int tok, bool first) {
-            if (SPLIT) {
-                asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gm.C * 32) : "memory");
-                const float4* x = ex;
+    while (more) {
+        // ---- Q of the piece's rows as B operands: fp16, scaled by a power of two into its range (bf16 has the wider
+        // one). A lane holds query g, head dims 16 t .. 16 t + 15 of a chunk; each warp takes every C-th chunk.
+        const int r0 = cur.rb * gm.rows;
+        least = pb.causal ? cur.len - pb.Nq + 1 : cur.len;
 #pragma unroll
-                for (int i = 0; i < kStepStrips; ++i)
+        for (int k = 0; k < NB; ++k) {
+            const int r = r0 + k * 8 + g;
+            const int h = cur.hk * G + r / pb.Nq, i = r % pb.Nq;
+            const uint16_t* q = static_cast<const uint16_t*>(a.f.q) + cur.b * pb.vq.sb + h * pb.vq.sh + i * pb.vq.sn;
+            uint4 x[CH], y[CH];
+            uint32_t amax = 0;  // magnitudes of 16-bit floats order as their bits do
 #pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        const float4 v0 = x[(i * NB + n) * 32], v1 = x[kExch + (i * NB + n) * 32];
-                        s[i][n][0] = v0.x + v1.x;
-                        s[i][n][1] = v0.y + v1.y;
-                        s[i][n][2] = v0.z + v1.z;
-                        s[i][n][3] = v0.w + v1.w;
-                    }
-                for (int w = 2; w < gm.C; ++w) {  // one order for every warp: all get the same bits
-                    x += w == 2 ? 2 * kExch : kExch;
-#pragma unroll
-                    for (int i = 0; i < kStepStrips; ++i)
-#pragma unroll
-                        for (int n = 0; n < NB; ++n) {
-                            const float4 v = x[(i * NB + n) * 32];
-                            s[i][n][0] += v.x;
-                            s[i][n][1] += v.y;
-                            s[i][n][2] += v.z;
-                            s[i][n][3] += v.w;
-                        }
+            for (int j = 0; j < CH; ++j) {
+                const int c = wg + j * gm.C;
+                x[j] = y[j] = make_uint4(0, 0, 0, 0);
+                if (r < R && c < gm.chunks) {
+                    const uint4* src = reinterpret_cast<const uint4*>(q + c * 64 + t * 16);
+                    x[j] = src[0];
+                    y[j] = src[1];
                 }
-                ex = ex == exch ? exch + exch_size : exch;
+                const uint32_t w[8] = {x[j].x, x[j].y, x[j].z, x[j].w, y[j].x, y[j].y, y[j].z, y[j].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax = max(amax, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
             }
-            // scores in log2 units above the reference; keys that a row does not see have none
+            float mul = 1.f;
+            if (bf16) {
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                if (SW < 4) {
+                    if (t == 0) sh.col[warp][k * 8 + g] = __uint_as_float(amax);
+                    group_sync();
+                    for (int w = 0; w < gm.C; ++w) amax = max(amax, __float_as_uint(sh.col[group * gm.C + w][k * 8 + g]));
+                }
+                // largest magnitude to [2^14, 2^15); rows of zeros or that are not finite stay as they are
+                const int e = static_cast<int>(amax >> 7);
+                if (amax > 0 && e < 255) mul = __uint_as_float(static_cast<uint32_t>(min(14 + 127 - e, 126) + 127) << 23);
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+                for (int j = 0; j < CH; ++j) {
+                    uint32_t w[8] = {x[j].x, x[j].y, x[j].z, x[j].w, y[j].x, y[j].y, y[j].z, y[j].w};
 #pragma unroll
-                for (int i = 0; i < kStepStrips; ++i)
+                    for (int v = 0; v < 8; ++v) {
+                        const float2 f = unpack2<true>(w[v]);
+                        w[v] = pack2<false>(f.x * mul, f.y * mul);
+                    }
+                    x[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                    y[j] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i][n][e] = fmaf(s[i][n][e], c2[n][e & 1], -m[n][e & 1]);
-            if (tok + 16 * kStepStrips > least || ns < kStepStrips) {
+            for (int j = 0; j < CH; ++j) {
+                const int c = wg + j * gm.C;
+                if (c < gm.chunks) {
+                    q_mem[(c * NB + k) * 64] = x[j];
+                    q_mem[(c * NB + k) * 64 + 32] = y[j];
+                }
+            }
+            const float scale = pb.scale_log2 / mul;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                c2[k][e] = __shfl_sync(0xffffffffu, scale, (2 * t + e) * 4);
+                limits[k][e] = pb.causal ? min(cur.len, least + (r0 + k * 8 + 2 * t + e) % pb.Nq) : cur.len;
+                m[k][e] = 0.f;
+                l[k][e] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-#pragma unroll
-                        for (int i = 0; i < kStepStrips; ++i)
-                            if (i >= ns || tok + 16 * i + g + 8 * (e >> 1) >= limits[n][e & 1]) s[i][n][e] = -INFINITY;
-            }
+                    for (int e = 0; e < 4; ++e) acc[c][i][n][e] = 0.f;
+        group_sync();
+
+        // ---- scores of a step, then the values of the one before: a barrier between a step's P and its values
+        int last_n = 0, last_tok = 0;
+        for (int at = cur.s0; at < cur.s1; at += steps) {
+            const int mine = at + wg * SW, n = max(0, min(SW, cur.s1 - mine));  // my strips of the step
+            const bool first = at == cur.s0;
+            ++step;
+            scores(n);
+            __syncwarp();
+            // my K place is read: the step after next's (or the next's) strips may come
+            if (lane == 0) load_k(k_place);
+            if (n > 0) k_used ^= 1u << k_place;
+            if (++k_place == gm.depth) k_place = 0;
+            // scores in log2 units above the reference; keys that a row does not see have none
             float top = -INFINITY;
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int k = 0; k < NB; ++k)
 #pragma unroll
-                for (int i = 0; i < kStepStrips; ++i)
+                for (int i = 0; i < SW; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i][n][e]);
-            if (first || __any_sync(0xffffffffu, top > kRefSpan)) {
+                    for (int e = 0; e < 4; ++e) s[i][k][e] = fmaf(s[i][k][e], c2[k][e & 1], -m[k][e & 1]);
+            if ((mine + SW) * 16 > least || n < SW) {
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
+                for (int k = 0; k < NB; ++k)
+#pragma unroll
+                    for (int i = 0; i < SW; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (i >= n || (mine + i) * 16 + g + 8 * (e >> 1) >= limits[k][e & 1]) s[i][k][e] = -INFINITY;
+            }
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+#pragma unroll
+                for (int i = 0; i < SW; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i][k][e]);
+            if (!first) {
+                const bool up = __any_sync(0xffffffffu, top > kRefSpan);
+                if (up && lane == 0) sh.up[group][step & 1] = step;
+                store_p();
+                values(last_n, last_tok, step - 1);
+            }
+            group_sync();
+            if (lane == 0) {
+                load_v(ld.loaded, v_place == 0 ? gm.depth - 1 : v_place - 1);  // the place that the last values had
+                ld.loaded = ld.issued;
+            }
+            if (first || *reinterpret_cast<volatile int*>(&sh.up[group][step & 1]) == step) {
+                // the reference moves, for all warps of the group alike
+#pragma unroll
+                for (int k = 0; k < NB; ++k)
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         float mx = -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < kStepStrips; ++i) mx = fmaxf(mx, fmaxf(s[i][n][q], s[i][n][q + 2]));
+                        for (int i = 0; i < SW; ++i) mx = fmaxf(mx, fmaxf(s[i][k][q], s[i][k][q + 2]));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        // how far the reference moves; a row's keys come first, so one without any in the piece's first
-                        // step has none in the piece
+                        if (g == 0) sh.col[warp][k * 8 + 2 * t + q] = mx;
+                    }
+                group_sync();
+#pragma unroll
+                for (int k = 0; k < NB; ++k)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float mx = -INFINITY;
+                        for (int w = 0; w < gm.C; ++w) mx = fmaxf(mx, sh.col[group * gm.C + w][k * 8 + 2 * t + q]);
+                        // how far it moves; a row's keys come first, so one without any in the piece's first step has
+                        // none in the piece
                         float up = mx - kRefBelow;
                         if (first ? mx == -INFINITY : up < 0.f) up = 0.f;
                         const float al = first ? 0.f : ex2_approx(-up);
-                        m[n][q] += up;
-                        l[n][q] *= al;
+                        m[k][q] += up;
+                        l[k][q] *= al;
 #pragma unroll
-                        for (int i = 0; i < kStepStrips; ++i) {
-                            s[i][n][q] -= up;
-                            s[i][n][q + 2] -= up;
+                        for (int i = 0; i < SW; ++i) {
+                            s[i][k][q] -= up;
+                            s[i][k][q + 2] -= up;
                         }
 #pragma unroll
                         for (int c = 0; c < CH; ++c)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                acc[c][i][n][q] *= al;
-                                acc[c][i][n][q + 2] *= al;
+                                acc[c][i][k][q] *= al;
+                                acc[c][i][k][q + 2] *= al;
                             }
                     }
+                store_p();
+                group_sync();
             }
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int k = 0; k < NB; ++k)
 #pragma unroll
-                for (int i = 0; i < kStepStrips; ++i) {
-                    float p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = ex2_approx(s[i][n][e]);
-                    l[n][0] += p[0] + p[2];
-                    l[n][1] += p[1] + p[3];
-                    // fp16 P: half a step of 2^-11, an eighth of what bf16 operands would cost
-                    pf[i][n][0] = transpose8x8(pack2<false>(p[0], p[1]));
-                    pf[i][n][1] = transpose8x8(pack2<false>(p[2], p[3]));
-                }
-        };
+                for (int q = 0; q < 2; ++q) l[k][q] += dl[k][q];
+            last_n = min(steps, cur.s1 - at);
+            last_tok = at * 16;
+        }
+        values(last_n, last_tok, step);
 
-        // O^T += V^T P^T over my chunks
-        auto values = [&](int ns, int tok) {
-            arrived(vb_full, v_phase, KS_V);
-            const uint8_t* vb = vp + chunk0 * kKv4Tile;
+        // ---- the group's sums
 #pragma unroll
-            for (int i = 0; i < kStepStrips; ++i) {
-                // cells behind the last token hold anything, as does the place of a second strip that is not there:
-                // their scales count as zero
-                uint32_t keep = 0xffffffffu;
-                if (i >= ns) {
-                    keep = 0;
-                } else if (tok + 16 * i + 16 > cur.len) {
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (tok + 16 * i + 2 * t + (j & 1) + 8 * (j >> 1) >= cur.len) keep &= ~(0xffu << (8 * j));
-                }
-#pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    const uint8_t* tile = vb + i * strip_bytes + c * kKv4Tile;
-                    const uint4 w = *reinterpret_cast<const uint4*>(tile + lane * 16);
-                    const uint32_t sc = *reinterpret_cast<const uint32_t*>(tile + 512 + ((g >> 1) * 4 + t) * 4) & keep;
-                    const uint32_t lo = scale_pair(sc, 0, 1), hi = scale_pair(sc, 2, 3);
-                    uint32_t even, odd, a0[4], a1[4], a2[4], a3[4];
-                    interleave(w.x, w.y, even, odd);
-                    kv4_dequant8(even, lo, a0);
-                    kv4_dequant8(odd, lo, a1);
-                    interleave(w.z, w.w, even, odd);
-                    kv4_dequant8(even, hi, a2);
-                    kv4_dequant8(odd, hi, a3);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-#pragma unroll
-                        for (int n = 0; n < NB; ++n)
-                            mma_f16_16816(acc[c][e][n], a0[e], a1[e], a2[e], a3[e], pf[i][n][0], pf[i][n][1]);
-                }
+            for (int q = 0; q < 2; ++q) {
+                l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 4);
+                l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 8);
+                l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 16);
+                if (g == 0) sh.sum[warp][n * 8 + 2 * t + q] = l[n][q];
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(vb_full + kEmpty);
-            vp += st_bytes;
-            ++vb_full;
-            if (vp == ring_v + gm.stages * st_bytes) {
-                vp = ring_v;
-                vb_full -= gm.stages;
-                v_phase ^= 1u;
+        group_sync();
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                l[n][q] = 0.f;
+                for (int w = 0; w < gm.C; ++w) l[n][q] += sh.sum[group * gm.C + w][n * 8 + 2 * t + q];
+                if (l[n][q] == 0.f) m[n][q] = -INFINITY;  // no keys, no reference
             }
-        };
 
-        // a part of the piece's rows to a slot of the workspace
-        auto store_part = [&](size_t slot) {
+        // ---- a whole unit's outputs, or a part of one
+        if (cur.s0 == 0 && cur.s1 == strips_of(cur.len)) {
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const int r = n * 8 + 2 * t + q;
-                    if (cur.rb * gm.rows + r >= R) continue;
+                    const int r = r0 + n * 8 + 2 * t + q;
+                    if (r >= R) continue;
+                    const int h = cur.hk * G + r / pb.Nq, i = r % pb.Nq;
+                    const float inv = l[n][q] == 0.f ? 0.f : 1.f / l[n][q];
+                    uint16_t* o = static_cast<uint16_t*>(a.f.o) + cur.b * pb.vo.sb + h * pb.vo.sh + i * pb.vo.sn;
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
                         if (chunk0 + c < wg * CH) continue;
-                        float4* o = reinterpret_cast<float4*>(gm.part + (slot * gm.rows + r) * pb.D + (chunk0 + c) * 64 + 8 * g);
-                        o[0] = make_float4(acc[c][0][n][q], acc[c][0][n][q + 2], acc[c][1][n][q], acc[c][1][n][q + 2]);
-                        o[1] = make_float4(acc[c][2][n][q], acc[c][2][n][q + 2], acc[c][3][n][q], acc[c][3][n][q + 2]);
-                    }
-                    if (wg == 0 && g == 0) {
-                        gm.ml[(slot * gm.rows + r) * 2] = m[n][q];
-                        gm.ml[(slot * gm.rows + r) * 2 + 1] = l[n][q];
-                    }
-                }
-        };
-        const size_t worker = static_cast<size_t>(blockIdx.x) * gm.NG + group;
-
-        bool more = range(group, cur);
-        while (more) {
-            // ---- Q of the piece's rows over my chunks, as B fragments: fp16, scaled by a power of two into its range
-            // (bf16 has the wider one). A lane holds query g, head dims 16 t .. 16 t + 15 of every chunk.
-            const int r0 = cur.rb * gm.rows;
-            least = pb.causal ? cur.len - pb.Nq + 1 : cur.len;  // first token that some row does not see
-            uint32_t amax[NB];  // magnitudes of 16-bit floats order as their bits do
+                        uint32_t x[4];
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const int r = r0 + n * 8 + g;
-                const int h = cur.hk * G + r / pb.Nq, i = r % pb.Nq;
-                const uint16_t* q = static_cast<const uint16_t*>(a.f.q) + cur.b * pb.vq.sb + h * pb.vq.sh + i * pb.vq.sn;
-                amax[n] = 0;
-#pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                    if (r < R && chunk0 + c >= wg * CH) {
-                        const uint4* src = reinterpret_cast<const uint4*>(q + (chunk0 + c) * 64 + t * 16);
-                        x = src[0];
-                        y = src[1];
-                    }
-                    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        qf[n][c][e >> 1][e & 1] = w[e];
-                        if (BF16) amax[n] = max(amax[n], max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-                    }
-                }
-                if (BF16) {
-                    amax[n] = max(amax[n], __shfl_xor_sync(0xffffffffu, amax[n], 1));
-                    amax[n] = max(amax[n], __shfl_xor_sync(0xffffffffu, amax[n], 2));
-                    if (SPLIT && t == 0) sh.qmax[warp][n * 8 + g] = amax[n];
-                }
-            }
-            // (the steps of a piece have this barrier too, so the last piece's maxima are read by now)
-            if (BF16 && SPLIT) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gm.C * 32) : "memory");
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                float mul = 1.f;
-                if (BF16) {
-                    if (SPLIT)
-                        for (int w = 0; w < gm.C; ++w) amax[n] = max(amax[n], sh.qmax[group * gm.C + w][n * 8 + g]);
-                    // largest magnitude to [2^14, 2^15); rows of zeros or that are not finite stay as they are
-                    const int e = static_cast<int>(amax[n] >> 7);
-                    if (amax[n] > 0 && e < 255) mul = __uint_as_float(static_cast<uint32_t>(min(14 + 127 - e, 126) + 127) << 23);
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float2 f = unpack2<true>(qf[n][c][k >> 1][k & 1]);
-                            qf[n][c][k >> 1][k & 1] = pack2<false>(f.x * mul, f.y * mul);
+                        for (int e = 0; e < 4; ++e) {
+                            const float lo = acc[c][e][n][q] * inv, hi = acc[c][e][n][q + 2] * inv;
+                            x[e] = bf16 ? pack2<true>(lo, hi) : pack2<false>(lo, hi);
                         }
+                        *reinterpret_cast<uint4*>(o + (chunk0 + c) * 64 + 8 * g) = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                    if (wg == 0 && g == 0)
+                        a.f.lse[(static_cast<long long>(cur.b) * pb.Hq + h) * pb.Nq + i] =
+                            l[n][q] == 0.f ? -INFINITY : (m[n][q] + lg2_approx(l[n][q])) * kLn2;
                 }
-                const float scale = pb.scale_log2 / mul;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    c2[n][e] = __shfl_sync(0xffffffffu, scale, (2 * t + e) * 4);
-                    limits[n][e] = pb.causal ? min(cur.len, least + (r0 + n * 8 + 2 * t + e) % pb.Nq) : cur.len;
-                    m[n][e] = 0.f;
-                    l[n][e] = 0.f;
-                }
+            more = next_piece(a, gm, cur);
+        } else {
+            Piece next = cur;
+            more = next_piece(a, gm, next);
+            if (more) {
+                store_part(2 * (static_cast<size_t>(blockIdx.x) * gm.NG + group));
+                cur = next;
+            } else {
+                pending = true;
             }
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int n = 0; n < NB; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[c][i][n][e] = 0.f;
-
-            // ---- the scores of a step are issued before the values of the one before
-            for (int at = cur.s0;; at += kStepStrips) {
-                const bool in = at < cur.s1;
-                if (in) scores();
-                if (at > cur.s0) values(min(kStepStrips, cur.s1 - at + kStepStrips), (at - kStepStrips) * 16);
-                if (!in) break;
-                softmax(min(kStepStrips, cur.s1 - at), at * 16, at == cur.s0);
-            }
+        }
+    }
+    // after a wait that ran out, copies may still be in flight: they end before the CTA does
+    if (lane == 0 && *reinterpret_cast<volatile int*>(&sh.abort_flag))
+        for (int i = 0; i < gm.depth; ++i) {
+            mbar_wait(&full_k[i], ((ld.k_armed >> i) & 1u) ^ 1u, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns, KS_DRAIN,
+                      false);
+            mbar_wait(&full_v[i], ((ld.v_armed >> i) & 1u) ^ 1u, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns, KS_DRAIN,
+                      false);
+        }
+    if (pending && wg == 0) {
+        if (lane == 0) {
+            sh.last[group][0] = cur.b;
+            sh.last[group][1] = cur.hk;
+            sh.last[group][2] = cur.rb;
+        }
+        if (g == 0)
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 4);
-                    l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 8);
-                    l[n][q] += __shfl_xor_sync(0xffffffffu, l[n][q], 16);
-                    if (l[n][q] == 0.f) m[n][q] = -INFINITY;  // no keys, no reference
+                    sh.ml[group][n * 8 + 2 * t + q][0] = m[n][q];
+                    sh.ml[group][n * 8 + 2 * t + q][1] = l[n][q];
                 }
-
-            // ---- a whole unit's outputs, or a part of one
-            if (cur.s0 == 0 && cur.s1 == strips_of(cur.len)) {
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int r = r0 + n * 8 + 2 * t + q;
-                        if (r >= R) continue;
-                        const int h = cur.hk * G + r / pb.Nq, i = r % pb.Nq;
-                        const float inv = l[n][q] == 0.f ? 0.f : 1.f / l[n][q];
-                        uint16_t* o = static_cast<uint16_t*>(a.f.o) + cur.b * pb.vo.sb + h * pb.vo.sh + i * pb.vo.sn;
-#pragma unroll
-                        for (int c = 0; c < CH; ++c) {
-                            if (chunk0 + c < wg * CH) continue;
-                            uint32_t x[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) x[e] = pack2<BF16>(acc[c][e][n][q] * inv, acc[c][e][n][q + 2] * inv);
-                            *reinterpret_cast<uint4*>(o + (chunk0 + c) * 64 + 8 * g) = make_uint4(x[0], x[1], x[2], x[3]);
-                        }
-                        if (wg == 0 && g == 0)
-                            a.f.lse[(static_cast<long long>(cur.b) * pb.Hq + h) * pb.Nq + i] =
-                                l[n][q] == 0.f ? -INFINITY : (m[n][q] + lg2_approx(l[n][q])) * kLn2;
-                    }
-                more = next_piece(a, gm, cur);
-            } else {
-                Piece next = cur;
-                more = next_piece(a, gm, next);
-                if (more) {
-                    store_part(2 * worker);
-                    cur = next;
-                } else {
-                    pending = true;
-                }
-            }
-        }
-        if (pending && wg == 0) {
-            if (lane == 0) {
-                sh.last[group][1] = cur.hk;
-                sh.last[group][2] = cur.rb;
-            }
-            if (g == 0)
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        sh.ml[group][n * 8 + 2 * t + q][0] = m[n][q];
-                        sh.ml[group][n * 8 + 2 * t + q][1] = l[n][q];
-                    }
-        }
     }
-    __syncthreads();  // every copy has been read: the rings are free
-    if (pending && wg == 0 && lane == 0) sh.last[group][0] = cur.b;
-    __syncthreads();
-    const bool compute = warp < warps - 1;
+    __syncthreads();  // every copy has been read: the buffers are free
 
     // ---- neighbouring groups that end in the same unit join their parts in shared memory, each group a share of it
     int run0 = group, run1 = group;
-    if (compute && pending) {
+    if (pending) {
         auto same = [&](int i) {
             return sh.last[i][0] == cur.b && sh.last[i][1] == cur.hk && sh.last[i][2] == cur.rb;
         };
@@ -777,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
     }
     float4* const buf = reinterpret_cast<float4*>(smem) + lane;
     constexpr int kRegs = CH * 4 * NB;  // float4 per lane
-    if (compute && pending) {
+    if (pending) {
         float4* mine = buf + static_cast<size_t>(warp) * kRegs * 32;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -789,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kv4_kernel(const Kv4Decode
                         make_float4(acc[c][i][n][0], acc[c][i][n][1], acc[c][i][n][2], acc[c][i][n][3]);
     }
     __syncthreads();
-    if (!compute || !pending) return;
+    if (!pending) return;
     // the part goes to slot 1 of the run's last group
     const size_t slot = 2 * (static_cast<size_t>(blockIdx.x) * gm.NG + run1) + 1;
     const int r0 = cur.rb * gm.rows;
@@ -933,14 +1031,16 @@ __global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_kernel(const Kv4
 struct Plan {
     Kv4Geo gm;
     int ctas;
-    int nb, ch;
+    int nb, ch, sw;
     int smem;
     size_t part_floats, bytes;
 };
 
 // Eight query rows per step up to G * Nq = 8, else blocks of sixteen. A warp
-// holds O^T of its chunks in registers: at most four chunks of eight rows or two
-// of sixteen (64 accumulators), dealt out evenly over the group's C warps.
+// accumulates two chunks of O^T; it scores four, two or one strips per step
+// in groups of one, two or more warps. As many groups as registers (128 per
+// thread for eight rows, 168 for sixteen) and shared memory hold; a second
+// place per strip where it fits.
 Plan plan(const Problem& pb)
 {
     Plan p{};
@@ -950,19 +1050,18 @@ Plan plan(const Problem& pb)
     p.nb = R <= 8 ? 1 : 2;
     gm.rows = 8 * p.nb;
     gm.rblocks = static_cast<int>((R + gm.rows - 1) / gm.rows);
-    const int most = p.nb == 1 ? 4 : 2;
-    gm.C = (gm.chunks + most - 1) / most;
-    p.ch = (gm.chunks + gm.C - 1) / gm.C;
-    // at least two stages for every head dim: five groups with 184 KB of rings and 20 of exchange at D = 512
-    for (gm.NG = kComputeWarps / gm.C; gm.NG > 1; --gm.NG) {
-        const int exch = gm.C > 1 ? gm.NG * 2 * gm.C * kStepStrips * p.nb * 32 * 16 : 0;
-        if (2 * gm.NG * 2 * stage_bytes(gm.chunks) + exch + 1024 + static_cast<int>(sizeof(DecShared)) <= kMaxSmem) break;
-    }
-    const int exch = gm.C > 1 ? gm.NG * 2 * gm.C * kStepStrips * p.nb * 32 * 16 : 0;
-    const int ring = gm.NG * 2 * stage_bytes(gm.chunks);
-    gm.stages = (kMaxSmem - 1024 - static_cast<int>(sizeof(DecShared)) - exch) / ring;
-    if (gm.stages > kMaxStages) gm.stages = kMaxStages;
-    p.smem = exch + gm.stages * ring;
+    p.ch = gm.chunks > 1 ? 2 : 1;
+    gm.C = (gm.chunks + p.ch - 1) / p.ch;
+    p.sw = gm.C == 1 ? 4 : gm.C == 2 ? 2 : 1;
+    const int strips = gm.C * p.sw, place = 2 * strips * gm.chunks * kKv4Tile;   // K and V
+    const int operands = gm.chunks * p.nb * 1024 + 2 * strips * p.nb * 256;      // Q and P
+    const int room = kMaxSmem - 1024 - static_cast<int>(sizeof(DecShared));
+    gm.NG = (p.nb == 1 ? 16 : 12) / gm.C;
+    if (gm.NG > room / (place + operands)) gm.NG = room / (place + operands);
+    gm.depth = gm.NG * (2 * place + operands) <= room ? 2 : 1;
+    gm.group_bytes = gm.depth * place + operands;
+    const int join = gm.NG * gm.C * p.ch * 4 * p.nb * 512;
+    p.smem = gm.NG * gm.group_bytes > join ? gm.NG * gm.group_bytes : join;
     const int sms = num_sms();
     p.ctas = sms > 0 ? sms : 152;
     gm.workers = p.ctas * gm.NG;
@@ -971,28 +1070,23 @@ Plan plan(const Problem& pb)
     return p;
 }
 
-template <int CH, int NB, bool SPLIT>
+template <int CH, int NB, int SW>
 cudaError_t launch_variant(const Kv4Decode& a, const Plan& p, cudaStream_t s)
 {
-    auto* kernel = a.f.bf16 ? decode_kv4_kernel<CH, NB, SPLIT, true> : decode_kv4_kernel<CH, NB, SPLIT, false>;
+    auto* kernel = decode_kv4_kernel<CH, NB, SW>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
     if (e != cudaSuccess) return e;
-    kernel<<<p.ctas, (p.gm.NG * p.gm.C + 1) * 32, p.smem, s>>>(a, p.gm);
+    kernel<<<p.ctas, p.gm.NG * p.gm.C * 32, p.smem, s>>>(a, p.gm);
     return cudaGetLastError();
 }
 
-// The chunks per warp that plan() can give, for one warp per group and for several.
-cudaError_t launch_main(const Kv4Decode& a, const Plan& p, cudaStream_t s)
+template <int NB>
+cudaError_t launch_rows(const Kv4Decode& a, const Plan& p, cudaStream_t s)
 {
-    if (p.nb == 1) {
-        if (p.gm.C > 1) return p.ch == 3 ? launch_variant<3, 1, true>(a, p, s) : launch_variant<4, 1, true>(a, p, s);
-        return p.ch == 1   ? launch_variant<1, 1, false>(a, p, s)
-               : p.ch == 2 ? launch_variant<2, 1, false>(a, p, s)
-               : p.ch == 3 ? launch_variant<3, 1, false>(a, p, s)
-                           : launch_variant<4, 1, false>(a, p, s);
-    }
-    if (p.gm.C > 1) return launch_variant<2, 2, true>(a, p, s);
-    return p.ch == 1 ? launch_variant<1, 2, false>(a, p, s) : launch_variant<2, 2, false>(a, p, s);
+    return p.ch == 1   ? launch_variant<1, NB, 4>(a, p, s)
+           : p.sw == 4 ? launch_variant<2, NB, 4>(a, p, s)
+           : p.sw == 2 ? launch_variant<2, NB, 2>(a, p, s)
+                       : launch_variant<2, NB, 1>(a, p, s);
 }
 
 }  // namespace
@@ -1004,8 +1098,8 @@ cudaError_t launch_decode_kv4(const Kv4Decode& a, void* workspace, cudaStream_t 
     Plan p = plan(a.f.pb);
     p.gm.part = static_cast<float*>(workspace);
     p.gm.ml = p.gm.part + p.part_floats;
-    cudaError_t e = launch_main(a, p, s);
-    if (e != cudaSuccess) return e;
+    const cudaError_t ran = p.nb == 1 ? launch_rows<1>(a, p, s) : launch_rows<2>(a, p, s);
+    if (ran != cudaSuccess) return ran;
     const Problem& pb = a.f.pb;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(pb.B) * pb.Hq * pb.Nq), (pb.D + 127) / 128);
