@@ -21,10 +21,11 @@
 //     computed once and its scores are never exchanged; for the values it takes
 //     two 64-wide head-dim chunks over all strips, so O^T stays in registers
 //     (32 for eight rows: 16 warps per SM). Between the two, P goes through
-//     shared memory as ready operands. One barrier per step.
-//   - each warp loads the strips it scores, K and V, by bulk copies: K into a
-//     place of its own as soon as its scores are done, V when the step's barrier
-//     says that the last values are.
+//     shared memory as ready operands. A step has two barriers: after its scores
+//     (P is there) and after its values.
+//   - one thread of the group loads the K of the next step after the first
+//     barrier, another its V after the second: each copy has the other half of a
+//     step to arrive, so one place for K and one for V are enough.
 //   - the softmax keeps a reference instead of the running maximum: it moves (and
 //     O is rescaled) only when a score passes it by 2^14. P <= 2^14 and its row's
 //     largest is >= 2^6 in fp16.
@@ -41,7 +42,6 @@ namespace ffpa {
 namespace {
 
 constexpr int kMaxWarps = 16;
-constexpr int kMaxDepth = 2;       // places per strip in the K and V buffers
 constexpr int kUnitCost = 4;       // strips' worth of a unit's start and end
 constexpr float kRefBelow = 6.f;   // the reference lies this far (log2) below the maximum it was taken from
 constexpr float kRefSpan = 14.f;   // and is kept until a score is this far above it
@@ -55,7 +55,6 @@ struct Kv4Geo {
     int NG;          // groups per CTA
     int rblocks;     // blocks of `rows` query rows per kv head's group of G * Nq
     int rows;        // 8 or 16
-    int depth;       // places per strip
     int group_bytes; // shared memory of one group
     int workers;     // groups of the whole grid
     float* part;     // [workers][2][rows][D] unnormalised partial O
@@ -178,30 +177,23 @@ __device__ __forceinline__ bool next_piece(const Kv4Decode& a, const Kv4Geo& gm,
     return p.s1 > 0;
 }
 
-// Strips [s, s + n) of a sequence's head: the head's K tiles in page 0, the block table's entry and the place in its
-// page of the first one. n = 0: none in this step, n < 0: no step.
-struct Strips {
-    const uint8_t* head;
-    const int* row;
-    int s, in, page, n;
-};
-
-// What a warp's lane 0 keeps of its loads.
+// What the thread that loads a group's K (or V) keeps: its piece, and the first strip of the next step with its place
+// in the block table and the page (fetched a step early).
 struct Loader {
     Piece piece;
-    Strips next, issued, loaded;  // of the next step; of the step whose K was issued last; whose V is next
+    const uint8_t* head;  // the head's tiles in page 0
+    const int* row;
+    int s, in, page;
+    int loads;            // steps loaded
     bool more;
-    int step_blk, step_in;        // a step's strips in pages and strips
-    uint32_t k_armed, v_armed;    // parities of the uses of each place
 };
 
 struct __align__(16) DecShared {
-    uint64_t full_k[kMaxWarps][kMaxDepth];  // per warp
-    uint64_t full_v[kMaxWarps][kMaxDepth];  // per group
+    uint64_t full[kMaxWarps][2];      // per group: K and V of a step are there
     long long sums[kMaxWarps];
     long long first_at[kMaxWarps];    // place where the units of each group's first sequence begin
     int first_b[kMaxWarps];
-    Loader load[kMaxWarps];
+    Loader load[kMaxWarps][2];
     int abort_flag;
     int up[kMaxWarps][2];             // per group and step parity: the last step in which a score passed the reference
     int last[kMaxWarps][3];           // sequence (-1: none), kv head and row block of the part a group ends with
@@ -288,9 +280,8 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
             if (lane >= d) incl += x;
         }
         if (lane == 31) sh.sums[warp] = incl;
-        if (threadIdx.x < kMaxWarps * kMaxDepth) {
-            mbar_init(&sh.full_k[0][0] + threadIdx.x, 1);
-            mbar_init(&sh.full_v[0][0] + threadIdx.x, gm.C);
+        if (threadIdx.x < kMaxWarps * 2) {
+            mbar_init(&sh.full[0][0] + threadIdx.x, 1);
             (&sh.up[0][0])[threadIdx.x] = 0;
             fence_barrier_init();
         }
@@ -328,15 +319,13 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
     const int strip_bytes = gm.chunks * kKv4Tile;
     // my chunks are chunk0 .. chunk0 + CH - 1; those before wg * CH are another warp's too and are not stored
     const int chunk0 = min(wg * CH, gm.chunks - CH);
-    // shared memory of the group: K places [depth][strips], V places, Q operands [chunks][NB][2][32] of 16 bytes,
-    // P operands [2][strips][NB][32] of 8 bytes
-    uint8_t* const base = smem + static_cast<size_t>(group) * gm.group_bytes;
-    const int place_bytes = steps * strip_bytes;
-    uint8_t* const k_mem = base + wg * SW * strip_bytes;
-    uint8_t* const v_mem = base + gm.depth * place_bytes;
-    uint4* const q_mem = reinterpret_cast<uint4*>(v_mem + gm.depth * place_bytes) + lane;
+    // shared memory of the group: K and V of a step [strips][chunks], Q operands [chunks][NB][2][32] of 16 bytes,
+    // P operands [strips][NB][32] of 8 bytes
+    uint8_t* const k_mem = smem + static_cast<size_t>(group) * gm.group_bytes;
+    uint8_t* const v_mem = k_mem + steps * strip_bytes;
+    uint4* const q_mem = reinterpret_cast<uint4*>(v_mem + steps * strip_bytes) + lane;
     uint2* const p_mem = reinterpret_cast<uint2*>(q_mem - lane + gm.chunks * NB * 64) + lane;
-    uint64_t *const full_k = sh.full_k[warp], *const full_v = sh.full_v[group];
+    uint64_t* const full = sh.full[group];
 
     auto group_sync = [&]() {
         if (SW == 4)  // groups of one warp
@@ -351,96 +340,77 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
         more = first_piece(a, gm, cur, at, min(at + chunk, total), sh.first_b[group], sh.first_at[group]);
     }
 
-    // ---- loads of my strips, `depth` steps ahead (lane 0). The place of the next step's strips in the block table
-    // moves by steps without a division, and its page is fetched a step early.
+    // ---- loads: K by the group's first warp, V by its second (lane 0). The place of a step in the block table moves
+    // without a division, and its first page is fetched a step early.
     const int spp = a.cache.page_size >> 4;  // strips per page
     const size_t v_off = static_cast<size_t>(pb.Hkv) * spp * strip_bytes, page_bytes = 2 * v_off;
-    Loader& ld = sh.load[warp];
+    const int v_warp = gm.C > 1 ? 1 : 0;
     auto valid_page = [&](int page, int b) {
         if (static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.num_pages)) return page;
         // the sequence's rows are undefined, but the copies stay inside the cache
         kv4_invalid(a.f.ctl.status, VS_KV4_DECODE, b);
         return 0;
     };
-    auto begin_piece = [&]() {
-        ld.next.s = ld.piece.s0 + wg * SW;
-        const int blk = ld.next.s / spp;
-        ld.next.in = ld.next.s - blk * spp;
-        ld.next.row = a.cache.table + ld.piece.b * a.cache.table_stride + blk;
-        ld.next.head = a.cache.data + static_cast<size_t>(ld.piece.hk) * spp * strip_bytes;
-        if (ld.next.s < ld.piece.s1) ld.next.page = valid_page(*ld.next.row, ld.piece.b);
+    auto begin_piece = [&](Loader& ld, int kv) {
+        ld.s = ld.piece.s0;
+        const int blk = ld.s / spp;
+        ld.in = ld.s - blk * spp;
+        ld.row = a.cache.table + ld.piece.b * a.cache.table_stride + blk;
+        ld.head = a.cache.data + static_cast<size_t>(ld.piece.hk) * spp * strip_bytes + (kv ? v_off : 0);
+        ld.page = valid_page(*ld.row, ld.piece.b);
     };
-    auto copy = [&](const Strips& x, size_t off, uint8_t* dst, uint64_t* bar) {
-        int run = SW == 1 ? 1 : min(x.n, spp - x.in);
-        bulk_load(dst, x.head + off + x.page * page_bytes + static_cast<size_t>(x.in) * strip_bytes, run * strip_bytes, bar);
-        if (SW > 1) {
-            const int* row = x.row;
-            for (int done = run; done < x.n; done += run) {
-                run = min(x.n - done, spp);
-                bulk_load(dst + done * strip_bytes, x.head + off + valid_page(*++row, ld.piece.b) * page_bytes,
-                          run * strip_bytes, bar);
-            }
-        }
-    };
-    // K of my strips of the next step
-    auto load_k = [&](int place) {
-        Strips x = ld.next;
-        x.n = ld.more ? max(0, min(SW, ld.piece.s1 - x.s)) : -1;
-        if (x.n > 0) {
-            ld.k_armed ^= 1u << place;
-            mbar_arrive_expect_tx(&full_k[place], x.n * strip_bytes);
-            copy(x, 0, k_mem + place * place_bytes, &full_k[place]);
-        }
-        ld.issued = x;
+    auto load = [&](int kv) {
+        Loader& ld = sh.load[group][kv];
         if (!ld.more) return;
-        x.s += steps;
-        if (x.s - wg * SW < ld.piece.s1) {
-            x.row += ld.step_blk;
-            x.in += ld.step_in;
-            if (x.in >= spp) {
-                x.in -= spp;
-                ++x.row;
+        const int s1 = ld.piece.s1;
+        int s = ld.s, in = ld.in, page = ld.page;
+        const int* row = ld.row;
+        const uint8_t* head = ld.head;
+        const int end = min(s + steps, s1);
+        uint8_t* dst = kv ? v_mem : k_mem;
+        mbar_arrive_expect_tx(&full[kv], (end - s) * strip_bytes);
+        for (;;) {  // runs of strips in a page
+            const int run = min(end - s, spp - in);
+            bulk_load(dst, head + page * page_bytes + static_cast<size_t>(in) * strip_bytes, run * strip_bytes, &full[kv]);
+            dst += run * strip_bytes;
+            s += run;
+            in += run;
+            if (in == spp) {
+                in = 0;
+                ++row;
+                if (s < s1) page = valid_page(*row, ld.piece.b);
             }
-            if (x.s < ld.piece.s1) x.page = valid_page(*x.row, ld.piece.b);
-            ld.next = x;
+            if (s >= end) break;
+        }
+        ++ld.loads;
+        if (s < s1) {
+            ld.s = s;
+            ld.in = in;
+            ld.row = row;
+            ld.page = page;
         } else {
             ld.more = next_piece(a, gm, ld.piece);
-            if (ld.more) begin_piece();
+            if (ld.more) begin_piece(ld, kv);
         }
     };
-    // V of strips whose K was issued
-    auto load_v = [&](const Strips& x, int place) {
-        if (x.n < 0) return;
-        ld.v_armed ^= 1u << place;
-        mbar_arrive_expect_tx(&full_v[place], x.n * strip_bytes);
-        if (x.n > 0) copy(x, v_off, v_mem + place * place_bytes + wg * SW * strip_bytes, &full_v[place]);
-    };
-    if (lane == 0) {
-        ld.piece = cur;
-        ld.more = more;
-        ld.k_armed = ld.v_armed = 0;
-        ld.step_blk = steps / spp;
-        ld.step_in = steps - ld.step_blk * spp;
-        if (more) {
-            begin_piece();
-            for (int i = 0; i < gm.depth; ++i) {
-                load_k(i);
-                load_v(ld.issued, i);
+    if (lane == 0)
+        for (int kv = 0; kv < 2; ++kv)
+            if (wg == (kv ? v_warp : 0)) {
+                Loader& ld = sh.load[group][kv];
+                ld.piece = cur;
+                ld.more = more;
+                ld.loads = 0;
+                if (more) {
+                    begin_piece(ld, kv);
+                    load(kv);
+                }
             }
-        }
-        ld.loaded.n = -1;
-    }
     __syncwarp();
-
     // Waits for a copy. After one that ran out of time no more are issued, the group's barriers go on.
-    auto arrived = [&](uint64_t* bar, uint32_t phase, uint32_t site) {
-        if (!mbar_try_wait(smem_u32(bar), phase) &&
-            !wait_slow(bar, phase, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns, site)) {
-            if (lane == 0) {
-                ld.more = false;
-                ld.loaded.n = ld.issued.n = -1;
-            }
-        }
+    auto arrived = [&](int kv, uint32_t phase) {
+        if (!mbar_try_wait(smem_u32(&full[kv]), phase) &&
+            !wait_slow(&full[kv], phase, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns, kv ? KS_V : KS_K))
+            sh.load[group][0].more = sh.load[group][1].more = false;
         __syncwarp();
     };
 
@@ -448,8 +418,6 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
     float acc[CH][4][NB][4];
     float m[NB][2], l[NB][2];
     int step = 0;                       // steps begun by my group
-    int k_place = 0, v_place = 0;
-    uint32_t k_used = 0, v_phase = 0;   // parities of my K places' uses; of the V places' round
     float s[SW][NB][4], c2[NB][2];
     int limits[NB][2], least = 0;       // first token that my columns' rows do not see, and that some row does not see
 
@@ -464,9 +432,9 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
                 for (int k = 0; k < NB; ++k)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sum[x][i][k][e] = 0.f;
+        arrived(0, (step - 1) & 1u);
         if (n > 0) {
-            arrived(&full_k[k_place], (k_used >> k_place) & 1u, KS_K);
-            const uint8_t* tile = k_mem + k_place * place_bytes;
+            const uint8_t* tile = k_mem + wg * SW * strip_bytes;
             const uint4* q = q_mem;
             auto one = [&](float (&to)[SW][NB][4]) {
                 uint4 q0[NB], q1[NB];
@@ -511,7 +479,7 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
     // P of my strips as operands to the step's buffer; their sums
     float dl[NB][2];
     auto store_p = [&]() {
-        uint2* p = p_mem + ((step & 1) * steps + wg * SW) * NB * 32;
+        uint2* p = p_mem + wg * SW * NB * 32;
 #pragma unroll
         for (int k = 0; k < NB; ++k) dl[k][0] = dl[k][1] = 0.f;
 #pragma unroll
@@ -527,11 +495,11 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
                 p[(i * NB + k) * 32] = make_uint2(transpose8x8(pack2<false>(x[0], x[1])), transpose8x8(pack2<false>(x[2], x[3])));
             }
     };
-    // O^T += V^T P^T over my chunks, for the n strips of step `of`, whose first token is tok
-    auto values = [&](int n, int tok, int of) {
-        arrived(&full_v[v_place], v_phase, KS_V);
-        const uint8_t* tile = v_mem + v_place * place_bytes + chunk0 * kKv4Tile;
-        const uint2* p = p_mem + (of & 1) * steps * NB * 32;
+    // O^T += V^T P^T over my chunks, for the n strips of a step, whose first token is tok
+    auto values = [&](int n, int tok) {
+        arrived(1, (step - 1) & 1u);
+        const uint8_t* tile = v_mem + chunk0 * kKv4Tile;
+        const uint2* p = p_mem;
         // cells behind the last token hold anything: their scales count as zero
         const int tail = cur.len - tok - 16 * (n - 1);
         uint32_t last_keep = 0xffffffffu;
@@ -558,10 +526,6 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
             }
             tile += strip_bytes;
             p += NB * 32;
-        }
-        if (++v_place == gm.depth) {
-            v_place = 0;
-            v_phase ^= 1u;
         }
     };
     // a part of the piece's rows to a slot of the workspace
@@ -662,18 +626,11 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
                     for (int e = 0; e < 4; ++e) acc[c][i][n][e] = 0.f;
         group_sync();
 
-        // ---- scores of a step, then the values of the one before: a barrier between a step's P and its values
-        int last_n = 0, last_tok = 0;
         for (int at = cur.s0; at < cur.s1; at += steps) {
             const int mine = at + wg * SW, n = max(0, min(SW, cur.s1 - mine));  // my strips of the step
             const bool first = at == cur.s0;
             ++step;
             scores(n);
-            __syncwarp();
-            // my K place is read: the step after next's (or the next's) strips may come
-            if (lane == 0) load_k(k_place);
-            if (n > 0) k_used ^= 1u << k_place;
-            if (++k_place == gm.depth) k_place = 0;
             // scores in log2 units above the reference; keys that a row does not see have none
             float top = -INFINITY;
 #pragma unroll
@@ -701,13 +658,9 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
                 const bool up = __any_sync(0xffffffffu, top > kRefSpan);
                 if (up && lane == 0) sh.up[group][step & 1] = step;
                 store_p();
-                values(last_n, last_tok, step - 1);
             }
-            group_sync();
-            if (lane == 0) {
-                load_v(ld.loaded, v_place == 0 ? gm.depth - 1 : v_place - 1);  // the place that the last values had
-                ld.loaded = ld.issued;
-            }
+            group_sync();  // P is there, K is read
+            if (lane == 0 && wg == 0) load(0);
             if (first || *reinterpret_cast<volatile int*>(&sh.up[group][step & 1]) == step) {
                 // the reference moves, for all warps of the group alike
 #pragma unroll
@@ -756,10 +709,10 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
             for (int k = 0; k < NB; ++k)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) l[k][q] += dl[k][q];
-            last_n = min(steps, cur.s1 - at);
-            last_tok = at * 16;
+            values(min(steps, cur.s1 - at), at * 16);
+            group_sync();  // V and P are read
+            if (lane == 0 && wg == v_warp) load(1);
         }
-        values(last_n, last_tok, step);
 
         // ---- the group's sums
 #pragma unroll
@@ -821,12 +774,10 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
     }
     // after a wait that ran out, copies may still be in flight: they end before the CTA does
     if (lane == 0 && *reinterpret_cast<volatile int*>(&sh.abort_flag))
-        for (int i = 0; i < gm.depth; ++i) {
-            mbar_wait(&full_k[i], ((ld.k_armed >> i) & 1u) ^ 1u, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns, KS_DRAIN,
-                      false);
-            mbar_wait(&full_v[i], ((ld.v_armed >> i) & 1u) ^ 1u, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns, KS_DRAIN,
-                      false);
-        }
+        for (int kv = 0; kv < 2; ++kv)
+            if (wg == (kv ? v_warp : 0) && sh.load[group][kv].loads > 0)
+                mbar_wait(&full[kv], (sh.load[group][kv].loads - 1) & 1u, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns,
+                          KS_DRAIN, false);
     if (pending && wg == 0) {
         if (lane == 0) {
             sh.last[group][0] = cur.b;
@@ -1037,10 +988,9 @@ struct Plan {
 };
 
 // Eight query rows per step up to G * Nq = 8, else blocks of sixteen. A warp
-// accumulates two chunks of O^T; it scores four, two or one strips per step
-// in groups of one, two or more warps. As many groups as registers (128 per
-// thread for eight rows, 168 for sixteen) and shared memory hold; a second
-// place per strip where it fits.
+// accumulates two chunks of O^T. As many groups as registers hold (128 per
+// thread for eight rows, 168 for sixteen), and steps as long as shared memory
+// then allows: four strips per warp in groups of one warp, else two or one.
 Plan plan(const Problem& pb)
 {
     Plan p{};
@@ -1052,14 +1002,17 @@ Plan plan(const Problem& pb)
     gm.rblocks = static_cast<int>((R + gm.rows - 1) / gm.rows);
     p.ch = gm.chunks > 1 ? 2 : 1;
     gm.C = (gm.chunks + p.ch - 1) / p.ch;
-    p.sw = gm.C == 1 ? 4 : gm.C == 2 ? 2 : 1;
-    const int strips = gm.C * p.sw, place = 2 * strips * gm.chunks * kKv4Tile;   // K and V
-    const int operands = gm.chunks * p.nb * 1024 + 2 * strips * p.nb * 256;      // Q and P
     const int room = kMaxSmem - 1024 - static_cast<int>(sizeof(DecShared));
     gm.NG = (p.nb == 1 ? 16 : 12) / gm.C;
-    if (gm.NG > room / (place + operands)) gm.NG = room / (place + operands);
-    gm.depth = gm.NG * (2 * place + operands) <= room ? 2 : 1;
-    gm.group_bytes = gm.depth * place + operands;
+    for (p.sw = gm.C == 1 ? 4 : 2;; p.sw >>= 1) {
+        const int strips = gm.C * p.sw;
+        gm.group_bytes = 2 * strips * gm.chunks * kKv4Tile + gm.chunks * p.nb * 1024 + strips * p.nb * 256;
+        if (gm.NG * gm.group_bytes <= room || gm.C == 1) break;
+        if (p.sw == 1) {
+            gm.NG = room / gm.group_bytes;
+            break;
+        }
+    }
     const int join = gm.NG * gm.C * p.ch * 4 * p.nb * 512;
     p.smem = gm.NG * gm.group_bytes > join ? gm.NG * gm.group_bytes : join;
     const int sms = num_sms();
