@@ -50,16 +50,49 @@ constexpr float kLn2 = 0.693147180559945309f;
 enum Kv4Site : uint32_t { KS_K = 0x7b, KS_V, KS_DRAIN };
 
 struct Kv4Geo {
-    int chunks;      // D / 64
-    int C;           // warps per group
-    int NG;          // groups per CTA
     int rblocks;     // blocks of `rows` query rows per kv head's group of G * Nq
     int rows;        // 8 or 16
-    int group_bytes; // shared memory of one group
+    int NG;          // groups per CTA
     int workers;     // groups of the whole grid
     float* part;     // [workers][2][rows][D] unnormalised partial O
     float* ml;       // [workers][2][rows][2] reference (log2) and sum
 };
+
+// Shape of a CTA for N head-dim chunks and NB blocks of eight query rows. A
+// warp accumulates two chunks of O^T. As many groups as registers hold (128
+// per thread for eight rows, 168 for sixteen), and steps as long as shared
+// memory then allows: four strips per warp in groups of one warp, else two or
+// one.
+struct Shape {
+    int CH;           // chunks per warp
+    int C;            // warps per group
+    int NG;           // groups per CTA
+    int SW;           // strips that a warp scores per step
+    int group_bytes;  // shared memory of a group
+    int smem;
+};
+constexpr int kStaticBytes = 9 * 1024;  // at least the kernel's static shared memory and the system's
+
+__host__ __device__ constexpr Shape shape_of(int N, int NB)
+{
+    Shape p{};
+    const int room = kMaxSmem - kStaticBytes;
+    p.CH = N > 1 ? 2 : 1;
+    p.C = (N + p.CH - 1) / p.CH;
+    p.NG = (NB == 1 ? 16 : 12) / p.C;
+    for (p.SW = p.C == 1 ? 4 : 2;; p.SW >>= 1) {
+        const int strips = p.C * p.SW;
+        p.group_bytes = 2 * strips * N * kKv4Tile + N * NB * 1024 + strips * NB * 256;
+        if (p.NG * p.group_bytes <= room) break;
+        if (p.SW == 1) {
+            p.NG = room / p.group_bytes;
+            break;
+        }
+    }
+    const int join = p.NG * p.C * p.CH * 4 * NB * 512;  // the parts that a CTA's groups end with
+    p.smem = p.NG * p.group_bytes > join ? p.NG * p.group_bytes : join;
+    return p;
+}
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
 {
@@ -252,15 +285,20 @@ __device__ __forceinline__ void v_tile(const uint8_t* tile, int lane, uint32_t k
     for (int e = 0; e < 4; ++e) a[e][3] = x[e];
 }
 
-// CH: chunks per warp; NB: blocks of eight query rows; SW: strips that a warp scores per step.
-template <int CH, int NB, int SW>
-__global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(const Kv4Decode a, const Kv4Geo gm)
+// N: head-dim chunks (D / 64); NB: blocks of eight query rows.
+template <int N, int NB>
+__global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1) decode_kv4_kernel(const Kv4Decode a, const Kv4Geo gm)
 {
+    constexpr Shape kShape = shape_of(N, NB);
+    constexpr int CH = kShape.CH, C = kShape.C, NG = kShape.NG, SW = kShape.SW, D = 64 * N, kRows = 8 * NB;
+    constexpr int steps = C * SW;                     // strips per step
+    constexpr int strip_bytes = N * kKv4Tile;
+    static_assert(sizeof(DecShared) + 1024 <= kStaticBytes, "static shared memory");
     pdl_trigger();
     const Problem& pb = a.f.pb;
     const bool bf16 = a.f.bf16 != 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int warps = blockDim.x >> 5;
+    constexpr int warps = NG * C, kThreads = 32 * warps;
     const int G = pb.Hq / pb.Hkv, R = G * pb.Nq;
     const int units_b = pb.Hkv * gm.rblocks;          // units per sequence
     __shared__ DecShared sh;
@@ -269,7 +307,7 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
     // ---- the line's length and the sequence in which each of my groups begins
     long long chunk, total;
     {
-        const int per = (pb.B + blockDim.x - 1) / blockDim.x;
+        const int per = (pb.B + kThreads - 1) / kThreads;
         const int b0 = min(static_cast<int>(threadIdx.x) * per, pb.B), b1 = min(b0 + per, pb.B);
         long long sum = 0;
         for (int b = b0; b < b1; ++b) sum += cost_of(cached_len(a, b));
@@ -296,8 +334,8 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
         total *= units_b;
         chunk = (total + gm.workers - 1) / gm.workers;
         const long long lo = (incl - sum) * units_b, hi = incl * units_b;
-        for (int i = 0; i < gm.NG; ++i) {
-            const long long at = (static_cast<long long>(blockIdx.x) * gm.NG + i) * chunk;
+        for (int i = 0; i < NG; ++i) {
+            const long long at = (static_cast<long long>(blockIdx.x) * NG + i) * chunk;
             if (at < lo || at >= hi || at >= total) continue;
             long long b_at = lo;
             for (int b = b0; b < b1; ++b) {
@@ -312,31 +350,29 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
         }
         __syncthreads();
     }
-    if (static_cast<long long>(blockIdx.x) * gm.NG * chunk >= total) return;
+    if (static_cast<long long>(blockIdx.x) * NG * chunk >= total) return;
 
-    const int group = warp / gm.C, wg = warp - group * gm.C;  // my group, my place in it
-    const int steps = gm.C * SW;                              // strips per step
-    const int strip_bytes = gm.chunks * kKv4Tile;
+    const int group = warp / C, wg = warp - group * C;  // my group, my place in it
     // my chunks are chunk0 .. chunk0 + CH - 1; those before wg * CH are another warp's too and are not stored
-    const int chunk0 = min(wg * CH, gm.chunks - CH);
+    const int chunk0 = min(wg * CH, N - CH);
     // shared memory of the group: K and V of a step [strips][chunks], Q operands [chunks][NB][2][32] of 16 bytes,
     // P operands [strips][NB][32] of 8 bytes
-    uint8_t* const k_mem = smem + static_cast<size_t>(group) * gm.group_bytes;
+    uint8_t* const k_mem = smem + static_cast<size_t>(group) * kShape.group_bytes;
     uint8_t* const v_mem = k_mem + steps * strip_bytes;
     uint4* const q_mem = reinterpret_cast<uint4*>(v_mem + steps * strip_bytes) + lane;
-    uint2* const p_mem = reinterpret_cast<uint2*>(q_mem - lane + gm.chunks * NB * 64) + lane;
+    uint2* const p_mem = reinterpret_cast<uint2*>(q_mem - lane + N * NB * 64) + lane;
     uint64_t* const full = sh.full[group];
 
     auto group_sync = [&]() {
         if (SW == 4)  // groups of one warp
             __syncwarp();
         else
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gm.C * 32) : "memory");
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(C * 32) : "memory");
     };
     Piece cur{};
     bool more;
     {
-        const long long at = (static_cast<long long>(blockIdx.x) * gm.NG + group) * chunk;
+        const long long at = (static_cast<long long>(blockIdx.x) * NG + group) * chunk;
         more = first_piece(a, gm, cur, at, min(at + chunk, total), sh.first_b[group], sh.first_at[group]);
     }
 
@@ -344,7 +380,7 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
     // without a division, and its first page is fetched a step early.
     const int spp = a.cache.page_size >> 4;  // strips per page
     const size_t v_off = static_cast<size_t>(pb.Hkv) * spp * strip_bytes, page_bytes = 2 * v_off;
-    const int v_warp = gm.C > 1 ? 1 : 0;
+    const int v_warp = C > 1 ? 1 : 0;
     auto valid_page = [&](int page, int b) {
         if (static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.num_pages)) return page;
         // the sequence's rows are undefined, but the copies stay inside the cache
@@ -458,16 +494,8 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
                 tile += kKv4Tile;
                 q += NB * 64;
             };
-            if (CH == 1) {
-                one(sum[0]);
-            } else {
-                int c = 0;
-                for (; c + 1 < gm.chunks; c += 2) {
-                    one(sum[0]);
-                    one(sum[SW == 1 ? 1 : 0]);
-                }
-                if (c < gm.chunks) one(sum[0]);
-            }
+#pragma unroll
+            for (int c = 0; c < N; ++c) one(sum[SW == 1 ? c & 1 : 0]);
         }
 #pragma unroll
         for (int i = 0; i < SW; ++i)
@@ -535,17 +563,17 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int r = n * 8 + 2 * t + q;
-                if (cur.rb * gm.rows + r >= R) continue;
+                if (cur.rb * kRows + r >= R) continue;
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     if (chunk0 + c < wg * CH) continue;
-                    float4* o = reinterpret_cast<float4*>(gm.part + (slot * gm.rows + r) * pb.D + (chunk0 + c) * 64 + 8 * g);
+                    float4* o = reinterpret_cast<float4*>(gm.part + (slot * kRows + r) * D + (chunk0 + c) * 64 + 8 * g);
                     o[0] = make_float4(acc[c][0][n][q], acc[c][0][n][q + 2], acc[c][1][n][q], acc[c][1][n][q + 2]);
                     o[1] = make_float4(acc[c][2][n][q], acc[c][2][n][q + 2], acc[c][3][n][q], acc[c][3][n][q + 2]);
                 }
                 if (wg == 0 && g == 0) {
-                    gm.ml[(slot * gm.rows + r) * 2] = m[n][q];
-                    gm.ml[(slot * gm.rows + r) * 2 + 1] = l[n][q];
+                    gm.ml[(slot * kRows + r) * 2] = m[n][q];
+                    gm.ml[(slot * kRows + r) * 2 + 1] = l[n][q];
                 }
             }
     };
@@ -553,7 +581,7 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
     while (more) {
         // ---- Q of the piece's rows as B operands: fp16, scaled by a power of two into its range (bf16 has the wider
         // one). A lane holds query g, head dims 16 t .. 16 t + 15 of a chunk; each warp takes every C-th chunk.
-        const int r0 = cur.rb * gm.rows;
+        const int r0 = cur.rb * kRows;
         least = pb.causal ? cur.len - pb.Nq + 1 : cur.len;
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
@@ -564,9 +592,9 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
             uint32_t amax = 0;  // magnitudes of 16-bit floats order as their bits do
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const int c = wg + j * gm.C;
+                const int c = wg + j * C;
                 x[j] = y[j] = make_uint4(0, 0, 0, 0);
-                if (r < R && c < gm.chunks) {
+                if (r < R && c < N) {
                     const uint4* src = reinterpret_cast<const uint4*>(q + c * 64 + t * 16);
                     x[j] = src[0];
                     y[j] = src[1];
@@ -582,7 +610,7 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
                 if (SW < 4) {
                     if (t == 0) sh.col[warp][k * 8 + g] = __uint_as_float(amax);
                     group_sync();
-                    for (int w = 0; w < gm.C; ++w) amax = max(amax, __float_as_uint(sh.col[group * gm.C + w][k * 8 + g]));
+                    for (int w = 0; w < C; ++w) amax = max(amax, __float_as_uint(sh.col[group * C + w][k * 8 + g]));
                 }
                 // largest magnitude to [2^14, 2^15); rows of zeros or that are not finite stay as they are
                 const int e = static_cast<int>(amax >> 7);
@@ -601,8 +629,8 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
             }
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const int c = wg + j * gm.C;
-                if (c < gm.chunks) {
+                const int c = wg + j * C;
+                if (c < N) {
                     q_mem[(c * NB + k) * 64] = x[j];
                     q_mem[(c * NB + k) * 64 + 32] = y[j];
                 }
@@ -681,7 +709,7 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         float mx = -INFINITY;
-                        for (int w = 0; w < gm.C; ++w) mx = fmaxf(mx, sh.col[group * gm.C + w][k * 8 + 2 * t + q]);
+                        for (int w = 0; w < C; ++w) mx = fmaxf(mx, sh.col[group * C + w][k * 8 + 2 * t + q]);
                         // how far it moves; a row's keys come first, so one without any in the piece's first step has
                         // none in the piece
                         float up = mx - kRefBelow;
@@ -730,7 +758,7 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 l[n][q] = 0.f;
-                for (int w = 0; w < gm.C; ++w) l[n][q] += sh.sum[group * gm.C + w][n * 8 + 2 * t + q];
+                for (int w = 0; w < C; ++w) l[n][q] += sh.sum[group * C + w][n * 8 + 2 * t + q];
                 if (l[n][q] == 0.f) m[n][q] = -INFINITY;  // no keys, no reference
             }
 
@@ -765,7 +793,7 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
             Piece next = cur;
             more = next_piece(a, gm, next);
             if (more) {
-                store_part(2 * (static_cast<size_t>(blockIdx.x) * gm.NG + group));
+                store_part(2 * (static_cast<size_t>(blockIdx.x) * NG + group));
                 cur = next;
             } else {
                 pending = true;
@@ -802,7 +830,7 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
             return sh.last[i][0] == cur.b && sh.last[i][1] == cur.hk && sh.last[i][2] == cur.rb;
         };
         while (run0 > 0 && same(run0 - 1)) --run0;
-        while (run1 + 1 < gm.NG && same(run1 + 1)) ++run1;
+        while (run1 + 1 < NG && same(run1 + 1)) ++run1;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -840,30 +868,30 @@ __global__ void __launch_bounds__(NB == 1 ? 512 : 384, 1) decode_kv4_kernel(cons
     __syncthreads();
     if (!pending) return;
     // the part goes to slot 1 of the run's last group
-    const size_t slot = 2 * (static_cast<size_t>(blockIdx.x) * gm.NG + run1) + 1;
-    const int r0 = cur.rb * gm.rows;
+    const size_t slot = 2 * (static_cast<size_t>(blockIdx.x) * NG + run1) + 1;
+    const int r0 = cur.rb * kRows;
     for (int e = group - run0; e < kRegs; e += run1 - run0 + 1) {
         const int c = e / (4 * NB), i = e / NB % 4, n = e % NB;
         if (chunk0 + c < wg * CH) continue;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = run0; k <= run1; ++k) {
-            const float4 v = buf[(static_cast<size_t>(k * gm.C + wg) * kRegs + e) * 32];
+            const float4 v = buf[(static_cast<size_t>(k * C + wg) * kRegs + e) * 32];
             x.x += v.x;
             x.y += v.y;
             x.z += v.z;
             x.w += v.w;
         }
         const int r = n * 8 + 2 * t;
-        float* o = gm.part + (slot * gm.rows + r) * pb.D + (chunk0 + c) * 64 + 8 * g + 2 * i;
+        float* o = gm.part + (slot * kRows + r) * D + (chunk0 + c) * 64 + 8 * g + 2 * i;
         if (r0 + r < R) *reinterpret_cast<float2*>(o) = make_float2(x.x, x.z);
-        if (r0 + r + 1 < R) *reinterpret_cast<float2*>(o + pb.D) = make_float2(x.y, x.w);
+        if (r0 + r + 1 < R) *reinterpret_cast<float2*>(o + D) = make_float2(x.y, x.w);
     }
     if (group == run1 && wg == 0 && g == 0)
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                float* ml = gm.ml + (slot * gm.rows + n * 8 + 2 * t + q) * 2;
+                float* ml = gm.ml + (slot * kRows + n * 8 + 2 * t + q) * 2;
                 ml[0] = m[n][q];
                 ml[1] = l[n][q];
             }
@@ -981,40 +1009,20 @@ __global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_kernel(const Kv4
 
 struct Plan {
     Kv4Geo gm;
-    int ctas;
-    int nb, ch, sw;
-    int smem;
+    int ctas, nb;
     size_t part_floats, bytes;
 };
 
-// Eight query rows per step up to G * Nq = 8, else blocks of sixteen. A warp
-// accumulates two chunks of O^T. As many groups as registers hold (128 per
-// thread for eight rows, 168 for sixteen), and steps as long as shared memory
-// then allows: four strips per warp in groups of one warp, else two or one.
+// Eight query rows per step up to G * Nq = 8, else blocks of sixteen.
 Plan plan(const Problem& pb)
 {
     Plan p{};
     Kv4Geo& gm = p.gm;
     const long long R = static_cast<long long>(pb.Hq / pb.Hkv) * pb.Nq;
-    gm.chunks = pb.D >> 6;
     p.nb = R <= 8 ? 1 : 2;
     gm.rows = 8 * p.nb;
     gm.rblocks = static_cast<int>((R + gm.rows - 1) / gm.rows);
-    p.ch = gm.chunks > 1 ? 2 : 1;
-    gm.C = (gm.chunks + p.ch - 1) / p.ch;
-    const int room = kMaxSmem - 1024 - static_cast<int>(sizeof(DecShared));
-    gm.NG = (p.nb == 1 ? 16 : 12) / gm.C;
-    for (p.sw = gm.C == 1 ? 4 : 2;; p.sw >>= 1) {
-        const int strips = gm.C * p.sw;
-        gm.group_bytes = 2 * strips * gm.chunks * kKv4Tile + gm.chunks * p.nb * 1024 + strips * p.nb * 256;
-        if (gm.NG * gm.group_bytes <= room || gm.C == 1) break;
-        if (p.sw == 1) {
-            gm.NG = room / gm.group_bytes;
-            break;
-        }
-    }
-    const int join = gm.NG * gm.C * p.ch * 4 * p.nb * 512;
-    p.smem = gm.NG * gm.group_bytes > join ? gm.NG * gm.group_bytes : join;
+    gm.NG = shape_of(pb.D >> 6, p.nb).NG;
     const int sms = num_sms();
     p.ctas = sms > 0 ? sms : 152;
     gm.workers = p.ctas * gm.NG;
@@ -1023,23 +1031,23 @@ Plan plan(const Problem& pb)
     return p;
 }
 
-template <int CH, int NB, int SW>
-cudaError_t launch_variant(const Kv4Decode& a, const Plan& p, cudaStream_t s)
+template <int N, int NB>
+cudaError_t launch_shape(const Kv4Decode& a, const Plan& p, cudaStream_t s)
 {
-    auto* kernel = decode_kv4_kernel<CH, NB, SW>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+    constexpr Shape shape = shape_of(N, NB);
+    auto* kernel = decode_kv4_kernel<N, NB>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shape.smem);
     if (e != cudaSuccess) return e;
-    kernel<<<p.ctas, p.gm.NG * p.gm.C * 32, p.smem, s>>>(a, p.gm);
+    kernel<<<p.ctas, shape.NG * shape.C * 32, shape.smem, s>>>(a, p.gm);
     return cudaGetLastError();
 }
 
-template <int NB>
-cudaError_t launch_rows(const Kv4Decode& a, const Plan& p, cudaStream_t s)
+template <int N>
+cudaError_t launch_chunks(const Kv4Decode& a, const Plan& p, cudaStream_t s)
 {
-    return p.ch == 1   ? launch_variant<1, NB, 4>(a, p, s)
-           : p.sw == 4 ? launch_variant<2, NB, 4>(a, p, s)
-           : p.sw == 2 ? launch_variant<2, NB, 2>(a, p, s)
-                       : launch_variant<2, NB, 1>(a, p, s);
+    if (a.f.pb.D >> 6 == N) return p.nb == 1 ? launch_shape<N, 1>(a, p, s) : launch_shape<N, 2>(a, p, s);
+    if constexpr (N > 1) return launch_chunks<N - 1>(a, p, s);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -1051,7 +1059,7 @@ cudaError_t launch_decode_kv4(const Kv4Decode& a, void* workspace, cudaStream_t 
     Plan p = plan(a.f.pb);
     p.gm.part = static_cast<float*>(workspace);
     p.gm.ml = p.gm.part + p.part_floats;
-    const cudaError_t ran = p.nb == 1 ? launch_rows<1>(a, p, s) : launch_rows<2>(a, p, s);
+    const cudaError_t ran = launch_chunks<16>(a, p, s);
     if (ran != cudaSuccess) return ran;
     const Problem& pb = a.f.pb;
     cudaLaunchConfig_t cfg{};
