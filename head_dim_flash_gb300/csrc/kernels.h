@@ -224,6 +224,7 @@ struct Kv4Io {
     const int* count;         // device [B]: tokens of each sequence (null: N); unused when packed
     const int* cu;            // device [B + 1]: packed token offsets, or null
     int total;
+    int strips_per_cta;       // set by the launch
     uint32_t* status;
 };
 cudaError_t launch_kv4_write(const Kv4Io& a, cudaStream_t s);

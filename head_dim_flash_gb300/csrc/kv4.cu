@@ -2,39 +2,256 @@
 // tokens back to 16 bits. The format is in kv4.cuh.
 //
 // Both are one pass over the data and bound by memory: a write reads 2 bytes
-// and stores 9/16 of a byte per value, a read the reverse. A warp owns one
-// tile of 16 tokens x 64 head dims, whose lanes hold it in the order in which
-// the cache stores it: a whole tile is one 16-byte store per lane plus the
-// scales, and the 16-bit side moves 128 contiguous bytes per token. A strip
-// that a sequence covers in part (its first and last) is stored token by
-// token, and the cells of other tokens are left as they were.
+// and stores 9/16 of a byte per value, a read the reverse. A warp owns a tile
+// of 16 tokens x 64 head dims of K and the one of V, whose lanes hold it in the
+// order in which the cache stores it: a whole tile is one 16-byte store per
+// lane plus the scales, and the 16-bit side moves 128 contiguous bytes per
+// token. A CTA takes some strips of 16 tokens of one (sequence, kv head), its
+// warps the head-dim chunks; the loads of the next tiles are issued before the
+// present ones are worked on. A strip that a sequence covers in part (its first
+// and last) is stored token by token, and the cells of other tokens are left as
+// they were.
+#include <type_traits>
+
 #include "kv4.cuh"
 
 namespace ffpa {
 namespace {
 
-constexpr int kIoWarps = 8;  // at most; one CTA per (sequence, kv head, strip of 16 tokens)
+constexpr int kIoWarps = 8;  // at most
+
+// The range of one (sequence, kv head), and its strips that this CTA takes.
+struct Range {
+    int b, h;
+    int p0, p1;         // cache positions
+    int first, last;    // strips [first, last)
+    long long row0;     // row of position p0 in the 16-bit tensor
+};
+
+__device__ __forceinline__ bool find_range(const Kv4Io& a, uint32_t site, Range& s)
+{
+    const long long u = unit_id();
+    if (u >= static_cast<long long>(a.B) * a.Hkv) return false;
+    s.b = static_cast<int>(u / a.Hkv);
+    s.h = static_cast<int>(u - static_cast<long long>(s.b) * a.Hkv);
+    int cnt;
+    if (!kv4_range(a, s.b, site, s.p0, cnt, s.row0)) return false;
+    s.p1 = s.p0 + cnt;
+    const long long first = (s.p0 >> 4) + static_cast<long long>(blockIdx.x) * a.strips_per_cta;
+    const int end = cnt > 0 ? ((s.p1 - 1) >> 4) + 1 : 0;
+    if (first >= end) return false;
+    s.first = static_cast<int>(first);
+    s.last = static_cast<int>(first + a.strips_per_cta < end ? first + a.strips_per_cta : end);
+    return true;
+}
+
+// Element offset of this (sequence, head)'s row of position 16 `strip`, which may lie before the range.
+__device__ __forceinline__ long long strip_row(const Kv4Io& a, const Range& s, const View& v, int strip)
+{
+    return (a.cu ? 0 : s.b * v.sb) + s.h * v.sh + (s.row0 + (16LL * strip - s.p0)) * v.sn;
+}
+
+// The K tiles of consecutive strips: null (and the status word) where the page is outside the cache.
+struct Tiles {
+    uint8_t* at;
+    int in;          // place of the strip in its page
+    const int* row;  // its entry in the block table
+};
+
+__device__ __forceinline__ void page_tiles(const Kv4Io& a, const Range& s, uint32_t site, Tiles& x)
+{
+    const int page = *x.row;
+    x.at = nullptr;
+    if (page >= 0 && page < a.cache.num_pages)
+        x.at = a.cache.data + kv4_strip_offset(a.cache, a.Hkv, a.D >> 6, page, 0, s.h, x.in);
+    else if (threadIdx.x == 0)
+        kv4_invalid(a.status, site, s.b);
+}
+
+__device__ __forceinline__ Tiles first_tiles(const Kv4Io& a, const Range& s, uint32_t site)
+{
+    const int spp = a.cache.page_size >> 4, block = s.first / spp;
+    Tiles x{nullptr, s.first - block * spp, a.cache.table + s.b * a.cache.table_stride + block};
+    page_tiles(a, s, site, x);
+    return x;
+}
+
+__device__ __forceinline__ void next_tiles(const Kv4Io& a, const Range& s, uint32_t site, Tiles& x)
+{
+    if (++x.in < a.cache.page_size >> 4) {
+        if (x.at) x.at += (a.D >> 6) * kKv4Tile;
+        return;
+    }
+    x.in = 0;
+    ++x.row;
+    page_tiles(a, s, site, x);
+}
+
+// The tokens of a tile that a lane holds: of K two (hi = 0, 1), of V four (j = 0 .. 3).
+__device__ __forceinline__ int k_token(int g, int hi) { return g + 8 * hi; }
+__device__ __forceinline__ int v_token(int t, int j) { return 2 * t + (j & 1) + 8 * (j >> 1); }
+
+// ---------------------------------------------------------------- write
+// Largest magnitude of four words of 16-bit values. A NaN is cleared from the words first: the cache has none, one is
+// stored as zero.
+template <bool BF16>
+__device__ __forceinline__ float amax8(uint32_t (&w)[4])
+{
+    using T2 = typename std::conditional<BF16, __nv_bfloat162, __half2>::type;
+    T2 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __habs2(*reinterpret_cast<T2*>(&w[i]));
+    const T2 m = __hmax2_nan(__hmax2_nan(x[0], x[1]), __hmax2_nan(x[2], x[3]));
+    float2 f = unpack2<BF16>(*reinterpret_cast<const uint32_t*>(&m));
+    if (f.x != f.x || f.y != f.y) {
+        f.x = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 v = unpack2<BF16>(w[i]);
+            if (v.x != v.x) w[i] &= 0xffff0000u, v.x = 0.f;
+            if (v.y != v.y) w[i] &= 0x0000ffffu, v.y = 0.f;
+            f.x = fmaxf(f.x, fmaxf(fabsf(v.x), fabsf(v.y)));
+        }
+        return f.x;
+    }
+    return fmaxf(f.x, f.y);
+}
 
 template <bool BF16>
-__device__ __forceinline__ void unpack8(uint4 w, float (&x)[8])
+__device__ __forceinline__ uint32_t codes(const uint32_t (&w)[4], float rcp)
 {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<BF16>(u[i]);
-        x[2 * i] = f.x == f.x ? f.x : 0.f;  // the cache has no NaN: one is stored as zero
-        x[2 * i + 1] = f.y == f.y ? f.y : 0.f;
+        const float2 f = unpack2<BF16>(w[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+    return kv4_code8(x, rcp);
+}
+
+__device__ __forceinline__ void load4(const uint16_t* p, uint32_t (&w)[4])
+{
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kIoWarps * 32, 4) kv4_write_kernel(const Kv4Io a)
+{
+    Range s;
+    if (!find_range(a, VS_KV4_WRITE, s)) return;
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int chunks = a.D >> 6;
+    const size_t v_off = static_cast<size_t>(a.Hkv) * (a.cache.page_size >> 4) * chunks * kKv4Tile;
+    const uint16_t* k = static_cast<const uint16_t*>(a.k) + strip_row(a, s, a.vk, s.first) + g * a.vk.sn + t * 16;
+    const uint16_t* v = static_cast<const uint16_t*>(a.v) + strip_row(a, s, a.vv, s.first) + 2 * t * a.vv.sn + g * 8;
+    const long long k8 = 8 * a.vk.sn, v1 = a.vv.sn, v8 = 8 * a.vv.sn;
+
+    // one tile of K (two tokens, 16 head dims of each per lane) and of V (four tokens, eight head dims)
+    struct Data {
+        uint32_t k[2][2][4], v[4][4];
+    };
+    const uint16_t *kr = k, *vr = v;  // the next strip's rows
+    auto load = [&](int strip, Data& d) {
+        const int lo = s.p0 - 16 * strip, hi = s.p1 - 16 * strip;  // tokens of the strip in the range
+        if (lo <= 0 && hi >= 16) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                load4(kr + x * k8, d.k[x][0]);
+                load4(kr + x * k8 + 8, d.k[x][1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load4(vr + (j & 1) * v1 + (j >> 1) * v8, d.v[j]);
+        } else {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const bool in = k_token(g, x) >= lo && k_token(g, x) < hi;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d.k[x][y][e] = 0;
+                    if (in) load4(kr + x * k8 + 8 * y, d.k[x][y]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d.v[j][e] = 0;
+                if (v_token(t, j) >= lo && v_token(t, j) < hi) load4(vr + (j & 1) * v1 + (j >> 1) * v8, d.v[j]);
+            }
+        }
+        kr += 2 * k8;
+        vr += 2 * v8;
+    };
+    auto store = [&](int strip, int ch, Data& d, uint8_t* tiles) {
+        uint32_t kc[4], ks[2], vc[4], vs = 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const float m = fmaxf(amax8<BF16>(d.k[x][0]), amax8<BF16>(d.k[x][1]));
+            ks[x] = kv4_scale_code(m);
+            const float rcp = kv4_scale_rcp(ks[x]);
+            kc[2 * x] = codes<BF16>(d.k[x][0], rcp);
+            kc[2 * x + 1] = codes<BF16>(d.k[x][1], rcp);
+        }
+        // a V group's halves are in lanes g and g ^ 1: the even one finds the scales of tokens 0 and 1, the odd one those
+        // of 2 and 3
+        float m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            m[j] = amax8<BF16>(d.v[j]);
+            m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 4));
+        }
+        const bool odd = g & 1;
+        const uint32_t c0 = kv4_scale_code(odd ? m[2] : m[0]), c1 = kv4_scale_code(odd ? m[3] : m[1]);
+        const uint32_t mine = c0 | (c1 << 8), other = __shfl_xor_sync(0xffffffffu, mine, 4);
+        vs = odd ? other | (mine << 16) : mine | (other << 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) vc[j] = codes<BF16>(d.v[j], kv4_scale_rcp((vs >> (8 * j)) & 0xffu));
+        if (!tiles) return;
+        uint8_t* tile = tiles + ch * kKv4Tile;
+        uint8_t* vtile = tile + v_off;
+        uint8_t* scale = vtile + 512 + ((g >> 1) * 4 + t) * 4;
+        const int lo = s.p0 - 16 * strip, hi = s.p1 - 16 * strip;
+        if (lo <= 0 && hi >= 16) {
+            *reinterpret_cast<uint4*>(tile + lane * 16) = make_uint4(kc[0], kc[1], kc[2], kc[3]);
+            *reinterpret_cast<uint16_t*>(tile + 512 + lane * 2) = static_cast<uint16_t>(ks[0] | (ks[1] << 8));
+            *reinterpret_cast<uint4*>(vtile + lane * 16) = make_uint4(vc[0], vc[1], vc[2], vc[3]);
+            if (!(g & 1)) *reinterpret_cast<uint32_t*>(scale) = vs;
+            return;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (k_token(g, x) >= lo && k_token(g, x) < hi) {
+                *reinterpret_cast<uint2*>(tile + lane * 16 + 8 * x) = make_uint2(kc[2 * x], kc[2 * x + 1]);
+                tile[512 + lane * 2 + x] = static_cast<uint8_t>(ks[x]);
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (v_token(t, j) >= lo && v_token(t, j) < hi) {
+                *reinterpret_cast<uint32_t*>(vtile + lane * 16 + 4 * j) = vc[j];
+                if (!(g & 1)) scale[j] = static_cast<uint8_t>(vs >> (8 * j));
+            }
+    };
+    for (int ch = warp; ch < chunks; ch += warps) {
+        kr = k + ch * 64;
+        vr = v + ch * 64;
+        Tiles tiles = first_tiles(a, s, VS_KV4_WRITE);
+        for (int strip = s.first;;) {
+            Data x;
+            load(strip, x);
+            store(strip, ch, x, tiles.at);
+            if (++strip == s.last) break;
+            next_tiles(a, s, VS_KV4_WRITE, tiles);
+        }
     }
 }
 
-__device__ __forceinline__ float amax8(const float (&x)[8])
-{
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-    return m;
-}
-
+// ----------------------------------------------------------------- read
 // Four fp16 pairs (exact cache values) in the element type.
 template <bool BF16>
 __device__ __forceinline__ uint4 pack8(const uint32_t (&h)[4])
@@ -51,183 +268,89 @@ __device__ __forceinline__ uint4 pack8(const uint32_t (&h)[4])
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// The strip of this CTA: false when the sequence does not reach it.
-struct Strip {
-    int b, h;
-    int t0;          // its first cache position
-    int p0, p1;      // the sequence's range of positions
-    long long row0;  // row of position p0 in the 16-bit tensor
-    uint8_t* base;   // first K tile
-    size_t v_off;    // from a K tile to the V tile
-};
-
-__device__ __forceinline__ bool find_strip(const Kv4Io& a, uint32_t site, Strip& s)
-{
-    const long long u = unit_id();
-    if (u >= static_cast<long long>(a.B) * a.Hkv) return false;
-    s.b = static_cast<int>(u / a.Hkv);
-    s.h = static_cast<int>(u % a.Hkv);
-    int cnt;
-    if (!kv4_range(a, s.b, site, s.p0, cnt, s.row0)) return false;
-    s.p1 = s.p0 + cnt;
-    const long long t0 = (static_cast<long long>(s.p0 >> 4) + blockIdx.x) << 4;
-    if (t0 >= s.p1) return false;
-    s.t0 = static_cast<int>(t0);
-    const int block = s.t0 / a.cache.page_size;
-    const int page = a.cache.table[s.b * a.cache.table_stride + block];
-    if (page < 0 || page >= a.cache.num_pages) {
-        if (threadIdx.x == 0) kv4_invalid(a.status, site, s.b);
-        return false;
-    }
-    const int chunks = a.D >> 6;
-    s.base = a.cache.data +
-             kv4_strip_offset(a.cache, a.Hkv, chunks, page, 0, s.h, (s.t0 - block * a.cache.page_size) >> 4);
-    s.v_off = static_cast<size_t>(a.Hkv) * (a.cache.page_size >> 4) * chunks * kKv4Tile;
-    return true;
-}
-
-// Element offset of position p's row of this (sequence, head).
-__device__ __forceinline__ long long row_offset(const Kv4Io& a, const Strip& s, const View& v, int p)
-{
-    return (a.cu ? 0 : s.b * v.sb) + s.h * v.sh + (s.row0 + (p - s.p0)) * v.sn;
-}
-
-template <bool BF16>
-__global__ void __launch_bounds__(kIoWarps * 32) kv4_write_kernel(const Kv4Io a)
-{
-    Strip s;
-    if (!find_strip(a, VS_KV4_WRITE, s)) return;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int chunks = a.D >> 6;
-    for (int it = threadIdx.x >> 5; it < 2 * chunks; it += blockDim.x >> 5) {
-        const int ch = it < chunks ? it : it - chunks;
-        uint8_t* tile = s.base + static_cast<size_t>(ch) * kKv4Tile;
-        if (it < chunks) {
-            uint32_t code[4];
-            uint32_t sc[2];
-            bool in[2];
-#pragma unroll
-            for (int hi = 0; hi < 2; ++hi) {
-                const int p = s.t0 + g + 8 * hi;
-                in[hi] = p >= s.p0 && p < s.p1;
-                uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-                if (in[hi]) {
-                    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) +
-                                                                      row_offset(a, s, a.vk, p) + ch * 64 + t * 16);
-                    w0 = src[0];
-                    w1 = src[1];
-                }
-                float x0[8], x1[8];
-                unpack8<BF16>(w0, x0);
-                unpack8<BF16>(w1, x1);
-                sc[hi] = kv4_scale_code(fmaxf(amax8(x0), amax8(x1)));
-                const float f = kv4_scale_value(sc[hi]), rcp = f > 0.f ? 1.f / f : 0.f;
-                code[2 * hi] = kv4_code8(x0, rcp);
-                code[2 * hi + 1] = kv4_code8(x1, rcp);
-            }
-            if (in[0] && in[1]) {
-                *reinterpret_cast<uint4*>(tile + lane * 16) = make_uint4(code[0], code[1], code[2], code[3]);
-                *reinterpret_cast<uint16_t*>(tile + 512 + lane * 2) = static_cast<uint16_t>(sc[0] | (sc[1] << 8));
-            } else {
-#pragma unroll
-                for (int hi = 0; hi < 2; ++hi)
-                    if (in[hi]) {
-                        *reinterpret_cast<uint2*>(tile + lane * 16 + 8 * hi) = make_uint2(code[2 * hi], code[2 * hi + 1]);
-                        tile[512 + lane * 2 + hi] = static_cast<uint8_t>(sc[hi]);
-                    }
-            }
-        } else {
-            tile += s.v_off;
-            uint32_t code[4], sc = 0;
-            bool in[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int p = s.t0 + 2 * t + (j & 1) + 8 * (j >> 1);
-                in[j] = p >= s.p0 && p < s.p1;
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (in[j])
-                    w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v) + row_offset(a, s, a.vv, p) +
-                                                        ch * 64 + g * 8);
-                float x[8];
-                unpack8<BF16>(w, x);
-                float m = amax8(x);
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));  // the group's other half
-                const uint32_t c = kv4_scale_code(m);
-                const float f = kv4_scale_value(c), rcp = f > 0.f ? 1.f / f : 0.f;
-                code[j] = kv4_code8(x, rcp);
-                sc |= c << (8 * j);
-            }
-            uint8_t* scale = tile + 512 + ((g >> 1) * 4 + t) * 4;
-            if (in[0] && in[1] && in[2] && in[3]) {
-                *reinterpret_cast<uint4*>(tile + lane * 16) = make_uint4(code[0], code[1], code[2], code[3]);
-                if (!(g & 1)) *reinterpret_cast<uint32_t*>(scale) = sc;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (in[j]) {
-                        *reinterpret_cast<uint32_t*>(tile + lane * 16 + 4 * j) = code[j];
-                        if (!(g & 1)) scale[j] = static_cast<uint8_t>(sc >> (8 * j));
-                    }
-            }
-        }
-    }
-}
-
 template <bool BF16>
 __global__ void __launch_bounds__(kIoWarps * 32) kv4_read_kernel(const Kv4Io a)
 {
-    Strip s;
-    if (!find_strip(a, VS_KV4_READ, s)) return;
+    Range s;
+    if (!find_range(a, VS_KV4_READ, s)) return;
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int chunks = a.D >> 6;
-    for (int it = threadIdx.x >> 5; it < 2 * chunks; it += blockDim.x >> 5) {
-        const int ch = it < chunks ? it : it - chunks;
-        const uint8_t* tile = s.base + static_cast<size_t>(ch) * kKv4Tile + (it < chunks ? 0 : s.v_off);
-        const uint4 w = *reinterpret_cast<const uint4*>(tile + lane * 16);
-        const uint32_t code[4] = {w.x, w.y, w.z, w.w};
-        if (it < chunks) {
-            const uint32_t sc = *reinterpret_cast<const uint16_t*>(tile + 512 + lane * 2);
+    const size_t v_off = static_cast<size_t>(a.Hkv) * (a.cache.page_size >> 4) * chunks * kKv4Tile;
+    uint16_t* k = static_cast<uint16_t*>(a.k) + strip_row(a, s, a.vk, s.first) + g * a.vk.sn + t * 16;
+    uint16_t* v = static_cast<uint16_t*>(a.v) + strip_row(a, s, a.vv, s.first) + 2 * t * a.vv.sn + g * 8;
+    const long long k8 = 8 * a.vk.sn, v1 = a.vv.sn, v8 = 8 * a.vv.sn;
+
+    struct Data {
+        uint4 k, v;
+        uint32_t ks, vs;
+    };
+    uint16_t *kr = k, *vr = v;  // the next strip's rows
+    auto load = [&](int ch, const uint8_t* tiles, Data& d) {
+        if (!tiles) return;
+        const uint8_t* tile = tiles + ch * kKv4Tile;
+        d.k = __ldcs(reinterpret_cast<const uint4*>(tile + lane * 16));
+        d.v = __ldcs(reinterpret_cast<const uint4*>(tile + v_off + lane * 16));
+        d.ks = __ldcs(reinterpret_cast<const uint16_t*>(tile + 512 + lane * 2));
+        d.vs = __ldcs(reinterpret_cast<const uint32_t*>(tile + v_off + 512 + ((g >> 1) * 4 + t) * 4));
+    };
+    auto store = [&](int strip, const Data& d) {
+        const int lo = s.p0 - 16 * strip, hi = s.p1 - 16 * strip;  // tokens of the strip in the range
+        const bool all = lo <= 0 && hi >= 16;
+        const uint32_t kc[4] = {d.k.x, d.k.y, d.k.z, d.k.w}, vc[4] = {d.v.x, d.v.y, d.v.z, d.v.w};
+        uint32_t h[4];
 #pragma unroll
-            for (int hi = 0; hi < 2; ++hi) {
-                const int p = s.t0 + g + 8 * hi;
-                if (p < s.p0 || p >= s.p1) continue;
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k) + row_offset(a, s, a.vk, p) + ch * 64 +
-                                                      t * 16);
-                const uint32_t s2 = kv4_scale2(sc >> (8 * hi));
-                uint32_t h[4];
-                kv4_dequant8(code[2 * hi], s2, h);
+        for (int x = 0; x < 2; ++x)
+            if (all || (k_token(g, x) >= lo && k_token(g, x) < hi)) {
+                const uint32_t s2 = kv4_scale2(d.ks >> (8 * x));
+                uint4* dst = reinterpret_cast<uint4*>(kr + x * k8);
+                kv4_dequant8(kc[2 * x], s2, h);
                 dst[0] = pack8<BF16>(h);
-                kv4_dequant8(code[2 * hi + 1], s2, h);
+                kv4_dequant8(kc[2 * x + 1], s2, h);
                 dst[1] = pack8<BF16>(h);
             }
-        } else {
-            const uint32_t sc = *reinterpret_cast<const uint32_t*>(tile + 512 + ((g >> 1) * 4 + t) * 4);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int p = s.t0 + 2 * t + (j & 1) + 8 * (j >> 1);
-                if (p < s.p0 || p >= s.p1) continue;
-                uint32_t h[4];
-                kv4_dequant8(code[j], kv4_scale2(sc >> (8 * j)), h);
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v) + row_offset(a, s, a.vv, p) + ch * 64 + g * 8) =
-                    pack8<BF16>(h);
+        for (int j = 0; j < 4; ++j)
+            if (all || (v_token(t, j) >= lo && v_token(t, j) < hi)) {
+                kv4_dequant8(vc[j], kv4_scale2(d.vs >> (8 * j)), h);
+                *reinterpret_cast<uint4*>(vr + (j & 1) * v1 + (j >> 1) * v8) = pack8<BF16>(h);
             }
+    };
+    for (int ch = warp; ch < chunks; ch += warps) {
+        kr = k + ch * 64;
+        vr = v + ch * 64;
+        Tiles tiles = first_tiles(a, s, VS_KV4_READ);
+        for (int strip = s.first;;) {
+            Data x;
+            load(ch, tiles.at, x);
+            if (tiles.at) store(strip, x);
+            kr += 2 * k8;
+            vr += 2 * v8;
+            if (++strip == s.last) break;
+            next_tiles(a, s, VS_KV4_READ, tiles);
         }
     }
 }
 
-// CTAs along x: the strips that N tokens can touch (one more when a start need not be a multiple of 16).
-bool io_grid(const Kv4Io& a, dim3* grid, unsigned* threads)
+// One warp per chunk, at most kIoWarps; CTAs along x cover the strips that N tokens can touch (one more when a start need
+// not be a multiple of 16). A CTA takes two strips where there are enough to keep the SMs full: at D = 512 that is worth
+// 6% of a prompt's write and 9% of a read against one, and four cost 5%.
+bool io_grid(Kv4Io& a, dim3* grid, unsigned* threads)
 {
     const long long strips = (static_cast<long long>(a.N) + (a.start ? 30 : 15)) >> 4;
-    const int items = 2 * (a.D >> 6);
-    *threads = 32u * static_cast<unsigned>(items < kIoWarps ? items : kIoWarps);
-    return unit_grid(static_cast<unsigned>(strips), static_cast<long long>(a.B) * a.Hkv, grid);
+    const long long units = static_cast<long long>(a.B) * a.Hkv, sms = num_sms() > 0 ? num_sms() : 152;
+    a.strips_per_cta = strips * units >= 32 * sms ? 2 : 1;
+    const int chunks = a.D >> 6;
+    const int rounds = (chunks + kIoWarps - 1) / kIoWarps;
+    *threads = 32u * static_cast<unsigned>((chunks + rounds - 1) / rounds);
+    return unit_grid(static_cast<unsigned>((strips + a.strips_per_cta - 1) / a.strips_per_cta), units, grid);
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_write(const Kv4Io& a, cudaStream_t s)
+cudaError_t launch_kv4_write(const Kv4Io& io, cudaStream_t s)
 {
+    Kv4Io a = io;
     dim3 grid;
     unsigned threads;
     if (!io_grid(a, &grid, &threads)) return cudaErrorInvalidConfiguration;
@@ -238,8 +361,9 @@ cudaError_t launch_kv4_write(const Kv4Io& a, cudaStream_t s)
     return cudaGetLastError();
 }
 
-cudaError_t launch_kv4_read(const Kv4Io& a, cudaStream_t s)
+cudaError_t launch_kv4_read(const Kv4Io& io, cudaStream_t s)
 {
+    Kv4Io a = io;
     dim3 grid;
     unsigned threads;
     if (!io_grid(a, &grid, &threads)) return cudaErrorInvalidConfiguration;

@@ -85,38 +85,46 @@ __device__ __forceinline__ void kv4_dequant8(uint32_t w, uint32_t scale2, uint32
     for (int i = 0; i < 4; ++i) h[i] = hmul2_u32(h[i], scale2);
 }
 
+// Quotients that have to fall on a border between two codes exactly when the
+// true quotient does. An input has at most 11 significant bits, a scale 4 and
+// a border 5: a true quotient that is not a border is at least 2^-11 of itself
+// away from one, and a product with an approximate reciprocal is 2^-22 of it
+// off. Rounding the product to a coarser grid that holds the borders puts it
+// back on a border that it belongs on and moves it across none, so the
+// nearest-even rounding that follows decides as it would on the true quotient.
+
 // Scale byte of a group whose largest magnitude is amax (not NaN; values past
 // 61440 = 6 x 10240, infinity among them, count as 61440, so that every cached
-// value is a finite fp16 number): amax / 6 rounded to nearest even to three
-// bits of mantissa, steps of 2^-17 below 2^-14. The division is correctly
-// rounded, and amax has at most 11 significant bits: a quotient that is not on
-// a border between two scales is further than 2^-12 of itself away from it, so
-// the fp32 quotient rounds as the exact one does.
+// value is a finite fp16 number): amax / 6, here to 16 significant bits, rounded
+// to nearest even to three bits of mantissa, steps of 2^-17 below 2^-14.
 __device__ __forceinline__ uint32_t kv4_scale_code(float amax)
 {
-    const float v = __fdiv_rn(fminf(amax, 61440.f), 6.f);
-    if (v < 6.103515625e-05f) return static_cast<uint32_t>(__float2int_rn(v * 131072.f));  // 2^-14, 2^17
-    uint32_t u = __float_as_uint(v);
-    u += 0x7ffffu + ((u >> 20) & 1u);
-    return (u >> 20) - ((127u - 15u) << 3);
+    const float v = __uint_as_float((__float_as_uint(fminf(amax, 61440.f) * (1.f / 6.f)) + 0x80u) & ~0xffu);
+    const uint32_t u = __float_as_uint(v);
+    const uint32_t normal = ((u + 0x7ffffu + ((u >> 20) & 1u)) >> 20) - ((127u - 15u) << 3);
+    const uint32_t small = __float_as_uint(v + 64.f) - __float_as_uint(64.f);  // 2^-17 is the last place of 64
+    return v < 6.103515625e-05f ? small : normal;                              // 2^-14
 }
 
-__device__ __forceinline__ float kv4_scale_value(uint32_t code)
+// 1 / scale (0 for a scale of 0), to 2^-22.
+__device__ __forceinline__ float kv4_scale_rcp(uint32_t code)
 {
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(code << 7)));
+    const float f = __half2float(__ushort_as_half(static_cast<unsigned short>(code << 7)));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(f));
+    return code ? r : 0.f;
 }
 
-// Codes of eight values (four bytes) from their products with 1 / scale. The quotient of an
-// input (at most 11 significant bits) by a scale (4 bits) either is a border
-// between two codes or is at least 2^-11 of itself away from it, while the
-// product with the rounded reciprocal is 2^-23 off: rounding it to 16 bits
-// puts it back on a border that it belongs on and moves it across none, so
-// the ties of the conversion (nearest even, saturating) are the exact ones.
-__device__ __forceinline__ float kv4_snap(float q)
+// |x| / scale on a grid of 2^-15 (the unit in the last place of 384; the
+// smallest border is 1/4, which a different quotient misses by 2^-13), with
+// the sign of x.
+__device__ __forceinline__ float kv4_quotient(float x, float rcp)
 {
-    return __uint_as_float((__float_as_uint(q) + 0x80u) & ~0xffu);
+    const float q = fmaf(fabsf(x), rcp, 384.f) - 384.f;
+    return __uint_as_float(__float_as_uint(q) | (__float_as_uint(x) & 0x80000000u));
 }
 
+// Codes of eight values (four bytes): nearest even, saturating.
 __device__ __forceinline__ uint32_t kv4_code8(const float (&x)[8], float rcp)
 {
     uint32_t r;
@@ -129,8 +137,9 @@ __device__ __forceinline__ uint32_t kv4_code8(const float (&x)[8], float rcp)
         " mov.b32 %0, {a, b, c, d};\n"
         "}\n"
         : "=r"(r)
-        : "f"(kv4_snap(x[0] * rcp)), "f"(kv4_snap(x[1] * rcp)), "f"(kv4_snap(x[2] * rcp)), "f"(kv4_snap(x[3] * rcp)),
-          "f"(kv4_snap(x[4] * rcp)), "f"(kv4_snap(x[5] * rcp)), "f"(kv4_snap(x[6] * rcp)), "f"(kv4_snap(x[7] * rcp)));
+        : "f"(kv4_quotient(x[0], rcp)), "f"(kv4_quotient(x[1], rcp)), "f"(kv4_quotient(x[2], rcp)),
+          "f"(kv4_quotient(x[3], rcp)), "f"(kv4_quotient(x[4], rcp)), "f"(kv4_quotient(x[5], rcp)),
+          "f"(kv4_quotient(x[6], rcp)), "f"(kv4_quotient(x[7], rcp)));
     return r;
 }
 
