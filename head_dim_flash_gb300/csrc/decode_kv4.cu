@@ -89,8 +89,7 @@ __host__ __device__ constexpr Shape shape_of(int N, int NB)
             break;
         }
     }
-    const int join = p.NG * p.C * p.CH * 4 * NB * 512;  // the parts that a CTA's groups end with
-    p.smem = p.NG * p.group_bytes > join ? p.NG * p.group_bytes : join;
+    p.smem = p.NG * p.group_bytes;
     return p;
 }
 
@@ -310,6 +309,7 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
         const int per = (pb.B + kThreads - 1) / kThreads;
         const int b0 = min(static_cast<int>(threadIdx.x) * per, pb.B), b1 = min(b0 + per, pb.B);
         long long sum = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) sum += cost_of(cached_len(a, b));
         long long incl = sum;
 #pragma unroll
@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
         if (threadIdx.x == 0) sh.abort_flag = 0;
         __syncthreads();
         total = 0;
+#pragma unroll 1
         for (int w = 0; w < warps; ++w) {
             if (w < warp) incl += sh.sums[w];
             total += sh.sums[w];
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
         total *= units_b;
         chunk = (total + gm.workers - 1) / gm.workers;
         const long long lo = (incl - sum) * units_b, hi = incl * units_b;
+#pragma unroll 1
         for (int i = 0; i < NG; ++i) {
             const long long at = (static_cast<long long>(blockIdx.x) * NG + i) * chunk;
             if (at < lo || at >= hi || at >= total) continue;
@@ -374,6 +376,25 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
     {
         const long long at = (static_cast<long long>(blockIdx.x) * NG + group) * chunk;
         more = first_piece(a, gm, cur, at, min(at + chunk, total), sh.first_b[group], sh.first_at[group]);
+    }
+
+    // Q of the piece's rows over every C-th chunk: a lane holds query g (of block k), head dims 16 t .. 16 t + 15 of a
+    // chunk; null where there is no such row or chunk
+    auto q_part = [&](int k, int j) -> const uint4* {
+        const int r = cur.rb * kRows + k * 8 + g, c = wg + j * C;
+        const int h = cur.hk * G + r / pb.Nq, i = r % pb.Nq;
+        return r < R && c < N ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.f.q) + cur.b * pb.vq.sb +
+                                                               h * pb.vq.sh + i * pb.vq.sn + c * 64 + t * 16)
+                              : nullptr;
+    };
+    if (more) {  // on its way while the loads are set up
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const uint4* q = q_part(k, j);
+                if (q) asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+            }
     }
 
     // ---- loads: K by the group's first warp, V by its second (lane 0). The place of a step in the block table moves
@@ -579,26 +600,18 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
     };
 
     while (more) {
-        // ---- Q of the piece's rows as B operands: fp16, scaled by a power of two into its range (bf16 has the wider
-        // one). A lane holds query g, head dims 16 t .. 16 t + 15 of a chunk; each warp takes every C-th chunk.
+        // ---- Q as B operands: fp16, scaled by a power of two into its range (bf16 has the wider one)
         const int r0 = cur.rb * kRows;
         least = pb.causal ? cur.len - pb.Nq + 1 : cur.len;
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int r = r0 + k * 8 + g;
-            const int h = cur.hk * G + r / pb.Nq, i = r % pb.Nq;
-            const uint16_t* q = static_cast<const uint16_t*>(a.f.q) + cur.b * pb.vq.sb + h * pb.vq.sh + i * pb.vq.sn;
             uint4 x[CH], y[CH];
             uint32_t amax = 0;  // magnitudes of 16-bit floats order as their bits do
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const int c = wg + j * C;
-                x[j] = y[j] = make_uint4(0, 0, 0, 0);
-                if (r < R && c < N) {
-                    const uint4* src = reinterpret_cast<const uint4*>(q + c * 64 + t * 16);
-                    x[j] = src[0];
-                    y[j] = src[1];
-                }
+                const uint4* q = q_part(k, j);
+                x[j] = q ? q[0] : make_uint4(0, 0, 0, 0);
+                y[j] = q ? q[1] : make_uint4(0, 0, 0, 0);
                 const uint32_t w[8] = {x[j].x, x[j].y, x[j].z, x[j].w, y[j].x, y[j].y, y[j].z, y[j].w};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) amax = max(amax, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
@@ -806,95 +819,65 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
             if (wg == (kv ? v_warp : 0) && sh.load[group][kv].loads > 0)
                 mbar_wait(&full[kv], (sh.load[group][kv].loads - 1) & 1u, &sh.abort_flag, a.f.ctl.status, a.f.ctl.limit_ns,
                           KS_DRAIN, false);
-    if (pending && wg == 0) {
-        if (lane == 0) {
-            sh.last[group][0] = cur.b;
-            sh.last[group][1] = cur.hk;
-            sh.last[group][2] = cur.rb;
-        }
-        if (g == 0)
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    sh.ml[group][n * 8 + 2 * t + q][0] = m[n][q];
-                    sh.ml[group][n * 8 + 2 * t + q][1] = l[n][q];
-                }
-    }
-    __syncthreads();  // every copy has been read: the buffers are free
-
-    // ---- neighbouring groups that end in the same unit join their parts in shared memory, each group a share of it
-    int run0 = group, run1 = group;
+    // ---- a part that the group ends with: to its own shared memory, [warp][row][head dims of the warp's chunks]
+    constexpr int kPartPitch = 64 * CH + 4, kPartFloats = kRows * kPartPitch;
+    static_assert(C * kPartFloats * 4 <= kShape.group_bytes, "a group's part");
     if (pending) {
-        auto same = [&](int i) {
-            return sh.last[i][0] == cur.b && sh.last[i][1] == cur.hk && sh.last[i][2] == cur.rb;
-        };
-        while (run0 > 0 && same(run0 - 1)) --run0;
-        while (run1 + 1 < NG && same(run1 + 1)) ++run1;
+        float* mine = reinterpret_cast<float*>(k_mem) + wg * kPartFloats;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int r = n * 8 + 2 * t + q;
-                float mx = -INFINITY, sum = 0.f;
-                for (int i = run0; i <= run1; ++i) mx = fmaxf(mx, sh.ml[i][r][0]);
-                const float mu = mx == -INFINITY ? 0.f : mx;
-                for (int i = run0; i <= run1; ++i) sum += sh.ml[i][r][1] * ex2_approx(sh.ml[i][r][0] - mu);
-                const float f = ex2_approx(m[n][q] - mu);
-                m[n][q] = mx;
-                l[n][q] = sum;
+                float4* o = reinterpret_cast<float4*>(mine + r * kPartPitch + 8 * g);
 #pragma unroll
-                for (int c = 0; c < CH; ++c)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        acc[c][i][n][q] *= f;
-                        acc[c][i][n][q + 2] *= f;
-                    }
+                for (int c = 0; c < CH; ++c) {
+                    o[16 * c] = make_float4(acc[c][0][n][q], acc[c][0][n][q + 2], acc[c][1][n][q], acc[c][1][n][q + 2]);
+                    o[16 * c + 1] = make_float4(acc[c][2][n][q], acc[c][2][n][q + 2], acc[c][3][n][q], acc[c][3][n][q + 2]);
+                }
+                if (wg == 0 && g == 0) {
+                    sh.ml[group][r][0] = m[n][q];
+                    sh.ml[group][r][1] = l[n][q];
+                }
             }
-    }
-    float4* const buf = reinterpret_cast<float4*>(smem) + lane;
-    constexpr int kRegs = CH * 4 * NB;  // float4 per lane
-    if (pending) {
-        float4* mine = buf + static_cast<size_t>(warp) * kRegs * 32;
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-                    mine[((c * 4 + i) * NB + n) * 32] =
-                        make_float4(acc[c][i][n][0], acc[c][i][n][1], acc[c][i][n][2], acc[c][i][n][3]);
+        if (wg == 0 && lane == 0) {
+            sh.last[group][0] = cur.b;
+            sh.last[group][1] = cur.hk;
+            sh.last[group][2] = cur.rb;
+        }
     }
     __syncthreads();
     if (!pending) return;
-    // the part goes to slot 1 of the run's last group
+    // neighbouring groups that end in the same unit join their parts, their threads taking the values in turn; the sum
+    // goes to slot 1 of the last of them
+    int run0 = group, run1 = group;
+    auto same = [&](int i) { return sh.last[i][0] == cur.b && sh.last[i][1] == cur.hk && sh.last[i][2] == cur.rb; };
+    while (run0 > 0 && same(run0 - 1)) --run0;
+    while (run1 + 1 < NG && same(run1 + 1)) ++run1;
     const size_t slot = 2 * (static_cast<size_t>(blockIdx.x) * NG + run1) + 1;
-    const int r0 = cur.rb * kRows;
-    for (int e = group - run0; e < kRegs; e += run1 - run0 + 1) {
-        const int c = e / (4 * NB), i = e / NB % 4, n = e % NB;
-        if (chunk0 + c < wg * CH) continue;
+    const int items = min(kRows, R - cur.rb * kRows) * (D / 4);
+#pragma unroll 1
+    for (int e = ((group - run0) * C + wg) * 32 + lane; e < items; e += (run1 - run0 + 1) * C * 32) {
+        const int r = e / (D / 4), d = e % (D / 4) * 4, w = d / (64 * CH);
+        const float* at = reinterpret_cast<const float*>(smem) + w * kPartFloats + r * kPartPitch + d - 64 * min(w * CH, N - CH);
+        float mx = -INFINITY, sum = 0.f;
+#pragma unroll 1
+        for (int k = run0; k <= run1; ++k) mx = fmaxf(mx, sh.ml[k][r][0]);
+        const float mu = mx == -INFINITY ? 0.f : mx;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
         for (int k = run0; k <= run1; ++k) {
-            const float4 v = buf[(static_cast<size_t>(k * C + wg) * kRegs + e) * 32];
-            x.x += v.x;
-            x.y += v.y;
-            x.z += v.z;
-            x.w += v.w;
+            const float f = ex2_approx(sh.ml[k][r][0] - mu);
+            const float4 v = *reinterpret_cast<const float4*>(at + k * (kShape.group_bytes / 4));
+            sum += sh.ml[k][r][1] * f;
+            x.x = fmaf(v.x, f, x.x);
+            x.y = fmaf(v.y, f, x.y);
+            x.z = fmaf(v.z, f, x.z);
+            x.w = fmaf(v.w, f, x.w);
         }
-        const int r = n * 8 + 2 * t;
-        float* o = gm.part + (slot * kRows + r) * D + (chunk0 + c) * 64 + 8 * g + 2 * i;
-        if (r0 + r < R) *reinterpret_cast<float2*>(o) = make_float2(x.x, x.z);
-        if (r0 + r + 1 < R) *reinterpret_cast<float2*>(o + D) = make_float2(x.y, x.w);
+        *reinterpret_cast<float4*>(gm.part + (slot * kRows + r) * D + d) = x;
+        if (d == 0) *reinterpret_cast<float2*>(gm.ml + (slot * kRows + r) * 2) = make_float2(mx, sum);
     }
-    if (group == run1 && wg == 0 && g == 0)
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                float* ml = gm.ml + (slot * kRows + n * 8 + 2 * t + q) * 2;
-                ml[0] = m[n][q];
-                ml[1] = l[n][q];
-            }
 }
 
 // Joins the parts of units that several groups worked on; writes the rows of
@@ -907,9 +890,8 @@ __global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_kernel(const Kv4
 {
     const Problem& pb = a.f.pb;
     __shared__ long long sums[2][kJoinThreads / 32];
-    __shared__ float4 acc[kJoinThreads];
-    extern __shared__ float weight[];  // [CTAs + 1], then the slots
-    int* const slots = reinterpret_cast<int*>(weight) + gm.workers / gm.NG + 1;
+    __shared__ float4 accs[kJoinThreads];
+    __shared__ float2 mls[kJoinThreads / 32];
     const long long row = blockIdx.x;
     const int i = static_cast<int>(row % pb.Nq), h = static_cast<int>(row / pb.Nq % pb.Hq);
     const int b = static_cast<int>(row / (static_cast<long long>(pb.Nq) * pb.Hq));
@@ -955,56 +937,63 @@ __global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_kernel(const Kv4
     // v1 ends in this unit unless its range reaches strips of the next one; the parts that groups of a CTA end with
     // are in slot 1 of the last of them, a part that is followed by another unit is in slot 0
     const bool ends = min((v1 + 1LL) * chunk, total) <= end + kUnitCost;
-    const int vl = ends ? v1 : v1 - 1, c0 = v0 / gm.NG, parts = vl / gm.NG - c0 + 1 + (ends ? 0 : 1);
-    float mx = -INFINITY;
-    for (int k = lane; k < parts; k += 32) {
-        const bool tail = !ends && k == parts - 1;
-        const int s = tail ? 2 * v1 : 2 * min(vl, (c0 + k) * gm.NG + gm.NG - 1) + 1;
-        if (warp == 0) slots[k] = s;
-        mx = fmaxf(mx, gm.ml[(static_cast<size_t>(s) * gm.rows + r % gm.rows) * 2]);
-    }
-#pragma unroll
-    for (int e = 16; e; e >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, e));
-    const float mu = mx == -INFINITY ? 0.f : mx;
-    __syncthreads();
-    float l = 0.f;
-    for (int k = lane; k < parts; k += 32) {
-        const float* ml = gm.ml + (static_cast<size_t>(slots[k]) * gm.rows + r % gm.rows) * 2;
-        const float w = ex2_approx(ml[0] - mu);
-        l += w * ml[1];
-        if (warp == 0) weight[k] = w;
-    }
-#pragma unroll
-    for (int e = 16; e; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
-    __syncthreads();
+    const int vl = ends ? v1 : v1 - 1, c0 = v0 / gm.NG, parts = vl / gm.NG - c0 + 1 + (ends ? 0 : 1), rr = r % gm.rows;
+    const bool in = d < pb.D;
+    // a warp's parts relative to their own largest reference; four in flight
+    float m = -INFINITY, l = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (d < pb.D) {
-#pragma unroll 4
-        for (int k = warp; k < parts; k += kJoinThreads / 32) {
-            const float w = weight[k];
-            const float4 v = *reinterpret_cast<const float4*>(
-                gm.part + (static_cast<size_t>(slots[k]) * gm.rows + r % gm.rows) * pb.D + d);
-            x.x = fmaf(w, v.x, x.x);
-            x.y = fmaf(w, v.y, x.y);
-            x.z = fmaf(w, v.z, x.z);
-            x.w = fmaf(w, v.w, x.w);
-        }
-    }
-    acc[threadIdx.x] = x;
-    __syncthreads();
-    if (warp == 0 && d < pb.D) {
+    for (int k0 = warp; k0 < parts; k0 += 4 * (kJoinThreads / 32)) {
+        float2 ml[4];
+        float4 v[4];
 #pragma unroll
-        for (int w = 1; w < kJoinThreads / 32; ++w) {
-            const float4 v = acc[w * 32 + lane];
-            x.x += v.x;
-            x.y += v.y;
-            x.z += v.z;
-            x.w += v.w;
+        for (int e = 0; e < 4; ++e) {
+            const int k = k0 + e * (kJoinThreads / 32);
+            ml[e] = make_float2(-INFINITY, 0.f);
+            v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k >= parts) continue;
+            const size_t slot = !ends && k == parts - 1 ? 2 * v1 : 2 * min(vl, (c0 + k) * gm.NG + gm.NG - 1) + 1;
+            ml[e] = *reinterpret_cast<const float2*>(gm.ml + (slot * gm.rows + rr) * 2);
+            if (in) v[e] = *reinterpret_cast<const float4*>(gm.part + (slot * gm.rows + rr) * pb.D + d);
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        *reinterpret_cast<uint2*>(o) = make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
+        const float mx = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+        const float mu = mx == -INFINITY ? 0.f : mx, f0 = ex2_approx(m - mu);
+        l *= f0;
+        x = make_float4(x.x * f0, x.y * f0, x.z * f0, x.w * f0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float f = ex2_approx(ml[e].x - mu);
+            l = fmaf(ml[e].y, f, l);
+            x.x = fmaf(v[e].x, f, x.x);
+            x.y = fmaf(v[e].y, f, x.y);
+            x.z = fmaf(v[e].z, f, x.z);
+            x.w = fmaf(v[e].w, f, x.w);
+        }
+        m = mx;
     }
-    if (blockIdx.y == 0 && threadIdx.x == 0) a.f.lse[row] = l == 0.f ? -INFINITY : (mx + lg2_approx(l)) * kLn2;
+    accs[threadIdx.x] = x;
+    if (lane == 0) mls[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp != 0) return;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, mls[w].x);
+    const float mu = mx == -INFINITY ? 0.f : mx;
+    x = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+        const float f = ex2_approx(mls[w].x - mu);
+        const float4 v = accs[w * 32 + lane];
+        l = fmaf(mls[w].y, f, l);
+        x.x = fmaf(v.x, f, x.x);
+        x.y = fmaf(v.y, f, x.y);
+        x.z = fmaf(v.z, f, x.z);
+        x.w = fmaf(v.w, f, x.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (in)
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
+    if (blockIdx.y == 0 && lane == 0) a.f.lse[row] = l == 0.f ? -INFINITY : (mx + lg2_approx(l)) * kLn2;
 }
 
 struct Plan {
@@ -1065,7 +1054,6 @@ cudaError_t launch_decode_kv4(const Kv4Decode& a, void* workspace, cudaStream_t 
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(pb.B) * pb.Hq * pb.Nq), (pb.D + 127) / 128);
     cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = 2 * (p.ctas + 1) * sizeof(float);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
