@@ -21,6 +21,7 @@ contiguous.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -531,13 +532,13 @@ def _out_view(x):
     return _view(x) if w is None else w  # _view() says what is wrong
 
 
-def _on(device, call, *args) -> int:
-    """call(*args, stream) on `device` and its current stream."""
-    i = device.index
-    if i == torch.cuda.current_device():
-        return call(*args, torch._C._cuda_getCurrentRawStream(i))
-    with torch.cuda.device(device):
-        return call(*args, torch._C._cuda_getCurrentRawStream(i))
+def _elsewhere(device) -> bool:
+    """True when `device` is not the current one, and a call has to enter it."""
+    return device.index != torch.cuda.current_device()
+
+
+def _raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def kv4_write(cache, block_table, k, v, start=None, count=None) -> None:
@@ -549,10 +550,14 @@ def kv4_write(cache, block_table, k, v, start=None, count=None) -> None:
     B = k.shape[0]
     c, Hkv, D, dev = _kv4(cache, block_table, B)
     N = _kv4_pair(k, v, 4, Hkv, D, dev)[2]
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kv4_write(cache, block_table, k, v, start, count)
     (k, wk), (v, wv) = _in_view(k), _in_view(v)
-    st = _on(dev, _ffi.load().ffpa_kv4_write, _dt(k), wk, wv, c, _lengths(start, B, "start", dev),
-             _lengths(count, B, "count", dev), B, Hkv, N, D)
-    _ffi.raise_for(st, "ffpa_kv4_write")
+    st = _ffi.load().ffpa_kv4_write(_dt(k), wk, wv, c, _lengths(start, B, "start", dev),
+                                    _lengths(count, B, "count", dev), B, Hkv, N, D, _raw_stream(dev))
+    if st:
+        _ffi.raise_for(st, "ffpa_kv4_write")
 
 
 def varlen_kv4_write(cache, block_table, k, v, cu_seqlens, max_seqlen: int, start=None) -> None:
@@ -561,11 +566,16 @@ def varlen_kv4_write(cache, block_table, k, v, cu_seqlens, max_seqlen: int, star
     B = cu_seqlens.numel() - 1
     c, Hkv, D, dev = _kv4(cache, block_table, B)
     T = _kv4_pair(k, v, 3, Hkv, D, dev)[0]
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return varlen_kv4_write(cache, block_table, k, v, cu_seqlens, max_seqlen, start)
     k, v = k.contiguous(), v.contiguous()
-    st = _on(dev, _ffi.load().ffpa_varlen_kv4_write, _dt(k), k.data_ptr(), v.data_ptr(), c,
-             _lengths(cu_seqlens, B + 1, "cu_seqlens", dev), _lengths(start, B, "start", dev), B, T, int(max_seqlen),
-             Hkv, D)
-    _ffi.raise_for(st, "ffpa_varlen_kv4_write")
+    st = _ffi.load().ffpa_varlen_kv4_write(_dt(k), k.data_ptr(), v.data_ptr(), c,
+                                           _lengths(cu_seqlens, B + 1, "cu_seqlens", dev),
+                                           _lengths(start, B, "start", dev), B, T, int(max_seqlen), Hkv, D,
+                                           _raw_stream(dev))
+    if st:
+        _ffi.raise_for(st, "ffpa_varlen_kv4_write")
 
 
 def kv4_read(cache, block_table, count, max_count: int | None = None, dtype=torch.bfloat16, start=None, k_out=None,
@@ -586,9 +596,14 @@ def kv4_read(cache, block_table, count, max_count: int | None = None, dtype=torc
     shape = _kv4_pair(k_out, v_out, 4, Hkv, D, dev)
     if shape[0] != B:
         raise ValueError(f"k_out has {shape[0]} sequences, block_table {B}")
-    st = _on(dev, _ffi.load().ffpa_kv4_read, _dt(k_out), c, _out_view(k_out), _out_view(v_out),
-             _lengths(start, B, "start", dev), _lengths(count, B, "count", dev), B, Hkv, shape[2], D)
-    _ffi.raise_for(st, "ffpa_kv4_read")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kv4_read(cache, block_table, count, start=start, k_out=k_out, v_out=v_out)
+    st = _ffi.load().ffpa_kv4_read(_dt(k_out), c, _out_view(k_out), _out_view(v_out),
+                                   _lengths(start, B, "start", dev), _lengths(count, B, "count", dev), B, Hkv,
+                                   shape[2], D, _raw_stream(dev))
+    if st:
+        _ffi.raise_for(st, "ffpa_kv4_read")
     return k_out, v_out
 
 
@@ -606,23 +621,30 @@ def varlen_kv4_read(cache, block_table, cu_seqlens, max_seqlen: int, total: int 
     T = _kv4_pair(k_out, v_out, 3, Hkv, D, dev)[0]
     if not k_out.is_contiguous() or not v_out.is_contiguous():
         raise ValueError("k_out and v_out must be contiguous")
-    st = _on(dev, _ffi.load().ffpa_varlen_kv4_read, _dt(k_out), c, k_out.data_ptr(), v_out.data_ptr(),
-             _lengths(cu_seqlens, B + 1, "cu_seqlens", dev), _lengths(start, B, "start", dev), B, T, int(max_seqlen),
-             Hkv, D)
-    _ffi.raise_for(st, "ffpa_varlen_kv4_read")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return varlen_kv4_read(cache, block_table, cu_seqlens, max_seqlen, start=start, k_out=k_out, v_out=v_out)
+    st = _ffi.load().ffpa_varlen_kv4_read(_dt(k_out), c, k_out.data_ptr(), v_out.data_ptr(),
+                                          _lengths(cu_seqlens, B + 1, "cu_seqlens", dev),
+                                          _lengths(start, B, "start", dev), B, T, int(max_seqlen), Hkv, D,
+                                          _raw_stream(dev))
+    if st:
+        _ffi.raise_for(st, "ffpa_varlen_kv4_read")
     return k_out, v_out
+
+
+@functools.lru_cache(maxsize=256)
+def _kv4_workspace_bytes(device: int, dt: int, B: int, Hq: int, Hkv: int, Nq: int, D: int) -> int:
+    """ffpa_decode_kv4_workspace_bytes, which depends on its arguments and the device's SMs alone."""
+    with torch.cuda.device(device):
+        return max(256, int(_ffi.load().ffpa_decode_kv4_workspace_bytes(dt, B, Hq, Hkv, Nq, D)))
 
 
 def decode_kv4_workspace(q, cache) -> torch.Tensor:
     """Device scratch for decode_fwd_kv4 (uint8, 256-byte aligned by the allocator)."""
     B, Hq, Nq, D = q.shape
-    with torch.cuda.device(q.device):
-        return _kv4_scratch(_dt(q), B, Hq, cache.shape[2], Nq, D, q.device)
-
-
-def _kv4_scratch(dt, B, Hq, Hkv, Nq, D, device):
-    n = _ffi.load().ffpa_decode_kv4_workspace_bytes(dt, B, Hq, Hkv, Nq, D)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    n = _kv4_workspace_bytes(q.device.index, _dt(q), B, Hq, cache.shape[2], Nq, D)
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
 def decode_fwd_kv4(q, cache, block_table, seq_lens, causal: bool = False, scale: float | None = None, out=None,
@@ -643,6 +665,9 @@ def decode_fwd_kv4(q, cache, block_table, seq_lens, causal: bool = False, scale:
         raise ValueError("q and the cache are on different devices")
     if seq_lens is None:
         raise ValueError("seq_lens is required")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return decode_fwd_kv4(q, cache, block_table, seq_lens, causal, scale, out, lse, workspace)
     q, wq = _in_view(q)
     dt = _dt(q)
     if out is None:
@@ -659,13 +684,16 @@ def decode_fwd_kv4(q, cache, block_table, seq_lens, causal: bool = False, scale:
         lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
     elif not lse.is_contiguous() or lse.dtype != torch.float32 or lse.shape != shape[:3] or lse.device != dev:
         raise ValueError("lse must be a contiguous fp32 [B, Hq, Nq] tensor")
-    args = (B, Hq, Hkv, Nq, D)
     if workspace is None:
-        workspace = _on(dev, lambda _: _kv4_scratch(dt, *args, dev))  # sized for the SMs of its device
-    st = _on(dev, _ffi.load().ffpa_decode_fwd_kv4, dt, wq, c, _lengths(seq_lens, B, "seq_lens", dev), wo,
-             lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), *args,
-             int(bool(causal)), _scale(scale, D))
-    _ffi.raise_for(st, "ffpa_decode_fwd_kv4")
+        n = _kv4_workspace_bytes(dev.index, dt, B, Hq, Hkv, Nq, D)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    else:
+        n = workspace.numel() * workspace.element_size()
+    st = _ffi.load().ffpa_decode_fwd_kv4(dt, wq, c, _lengths(seq_lens, B, "seq_lens", dev), wo, lse.data_ptr(),
+                                         workspace.data_ptr(), n, B, Hq, Hkv, Nq, D, int(bool(causal)),
+                                         _scale(scale, D), _raw_stream(dev))
+    if st:
+        _ffi.raise_for(st, "ffpa_decode_fwd_kv4")
     return out, lse
 
 

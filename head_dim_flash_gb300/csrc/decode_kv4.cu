@@ -36,6 +36,8 @@
 //     others go to the workspace, those that the groups of a CTA end with joined
 //     there first, and a second kernel joins the parts in a fixed order. It is
 //     launched as a dependent, so its start overlaps the first kernel.
+#include <atomic>
+
 #include "kv4.cuh"
 
 namespace ffpa {
@@ -1025,8 +1027,17 @@ cudaError_t launch_shape(const Kv4Decode& a, const Plan& p, cudaStream_t s)
 {
     constexpr Shape shape = shape_of(N, NB);
     auto* kernel = decode_kv4_kernel<N, NB>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shape.smem);
+    // the attribute outlasts a call: once per device (those past 64 set it every time)
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shape.smem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
     kernel<<<p.ctas, shape.NG * shape.C * 32, shape.smem, s>>>(a, p.gm);
     return cudaGetLastError();
 }
