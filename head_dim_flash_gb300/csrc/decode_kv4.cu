@@ -79,9 +79,9 @@ __host__ __device__ constexpr Shape shape_of(int N, int NB)
 {
     Shape p{};
     const int room = kMaxSmem - kStaticBytes;
-    p.CH = N > 1 ? 2 : 1;
+    p.CH = N == 1 || N == 3 || (NB == 2 && N <= 4) ? 1 : 2;
     p.C = (N + p.CH - 1) / p.CH;
-    p.NG = (NB == 1 ? 16 : 12) / p.C;
+    p.NG = (p.CH * NB <= 2 ? 16 : 12) / p.C;
     for (p.SW = p.C == 1 ? 4 : 2;; p.SW >>= 1) {
         const int strips = p.C * p.SW;
         p.group_bytes = 2 * strips * N * kKv4Tile + N * NB * 1024 + strips * NB * 256;
@@ -158,6 +158,11 @@ __device__ __forceinline__ int strips_of(int len) { return (len >> 4) + ((len & 
 // places of one unit on the line
 __device__ __forceinline__ int cost_of(int len) { return len > 0 ? strips_of(len) + kUnitCost : 0; }
 
+__device__ __forceinline__ long long div_up(long long x, int d)
+{
+    return x < 0x7fffffff ? (static_cast<unsigned>(x) + d - 1) / static_cast<unsigned>(d) : (x + d - 1) / d;
+}
+
 // A run of strips [s0, s1) of one unit within a group's range [.., end) of the line; `unit` is the line place where
 // the unit begins, its first strip lies kUnitCost behind.
 struct Piece {
@@ -182,7 +187,7 @@ __device__ __forceinline__ bool first_piece(const Kv4Decode& a, const Kv4Geo& gm
     p.b = b;
     p.len = cached_len(a, b);
     p.end = end;
-    const int cost = cost_of(p.len), u = static_cast<int>((at - b_at) / cost);
+    const int cost = cost_of(p.len), u = static_cast<int>(div_up(at - b_at + 1, cost)) - 1;
     p.unit = b_at + static_cast<long long>(u) * cost;
     p.hk = u / gm.rblocks;
     p.rb = u - p.hk * gm.rblocks;
@@ -212,21 +217,20 @@ __device__ __forceinline__ bool next_piece(const Kv4Decode& a, const Kv4Geo& gm,
 }
 
 // What the thread that loads a group's K (or V) keeps: its piece, and the first strip of the next step with its place
-// in the block table and the page (fetched a step early).
+// in the block table (its page is in a register, fetched a step early).
 struct Loader {
     Piece piece;
     const uint8_t* head;  // the head's tiles in page 0
     const int* row;
-    int s, in, page;
+    int s, in;
     int loads;            // steps loaded
     bool more;
 };
 
 struct __align__(16) DecShared {
     uint64_t full[kMaxWarps][2];      // per group: K and V of a step are there
-    long long sums[kMaxWarps];
-    long long first_at[kMaxWarps];    // place where the units of each group's first sequence begin
-    int first_b[kMaxWarps];
+    Piece first[kMaxWarps];           // per group: what its range begins with
+    bool any[kMaxWarps];              // and whether it holds strips
     Loader load[kMaxWarps][2];
     int abort_flag;
     int up[kMaxWarps][2];             // per group and step parity: the last step in which a score passed the reference
@@ -299,62 +303,19 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
     const Problem& pb = a.f.pb;
     const bool bf16 = a.f.bf16 != 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    constexpr int warps = NG * C, kThreads = 32 * warps;
     const int G = pb.Hq / pb.Hkv, R = G * pb.Nq;
     const int units_b = pb.Hkv * gm.rblocks;          // units per sequence
     __shared__ DecShared sh;
     extern __shared__ __align__(128) uint8_t smem[];
 
-    // ---- the line's length and the sequence in which each of my groups begins
-    long long chunk, total;
-    {
-        const int per = (pb.B + kThreads - 1) / kThreads;
-        const int b0 = min(static_cast<int>(threadIdx.x) * per, pb.B), b1 = min(b0 + per, pb.B);
-        long long sum = 0;
-#pragma unroll 1
-        for (int b = b0; b < b1; ++b) sum += cost_of(cached_len(a, b));
-        long long incl = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += x;
-        }
-        if (lane == 31) sh.sums[warp] = incl;
-        if (threadIdx.x < kMaxWarps * 2) {
-            mbar_init(&sh.full[0][0] + threadIdx.x, 1);
-            (&sh.up[0][0])[threadIdx.x] = 0;
-            fence_barrier_init();
-        }
-        if (threadIdx.x < kMaxWarps) sh.last[threadIdx.x][0] = -1;
-        if (threadIdx.x == 0) sh.abort_flag = 0;
-        __syncthreads();
-        total = 0;
-#pragma unroll 1
-        for (int w = 0; w < warps; ++w) {
-            if (w < warp) incl += sh.sums[w];
-            total += sh.sums[w];
-        }
-        total *= units_b;
-        chunk = (total + gm.workers - 1) / gm.workers;
-        const long long lo = (incl - sum) * units_b, hi = incl * units_b;
-#pragma unroll 1
-        for (int i = 0; i < NG; ++i) {
-            const long long at = (static_cast<long long>(blockIdx.x) * NG + i) * chunk;
-            if (at < lo || at >= hi || at >= total) continue;
-            long long b_at = lo;
-            for (int b = b0; b < b1; ++b) {
-                const long long n = static_cast<long long>(cost_of(cached_len(a, b))) * units_b;
-                if (at < b_at + n) {
-                    sh.first_b[i] = b;
-                    sh.first_at[i] = b_at;
-                    break;
-                }
-                b_at += n;
-            }
-        }
-        __syncthreads();
+    if (threadIdx.x < kMaxWarps * 2) {
+        mbar_init(&sh.full[0][0] + threadIdx.x, 1);
+        (&sh.up[0][0])[threadIdx.x] = 0;
+        fence_barrier_init();
     }
-    if (static_cast<long long>(blockIdx.x) * NG * chunk >= total) return;
+    if (threadIdx.x < kMaxWarps) sh.last[threadIdx.x][0] = -1;
+    if (threadIdx.x == 0) sh.abort_flag = 0;
+    __syncthreads();
 
     const int group = warp / C, wg = warp - group * C;  // my group, my place in it
     // my chunks are chunk0 .. chunk0 + CH - 1; those before wg * CH are another warp's too and are not stored
@@ -373,12 +334,45 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
         else
             asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(C * 32) : "memory");
     };
-    Piece cur{};
-    bool more;
-    {
+    // ---- my group's range of the line: its first warp adds the line up, a lane a run of sequences
+    if (wg == 0) {
+        const int per = (pb.B + 31) >> 5, b0 = min(lane * per, pb.B), b1 = min(b0 + per, pb.B);
+        long long sum = 0;
+#pragma unroll 4
+        for (int b = b0; b < b1; ++b) sum += cost_of(cached_len(a, b));
+        long long incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += x;
+        }
+        const long long total = __shfl_sync(0xffffffffu, incl, 31) * units_b, chunk = div_up(total, gm.workers);
+        const long long lo = (incl - sum) * units_b, hi = incl * units_b;
         const long long at = (static_cast<long long>(blockIdx.x) * NG + group) * chunk;
-        more = first_piece(a, gm, cur, at, min(at + chunk, total), sh.first_b[group], sh.first_at[group]);
+        const unsigned in = __ballot_sync(0xffffffffu, at >= lo && at < hi);
+        Piece p{};
+        bool any = false;
+        if (in != 0) {
+            const int src = __ffs(in) - 1;
+            long long b_at = __shfl_sync(0xffffffffu, lo, src);
+            int b = src * per;
+            for (;;) {  // one of that lane's sequences
+                const long long n = static_cast<long long>(cost_of(cached_len(a, b))) * units_b;
+                if (at < b_at + n) break;
+                b_at += n;
+                ++b;
+            }
+            any = first_piece(a, gm, p, at, min(at + chunk, total), b, b_at);
+        }
+        if (lane == 0) {
+            sh.first[group] = p;
+            sh.any[group] = any;
+        }
+        __syncwarp();
     }
+    group_sync();
+    Piece cur = sh.first[group];
+    bool more = sh.any[group];
 
     // Q of the piece's rows over every C-th chunk: a lane holds query g (of block k), head dims 16 t .. 16 t + 15 of a
     // chunk; null where there is no such row or chunk
@@ -410,19 +404,20 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
         kv4_invalid(a.f.ctl.status, VS_KV4_DECODE, b);
         return 0;
     };
+    int page_ahead[2] = {0, 0};  // of the next step: on its way, not waited for
     auto begin_piece = [&](Loader& ld, int kv) {
         ld.s = ld.piece.s0;
         const int blk = ld.s / spp;
         ld.in = ld.s - blk * spp;
         ld.row = a.cache.table + ld.piece.b * a.cache.table_stride + blk;
         ld.head = a.cache.data + static_cast<size_t>(ld.piece.hk) * spp * strip_bytes + (kv ? v_off : 0);
-        ld.page = valid_page(*ld.row, ld.piece.b);
+        page_ahead[kv] = *ld.row;
     };
     auto load = [&](int kv) {
         Loader& ld = sh.load[group][kv];
         if (!ld.more) return;
         const int s1 = ld.piece.s1;
-        int s = ld.s, in = ld.in, page = ld.page;
+        int s = ld.s, in = ld.in, page = valid_page(page_ahead[kv], ld.piece.b);
         const int* row = ld.row;
         const uint8_t* head = ld.head;
         const int end = min(s + steps, s1);
@@ -437,16 +432,16 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
             if (in == spp) {
                 in = 0;
                 ++row;
-                if (s < s1) page = valid_page(*row, ld.piece.b);
             }
             if (s >= end) break;
+            page = valid_page(*row, ld.piece.b);
         }
         ++ld.loads;
         if (s < s1) {
             ld.s = s;
             ld.in = in;
             ld.row = row;
-            ld.page = page;
+            page_ahead[kv] = *row;
         } else {
             ld.more = next_piece(a, gm, ld.piece);
             if (ld.more) begin_piece(ld, kv);
@@ -932,7 +927,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_kernel(const Kv4
     }
     // the unit's strips lie at [first, end) of the line; groups v0 .. v1 hold them
     const long long first = before * units_b + static_cast<long long>((h / G) * gm.rblocks + r / gm.rows) * cost_of(len) + kUnitCost;
-    const long long end = first + n, chunk = (total + gm.workers - 1) / gm.workers;
+    const long long end = first + n, chunk = div_up(total, gm.workers);
     const int v0 = static_cast<int>(first / chunk), v1 = static_cast<int>((end - 1) / chunk);
     pdl_wait();
     if (v0 == v1) return;  // written by its group
