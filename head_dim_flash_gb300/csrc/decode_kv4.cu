@@ -299,7 +299,6 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
     constexpr int steps = C * SW;                     // strips per step
     constexpr int strip_bytes = N * kKv4Tile;
     static_assert(sizeof(DecShared) + 1024 <= kStaticBytes, "static shared memory");
-    pdl_trigger();
     const Problem& pb = a.f.pb;
     const bool bf16 = a.f.bf16 != 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -316,6 +315,8 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
     if (threadIdx.x < kMaxWarps) sh.last[threadIdx.x][0] = -1;
     if (threadIdx.x == 0) sh.abort_flag = 0;
     __syncthreads();
+    pdl_wait();     // what the call reads and writes may belong to the kernel before it until here
+    pdl_trigger();
 
     const int group = warp / C, wg = warp - group * C;  // my group, my place in it
     // my chunks are chunk0 .. chunk0 + CH - 1; those before wg * CH are another warp's too and are not stored
@@ -502,12 +503,13 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
                     uint32_t x[4][4];
                     k_tile(tile + i * strip_bytes, lane, x);
 #pragma unroll
-                    for (int k = 0; k < NB; ++k) {
-                        mma_f16_16816(to[i][k], x[0][0], x[0][1], x[0][2], x[0][3], q0[k].x, q0[k].y);
-                        mma_f16_16816(to[i][k], x[1][0], x[1][1], x[1][2], x[1][3], q0[k].z, q0[k].w);
-                        mma_f16_16816(to[i][k], x[2][0], x[2][1], x[2][2], x[2][3], q1[k].x, q1[k].y);
-                        mma_f16_16816(to[i][k], x[3][0], x[3][1], x[3][2], x[3][3], q1[k].z, q1[k].w);
-                    }
+                    for (int k = 0; k < NB; ++k) mma_f16_16816(to[i][k], x[0][0], x[0][1], x[0][2], x[0][3], q0[k].x, q0[k].y);
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) mma_f16_16816(to[i][k], x[1][0], x[1][1], x[1][2], x[1][3], q0[k].z, q0[k].w);
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) mma_f16_16816(to[i][k], x[2][0], x[2][1], x[2][2], x[2][3], q1[k].x, q1[k].y);
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) mma_f16_16816(to[i][k], x[3][0], x[3][1], x[3][2], x[3][3], q1[k].z, q1[k].w);
                 }
                 tile += kKv4Tile;
                 q += NB * 64;
@@ -885,6 +887,7 @@ constexpr int kJoinThreads = 128;
 template <bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_kernel(const Kv4Decode a, const Kv4Geo gm)
 {
+    pdl_trigger();
     const Problem& pb = a.f.pb;
     __shared__ long long sums[2][kJoinThreads / 32];
     __shared__ float4 accs[kJoinThreads];
@@ -1017,6 +1020,23 @@ Plan plan(const Problem& pb)
     return p;
 }
 
+// Both kernels start before the one before them in the stream has ended, and wait for its end before they touch memory.
+cudaError_t launch_dependent(void (*kernel)(Kv4Decode, Kv4Geo), dim3 grid, int threads, int smem, cudaStream_t s,
+                             const Kv4Decode& a, const Kv4Geo& gm)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, gm);
+}
+
 template <int N, int NB>
 cudaError_t launch_shape(const Kv4Decode& a, const Plan& p, cudaStream_t s)
 {
@@ -1033,8 +1053,7 @@ cudaError_t launch_shape(const Kv4Decode& a, const Plan& p, cudaStream_t s)
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    kernel<<<p.ctas, shape.NG * shape.C * 32, shape.smem, s>>>(a, p.gm);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3(p.ctas), shape.NG * shape.C * 32, shape.smem, s, a, p.gm);
 }
 
 template <int N>
@@ -1057,16 +1076,9 @@ cudaError_t launch_decode_kv4(const Kv4Decode& a, void* workspace, cudaStream_t 
     const cudaError_t ran = launch_chunks<16>(a, p, s);
     if (ran != cudaSuccess) return ran;
     const Problem& pb = a.f.pb;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(pb.B) * pb.Hq * pb.Nq), (pb.D + 127) / 128);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, a.f.bf16 ? decode_kv4_join_kernel<true> : decode_kv4_join_kernel<false>, a, p.gm);
+    const dim3 grid(static_cast<unsigned>(static_cast<long long>(pb.B) * pb.Hq * pb.Nq), (pb.D + 127) / 128);
+    return launch_dependent(a.f.bf16 ? decode_kv4_join_kernel<true> : decode_kv4_join_kernel<false>, grid, kJoinThreads, 0, s,
+                            a, p.gm);
 }
 
 }  // namespace ffpa
