@@ -56,6 +56,10 @@ struct Kv4Geo {
     int rows;        // 8 or 16
     int NG;          // groups per CTA
     int workers;     // groups of the whole grid
+    int spp;         // strips per page
+    int step_blk;    // a step moves by so many pages
+    int step_in;     // and strips
+    size_t v_off;    // bytes from a page's K to its V
     float* part;     // [workers][2][rows][D] unnormalised partial O
     float* ml;       // [workers][2][rows][2] reference (log2) and sum
 };
@@ -82,7 +86,7 @@ __host__ __device__ constexpr Shape shape_of(int N, int NB)
     p.CH = N == 1 || N == 3 || (NB == 2 && N <= 4) ? 1 : 2;
     p.C = (N + p.CH - 1) / p.CH;
     p.NG = (p.CH * NB <= 2 ? 16 : 12) / p.C;
-    for (p.SW = p.C == 1 ? 4 : 2;; p.SW >>= 1) {
+    for (p.SW = p.C > 1 ? 2 : 8;; p.SW >>= 1) {
         const int strips = p.C * p.SW;
         p.group_bytes = 2 * strips * N * kKv4Tile + N * NB * 1024 + strips * NB * 256;
         if (p.NG * p.group_bytes <= room) break;
@@ -216,8 +220,8 @@ __device__ __forceinline__ bool next_piece(const Kv4Decode& a, const Kv4Geo& gm,
     return p.s1 > 0;
 }
 
-// What the thread that loads a group's K (or V) keeps: its piece, and the first strip of the next step with its place
-// in the block table (its page is in a register, fetched a step early).
+// What the warp that loads a group's K (or V) keeps: its piece, and the first strip of the next step with its place in
+// the block table (the pages of the step are in the lanes' registers, fetched a step early).
 struct Loader {
     Piece piece;
     const uint8_t* head;  // the head's tiles in page 0
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
     uint64_t* const full = sh.full[group];
 
     auto group_sync = [&]() {
-        if (SW == 4)  // groups of one warp
+        if (C == 1)
             __syncwarp();
         else
             asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(C * 32) : "memory");
@@ -394,72 +398,80 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
             }
     }
 
-    // ---- loads: K by the group's first warp, V by its second (lane 0). The place of a step in the block table moves
-    // without a division, and its first page is fetched a step early.
-    const int spp = a.cache.page_size >> 4;  // strips per page
-    const size_t v_off = static_cast<size_t>(pb.Hkv) * spp * strip_bytes, page_bytes = 2 * v_off;
-    const int v_warp = C > 1 ? 1 : 0;
-    auto valid_page = [&](int page, int b) {
-        if (static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.num_pages)) return page;
-        // the sequence's rows are undefined, but the copies stay inside the cache
-        kv4_invalid(a.f.ctl.status, VS_KV4_DECODE, b);
-        return 0;
+    // ---- loads: K by the group's first warp, V by its second. Lane j copies the run of the step's strips that lies in
+    // the j-th page, and has fetched that page's number a step early.
+    constexpr int v_warp = C > 1 ? 1 : 0, kPlaces = C > 1 ? 1 : 2;  // a group of one warp loads both
+    static_assert(steps <= 31, "a lane per page of a step");
+    int page[kPlaces];
+    // the step's strip that my page begins with, in a step that begins `in` strips into a page (below 2^32)
+    auto my_run = [&](int in) { return lane ? lane * static_cast<unsigned>(gm.spp) - in : 0u; };
+    auto fetch_pages = [&](const int* row, int in, unsigned n, int kv) {
+        if (my_run(in) < n) page[kv < kPlaces ? kv : 0] = row[lane];
     };
-    int page_ahead[2] = {0, 0};  // of the next step: on its way, not waited for
     auto begin_piece = [&](Loader& ld, int kv) {
-        ld.s = ld.piece.s0;
-        const int blk = ld.s / spp;
-        ld.in = ld.s - blk * spp;
-        ld.row = a.cache.table + ld.piece.b * a.cache.table_stride + blk;
-        ld.head = a.cache.data + static_cast<size_t>(ld.piece.hk) * spp * strip_bytes + (kv ? v_off : 0);
-        page_ahead[kv] = *ld.row;
+        const int s0 = ld.piece.s0, blk = s0 / gm.spp, in = s0 - blk * gm.spp;
+        const int* row = a.cache.table + ld.piece.b * a.cache.table_stride + blk;
+        fetch_pages(row, in, min(ld.piece.s1 - s0, steps), kv);
+        if (lane == 0) {
+            ld.s = s0;
+            ld.in = in;
+            ld.row = row;
+            ld.head = a.cache.data + static_cast<size_t>(ld.piece.hk) * gm.spp * strip_bytes + (kv ? gm.v_off : 0);
+        }
     };
     auto load = [&](int kv) {
         Loader& ld = sh.load[group][kv];
         if (!ld.more) return;
-        const int s1 = ld.piece.s1;
-        int s = ld.s, in = ld.in, page = valid_page(page_ahead[kv], ld.piece.b);
-        const int* row = ld.row;
-        const uint8_t* head = ld.head;
-        const int end = min(s + steps, s1);
-        uint8_t* dst = kv ? v_mem : k_mem;
-        mbar_arrive_expect_tx(&full[kv], (end - s) * strip_bytes);
-        for (;;) {  // runs of strips in a page
-            const int run = min(end - s, spp - in);
-            bulk_load(dst, head + page * page_bytes + static_cast<size_t>(in) * strip_bytes, run * strip_bytes, &full[kv]);
-            dst += run * strip_bytes;
-            s += run;
-            in += run;
-            if (in == spp) {
-                in = 0;
-                ++row;
+        const int s = ld.s, s1 = ld.piece.s1, in = ld.in, n = min(s1 - s, steps);
+        const unsigned at = my_run(in);
+        if (lane == 0) mbar_arrive_expect_tx(&full[kv], n * strip_bytes);
+        __syncwarp();
+        if (at < static_cast<unsigned>(n)) {
+            int pg = page[kv < kPlaces ? kv : 0];
+            if (static_cast<unsigned>(pg) >= static_cast<unsigned>(a.cache.num_pages)) {
+                // the sequence's rows are undefined, but the copies stay inside the cache
+                kv4_invalid(a.f.ctl.status, VS_KV4_DECODE, ld.piece.b);
+                pg = 0;
             }
-            if (s >= end) break;
-            page = valid_page(*row, ld.piece.b);
+            const int skip = lane ? 0 : in;
+            bulk_load((kv ? v_mem : k_mem) + at * strip_bytes, ld.head + pg * (2 * gm.v_off) + static_cast<size_t>(skip) * strip_bytes,
+                      min(n - static_cast<int>(at), gm.spp - skip) * strip_bytes, &full[kv]);
         }
-        ++ld.loads;
-        if (s < s1) {
-            ld.s = s;
-            ld.in = in;
-            ld.row = row;
-            page_ahead[kv] = *row;
+        if (s + steps < s1) {
+            const int wrap = in + gm.step_in >= gm.spp, next = in + gm.step_in - (wrap ? gm.spp : 0);
+            const int* row = ld.row + gm.step_blk + wrap;
+            fetch_pages(row, next, min(s1 - s - steps, steps), kv);
+            __syncwarp();
+            if (lane == 0) {
+                ld.s = s + steps;
+                ld.in = next;
+                ld.row = row;
+                ++ld.loads;
+            }
         } else {
-            ld.more = next_piece(a, gm, ld.piece);
+            __syncwarp();
+            if (lane == 0) {
+                ++ld.loads;
+                ld.more = next_piece(a, gm, ld.piece);
+            }
+            __syncwarp();
             if (ld.more) begin_piece(ld, kv);
         }
     };
-    if (lane == 0)
-        for (int kv = 0; kv < 2; ++kv)
-            if (wg == (kv ? v_warp : 0)) {
-                Loader& ld = sh.load[group][kv];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+        if (wg == (kv ? v_warp : 0)) {
+            Loader& ld = sh.load[group][kv];
+            if (lane == 0) {
                 ld.piece = cur;
                 ld.more = more;
                 ld.loads = 0;
-                if (more) {
-                    begin_piece(ld, kv);
-                    load(kv);
-                }
             }
+            __syncwarp();
+            if (more) begin_piece(ld, kv);
+            __syncwarp();
+            if (more) load(kv);
+        }
     __syncwarp();
     // Waits for a copy. After one that ran out of time no more are issued, the group's barriers go on.
     auto arrived = [&](int kv, uint32_t phase) {
@@ -619,7 +631,7 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
             if (bf16) {
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                if (SW < 4) {
+                if (C > 1) {
                     if (t == 0) sh.col[warp][k * 8 + g] = __uint_as_float(amax);
                     group_sync();
                     for (int w = 0; w < C; ++w) amax = max(amax, __float_as_uint(sh.col[group * C + w][k * 8 + g]));
@@ -700,7 +712,7 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
                 store_p();
             }
             group_sync();  // P is there, K is read
-            if (lane == 0 && wg == 0) load(0);
+            if (wg == 0) load(0);
             if (first || *reinterpret_cast<volatile int*>(&sh.up[group][step & 1]) == step) {
                 // the reference moves, for all warps of the group alike
 #pragma unroll
@@ -751,7 +763,7 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
                 for (int q = 0; q < 2; ++q) l[k][q] += dl[k][q];
             values(min(steps, cur.s1 - at), at * 16);
             group_sync();  // V and P are read
-            if (lane == 0 && wg == v_warp) load(1);
+            if (wg == v_warp) load(1);
         }
 
         // ---- the group's sums
@@ -1071,6 +1083,11 @@ size_t kv4_decode_workspace_bytes(const Problem& pb) { return plan(pb).bytes; }
 cudaError_t launch_decode_kv4(const Kv4Decode& a, void* workspace, cudaStream_t s)
 {
     Plan p = plan(a.f.pb);
+    const Shape shape = shape_of(a.f.pb.D >> 6, p.nb);
+    p.gm.spp = a.cache.page_size >> 4;
+    p.gm.step_blk = shape.C * shape.SW / p.gm.spp;
+    p.gm.step_in = shape.C * shape.SW % p.gm.spp;
+    p.gm.v_off = static_cast<size_t>(a.f.pb.Hkv) * p.gm.spp * (a.f.pb.D >> 6) * kKv4Tile;
     p.gm.part = static_cast<float*>(workspace);
     p.gm.ml = p.gm.part + p.part_floats;
     const cudaError_t ran = launch_chunks<16>(a, p, s);
