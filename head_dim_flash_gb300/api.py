@@ -687,6 +687,8 @@ def decode_fwd_kv4(q, cache, block_table, seq_lens, causal: bool = False, scale:
     if workspace is None:
         n = _kv4_workspace_bytes(dev.index, dt, B, Hq, Hkv, Nq, D)
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on q's device")
     else:
         n = workspace.numel() * workspace.element_size()
     st = _ffi.load().ffpa_decode_fwd_kv4(dt, wq, c, _lengths(seq_lens, B, "seq_lens", dev), wo, lse.data_ptr(),

@@ -642,7 +642,7 @@ ffpa_status check_kv4_cache(const ffpa_kv4_cache& c, bool used, int Hkv, int D, 
     out->num_pages = c.num_pages;
     out->page_size = c.page_size;
     out->table = c.block_table;
-    out->max_blocks = c.max_blocks;
+    out->max_blocks = c.num_pages > 0 ? c.max_blocks : 0;  // a cache without pages holds no tokens
     out->table_stride = c.block_stride;
     return FFPA_OK;
 }

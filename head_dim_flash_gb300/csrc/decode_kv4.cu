@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
                 for (int i = 0; i < SW; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[i][k][e] = fmaf(s[i][k][e], c2[k][e & 1], -m[k][e & 1]);
-            if ((mine + SW) * 16 > least || n < SW) {
+            if (mine + SW > least >> 4 || n < SW) {  // in strips: tokens may reach 2^31
 #pragma unroll
                 for (int k = 0; k < NB; ++k)
 #pragma unroll

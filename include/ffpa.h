@@ -283,7 +283,7 @@ FFPA_API ffpa_status ffpa_varlen_kv4_read(ffpa_dtype dt, ffpa_kv4_cache cache, v
  * (device int32 [B]). Causal is bottom-right per sequence: query row i sees
  * cached token j iff j <= i + seq_lens[b] - Nq. A sequence of length 0, and any
  * row with no legal key, gives O = 0 and LSE = -inf.
- *   q, o: [B, Hq, Nq, D] views; lse: contiguous fp32 [B, Hq, Nq].
+ *   q, o: [B, Hq, Nq, D] views (o may be q's own); lse: contiguous fp32 [B, Hq, Nq].
  *   workspace: device scratch of at least ffpa_decode_kv4_workspace_bytes()
  *   bytes, 256-byte aligned, sized on the current device; one call at a time
  *   per workspace.

@@ -274,6 +274,51 @@ def test_decode_pages_and_ragged_lengths(page):
     decode_case([1, 0, 700, 16, 0, 4095, 333], 1, 4, 1, 256, page, False, FP16, seed=page, width=3)
 
 
+@pytest.mark.parametrize("D", [64, 128, 320, 512, 896, 1024])
+@pytest.mark.parametrize("page", [16, 48, 112, 2048])
+def test_decode_steps_over_pages(D, page):
+    # steps that begin and end anywhere in a page, and span many; short and long groups, eight and sixteen rows
+    lens = [1500, 17, 0, 790]
+    decode_case(lens, 2, 2, 1, D, page, False, BF16, seed=D + page)
+    decode_case(lens, 1, 5, 3, D, page, True, FP16, seed=2 * D + page)
+
+
+def test_decode_up_to_the_last_token_an_int_can_count():
+    """2^31 - 1 tokens on two pages: every block is the first, the last block the second, whose own last token
+    (position 2^31 - 1, one past the sequence) would outweigh all others.
+
+    The oracle is the softmax with every key counted as often as it occurs. 16 groups on each of more than 140 SMs
+    share 2^27 strips: below 2^16 per group, and one addition per strip to a lane's sum (2^-24 each) and to a product
+    (2^-23): at most 2^-8 of the sum and 2^-7 of A; P's rounding is 2^-11 of A, the output's 2^-9 of itself."""
+    D, page, n = 64, 1 << 20, (1 << 31) - 1
+    blocks = 1 << 11
+    cache = api.kv4_cache(2, page, 1, D)
+    q = torch.randn(1, 4, 1, D, device="cuda").to(BF16)
+    k, v = (torch.randn(1, 1, page, D, device="cuda").to(BF16) for _ in range(2))
+    both = torch.tensor([[0], [1]], dtype=torch.int32, device="cuda")
+    k2 = k.clone()
+    k2[0, 0, -1] = 40 * q.sum(1)[0, 0]
+    for p, kk in ((0, k), (1, k2)):
+        api.kv4_write(cache, both[p:p + 1], kk, v)
+    table = torch.zeros(1, blocks, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    o, lse = api.decode_fwd_kv4(q, cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    rk, rv = api.kv4_read(cache, both[:1], torch.tensor([page], dtype=torch.int32, device="cuda"), max_count=page)
+    api.get_status()
+    s = q[0, :, 0].double() @ rk[0, 0].double().T / 8
+    w = torch.full((page,), float(blocks), dtype=torch.float64, device="cuda")
+    w[-1] -= 1
+    e = (s - s.amax(1, keepdim=True)).exp() * w
+    l = e.sum(1, keepdim=True)
+    want, mean = e @ rv[0, 0].double() / l, e @ rv[0, 0].double().abs() / l
+    m = (q[0, :, 0].double().abs() @ rk[0, 0].double().abs().T).amax(1, keepdim=True) / 8
+    e_s = (D / 16 + 8) * 2.0 ** -23 * m
+    assert ((o[0, :, 0].double() - want).abs() <= 2.0 ** -9 * want.abs() + (2.0 ** -7 + 2.0 ** -8 + 2.0 ** -11 + 2 * e_s) * mean +
+            2.0 ** -17 * rv.abs().max().double()).all()
+    assert ((lse[0, :, 0:1].double() - (l.log() + s.amax(1, keepdim=True))).abs() <= 2.0 ** -8 + 2.0 ** -20 + e_s +
+            2.0 ** -19).all()
+
+
 def test_decode_long_context_on_few_heads():
     decode_case([40000], 1, 2, 1, 128, 64, False, BF16, seed=1)
     decode_case([9000], 1, 16, 2, 1024, 128, True, FP16, seed=2)
@@ -431,7 +476,73 @@ def test_another_stream():
     torch.cuda.current_stream().wait_stream(s)
 
 
+def test_calls_at_once_on_two_streams():
+    """Decodes with their own workspaces, and writes to other pages of the same cache, at the same time."""
+    rng = np.random.default_rng(30)
+    Hkv, G, D, page = 2, 4, 320, 32
+    lens = [[900, 3, 411], [64, 2000, 5]]
+    table, pages = block_tables(lens[0] + lens[1], page, rng)
+    cache = dev(random_cache(pages + 1, page, Hkv, D, rng))
+    spare = torch.full((1, 1), pages, dtype=torch.int32, device="cuda")
+    x = torch.randn(1, Hkv, page, D, device="cuda").to(BF16)
+    q = torch.randn(3, Hkv * G, 2, D, device="cuda").to(BF16)
+    tables = [dev(table[:3]), dev(table[3:])]
+    ln = [dev(np.array(n, np.int32)) for n in lens]
+    want = [api.decode_fwd_kv4(q, cache, tables[i], ln[i], True) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(api.decode_fwd_kv4(q, cache, tables[i], ln[i], True))
+                if i:
+                    api.kv4_write(cache, spare, x, x)
+    torch.cuda.synchronize()
+    api.get_status()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_results_take_the_place_of_their_inputs():
+    # the rows of a unit are read before any of them is written
+    q, cache, t, ln, o, lse = decode_case([3000, 17, 900, 0], 2, 8, 2, 256, 64, True, BF16, seed=31)
+    api.decode_fwd_kv4(q, cache, t, ln, True, out=q, lse=lse)
+    api.get_status()
+    assert torch.equal(q, o)
+
+
 # ----------------------------------------------------------------- refusals
+def test_a_cache_without_pages_holds_no_tokens():
+    cache = api.kv4_cache(0, 16, 1, 128)
+    table = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    ln = torch.tensor([3, 0], dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 4, 1, 128, device="cuda").to(BF16)
+    x = torch.randn(2, 1, 3, 128, device="cuda").to(BF16)
+    for call in (lambda: api.decode_fwd_kv4(q, cache, table, ln), lambda: api.kv4_read(cache, table, ln, max_count=3),
+                 lambda: api.kv4_write(cache, table, x, x, count=ln)):
+        out = call()
+        with pytest.raises(ValueError, match="sequence 0"):
+            api.get_status()
+        if out is not None:
+            assert (out[0][1] == 0).all()
+
+
+def test_workspace_refusals():
+    cache = api.kv4_cache(4, 16, 2, 128)
+    table = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    ln = torch.tensor([3, 3], dtype=torch.int32, device="cuda")
+    q = torch.zeros(2, 4, 1, 128, dtype=BF16, device="cuda")
+    ws = api.decode_kv4_workspace(q, cache)
+    big = torch.empty(2 * ws.numel(), dtype=torch.uint8, device="cuda")
+    for bad in (ws.cpu(), big[::2], ws[:-1], big[8:]):   # elsewhere, strided, too small, not aligned
+        with pytest.raises(ValueError, match="workspace"):
+            api.decode_fwd_kv4(q, cache, table, ln, workspace=bad)
+    api.decode_fwd_kv4(q, cache, table, ln, workspace=ws)
+    api.get_status()
+
+
 @pytest.mark.parametrize("bad", ["page", "negative page", "length", "negative length"])
 def test_a_sequence_outside_its_cache_is_an_error_and_others_are_not(bad):
     rng = np.random.default_rng(12)
