@@ -379,24 +379,36 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
     Piece cur = sh.first[group];
     bool more = sh.any[group];
 
-    // Q of the piece's rows over every C-th chunk: a lane holds query g (of block k), head dims 16 t .. 16 t + 15 of a
-    // chunk; null where there is no such row or chunk
-    auto q_part = [&](int k, int j) -> const uint4* {
-        const int r = cur.rb * kRows + k * 8 + g, c = wg + j * C;
-        const int h = cur.hk * G + r / pb.Nq, i = r % pb.Nq;
-        return r < R && c < N ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.f.q) + cur.b * pb.vq.sb +
-                                                               h * pb.vq.sh + i * pb.vq.sn + c * 64 + t * 16)
-                              : nullptr;
+    // Q of the piece's rows over every C-th chunk: a lane takes query g (of block k), head dims 16 t .. 16 t + 15 of a
+    // chunk, zeros where there is no such row, to the places of its operands
+    struct Queries {
+        uint4 x[NB][CH], y[NB][CH];
     };
-    if (more) {  // on its way while the loads are set up
+    auto fetch_q = [&](Queries& to) {
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            const int r = cur.rb * kRows + k * 8 + g, hq = r / pb.Nq, h = cur.hk * G + hq, i = r - hq * pb.Nq;
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.f.q) + cur.b * pb.vq.sb +
+                                                            h * pb.vq.sh + i * pb.vq.sn + wg * 64 + t * 16);
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const bool in = r < R && wg + j * C < N;
+                to.x[k][j] = in ? q[j * C * 8] : make_uint4(0, 0, 0, 0);
+                to.y[k][j] = in ? q[j * C * 8 + 1] : make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+    auto put_q = [&](const Queries& from) {
 #pragma unroll
         for (int k = 0; k < NB; ++k)
 #pragma unroll
-            for (int j = 0; j < CH; ++j) {
-                const uint4* q = q_part(k, j);
-                if (q) asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
-            }
-    }
+            for (int j = 0; j < CH; ++j)
+                if (wg + j * C < N) {
+                    uint4* const q = q_mem + ((wg + j * C) * NB + k) * 64;
+                    q[0] = from.x[k][j];
+                    q[32] = from.y[k][j];
+                }
+    };
 
     // ---- loads: K by the group's first warp, V by its second. Lane j copies the run of the step's strips that lies in
     // the j-th page, and has fetched that page's number a step early.
@@ -470,8 +482,15 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
             __syncwarp();
             if (more) begin_piece(ld, kv);
             __syncwarp();
-            if (more) load(kv);
         }
+    if (more) {
+        Queries q;
+        fetch_q(q);  // on its way while the loads wait for their pages
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+            if (wg == (kv ? v_warp : 0)) load(kv);
+        put_q(q);
+    }
     __syncwarp();
     // Waits for a copy. After one that ran out of time no more are issued, the group's barriers go on.
     auto arrived = [&](int kv, uint32_t phase) {
@@ -620,9 +639,9 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
             uint32_t amax = 0;  // magnitudes of 16-bit floats order as their bits do
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const uint4* q = q_part(k, j);
-                x[j] = q ? q[0] : make_uint4(0, 0, 0, 0);
-                y[j] = q ? q[1] : make_uint4(0, 0, 0, 0);
+                const bool in = wg + j * C < N;
+                x[j] = in ? q_mem[((wg + j * C) * NB + k) * 64] : make_uint4(0, 0, 0, 0);
+                y[j] = in ? q_mem[((wg + j * C) * NB + k) * 64 + 32] : make_uint4(0, 0, 0, 0);
                 const uint32_t w[8] = {x[j].x, x[j].y, x[j].z, x[j].w, y[j].x, y[j].y, y[j].z, y[j].w};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) amax = max(amax, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
@@ -822,6 +841,11 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
             } else {
                 pending = true;
             }
+        }
+        if (more) {
+            Queries q;
+            fetch_q(q);
+            put_q(q);
         }
     }
     // after a wait that ran out, copies may still be in flight: they end before the CTA does
