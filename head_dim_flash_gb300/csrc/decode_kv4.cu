@@ -15,27 +15,42 @@
 //     tokens are interleaved before the conversion, which costs half of what
 //     exchanging the converted halves would. The operands of both products are
 //     fp16 for either element type: cached values and (power-of-two scaled)
-//     queries are exact.
+//     queries are exact. (tcgen05 would want 128 rows of dequantised operands in
+//     shared or tensor memory: the same conversions, and a store of each value.)
 //   - a group of C warps works on a step of C * SW strips of 16 tokens. For the
 //     scores each warp takes SW strips over the whole head dim, so a softmax is
 //     computed once and its scores are never exchanged; for the values it takes
-//     two 64-wide head-dim chunks over all strips, so O^T stays in registers
-//     (32 for eight rows: 16 warps per SM). Between the two, P goes through
-//     shared memory as ready operands. A step has two barriers: after its scores
-//     (P is there) and after its values.
-//   - one thread of the group loads the K of the next step after the first
-//     barrier, another its V after the second: each copy has the other half of a
-//     step to arrive, so one place for K and one for V are enough.
+//     one or two 64-wide head-dim chunks over all strips, so O^T stays in
+//     registers. Between the two, P goes through shared memory as ready operands.
+//     A step has two barriers: after its scores (P is there) and after its values.
+//   - one warp of the group loads the K of the next step after the first barrier,
+//     another its V after the second: each copy has the other half of a step to
+//     arrive, so one place for K and one for V are enough. A lane copies the part
+//     of a step that lies in one page: with one lane walking the pages, pages of
+//     16 tokens cost 18% more time than pages of 64, now 4%.
 //   - the softmax keeps a reference instead of the running maximum: it moves (and
 //     O is rescaled) only when a score passes it by 2^14. P <= 2^14 and its row's
 //     largest is >= 2^6 in fp16.
 //   - the strips of all (sequence, kv head, row block) units form one line, cut
 //     into equal ranges, one per group: lengths live on the device, so the cut is
-//     made there. A unit counts kUnitCost strips more than it has, for its start
-//     and end. A group that covers a unit alone writes its outputs; parts of
-//     others go to the workspace, those that the groups of a CTA end with joined
-//     there first, and a second kernel joins the parts in a fixed order. It is
-//     launched as a dependent, so its start overlaps the first kernel.
+//     made there. A unit counts a few strips more than it has, for its start and
+//     end. A group that covers a unit alone writes its outputs; parts of others
+//     go to the workspace, those that the groups of a CTA end with joined there
+//     first, and a second kernel joins the parts in a fixed order. Ranges are not
+//     shared out as groups become free: the shared counter between two barriers
+//     cost 8 us of 108, and the tail that it evens out is bound by memory too.
+//   - both kernels are launched as dependents of the one before them.
+//
+// Measured on a GB300 (a copy runs at 6.77 TB/s), calls in a row, the cache not
+// in the L2: 8 sequences of 16384 tokens, 8 kv heads, 4 query heads each,
+// D = 512 (604 MB): 105 us, 5.8 TB/s; one sequence of 131000 tokens: 102 us.
+// Bound by memory: 90 us of it are the steps, 7 us pass before the first one is
+// worked on, 4 us after the last one in the second kernel. Sixteen rows per
+// head: 152 us for 600 MB; issue slots (74 instructions a tile at 0.5 per clock:
+// registers leave three warps per scheduler) and the matrix unit, 44% busy,
+// bound it. Short calls are those 11 us and their steps: one sequence of 2000
+// tokens 12.5 us; 64 sequences of 20 to 1000 tokens, 16 heads of D = 128
+// (69 MB), 26 us.
 #include <atomic>
 
 #include "kv4.cuh"
@@ -44,7 +59,6 @@ namespace ffpa {
 namespace {
 
 constexpr int kMaxWarps = 16;
-constexpr int kUnitCost = 4;       // strips' worth of a unit's start and end
 constexpr float kRefBelow = 6.f;   // the reference lies this far (log2) below the maximum it was taken from
 constexpr float kRefSpan = 14.f;   // and is kept until a score is this far above it
 constexpr float kLn2 = 0.693147180559945309f;
@@ -56,6 +70,7 @@ struct Kv4Geo {
     int rows;        // 8 or 16
     int NG;          // groups per CTA
     int workers;     // groups of the whole grid
+    int unit_cost;   // strips' worth of a unit's start and end
     int spp;         // strips per page
     int step_blk;    // a step moves by so many pages
     int step_in;     // and strips
@@ -64,11 +79,17 @@ struct Kv4Geo {
     float* ml;       // [workers][2][rows][2] reference (log2) and sum
 };
 
-// Shape of a CTA for N head-dim chunks and NB blocks of eight query rows. A
-// warp accumulates two chunks of O^T. As many groups as registers hold (128
-// per thread for eight rows, 168 for sixteen), and steps as long as shared
-// memory then allows: four strips per warp in groups of one warp, else two or
-// one.
+// Shape of a CTA for N head-dim chunks and NB blocks of eight query rows.
+// CH: two chunks of O^T per warp need the fewest exchanges, but where groups are
+// small one chunk frees registers or saves the chunk that two warps of an odd N
+// both compute: 46.5 -> 41.8 us at N = 3 with eight rows, 40.7 -> 34.6 and
+// 35.1 -> 34.2 at N = 2 and 4 with sixteen, against 38.8 -> 41.1 at N = 8 with
+// eight and 36.9 -> 39.6 at N = 5 with sixteen (151 MB and 75 MB of cache).
+// NG: as many groups as registers hold, 128 per thread where O^T takes 32 of
+// them and 168 where it takes 64 (16 warps there spill: 155 -> 184 us at N = 5,
+// 600 MB). SW: steps as long as shared memory then allows, from eight strips per
+// warp in groups of one warp (142 -> 121 us at N = 1 against four, 600 MB) or
+// two in others.
 struct Shape {
     int CH;           // chunks per warp
     int C;            // warps per group
@@ -160,7 +181,7 @@ __device__ __forceinline__ int cached_len(const Kv4Decode& a, int b)
 
 __device__ __forceinline__ int strips_of(int len) { return (len >> 4) + ((len & 15) != 0); }
 // places of one unit on the line
-__device__ __forceinline__ int cost_of(int len) { return len > 0 ? strips_of(len) + kUnitCost : 0; }
+__device__ __forceinline__ int cost_of(const Kv4Geo& gm, int len) { return len > 0 ? strips_of(len) + gm.unit_cost : 0; }
 
 __device__ __forceinline__ long long div_up(long long x, int d)
 {
@@ -168,17 +189,17 @@ __device__ __forceinline__ long long div_up(long long x, int d)
 }
 
 // A run of strips [s0, s1) of one unit within a group's range [.., end) of the line; `unit` is the line place where
-// the unit begins, its first strip lies kUnitCost behind.
+// the unit begins, its first strip lies gm.unit_cost behind.
 struct Piece {
     int b, hk, rb, len;
     int s0, s1;
     long long unit, end;
 };
 
-__device__ __forceinline__ void piece_end(Piece& p)
+__device__ __forceinline__ void piece_end(const Kv4Geo& gm, Piece& p)
 {
     const int n = strips_of(p.len);
-    const long long left = p.end - p.unit - kUnitCost;
+    const long long left = p.end - p.unit - gm.unit_cost;
     p.s1 = left < n ? static_cast<int>(left) : n;
 }
 
@@ -191,20 +212,20 @@ __device__ __forceinline__ bool first_piece(const Kv4Decode& a, const Kv4Geo& gm
     p.b = b;
     p.len = cached_len(a, b);
     p.end = end;
-    const int cost = cost_of(p.len), u = static_cast<int>(div_up(at - b_at + 1, cost)) - 1;
+    const int cost = cost_of(gm, p.len), u = static_cast<int>(div_up(at - b_at + 1, cost)) - 1;
     p.unit = b_at + static_cast<long long>(u) * cost;
     p.hk = u / gm.rblocks;
     p.rb = u - p.hk * gm.rblocks;
     const int r = static_cast<int>(at - p.unit);
-    p.s0 = r > kUnitCost ? r - kUnitCost : 0;
-    piece_end(p);
+    p.s0 = r > gm.unit_cost ? r - gm.unit_cost : 0;
+    piece_end(gm, p);
     return p.s1 > p.s0;
 }
 
 __device__ __forceinline__ bool next_piece(const Kv4Decode& a, const Kv4Geo& gm, Piece& p)
 {
-    p.unit += cost_of(p.len);
-    if (p.unit + kUnitCost >= p.end) return false;
+    p.unit += cost_of(gm, p.len);
+    if (p.unit + gm.unit_cost >= p.end) return false;
     if (++p.rb == gm.rblocks) {
         p.rb = 0;
         if (++p.hk == a.f.pb.Hkv) {
@@ -216,7 +237,7 @@ __device__ __forceinline__ bool next_piece(const Kv4Decode& a, const Kv4Geo& gm,
         }
     }
     p.s0 = 0;
-    piece_end(p);
+    piece_end(gm, p);
     return p.s1 > 0;
 }
 
@@ -296,7 +317,8 @@ __device__ __forceinline__ void v_tile(const uint8_t* tile, int lane, uint32_t k
 
 // N: head-dim chunks (D / 64); NB: blocks of eight query rows.
 template <int N, int NB>
-__global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1) decode_kv4_kernel(const Kv4Decode a, const Kv4Geo gm)
+__global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1)
+    decode_kv4_kernel(const Kv4Decode a, const Kv4Geo gm)
 {
     constexpr Shape kShape = shape_of(N, NB);
     constexpr int CH = kShape.CH, C = kShape.C, NG = kShape.NG, SW = kShape.SW, D = 64 * N, kRows = 8 * NB;
@@ -344,7 +366,7 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
         const int per = (pb.B + 31) >> 5, b0 = min(lane * per, pb.B), b1 = min(b0 + per, pb.B);
         long long sum = 0;
 #pragma unroll 4
-        for (int b = b0; b < b1; ++b) sum += cost_of(cached_len(a, b));
+        for (int b = b0; b < b1; ++b) sum += cost_of(gm, cached_len(a, b));
         long long incl = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -362,7 +384,7 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
             long long b_at = __shfl_sync(0xffffffffu, lo, src);
             int b = src * per;
             for (;;) {  // one of that lane's sequences
-                const long long n = static_cast<long long>(cost_of(cached_len(a, b))) * units_b;
+                const long long n = static_cast<long long>(cost_of(gm, cached_len(a, b))) * units_b;
                 if (at < b_at + n) break;
                 b_at += n;
                 ++b;
@@ -446,7 +468,8 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
                 pg = 0;
             }
             const int skip = lane ? 0 : in;
-            bulk_load((kv ? v_mem : k_mem) + at * strip_bytes, ld.head + pg * (2 * gm.v_off) + static_cast<size_t>(skip) * strip_bytes,
+            bulk_load((kv ? v_mem : k_mem) + at * strip_bytes,
+                      ld.head + pg * (2 * gm.v_off) + static_cast<size_t>(skip) * strip_bytes,
                       min(n - static_cast<int>(at), gm.spp - skip) * strip_bytes, &full[kv]);
         }
         if (s + steps < s1) {
@@ -534,13 +557,17 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
                     uint32_t x[4][4];
                     k_tile(tile + i * strip_bytes, lane, x);
 #pragma unroll
-                    for (int k = 0; k < NB; ++k) mma_f16_16816(to[i][k], x[0][0], x[0][1], x[0][2], x[0][3], q0[k].x, q0[k].y);
+                    for (int k = 0; k < NB; ++k)
+                        mma_f16_16816(to[i][k], x[0][0], x[0][1], x[0][2], x[0][3], q0[k].x, q0[k].y);
 #pragma unroll
-                    for (int k = 0; k < NB; ++k) mma_f16_16816(to[i][k], x[1][0], x[1][1], x[1][2], x[1][3], q0[k].z, q0[k].w);
+                    for (int k = 0; k < NB; ++k)
+                        mma_f16_16816(to[i][k], x[1][0], x[1][1], x[1][2], x[1][3], q0[k].z, q0[k].w);
 #pragma unroll
-                    for (int k = 0; k < NB; ++k) mma_f16_16816(to[i][k], x[2][0], x[2][1], x[2][2], x[2][3], q1[k].x, q1[k].y);
+                    for (int k = 0; k < NB; ++k)
+                        mma_f16_16816(to[i][k], x[2][0], x[2][1], x[2][2], x[2][3], q1[k].x, q1[k].y);
 #pragma unroll
-                    for (int k = 0; k < NB; ++k) mma_f16_16816(to[i][k], x[3][0], x[3][1], x[3][2], x[3][3], q1[k].z, q1[k].w);
+                    for (int k = 0; k < NB; ++k)
+                        mma_f16_16816(to[i][k], x[3][0], x[3][1], x[3][2], x[3][3], q1[k].z, q1[k].w);
                 }
                 tile += kKv4Tile;
                 q += NB * 64;
@@ -553,7 +580,8 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
 #pragma unroll
             for (int k = 0; k < NB; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[i][k][e] = SW == 1 ? sum[0][i][k][e] + sum[SW == 1 ? 1 : 0][i][k][e] : sum[0][i][k][e];
+                for (int e = 0; e < 4; ++e)
+                    s[i][k][e] = SW == 1 ? sum[0][i][k][e] + sum[SW == 1 ? 1 : 0][i][k][e] : sum[0][i][k][e];
     };
     // P of my strips as operands to the step's buffer; their sums
     float dl[NB][2];
@@ -571,7 +599,8 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
                 dl[k][0] += x[0] + x[2];
                 dl[k][1] += x[1] + x[3];
                 // fp16 P: half a step of 2^-11, an eighth of what bf16 operands would cost
-                p[(i * NB + k) * 32] = make_uint2(transpose8x8(pack2<false>(x[0], x[1])), transpose8x8(pack2<false>(x[2], x[3])));
+                p[(i * NB + k) * 32] =
+                    make_uint2(transpose8x8(pack2<false>(x[0], x[1])), transpose8x8(pack2<false>(x[2], x[3])));
             }
     };
     // O^T += V^T P^T over my chunks, for the n strips of a step, whose first token is tok
@@ -657,7 +686,8 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
                 }
                 // largest magnitude to [2^14, 2^15); rows of zeros or that are not finite stay as they are
                 const int e = static_cast<int>(amax >> 7);
-                if (amax > 0 && e < 255) mul = __uint_as_float(static_cast<uint32_t>(min(14 + 127 - e, 126) + 127) << 23);
+                if (amax > 0 && e < 255)
+                    mul = __uint_as_float(static_cast<uint32_t>(min(14 + 127 - e, 126) + 127) << 23);
 #pragma unroll
                 for (int j = 0; j < CH; ++j) {
                     uint32_t w[8] = {x[j].x, x[j].y, x[j].z, x[j].w, y[j].x, y[j].y, y[j].z, y[j].w};
@@ -894,7 +924,8 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
 #pragma unroll 1
     for (int e = ((group - run0) * C + wg) * 32 + lane; e < items; e += (run1 - run0 + 1) * C * 32) {
         const int r = e / (D / 4), d = e % (D / 4) * 4, w = d / (64 * CH);
-        const float* at = reinterpret_cast<const float*>(smem) + w * kPartFloats + r * kPartPitch + d - 64 * min(w * CH, N - CH);
+        const float* at =
+            reinterpret_cast<const float*>(smem) + w * kPartFloats + r * kPartPitch + d - 64 * min(w * CH, N - CH);
         float mx = -INFINITY, sum = 0.f;
 #pragma unroll 1
         for (int k = run0; k <= run1; ++k) mx = fmaxf(mx, sh.ml[k][r][0]);
@@ -935,7 +966,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_kernel(const Kv4
     const int units_b = pb.Hkv * gm.rblocks;
     long long total = 0, before = 0;  // places of the line, and those before sequence b
     for (int k = threadIdx.x; k < pb.B; k += kJoinThreads) {
-        const int c = cost_of(cached_len(a, k));
+        const int c = cost_of(gm, cached_len(a, k));
         total += c;
         before += k < b ? c : 0;
     }
@@ -965,14 +996,15 @@ __global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_kernel(const Kv4
         return;
     }
     // the unit's strips lie at [first, end) of the line; groups v0 .. v1 hold them
-    const long long first = before * units_b + static_cast<long long>((h / G) * gm.rblocks + r / gm.rows) * cost_of(len) + kUnitCost;
+    const int unit = (h / G) * gm.rblocks + r / gm.rows;
+    const long long first = before * units_b + static_cast<long long>(unit) * cost_of(gm, len) + gm.unit_cost;
     const long long end = first + n, chunk = div_up(total, gm.workers);
     const int v0 = static_cast<int>(first / chunk), v1 = static_cast<int>((end - 1) / chunk);
     pdl_wait();
     if (v0 == v1) return;  // written by its group
     // v1 ends in this unit unless its range reaches strips of the next one; the parts that groups of a CTA end with
     // are in slot 1 of the last of them, a part that is followed by another unit is in slot 0
-    const bool ends = min((v1 + 1LL) * chunk, total) <= end + kUnitCost;
+    const bool ends = min((v1 + 1LL) * chunk, total) <= end + gm.unit_cost;
     const int vl = ends ? v1 : v1 - 1, c0 = v0 / gm.NG, parts = vl / gm.NG - c0 + 1 + (ends ? 0 : 1), rr = r % gm.rows;
     const bool in = d < pb.D;
     // a warp's parts relative to their own largest reference; four in flight
@@ -1048,6 +1080,9 @@ Plan plan(const Problem& pb)
     gm.rows = 8 * p.nb;
     gm.rblocks = static_cast<int>((R + gm.rows - 1) / gm.rows);
     gm.NG = shape_of(pb.D >> 6, p.nb).NG;
+    // Its queries, its sums and its part or outputs. With eight rows 2 strips cost up to 5% (64 sequences of 20 to 1000
+    // tokens) and 8 the same to 2%, none 50%; with sixteen 4 cost up to 10% (5000 tokens on one head), 12 up to 4%.
+    gm.unit_cost = 4 * p.nb;
     const int sms = num_sms();
     p.ctas = sms > 0 ? sms : 152;
     gm.workers = p.ctas * gm.NG;
@@ -1118,8 +1153,8 @@ cudaError_t launch_decode_kv4(const Kv4Decode& a, void* workspace, cudaStream_t 
     if (ran != cudaSuccess) return ran;
     const Problem& pb = a.f.pb;
     const dim3 grid(static_cast<unsigned>(static_cast<long long>(pb.B) * pb.Hq * pb.Nq), (pb.D + 127) / 128);
-    return launch_dependent(a.f.bf16 ? decode_kv4_join_kernel<true> : decode_kv4_join_kernel<false>, grid, kJoinThreads, 0, s,
-                            a, p.gm);
+    auto* join = a.f.bf16 ? decode_kv4_join_kernel<true> : decode_kv4_join_kernel<false>;
+    return launch_dependent(join, grid, kJoinThreads, 0, s, a, p.gm);
 }
 
 }  // namespace ffpa
