@@ -10,6 +10,7 @@
 
 #include "../../include/ffpa.h"
 #include "kernels.h"
+#include "kv4.h"
 #include "ptx.cuh"
 
 namespace {

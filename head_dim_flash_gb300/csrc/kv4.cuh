@@ -29,7 +29,7 @@
 
 #include <cstdint>
 
-#include "kernels.h"
+#include "kv4.h"
 #include "ptx.cuh"
 #include "tile_common.cuh"
 

@@ -116,9 +116,6 @@ __device__ __forceinline__ bool mbar_test_cluster(uint64_t* bar, uint32_t parity
 // high half a block or sequence index): the ffpa_status of the failure.
 enum : uint32_t { DEV_OK = 0, DEV_INVALID = 1, DEV_TIMEOUT = 4 };
 
-// Sites of a sequence that breaks the contract of a 4-bit cache.
-enum : uint32_t { VS_KV4_WRITE = 0x78, VS_KV4_READ = 0x79, VS_KV4_DECODE = 0x7a };
-
 // Bounded wait on the phase `parity` of `bar`. Gives up when the CTA-wide
 // abort flag is raised, when another block has already recorded a failure in
 // the device status word, or after `limit_ns` of wall time; on a time-out it
