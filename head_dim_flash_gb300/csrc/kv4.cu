@@ -30,10 +30,10 @@ struct Range {
 
 __device__ __forceinline__ bool find_range(const Kv4Io& a, uint32_t site, Range& s)
 {
-    const long long u = unit_id();
-    if (u >= static_cast<long long>(a.B) * a.Hkv) return false;
-    s.b = static_cast<int>(u / a.Hkv);
-    s.h = static_cast<int>(u - static_cast<long long>(s.b) * a.Hkv);
+    const unsigned u = static_cast<unsigned>(unit_id());  // at most 65535^2 units: below 2^32
+    if (u >= static_cast<unsigned long long>(a.B) * a.Hkv) return false;
+    s.b = static_cast<int>(u / static_cast<unsigned>(a.Hkv));
+    s.h = static_cast<int>(u - static_cast<unsigned>(s.b) * static_cast<unsigned>(a.Hkv));
     int cnt;
     if (!kv4_range(a, s.b, site, s.p0, cnt, s.row0)) return false;
     s.p1 = s.p0 + cnt;
@@ -70,8 +70,8 @@ __device__ __forceinline__ void page_tiles(const Kv4Io& a, const Range& s, uint3
 
 __device__ __forceinline__ Tiles first_tiles(const Kv4Io& a, const Range& s, uint32_t site)
 {
-    const int spp = a.cache.page_size >> 4, block = s.first / spp;
-    Tiles x{nullptr, s.first - block * spp, a.cache.table + s.b * a.cache.table_stride + block};
+    const unsigned spp = a.cache.page_size >> 4, block = static_cast<unsigned>(s.first) / spp;
+    Tiles x{nullptr, static_cast<int>(s.first - block * spp), a.cache.table + s.b * a.cache.table_stride + block};
     page_tiles(a, s, site, x);
     return x;
 }
@@ -92,29 +92,38 @@ __device__ __forceinline__ int k_token(int g, int hi) { return g + 8 * hi; }
 __device__ __forceinline__ int v_token(int t, int j) { return 2 * t + (j & 1) + 8 * (j >> 1); }
 
 // ---------------------------------------------------------------- write
-// Largest magnitude of four words of 16-bit values. A NaN is cleared from the words first: the cache has none, one is
-// stored as zero.
 template <bool BF16>
-__device__ __forceinline__ float amax8(uint32_t (&w)[4])
+using Pair = typename std::conditional<BF16, __nv_bfloat162, __half2>::type;
+
+// Largest magnitudes of the low and the high halves of four words of 16-bit values; NaN where there is one.
+template <bool BF16>
+__device__ __forceinline__ Pair<BF16> amax4(uint32_t (&w)[4])
 {
-    using T2 = typename std::conditional<BF16, __nv_bfloat162, __half2>::type;
-    T2 x[4];
+    Pair<BF16> x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __habs2(*reinterpret_cast<T2*>(&w[i]));
-    const T2 m = __hmax2_nan(__hmax2_nan(x[0], x[1]), __hmax2_nan(x[2], x[3]));
-    float2 f = unpack2<BF16>(*reinterpret_cast<const uint32_t*>(&m));
-    if (f.x != f.x || f.y != f.y) {
-        f.x = 0.f;
+    for (int i = 0; i < 4; ++i) x[i] = __habs2(*reinterpret_cast<Pair<BF16>*>(&w[i]));
+    return __hmax2_nan(__hmax2_nan(x[0], x[1]), __hmax2_nan(x[2], x[3]));
+}
+
+// The larger half of a in the low half, that of b in the high half.
+template <bool BF16>
+__device__ __forceinline__ Pair<BF16> halves(Pair<BF16> a, Pair<BF16> b)
+{
+    const uint32_t x = *reinterpret_cast<uint32_t*>(&a), y = *reinterpret_cast<uint32_t*>(&b);
+    uint32_t lo = __byte_perm(x, y, 0x5410), hi = __byte_perm(x, y, 0x7632);
+    return __hmax2(*reinterpret_cast<Pair<BF16>*>(&lo), *reinterpret_cast<Pair<BF16>*>(&hi));
+}
+
+// The cache has no NaN, one is stored as zero.
+template <bool BF16>
+__device__ __forceinline__ void clear_nan(uint32_t (&w)[4])
+{
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float2 v = unpack2<BF16>(w[i]);
-            if (v.x != v.x) w[i] &= 0xffff0000u, v.x = 0.f;
-            if (v.y != v.y) w[i] &= 0x0000ffffu, v.y = 0.f;
-            f.x = fmaxf(f.x, fmaxf(fabsf(v.x), fabsf(v.y)));
-        }
-        return f.x;
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = kv4_unpack<BF16>(w[i]);
+        if (v.x != v.x) w[i] &= 0xffff0000u;
+        if (v.y != v.y) w[i] &= 0x0000ffffu;
     }
-    return fmaxf(f.x, f.y);
 }
 
 template <bool BF16>
@@ -123,7 +132,7 @@ __device__ __forceinline__ uint32_t codes(const uint32_t (&w)[4], float rcp)
     float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<BF16>(w[i]);
+        const float2 f = kv4_unpack<BF16>(w[i]);
         x[2 * i] = f.x;
         x[2 * i + 1] = f.y;
     }
@@ -189,27 +198,50 @@ __global__ void __launch_bounds__(kIoWarps * 32, 4) kv4_write_kernel(const Kv4Io
         vr += 2 * v8;
     };
     auto store = [&](int strip, int ch, Data& d, uint8_t* tiles) {
-        uint32_t kc[4], ks[2], vc[4], vs = 0;
+        // magnitudes stay 16-bit pairs (a maximum is exact) down to one per group
+        Pair<BF16> mk[2], mv[4];
+        for (;;) {
+            mk[0] = __hmax2_nan(amax4<BF16>(d.k[0][0]), amax4<BF16>(d.k[0][1]));
+            mk[1] = __hmax2_nan(amax4<BF16>(d.k[1][0]), amax4<BF16>(d.k[1][1]));
+            Pair<BF16> all = __hmax2_nan(mk[0], mk[1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mv[j] = amax4<BF16>(d.v[j]);
+                all = __hmax2_nan(all, mv[j]);
+            }
+            const float2 f = kv4_unpack<BF16>(*reinterpret_cast<uint32_t*>(&all));
+            if (f.x == f.x && f.y == f.y) break;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                clear_nan<BF16>(d.k[x][0]);
+                clear_nan<BF16>(d.k[x][1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) clear_nan<BF16>(d.v[j]);
+        }
+        __syncwarp();
+        uint32_t kc[4], ks[2], vc[4];
+        Pair<BF16> m = halves<BF16>(mk[0], mk[1]);
+        float2 f = kv4_unpack<BF16>(*reinterpret_cast<uint32_t*>(&m));
+        ks[0] = kv4_scale_code(f.x);
+        ks[1] = kv4_scale_code(f.y);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const float m = fmaxf(amax8<BF16>(d.k[x][0]), amax8<BF16>(d.k[x][1]));
-            ks[x] = kv4_scale_code(m);
             const float rcp = kv4_scale_rcp(ks[x]);
             kc[2 * x] = codes<BF16>(d.k[x][0], rcp);
             kc[2 * x + 1] = codes<BF16>(d.k[x][1], rcp);
         }
         // a V group's halves are in lanes g and g ^ 1: the even one finds the scales of tokens 0 and 1, the odd one those
         // of 2 and 3
-        float m[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            m[j] = amax8<BF16>(d.v[j]);
-            m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 4));
-        }
         const bool odd = g & 1;
-        const uint32_t c0 = kv4_scale_code(odd ? m[2] : m[0]), c1 = kv4_scale_code(odd ? m[3] : m[1]);
-        const uint32_t mine = c0 | (c1 << 8), other = __shfl_xor_sync(0xffffffffu, mine, 4);
-        vs = odd ? other | (mine << 16) : mine | (other << 16);
+        Pair<BF16> v01 = halves<BF16>(mv[0], mv[1]), v23 = halves<BF16>(mv[2], mv[3]);
+        Pair<BF16> mine = odd ? v23 : v01, other = odd ? v01 : v23;
+        uint32_t got = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&other), 4);
+        m = __hmax2(mine, *reinterpret_cast<Pair<BF16>*>(&got));
+        f = kv4_unpack<BF16>(*reinterpret_cast<uint32_t*>(&m));
+        const uint32_t half = kv4_scale_code(f.x) | (kv4_scale_code(f.y) << 8);
+        got = __shfl_xor_sync(0xffffffffu, half, 4);
+        const uint32_t vs = odd ? got | (half << 16) : half | (got << 16);
 #pragma unroll
         for (int j = 0; j < 4; ++j) vc[j] = codes<BF16>(d.v[j], kv4_scale_rcp((vs >> (8 * j)) & 0xffu));
         if (!tiles) return;

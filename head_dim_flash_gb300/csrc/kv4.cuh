@@ -40,6 +40,15 @@ __device__ __forceinline__ void kv4_invalid(uint32_t* status, uint32_t site, int
     atomicCAS(status, 0u, DEV_INVALID | (site << 8) | ((static_cast<uint32_t>(b) & 0xffffu) << 16));
 }
 
+// The two values of a 16-bit pair. (A bf16 is the upper half of its float: one operation each, half of what the
+// conversion takes.)
+template <bool BF16>
+__device__ __forceinline__ float2 kv4_unpack(uint32_t w)
+{
+    if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    return unpack2<BF16>(w);
+}
+
 // Byte offset of the first tile of strip `strip` (16 tokens) of a page.
 __device__ __forceinline__ size_t kv4_strip_offset(const Kv4Cache& c, int Hkv, int chunks, int page, int kv, int h,
                                                    int strip)
