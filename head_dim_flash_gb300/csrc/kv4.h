@@ -31,6 +31,7 @@ struct Kv4Io {
     const int* cu;            // device [B + 1]: packed token offsets, or null
     int total;
     int strips_per_cta;       // set by the launch
+    int wide;                 // the same: every row of k begins on 32 bytes
     uint32_t* status;
 };
 cudaError_t launch_kv4_write(const Kv4Io& a, cudaStream_t s);

@@ -94,6 +94,31 @@ def test_write_matches_the_reference_byte_for_byte(dt, D, page, H, lo, new, tran
     assert np.array_equal(cache.cpu().numpy(), ref)  # the written cells, and every other byte as it was
 
 
+@pytest.mark.parametrize("first,pitch", [(8, 208), (0, 200), (8, 200), (16, 224)])
+def test_rows_on_sixteen_and_on_thirty_two_bytes(first, pitch):
+    # rows that begin on an odd multiple of 16 bytes, every row or every other one, against rows on 32
+    rng = np.random.default_rng(first + pitch)
+    B, N, H, D, page = 2, 37, 2, 192, 32
+    table, pages = block_tables([N, N + 3], page, rng)
+    ref = random_cache(pages, page, H, D, rng)
+    cache, t = dev(ref), dev(table)
+    wide = [torch.from_numpy(rng.standard_normal((B, N, H, pitch))).to(BF16).cuda() for _ in range(2)]
+    k, v = (w[..., first:first + D].transpose(1, 2) for w in wide)
+    start, count = (dev(np.array(x, np.int32)) for x in ((0, 3), (N, N)))
+    api.kv4_write(cache, t, k, v, start=start)
+    out = [torch.full_like(w, -7.0) for w in wide]
+    api.kv4_read(cache, t, count, start=start, k_out=out[0][..., first:first + D].transpose(1, 2),
+                 v_out=out[1][..., first:first + D].transpose(1, 2))
+    api.get_status()
+    for b in range(B):
+        lo = int(start[b])
+        kv4.write(ref, table[b], lo, f64(k[b].transpose(0, 1)), f64(v[b].transpose(0, 1)))
+        for got, want in zip(out, kv4.read(ref, table[b], lo, N)):
+            assert np.array_equal(f64(got[b, ..., first:first + D]), want)
+            assert (got[b, ..., :first] == -7).all() and (got[b, ..., first + D:] == -7).all()
+    assert np.array_equal(cache.cpu().numpy(), ref)
+
+
 @pytest.mark.parametrize("start", [None, (3, 0, 50, 17)])
 def test_packed_write_matches_the_reference(start):
     rng = np.random.default_rng(5)
