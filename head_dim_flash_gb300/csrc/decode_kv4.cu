@@ -80,11 +80,14 @@ struct Kv4Geo {
 };
 
 // Shape of a CTA for N head-dim chunks and NB blocks of eight query rows.
-// CH: two chunks of O^T per warp need the fewest exchanges, but where groups are
-// small one chunk frees registers or saves the chunk that two warps of an odd N
-// both compute: 46.5 -> 41.8 us at N = 3 with eight rows, 40.7 -> 34.6 and
-// 35.1 -> 34.2 at N = 2 and 4 with sixteen, against 38.8 -> 41.1 at N = 8 with
-// eight and 36.9 -> 39.6 at N = 5 with sixteen (151 MB and 75 MB of cache).
+// CH: two chunks of O^T per warp need the fewest exchanges and barriers, but one
+// halves its registers (16 warps for sixteen rows) and saves the chunk that two
+// warps of an odd N both compute. Eight rows, two against one (151 MB of cache):
+// 46.5 and 41.8 us at N = 3, 38.8 and 41.1 at N = 8. Sixteen rows (75 MB, and
+// 600 MB): 40.7 and 34.6 at N = 2, 33.3 and 32.8 (157, 138) at N = 6, 36.3 and
+// 34.5 (166, 162) at N = 7, 34.3 and 32.7 (159, 147) at N = 8; but 31.5 and 32.8
+// (151, 147) at N = 5, whose 15 warps take long steps, and 37.8 and 40.3 (177,
+// 176) at N = 9, where one chunk leaves nine warps.
 // NG: as many groups as registers hold, 128 per thread where O^T takes 32 of
 // them and 168 where it takes 64 (16 warps there spill: 155 -> 184 us at N = 5,
 // 600 MB). SW: steps as long as shared memory then allows, from eight strips per
@@ -104,7 +107,7 @@ __host__ __device__ constexpr Shape shape_of(int N, int NB)
 {
     Shape p{};
     const int room = kMaxSmem - kStaticBytes;
-    p.CH = N == 1 || N == 3 || (NB == 2 && N <= 4) ? 1 : 2;
+    p.CH = N == 1 || (NB == 1 ? N == 3 : N <= 8 && N != 5) ? 1 : 2;
     p.C = (N + p.CH - 1) / p.CH;
     p.NG = (p.CH * NB <= 2 ? 16 : 12) / p.C;
     for (p.SW = p.C > 1 ? 2 : 8;; p.SW >>= 1) {
