@@ -46,11 +46,11 @@
 // D = 512 (604 MB): 105 us, 5.8 TB/s; one sequence of 131000 tokens: 102 us.
 // Bound by memory: 90 us of it are the steps, 7 us pass before the first one is
 // worked on, 4 us after the last one in the second kernel. Sixteen rows per
-// head: 152 us for 600 MB; issue slots (74 instructions a tile at 0.5 per clock:
-// registers leave three warps per scheduler) and the matrix unit, 44% busy,
-// bound it. Short calls are those 11 us and their steps: one sequence of 2000
-// tokens 12.5 us; 64 sequences of 20 to 1000 tokens, 16 heads of D = 128
-// (69 MB), 26 us.
+// head: 147 us for 600 MB at D = 512; 74 instructions and eight matrix products
+// a tile, whose conversions (the ALU 44% busy), matrix unit (43%) and issue
+// slots (54%) three or four warps per scheduler cannot overlap further. Short
+// calls are those 11 us and their steps: one sequence of 2000 tokens 12.5 us; 64
+// sequences of 20 to 1000 tokens, 16 heads of D = 128 (69 MB), 26 us.
 #include <atomic>
 
 #include "kv4.cuh"
