@@ -727,7 +727,7 @@ ffpa_status ffpa_varlen_kv4_read(ffpa_dtype dt, ffpa_kv4_cache cache, void* k, v
 
 size_t ffpa_decode_kv4_workspace_bytes(ffpa_dtype, int B, int Hq, int Hkv, int Nq, int D)
 {
-    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Nq <= 0 || D <= 0 || Hq % Hkv != 0) return 0;
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Nq <= 0 || Hq % Hkv != 0 || D < 64 || D > 1024 || D % 64 != 0) return 0;
     return ffpa::kv4_decode_workspace_bytes(dense_problem(B, Hq, Hkv, Nq, 0, D, 0, 1.f));
 }
 

@@ -289,6 +289,7 @@ FFPA_API ffpa_status ffpa_varlen_kv4_read(ffpa_dtype dt, ffpa_kv4_cache cache, v
  *   per workspace.
  * Meant for few query rows per kv head (Hq / Hkv * Nq); for a long chunk of
  * queries, ffpa_varlen_kv4_read and ffpa_varlen_fwd.
+ * The workspace query returns 0 for sizes outside the operation.
  */
 FFPA_API size_t ffpa_decode_kv4_workspace_bytes(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int D);
 FFPA_API ffpa_status ffpa_decode_fwd_kv4(ffpa_dtype dt, ffpa_view q, ffpa_kv4_cache cache, const int* seq_lens,

@@ -116,3 +116,16 @@ def test_cache_bytes(lib):  # noqa: F811
     assert lib.ffpa_kv4_cache_bytes(1 << 20, 64, 8, 512) == (1 << 20) * 294912
     for bad in ((7, 24, 8, 512), (7, 0, 8, 512), (7, 16, 8, 96), (7, 16, 8, 1088), (-1, 16, 8, 64)):
         assert lib.ffpa_kv4_cache_bytes(*bad) == 0
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,D", [(2, 4, 2, 1, 32), (2, 4, 2, 1, 96), (2, 4, 2, 1, 0), (2, 4, 2, 1, -64),
+                                           (2, 4, 2, 1, 1088), (2, 4, 2, 1, 1 << 30), (0, 4, 2, 1, 64), (2, 3, 2, 1, 64),
+                                           (2, 4, 0, 1, 64), (2, 4, 2, 0, 64)])
+def test_workspace_of_sizes_outside_the_operation_is_empty(lib, B, Hq, Hkv, Nq, D):  # noqa: F811
+    assert lib.ffpa_decode_kv4_workspace_bytes(0, B, Hq, Hkv, Nq, D) == 0
+
+
+def test_workspace_covers_every_head_dim_and_row_count(lib):  # noqa: F811
+    for D in range(64, 1025, 64):
+        for Nq in (1, 2, 3, 1000):
+            assert lib.ffpa_decode_kv4_workspace_bytes(0, 2, 8, 2, Nq, D) > 0
