@@ -152,6 +152,25 @@ __device__ __forceinline__ uint32_t kv4_code8(const float (&x)[8], float rcp)
     return r;
 }
 
+// Launches a kernel of the 4-bit cache. It starts before the one before it in the stream has ended, and waits for that
+// end (pdl_wait) before it touches memory; every CTA does, so that its own end follows from it.
+template <typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t s,
+                             const Args&... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Sequence range [p0, p0 + cnt) of cache positions and its first row in the
 // 16-bit tensor, from the device arrays. A range outside the cache's blocks or
 // the tensor's rows records DEV_INVALID and is not processed.
