@@ -530,6 +530,40 @@ def test_calls_at_once_on_two_streams():
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
 
 
+def test_calls_read_what_the_kernels_before_them_write():
+    """A chain whose every call reads the outputs of the one before it, against the same calls one at a time: the
+    forward's kernels let the next one start before they end."""
+    torch.manual_seed(5)
+    B, H, N, D, page = 1, 4, 1000, 256, 64
+    x = [torch.randn(B, H, N, D, device="cuda").to(BF16) for _ in range(3)]
+    table = torch.arange(16, dtype=torch.int32, device="cuda").view(1, 16)
+    n = torch.tensor([N], dtype=torch.int32, device="cuda")
+
+    def chain(wait):
+        cache = api.kv4_cache(16, page, H, D)
+        q, k, v = x
+        for _ in range(4):
+            k, _ = api.fwd(q, k, v, True)
+            wait()
+            api.kv4_write(cache, table, k, k)
+            wait()
+            o, lse = api.decode_fwd_kv4(k[:, :, -2:], cache, table, n, True)
+            wait()
+            api.kv4_write(cache, table, o, o, start=n - 2)
+            wait()
+            k, v = api.kv4_read(cache, table, n, max_count=N)
+            wait()
+            v, _ = api.fwd(v, k, v)
+            wait()
+        return cache, k, v, o, lse
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(5):
+        got = chain(lambda: None)
+        api.get_status()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_results_take_the_place_of_their_inputs():
     # the rows of a unit are read before any of them is written
     q, cache, t, ln, o, lse = decode_case([3000, 17, 900, 0], 2, 8, 2, 256, 64, True, BF16, seed=31)
