@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kIoWarps * 32) kv4_read_kernel(const Kv4Io a)
 
 // Completes the arguments. One warp per chunk, at most kIoWarps; CTAs along x cover the strips that N tokens can touch
 // (one more when a start need not be a multiple of 16). A CTA takes two strips where there are enough to keep the SMs
-// full: at D = 512 that is worth 6% of a prompt's write and 9% of a read against one, and four cost 5%.
+// full: at D = 512 that is worth 6% of a prompt's write and 9% of a read against one; four cost 2 to 3% more than two.
 bool io_grid(Kv4Io& a, dim3* grid, unsigned* threads)
 {
     const long long strips = (static_cast<long long>(a.N) + (a.start ? 30 : 15)) >> 4;
