@@ -31,6 +31,13 @@
 //   - the softmax keeps a reference instead of the running maximum: it moves (and
 //     O is rescaled) only when a score passes it by 2^14. P <= 2^14 and its row's
 //     largest is >= 2^6 in fp16.
+//   - P in fp16 costs as much as the rounding of an fp16 output, up to 1.4 times its error against 64 bits (one sequence
+//     of 131000 tokens: 2.9e-4 where 2.1e-4 is the output's own). With up to four rows half of the matrix product's
+//     eight columns are idle: for fp16 outputs they take the rows a second time, with the fp16 remainders of P, and the
+//     two are added in the end (2.1e-4). That costs 0 to 1% at D >= 256, 2 to 3% below (118.3 -> 121.4 us at D = 64, 604
+//     MB; 12.8 -> 12.9 one short sequence). More rows would need a second product of the same values: 108.5 -> 121 us for
+//     eight rows, 144 -> 175 for sixteen (D = 512, 604 MB); they and bf16 outputs, whose own rounding is eight times
+//     P's, keep one.
 //   - the strips of all (sequence, kv head, row block) units form one line, cut
 //     into equal ranges, one per group: lengths live on the device, so the cut is
 //     made there. A unit counts a few strips more than it has, for its start and
@@ -147,6 +154,21 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t phase, volatile i
                                        uint64_t limit_ns, uint32_t site)
 {
     return *abort_flag == 0 && mbar_wait(bar, phase, abort_flag, status, limit_ns, site, false);
+}
+
+// Two values less `minus` (fp16) times their fp16 roundings h, rounded to fp16.
+__device__ __forceinline__ uint32_t remainders(uint32_t h, unsigned short minus, float x, float y)
+{
+    float a, b;
+    asm("{\n"
+        " .reg .b16 lo, hi;\n"
+        " mov.b32 {lo, hi}, %2;\n"
+        " fma.rn.f32.f16 %0, lo, %3, %4;\n"
+        " fma.rn.f32.f16 %1, hi, %3, %5;\n"
+        "}\n"
+        : "=f"(a), "=f"(b)
+        : "r"(h), "h"(minus), "f"(x), "f"(y));
+    return pack2<false>(a, b);
 }
 
 // 8 x 8 matrix of 16-bit values held as an MMA fragment -> its transpose.
@@ -334,6 +356,9 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int G = pb.Hq / pb.Hkv, R = G * pb.Nq;
     const int units_b = pb.Hkv * gm.rblocks;          // units per sequence
+    // fp16 outputs, up to four rows: columns 4 .. 7 hold the rows again, with what P loses in fp16
+    const bool again = NB == 1 && R <= 4 && !bf16;
+    const unsigned short minus = again && t >= 2 ? 0xbc00 : 0;  // fp16 -1 or 0
     __shared__ DecShared sh;
     extern __shared__ __align__(128) uint8_t smem[];
 
@@ -413,7 +438,7 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
     auto fetch_q = [&](Queries& to) {
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int r = cur.rb * kRows + k * 8 + g, hq = r / pb.Nq, h = cur.hk * G + hq, i = r - hq * pb.Nq;
+            const int r = cur.rb * kRows + k * 8 + (again ? g & 3 : g), hq = r / pb.Nq, h = cur.hk * G + hq, i = r - hq * pb.Nq;
             const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.f.q) + cur.b * pb.vq.sb +
                                                             h * pb.vq.sh + i * pb.vq.sn + wg * 64 + t * 16);
 #pragma unroll
@@ -602,9 +627,13 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
                 for (int e = 0; e < 4; ++e) x[e] = ex2_approx(s[i][k][e]);
                 dl[k][0] += x[0] + x[2];
                 dl[k][1] += x[1] + x[3];
-                // fp16 P: half a step of 2^-11, an eighth of what bf16 operands would cost
-                p[(i * NB + k) * 32] =
-                    make_uint2(transpose8x8(pack2<false>(x[0], x[1])), transpose8x8(pack2<false>(x[2], x[3])));
+                // fp16 P: half a step of 2^-11, an eighth of the rounding of a bf16 output
+                uint32_t h0 = pack2<false>(x[0], x[1]), h1 = pack2<false>(x[2], x[3]);
+                if (again) {
+                    h0 = remainders(h0, minus, x[0], x[1]);
+                    h1 = remainders(h1, minus, x[2], x[3]);
+                }
+                p[(i * NB + k) * 32] = make_uint2(transpose8x8(h0), transpose8x8(h1));
             }
     };
     // O^T += V^T P^T over my chunks, for the n strips of a step, whose first token is tok
@@ -716,7 +745,7 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 c2[k][e] = __shfl_sync(0xffffffffu, scale, (2 * t + e) * 4);
-                limits[k][e] = pb.causal ? min(cur.len, least + (r0 + k * 8 + 2 * t + e) % pb.Nq) : cur.len;
+                limits[k][e] = pb.causal ? min(cur.len, least + (r0 + k * 8 + (again ? (2 * t + e) & 3 : 2 * t + e)) % pb.Nq) : cur.len;
                 m[k][e] = 0.f;
                 l[k][e] = 0.f;
             }
@@ -838,6 +867,15 @@ __global__ void __launch_bounds__(shape_of(N, NB).NG * shape_of(N, NB).C * 32, 1
                 for (int w = 0; w < C; ++w) l[n][q] += sh.sum[group * C + w][n * 8 + 2 * t + q];
                 if (l[n][q] == 0.f) m[n][q] = -INFINITY;  // no keys, no reference
             }
+
+        if (again) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[c][i][0][e] += __shfl_xor_sync(0xffffffffu, acc[c][i][0][e], 2);
+        }
 
         // ---- a whole unit's outputs, or a part of one
         if (cur.s0 == 0 && cur.s1 == strips_of(cur.len)) {

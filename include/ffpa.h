@@ -283,6 +283,10 @@ FFPA_API ffpa_status ffpa_varlen_kv4_read(ffpa_dtype dt, ffpa_kv4_cache cache, v
  * (device int32 [B]). Causal is bottom-right per sequence: query row i sees
  * cached token j iff j <= i + seq_lens[b] - Nq. A sequence of length 0, and any
  * row with no legal key, gives O = 0 and LSE = -inf.
+ * Precision: the products run on exact operands but for the probabilities,
+ * which are rounded to fp16 (2^-12 to 2^-11 of each; for FFPA_FP16 with
+ * Hq / Hkv * Nq <= 4, to 22 bits). Sums, the softmax and O up to its final
+ * rounding are fp32.
  *   q, o: [B, Hq, Nq, D] views (o may be q's own); lse: contiguous fp32 [B, Hq, Nq].
  *   workspace: device scratch of at least ffpa_decode_kv4_workspace_bytes()
  *   bytes, 256-byte aligned, sized on the current device; one call at a time

@@ -401,6 +401,38 @@ def test_decode_a_row_that_is_not_finite_stays_alone():
     assert torch.isnan(o2[0, 3, 1]).all() and not torch.isfinite(o2[1, 0, 0]).any()
 
 
+@pytest.mark.parametrize("G,Nq", [(1, 1), (3, 1), (4, 1), (2, 2)])
+@pytest.mark.parametrize("D,n", [(64, 32), (128, 47), (320, 64), (512, 32), (1024, 34)])
+def test_decode_of_up_to_four_rows_in_fp16_rounds_its_output_alone(G, Nq, D, n):
+    """P in 22 bits, where values cancel: |O| is far below A = sum P |V| / l, so 11 bits of P would show.
+
+    P is fp16 and an fp16 remainder: 2^-22 of itself, or 2^-25 where the remainder is subnormal, next to a largest P
+    of at least 2^6 (n 2^-31 max|V|). The rest is as at the top of this file."""
+    rng = np.random.default_rng(D + n + G)
+    page, Hkv, B = 16, 2, 2
+    lens = [n, n]
+    table, pages = block_tables(lens, page, rng)
+    signs = np.where(np.arange(n) % 2, 1.0, -1.0)
+    v = np.stack([rng.permutation(signs) for _ in range(B * Hkv * D)]).reshape(B, Hkv, D, n).transpose(0, 1, 3, 2)
+    k, v = dev(rng.standard_normal((B, Hkv, n, D)), FP16), dev(v, FP16)
+    q = dev(0.1 * rng.standard_normal((B, Hkv * G, Nq, D)), FP16)
+    cache, t, ln = api.kv4_cache(pages, page, Hkv, D), dev(table), dev(np.array(lens, np.int32))
+    api.kv4_write(cache, t, k, v)
+    rk, rv = api.kv4_read(cache, t, ln, max_count=n, dtype=FP16)
+    o, lse = api.decode_fwd_kv4(q, cache, t, ln)
+    api.get_status()
+    check_attention(q, rk, rv, lens, False, None, o, lse)
+    want, _ = oracle.attention_fwd(q.cpu(), rk.cpu(), rv.cpu(), False, 1 / math.sqrt(D))
+    mean, _ = oracle.attention_fwd(q.cpu(), rk.cpu(), rv.abs().cpu(), False, 1 / math.sqrt(D))
+    qa = np.abs(f64(q)).reshape(B, Hkv, G * Nq, D)
+    m = np.einsum("bhrd,bhjd->bhrj", qa, np.abs(f64(rk))).max(-1).reshape(B, Hkv * G, Nq, 1) / math.sqrt(D)
+    e_s = (D / 16 + 8) * 2.0 ** -23 * m
+    tol = torch.finfo(FP16).eps / 2 * np.abs(want) + n * 2.0 ** -31 * float(rv.abs().max()) + \
+        (2.0 ** -22 + (n / 16 + 64) * 2.0 ** -23 + 2 * e_s) * mean
+    off = np.abs(f64(o) - want) / tol
+    assert off.max() <= 1, off.max()
+
+
 def test_decode_strided_views_and_shared_pages():
     rng = np.random.default_rng(2)
     B, Hkv, G, Nq, D, page = 3, 2, 4, 2, 256, 32
