@@ -522,9 +522,14 @@ def _in_view(x):
     """(tensor, its ffpa_view) of an input, copied only where no view of it fits."""
     w = _view_or_none(x)
     if w is None:
-        x = x.contiguous()
+        x = x.clone(memory_format=torch.contiguous_format)  # what is contiguous may begin off 16 bytes
         w = _view(x)
     return x, w
+
+
+def _in_packed(x):
+    """A packed input, copied only where it is not contiguous from 16 bytes on."""
+    return x if x.is_contiguous() and not x.data_ptr() & 15 else x.clone(memory_format=torch.contiguous_format)
 
 
 def _out_view(x):
@@ -569,7 +574,7 @@ def varlen_kv4_write(cache, block_table, k, v, cu_seqlens, max_seqlen: int, star
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return varlen_kv4_write(cache, block_table, k, v, cu_seqlens, max_seqlen, start)
-    k, v = k.contiguous(), v.contiguous()
+    k, v = _in_packed(k), _in_packed(v)
     st = _ffi.load().ffpa_varlen_kv4_write(_dt(k), k.data_ptr(), v.data_ptr(), c,
                                            _lengths(cu_seqlens, B + 1, "cu_seqlens", dev),
                                            _lengths(start, B, "start", dev), B, T, int(max_seqlen), Hkv, D,

@@ -119,6 +119,31 @@ def test_rows_on_sixteen_and_on_thirty_two_bytes(first, pitch):
     assert np.array_equal(cache.cpu().numpy(), ref)
 
 
+@pytest.mark.parametrize("off", [1, 4, 8])
+def test_inputs_that_do_not_begin_on_sixteen_bytes_are_copied(off):
+    def at(shape):  # contiguous, 2 `off` bytes into an allocation
+        n = math.prod(shape)
+        return torch.randn(n + off, device="cuda").to(BF16)[off:].view(shape)
+
+    Hkv, D, page, lens = 2, 128, 16, [20, 3]
+    cu = torch.tensor([0, 20, 23], dtype=torch.int32, device="cuda")
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    k, v, q = at((23, Hkv, D)), at((23, Hkv, D)), at((2, 4, 1, D))
+    kd, vd = at((2, Hkv, 20, D)), at((2, Hkv, 20, D))
+    calls = [lambda c, k, v: api.varlen_kv4_write(c, table, k, v, cu, 20), lambda c, k, v: api.kv4_write(c, table, k, v)]
+    for call, x, y in zip(calls, (k, kd), (v, vd)):
+        got, want = (api.kv4_cache(4, page, Hkv, D) for _ in range(2))
+        call(got, x, y)
+        call(want, x.clone(), y.clone())
+        api.get_status()
+        assert torch.equal(got, want)
+    o, lse = api.decode_fwd_kv4(q, got, table, ln)
+    want, want_l = api.decode_fwd_kv4(q.clone(), got, table, ln)
+    api.get_status()
+    assert torch.equal(o, want) and torch.equal(lse, want_l)
+
+
 @pytest.mark.parametrize("start", [None, (3, 0, 50, 17)])
 def test_packed_write_matches_the_reference(start):
     rng = np.random.default_rng(5)
