@@ -36,3 +36,10 @@ def test_packed_inputs(off):
     t = at((7, 4, 64), off)[:, 1:3]   # heads of a wider tensor
     y = api._in_packed(t)
     assert torch.equal(t, y) and y.is_contiguous() and y.data_ptr() % 16 == 0
+
+
+def test_the_package_uses_public_names_of_torch():
+    import pathlib
+
+    for f in pathlib.Path(api.__file__).parent.glob("*.py"):
+        assert "torch._C" not in f.read_text(), f.name
