@@ -642,7 +642,7 @@ def _kv4_workspace_bytes(device: int, dt: int, B: int, Hq: int, Hkv: int, Nq: in
 
 
 def decode_kv4_workspace(q, cache) -> torch.Tensor:
-    """Device scratch for decode_fwd_kv4 (uint8, 256-byte aligned by the allocator)."""
+    """Device scratch for decode_fwd_kv4 (uint8, 256-byte aligned by the allocator), for one call at a time."""
     B, Hq, Nq, D = q.shape
     n = _kv4_workspace_bytes(q.device.index, _dt(q), B, Hq, cache.shape[2], Nq, D)
     return torch.empty(n, dtype=torch.uint8, device=q.device)

@@ -43,3 +43,11 @@ def test_the_package_uses_public_names_of_torch():
 
     for f in pathlib.Path(api.__file__).parent.glob("*.py"):
         assert "torch._C" not in f.read_text(), f.name
+
+
+def test_the_decode_workspace_is_in_the_package():
+    import head_dim_flash_gb300 as ffpa
+
+    assert ffpa.decode_kv4_workspace is api.decode_kv4_workspace and "decode_kv4_workspace" in ffpa.__all__
+    for name in ffpa.__all__:
+        assert hasattr(ffpa, name)
