@@ -313,6 +313,15 @@ def test_decode_head_dims(D):
     decode_case([129], 1, 3, 4, D, 16, True, BF16, seed=D + 1)
 
 
+@pytest.mark.parametrize("D", [768, 960])
+def test_decode_head_dims_of_twelve_and_fifteen_chunks(D):
+    # eight and sixteen rows, across parts and pages
+    decode_case([300, 77], 2, 4, 1, D, 32, False, FP16, seed=D)
+    decode_case([129], 1, 3, 4, D, 16, True, BF16, seed=D + 1)
+    decode_case([1500, 17, 0, 790], 2, 8, 1, D, 48, False, BF16, seed=D + 2)
+    decode_case([1500, 17, 0, 790], 1, 5, 3, D, 112, True, FP16, seed=D + 3)
+
+
 @pytest.mark.parametrize("G,Nq", [(1, 1), (3, 1), (8, 1), (16, 1), (32, 1), (4, 2), (4, 4), (5, 7), (1, 40), (16, 4)])
 @pytest.mark.parametrize("causal", [False, True])
 def test_decode_groups_and_rows(G, Nq, causal):

@@ -59,6 +59,26 @@ def test_scales_by_hand(amax, scale):
     assert v[3] == -6 * scale or amax < 1
 
 
+@pytest.mark.parametrize("amax,value", [
+    (6 * 2.0 ** -17, 6 * 2.0 ** -17),
+    (3 * 2.0 ** -17, 0.0),              # a scale that ties with zero
+    (3.1 * 2.0 ** -17, 3 * 2.0 ** -17),     # level 3, the nearest to 3.1 scales
+    (5 * 2.0 ** -17, 4 * 2.0 ** -17),       # a tie between levels 4 and 6, to the even code
+    (5.1 * 2.0 ** -17, 6 * 2.0 ** -17),
+    (9 * 2.0 ** -17, 8 * 2.0 ** -17),       # 1.5 steps, a tie, to two: 4.5 scales, level 4
+    (6 * 7 * 2.0 ** -17, 42 * 2.0 ** -17),
+    (6 * 2.0 ** -14, 6 * 2.0 ** -14),
+    (0.75, 0.75),
+    (0.0, 0.0),
+])
+def test_largest_values_of_small_groups_by_hand(amax, value):
+    for sign in (1, -1):
+        x = np.zeros(16)
+        x[3] = sign * amax
+        v = kv4.dequantize(*kv4.quantize(x))
+        assert v[3] == sign * value and not v[:3].any() and not v[4:].any()
+
+
 def test_not_a_number_counts_as_zero():
     x = np.linspace(-1, 1, 16)
     y = x.copy()
