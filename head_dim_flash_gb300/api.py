@@ -542,6 +542,10 @@ def _elsewhere(device) -> bool:
     return device.index != torch.cuda.current_device()
 
 
+def _raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def kv4_write(cache, block_table, k, v, start=None, count=None) -> None:
     """Quantises new tokens into the cache through ffpa_kv4_write (views, no copy):
     row i of sequence b becomes cached token start[b] + i, for i < count[b].
@@ -556,7 +560,7 @@ def kv4_write(cache, block_table, k, v, start=None, count=None) -> None:
             return kv4_write(cache, block_table, k, v, start, count)
     (k, wk), (v, wv) = _in_view(k), _in_view(v)
     st = _ffi.load().ffpa_kv4_write(_dt(k), wk, wv, c, _lengths(start, B, "start", dev),
-                                    _lengths(count, B, "count", dev), B, Hkv, N, D, _stream())
+                                    _lengths(count, B, "count", dev), B, Hkv, N, D, _raw_stream(dev))
     if st:
         _ffi.raise_for(st, "ffpa_kv4_write")
 
@@ -574,7 +578,7 @@ def varlen_kv4_write(cache, block_table, k, v, cu_seqlens, max_seqlen: int, star
     st = _ffi.load().ffpa_varlen_kv4_write(_dt(k), k.data_ptr(), v.data_ptr(), c,
                                            _lengths(cu_seqlens, B + 1, "cu_seqlens", dev),
                                            _lengths(start, B, "start", dev), B, T, int(max_seqlen), Hkv, D,
-                                           _stream())
+                                           _raw_stream(dev))
     if st:
         _ffi.raise_for(st, "ffpa_varlen_kv4_write")
 
@@ -602,7 +606,7 @@ def kv4_read(cache, block_table, count, max_count: int | None = None, dtype=torc
             return kv4_read(cache, block_table, count, start=start, k_out=k_out, v_out=v_out)
     st = _ffi.load().ffpa_kv4_read(_dt(k_out), c, _out_view(k_out), _out_view(v_out),
                                    _lengths(start, B, "start", dev), _lengths(count, B, "count", dev), B, Hkv,
-                                   shape[2], D, _stream())
+                                   shape[2], D, _raw_stream(dev))
     if st:
         _ffi.raise_for(st, "ffpa_kv4_read")
     return k_out, v_out
@@ -628,7 +632,7 @@ def varlen_kv4_read(cache, block_table, cu_seqlens, max_seqlen: int, total: int 
     st = _ffi.load().ffpa_varlen_kv4_read(_dt(k_out), c, k_out.data_ptr(), v_out.data_ptr(),
                                           _lengths(cu_seqlens, B + 1, "cu_seqlens", dev),
                                           _lengths(start, B, "start", dev), B, T, int(max_seqlen), Hkv, D,
-                                          _stream())
+                                          _raw_stream(dev))
     if st:
         _ffi.raise_for(st, "ffpa_varlen_kv4_read")
     return k_out, v_out
@@ -694,7 +698,7 @@ def decode_fwd_kv4(q, cache, block_table, seq_lens, causal: bool = False, scale:
         n = workspace.numel() * workspace.element_size()
     st = _ffi.load().ffpa_decode_fwd_kv4(dt, wq, c, _lengths(seq_lens, B, "seq_lens", dev), wo, lse.data_ptr(),
                                          workspace.data_ptr(), n, B, Hq, Hkv, Nq, D, int(bool(causal)),
-                                         _scale(scale, D), _stream())
+                                         _scale(scale, D), _raw_stream(dev))
     if st:
         _ffi.raise_for(st, "ffpa_decode_fwd_kv4")
     return out, lse
