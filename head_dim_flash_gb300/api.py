@@ -542,8 +542,16 @@ def _elsewhere(device) -> bool:
     return device.index != torch.cuda.current_device()
 
 
+# Not a public name of torch, but a tenth of torch.cuda.current_stream's time (0.1 us against 1.1; a written token 22.5
+# against 26.3): that one takes its place in a torch without it.
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    """The current stream of a device."""
+    if _raw_stream_of is None:
+        return torch.cuda.current_stream(device.index).cuda_stream
+    return _raw_stream_of(device.index)
 
 
 def kv4_write(cache, block_table, k, v, start=None, count=None) -> None:

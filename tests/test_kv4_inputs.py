@@ -44,3 +44,15 @@ def test_the_decode_workspace_is_in_the_package():
     assert ffpa.decode_kv4_workspace is api.decode_kv4_workspace and "decode_kv4_workspace" in ffpa.__all__
     for name in ffpa.__all__:
         assert hasattr(ffpa, name)
+
+
+def test_the_current_stream_without_torchs_private_name(monkeypatch):
+    import importlib.util
+    import types
+
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: types.SimpleNamespace(cuda_stream=100 + device))
+    spec = importlib.util.spec_from_file_location("head_dim_flash_gb300.api_again", api.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    assert again._raw_stream(torch.device("cuda", 3)) == 103
