@@ -542,8 +542,8 @@ def _elsewhere(device) -> bool:
     return device.index != torch.cuda.current_device()
 
 
-# Not a public name of torch, but a tenth of torch.cuda.current_stream's time (0.1 us against 1.1; a written token 22.5
-# against 26.3): that one takes its place in a torch without it.
+# Not a public name of torch, but a tenth of torch.cuda.current_stream's time (0.1 us against 1.1; a token written and
+# read back 22.5 against 26.3): that one takes its place in a torch without it.
 _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -713,5 +713,6 @@ def decode_fwd_kv4(q, cache, block_table, seq_lens, causal: bool = False, scale:
 
 
 def get_status() -> None:
-    """Synchronises the current stream and raises if a kernel reported a device time-out."""
+    """Synchronises the current stream and raises if a kernel reported a device time-out, a packed
+    sequence that breaks the varlen contract, or one whose lengths or pages lie outside its 4-bit cache."""
     _ffi.raise_for(_ffi.ffpa_get_status(_stream()), "device status")

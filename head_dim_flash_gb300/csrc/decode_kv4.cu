@@ -22,7 +22,8 @@
 //     computed once and its scores are never exchanged; for the values it takes
 //     one or two 64-wide head-dim chunks over all strips, so O^T stays in
 //     registers. Between the two, P goes through shared memory as ready operands.
-//     A step has two barriers: after its scores (P is there) and after its values.
+//     A step has two barriers: after its scores (P is there) and after its values; two more where the softmax's
+//     reference moves, as in a unit's first step.
 //   - one warp of the group loads the K of the next step after the first barrier,
 //     another its V after the second: each copy has the other half of a step to
 //     arrive, so one place for K and one for V are enough. A lane copies the part
@@ -51,14 +52,15 @@
 //
 // Measured on a GB300 (a copy runs at 6.77 TB/s), calls in a row, the cache not
 // in the L2: 8 sequences of 16384 tokens, 8 kv heads, 4 query heads each,
-// D = 512 (604 MB): 105 us, 5.8 TB/s; one sequence of 131000 tokens: 102 us.
-// Bound by memory: 90 us of it are the steps, 7 us pass before the first one is
-// worked on, 4 us after the last one in the second kernel. Sixteen rows per
-// head: 147 us for 600 MB at D = 512; 74 instructions and eight matrix products
-// a tile, whose conversions (the ALU 44% busy), matrix unit (43%) and issue
-// slots (54%) three or four warps per scheduler cannot overlap further. Short
-// calls are those 11 us and their steps: one sequence of 2000 tokens 12.5 us; 64
-// sequences of 20 to 1000 tokens, 16 heads of D = 128 (69 MB), 26 us.
+// D = 512 (604 MB): 105 us, 5.8 TB/s; one sequence of 131000 tokens: 103 us.
+// Bound by memory: 6 us pass until a group has its first keys, 96 are the steps
+// (the last group is done 3 us after the median one), 3 the second kernel.
+// Sixteen rows per head: 144 us for 600 MB at D = 512; 74 instructions and eight
+// matrix products a tile, whose conversions (the ALU 44% busy), matrix unit (43%)
+// and issue slots (54%) three or four warps per scheduler cannot overlap further.
+// Short calls are mostly their start and end: one sequence of 2000 tokens takes
+// 12.9 us, 4 until the first keys, 3 of steps, 6 for the second kernel and the
+// launches; 64 sequences of 20 to 1000 tokens, 16 heads of D = 128 (69 MB), 26 us.
 #include <atomic>
 
 #include "kv4.cuh"
@@ -90,15 +92,30 @@ struct Kv4Geo {
 // Shape of a CTA for N head-dim chunks and NB blocks of eight query rows.
 // CH: two chunks of O^T per warp need the fewest exchanges and barriers, but one
 // halves its registers (16 warps for sixteen rows) and saves the chunk that two
-// warps of an odd N both compute. Eight rows, two against one (151 MB of cache):
-// 46.5 and 41.8 us at N = 3, 38.8 and 41.1 at N = 8. Sixteen rows (75 MB, and
-// 600 MB): 40.7 and 34.6 at N = 2, 33.3 and 32.8 (157, 138) at N = 6, 36.3 and
-// 34.5 (166, 162) at N = 7, 34.3 and 32.7 (159, 147) at N = 8; but 31.5 and 32.8
-// (151, 147) at N = 5, whose 15 warps take long steps, and 37.8 and 40.3 (177,
-// 176) at N = 9, where one chunk leaves nine warps.
+// warps of an odd N both compute. Two against one, us, at 76 and 605 MB of cache:
+//   eight rows    N = 2: 26.7, 26.5 and 110, 131   N = 3: 27.5, 25.3 and 124, 118
+//     N = 4: 25.4, 25.7 and 103, 106   N = 5: 26.2, 26.3 and 113, 108
+//     N = 6: 25.0, 25.5 and 114, 103   N = 7: 26.2, 26.8 and 114, 120
+//     N = 8: 25.7, 25.9 and 105, 108   N = 9: 27.2, 30.6 and 110, 127
+//     N = 10: 27.2, 28.9 and 105, 128   N = 11: 27.9, 30.3 and 108, 120
+//     N = 12: 27.6, 28.9 and 105, 111   N = 13: 31.0, 32.3 and 132, 127
+//   sixteen rows  N = 2: 33.8, 31.9 and 153, 159   N = 3: 36.8, 32.8 and 172, 150
+//     N = 4: 34.1, 33.2 and 146, 140   N = 5: 36.4, 37.9 and 148, 144
+//     N = 6: 37.1, 36.6 and 155, 136   N = 7: 41.3, 40.4 and 163, 160
+//     N = 8: 39.5, 39.4 and 156, 144   N = 9: 46.0, 47.2 and 176, 174
+//     N = 10: 45.0, 44.1 and 167, 167   N = 11: 46.9, 46.1 and 154, 157
+//     N = 12: 46.9, 46.3 and 149, 146
+// So one for N = 3 with eight rows and N <= 8 with sixteen, but not N = 5 there;
+// two elsewhere. Where the sizes disagree this is the smaller cache's side, and
+// leaves 3 to 4% of large caches at N = 2 (sixteen rows) and 5, 9% at N = 6 (eight
+// rows). N = 5 with sixteen rows, further: 23.9, 21.8 at 20 MB, 52.0, 53.0 at 152,
+// 84.3, 83.8 at 303; 42.0, 43.9 over 16 contexts of 1 to 8000 tokens (102 MB), which
+// end more often inside a step of one chunk's ten strips than of two chunks' six.
+// From N = 14 on (13 with sixteen rows) a step with one chunk per warp does not fit.
 // NG: as many groups as registers hold, 128 per thread where O^T takes 32 of
 // them and 168 where it takes 64 (16 warps there spill: 155 -> 184 us at N = 5,
-// 600 MB). SW: steps as long as shared memory then allows, from eight strips per
+// 600 MB; the kept shapes spill 4 to 60 bytes: sixteen rows but for N = 6 and N >=
+// 13, eight rows at N <= 2). SW: steps as long as shared memory then allows, from eight strips per
 // warp in groups of one warp (142 -> 121 us at N = 1 against four, 600 MB) or
 // two in others.
 struct Shape {

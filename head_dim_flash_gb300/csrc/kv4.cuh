@@ -57,7 +57,7 @@ __device__ __forceinline__ size_t kv4_strip_offset(const Kv4Cache& c, int Hkv, i
     return (((static_cast<size_t>(page) * 2 + kv) * Hkv + h) * strips + strip) * (static_cast<size_t>(chunks) * kKv4Tile);
 }
 
-// One byte of codes -> two fp16 values (low nibble in the low half).
+// Four bytes of codes -> four fp16 pairs, a byte's low nibble in the low half.
 __device__ __forceinline__ void kv4_decode8(uint32_t w, uint32_t (&h)[4])
 {
     asm("{\n"
