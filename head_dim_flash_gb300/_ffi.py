@@ -41,6 +41,13 @@ EXPORTS = (
     "ffpa_varlen_kv4_read",
     "ffpa_decode_kv4_workspace_bytes",
     "ffpa_decode_fwd_kv4",
+    "ffpa_rope",
+    "ffpa_varlen_rope",
+    "ffpa_decode_shared_workspace_bytes",
+    "ffpa_decode_fwd_shared",
+    "ffpa_decode_weights_workspace_bytes",
+    "ffpa_decode_fwd_weights",
+    "ffpa_kv_evict",
     "ffpa_bwd_stages",
     "ffpa_bwd_noalloc",
     "ffpa_varlen_fwd",
@@ -77,6 +84,13 @@ class Kv4Cache(ctypes.Structure):
 
     _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
                 ("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int), ("block_stride", ctypes.c_int64)]
+
+
+class RopePlan(ctypes.Structure):
+    """``ffpa_rope_plan``: turns per position of each pair of a head's rotated dims."""
+
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("mscale", ctypes.c_float)]
 
 
 def _declare(lib):
@@ -124,6 +138,22 @@ def _declare(lib):
     lib.ffpa_decode_kv4_workspace_bytes.restype = _sz
     lib.ffpa_decode_fwd_kv4.argtypes = [_i, View, Kv4Cache, _p, View, _p, _p, _sz, _i, _i, _i, _i, _i, _i, _f, _p]
     lib.ffpa_decode_fwd_kv4.restype = _i
+    lib.ffpa_rope.argtypes = [_i, View, View, View, View, RopePlan, _p, _p, _i, _i, _i, _i, _i, _i, _p]
+    lib.ffpa_rope.restype = _i
+    lib.ffpa_varlen_rope.argtypes = [_i, _p, _p, _p, _p, RopePlan, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p]
+    lib.ffpa_varlen_rope.restype = _i
+    lib.ffpa_decode_shared_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i, _i]
+    lib.ffpa_decode_shared_workspace_bytes.restype = _sz
+    lib.ffpa_decode_fwd_shared.argtypes = [_i, View, View, View, View, View, _p, View, _p, _p, _sz, _i, _i, _i, _i, _i,
+                                           _i, _i, _i, _f, _p]
+    lib.ffpa_decode_fwd_shared.restype = _i
+    lib.ffpa_decode_weights_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i]
+    lib.ffpa_decode_weights_workspace_bytes.restype = _sz
+    lib.ffpa_decode_fwd_weights.argtypes = [_i, View, View, View, _p, _p, _p, View, _p, _p, _sz, _i, _i, _i, _i, _i, _i,
+                                            _i, _f, _p]
+    lib.ffpa_decode_fwd_weights.restype = _i
+    lib.ffpa_kv_evict.argtypes = [_i, View, View, _p, _p, View, View, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _p]
+    lib.ffpa_kv_evict.restype = _i
     lib.ffpa_bwd_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i]
     lib.ffpa_bwd_workspace_bytes.restype = _sz
     lib.ffpa_bwd.argtypes = [_i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _i, _i, _i, _i, _i, _i, _i, _f, _p]
@@ -280,6 +310,34 @@ def ffpa_decode_kv4_workspace_bytes(*args):
 
 def ffpa_decode_fwd_kv4(*args):
     return load().ffpa_decode_fwd_kv4(*args)
+
+
+def ffpa_rope(*args):
+    return load().ffpa_rope(*args)
+
+
+def ffpa_varlen_rope(*args):
+    return load().ffpa_varlen_rope(*args)
+
+
+def ffpa_decode_shared_workspace_bytes(*args):
+    return load().ffpa_decode_shared_workspace_bytes(*args)
+
+
+def ffpa_decode_fwd_shared(*args):
+    return load().ffpa_decode_fwd_shared(*args)
+
+
+def ffpa_decode_weights_workspace_bytes(*args):
+    return load().ffpa_decode_weights_workspace_bytes(*args)
+
+
+def ffpa_decode_fwd_weights(*args):
+    return load().ffpa_decode_fwd_weights(*args)
+
+
+def ffpa_kv_evict(*args):
+    return load().ffpa_kv_evict(*args)
 
 
 def ffpa_bwd_workspace_bytes(*args):

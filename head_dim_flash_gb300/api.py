@@ -313,11 +313,23 @@ class _Attention(torch.autograd.Function):
         return dq, dk, dv, None, None
 
 
-def attention(q, k, v, causal: bool = False, scale: float | None = None, return_lse: bool = False):
+def attention(q, k, v, causal: bool = False, scale: float | None = None, return_lse: bool = False, rope=None):
     """O = softmax(scale * Q K^T [bottom-right causal]) V, differentiable w.r.t. q, k, v.
 
     The gradient of the returned LSE is not propagated (it is an auxiliary output).
+    rope (a plan of rope_plan()): q and k are turned first, key j at position j and query i
+    at i + Nkv - Nq, as the causal mask aligns them.
     """
+    if rope is not None:
+        if q.dim() != 4 or k.dim() != 4:
+            raise ValueError("expected q [B,Hq,Nq,D], k and v [B,Hkv,Nkv,D]")
+        ahead = k.shape[2] - q.shape[2]
+        if ahead == 0:
+            q, k = _rope_apply(q, k, rope)
+        else:
+            start = torch.full((q.shape[0],), ahead, dtype=torch.int32, device=q.device)
+            q, _ = _rope_apply(q, None, rope, start=start)
+            k, _ = _rope_apply(k, None, rope)
     o, lse = _Attention.apply(q, k, v, bool(causal), scale)
     return (o, lse) if return_lse else o
 
@@ -431,14 +443,22 @@ class _VarlenAttention(torch.autograd.Function):
 
 
 def varlen_attention(q, k, v, cu_seqlens_q, cu_seqlens_k=None, max_seqlen_q=None, max_seqlen_k=None,
-                     causal: bool = False, scale: float | None = None, return_lse: bool = False):
+                     causal: bool = False, scale: float | None = None, return_lse: bool = False, rope=None):
     """Packed-THD attention (FFPA docs, "CuTe-DSL Backend" page, "Varlen (packed THD) API").
 
     cu_seqlens_k=None means cu_seqlens_k = cu_seqlens_q. When max_seqlen_* is
     None it is read from cu_seqlens (one device-to-host copy).
+    rope (a plan of rope_plan()): as in attention(), per sequence.
     """
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
+    if rope is not None:
+        rq, rk = _cu(cu_seqlens_q, q.device), _cu(cu_seqlens_k, q.device)
+        if cu_seqlens_k is cu_seqlens_q:
+            q, k = varlen_rope(q, k, rope, rq)
+        else:
+            q, _ = varlen_rope(q, None, rope, rq, start=rk.diff() - rq.diff())
+            k, _ = varlen_rope(k, None, rope, rk)
     if max_seqlen_q is None:
         max_seqlen_q = int((cu_seqlens_q[1:] - cu_seqlens_q[:-1]).max().item()) if cu_seqlens_q.numel() > 1 else 0
     if max_seqlen_k is None:
@@ -712,7 +732,398 @@ def decode_fwd_kv4(q, cache, block_table, seq_lens, causal: bool = False, scale:
     return out, lse
 
 
+# ----------------------------------------------------------------- rotary positions
+class RopePlan:
+    """Rotary positions of rope_plan(): the frequencies on one device, the pairs and the factor."""
+
+    __slots__ = ("turns", "rot_dim", "interleaved", "mscale", "_c")
+
+    def __init__(self, turns: torch.Tensor, interleaved: bool, mscale: float):
+        self.turns, self.rot_dim = turns, 2 * turns.numel()
+        self.interleaved, self.mscale = bool(interleaved), float(mscale)
+        self._c = _ffi.RopePlan(turns.data_ptr(), self.rot_dim, int(self.interleaved), self.mscale)
+
+
+def rope_plan(rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+              factor: float = 1.0, original_len: int | None = None, inv_freq=None, mscale: float | None = None,
+              device="cuda") -> RopePlan:
+    """A plan for rope(), varlen_rope(), attention(rope=) and varlen_attention(rope=).
+
+    Pair p of the first rot_dim head dims turns by theta_p = base^(-2p / rot_dim) radians per
+    position; pairs are (p, p + rot_dim / 2), or (2p, 2p + 1) when interleaved. For contexts
+    `factor` times as long as trained:
+      "linear"  theta / factor;
+      "ntk"     base * factor^(rot_dim / (rot_dim - 2));
+      "yarn"    by parts (Peng et al. 2023): pairs that turn at least 32 times within
+                original_len positions keep theta, those that turn at most once take
+                theta / factor, in between linearly; values are multiplied by 0.1 ln(factor) + 1.
+    inv_freq (64-bit radians per position, rot_dim / 2 of them) and mscale replace what these give."""
+    if rot_dim < 16 or rot_dim % 16 != 0:
+        raise NotImplementedError(f"rot_dim {rot_dim}: a positive multiple of 16")
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError(f'scaling {scaling!r}: "none", "linear", "ntk" or "yarn"')
+    if not (base > 0 and factor > 0):
+        raise ValueError("base and factor must be positive")
+    m = 1.0
+    if inv_freq is None:
+        p = torch.arange(rot_dim // 2, dtype=torch.float64)
+        if scaling == "ntk":
+            base = base * factor ** (rot_dim / (rot_dim - 2))
+        theta = base ** (-2.0 * p / rot_dim)
+        if scaling == "linear":
+            theta = theta / factor
+        elif scaling == "yarn":
+            if original_len is None or original_len <= 0:
+                raise ValueError('scaling "yarn" needs original_len')
+            keep = ((original_len * theta / (2 * math.pi) - 1) / 31).clamp(0, 1)
+            theta = theta * keep + theta / factor * (1 - keep)
+            m = 0.1 * math.log(factor) + 1 if factor > 1 else 1.0
+    else:
+        theta = torch.as_tensor(inv_freq, dtype=torch.float64).detach().cpu().reshape(-1)
+        if theta.numel() != rot_dim // 2 or not bool(torch.isfinite(theta).all()):
+            raise ValueError(f"inv_freq must hold {rot_dim // 2} finite values")
+    m = m if mscale is None else float(mscale)
+    if not math.isfinite(m):
+        raise ValueError("mscale must be finite")
+    # turns per position as a 64-bit fraction; whole turns do not count
+    turns = [round(t * 2 ** 64) % 2 ** 64 for t in (theta / (2 * math.pi)).tolist()]
+    turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64)
+    return RopePlan(turns.to(device), interleaved, m)
+
+
+def _rope_positions(start, positions, B: int, shape, dev):
+    if start is not None and positions is not None:
+        raise ValueError("give start or positions, not both")
+    if positions is not None:
+        if positions.dtype is not torch.int32 or positions.shape != shape or not positions.is_contiguous() \
+                or positions.device != dev:
+            raise ValueError(f"positions must be a contiguous int32 {list(shape)} tensor on {dev}")
+        return None, positions.data_ptr()
+    return _lengths(start, B, "start", dev), None
+
+
+_NO_VIEW = _ffi.View(None, 0, 0, 0)
+
+
+def _rope_out(x, out, name: str):
+    if out is None:
+        out = torch.empty_like(x)
+        w = _view_or_none(out)
+        if w is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            w = _view(out)
+        return out, w
+    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+        raise ValueError(f"{name} must have its input's shape, dtype and device")
+    return out, _out_view(out)
+
+
+def _rope_pair(q, k, plan: RopePlan, dims: int):
+    """Shared checks; returns the device."""
+    dev = q.device
+    if dev.type != "cuda" or plan.turns.device != dev:
+        raise ValueError("q and the plan must be on one CUDA device")
+    if q.dim() != dims:
+        raise ValueError("expected q [B,Hq,N,D]" if dims == 4 else "expected q [T,Hq,D]")
+    if k is not None:
+        if k.dim() != dims or k.shape[-1] != q.shape[-1] or k.shape[0] != q.shape[0] or \
+                dims == 4 and k.shape[2] != q.shape[2]:
+            raise ValueError(f"k {tuple(k.shape)} does not match q {tuple(q.shape)}")
+        if k.device != dev:
+            raise ValueError("q and k are on different devices")
+        if k.dtype != q.dtype:
+            raise ValueError(f"mixed dtypes {q.dtype} and {k.dtype}")
+    return dev
+
+
+def _rope_dense(q, k, plan, start, positions, inverse, q_out=None, k_out=None):
+    dev = _rope_pair(q, k, plan, 4)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return _rope_dense(q, k, plan, start, positions, inverse, q_out, k_out)
+    B, Hq, N, D = q.shape
+    ps, pp = _rope_positions(start, positions, B, (B, N), dev)
+    q, wq = _in_view(q)
+    q_out, woq = _rope_out(q, q_out, "q_out")
+    Hk, wk, wok = 0, _NO_VIEW, _NO_VIEW
+    if k is not None:
+        Hk = k.shape[1]
+        k, wk = _in_view(k)
+        k_out, wok = _rope_out(k, k_out, "k_out")
+    st = _ffi.load().ffpa_rope(_dt(q), wq, wk, woq, wok, plan._c, ps, pp, B, Hq, Hk, N, D, inverse, _raw_stream(dev))
+    if st:
+        _ffi.raise_for(st, "ffpa_rope")
+    return q_out, k_out
+
+
+def _rope_packed(q, k, plan, cu, start, positions, inverse, q_out=None, k_out=None):
+    dev = _rope_pair(q, k, plan, 3)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return _rope_packed(q, k, plan, cu, start, positions, inverse, q_out, k_out)
+    T, Hq, D = q.shape
+    B = cu.numel() - 1
+    ps, pp = _rope_positions(start, positions, B, (T,), dev)
+    Hk, pk, pok = 0, None, None
+    outs = []
+    for x, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if x is None:
+            continue
+        if out is None:
+            # rows of no sequence are not written
+            out = torch.zeros(x.shape, dtype=x.dtype, device=dev) if inverse else torch.empty(x.shape, dtype=x.dtype, device=dev)
+        elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
+            raise ValueError(f"{name} must be contiguous, with its input's shape, dtype and device")
+        outs.append(out)
+    q = _in_packed(q)
+    if k is not None:
+        Hk, k = k.shape[1], _in_packed(k)
+        pk, pok = k.data_ptr(), outs[1].data_ptr()
+    st = _ffi.load().ffpa_varlen_rope(_dt(q), q.data_ptr(), pk, outs[0].data_ptr(), pok, plan._c,
+                                      _lengths(cu, B + 1, "cu_seqlens", dev), ps, pp, B, T, Hq, Hk, D, inverse,
+                                      _raw_stream(dev))
+    if st:
+        _ffi.raise_for(st, "ffpa_varlen_rope")
+    return outs[0], outs[1] if k is not None else None
+
+
+class _Rope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, plan, cu, start, positions):
+        ctx.save_for_backward(cu, start, positions)
+        ctx.plan = plan
+        if cu is None:
+            return _rope_dense(q, k, plan, start, positions, 0)
+        return _rope_packed(q, k, plan, cu, start, positions, 0)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        cu, start, positions = ctx.saved_tensors
+        if cu is None:
+            dq, dk = _rope_dense(dq, dk, ctx.plan, start, positions, 1)
+        else:
+            dq, dk = _rope_packed(dq, dk, ctx.plan, cu, start, positions, 1)
+        return dq, dk, None, None, None, None
+
+
+def _needs_grad(q, k) -> bool:
+    return torch.is_grad_enabled() and (q.requires_grad or k is not None and k.requires_grad)
+
+
+def rope(q, k, plan: RopePlan, start=None, positions=None, q_out=None, k_out=None):
+    """Rotary positions on q [B, Hq, N, D] and k [B, Hkv, N, D] (or None) through ffpa_rope
+    (views, no copy), differentiable. Token i of sequence b is at positions[b, i], or at
+    start[b] + i (int32 on the device; neither: i). q_out and k_out may be q and k.
+    Returns (q, k) rotated."""
+    if _needs_grad(q, k):
+        if q_out is not None or k_out is not None:
+            raise ValueError("q_out and k_out are for inputs that need no gradient")
+        return _Rope.apply(q, k, plan, None, start, positions)
+    return _rope_dense(q, k, plan, start, positions, 0, q_out, k_out)
+
+
+_rope_apply = rope  # attention() has a parameter of that name
+
+
+def varlen_rope(q, k, plan: RopePlan, cu_seqlens, start=None, positions=None, q_out=None, k_out=None):
+    """As rope, for a packed batch: q [T, Hq, D], k [T, Hkv, D] (or None), sequence b's tokens the
+    rows [cu_seqlens[b], cu_seqlens[b + 1]) (int32 on the device); positions: int32 [T]. Rows of no
+    sequence are not written; their gradient is zero."""
+    if _needs_grad(q, k):
+        if q_out is not None or k_out is not None:
+            raise ValueError("q_out and k_out are for inputs that need no gradient")
+        return _Rope.apply(q, k, plan, cu_seqlens, start, positions)
+    return _rope_packed(q, k, plan, cu_seqlens, start, positions, 0, q_out, k_out)
+
+
+# ----------------------------------------------------------------- decode over caches of different lengths
+@functools.lru_cache(maxsize=256)
+def _shared_workspace_bytes(device: int, dt: int, *sizes: int) -> int:
+    """ffpa_decode_shared_workspace_bytes, which depends on its arguments and the device's SMs alone."""
+    with torch.cuda.device(device):
+        return max(256, int(_ffi.load().ffpa_decode_shared_workspace_bytes(dt, *sizes)))
+
+
+@functools.lru_cache(maxsize=256)
+def _weights_workspace_bytes(device: int, dt: int, *sizes: int) -> int:
+    """ffpa_decode_weights_workspace_bytes, which depends on its arguments and the device's SMs alone."""
+    with torch.cuda.device(device):
+        return max(256, int(_ffi.load().ffpa_decode_weights_workspace_bytes(dt, *sizes)))
+
+
+def decode_shared_workspace(q, k_prefix, k) -> torch.Tensor:
+    """Device scratch for decode_fwd_shared (uint8, 256-byte aligned by the allocator), for one call at a time."""
+    B, Hq, Nq, D = q.shape
+    n = _shared_workspace_bytes(q.device.index, _dt(q), B, Hq, k.shape[1], Nq, k_prefix.shape[2], k.shape[2], D)
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def decode_weights_workspace(q, k) -> torch.Tensor:
+    """Device scratch for decode_fwd_weights (uint8, 256-byte aligned by the allocator), for one call at a time."""
+    B, Hq, Nq, D = q.shape
+    n = _weights_workspace_bytes(q.device.index, _dt(q), B, Hq, k.shape[1], Nq, k.shape[2], D)
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def _line_checks(q, *caches):
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("expected q [B,Hq,Nq,D]")
+    dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    for k, v, batch in caches:
+        ks = k.shape
+        if len(ks) != 4 or v.shape != ks or ks[0] != batch or ks[3] != shape[3] or ks[1] != caches[-1][0].shape[1]:
+            raise ValueError(f"k {tuple(ks)} and v {tuple(v.shape)} do not match q {tuple(shape)}")
+        if k.device != dev or v.device != dev:
+            raise ValueError("q, k and v must be on one device")
+        if k.dtype != dt or v.dtype != dt:
+            raise ValueError(f"mixed dtypes {dt}, {k.dtype} and {v.dtype}")
+    return shape, dev
+
+
+def _line_outputs(q, shape, dev, out, lse, workspace, workspace_bytes):
+    if out is None:
+        out = torch.empty_like(q)
+        wo = _view_or_none(out)
+        if wo is None:
+            out = torch.empty(shape, dtype=q.dtype, device=dev)
+            wo = _view(out)
+    elif out.shape != shape or out.dtype != q.dtype or out.device != dev:
+        raise ValueError("out must have q's shape, dtype and device")
+    else:
+        wo = _out_view(out)
+    if lse is None:
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
+    elif not lse.is_contiguous() or lse.dtype != torch.float32 or lse.shape != shape[:3] or lse.device != dev:
+        raise ValueError("lse must be a contiguous fp32 [B, Hq, Nq] tensor")
+    if workspace is None:
+        workspace = torch.empty(workspace_bytes, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on q's device")
+    else:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    return out, wo, lse, workspace, workspace_bytes
+
+
+def decode_fwd_shared(q, k_prefix, v_prefix, k, v, lens=None, causal: bool = False, scale: float | None = None,
+                      out=None, lse=None, workspace=None):
+    """Decode / short-query forward of a batch that shares a prefix, through ffpa_decode_fwd_shared:
+    the keys of sequence b are the prefix (k_prefix, v_prefix [1, Hkv, Np, D]), then the first
+    lens[b] rows of its own cache (k, v [B, Hkv, N, D]; int32 [B] on the device, None: N each);
+    causal is bottom-right over all of them. The prefix is read once for the batch.
+    q [B, Hq, Nq, D]; returns (o, lse)."""
+    shape, dev = _line_checks(q, (k_prefix, v_prefix, 1), (k, v, q.shape[0]))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return decode_fwd_shared(q, k_prefix, v_prefix, k, v, lens, causal, scale, out, lse, workspace)
+    B, Hq, Nq, D = shape
+    Hkv, N, Np = k.shape[1], k.shape[2], k_prefix.shape[2]
+    dt = _dt(q)
+    q, wq = _in_view(q)
+    (kp, wkp), (vp, wvp), (k, wk), (v, wv) = _in_view(k_prefix), _in_view(v_prefix), _in_view(k), _in_view(v)
+    need = 0 if workspace is not None else _shared_workspace_bytes(dev.index, dt, B, Hq, Hkv, Nq, Np, N, D)
+    out, wo, lse, workspace, n = _line_outputs(q, shape, dev, out, lse, workspace, need)
+    st = _ffi.load().ffpa_decode_fwd_shared(dt, wq, wkp, wvp, wk, wv, _lengths(lens, B, "lens", dev), wo,
+                                            lse.data_ptr(), workspace.data_ptr(), n, B, Hq, Hkv, Nq, Np, N, D,
+                                            int(bool(causal)), _scale(scale, D), _raw_stream(dev))
+    if st:
+        _ffi.raise_for(st, "ffpa_decode_fwd_shared")
+    return out, lse
+
+
+def _weights_ptr(x, shape, name: str, dev) -> int:
+    if x.dtype is not torch.float32 or x.shape != shape or not x.is_contiguous() or x.device != dev:
+        raise ValueError(f"{name} must be a contiguous fp32 {list(shape)} tensor on {dev}, got {x.dtype} "
+                         f"{tuple(x.shape)} on {x.device}")
+    return x.data_ptr()
+
+
+def decode_fwd_weights(q, k, v, weights, lens=None, causal: bool = False, scale: float | None = None, out=None,
+                       lse=None, weights_out=None, workspace=None):
+    """Decode / short-query forward that scores its cache, through ffpa_decode_fwd_weights: the keys
+    of sequence b are the first lens[b] rows of k, v [B, Hkv, N, D] (int32 [B] on the device, None:
+    N each), and the softmax weight that each gets from the rows of its kv head is added to
+    weights [B, Hkv, N] (fp32), in place or into weights_out. q [B, Hq, Nq, D]; returns
+    (o, lse, weights_out)."""
+    shape, dev = _line_checks(q, (k, v, q.shape[0]))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return decode_fwd_weights(q, k, v, weights, lens, causal, scale, out, lse, weights_out, workspace)
+    B, Hq, Nq, D = shape
+    Hkv, N = k.shape[1], k.shape[2]
+    dt = _dt(q)
+    if weights_out is None:
+        weights_out = weights
+    pw = _weights_ptr(weights, (B, Hkv, N), "weights", dev)
+    po = _weights_ptr(weights_out, (B, Hkv, N), "weights_out", dev)
+    q, wq = _in_view(q)
+    (k, wk), (v, wv) = _in_view(k), _in_view(v)
+    need = 0 if workspace is not None else _weights_workspace_bytes(dev.index, dt, B, Hq, Hkv, Nq, N, D)
+    out, wo, lse, workspace, n = _line_outputs(q, shape, dev, out, lse, workspace, need)
+    st = _ffi.load().ffpa_decode_fwd_weights(dt, wq, wk, wv, _lengths(lens, B, "lens", dev), pw, po, wo,
+                                             lse.data_ptr(), workspace.data_ptr(), n, B, Hq, Hkv, Nq, N, D,
+                                             int(bool(causal)), _scale(scale, D), _raw_stream(dev))
+    if st:
+        _ffi.raise_for(st, "ffpa_decode_fwd_weights")
+    return out, lse, weights_out
+
+
+def kv_evict(k, v, weights, lens, keep: int, recent: int = 0, k_out=None, v_out=None, weights_out=None,
+             lens_out=None):
+    """Cuts each kv head's cache k, v [B, Hkv, N, D] to `keep` tokens through ffpa_kv_evict: the
+    last `recent` of the lens[b] tokens and, of the others, those with the largest weights
+    [B, Hkv, N] (fp32; of equal ones the earlier), in their order. In place, or into k_out and
+    v_out [B, Hkv, N_out, D], weights_out [B, Hkv, N_out] and lens_out; rows behind the kept
+    ones are left as they are. Returns (k_out, v_out, weights_out, lens_out, kept), kept int32
+    [B, Hkv, keep]: where each token was, -1 behind the last."""
+    shape, dev = k.shape, k.device
+    if len(shape) != 4 or v.shape != shape:
+        raise ValueError("expected k and v [B,Hkv,N,D]")
+    if dev.type != "cuda" or v.device != dev:
+        raise ValueError("k and v must be on one CUDA device")
+    if v.dtype != k.dtype:
+        raise ValueError(f"mixed dtypes {k.dtype} and {v.dtype}")
+    if (k_out is None) != (v_out is None) or (k_out is None) != (weights_out is None):
+        raise ValueError("give k_out, v_out and weights_out together, or none of them")
+    if lens is None:
+        raise ValueError("lens is required")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kv_evict(k, v, weights, lens, keep, recent, k_out, v_out, weights_out, lens_out)
+    B, Hkv, N, D = shape
+    if k_out is None:
+        k_out, v_out, weights_out = k, v, weights
+        wk, wv = _out_view(k), _out_view(v)  # in place: no copy would do
+        wok, wov, Nout = wk, wv, N
+        if lens_out is None:
+            lens_out = lens
+    else:
+        Nout = k_out.shape[2] if k_out.dim() == 4 else -1
+        for x, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if x.shape != (B, Hkv, Nout, D) or x.dtype != k.dtype or x.device != dev:
+                raise ValueError(f"{name} must be [B, Hkv, N_out, D] of k's dtype on k's device")
+        k, wk = _in_view(k)
+        v, wv = _in_view(v)
+        wok, wov = _out_view(k_out), _out_view(v_out)
+        if lens_out is None:
+            lens_out = torch.empty_like(lens)
+    pw = _weights_ptr(weights, (B, Hkv, N), "weights", dev)
+    po = _weights_ptr(weights_out, (B, Hkv, Nout), "weights_out", dev)
+    if keep < 1:
+        raise ValueError(f"keep={keep} must be positive")
+    kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev)
+    st = _ffi.load().ffpa_kv_evict(_dt(k), wk, wv, pw, _lengths(lens, B, "lens", dev), wok, wov, po,
+                                   _lengths(lens_out, B, "lens_out", dev), kept.data_ptr(), B, Hkv, N, Nout, D,
+                                   int(keep), int(recent), _raw_stream(dev))
+    if st:
+        _ffi.raise_for(st, "ffpa_kv_evict")
+    return k_out, v_out, weights_out, lens_out, kept
+
+
 def get_status() -> None:
     """Synchronises the current stream and raises if a kernel reported a device time-out, a packed
-    sequence that breaks the varlen contract, or one whose lengths or pages lie outside its 4-bit cache."""
+    sequence that breaks the varlen contract, one whose lengths or pages lie outside its 4-bit cache, or one whose
+    length lies outside its cache."""
     _ffi.raise_for(_ffi.ffpa_get_status(_stream()), "device status")

@@ -9,6 +9,7 @@
 #include <string>
 
 #include "../../include/ffpa.h"
+#include "cache_ops.h"
 #include "kernels.h"
 #include "kv4.h"
 #include "ptx.cuh"
@@ -766,6 +767,259 @@ ffpa_status ffpa_decode_fwd_kv4(ffpa_dtype dt, ffpa_view q, ffpa_kv4_cache cache
                          "4-bit decode launch");
 }
 
+}  // extern "C"
+
+// ------------------------------------------------ rotary positions, cache operators
+namespace {
+
+ffpa_status run_rope(ffpa_dtype dt, const ffpa_view& q, const ffpa_view& k, const ffpa_view& q_out,
+                     const ffpa_view& k_out, const ffpa_rope_plan& plan, const int* start, const int* positions,
+                     const int* cu, int B, int total, int Hq, int Hkv, int N, int D, int inverse, ffpa_stream_t stream)
+{
+    FFPA_TRY(check_common(dt, 0, 0, D, 1.f));
+    if (B < 0 || N < 0 || total < 0 || Hq < 0 || Hkv < 0)
+        return fail(FFPA_ERR_INVALID_VALUE, "negative size B=%d N=%d total=%d Hq=%d Hkv=%d", B, N, total, Hq, Hkv);
+    if (plan.rot_dim < 16 || plan.rot_dim > D || plan.rot_dim % 16 != 0)
+        return fail(FFPA_ERR_NOT_SUPPORTED, "rot_dim=%d must be a multiple of 16 in [16, D=%d]", plan.rot_dim, D);
+    if (!std::isfinite(plan.mscale)) return fail(FFPA_ERR_INVALID_VALUE, "mscale must be finite");
+    if (static_cast<long long>(Hq) + Hkv > INT_MAX / 64)
+        return fail(FFPA_ERR_NOT_SUPPORTED, "Hq + Hkv = %lld heads exceed %d", static_cast<long long>(Hq) + Hkv, INT_MAX / 64);
+    const long long tokens = cu ? total : static_cast<long long>(B) * N;
+    if (tokens > INT_MAX) return fail(FFPA_ERR_NOT_SUPPORTED, "%lld tokens exceed 2^31 - 1", tokens);
+    const bool any = tokens > 0 && B > 0 && Hq + Hkv > 0;
+    if (any && !plan.turns) return fail(FFPA_ERR_INVALID_VALUE, "the plan's turns are NULL");
+    if (reinterpret_cast<uintptr_t>(plan.turns) & 7u) return fail(FFPA_ERR_INVALID_VALUE, "turns must be 8-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(start) & 3u) || (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+        (reinterpret_cast<uintptr_t>(cu) & 3u))
+        return fail(FFPA_ERR_INVALID_VALUE, "start, positions and cu_seqlens must be 4-byte aligned");
+    if (start && positions) return fail(FFPA_ERR_INVALID_VALUE, "give start or positions, not both");
+    const int eb = cu ? 1 : B, en = cu ? total : N;
+    FFPA_TRY(check_view(q, any && Hq > 0, "q", eb, Hq, en));
+    FFPA_TRY(check_view(q_out, any && Hq > 0, "q_out", eb, Hq, en));
+    FFPA_TRY(check_view(k, any && Hkv > 0, "k", eb, Hkv, en));
+    FFPA_TRY(check_view(k_out, any && Hkv > 0, "k_out", eb, Hkv, en));
+    if (!any) return ok();
+    ffpa::DeviceCtl ctl;
+    FFPA_TRY(device_ctl(&ctl));
+    ffpa::RopeArgs a{};
+    a.bf16 = dt == FFPA_BF16;
+    a.q = q.data;
+    a.k = k.data;
+    a.oq = q_out.data;
+    a.ok = k_out.data;
+    a.vq = to_view(q);
+    a.vk = to_view(k);
+    a.voq = to_view(q_out);
+    a.vok = to_view(k_out);
+    a.turns = reinterpret_cast<const unsigned long long*>(plan.turns);
+    a.rot = plan.rot_dim;
+    a.interleaved = plan.interleaved != 0;
+    a.mscale = plan.mscale;
+    a.sign = inverse ? -1.f : 1.f;
+    a.start = start;
+    a.pos = positions;
+    a.cu = cu;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hk = Hkv;
+    a.N = N;
+    a.total = total;
+    a.D = D;
+    return launch_result(ffpa::launch_rope(a, reinterpret_cast<cudaStream_t>(stream)), "rotary launch");
+}
+
+// What the two decode forms over caches of different lengths have in common.
+ffpa_status check_line(ffpa_dtype dt, const ffpa_view& q, const ffpa_view& k, const ffpa_view& v, const int* lens,
+                       const ffpa_view& o, const float* lse, int B, int Hq, int Hkv, int Nq, int N, int D, int causal,
+                       float scale, bool shared, int Np, ffpa::LineArgs* a)
+{
+    FFPA_TRY(check_common(dt, Hq, Hkv, D, scale));
+    FFPA_TRY(check_dense_sizes(B, Hq, Nq, N));
+    if (D % 64 != 0) return fail(FFPA_ERR_NOT_SUPPORTED, "decode path: D=%d must be a multiple of 64", D);
+    if (Np < 0) return fail(FFPA_ERR_INVALID_VALUE, "negative prefix length %d", Np);
+    if (static_cast<long long>(Np) + N > INT_MAX)
+        return fail(FFPA_ERR_NOT_SUPPORTED, "prefix and cache hold %lld keys, above 2^31 - 1", static_cast<long long>(Np) + N);
+    const long q_rows = static_cast<long>(B) * Hq * Nq;
+    a->f.pb = dense_problem(B, Hq, Hkv, Nq, N, D, causal, scale);
+    if (q_rows > 0 && !ffpa::line_fits(a->f.pb, shared, Np))
+        return fail(FFPA_ERR_NOT_SUPPORTED, "B*Hq*Nq=%ld rows over N=%d keys exceed the launch's units", q_rows, N);
+    FFPA_TRY(check_view(q, q_rows > 0, "q", B, Hq, Nq));
+    FFPA_TRY(check_view(o, q_rows > 0, "o", B, Hq, Nq));
+    FFPA_TRY(check_view(k, q_rows > 0 && N > 0, "k", B, Hkv, N));
+    FFPA_TRY(check_view(v, q_rows > 0 && N > 0, "v", B, Hkv, N));
+    FFPA_TRY(check_ptr(lse, q_rows > 0, "lse"));
+    if (reinterpret_cast<uintptr_t>(lens) & 3u) return fail(FFPA_ERR_INVALID_VALUE, "lens must be 4-byte aligned");
+    a->f.pb.vq = to_view(q);
+    a->f.pb.vo = to_view(o);
+    a->f.pb.vk = to_view(k);
+    a->f.pb.vv = to_view(v);
+    a->f.bf16 = dt == FFPA_BF16;
+    a->f.q = q.data;
+    a->f.k = k.data;
+    a->f.v = v.data;
+    a->f.o = o.data;
+    a->f.lse = const_cast<float*>(lse);
+    a->lens = lens;
+    a->shared = shared;
+    a->Np = Np;
+    return FFPA_OK;
+}
+
+ffpa_status run_line(ffpa::LineArgs& a, void* workspace, size_t workspace_bytes, ffpa_stream_t stream)
+{
+    const size_t need = ffpa::line_workspace_bytes(a.f.pb, a.shared, a.Np);
+    if (workspace_bytes < need)
+        return fail(FFPA_ERR_INVALID_VALUE, "decode workspace too small: %zu < %zu bytes", workspace_bytes, need);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return fail(FFPA_ERR_INVALID_VALUE, "decode workspace must be non-NULL and 256-byte aligned");
+    FFPA_TRY(device_ctl(&a.f.ctl));
+    return launch_result(ffpa::launch_line(a, workspace, reinterpret_cast<cudaStream_t>(stream)), "decode launch");
+}
+
+// Workspace queries answer 0 for sizes outside the operation.
+bool line_sizes_ok(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int N, int D, int Np)
+{
+    return (dt == FFPA_BF16 || dt == FFPA_FP16) && B > 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && Nq > 0 && N >= 0 &&
+           Np >= 0 && D >= 64 && D <= 1024 && D % 64 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+ffpa_status ffpa_rope(ffpa_dtype dt, ffpa_view q, ffpa_view k, ffpa_view q_out, ffpa_view k_out, ffpa_rope_plan plan,
+                      const int* start, const int* positions, int B, int Hq, int Hkv, int N, int D, int inverse,
+                      ffpa_stream_t stream)
+{
+    return run_rope(dt, q, k, q_out, k_out, plan, start, positions, nullptr, B, 0, Hq, Hkv, N, D, inverse, stream);
+}
+
+ffpa_status ffpa_varlen_rope(ffpa_dtype dt, const void* q, const void* k, void* q_out, void* k_out,
+                             ffpa_rope_plan plan, const int* cu_seqlens, const int* start, const int* positions,
+                             int batch, int total, int Hq, int Hkv, int D, int inverse, ffpa_stream_t stream)
+{
+    if (!cu_seqlens) return fail(FFPA_ERR_INVALID_VALUE, "cu_seqlens is NULL");
+    const int hq = Hq > 0 ? Hq : 1, hk = Hkv > 0 ? Hkv : 1;
+    return run_rope(dt, packed_rows(const_cast<void*>(q), hq, D), packed_rows(const_cast<void*>(k), hk, D),
+                    packed_rows(q_out, hq, D), packed_rows(k_out, hk, D), plan, start, positions, cu_seqlens, batch,
+                    total, Hq, Hkv, total, D, inverse, stream);
+}
+
+size_t ffpa_decode_shared_workspace_bytes(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int Np, int N, int D)
+{
+    if (!line_sizes_ok(dt, B, Hq, Hkv, Nq, N, D, Np)) return 0;
+    const ffpa::Problem pb = dense_problem(B, Hq, Hkv, Nq, N, D, 0, 1.f);
+    return ffpa::line_fits(pb, true, Np) ? ffpa::line_workspace_bytes(pb, true, Np) : 0;
+}
+
+ffpa_status ffpa_decode_fwd_shared(ffpa_dtype dt, ffpa_view q, ffpa_view k_prefix, ffpa_view v_prefix, ffpa_view k,
+                                   ffpa_view v, const int* lens, ffpa_view o, float* lse, void* workspace,
+                                   size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int Np, int N, int D,
+                                   int causal, float scale, ffpa_stream_t stream)
+{
+    ffpa::LineArgs a{};
+    FFPA_TRY(check_line(dt, q, k, v, lens, o, lse, B, Hq, Hkv, Nq, N, D, causal, scale, true, Np, &a));
+    const long q_rows = static_cast<long>(B) * Hq * Nq;
+    FFPA_TRY(check_view(k_prefix, q_rows > 0 && Np > 0, "k_prefix", 1, Hkv, Np));
+    FFPA_TRY(check_view(v_prefix, q_rows > 0 && Np > 0, "v_prefix", 1, Hkv, Np));
+    if (q_rows == 0) return ok();
+    a.kp = k_prefix.data;
+    a.vp = v_prefix.data;
+    a.vkp = to_view(k_prefix);
+    a.vvp = to_view(v_prefix);
+    return run_line(a, workspace, workspace_bytes, stream);
+}
+
+size_t ffpa_decode_weights_workspace_bytes(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int N, int D)
+{
+    if (!line_sizes_ok(dt, B, Hq, Hkv, Nq, N, D, 0)) return 0;
+    const ffpa::Problem pb = dense_problem(B, Hq, Hkv, Nq, N, D, 0, 1.f);
+    return ffpa::line_fits(pb, false, 0) ? ffpa::line_workspace_bytes(pb, false, 0) : 0;
+}
+
+ffpa_status ffpa_decode_fwd_weights(ffpa_dtype dt, ffpa_view q, ffpa_view k, ffpa_view v, const int* lens,
+                                    const float* weights, float* weights_out, ffpa_view o, float* lse,
+                                    void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int N,
+                                    int D, int causal, float scale, ffpa_stream_t stream)
+{
+    ffpa::LineArgs a{};
+    FFPA_TRY(check_line(dt, q, k, v, lens, o, lse, B, Hq, Hkv, Nq, N, D, causal, scale, false, 0, &a));
+    const long q_rows = static_cast<long>(B) * Hq * Nq;
+    FFPA_TRY(check_ptr(weights, q_rows > 0 && N > 0, "weights"));
+    FFPA_TRY(check_ptr(weights_out, q_rows > 0 && N > 0, "weights_out"));
+    if (q_rows == 0) return ok();
+    a.weights = weights;
+    a.oweights = weights_out;
+    return run_line(a, workspace, workspace_bytes, stream);
+}
+
+ffpa_status ffpa_kv_evict(ffpa_dtype dt, ffpa_view k, ffpa_view v, const float* weights, const int* lens,
+                          ffpa_view k_out, ffpa_view v_out, float* weights_out, int* lens_out, int* kept, int B,
+                          int Hkv, int N, int N_out, int D, int keep, int recent, ffpa_stream_t stream)
+{
+    FFPA_TRY(check_common(dt, Hkv, Hkv, D, 1.f));
+    if (B < 0 || N < 0 || N_out < 0) return fail(FFPA_ERR_INVALID_VALUE, "negative size B=%d N=%d N_out=%d", B, N, N_out);
+    if (keep < 1 || recent < 0 || recent > keep)
+        return fail(FFPA_ERR_INVALID_VALUE, "keep=%d must be positive and recent=%d in [0, keep]", keep, recent);
+    if (N_out < (keep < N ? keep : N))
+        return fail(FFPA_ERR_INVALID_VALUE, "N_out=%d does not hold min(keep=%d, N=%d) tokens", N_out, keep, N);
+    if (static_cast<long long>(B) * Hkv > INT_MAX / 2)
+        return fail(FFPA_ERR_NOT_SUPPORTED, "B*Hkv=%lld exceeds %d", static_cast<long long>(B) * Hkv, INT_MAX / 2);
+    const bool any = B > 0 && Hkv > 0;
+    FFPA_TRY(check_view(k, any && N > 0, "k", B, Hkv, N));
+    FFPA_TRY(check_view(v, any && N > 0, "v", B, Hkv, N));
+    FFPA_TRY(check_view(k_out, any && N > 0, "k_out", B, Hkv, N_out));
+    FFPA_TRY(check_view(v_out, any && N > 0, "v_out", B, Hkv, N_out));
+    FFPA_TRY(check_ptr(weights, any && N > 0, "weights"));
+    FFPA_TRY(check_ptr(weights_out, any && N > 0, "weights_out"));
+    const void* ints[3] = {lens, lens_out, kept};
+    const char* names[3] = {"lens", "lens_out", "kept"};
+    for (int i = 0; i < 3; ++i) {
+        if (any && !ints[i]) return fail(FFPA_ERR_INVALID_VALUE, "%s is NULL", names[i]);
+        if (reinterpret_cast<uintptr_t>(ints[i]) & 3u)
+            return fail(FFPA_ERR_INVALID_VALUE, "%s must be 4-byte aligned", names[i]);
+    }
+    auto same = [](const ffpa_view& x, const ffpa_view& y) {
+        return x.data == y.data && x.stride_b == y.stride_b && x.stride_h == y.stride_h && x.stride_n == y.stride_n;
+    };
+    // in place is all of it in place: one tensor over another's storage would be read while it is written
+    const bool in_place = k.data == k_out.data;
+    if (any && N > 0) {
+        if (in_place != (v.data == v_out.data) || in_place != (weights == weights_out) || k.data == v_out.data ||
+            v.data == k_out.data)
+            return fail(FFPA_ERR_INVALID_VALUE, "k, v and weights are cut all in place or all into other tensors");
+        if (in_place && (!same(k, k_out) || !same(v, v_out) || N != N_out))
+            return fail(FFPA_ERR_INVALID_VALUE, "in place, the outputs must be the inputs' own views");
+    }
+    if (!any) return ok();
+    ffpa::DeviceCtl ctl;
+    FFPA_TRY(device_ctl(&ctl));
+    ffpa::EvictArgs a{};
+    a.k = k.data;
+    a.v = v.data;
+    a.ok = k_out.data;
+    a.ov = v_out.data;
+    a.vk = to_view(k);
+    a.vv = to_view(v);
+    a.vok = to_view(k_out);
+    a.vov = to_view(v_out);
+    a.weights = weights;
+    a.oweights = weights_out;
+    a.lens = lens;
+    a.olens = lens_out;
+    a.kept = kept;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.N = N;
+    a.Nout = N_out;
+    a.D = D;
+    a.keep = keep;
+    a.recent = recent;
+    a.in_place = in_place;
+    a.status = ctl.status;
+    return launch_result(ffpa::launch_evict(a, reinterpret_cast<cudaStream_t>(stream)), "eviction launch");
+}
+
 size_t ffpa_bwd_workspace_bytes_ds(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int Nkv, int D, int causal)
 {
     const size_t small = ffpa_bwd_workspace_bytes(dt, B, Hq, Hkv, Nq, Nkv, D);
@@ -927,6 +1181,11 @@ ffpa_status ffpa_get_status(ffpa_stream_t stream)
                     "4-bit cache: sequence %u breaks the contract of its lengths and block table (a negative length or "
                     "start, tokens past max_blocks * page_size or past the tensor's rows, or a page outside "
                     "[0, num_pages)); the outputs of that call are undefined for it (site 0x%02x)",
+                    word >> 16, site);
+    if ((word & 0xffu) == ffpa::DEV_INVALID && (site == ffpa::VS_LINE || site == ffpa::VS_EVICT))
+        return fail(FFPA_ERR_INVALID_VALUE,
+                    "cache: the length of sequence %u is negative or above the tokens that its cache holds; the outputs "
+                    "of that call are undefined (site 0x%02x)",
                     word >> 16, site);
     if ((word & 0xffu) == ffpa::DEV_INVALID)
         return fail(FFPA_ERR_INVALID_VALUE,

@@ -1,0 +1,929 @@
+// Decode forward over 16-bit caches of different lengths: beside a prefix that
+// the whole batch shares, or with every cached token's attention weight added
+// to its score.
+//
+// With few query rows the work is reading K and V once. The key tiles of all
+// units (sequence, kv head, block of rows) form one line, the shared prefix's
+// units at its front, and the line is cut into equal ranges, one per group of
+// warps: ragged lengths keep every SM busy to the end. The cut is made on the
+// device, from the lengths there. A range's first and last unit may reach
+// into its neighbours': such a piece leaves a normalised O (fp32) and the log2
+// of its sum in the workspace, and a second kernel joins them:
+//   L = log2 sum_s 2^L_s,  O = sum_s 2^(L_s - L) O_s.
+//
+// A group's warps own 64-wide head-dim chunks of K and V (two each above
+// D = 512). TMA brings tiles into the group's ring; scores S = Q K^T are partial
+// per warp (mma.m16n8k16 over its chunks) and summed through shared memory;
+// the online softmax is done by every warp alike; O += P V stays with the
+// chunks, in registers. The scores of tile t + 1 are issued before the values
+// of tile t. A slot is refilled by the group's first warp when all warps have
+// passed the barrier of the sum, so there is no producer warp. Head dims up to
+// 256 leave room for two to eight groups, which share nothing but the SM.
+//
+// The scoring form also stores the scores (fp32, log2 units: 4 bytes per row
+// and key beside 4 D of K and V), and the second kernel turns them into weights
+// with the joined sums: w_j = sum_r 2^(s_rj - L_r), added in the order of the
+// rows.
+//
+// Rows behind a sequence's length hold anything: their scores are replaced,
+// not multiplied, and their V rows are zeroed in shared memory.
+#include <cstring>
+
+#include "cache_ops.h"
+#include "kv4.cuh"
+
+namespace ffpa {
+namespace {
+
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr int kMaxStages = 8;
+constexpr int kMaxGroups = 8;
+constexpr int kLens = 1024;     // lengths staged in shared memory; longer batches read them from L2
+constexpr int kLineThreads = 256;
+constexpr int kJoinThreads = 256;
+
+enum LineSite : uint32_t { LS_FULL = 0x58, LS_DRAIN };
+
+struct LineGeo {
+    int kt, chunks, warps, groups, stages, stage_bytes;
+    int rows;            // query rows of a unit (16 or 32)
+    int R, rblocks;      // rows of a kv head's group, their blocks
+    int Rp, rblocks_p;   // the same for the shared prefix's units (rblocks_p = 0: not in the line)
+    int tiles_p;         // tiles of one prefix unit
+    long long ranges;    // groups of the whole grid
+    float *o_cut, *l_cut;      // [2 * ranges][rows][D], [2 * ranges][rows]
+    float *o_whole, *l_whole;  // [B * Hq * Nq][D] (shared), [B * Hq * Nq]: units inside one range
+    float *o_whole_p, *l_whole_p;  // [Hkv * Rp][D], [Hkv * Rp]
+    float* scores;       // [B * Hq * Nq][pitch]
+    int pitch;
+};
+
+struct __align__(1024) LineStatic {
+    uint64_t full[kMaxGroups][kMaxStages];
+    int abort_flag;
+};
+static_assert(sizeof(LineStatic) == 1024, "static shared block must be exactly 1 KiB");
+
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (BF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+// Length of sequence b; one outside its cache counts as 0 (and is recorded by stage_lens).
+__device__ __forceinline__ int clamp_len(const LineArgs& a, int b)
+{
+    const int n = a.lens ? a.lens[b] : a.f.pb.Nkv;
+    return n >= 0 && n <= a.f.pb.Nkv ? n : 0;
+}
+
+__device__ __forceinline__ int tiles_of(int keys, int kt) { return (keys + kt - 1) / kt; }
+
+// Tiles of the whole line, and those of the sequences before `b` (a warp's sum).
+__device__ __forceinline__ void line_sums(const LineArgs& a, const LineGeo& g, int b, long long& total,
+                                          long long& before)
+{
+    const Problem& pb = a.f.pb;
+    long long t = 0, p = 0;
+    for (int i = threadIdx.x & 31; i < pb.B; i += 32) {
+        const int n = tiles_of(clamp_len(a, i), g.kt);
+        t += n;
+        if (i < b) p += n;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        t += __shfl_xor_sync(0xffffffffu, t, d);
+        p += __shfl_xor_sync(0xffffffffu, p, d);
+    }
+    const long long per = static_cast<long long>(pb.Hkv) * g.rblocks;
+    const long long prefix = static_cast<long long>(pb.Hkv) * g.rblocks_p * g.tiles_p;
+    total = prefix + t * per;
+    before = prefix + p * per;
+}
+
+// Ranges that the line is cut into: no more than it has tiles, so that none is empty.
+__device__ __forceinline__ long long cuts(const LineGeo& g, long long total) { return min(g.ranges, total); }
+
+// A place in the line.
+struct Spot {
+    int b;        // sequence, -1: the shared prefix
+    int hk, rb;
+    int tile, tiles;
+    int keys;     // of the unit
+};
+
+struct Line {
+    const LineArgs& a;
+    const LineGeo& g;
+    const int* lens;  // staged, or null
+    __device__ int len(int b) const { return lens ? lens[b] : clamp_len(a, b); }
+    __device__ void enter(Spot& s) const  // the first unit with tiles at or behind sequence s.b
+    {
+        s.hk = s.rb = s.tile = 0;
+        s.tiles = 0;
+        while (s.b < a.f.pb.B) {
+            s.keys = len(s.b);
+            s.tiles = tiles_of(s.keys, g.kt);
+            if (s.tiles > 0) return;
+            ++s.b;
+        }
+    }
+    __device__ void next_unit(Spot& s) const
+    {
+        s.tile = 0;
+        if (++s.rb < (s.b < 0 ? g.rblocks_p : g.rblocks)) return;
+        s.rb = 0;
+        if (++s.hk < a.f.pb.Hkv) return;
+        s.hk = 0;
+        ++s.b;
+        enter(s);
+    }
+    // The place of tile t of the line (called by whole warps).
+    __device__ Spot find(long long t) const
+    {
+        Spot s{};
+        const int H = a.f.pb.Hkv;
+        const long long prefix = static_cast<long long>(H) * g.rblocks_p * g.tiles_p;
+        if (t < prefix) {
+            const int unit = static_cast<int>(t / g.tiles_p);
+            s.b = -1;
+            s.hk = unit / g.rblocks_p;
+            s.rb = unit % g.rblocks_p;
+            s.tile = static_cast<int>(t - static_cast<long long>(unit) * g.tiles_p);
+            s.tiles = g.tiles_p;
+            s.keys = a.Np;
+            return s;
+        }
+        t -= prefix;
+        const long long per = static_cast<long long>(H) * g.rblocks;
+        const int lane = threadIdx.x & 31;
+        long long run = 0;
+        s.b = a.f.pb.B;
+        for (int i0 = 0; i0 < a.f.pb.B; i0 += 32) {
+            const int n = i0 + lane < a.f.pb.B ? tiles_of(len(i0 + lane), g.kt) : 0;
+            long long incl = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += o;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, (run + incl) * per > t);
+            if (past) {
+                const int at = __ffs(past) - 1;
+                const long long first = __shfl_sync(0xffffffffu, (run + incl - n) * per, at);
+                s.b = i0 + at;
+                s.tiles = __shfl_sync(0xffffffffu, n, at);
+                const long long rest = t - first;
+                const int unit = static_cast<int>(rest / s.tiles);
+                s.tile = static_cast<int>(rest - static_cast<long long>(unit) * s.tiles);
+                s.hk = unit / g.rblocks;
+                s.rb = unit % g.rblocks;
+                s.keys = len(s.b);
+                return s;
+            }
+            run += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        return s;
+    }
+};
+
+// Row r of a unit: its (sequence, query head within the group, query).
+__device__ __forceinline__ void row_of(int r, int b, int Nq, int R, int& bb, int& gg, int& i)
+{
+    bb = b;
+    if (b < 0) {
+        bb = r / R;
+        r -= bb * R;
+    }
+    gg = r / Nq;
+    i = r - gg * Nq;
+}
+
+template <bool BF16, int MT, int CC, bool SCORE>
+__global__ void __launch_bounds__(kLineThreads, 1)
+    line_kernel(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CUtensorMap tV,
+                const __grid_constant__ CUtensorMap tKp, const __grid_constant__ CUtensorMap tVp, const LineArgs a,
+                const LineGeo g)
+{
+    pdl_wait();
+    pdl_trigger();
+    constexpr int KT = CC == 1 && MT == 1 ? 32 : 16;  // keys of a tile
+    constexpr int NT = KT / 8;
+    constexpr int ROWS = 16 * MT;
+    constexpr int SLOTS = MT * NT * 2;                // float2 a lane holds of a tile's scores
+    const Problem& pb = a.f.pb;
+    __shared__ LineStatic sh;
+    __shared__ int s_len[kLens];
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) atomicCAS(a.f.ctl.status, 0u, 5u | (0xffu << 8));
+        return;
+    }
+    if (threadIdx.x < g.groups * g.stages) mbar_init(&sh.full[threadIdx.x / g.stages][threadIdx.x % g.stages], 1);
+    if (threadIdx.x == 0) sh.abort_flag = 0;
+    if (a.lens)
+        for (int i = threadIdx.x; i < pb.B; i += blockDim.x) {
+            const int n = a.lens[i];
+            const bool good = n >= 0 && n <= pb.Nkv;
+            if (!good && blockIdx.x == 0)
+                atomicCAS(a.f.ctl.status, 0u, DEV_INVALID | (VS_LINE << 8) | ((static_cast<uint32_t>(i) & 0xffffu) << 16));
+            if (pb.B <= kLens) s_len[i] = good ? n : 0;
+        }
+    fence_barrier_init();
+    __syncthreads();
+    const int group = warp / g.warps, wg = warp - group * g.warps;
+    const Line line{a, g, a.lens && pb.B <= kLens ? s_len : nullptr};
+
+    // my group's range of the line
+    long long total, unused;
+    line_sums(a, g, 0, total, unused);
+    // (neighbouring ranges go to different SMs: a line of few tiles does not crowd a few of them)
+    const long long range = static_cast<long long>(group) * gridDim.x + blockIdx.x, ranges = cuts(g, total);
+    if (range >= ranges) return;  // no barrier below spans groups
+    const long long begin = total * range / ranges, end = total * (range + 1) / ranges;
+    const int n = static_cast<int>(end - begin);
+    Spot spot = line.find(begin);
+
+    uint8_t* const ring = smem + static_cast<size_t>(group) * g.stages * g.stage_bytes;
+    float2* const part = reinterpret_cast<float2*>(smem + static_cast<size_t>(g.groups) * g.stages * g.stage_bytes) +
+                         group * (g.warps > 1 ? (g.warps + 1) * SLOTS * 32 : 0);
+    float2* const fin = part + g.warps * SLOTS * 32;
+    uint64_t* const full = sh.full[group];
+    volatile int* abort_p = &sh.abort_flag;
+    uint32_t* status = a.f.ctl.status;
+    const uint64_t lim = a.f.ctl.limit_ns;
+    const int S = g.stages;
+    const uint32_t half_bytes = static_cast<uint32_t>(g.stage_bytes / 2);
+    auto sync_group = [&] {
+        if (g.warps > 1)
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(g.warps * 32) : "memory");
+        else
+            __syncwarp();
+    };
+
+    // -------------------------------------------------------------- loads
+    // lanes 0 (K) and 1 (V) of the group's first warp; both walk the line ahead of the products
+    Spot ahead = spot;
+    int issued = 0;
+    auto issue = [&] {
+        if (wg != 0 || issued >= n) return;
+        if (lane < 2) {
+            const int st = issued % S;
+            uint8_t* dst = ring + st * g.stage_bytes + lane * half_bytes;
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], g.stage_bytes);
+            const CUtensorMap* m = ahead.b < 0 ? (lane ? &tVp : &tKp) : (lane ? &tV : &tK);
+            tma_load_5d(dst, m, &full[st], 0, ahead.tile * KT, 0, ahead.hk, max(ahead.b, 0));
+        }
+        ++issued;
+        if (++ahead.tile == ahead.tiles) line.next_unit(ahead);
+    };
+    for (int i = 0; i < S; ++i) issue();
+
+    // ------------------------------------------------------------ products
+    const int my_chunks = CC == 1 ? 1 : (wg < g.chunks) + (wg + 8 < g.chunks);
+    const int r_lo = lane >> 2, cpair = (lane & 3) * 2;
+    const int R = g.R, G = pb.Hq / pb.Hkv;
+    uint32_t qa[CC][4][MT][4];
+    float o_acc[CC][8][MT][4];
+    float m_run[MT][2], l_run[MT][2], alpha[MT][2];
+    int jlim[MT][2];                // legal keys of the score rows: below this
+    uint32_t pa[MT][NT / 2][4];
+    float s[MT][NT][4];
+    bool ok = true;
+    Spot unit = spot;               // the unit whose scores are computed
+
+    auto unit_rows = [&](const Spot& u) { return (u.b < 0 ? g.Rp : R) - u.rb * ROWS; };
+    // queries and key limits of a unit
+    auto enter_unit = [&](const Spot& u) {
+        const int rows = unit_rows(u);
+        const int total_keys = u.b < 0 ? 0 : (a.shared ? a.Np : 0) + u.keys;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                const int r = mt * 16 + hi * 8 + r_lo;
+                jlim[mt][hi] = 0;
+                const uint16_t* q = nullptr;
+                if (r < rows) {
+                    int bb, gg, i;
+                    row_of(u.rb * ROWS + r, u.b, pb.Nq, R, bb, gg, i);
+                    q = static_cast<const uint16_t*>(a.f.q) + bb * pb.vq.sb + (u.hk * G + gg) * pb.vq.sh + i * pb.vq.sn;
+                    int lim_j = u.keys;
+                    if (pb.causal) {
+                        // keys of the row's whole sequence, then of this unit
+                        const int all = u.b < 0 ? a.Np + line.len(bb) : total_keys;
+                        const int first = u.b < 0 ? 0 : all - u.keys;
+                        lim_j = min(lim_j, all - pb.Nq + i + 1 - first);
+                    }
+                    jlim[mt][hi] = lim_j;
+                }
+#pragma unroll
+                for (int cc = 0; cc < CC; ++cc)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+                        for (int k8 = 0; k8 < 2; ++k8)
+                            qa[cc][ks][mt][hi + 2 * k8] =
+                                q && cc < my_chunks ? *reinterpret_cast<const uint32_t*>(
+                                                          q + (wg + 8 * cc) * 64 + ks * 16 + k8 * 8 + cpair)
+                                                    : 0u;
+            }
+    };
+    auto reset = [&] {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                m_run[mt][hi] = -INFINITY;
+                l_run[mt][hi] = 0.f;
+                alpha[mt][hi] = 1.f;
+            }
+#pragma unroll
+            for (int cc = 0; cc < CC; ++cc)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o_acc[cc][i][mt][e] = 0.f;
+        }
+    };
+    auto scores = [&](int t) {
+        const int st = t % S;
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (t / S) & 1, abort_p, status, lim, LS_FULL));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.f;
+        if (!ok) return;
+        const uint32_t kbase = smem_u32(ring + st * g.stage_bytes);
+#pragma unroll
+        for (int cc = 0; cc < CC; ++cc) {
+            if (cc >= my_chunks) break;
+            const uint32_t blk = kbase + (wg + 8 * cc) * KT * 128;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+                for (int np = 0; np < NT / 2; ++np) {
+                    uint32_t kb[4];
+                    const int krow = np * 16 + (lane & 7) + ((lane >> 4) << 3);
+                    ldsm4(blk + sw128_offset(krow, ks * 2 + ((lane >> 3) & 1)), kb);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma16816<BF16>(s[mt][np * 2], qa[cc][ks][mt], kb[0], kb[1]);
+                        mma16816<BF16>(s[mt][np * 2 + 1], qa[cc][ks][mt], kb[2], kb[3]);
+                    }
+                }
+        }
+    };
+    // the sum over the group's warps, the mask, and P and the factors of tile t (the unit `u`'s)
+    auto softmax = [&](int t, const Spot& u, int prev_stage) {
+        if (g.warps > 1) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    part[(wg * SLOTS + (mt * NT + i) * 2) * 32 + lane] = make_float2(s[mt][i][0], s[mt][i][1]);
+                    part[(wg * SLOTS + (mt * NT + i) * 2 + 1) * 32 + lane] = make_float2(s[mt][i][2], s[mt][i][3]);
+                }
+        }
+        sync_group();
+        // every warp has left the slot before: it is free
+        if (prev_stage >= 0 && ok) issue();
+        if (g.warps > 1) {
+            for (int sl = wg; sl < SLOTS; sl += g.warps) {
+                float2 acc = make_float2(0.f, 0.f);
+                for (int w = 0; w < g.warps; ++w) {
+                    const float2 p = part[(w * SLOTS + sl) * 32 + lane];
+                    acc.x += p.x;
+                    acc.y += p.y;
+                }
+                fin[sl * 32 + lane] = acc;
+            }
+            sync_group();
+        }
+        const float c2 = pb.scale_log2;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float x[NT][4];
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                float2 v[2] = {make_float2(s[mt][i][0], s[mt][i][1]), make_float2(s[mt][i][2], s[mt][i][3])};
+                if (g.warps > 1) {
+                    v[0] = fin[((mt * NT + i) * 2) * 32 + lane];
+                    v[1] = fin[((mt * NT + i) * 2 + 1) * 32 + lane];
+                }
+                const int j = u.tile * KT + i * 8 + cpair;
+#pragma unroll
+                for (int hi = 0; hi < 2; ++hi) {
+                    x[i][2 * hi] = j < jlim[mt][hi] ? v[hi].x * c2 : -INFINITY;
+                    x[i][2 * hi + 1] = j + 1 < jlim[mt][hi] ? v[hi].y * c2 : -INFINITY;
+                    top[hi] = fmaxf(top[hi], fmaxf(x[i][2 * hi], x[i][2 * hi + 1]));
+                }
+            }
+            if constexpr (SCORE) {
+                // one warp of the group stores the tile's scores, each in turn
+                if (wg == t % g.warps) {
+#pragma unroll
+                    for (int hi = 0; hi < 2; ++hi) {
+                        const int r = u.rb * ROWS + mt * 16 + hi * 8 + r_lo;
+                        if (r < R) {
+                            float* dst = g.scores +
+                                         ((static_cast<size_t>(u.b) * pb.Hkv + u.hk) * R + r) * g.pitch + u.tile * KT + cpair;
+#pragma unroll
+                            for (int i = 0; i < NT; ++i)
+                                if (u.tile * KT + i * 8 + cpair < u.keys)
+                                    *reinterpret_cast<float2*>(dst + i * 8) = make_float2(x[i][2 * hi], x[i][2 * hi + 1]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                float tm = top[hi];
+                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
+                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
+                const float mn = fmaxf(m_run[mt][hi], tm);
+                alpha[mt][hi] = mn == -INFINITY ? 1.f : ex2_approx(m_run[mt][hi] - mn);
+                m_run[mt][hi] = mn;
+                const float mu = mn == -INFINITY ? 0.f : mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const float p0 = ex2_approx(x[i][2 * hi] - mu), p1 = ex2_approx(x[i][2 * hi + 1] - mu);
+                    sum += p0 + p1;
+                    pa[mt][i >> 1][(i & 1) * 2 + hi] = pack2<BF16>(p0, p1);
+                }
+                l_run[mt][hi] = l_run[mt][hi] * alpha[mt][hi] + sum;
+            }
+        }
+    };
+    auto values = [&](int t, const Spot& u) {
+        const int st = t % S;
+        const uint32_t vbase = smem_u32(ring + st * g.stage_bytes) + half_bytes;
+        const int valid = u.keys - u.tile * KT;
+#pragma unroll
+        for (int cc = 0; cc < CC; ++cc) {
+            if (cc >= my_chunks) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    o_acc[cc][i][mt][0] *= alpha[mt][0];
+                    o_acc[cc][i][mt][1] *= alpha[mt][0];
+                    o_acc[cc][i][mt][2] *= alpha[mt][1];
+                    o_acc[cc][i][mt][3] *= alpha[mt][1];
+                }
+            if (!ok) continue;
+            const uint32_t blk = vbase + (wg + 8 * cc) * KT * 128;
+            if (valid < KT) {
+                // rows behind the last key: zero (what lies there may be NaN)
+                for (int e = valid * 8 + lane; e < KT * 8; e += 32)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(blk + e * 16), "r"(0) : "memory");
+                fence_proxy_async_smem();  // the slot is TMA's again after this tile
+                __syncwarp();
+            }
+#pragma unroll
+            for (int kp = 0; kp < NT / 2; ++kp)
+#pragma unroll
+                for (int np = 0; np < 4; ++np) {
+                    uint32_t vb[4];
+                    const int vrow = kp * 16 + (lane & 7) + (((lane >> 3) & 1) << 3);
+                    ldsm4_trans(blk + sw128_offset(vrow, np * 2 + (lane >> 4)), vb);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma16816<BF16>(o_acc[cc][np * 2][mt], pa[mt][kp], vb[0], vb[1]);
+                        mma16816<BF16>(o_acc[cc][np * 2 + 1][mt], pa[mt][kp], vb[2], vb[3]);
+                    }
+                }
+        }
+    };
+    // the piece of unit u that this range holds: its tiles [first, last)
+    auto finish = [&](const Spot& u, int first, int last) {
+        const bool whole = first == 0 && last == u.tiles;
+        const int rows = unit_rows(u);
+        const size_t cut = static_cast<size_t>(2 * range + (first == 0 ? 1 : 0)) * ROWS;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                float l = l_run[mt][hi];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                const int r = mt * 16 + hi * 8 + r_lo;
+                if (r >= rows) continue;
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float l2 = l > 0.f ? m_run[mt][hi] + log2f(l) : -INFINITY;
+                const int ur = u.rb * ROWS + r;  // row of the kv head's group
+                const size_t row = (static_cast<size_t>(max(u.b, 0)) * pb.Hkv + u.hk) * (u.b < 0 ? g.Rp : R) + ur;
+                float* dst = nullptr;
+                uint16_t* out = nullptr;
+                if (!whole) {
+                    dst = g.o_cut + (cut + r) * pb.D;
+                } else if (u.b < 0) {
+                    dst = g.o_whole_p + row * pb.D;
+                } else if (a.shared) {
+                    dst = g.o_whole + row * pb.D;
+                } else {
+                    int bb, gg, i;
+                    row_of(ur, u.b, pb.Nq, R, bb, gg, i);
+                    out = static_cast<uint16_t*>(a.f.o) + bb * pb.vo.sb + (u.hk * G + gg) * pb.vo.sh + i * pb.vo.sn;
+                }
+#pragma unroll
+                for (int cc = 0; cc < CC; ++cc) {
+                    if (cc >= my_chunks) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int col = (wg + 8 * cc) * 64 + i * 8 + cpair;
+                        const float v0 = o_acc[cc][i][mt][2 * hi] * inv, v1 = o_acc[cc][i][mt][2 * hi + 1] * inv;
+                        if (out)
+                            *reinterpret_cast<uint32_t*>(out + col) = pack2<BF16>(v0, v1);
+                        else
+                            *reinterpret_cast<float2*>(dst + col) = make_float2(v0, v1);
+                    }
+                }
+                if (wg == 0 && (lane & 3) == 0) {
+                    if (!whole)
+                        g.l_cut[cut + r] = l2;
+                    else if (u.b < 0)
+                        g.l_whole_p[row] = l2;
+                    else
+                        g.l_whole[row] = l2;
+                    if (out) a.f.lse[row] = l2 * kLn2;
+                }
+            }
+    };
+
+    reset();
+    enter_unit(unit);
+    int first = unit.tile;      // first tile of the unit in this range
+    scores(0);
+    softmax(0, unit, -1);
+    for (int t = 0; t < n; ++t) {
+        const Spot cur = unit;
+        const bool more = t + 1 < n;
+        bool fresh = false;
+        if (++unit.tile == unit.tiles) {
+            if (more) line.next_unit(unit);
+            fresh = more;
+        }
+        if (more) {
+            if (fresh) enter_unit(unit);
+            scores(t + 1);
+        }
+        values(t, cur);
+        if (fresh || !more) {
+            finish(cur, first, cur.tile + 1);
+            first = 0;
+            reset();
+        }
+        if (more) softmax(t + 1, unit, t % S);
+    }
+    // a range whose wait ran out leaves none of its copies in flight
+    if (!ok && wg == 0 && lane == 0) {
+        for (int t = max(0, issued - S); t < issued; ++t) {
+            int dummy = 0;
+            if (!mbar_wait(&full[t % S], (t / S) & 1, &dummy, status, lim, LS_DRAIN, false)) break;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ joining
+// The ranges that hold tiles [s0, s0 + tiles) of the line.
+__device__ __forceinline__ void unit_ranges(const LineGeo& g, long long total, long long s0, int tiles, long long& g0,
+                                            long long& g1, bool& whole)
+{
+    const long long ranges = cuts(g, total);
+    auto holds = [&](long long t) {
+        long long r = t * ranges / total;
+        while (r + 1 < ranges && total * (r + 1) / ranges <= t) ++r;
+        while (r > 0 && total * r / ranges > t) --r;
+        return r;
+    };
+    if (tiles <= 0) {
+        g0 = 0;
+        g1 = -1;
+        whole = false;
+        return;
+    }
+    g0 = holds(s0);
+    g1 = holds(s0 + tiles - 1);
+    whole = g0 == g1;
+}
+
+// Cut slot of range r for a unit that begins at tile s0: 1 where the unit begins inside the range.
+__device__ __forceinline__ long long cut_slot(const LineGeo& g, long long total, long long s0, long long r)
+{
+    return 2 * r + (s0 >= total * r / cuts(g, total) ? 1 : 0);
+}
+
+constexpr int kMaxPieces = 1280;  // of a row: the ranges of the grid (8 per SM) and one more
+
+// One CTA per query row; then, when scoring, CTAs that add the weights of kWeighKeys tokens of a kv head.
+constexpr int kWeighKeys = 1024;
+
+template <bool BF16, bool SCORE>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, const LineGeo g, const long long rows,
+                                                            const int key_blocks)
+{
+    pdl_wait();
+    pdl_trigger();
+    const Problem& pb = a.f.pb;
+    __shared__ float weight[kMaxPieces];
+    __shared__ float row_l[1024];
+    __shared__ float red[kJoinThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int R = g.R;
+    const long long cta = static_cast<long long>(blockIdx.x) + static_cast<long long>(gridDim.x) * blockIdx.y;
+    const bool is_row = cta < rows;
+    long long bh;  // (sequence, kv head)
+    int block = 0;
+    if (is_row) {
+        bh = cta / R;
+    } else {
+        if (!SCORE || cta >= rows + static_cast<long long>(pb.B) * pb.Hkv * key_blocks) return;
+        bh = (cta - rows) / key_blocks;
+        block = static_cast<int>((cta - rows) - bh * key_blocks);
+    }
+    const int b = static_cast<int>(bh / pb.Hkv), hk = static_cast<int>(bh - static_cast<long long>(b) * pb.Hkv);
+    const int len = clamp_len(a, b);
+    if (!is_row && block * kWeighKeys >= len) return;
+    long long total, before;
+    line_sums(a, g, b, total, before);
+    const int tiles = tiles_of(len, g.kt);
+    auto unit_start = [&](int rb) { return before + (static_cast<long long>(hk) * g.rblocks + rb) * tiles; };
+
+    if (is_row) {
+        const int r = static_cast<int>(cta - bh * R);
+        const int rb = r / g.rows, ur = r - rb * g.rows;
+        long long g0, g1, p0 = 0, p1 = -1;
+        bool whole, whole_p = false;
+        const long long s0 = unit_start(rb);
+        unit_ranges(g, total, s0, tiles, g0, g1, whole);
+        if (!a.shared && whole) return;  // written by the first kernel
+        const int rp = b * R + r, rbp = rp / g.rows, urp = rp - rbp * g.rows;
+        const long long s0p = (static_cast<long long>(hk) * g.rblocks_p + rbp) * g.tiles_p;
+        if (g.rblocks_p) unit_ranges(g, total, s0p, g.tiles_p, p0, p1, whole_p);
+        const int np = static_cast<int>(p1 - p0 + 1), no = static_cast<int>(g1 - g0 + 1);
+        const int pieces = np + no;
+        auto l_of = [&](int i) -> float {
+            if (i < np)
+                return whole_p ? g.l_whole_p[static_cast<size_t>(hk) * g.Rp + rp]
+                               : g.l_cut[cut_slot(g, total, s0p, p0 + i) * g.rows + urp];
+            return whole ? g.l_whole[bh * R + r] : g.l_cut[cut_slot(g, total, s0, g0 + i - np) * g.rows + ur];
+        };
+        auto o_of = [&](int i) -> const float* {
+            if (i < np)
+                return whole_p ? g.o_whole_p + (static_cast<size_t>(hk) * g.Rp + rp) * pb.D
+                               : g.o_cut + (cut_slot(g, total, s0p, p0 + i) * g.rows + urp) * pb.D;
+            return whole ? g.o_whole + (bh * R + r) * pb.D
+                         : g.o_cut + (cut_slot(g, total, s0, g0 + i - np) * g.rows + ur) * pb.D;
+        };
+        float mx = -INFINITY;
+        for (int i = tid; i < pieces; i += kJoinThreads) {
+            const float l = l_of(i);
+            weight[i] = l;
+            mx = fmaxf(mx, l);
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        if (lane == 0) red[warp] = mx;
+        __syncthreads();
+        mx = red[0];
+#pragma unroll
+        for (int w = 1; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, red[w]);
+        float sum = 0.f;
+        for (int i = 0; i < pieces; ++i) sum += mx == -INFINITY ? 0.f : exp2f(weight[i] - mx);
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const int gg = r / pb.Nq, i = r - gg * pb.Nq;
+        uint16_t* out = static_cast<uint16_t*>(a.f.o) + b * pb.vo.sb + (hk * (pb.Hq / pb.Hkv) + gg) * pb.vo.sh + i * pb.vo.sn;
+        for (int c = 2 * tid; c < pb.D; c += 2 * kJoinThreads) {
+            float v0 = 0.f, v1 = 0.f;
+            if (mx > -INFINITY) {
+#pragma unroll 4
+                for (int k = 0; k < pieces; ++k) {
+                    const float2 p = *reinterpret_cast<const float2*>(o_of(k) + c);
+                    const float w = exp2f(weight[k] - mx);
+                    v0 = fmaf(w, p.x, v0);
+                    v1 = fmaf(w, p.y, v1);
+                }
+            }
+            *reinterpret_cast<uint32_t*>(out + c) = pack2<BF16>(v0 * inv, v1 * inv);
+        }
+        if (tid == 0) a.f.lse[bh * R + r] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+        return;
+    }
+    if constexpr (SCORE) {
+        // the rows' log2 sums, a warp per row
+        const int batch = 1024;
+        float acc[kWeighKeys / kJoinThreads] = {};
+        const int j0 = block * kWeighKeys;
+        for (int rbase = 0; rbase < R; rbase += batch) {
+            const int nr = min(batch, R - rbase);
+            __syncthreads();
+            for (int q = warp; q < nr; q += kJoinThreads / 32) {
+                const int r = rbase + q;
+                const int rb = r / g.rows, ur = r - rb * g.rows;
+                long long g0, g1;
+                bool whole;
+                const long long s0 = unit_start(rb);
+                unit_ranges(g, total, s0, tiles, g0, g1, whole);
+                float l2;
+                if (whole) {
+                    l2 = g.l_whole[bh * R + r];
+                } else {
+                    float mx = -INFINITY;
+                    for (long long k = g0 + lane; k <= g1; k += 32)
+                        mx = fmaxf(mx, g.l_cut[cut_slot(g, total, s0, k) * g.rows + ur]);
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    float sum = 0.f;
+                    for (long long k = g0 + lane; k <= g1; k += 32)
+                        if (mx > -INFINITY) sum += exp2f(g.l_cut[cut_slot(g, total, s0, k) * g.rows + ur] - mx);
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                    l2 = sum > 0.f ? mx + log2f(sum) : -INFINITY;
+                }
+                // a row that saw no key adds nothing: all its scores are -inf
+                if (lane == 0) row_l[q] = l2 == -INFINITY ? 0.f : l2;
+            }
+            __syncthreads();
+            for (int q = 0; q < nr; ++q) {
+                const float* src = g.scores + (bh * R + rbase + q) * g.pitch + j0;
+                const float l2 = row_l[q];
+#pragma unroll
+                for (int k = 0; k < kWeighKeys / kJoinThreads; ++k) {
+                    const int j = k * kJoinThreads + tid;
+                    if (j0 + j < len) acc[k] += exp2f(src[j] - l2);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kWeighKeys / kJoinThreads; ++k) {
+            const int j = j0 + k * kJoinThreads + tid;
+            if (j < len) {
+                const size_t at = bh * pb.Nkv + j;
+                a.oweights[at] = a.weights[at] + acc[k];
+            }
+        }
+    }
+}
+
+struct LinePlan {
+    LineGeo g;
+    int ctas;
+    int smem;
+    size_t o_cut, l_cut, o_whole, l_whole, o_whole_p, l_whole_p, scores, total;  // byte offsets
+};
+
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+LinePlan line_plan(const Problem& pb, bool shared, int Np)
+{
+    LinePlan p{};
+    LineGeo& g = p.g;
+    g.chunks = pb.D / 64;
+    g.R = pb.Hq / pb.Hkv * pb.Nq;
+    g.Rp = pb.B * g.R;
+    const int most = shared ? max(g.R, g.Rp) : g.R;
+    const int mt = g.chunks > 8 || most <= 16 ? 1 : 2;
+    g.rows = 16 * mt;
+    g.rblocks = (g.R + g.rows - 1) / g.rows;
+    g.kt = g.chunks <= 8 && mt == 1 ? 32 : 16;
+    if (shared) {
+        g.rblocks_p = (g.Rp + g.rows - 1) / g.rows;
+        g.tiles_p = (Np + g.kt - 1) / g.kt;
+        if (g.tiles_p == 0) g.rblocks_p = 0;
+    }
+    g.warps = min(g.chunks, 8);
+    g.groups = 8 / g.warps;
+    g.stage_bytes = 2 * g.kt * g.chunks * 128;
+    const int slots = mt * g.kt / 8 * 2;
+    const int exchange = g.warps > 1 ? g.groups * (g.warps + 1) * slots * 256 : 0;
+    const int budget = kMaxSmem - static_cast<int>(sizeof(LineStatic)) - kLens * 4 - exchange;
+    g.stages = min(kMaxStages, budget / (g.groups * g.stage_bytes));
+    p.smem = g.groups * g.stages * g.stage_bytes + exchange;
+    p.ctas = num_sms() > 0 ? num_sms() : 152;
+    g.ranges = static_cast<long long>(p.ctas) * g.groups;
+    g.pitch = (pb.Nkv + 3) & ~3;
+    const size_t rows_all = static_cast<size_t>(pb.B) * pb.Hq * pb.Nq, D = pb.D;
+    size_t at = 0;
+    auto take = [&](size_t floats) {
+        const size_t here = at;
+        at = up256(at + floats * sizeof(float));
+        return here;
+    };
+    p.o_cut = take(2 * g.ranges * g.rows * D);
+    p.l_cut = take(2 * g.ranges * g.rows);
+    p.l_whole = take(rows_all);
+    if (shared) {
+        p.o_whole = take(rows_all * D);
+        p.o_whole_p = take(g.rblocks_p ? rows_all * D : 0);
+        p.l_whole_p = take(g.rblocks_p ? rows_all : 0);
+    } else {
+        p.scores = take(rows_all * g.pitch);
+    }
+    p.total = at;
+    return p;
+}
+
+template <bool BF16, int MT, int CC>
+cudaError_t launch_variant(const LineArgs& a, const LinePlan& p, const CUtensorMap* m, cudaStream_t s)
+{
+    auto kern = a.shared ? line_kernel<BF16, MT, CC, false> : line_kernel<BF16, MT, CC, true>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(p.ctas), p.g.groups * p.g.warps * 32, p.smem, s, m[0], m[1], m[2], m[3], a, p.g);
+}
+
+}  // namespace
+
+bool line_fits(const Problem& pb, bool shared, int Np)
+{
+    const long long R = static_cast<long long>(pb.Hq / pb.Hkv) * pb.Nq;
+    if (R * pb.B > 0x7fffffffLL) return false;
+    // rows are joined by a CTA each; key tiles of a range are counted in 31 bits
+    const long long units = static_cast<long long>(pb.B) * pb.Hkv * ((R + 15) / 16);
+    const long long tiles = units * (pb.Nkv / 16 + 1) + (shared ? static_cast<long long>(pb.Hkv) * ((R * pb.B + 15) / 16) * (Np / 16 + 1) : 0);
+    return tiles < 0x7fffffffLL && R * pb.B * pb.Hkv < 0x7fffffffLL;
+}
+
+size_t line_workspace_bytes(const Problem& pb, bool shared, int Np)
+{
+    if (pb.B <= 0 || pb.Hq <= 0 || pb.Nq <= 0) return 0;
+    return line_plan(pb, shared, Np).total;
+}
+
+cudaError_t launch_line(const LineArgs& args, void* workspace, cudaStream_t s)
+{
+    LineArgs a = args;
+    const Problem& pb = a.f.pb;
+    LinePlan p = line_plan(pb, a.shared, a.Np);
+    LineGeo& g = p.g;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
+    g.o_cut = at(p.o_cut);
+    g.l_cut = at(p.l_cut);
+    g.o_whole = at(p.o_whole);
+    g.l_whole = at(p.l_whole);
+    g.o_whole_p = at(p.o_whole_p);
+    g.l_whole_p = at(p.l_whole_p);
+    g.scores = at(p.scores);
+    CUtensorMap m[4];
+    std::memset(m, 0, sizeof(m));
+    Problem pp = pb;  // the prefix as one batch entry
+    pp.B = 1;
+    pp.Nkv = a.Np;
+    // maps of sides without keys are never read
+    if (pb.Nkv > 0 && (!make_slab_map(&m[0], a.f.k, pb, true, a.f.bf16, g.kt, g.chunks, pb.vk) ||
+                       !make_slab_map(&m[1], a.f.v, pb, true, a.f.bf16, g.kt, g.chunks, pb.vv)))
+        return cudaErrorInvalidValue;
+    if (g.rblocks_p && (!make_slab_map(&m[2], a.kp, pp, true, a.f.bf16, g.kt, g.chunks, a.vkp) ||
+                        !make_slab_map(&m[3], a.vp, pp, true, a.f.bf16, g.kt, g.chunks, a.vvp)))
+        return cudaErrorInvalidValue;
+    cudaError_t e;
+    if (g.chunks > 8)
+        e = a.f.bf16 ? launch_variant<true, 1, 2>(a, p, m, s) : launch_variant<false, 1, 2>(a, p, m, s);
+    else if (g.rows == 16)
+        e = a.f.bf16 ? launch_variant<true, 1, 1>(a, p, m, s) : launch_variant<false, 1, 1>(a, p, m, s);
+    else
+        e = a.f.bf16 ? launch_variant<true, 2, 1>(a, p, m, s) : launch_variant<false, 2, 1>(a, p, m, s);
+    if (e != cudaSuccess) return e;
+    const long long rows = static_cast<long long>(pb.B) * pb.Hq * pb.Nq;
+    const int key_blocks = a.shared ? 0 : (pb.Nkv + kWeighKeys - 1) / kWeighKeys;
+    const long long ctas = rows + static_cast<long long>(pb.B) * pb.Hkv * key_blocks;
+    const long long x = ctas < 0x40000000LL ? ctas : 0x40000000LL;
+    const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>((ctas + x - 1) / x));
+    auto join = a.f.bf16 ? (a.shared ? join_kernel<true, false> : join_kernel<true, true>)
+                         : (a.shared ? join_kernel<false, false> : join_kernel<false, true>);
+    return launch_dependent(join, grid, kJoinThreads, 0, s, a, g, rows, key_blocks);
+}
+
+}  // namespace ffpa

@@ -301,6 +301,101 @@ FFPA_API ffpa_status ffpa_decode_fwd_kv4(ffpa_dtype dt, ffpa_view q, ffpa_kv4_ca
                                          int Hq, int Hkv, int Nq, int D, int causal, float scale,
                                          ffpa_stream_t stream);
 
+/*
+ * Rotary positions (the docs have no counterpart: they take q and k as given).
+ * Pair p of a head's first rot_dim dims is turned by position * theta_p:
+ *   (x, y) -> mscale * (x cos - y sin, x sin + y cos);
+ * pairs are (p, p + rot_dim / 2), or (2p, 2p + 1) when interleaved; the other
+ * dims are copied. theta_p is given as turns[p] = round(theta_p / 2 pi * 2^64)
+ * (mod 2^64; device memory, rot_dim / 2 entries), so that the angle of every
+ * 32-bit position is exact to 2^-33 turns. sin, cos and the products are fp32.
+ * rot_dim: a multiple of 16 in [16, D]; D: a multiple of 32 in [64, 1024].
+ */
+typedef struct ffpa_rope_plan {
+    const uint64_t* turns;
+    int rot_dim, interleaved;
+    float mscale;
+} ffpa_rope_plan;
+
+/*
+ * q, q_out: [B, Hq, N, D] views; k, k_out: [B, Hkv, N, D] views (Hq or Hkv may
+ * be 0); an output may be its input's own view, otherwise they must not overlap.
+ * The position of token i of sequence b is positions[b * N + i], or start[b] + i
+ * (device int32; both NULL: i). inverse: turns back, which is the gradient of
+ * the forward (mscale included).
+ */
+FFPA_API ffpa_status ffpa_rope(ffpa_dtype dt, ffpa_view q, ffpa_view k, ffpa_view q_out, ffpa_view k_out,
+                               ffpa_rope_plan plan, const int* start, const int* positions, int B, int Hq, int Hkv,
+                               int N, int D, int inverse, ffpa_stream_t stream);
+/* The same for a packed batch: [total, H, D] contiguous, sequence b's tokens the
+ * rows [cu_seqlens[b], cu_seqlens[b + 1]) (device int32 [batch + 1], nondecreasing);
+ * positions: device int32 [total]. Rows of no sequence are left as they are. */
+FFPA_API ffpa_status ffpa_varlen_rope(ffpa_dtype dt, const void* q, const void* k, void* q_out, void* k_out,
+                                      ffpa_rope_plan plan, const int* cu_seqlens, const int* start,
+                                      const int* positions, int batch, int total, int Hq, int Hkv, int D, int inverse,
+                                      ffpa_stream_t stream);
+
+/*
+ * Decode / short-query forward of a batch that shares the keys of a long
+ * prefix: the keys of sequence b are the Np prefix keys, then the first
+ * lens[b] of its own cache (device int32 [B]; NULL: N each). Causal is
+ * bottom-right over all of them: row i sees key j iff j <= i + Np + lens[b] - Nq.
+ * The prefix is read once for the whole batch, whatever B is.
+ *   q, o: [B, Hq, Nq, D] views (o may be q's own); k_prefix, v_prefix:
+ *   [1, Hkv, Np, D] views (stride_b unused); k, v: [B, Hkv, N, D] views, whose
+ *   rows at and past lens[b] may hold anything; lse: contiguous fp32 [B, Hq, Nq].
+ *   D: a multiple of 64 in [64, 1024].
+ *   workspace: device scratch of at least ffpa_decode_shared_workspace_bytes()
+ *   bytes, 256-byte aligned, sized on the current device; one call at a time
+ *   per workspace. The query returns 0 for sizes outside the operation.
+ * P is rounded to the input type, sums and O up to its final rounding are fp32.
+ * A length below 0 or above N records FFPA_ERR_INVALID_VALUE in the device
+ * status word (ffpa_get_status) and the outputs of the call are undefined.
+ */
+FFPA_API size_t ffpa_decode_shared_workspace_bytes(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int Np, int N,
+                                                   int D);
+FFPA_API ffpa_status ffpa_decode_fwd_shared(ffpa_dtype dt, ffpa_view q, ffpa_view k_prefix, ffpa_view v_prefix,
+                                            ffpa_view k, ffpa_view v, const int* lens, ffpa_view o, float* lse,
+                                            void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq,
+                                            int Np, int N, int D, int causal, float scale, ffpa_stream_t stream);
+
+/*
+ * Decode / short-query forward that also scores the cache: the keys of sequence
+ * b are the first lens[b] of its cache (NULL: N each), and
+ *   weights_out[b, h, j] = weights[b, h, j] + sum over the rows of kv head h's
+ *                          group of softmax weight (row, j),  j < lens[b]
+ * (fp32 [B, Hkv, N] contiguous, 16-byte aligned; weights_out may be weights).
+ * Entries at and past lens[b] keep what they hold. The order of the sum is
+ * fixed. Other arguments and the checks as for ffpa_decode_fwd_shared. The
+ * workspace holds the scores: 4 bytes per query row and cached token.
+ */
+FFPA_API size_t ffpa_decode_weights_workspace_bytes(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int N, int D);
+FFPA_API ffpa_status ffpa_decode_fwd_weights(ffpa_dtype dt, ffpa_view q, ffpa_view k, ffpa_view v, const int* lens,
+                                             const float* weights, float* weights_out, ffpa_view o, float* lse,
+                                             void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq,
+                                             int N, int D, int causal, float scale, ffpa_stream_t stream);
+
+/*
+ * Cuts each kv head's cache to `keep` tokens. A sequence of at most `keep`
+ * tokens stays whole. Otherwise its last `recent` tokens stay, and of the
+ * others the keep - recent with the largest weights: of equal ones the earlier,
+ * NaN below everything, -0 equal to +0. Kept tokens stay in their order, at rows
+ * [0, min(lens[b], keep)); rows behind keep what they hold.
+ *   k, v: [B, Hkv, N, D] views; weights: fp32 [B, Hkv, N]; lens: device int32 [B].
+ *   k_out, v_out: [B, Hkv, N_out, D] views, N_out >= min(keep, N); weights_out
+ *   fp32 [B, Hkv, N_out]: the kept tokens' weights. Either all three are the
+ *   inputs' own (in place) or none overlaps any input.
+ *   lens_out: device int32 [B], min(lens[b], keep); may be lens.
+ *   kept: device int32 [B, Hkv, keep], where each kept token was; -1 behind the last.
+ *   D: a multiple of 32 in [64, 1024]; keep >= 1; 0 <= recent <= keep.
+ * A length below 0 or above N records FFPA_ERR_INVALID_VALUE in the device
+ * status word; the outputs of that sequence are undefined.
+ */
+FFPA_API ffpa_status ffpa_kv_evict(ffpa_dtype dt, ffpa_view k, ffpa_view v, const float* weights, const int* lens,
+                                   ffpa_view k_out, ffpa_view v_out, float* weights_out, int* lens_out, int* kept,
+                                   int B, int Hkv, int N, int N_out, int D, int keep, int recent,
+                                   ffpa_stream_t stream);
+
 /* Workspace bytes ffpa_bwd needs for this problem (fp32 row statistics). */
 FFPA_API size_t ffpa_bwd_workspace_bytes(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int Nkv, int D);
 /*
@@ -484,7 +579,8 @@ FFPA_API ffpa_status ffpa_varlen_bwd(ffpa_dtype dt, const void* q, const void* k
  * returned early and its outputs are undefined), FFPA_ERR_INVALID_VALUE (a
  * packed varlen sequence broke the cu_seqlens / max_seqlen contract, see
  * ffpa_varlen_fwd, or a sequence of a 4-bit cache the contract of its lengths
- * and block table, see ffpa_kv4_cache) or FFPA_ERR_CUDA (the stream reported an error).
+ * and block table, see ffpa_kv4_cache, or a cache's length its bounds, see
+ * ffpa_decode_fwd_shared) or FFPA_ERR_CUDA (the stream reported an error).
  */
 FFPA_API ffpa_status ffpa_get_status(ffpa_stream_t stream);
 
