@@ -56,6 +56,10 @@ struct LineGeo {
     float *o_whole_p, *l_whole_p;  // [Hkv * Rp][D], [Hkv * Rp]
     float* scores;       // [B * Hq * Nq][pitch]
     int pitch;
+    // many rows: the prefix is the tensor cores' (launch_xchg, split over the keys)
+    int splits, split_keys;
+    float *o_split, *l_split;  // [splits][Hkv][Rp][D], [splits][Hkv][Rp]
+    uint16_t* q_rows;          // [Hkv][Rp][D]: the queries as its rows
 };
 
 struct __align__(1024) LineStatic {
@@ -255,6 +259,19 @@ __global__ void __launch_bounds__(kLineThreads, 1)
                 atomicCAS(a.f.ctl.status, 0u, DEV_INVALID | (VS_LINE << 8) | ((static_cast<uint32_t>(i) & 0xffffu) << 16));
             if (pb.B <= kLens) s_len[i] = good ? n : 0;
         }
+    if (g.splits) {
+        const int nv = pb.D >> 3, each = pb.Hq / pb.Hkv * pb.Nq;
+        const long long vecs = static_cast<long long>(pb.B) * pb.Hq * pb.Nq * nv;
+        for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < vecs;
+             e += static_cast<long long>(gridDim.x) * blockDim.x) {
+            const long long row = e / nv;  // [Hkv][B][group][Nq]
+            const int col = static_cast<int>(e - row * nv) * 8;
+            const int hk = static_cast<int>(row / g.Rp), rp = static_cast<int>(row - static_cast<long long>(hk) * g.Rp);
+            const int b = rp / each, r = rp - b * each, gg = r / pb.Nq, i = r - gg * pb.Nq;
+            *reinterpret_cast<uint4*>(g.q_rows + row * pb.D + col) = *reinterpret_cast<const uint4*>(
+                static_cast<const uint16_t*>(a.f.q) + b * pb.vq.sb + (hk * (pb.Hq / pb.Hkv) + gg) * pb.vq.sh + i * pb.vq.sn + col);
+        }
+    }
     fence_barrier_init();
     __syncthreads();
     const int group = warp / g.warps, wg = warp - group * g.warps;
@@ -691,15 +708,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
         const int rp = b * R + r, rbp = rp / g.rows, urp = rp - rbp * g.rows;
         const long long s0p = (static_cast<long long>(hk) * g.rblocks_p + rbp) * g.tiles_p;
         if (g.rblocks_p) unit_ranges(g, total, s0p, g.tiles_p, p0, p1, whole_p);
-        const int np = static_cast<int>(p1 - p0 + 1), no = static_cast<int>(g1 - g0 + 1);
+        const int np = g.splits ? g.splits : static_cast<int>(p1 - p0 + 1), no = static_cast<int>(g1 - g0 + 1);
         const int pieces = np + no;
         auto l_of = [&](int i) -> float {
+            if (i < np && g.splits) return g.l_split[(static_cast<size_t>(i) * pb.Hkv + hk) * g.Rp + rp];
             if (i < np)
                 return whole_p ? g.l_whole_p[static_cast<size_t>(hk) * g.Rp + rp]
                                : g.l_cut[cut_slot(g, total, s0p, p0 + i) * g.rows + urp];
             return whole ? g.l_whole[bh * R + r] : g.l_cut[cut_slot(g, total, s0, g0 + i - np) * g.rows + ur];
         };
         auto o_of = [&](int i) -> const float* {
+            if (i < np && g.splits) return g.o_split + ((static_cast<size_t>(i) * pb.Hkv + hk) * g.Rp + rp) * pb.D;
             if (i < np)
                 return whole_p ? g.o_whole_p + (static_cast<size_t>(hk) * g.Rp + rp) * pb.D
                                : g.o_cut + (cut_slot(g, total, s0p, p0 + i) * g.rows + urp) * pb.D;
@@ -800,7 +819,8 @@ struct LinePlan {
     LineGeo g;
     int ctas;
     int smem;
-    size_t o_cut, l_cut, o_whole, l_whole, o_whole_p, l_whole_p, scores, total;  // byte offsets
+    size_t o_cut, l_cut, o_whole, l_whole, o_whole_p, l_whole_p, scores, o_split, l_split, q_rows, total;  // byte offsets
+    Problem prefix;  // the prefix as one batch entry of Rp queries per kv head
 };
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -812,12 +832,26 @@ LinePlan line_plan(const Problem& pb, bool shared, int Np)
     g.chunks = pb.D / 64;
     g.R = pb.Hq / pb.Hkv * pb.Nq;
     g.Rp = pb.B * g.R;
-    const int most = shared ? max(g.R, g.Rp) : g.R;
+    // Rows that a unit's registers hold serve the prefix as well; more rows than
+    // that are the tensor cores'.
+    const int held = g.chunks > 8 ? 16 : 32;
+    const bool split = shared && Np > 0 && g.Rp > held;
+    const int most = shared && !split ? g.Rp : g.R;
     const int mt = g.chunks > 8 || most <= 16 ? 1 : 2;
     g.rows = 16 * mt;
     g.rblocks = (g.R + g.rows - 1) / g.rows;
     g.kt = g.chunks <= 8 && mt == 1 ? 32 : 16;
-    if (shared) {
+    if (split) {
+        p.prefix = pb;
+        p.prefix.B = 1;
+        p.prefix.Hq = pb.Hkv;
+        p.prefix.Nq = g.Rp;
+        p.prefix.Nkv = Np;
+        p.prefix.causal = 0;
+        g.splits = xchg_splits(p.prefix);
+        const int tiles = (Np + 127) / 128;
+        g.split_keys = (tiles + g.splits - 1) / g.splits * 128;
+    } else if (shared) {
         g.rblocks_p = (g.Rp + g.rows - 1) / g.rows;
         g.tiles_p = (Np + g.kt - 1) / g.kt;
         if (g.tiles_p == 0) g.rblocks_p = 0;
@@ -847,6 +881,9 @@ LinePlan line_plan(const Problem& pb, bool shared, int Np)
         p.o_whole = take(rows_all * D);
         p.o_whole_p = take(g.rblocks_p ? rows_all * D : 0);
         p.l_whole_p = take(g.rblocks_p ? rows_all : 0);
+        p.o_split = take(g.splits * rows_all * D);
+        p.l_split = take(g.splits * rows_all);
+        p.q_rows = take(g.splits ? rows_all * D / 2 : 0);
     } else {
         p.scores = take(rows_all * g.pitch);
     }
@@ -896,6 +933,9 @@ cudaError_t launch_line(const LineArgs& args, void* workspace, cudaStream_t s)
     g.o_whole_p = at(p.o_whole_p);
     g.l_whole_p = at(p.l_whole_p);
     g.scores = at(p.scores);
+    g.o_split = at(p.o_split);
+    g.l_split = at(p.l_split);
+    g.q_rows = reinterpret_cast<uint16_t*>(ws + p.q_rows);
     CUtensorMap m[4];
     std::memset(m, 0, sizeof(m));
     Problem pp = pb;  // the prefix as one batch entry
@@ -916,6 +956,30 @@ cudaError_t launch_line(const LineArgs& args, void* workspace, cudaStream_t s)
     else
         e = a.f.bf16 ? launch_variant<true, 2, 1>(a, p, m, s) : launch_variant<false, 2, 1>(a, p, m, s);
     if (e != cudaSuccess) return e;
+    if (g.splits) {
+        XArgs x{};
+        x.pb = p.prefix;
+        const long long D = pb.D;
+        x.pb.vq = View{0, g.Rp * D, D};
+        x.pb.vk = a.vkp;
+        x.pb.vv = a.vvp;
+        x.bf16 = a.f.bf16;
+        x.q = g.q_rows;
+        x.k = a.kp;
+        x.v = a.vp;
+        x.ctl = a.f.ctl;
+        x.pdl = 1;
+        x.splits = g.splits;
+        x.split_keys = g.split_keys;
+        x.split_rows = g.R;
+        x.split_nq = pb.Nq;
+        x.split_causal = pb.causal;
+        x.split_lens = a.lens;
+        x.split_most = pb.Nkv;
+        x.o_part = g.o_split;
+        x.l_part = g.l_split;
+        if ((e = launch_xchg(XOP_FWD, x, s)) != cudaSuccess) return e;
+    }
     const long long rows = static_cast<long long>(pb.B) * pb.Hq * pb.Nq;
     const int key_blocks = a.shared ? 0 : (pb.Nkv + kWeighKeys - 1) / kWeighKeys;
     const long long ctas = rows + static_cast<long long>(pb.B) * pb.Hkv * key_blocks;

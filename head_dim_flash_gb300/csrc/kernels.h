@@ -102,6 +102,15 @@ struct XArgs {
     // entry (ng = 0: all of them); the stored tile buffers then hold the query
     // heads of those groups only, [B, ng * G, Nkv, ldq] (packed: [1, ng * G, ...])
     int g0, ng;
+    // Forward split over the keys (splits > 0; pb.B = 1, no mask of pb's own): the
+    // queries are the rows of a whole batch, split i takes the keys from
+    // i * split_keys on and leaves a normalised fp32 O and the log2 of its sum,
+    // [splits][Hkv][Nq][D] and [splits][Hkv][Nq]. Row r belongs to sequence
+    // r / split_rows; when split_causal it is query r % split_nq of it and sees
+    // the keys up to Nkv + split_lens[sequence] - split_nq + query.
+    int splits, split_keys, split_rows, split_nq, split_causal, split_most;
+    const int* split_lens;             // device, null: split_most each
+    float *o_part, *l_part;
 };
 
 // The GEMMs over the tiles the dK kernel stored (dense, D a multiple of 64 up to 1024;
@@ -146,6 +155,8 @@ cudaError_t launch_fwd_fp8(const FwdArgs& a, void* workspace, cudaStream_t s, bo
 // one-CTA-per-slab form (clusters of C CTAs, every other head dim);
 // FFPA_KERNEL=pair|single in the environment forces one of them.
 cudaError_t launch_xchg(int op, const XArgs& a, cudaStream_t s);
+// The key splits of a forward that is split over them, chosen for `rows` queries of each of H kv heads.
+int xchg_splits(const Problem& pb);
 bool xchg_uses_pair(const Problem& pb);  // the family launch_xchg picks for this problem
 cudaError_t launch_pair(int op, const XArgs& a, cudaStream_t s);
 cudaError_t launch_single(int op, const XArgs& a, cudaStream_t s);

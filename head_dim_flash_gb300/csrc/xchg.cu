@@ -27,6 +27,7 @@
 //
 // Warp roles: warp 0 TMA producer, warp 1 MMA issuer (and TMEM owner),
 // warps 2..5 elementwise (one tile row per thread) and epilogue.
+#include <algorithm>
 #include <cstdlib>
 #include <cstring>
 
@@ -92,7 +93,7 @@ __host__ __device__ inline int stats_bytes(int op, int C)
     return (b + 1023) & ~1023;
 }
 
-template <int OP, bool BF16, bool VARLEN>
+template <int OP, bool BF16, bool VARLEN, bool SPLIT = false>
 __global__ void __launch_bounds__(kThreads, 1)
     xchg_kernel(const __grid_constant__ CUtensorMap tA1, const __grid_constant__ CUtensorMap tA2,
                 const __grid_constant__ CUtensorMap tB1, const __grid_constant__ CUtensorMap tB2,
@@ -102,6 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     // the next GEMM kernel of a backward may take SMs as this grid's last CTAs start
     pdl_trigger();
+    if constexpr (SPLIT) pdl_wait();  // the kernel before lays out the queries
     using T = Traits<OP>;
     const Problem& pb = a.pb;
     const int C = gm.C;
@@ -134,6 +136,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int lq, lk, tq0 = 0, tk0 = 0;
     if constexpr (VARLEN) {
         if (!varlen_seq(pb, b, a.ctl.status, VS_SINGLE, tq0, lq, tk0, lk)) return;  // uniform over the cluster
+    } else if constexpr (SPLIT) {
+        lq = pb.Nq;  // b is the split
+        tk0 = b * a.split_keys;
+        lk = min(a.split_keys, pb.Nkv - tk0);
     } else {
         lq = pb.Nq;
         lk = pb.Nkv;
@@ -272,10 +278,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // TMA coordinates: row maps (d, row or token, head, b or 0), slab maps
     // (0, row or token, chunk, head, b or 0).
-    const int bco = VARLEN ? 0 : b;
+    const int bco = VARLEN || SPLIT ? 0 : b;
     const int row_head = T::kRowsQ ? h : hk;
     auto row_co = [&](int row) { return VARLEN ? (T::kRowsQ ? tq0 : tk0) + row : row; };
-    auto col_co = [&](int row) { return VARLEN ? (T::kRowsQ ? tk0 : tq0) + row : row; };
+    auto col_co = [&](int row) { return VARLEN || SPLIT ? (T::kRowsQ ? tk0 : tq0) + row : row; };
     // key row -> row of the stored tile buffers (packed batches: sequence b's rows
     // start at cu_k[b] + 256 b, so that no tile reaches the next sequence's rows)
     auto tile_row = [&](int row) { return VARLEN ? tk0 + 256 * b + row : row; };
@@ -471,7 +477,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float c2 = pb.scale_log2;
         const int row = r0 + r;  // query (rows = queries) or key (rows = keys)
         // rows = queries: legal keys [0, key_end); rows = keys: legal queries [i_min, lq)
-        const int key_end = pb.causal ? min(lk, row + off + 1) : lk;
+        int key_end = pb.causal ? min(lk, row + off + 1) : lk;
+        if (SPLIT && a.split_causal && row < row_len) {
+            const int n = a.split_lens ? a.split_lens[row / a.split_rows] : a.split_most;
+            key_end = min(lk, pb.Nkv + n - a.split_nq + row % a.split_nq + 1 - tk0);
+        }
         const int i_min = pb.causal ? max(0, row - off) : 0;
         const bool row_ok = row < row_len;
         float l2_row = INFINITY, dl_row = 0.f;  // dQ: own row statistics
@@ -850,6 +860,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t orow = static_cast<size_t>(bco) * ov.sb + static_cast<size_t>(row_head) * ov.sh +
                                 static_cast<size_t>(row_co(row)) * ov.sn;
             uint16_t* dst = reinterpret_cast<uint16_t*>(out) + orow + d0;
+            // a split's part: row of [splits][H][Nq]
+            const size_t prow = (static_cast<size_t>(b) * pb.Hq + h) * pb.Nq + row;
+            float* part = SPLIT ? a.o_part + prow * pb.D + d0 : nullptr;
             // Whole 128-row tiles leave through the idle ring (after its first KiB,
             // the forward's row-sum scratch) and one TMA store per 64-column chunk of
             // the slab: one row per thread would make every warp store touch 32 rows.
@@ -893,6 +906,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0u;
                 }
+                if constexpr (SPLIT) {
+                    if (row_ok) {
+                        float4* d4 = reinterpret_cast<float4*>(part + cc);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            d4[e] = make_float4(__uint_as_float(v[4 * e]) * mul, __uint_as_float(v[4 * e + 1]) * mul,
+                                                __uint_as_float(v[4 * e + 2]) * mul, __uint_as_float(v[4 * e + 3]) * mul);
+                    }
+                    continue;
+                }
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
@@ -904,10 +927,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (OP == XOP_FWD && c == 0 && half == 0 && row_ok) {
-                const float lse = l_tot > 0.f ? (m_ref + log2f(l_tot)) * kLn2 : -INFINITY;
+                const float lse = l_tot > 0.f ? (m_ref + log2f(l_tot)) * (SPLIT ? 1.f : kLn2) : -INFINITY;
                 const size_t li = VARLEN ? static_cast<size_t>(h) * pb.total_q + tq0 + row
                                          : (static_cast<size_t>(b) * pb.Hq + h) * pb.Nq + row;
-                a.lse[li] = lse;
+                (SPLIT ? a.l_part : a.lse)[li] = lse;
             }
         }
     }
@@ -927,10 +950,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) pdl_wait();
 }
 
-template <int OP, bool BF16, bool VARLEN>
+template <int OP, bool BF16, bool VARLEN, bool SPLIT = false>
 cudaError_t launch_op(const XArgs& a, const CUtensorMap* maps, Geo gm, int n_rt, int bz, int smem, cudaStream_t s)
 {
-    auto kern = xchg_kernel<OP, BF16, VARLEN>;
+    auto kern = xchg_kernel<OP, BF16, VARLEN, SPLIT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     gm.n_rt = n_rt;
@@ -1017,8 +1040,10 @@ cudaError_t launch_single(int op, const XArgs& a, cudaStream_t s)
     if (a.g0 < 0 || a.g0 + ng > pb.Hkv) return cudaErrorInvalidValue;
     switch (op) {
     case XOP_FWD:
+        if (a.splits > 0 && (pb.B != 1 || pb.varlen || pb.causal || q_empty || kv_empty || pb.D % 64 != 0))
+            return cudaErrorInvalidConfiguration;
         mk(0, sq, 128); mk(1, sq, 128); mk(2, sk, 128); mk(3, sk, 128); mk(4, sv, 32);
-        n_rt = (pb.Nq + 127) / 128; bz = pb.B * pb.Hq;
+        n_rt = (pb.Nq + 127) / 128; bz = (a.splits > 0 ? a.splits : pb.B) * pb.Hq;
         break;
     case XOP_DQ:
         mk(0, sq, 128); mk(1, sdo, 128); mk(2, sk, 128); mk(3, sv, 128); mk(4, sk, 32);
@@ -1039,6 +1064,12 @@ cudaError_t launch_single(int op, const XArgs& a, cudaStream_t s)
     if (op == XOP_DK && a.store_p) okm = okm && make_ds_map(&m[6], a.p, pb, a.bf16, 128, ng * (pb.Hq / pb.Hkv));
     else m[6] = m[0];
     if (!okm) return cudaErrorInvalidValue;
+    if (a.splits > 0) {  // fp32 parts: stored row by row
+        gm.ostore = 0;
+        m[7] = m[0];
+        return a.bf16 ? launch_op<XOP_FWD, true, false, true>(a, m, gm, n_rt, bz, smem, s)
+                      : launch_op<XOP_FWD, false, false, true>(a, m, gm, n_rt, bz, smem, s);
+    }
     // the output as 128-row x 1-chunk boxes (whole row tiles leave through it;
     // head dims that are not whole 64-column chunks, and views the map cannot
     // describe, keep the per-row stores)
@@ -1068,8 +1099,45 @@ bool xchg_uses_pair(const Problem& pb)
     return pb.D % 64 == 0 && (forced ? forced == 2 : (pb.D % 128 == 0 && pb.D <= 768));
 }
 
+namespace {
+
+// A split forward takes pairs where the forward does and its rows fill more
+// than one CTA's 128.
+bool split_uses_pair(const Problem& pb) { return xchg_uses_pair(pb) && pb.Nq > 128; }
+
+}  // namespace
+
+int xchg_splits(const Problem& pb)
+{
+    const bool pair = split_uses_pair(pb);
+    const int C = pair ? ((pb.D + 127) / 128 * 128 + 255) / 256 : ((pb.D + 63) / 64 + 3) / 4;
+    const int cluster = pair ? 2 * C : C;
+    const int sms = num_sms() > 0 ? num_sms() : 152;
+    // clusters that run at once: cluster sizes above 2 do not reach every SM
+    const long long at_once = std::max(1, (cluster <= 2 ? sms : sms - 8) / cluster);
+    const long long units = static_cast<long long>(pb.Hq) * ((pb.Nq + (pair ? 255 : 127)) / (pair ? 256 : 128));
+    const int tiles = (pb.Nkv + 127) / 128;
+    // time in super-steps of C tiles: the waves' steps and a start and end worth
+    // four of them; a split's parts are written and read again (fp32), which is
+    // worth half a step of every cluster
+    double best = 0;
+    int splits = 1;
+    for (int n = 1; n <= std::min(tiles, kDecodeMaxSplits); ++n) {
+        const int per = (tiles + n - 1) / n;
+        if ((tiles + per - 1) / per != n) continue;
+        const double cost = static_cast<double>((units * n + at_once - 1) / at_once) * ((per + C - 1) / C + 4) +
+                            0.5 * static_cast<double>(units * n) / at_once;
+        if (best == 0 || cost < best) {
+            best = cost;
+            splits = n;
+        }
+    }
+    return splits;
+}
+
 cudaError_t launch_xchg(int op, const XArgs& a, cudaStream_t s)
 {
+    if (a.splits > 0) return split_uses_pair(a.pb) ? launch_pair(op, a, s) : launch_single(op, a, s);
     return xchg_uses_pair(a.pb) ? launch_pair(op, a, s) : launch_single(op, a, s);
 }
 

@@ -112,7 +112,7 @@ __host__ __device__ inline int pair_stats_bytes(int op, int C)
 // 16 KiB, the MMAs are kind::f8f6f4 (the same 32 bytes per instruction), and
 // the per-head dequantization scales enter the softmax exponent (Q, K) and
 // the epilogue (V). BF16 is then the output type.
-template <int OP, bool BF16, bool VARLEN, bool F8 = false>
+template <int OP, bool BF16, bool VARLEN, bool F8 = false, bool SPLIT = false>
 __global__ void __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tA1, const __grid_constant__ CUtensorMap tA2,
                 const __grid_constant__ CUtensorMap tB1, const __grid_constant__ CUtensorMap tB2,
@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     // the next GEMM kernel of a backward may take SMs as this grid's last CTAs start
     pdl_trigger();
+    if constexpr (SPLIT) pdl_wait();  // the kernel before lays out the queries
     using T = Traits<OP>;
     const Problem& pb = a.pb;
     const int C = gm.C;
@@ -156,6 +157,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int lq, lk, tq0 = 0, tk0 = 0;
     if constexpr (VARLEN) {
         if (!varlen_seq(pb, b, a.ctl.status, VS_PAIR, tq0, lq, tk0, lk)) return;  // uniform over the cluster
+    } else if constexpr (SPLIT) {
+        lq = pb.Nq;  // b is the split
+        tk0 = b * a.split_keys;
+        lk = min(a.split_keys, pb.Nkv - tk0);
     } else {
         lq = pb.Nq;
         lk = pb.Nkv;
@@ -311,10 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         return T::kRowsQ ? tc * 128 : (m_start + tc % max(n_mt, 1)) * 128;
     };
     // TMA coordinates of the 5-D maps: (0, row or token, chunk, head, b or 0).
-    const int bco = VARLEN ? 0 : b;
+    const int bco = VARLEN || SPLIT ? 0 : b;
     const int row_head = T::kRowsQ ? h : hk;
     auto row_co = [&](int row) { return VARLEN ? (T::kRowsQ ? tq0 : tk0) + row : row; };
-    auto col_co = [&](int row) { return VARLEN ? (T::kRowsQ ? tk0 : tq0) + row : row; };
+    auto col_co = [&](int row) { return VARLEN || SPLIT ? (T::kRowsQ ? tk0 : tq0) + row : row; };
     // key row -> row of the stored tile buffers (packed batches: sequence b's rows
     // start at cu_k[b] + 256 b, so that no tile reaches the next sequence's rows)
     auto tile_row = [&](int row) { return VARLEN ? tk0 + 256 * b + row : row; };
@@ -734,7 +739,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             : pb.scale_log2;
         const int row = r0 + r;  // query (rows = queries) or key (rows = keys)
         // rows = queries: legal keys [0, key_end); rows = keys: legal queries [i_min, lq)
-        const int key_end = pb.causal ? min(lk, row + off + 1) : lk;
+        int key_end = pb.causal ? min(lk, row + off + 1) : lk;
+        if (SPLIT && a.split_causal && row < row_len) {
+            const int n = a.split_lens ? a.split_lens[row / a.split_rows] : a.split_most;
+            key_end = min(lk, pb.Nkv + n - a.split_nq + row % a.split_nq + 1 - tk0);
+        }
         const int i_min = pb.causal ? max(0, row - off) : 0;
         const bool row_ok = row < row_len;
         float l2_row = INFINITY, dl_row = 0.f;  // dQ: own row statistics
@@ -1120,6 +1129,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t orow = static_cast<size_t>(bco) * ov.sb + static_cast<size_t>(row_head) * ov.sh +
                                 static_cast<size_t>(row_co(row)) * ov.sn;
             uint16_t* dst = reinterpret_cast<uint16_t*>(out) + orow + d0;
+            // a split's part: row of [splits][H][Nq]
+            const size_t prow = (static_cast<size_t>(b) * pb.Hq + h) * pb.Nq + row;
+            float* part = SPLIT ? a.o_part + prow * pb.D + d0 : nullptr;
             // Whole 128-row tiles leave through the idle ring (after its first KiB,
             // the forward's row-sum scratch) and TMA stores of 128 rows x 128
             // columns: one row per thread would make every warp store touch 32 rows.
@@ -1171,6 +1183,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0u;
                 }
+                if constexpr (SPLIT) {
+                    if (row_ok) {
+                        float4* d4 = reinterpret_cast<float4*>(part + cc);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            d4[e] = make_float4(__uint_as_float(v[4 * e]) * mul, __uint_as_float(v[4 * e + 1]) * mul,
+                                                __uint_as_float(v[4 * e + 2]) * mul, __uint_as_float(v[4 * e + 3]) * mul);
+                    }
+                    continue;
+                }
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
@@ -1182,10 +1204,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (OP == XOP_FWD && c == 0 && half == 0 && row_ok) {
-                const float lse = l_tot > 0.f ? (m_ref + log2f(l_tot)) * kLn2 : -INFINITY;
+                const float lse = l_tot > 0.f ? (m_ref + log2f(l_tot)) * (SPLIT ? 1.f : kLn2) : -INFINITY;
                 const size_t li = VARLEN ? static_cast<size_t>(h) * pb.total_q + tq0 + row
                                          : (static_cast<size_t>(b) * pb.Hq + h) * pb.Nq + row;
-                a.lse[li] = lse;
+                (SPLIT ? a.l_part : a.lse)[li] = lse;
             }
         }
     }
@@ -1206,10 +1228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) pdl_wait();
 }
 
-template <int OP, bool BF16, bool VARLEN, bool F8 = false>
+template <int OP, bool BF16, bool VARLEN, bool F8 = false, bool SPLIT = false>
 cudaError_t launch_op(const XArgs& a, const CUtensorMap* maps, PGeo gm, int n_rt, int bz, int smem, cudaStream_t s)
 {
-    auto kern = pair_kernel<OP, BF16, VARLEN, F8>;
+    auto kern = pair_kernel<OP, BF16, VARLEN, F8, SPLIT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     gm.n_rt = n_rt;
@@ -1332,8 +1354,10 @@ cudaError_t launch_pair(int op, const XArgs& a, cudaStream_t s)
     }
     switch (op) {
     case XOP_FWD:
+        if (a.splits > 0 && (pb.B != 1 || pb.varlen || pb.causal || q_empty || kv_empty))
+            return cudaErrorInvalidConfiguration;
         row(0, sq); row(1, sq); col(2, sk); col(3, sk); val(4, sv);
-        n_rows = pb.Nq; bz = pb.B * pb.Hq;
+        n_rows = pb.Nq; bz = (a.splits > 0 ? a.splits : pb.B) * pb.Hq;
         break;
     case XOP_DQ:
         row(0, sq); row(1, sdo); col(2, sk); col(3, sv); val(4, sk);
@@ -1355,6 +1379,13 @@ cudaError_t launch_pair(int op, const XArgs& a, cudaStream_t s)
     if (op == XOP_DK && a.store_p) okm = okm && make_ds_map(&m[6], a.p, pb, a.bf16, 128, ng * (pb.Hq / pb.Hkv));
     else m[6] = m[0];
     if (!okm) return cudaErrorInvalidValue;
+    if (a.splits > 0) {  // fp32 parts: stored row by row
+        gm.ostore = 0;
+        m[7] = m[0];
+        const int n_rt_s = (n_rows + 255) / 256;
+        return a.bf16 ? launch_op<XOP_FWD, true, false, false, true>(a, m, gm, n_rt_s, bz, smem, s)
+                      : launch_op<XOP_FWD, false, false, false, true>(a, m, gm, n_rt_s, bz, smem, s);
+    }
     // the output as 128-row x 2-chunk boxes (the kernel stores whole row tiles
     // through it; a view the map cannot describe keeps the per-row stores)
     {
