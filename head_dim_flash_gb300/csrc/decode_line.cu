@@ -16,9 +16,10 @@
 // per warp (mma.m16n8k16 over its chunks) and summed through shared memory;
 // the online softmax is done by every warp alike; O += P V stays with the
 // chunks, in registers. The scores of tile t + 1 are issued before the values
-// of tile t. A slot is refilled by the group's first warp when all warps have
-// passed the barrier of the sum, so there is no producer warp. Head dims up to
-// 256 leave room for two to eight groups, which share nothing but the SM.
+// of tile t. A tile is a chain of waits (data, sum, maximum, P), so an SM runs
+// two groups or more, which share nothing. A slot is refilled by the group's last
+// warp, which has little to sum, when all warps have passed the barrier of the
+// sum: a producer warp would cost every thread registers.
 //
 // The scoring form also stores the scores (fp32, log2 units: 4 bytes per row
 // and key beside 4 D of K and V), and the second kernel turns them into weights
@@ -36,21 +37,21 @@ namespace ffpa {
 namespace {
 
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 12;
 constexpr int kMaxGroups = 8;
 constexpr int kLens = 1024;     // lengths staged in shared memory; longer batches read them from L2
-constexpr int kLineThreads = 256;
+constexpr int kTileKeys = 16;   // keys of a tile: one k16 step of the value product
 constexpr int kJoinThreads = 256;
 
 enum LineSite : uint32_t { LS_FULL = 0x58, LS_DRAIN };
 
 struct LineGeo {
-    int kt, chunks, warps, groups, stages, stage_bytes;
+    int chunks, warps, groups, stages, stage_bytes;
     int rows;            // query rows of a unit (16 or 32)
     int R, rblocks;      // rows of a kv head's group, their blocks
     int Rp, rblocks_p;   // the same for the shared prefix's units (rblocks_p = 0: not in the line)
     int tiles_p;         // tiles of one prefix unit
-    long long ranges;    // groups of the whole grid
+    int ranges;          // groups of the whole grid
     float *o_cut, *l_cut;      // [2 * ranges][rows][D], [2 * ranges][rows]
     float *o_whole, *l_whole;  // [B * Hq * Nq][D] (shared), [B * Hq * Nq]: units inside one range
     float *o_whole_p, *l_whole_p;  // [Hkv * Rp][D], [Hkv * Rp]
@@ -62,11 +63,23 @@ struct LineGeo {
     uint16_t* q_rows;          // [Hkv][Rp][D]: the queries as its rows
 };
 
+// A place in the line.
+struct Spot {
+    int b;        // sequence, -1: the shared prefix
+    int hk, rb;
+    int tile, tiles;
+    int keys;     // of the unit
+};
+
 struct __align__(1024) LineStatic {
     uint64_t full[kMaxGroups][kMaxStages];
+    struct {
+        Spot at;              // of the next tile to load
+        int left, stage;      // tiles to load, the slot of the next
+    } ahead[kMaxGroups];
     int abort_flag;
 };
-static_assert(sizeof(LineStatic) == 1024, "static shared block must be exactly 1 KiB");
+static_assert(sizeof(LineStatic) == 2048, "static shared block must be whole KiB");
 
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -106,39 +119,42 @@ __device__ __forceinline__ int clamp_len(const LineArgs& a, int b)
     return n >= 0 && n <= a.f.pb.Nkv ? n : 0;
 }
 
-__device__ __forceinline__ int tiles_of(int keys, int kt) { return (keys + kt - 1) / kt; }
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + kTileKeys - 1) / kTileKeys; }
 
-// Tiles of the whole line, and those of the sequences before `b` (a warp's sum).
-__device__ __forceinline__ void line_sums(const LineArgs& a, const LineGeo& g, int b, long long& total,
-                                          long long& before)
+// Tiles of the whole line (below 2^31), and those before sequence `b` (by whole warps).
+__device__ __forceinline__ void line_sums(const LineArgs& a, const LineGeo& g, int b, int& total, int& before)
 {
     const Problem& pb = a.f.pb;
-    long long t = 0, p = 0;
+    int t = 0, p = 0;
+#pragma unroll 4
     for (int i = threadIdx.x & 31; i < pb.B; i += 32) {
-        const int n = tiles_of(clamp_len(a, i), g.kt);
+        const int n = tiles_of(clamp_len(a, i));
         t += n;
         if (i < b) p += n;
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        t += __shfl_xor_sync(0xffffffffu, t, d);
-        p += __shfl_xor_sync(0xffffffffu, p, d);
-    }
-    const long long per = static_cast<long long>(pb.Hkv) * g.rblocks;
-    const long long prefix = static_cast<long long>(pb.Hkv) * g.rblocks_p * g.tiles_p;
+    t = __reduce_add_sync(0xffffffffu, t);
+    p = __reduce_add_sync(0xffffffffu, p);
+    const int per = pb.Hkv * g.rblocks, prefix = pb.Hkv * g.rblocks_p * g.tiles_p;
     total = prefix + t * per;
     before = prefix + p * per;
 }
 
-// Ranges that the line is cut into: no more than it has tiles, so that none is empty.
-__device__ __forceinline__ long long cuts(const LineGeo& g, long long total) { return min(g.ranges, total); }
-
-// A place in the line.
-struct Spot {
-    int b;        // sequence, -1: the shared prefix
-    int hk, rb;
-    int tile, tiles;
-    int keys;     // of the unit
+// The line cut into ranges, no more than it has tiles, so that none is empty:
+// the first `longer` hold one tile more than the others.
+struct Cuts {
+    int ranges, each, longer;
+    __device__ Cuts(const LineGeo& g, int total)
+    {
+        ranges = min(g.ranges, total);
+        each = ranges > 0 ? total / ranges : 0;
+        longer = total - each * ranges;
+    }
+    __device__ int begin(int r) const { return r * each + min(r, longer); }
+    __device__ int holding(int t) const  // the range that holds tile t
+    {
+        const int head = longer * (each + 1);
+        return t < head ? t / (each + 1) : longer + (t - head) / each;
+    }
 };
 
 struct Line {
@@ -152,7 +168,7 @@ struct Line {
         s.tiles = 0;
         while (s.b < a.f.pb.B) {
             s.keys = len(s.b);
-            s.tiles = tiles_of(s.keys, g.kt);
+            s.tiles = tiles_of(s.keys);
             if (s.tiles > 0) return;
             ++s.b;
         }
@@ -168,45 +184,43 @@ struct Line {
         enter(s);
     }
     // The place of tile t of the line (called by whole warps).
-    __device__ Spot find(long long t) const
+    __device__ Spot find(int t) const
     {
         Spot s{};
         const int H = a.f.pb.Hkv;
-        const long long prefix = static_cast<long long>(H) * g.rblocks_p * g.tiles_p;
+        const int prefix = H * g.rblocks_p * g.tiles_p;
         if (t < prefix) {
-            const int unit = static_cast<int>(t / g.tiles_p);
+            const int unit = t / g.tiles_p;
             s.b = -1;
             s.hk = unit / g.rblocks_p;
-            s.rb = unit % g.rblocks_p;
-            s.tile = static_cast<int>(t - static_cast<long long>(unit) * g.tiles_p);
+            s.rb = unit - s.hk * g.rblocks_p;
+            s.tile = t - unit * g.tiles_p;
             s.tiles = g.tiles_p;
             s.keys = a.Np;
             return s;
         }
         t -= prefix;
-        const long long per = static_cast<long long>(H) * g.rblocks;
-        const int lane = threadIdx.x & 31;
-        long long run = 0;
+        const int per = H * g.rblocks, lane = threadIdx.x & 31;
+        int run = 0;
         s.b = a.f.pb.B;
         for (int i0 = 0; i0 < a.f.pb.B; i0 += 32) {
-            const int n = i0 + lane < a.f.pb.B ? tiles_of(len(i0 + lane), g.kt) : 0;
-            long long incl = n;
+            const int n = i0 + lane < a.f.pb.B ? tiles_of(len(i0 + lane)) : 0;
+            int incl = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+                const int o = __shfl_up_sync(0xffffffffu, incl, d);
                 if (lane >= d) incl += o;
             }
             const uint32_t past = __ballot_sync(0xffffffffu, (run + incl) * per > t);
             if (past) {
                 const int at = __ffs(past) - 1;
-                const long long first = __shfl_sync(0xffffffffu, (run + incl - n) * per, at);
+                const int rest = t - __shfl_sync(0xffffffffu, (run + incl - n) * per, at);
                 s.b = i0 + at;
                 s.tiles = __shfl_sync(0xffffffffu, n, at);
-                const long long rest = t - first;
-                const int unit = static_cast<int>(rest / s.tiles);
-                s.tile = static_cast<int>(rest - static_cast<long long>(unit) * s.tiles);
+                const int unit = rest / s.tiles;
+                s.tile = rest - unit * s.tiles;
                 s.hk = unit / g.rblocks;
-                s.rb = unit % g.rblocks;
+                s.rb = unit - s.hk * g.rblocks;
                 s.keys = len(s.b);
                 return s;
             }
@@ -228,28 +242,32 @@ __device__ __forceinline__ void row_of(int r, int b, int Nq, int R, int& bb, int
     i = r - gg * Nq;
 }
 
+// Threads of a variant: sixteen warps of 128 registers a thread where that
+// holds its rows, else eight.
+template <int MT, int CC>
+constexpr int line_threads() { return MT == 1 && CC == 1 ? 512 : 256; }
+
 template <bool BF16, int MT, int CC, bool SCORE>
-__global__ void __launch_bounds__(kLineThreads, 1)
+__global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
     line_kernel(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CUtensorMap tV,
                 const __grid_constant__ CUtensorMap tKp, const __grid_constant__ CUtensorMap tVp, const LineArgs a,
                 const LineGeo g)
 {
     pdl_wait();
     pdl_trigger();
-    constexpr int KT = CC == 1 && MT == 1 ? 32 : 16;  // keys of a tile
-    constexpr int NT = KT / 8;
-    constexpr int ROWS = 16 * MT;
-    constexpr int SLOTS = MT * NT * 2;                // float2 a lane holds of a tile's scores
+    constexpr int KT = kTileKeys, NT = KT / 8, ROWS = 16 * MT;
+    constexpr int SLOTS = MT * NT * 2;  // float2 a lane holds of a tile's scores
     const Problem& pb = a.f.pb;
     __shared__ LineStatic sh;
     __shared__ int s_len[kLens];
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = g.stages;
     if (smem_u32(smem) & 1023u) {
         if (threadIdx.x == 0) atomicCAS(a.f.ctl.status, 0u, 5u | (0xffu << 8));
         return;
     }
-    if (threadIdx.x < g.groups * g.stages) mbar_init(&sh.full[threadIdx.x / g.stages][threadIdx.x % g.stages], 1);
+    if (threadIdx.x < g.groups * S) mbar_init(&sh.full[threadIdx.x / S][threadIdx.x % S], 1);
     if (threadIdx.x == 0) sh.abort_flag = 0;
     if (a.lens)
         for (int i = threadIdx.x; i < pb.B; i += blockDim.x) {
@@ -264,63 +282,62 @@ __global__ void __launch_bounds__(kLineThreads, 1)
         const long long vecs = static_cast<long long>(pb.B) * pb.Hq * pb.Nq * nv;
         for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < vecs;
              e += static_cast<long long>(gridDim.x) * blockDim.x) {
-            const long long row = e / nv;  // [Hkv][B][group][Nq]
-            const int col = static_cast<int>(e - row * nv) * 8;
-            const int hk = static_cast<int>(row / g.Rp), rp = static_cast<int>(row - static_cast<long long>(hk) * g.Rp);
+            const int row = static_cast<int>(e / nv);  // [Hkv][B][group][Nq], below 2^31
+            const int col = static_cast<int>(e - static_cast<long long>(row) * nv) * 8;
+            const int hk = row / g.Rp, rp = row - hk * g.Rp;
             const int b = rp / each, r = rp - b * each, gg = r / pb.Nq, i = r - gg * pb.Nq;
-            *reinterpret_cast<uint4*>(g.q_rows + row * pb.D + col) = *reinterpret_cast<const uint4*>(
+            *reinterpret_cast<uint4*>(g.q_rows + static_cast<size_t>(row) * pb.D + col) = *reinterpret_cast<const uint4*>(
                 static_cast<const uint16_t*>(a.f.q) + b * pb.vq.sb + (hk * (pb.Hq / pb.Hkv) + gg) * pb.vq.sh + i * pb.vq.sn + col);
         }
     }
     fence_barrier_init();
     __syncthreads();
-    const int group = warp / g.warps, wg = warp - group * g.warps;
     const Line line{a, g, a.lens && pb.B <= kLens ? s_len : nullptr};
-
-    // my group's range of the line
-    long long total, unused;
+    int total, unused;
     line_sums(a, g, 0, total, unused);
-    // (neighbouring ranges go to different SMs: a line of few tiles does not crowd a few of them)
-    const long long range = static_cast<long long>(group) * gridDim.x + blockIdx.x, ranges = cuts(g, total);
-    if (range >= ranges) return;  // no barrier below spans groups
-    const long long begin = total * range / ranges, end = total * (range + 1) / ranges;
-    const int n = static_cast<int>(end - begin);
-    Spot spot = line.find(begin);
-
-    uint8_t* const ring = smem + static_cast<size_t>(group) * g.stages * g.stage_bytes;
-    float2* const part = reinterpret_cast<float2*>(smem + static_cast<size_t>(g.groups) * g.stages * g.stage_bytes) +
-                         group * (g.warps > 1 ? (g.warps + 1) * SLOTS * 32 : 0);
-    float2* const fin = part + g.warps * SLOTS * 32;
-    uint64_t* const full = sh.full[group];
+    const Cuts cuts(g, total);
     volatile int* abort_p = &sh.abort_flag;
     uint32_t* status = a.f.ctl.status;
     const uint64_t lim = a.f.ctl.limit_ns;
-    const int S = g.stages;
     const uint32_t half_bytes = static_cast<uint32_t>(g.stage_bytes / 2);
-    auto sync_group = [&] {
-        if (g.warps > 1)
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(g.warps * 32) : "memory");
-        else
-            __syncwarp();
-    };
+    const int group = warp / g.warps, wg = warp - group * g.warps;
+    // neighbouring ranges go to different SMs: a line of few tiles does not crowd a few of them
+    const int range = group * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    if (range >= cuts.ranges) return;  // no barrier below spans groups
+    const int n = cuts.begin(range + 1) - cuts.begin(range);
+    const Spot spot = line.find(cuts.begin(range));
+    uint8_t* const ring = smem + static_cast<size_t>(group) * S * g.stage_bytes;
+    float2* const part = reinterpret_cast<float2*>(smem + static_cast<size_t>(g.groups) * S * g.stage_bytes) +
+                         group * (g.warps > 1 ? (g.warps + 1) * SLOTS * 32 : 0);
+    float2* const fin = part + g.warps * SLOTS * 32;
+    auto sync_group = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(g.warps * 32) : "memory"); };
 
     // -------------------------------------------------------------- loads
-    // lanes 0 (K) and 1 (V) of the group's first warp; both walk the line ahead of the products
-    Spot ahead = spot;
-    int issued = 0;
+    // lane 0 of the group's last warp; its place in the line is ahead of the products'
+    const bool loads = wg == g.warps - 1 && lane == 0;
     auto issue = [&] {
-        if (wg != 0 || issued >= n) return;
-        if (lane < 2) {
-            const int st = issued % S;
-            uint8_t* dst = ring + st * g.stage_bytes + lane * half_bytes;
-            if (lane == 0) mbar_arrive_expect_tx(&full[st], g.stage_bytes);
-            const CUtensorMap* m = ahead.b < 0 ? (lane ? &tVp : &tKp) : (lane ? &tV : &tK);
-            tma_load_5d(dst, m, &full[st], 0, ahead.tile * KT, 0, ahead.hk, max(ahead.b, 0));
+        auto& h = sh.ahead[group];
+        if (h.left == 0) return;
+        --h.left;
+        uint8_t* dst = ring + h.stage * g.stage_bytes;
+        uint64_t* bar = &sh.full[group][h.stage];
+        if (++h.stage == S) h.stage = 0;
+        const bool prefix = h.at.b < 0;
+        mbar_arrive_expect_tx(bar, g.stage_bytes);
+        tma_load_5d(dst, prefix ? &tKp : &tK, bar, 0, h.at.tile * KT, 0, h.at.hk, max(h.at.b, 0));
+        tma_load_5d(dst + half_bytes, prefix ? &tVp : &tV, bar, 0, h.at.tile * KT, 0, h.at.hk, max(h.at.b, 0));
+        if (++h.at.tile == h.at.tiles && h.left) {
+            Spot at = h.at;
+            line.next_unit(at);
+            h.at = at;
         }
-        ++issued;
-        if (++ahead.tile == ahead.tiles) line.next_unit(ahead);
     };
-    for (int i = 0; i < S; ++i) issue();
+    if (loads) {
+        sh.ahead[group].at = spot;
+        sh.ahead[group].left = n;
+        sh.ahead[group].stage = 0;
+        for (int i = 0; i < S; ++i) issue();
+    }
 
     // ------------------------------------------------------------ products
     const int my_chunks = CC == 1 ? 1 : (wg < g.chunks) + (wg + 8 < g.chunks);
@@ -389,17 +406,22 @@ __global__ void __launch_bounds__(kLineThreads, 1)
                     for (int e = 0; e < 4; ++e) o_acc[cc][i][mt][e] = 0.f;
         }
     };
-    auto scores = [&](int t) {
-        const int st = t % S;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (t / S) & 1, abort_p, status, lim, LS_FULL));
+    int k_st = 0, v_st = 0, turn = 0;   // stages of the next scores and values; the warp that stores scores
+    uint32_t k_phase = 0;
+    auto scores = [&] {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sh.full[group][k_st], k_phase, abort_p, status, lim, LS_FULL));
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.f;
+        const uint32_t kbase = smem_u32(ring + k_st * g.stage_bytes);
+        if (++k_st == S) {
+            k_st = 0;
+            k_phase ^= 1u;
+        }
         if (!ok) return;
-        const uint32_t kbase = smem_u32(ring + st * g.stage_bytes);
 #pragma unroll
         for (int cc = 0; cc < CC; ++cc) {
             if (cc >= my_chunks) break;
@@ -420,7 +442,7 @@ __global__ void __launch_bounds__(kLineThreads, 1)
         }
     };
     // the sum over the group's warps, the mask, and P and the factors of tile t (the unit `u`'s)
-    auto softmax = [&](int t, const Spot& u, int prev_stage) {
+    auto softmax = [&](const Spot& u, bool refill) {
         if (g.warps > 1) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -430,21 +452,25 @@ __global__ void __launch_bounds__(kLineThreads, 1)
                     part[(wg * SLOTS + (mt * NT + i) * 2 + 1) * 32 + lane] = make_float2(s[mt][i][2], s[mt][i][3]);
                 }
         }
-        sync_group();
-        // every warp has left the slot before: it is free
-        if (prev_stage >= 0 && ok) issue();
         if (g.warps > 1) {
+            sync_group();
+            // every warp has left the values of the tile before: its slot is free
+            if (refill && ok && loads) issue();
             for (int sl = wg; sl < SLOTS; sl += g.warps) {
-                float2 acc = make_float2(0.f, 0.f);
-                for (int w = 0; w < g.warps; ++w) {
-                    const float2 p = part[(w * SLOTS + sl) * 32 + lane];
-                    acc.x += p.x;
-                    acc.y += p.y;
-                }
-                fin[sl * 32 + lane] = acc;
+                float2 p[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w)
+                    p[w] = w < g.warps ? part[(w * SLOTS + sl) * 32 + lane] : make_float2(0.f, 0.f);
+                fin[sl * 32 + lane] = make_float2(((p[0].x + p[1].x) + (p[2].x + p[3].x)) + ((p[4].x + p[5].x) + (p[6].x + p[7].x)),
+                                                  ((p[0].y + p[1].y) + (p[2].y + p[3].y)) + ((p[4].y + p[5].y) + (p[6].y + p[7].y)));
             }
             sync_group();
+        } else if (refill && ok) {
+            __syncwarp();
+            if (loads) issue();
         }
+        const bool store = wg == turn;
+        if (++turn == g.warps) turn = 0;
         const float c2 = pb.scale_log2;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -467,7 +493,7 @@ __global__ void __launch_bounds__(kLineThreads, 1)
             }
             if constexpr (SCORE) {
                 // one warp of the group stores the tile's scores, each in turn
-                if (wg == t % g.warps) {
+                if (store) {
 #pragma unroll
                     for (int hi = 0; hi < 2; ++hi) {
                         const int r = u.rb * ROWS + mt * 16 + hi * 8 + r_lo;
@@ -502,9 +528,8 @@ __global__ void __launch_bounds__(kLineThreads, 1)
             }
         }
     };
-    auto values = [&](int t, const Spot& u) {
-        const int st = t % S;
-        const uint32_t vbase = smem_u32(ring + st * g.stage_bytes) + half_bytes;
+    auto values = [&](const Spot& u) {
+        const uint32_t vbase = smem_u32(ring + v_st * g.stage_bytes) + half_bytes;
         const int valid = u.keys - u.tile * KT;
 #pragma unroll
         for (int cc = 0; cc < CC; ++cc) {
@@ -541,6 +566,7 @@ __global__ void __launch_bounds__(kLineThreads, 1)
                     }
                 }
         }
+        if (++v_st == S) v_st = 0;
     };
     // the piece of unit u that this range holds: its tiles [first, last)
     auto finish = [&](const Spot& u, int first, int last) {
@@ -601,8 +627,8 @@ __global__ void __launch_bounds__(kLineThreads, 1)
     reset();
     enter_unit(unit);
     int first = unit.tile;      // first tile of the unit in this range
-    scores(0);
-    softmax(0, unit, -1);
+    scores();
+    softmax(unit, false);
     for (int t = 0; t < n; ++t) {
         const Spot cur = unit;
         const bool more = t + 1 < n;
@@ -613,123 +639,106 @@ __global__ void __launch_bounds__(kLineThreads, 1)
         }
         if (more) {
             if (fresh) enter_unit(unit);
-            scores(t + 1);
+            scores();
         }
-        values(t, cur);
+        values(cur);
         if (fresh || !more) {
             finish(cur, first, cur.tile + 1);
             first = 0;
             reset();
         }
-        if (more) softmax(t + 1, unit, t % S);
+        if (more) softmax(unit, true);
     }
     // a range whose wait ran out leaves none of its copies in flight
-    if (!ok && wg == 0 && lane == 0) {
+    if (!ok && loads) {
+        const int issued = n - sh.ahead[group].left;
         for (int t = max(0, issued - S); t < issued; ++t) {
             int dummy = 0;
-            if (!mbar_wait(&full[t % S], (t / S) & 1, &dummy, status, lim, LS_DRAIN, false)) break;
+            if (!mbar_wait(&sh.full[group][t % S], (t / S) & 1, &dummy, status, lim, LS_DRAIN, false)) break;
         }
     }
 }
 
 // ------------------------------------------------------------------ joining
-// The ranges that hold tiles [s0, s0 + tiles) of the line.
-__device__ __forceinline__ void unit_ranges(const LineGeo& g, long long total, long long s0, int tiles, long long& g0,
-                                            long long& g1, bool& whole)
-{
-    const long long ranges = cuts(g, total);
-    auto holds = [&](long long t) {
-        long long r = t * ranges / total;
-        while (r + 1 < ranges && total * (r + 1) / ranges <= t) ++r;
-        while (r > 0 && total * r / ranges > t) --r;
-        return r;
-    };
-    if (tiles <= 0) {
-        g0 = 0;
-        g1 = -1;
-        whole = false;
-        return;
+// The pieces of a unit's tiles [s0, s0 + tiles): one per range that holds some.
+// The first begins inside its range (cut slot 1 there), later ones at theirs (slot 0).
+struct Pieces {
+    int first, count;
+    bool whole;  // one range holds it all: not in the cut slots
+    __device__ Pieces(const Cuts& c, int s0, int tiles)
+    {
+        first = tiles > 0 ? c.holding(s0) : 0;
+        count = tiles > 0 ? c.holding(s0 + tiles - 1) - first + 1 : 0;
+        whole = count == 1;
     }
-    g0 = holds(s0);
-    g1 = holds(s0 + tiles - 1);
-    whole = g0 == g1;
-}
-
-// Cut slot of range r for a unit that begins at tile s0: 1 where the unit begins inside the range.
-__device__ __forceinline__ long long cut_slot(const LineGeo& g, long long total, long long s0, long long r)
-{
-    return 2 * r + (s0 >= total * r / cuts(g, total) ? 1 : 0);
-}
+    __device__ int slot(int i) const { return i == 0 ? 2 * first + 1 : 2 * (first + i); }
+};
 
 constexpr int kMaxPieces = 1280;  // of a row: the ranges of the grid (8 per SM) and one more
 
 // One CTA per query row; then, when scoring, CTAs that add the weights of kWeighKeys tokens of a kv head.
-constexpr int kWeighKeys = 1024;
+constexpr int kWeighKeys = 512;
 
 template <bool BF16, bool SCORE>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, const LineGeo g, const long long rows,
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, const LineGeo g, const int rows,
                                                             const int key_blocks)
 {
     pdl_wait();
     pdl_trigger();
     const Problem& pb = a.f.pb;
     __shared__ float weight[kMaxPieces];
-    __shared__ float row_l[1024];
+    __shared__ const float* from[kMaxPieces];
+    __shared__ float row_l[SCORE ? 512 : 1];
     __shared__ float red[kJoinThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int R = g.R;
     const long long cta = static_cast<long long>(blockIdx.x) + static_cast<long long>(gridDim.x) * blockIdx.y;
     const bool is_row = cta < rows;
-    long long bh;  // (sequence, kv head)
-    int block = 0;
+    int bh, block = 0;  // (sequence, kv head)
     if (is_row) {
-        bh = cta / R;
+        bh = static_cast<int>(cta) / R;
     } else {
-        if (!SCORE || cta >= rows + static_cast<long long>(pb.B) * pb.Hkv * key_blocks) return;
-        bh = (cta - rows) / key_blocks;
-        block = static_cast<int>((cta - rows) - bh * key_blocks);
+        const long long rest = cta - rows;
+        if (!SCORE || rest >= static_cast<long long>(pb.B) * pb.Hkv * key_blocks) return;
+        bh = static_cast<int>(rest / key_blocks);
+        block = static_cast<int>(rest - static_cast<long long>(bh) * key_blocks);
     }
-    const int b = static_cast<int>(bh / pb.Hkv), hk = static_cast<int>(bh - static_cast<long long>(b) * pb.Hkv);
+    const int b = bh / pb.Hkv, hk = bh - b * pb.Hkv;
     const int len = clamp_len(a, b);
     if (!is_row && block * kWeighKeys >= len) return;
-    long long total, before;
+    int total, before;
     line_sums(a, g, b, total, before);
-    const int tiles = tiles_of(len, g.kt);
-    auto unit_start = [&](int rb) { return before + (static_cast<long long>(hk) * g.rblocks + rb) * tiles; };
+    const Cuts cuts(g, total);
+    const int tiles = tiles_of(len);
 
     if (is_row) {
-        const int r = static_cast<int>(cta - bh * R);
+        const int r = static_cast<int>(cta) - bh * R;
         const int rb = r / g.rows, ur = r - rb * g.rows;
-        long long g0, g1, p0 = 0, p1 = -1;
-        bool whole, whole_p = false;
-        const long long s0 = unit_start(rb);
-        unit_ranges(g, total, s0, tiles, g0, g1, whole);
-        if (!a.shared && whole) return;  // written by the first kernel
+        const Pieces own(cuts, before + (hk * g.rblocks + rb) * tiles, tiles);
+        if (!a.shared && own.whole) return;  // written by the first kernel
         const int rp = b * R + r, rbp = rp / g.rows, urp = rp - rbp * g.rows;
-        const long long s0p = (static_cast<long long>(hk) * g.rblocks_p + rbp) * g.tiles_p;
-        if (g.rblocks_p) unit_ranges(g, total, s0p, g.tiles_p, p0, p1, whole_p);
-        const int np = g.splits ? g.splits : static_cast<int>(p1 - p0 + 1), no = static_cast<int>(g1 - g0 + 1);
-        const int pieces = np + no;
-        auto l_of = [&](int i) -> float {
-            if (i < np && g.splits) return g.l_split[(static_cast<size_t>(i) * pb.Hkv + hk) * g.Rp + rp];
-            if (i < np)
-                return whole_p ? g.l_whole_p[static_cast<size_t>(hk) * g.Rp + rp]
-                               : g.l_cut[cut_slot(g, total, s0p, p0 + i) * g.rows + urp];
-            return whole ? g.l_whole[bh * R + r] : g.l_cut[cut_slot(g, total, s0, g0 + i - np) * g.rows + ur];
-        };
-        auto o_of = [&](int i) -> const float* {
-            if (i < np && g.splits) return g.o_split + ((static_cast<size_t>(i) * pb.Hkv + hk) * g.Rp + rp) * pb.D;
-            if (i < np)
-                return whole_p ? g.o_whole_p + (static_cast<size_t>(hk) * g.Rp + rp) * pb.D
-                               : g.o_cut + (cut_slot(g, total, s0p, p0 + i) * g.rows + urp) * pb.D;
-            return whole ? g.o_whole + (bh * R + r) * pb.D
-                         : g.o_cut + (cut_slot(g, total, s0, g0 + i - np) * g.rows + ur) * pb.D;
-        };
+        const Pieces pre(cuts, (hk * g.rblocks_p + rbp) * g.tiles_p, g.rblocks_p ? g.tiles_p : 0);
+        const int np = g.splits ? g.splits : pre.count, pieces = np + own.count;
         float mx = -INFINITY;
         for (int i = tid; i < pieces; i += kJoinThreads) {
-            const float l = l_of(i);
-            weight[i] = l;
-            mx = fmaxf(mx, l);
+            size_t at;
+            const float *l, *o;
+            if (i < np && g.splits) {
+                at = (static_cast<size_t>(i) * pb.Hkv + hk) * g.Rp + rp;
+                l = g.l_split;
+                o = g.o_split;
+            } else if (i < np) {
+                at = pre.whole ? static_cast<size_t>(hk) * g.Rp + rp : static_cast<size_t>(pre.slot(i)) * g.rows + urp;
+                l = pre.whole ? g.l_whole_p : g.l_cut;
+                o = pre.whole ? g.o_whole_p : g.o_cut;
+            } else {
+                at = own.whole ? static_cast<size_t>(bh) * R + r : static_cast<size_t>(own.slot(i - np)) * g.rows + ur;
+                l = own.whole ? g.l_whole : g.l_cut;
+                o = own.whole ? g.o_whole : g.o_cut;
+            }
+            weight[i] = l[at];
+            from[i] = o + at * pb.D;
+            mx = fmaxf(mx, weight[i]);
         }
 #pragma unroll
         for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -738,77 +747,75 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
         mx = red[0];
 #pragma unroll
         for (int w = 1; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, red[w]);
+        for (int i = tid; i < pieces; i += kJoinThreads) weight[i] = mx == -INFINITY ? 0.f : exp2f(weight[i] - mx);
+        __syncthreads();
         float sum = 0.f;
-        for (int i = 0; i < pieces; ++i) sum += mx == -INFINITY ? 0.f : exp2f(weight[i] - mx);
+        for (int i = 0; i < pieces; ++i) sum += weight[i];
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const int gg = r / pb.Nq, i = r - gg * pb.Nq;
         uint16_t* out = static_cast<uint16_t*>(a.f.o) + b * pb.vo.sb + (hk * (pb.Hq / pb.Hkv) + gg) * pb.vo.sh + i * pb.vo.sn;
         for (int c = 2 * tid; c < pb.D; c += 2 * kJoinThreads) {
             float v0 = 0.f, v1 = 0.f;
             if (mx > -INFINITY) {
-#pragma unroll 4
+#pragma unroll 8
                 for (int k = 0; k < pieces; ++k) {
-                    const float2 p = *reinterpret_cast<const float2*>(o_of(k) + c);
-                    const float w = exp2f(weight[k] - mx);
-                    v0 = fmaf(w, p.x, v0);
-                    v1 = fmaf(w, p.y, v1);
+                    const float2 p = *reinterpret_cast<const float2*>(from[k] + c);
+                    v0 = fmaf(weight[k], p.x, v0);
+                    v1 = fmaf(weight[k], p.y, v1);
                 }
             }
             *reinterpret_cast<uint32_t*>(out + c) = pack2<BF16>(v0 * inv, v1 * inv);
         }
-        if (tid == 0) a.f.lse[bh * R + r] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+        if (tid == 0) a.f.lse[cta] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
         return;
     }
     if constexpr (SCORE) {
-        // the rows' log2 sums, a warp per row
-        const int batch = 1024;
-        float acc[kWeighKeys / kJoinThreads] = {};
+        constexpr int kBatch = 512, kEach = kWeighKeys / kJoinThreads;
+        float acc[kEach] = {};
         const int j0 = block * kWeighKeys;
-        for (int rbase = 0; rbase < R; rbase += batch) {
-            const int nr = min(batch, R - rbase);
+        for (int rbase = 0; rbase < R; rbase += kBatch) {
+            const int nr = min(kBatch, R - rbase);
             __syncthreads();
-            for (int q = warp; q < nr; q += kJoinThreads / 32) {
-                const int r = rbase + q;
+            // the rows' log2 sums, eight lanes to a row
+            for (int q0 = warp * 4; q0 < nr; q0 += kJoinThreads / 8) {
+                const int q = q0 + (lane >> 3), r = rbase + min(q, nr - 1);
                 const int rb = r / g.rows, ur = r - rb * g.rows;
-                long long g0, g1;
-                bool whole;
-                const long long s0 = unit_start(rb);
-                unit_ranges(g, total, s0, tiles, g0, g1, whole);
-                float l2;
-                if (whole) {
-                    l2 = g.l_whole[bh * R + r];
+                const Pieces own(cuts, before + (hk * g.rblocks + rb) * tiles, tiles);
+                float mx = -INFINITY, sum = 0.f;
+                if (own.whole) {
+                    mx = g.l_whole[static_cast<size_t>(bh) * R + r];
+                    sum = 0.125f;  // of eight lanes
                 } else {
-                    float mx = -INFINITY;
-                    for (long long k = g0 + lane; k <= g1; k += 32)
-                        mx = fmaxf(mx, g.l_cut[cut_slot(g, total, s0, k) * g.rows + ur]);
-#pragma unroll
-                    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    float sum = 0.f;
-                    for (long long k = g0 + lane; k <= g1; k += 32)
-                        if (mx > -INFINITY) sum += exp2f(g.l_cut[cut_slot(g, total, s0, k) * g.rows + ur] - mx);
-#pragma unroll
-                    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                    l2 = sum > 0.f ? mx + log2f(sum) : -INFINITY;
+                    for (int k = lane & 7; k < own.count; k += 8)
+                        mx = fmaxf(mx, g.l_cut[static_cast<size_t>(own.slot(k)) * g.rows + ur]);
                 }
+#pragma unroll
+                for (int d = 4; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                if (!own.whole && mx > -INFINITY)
+                    for (int k = lane & 7; k < own.count; k += 8)
+                        sum += exp2f(g.l_cut[static_cast<size_t>(own.slot(k)) * g.rows + ur] - mx);
+#pragma unroll
+                for (int d = 4; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 // a row that saw no key adds nothing: all its scores are -inf
-                if (lane == 0) row_l[q] = l2 == -INFINITY ? 0.f : l2;
+                if ((lane & 7) == 0 && q < nr) row_l[q] = mx == -INFINITY ? 0.f : mx + log2f(sum);
             }
             __syncthreads();
+            const float* src = g.scores + (static_cast<size_t>(bh) * R + rbase) * g.pitch + j0 + tid;
+            const bool in0 = j0 + tid < len, in1 = j0 + tid + kJoinThreads < len;
+#pragma unroll 8
             for (int q = 0; q < nr; ++q) {
-                const float* src = g.scores + (bh * R + rbase + q) * g.pitch + j0;
                 const float l2 = row_l[q];
-#pragma unroll
-                for (int k = 0; k < kWeighKeys / kJoinThreads; ++k) {
-                    const int j = k * kJoinThreads + tid;
-                    if (j0 + j < len) acc[k] += exp2f(src[j] - l2);
-                }
+                if (in0) acc[0] += exp2f(src[0] - l2);
+                if (in1) acc[1] += exp2f(src[kJoinThreads] - l2);
+                src += g.pitch;
             }
         }
+        static_assert(kEach == 2, "two keys per thread");
 #pragma unroll
-        for (int k = 0; k < kWeighKeys / kJoinThreads; ++k) {
+        for (int k = 0; k < kEach; ++k) {
             const int j = j0 + k * kJoinThreads + tid;
             if (j < len) {
-                const size_t at = bh * pb.Nkv + j;
+                const size_t at = static_cast<size_t>(bh) * pb.Nkv + j;
                 a.oweights[at] = a.weights[at] + acc[k];
             }
         }
@@ -840,7 +847,6 @@ LinePlan line_plan(const Problem& pb, bool shared, int Np)
     const int mt = g.chunks > 8 || most <= 16 ? 1 : 2;
     g.rows = 16 * mt;
     g.rblocks = (g.R + g.rows - 1) / g.rows;
-    g.kt = g.chunks <= 8 && mt == 1 ? 32 : 16;
     if (split) {
         p.prefix = pb;
         p.prefix.B = 1;
@@ -853,19 +859,21 @@ LinePlan line_plan(const Problem& pb, bool shared, int Np)
         g.split_keys = (tiles + g.splits - 1) / g.splits * 128;
     } else if (shared) {
         g.rblocks_p = (g.Rp + g.rows - 1) / g.rows;
-        g.tiles_p = (Np + g.kt - 1) / g.kt;
+        g.tiles_p = (Np + kTileKeys - 1) / kTileKeys;
         if (g.tiles_p == 0) g.rblocks_p = 0;
     }
+    // Groups: what sixteen compute warps hold (eight where a thread needs more
+    // than 120 registers), two at least with sixteen, no more than kMaxGroups.
     g.warps = min(g.chunks, 8);
-    g.groups = 8 / g.warps;
-    g.stage_bytes = 2 * g.kt * g.chunks * 128;
-    const int slots = mt * g.kt / 8 * 2;
+    g.groups = min(kMaxGroups, (mt == 1 && g.chunks <= 8 ? 16 : 8) / g.warps);
+    g.stage_bytes = 2 * kTileKeys * g.chunks * 128;
+    const int slots = mt * kTileKeys / 8 * 2;
     const int exchange = g.warps > 1 ? g.groups * (g.warps + 1) * slots * 256 : 0;
     const int budget = kMaxSmem - static_cast<int>(sizeof(LineStatic)) - kLens * 4 - exchange;
     g.stages = min(kMaxStages, budget / (g.groups * g.stage_bytes));
     p.smem = g.groups * g.stages * g.stage_bytes + exchange;
     p.ctas = num_sms() > 0 ? num_sms() : 152;
-    g.ranges = static_cast<long long>(p.ctas) * g.groups;
+    g.ranges = p.ctas * g.groups;
     g.pitch = (pb.Nkv + 3) & ~3;
     const size_t rows_all = static_cast<size_t>(pb.B) * pb.Hq * pb.Nq, D = pb.D;
     size_t at = 0;
@@ -874,8 +882,8 @@ LinePlan line_plan(const Problem& pb, bool shared, int Np)
         at = up256(at + floats * sizeof(float));
         return here;
     };
-    p.o_cut = take(2 * g.ranges * g.rows * D);
-    p.l_cut = take(2 * g.ranges * g.rows);
+    p.o_cut = take(2 * static_cast<size_t>(g.ranges) * g.rows * D);
+    p.l_cut = take(2 * static_cast<size_t>(g.ranges) * g.rows);
     p.l_whole = take(rows_all);
     if (shared) {
         p.o_whole = take(rows_all * D);
@@ -942,11 +950,11 @@ cudaError_t launch_line(const LineArgs& args, void* workspace, cudaStream_t s)
     pp.B = 1;
     pp.Nkv = a.Np;
     // maps of sides without keys are never read
-    if (pb.Nkv > 0 && (!make_slab_map(&m[0], a.f.k, pb, true, a.f.bf16, g.kt, g.chunks, pb.vk) ||
-                       !make_slab_map(&m[1], a.f.v, pb, true, a.f.bf16, g.kt, g.chunks, pb.vv)))
+    if (pb.Nkv > 0 && (!make_slab_map(&m[0], a.f.k, pb, true, a.f.bf16, kTileKeys, g.chunks, pb.vk) ||
+                       !make_slab_map(&m[1], a.f.v, pb, true, a.f.bf16, kTileKeys, g.chunks, pb.vv)))
         return cudaErrorInvalidValue;
-    if (g.rblocks_p && (!make_slab_map(&m[2], a.kp, pp, true, a.f.bf16, g.kt, g.chunks, a.vkp) ||
-                        !make_slab_map(&m[3], a.vp, pp, true, a.f.bf16, g.kt, g.chunks, a.vvp)))
+    if (g.rblocks_p && (!make_slab_map(&m[2], a.kp, pp, true, a.f.bf16, kTileKeys, g.chunks, a.vkp) ||
+                        !make_slab_map(&m[3], a.vp, pp, true, a.f.bf16, kTileKeys, g.chunks, a.vvp)))
         return cudaErrorInvalidValue;
     cudaError_t e;
     if (g.chunks > 8)
@@ -980,7 +988,7 @@ cudaError_t launch_line(const LineArgs& args, void* workspace, cudaStream_t s)
         x.l_part = g.l_split;
         if ((e = launch_xchg(XOP_FWD, x, s)) != cudaSuccess) return e;
     }
-    const long long rows = static_cast<long long>(pb.B) * pb.Hq * pb.Nq;
+    const int rows = pb.B * pb.Hq * pb.Nq;
     const int key_blocks = a.shared ? 0 : (pb.Nkv + kWeighKeys - 1) / kWeighKeys;
     const long long ctas = rows + static_cast<long long>(pb.B) * pb.Hkv * key_blocks;
     const long long x = ctas < 0x40000000LL ? ctas : 0x40000000LL;
