@@ -674,31 +674,34 @@ struct Pieces {
     __device__ int slot(int i) const { return i == 0 ? 2 * first + 1 : 2 * (first + i); }
 };
 
-constexpr int kMaxPieces = 1280;  // of a row: the ranges of the grid (8 per SM) and one more
-
-// One CTA per query row; then, when scoring, CTAs that add the weights of kWeighKeys tokens of a kv head.
-constexpr int kWeighKeys = 512;
+// A warp per query row and 128 head dims, then, when scoring, a CTA per kWeighKeys
+// tokens of a kv head. The row warps each find their row's pieces again: that is
+// cheaper than sharing them, and short contexts have few.
+constexpr int kWeighKeys = 1024;
+constexpr int kJoinWarps = kJoinThreads / 32;
 
 template <bool BF16, bool SCORE>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, const LineGeo g, const int rows,
-                                                            const int key_blocks)
+                                                            const int row_ctas, const int key_blocks)
 {
     pdl_wait();
     pdl_trigger();
     const Problem& pb = a.f.pb;
-    __shared__ float weight[kMaxPieces];
-    __shared__ const float* from[kMaxPieces];
     __shared__ float row_l[SCORE ? 512 : 1];
-    __shared__ float red[kJoinThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int R = g.R;
     const long long cta = static_cast<long long>(blockIdx.x) + static_cast<long long>(gridDim.x) * blockIdx.y;
-    const bool is_row = cta < rows;
-    int bh, block = 0;  // (sequence, kv head)
+    const bool is_row = cta < row_ctas;
+    const int slices = (pb.D + 127) >> 7;
+    int bh, block = 0, row = 0, slice = 0;  // (sequence, kv head)
     if (is_row) {
-        bh = static_cast<int>(cta) / R;
+        const long long unit = cta * kJoinWarps + warp;
+        if (unit >= static_cast<long long>(rows) * slices) return;  // warps are on their own
+        row = static_cast<int>(unit / slices);
+        slice = static_cast<int>(unit - static_cast<long long>(row) * slices);
+        bh = row / R;
     } else {
-        const long long rest = cta - rows;
+        const long long rest = cta - row_ctas;
         if (!SCORE || rest >= static_cast<long long>(pb.B) * pb.Hkv * key_blocks) return;
         bh = static_cast<int>(rest / key_blocks);
         block = static_cast<int>(rest - static_cast<long long>(bh) * key_blocks);
@@ -712,17 +715,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
     const int tiles = tiles_of(len);
 
     if (is_row) {
-        const int r = static_cast<int>(cta) - bh * R;
+        const int r = row - bh * R;
         const int rb = r / g.rows, ur = r - rb * g.rows;
         const Pieces own(cuts, before + (hk * g.rblocks + rb) * tiles, tiles);
         if (!a.shared && own.whole) return;  // written by the first kernel
         const int rp = b * R + r, rbp = rp / g.rows, urp = rp - rbp * g.rows;
         const Pieces pre(cuts, (hk * g.rblocks_p + rbp) * g.tiles_p, g.rblocks_p ? g.tiles_p : 0);
         const int np = g.splits ? g.splits : pre.count, pieces = np + own.count;
-        float mx = -INFINITY;
-        for (int i = tid; i < pieces; i += kJoinThreads) {
+        auto find = [&](int i, const float*& l, const float*& o) {
             size_t at;
-            const float *l, *o;
             if (i < np && g.splits) {
                 at = (static_cast<size_t>(i) * pb.Hkv + hk) * g.Rp + rp;
                 l = g.l_split;
@@ -736,37 +737,58 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
                 l = own.whole ? g.l_whole : g.l_cut;
                 o = own.whole ? g.o_whole : g.o_cut;
             }
-            weight[i] = l[at];
-            from[i] = o + at * pb.D;
-            mx = fmaxf(mx, weight[i]);
+            l += at;
+            o += at * pb.D;
+        };
+        const int col = slice * 128 + lane * 4;
+        const bool mine = col < pb.D;
+        float mx = -INFINITY, sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        // 32 pieces at a time, a lane for each; the sums are rescaled when a later 32 hold a larger maximum
+        for (int p0 = 0; p0 < pieces; p0 += 32) {
+            const float *l = nullptr, *o = nullptr;
+            float w = -INFINITY;
+            if (p0 + lane < pieces) {
+                find(p0 + lane, l, o);
+                w = *l;
+            }
+            float top = w;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            if (top == -INFINITY) continue;
+            const float now = fmaxf(mx, top), scale = mx == -INFINITY ? 0.f : exp2f(mx - now);
+            mx = now;
+            w = w == -INFINITY ? 0.f : exp2f(w - now);
+            float part = w;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+            sum = sum * scale + part;
+            v.x *= scale;
+            v.y *= scale;
+            v.z *= scale;
+            v.w *= scale;
+            const int n = min(32, pieces - p0);
+#pragma unroll 8
+            for (int k = 0; k < n; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, k);
+                const float* ok = reinterpret_cast<const float*>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), k));
+                if (mine) {
+                    const float4 p = *reinterpret_cast<const float4*>(ok + col);
+                    v.x = fmaf(wk, p.x, v.x);
+                    v.y = fmaf(wk, p.y, v.y);
+                    v.z = fmaf(wk, p.z, v.z);
+                    v.w = fmaf(wk, p.w, v.w);
+                }
+            }
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        if (lane == 0) red[warp] = mx;
-        __syncthreads();
-        mx = red[0];
-#pragma unroll
-        for (int w = 1; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, red[w]);
-        for (int i = tid; i < pieces; i += kJoinThreads) weight[i] = mx == -INFINITY ? 0.f : exp2f(weight[i] - mx);
-        __syncthreads();
-        float sum = 0.f;
-        for (int i = 0; i < pieces; ++i) sum += weight[i];
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const int gg = r / pb.Nq, i = r - gg * pb.Nq;
         uint16_t* out = static_cast<uint16_t*>(a.f.o) + b * pb.vo.sb + (hk * (pb.Hq / pb.Hkv) + gg) * pb.vo.sh + i * pb.vo.sn;
-        for (int c = 2 * tid; c < pb.D; c += 2 * kJoinThreads) {
-            float v0 = 0.f, v1 = 0.f;
-            if (mx > -INFINITY) {
-#pragma unroll 8
-                for (int k = 0; k < pieces; ++k) {
-                    const float2 p = *reinterpret_cast<const float2*>(from[k] + c);
-                    v0 = fmaf(weight[k], p.x, v0);
-                    v1 = fmaf(weight[k], p.y, v1);
-                }
-            }
-            *reinterpret_cast<uint32_t*>(out + c) = pack2<BF16>(v0 * inv, v1 * inv);
-        }
-        if (tid == 0) a.f.lse[cta] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+        if (mine)
+            *reinterpret_cast<uint2*>(out + col) =
+                make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
+        if (slice == 0 && lane == 0) a.f.lse[row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
         return;
     }
     if constexpr (SCORE) {
@@ -801,16 +823,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
             }
             __syncthreads();
             const float* src = g.scores + (static_cast<size_t>(bh) * R + rbase) * g.pitch + j0 + tid;
-            const bool in0 = j0 + tid < len, in1 = j0 + tid + kJoinThreads < len;
-#pragma unroll 8
+#pragma unroll 4
             for (int q = 0; q < nr; ++q) {
                 const float l2 = row_l[q];
-                if (in0) acc[0] += exp2f(src[0] - l2);
-                if (in1) acc[1] += exp2f(src[kJoinThreads] - l2);
+#pragma unroll
+                for (int k = 0; k < kEach; ++k)
+                    if (j0 + k * kJoinThreads + tid < len) acc[k] += exp2f(src[k * kJoinThreads] - l2);
                 src += g.pitch;
             }
         }
-        static_assert(kEach == 2, "two keys per thread");
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int j = j0 + k * kJoinThreads + tid;
@@ -990,12 +1011,13 @@ cudaError_t launch_line(const LineArgs& args, void* workspace, cudaStream_t s)
     }
     const int rows = pb.B * pb.Hq * pb.Nq;
     const int key_blocks = a.shared ? 0 : (pb.Nkv + kWeighKeys - 1) / kWeighKeys;
-    const long long ctas = rows + static_cast<long long>(pb.B) * pb.Hkv * key_blocks;
+    const int row_ctas = static_cast<int>((static_cast<long long>(rows) * ((pb.D + 127) >> 7) + kJoinWarps - 1) / kJoinWarps);
+    const long long ctas = row_ctas + static_cast<long long>(pb.B) * pb.Hkv * key_blocks;
     const long long x = ctas < 0x40000000LL ? ctas : 0x40000000LL;
     const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>((ctas + x - 1) / x));
     auto join = a.f.bf16 ? (a.shared ? join_kernel<true, false> : join_kernel<true, true>)
                          : (a.shared ? join_kernel<false, false> : join_kernel<false, true>);
-    return launch_dependent(join, grid, kJoinThreads, 0, s, a, g, rows, key_blocks);
+    return launch_dependent(join, grid, kJoinThreads, 0, s, a, g, rows, row_ctas, key_blocks);
 }
 
 }  // namespace ffpa

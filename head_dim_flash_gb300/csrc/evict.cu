@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelEach = 4;       // keys per thread and tile of the ordered pass
+constexpr int kHeld = 16;         // keys per thread kept in registers over the passes
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 8;     // 16-byte pieces that a thread has in flight
@@ -101,15 +102,25 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     uint32_t known = 0, bits = 0;
     int left = places;
     if (places > 0) {
+        // the first 16384 keys stay in registers; the others are read again (L2)
+        uint32_t held[kHeld];
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            const int i = j * kSelThreads + tid;
+            held[j] = i < early ? score_key(w[i]) : 0u;
+        }
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             const int width = pass < 2 ? 11 : 10, shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
             __syncthreads();
-            for (int i = tid; i < early; i += kSelThreads) {
-                const uint32_t key = score_key(w[i]);
+            auto count = [&](uint32_t key) {
                 if ((key & bits) == known) atomicAdd(&hist[(key >> shift) & ((1u << width) - 1)], 1);
-            }
+            };
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j)
+                if (j * kSelThreads + tid < early) count(held[j]);
+            for (int i = kHeld * kSelThreads + tid; i < early; i += kSelThreads) count(score_key(w[i]));
             __syncthreads();
             // bins from the largest down, two per thread
             const int hi = kBins - 1 - 2 * tid;
