@@ -791,10 +791,55 @@ def rope_plan(rot_dim: int, base: float = 10000.0, interleaved: bool = False, sc
     return RopePlan(turns.to(device), interleaved, m)
 
 
+# The calls below run once per layer and token as well, on tensors of a few
+# kilobytes. What follows from shapes, strides, types and devices alone is worked
+# out once for each combination of them.
+def _meta(x):
+    """All that a layout is looked up by."""
+    return x.shape, x.stride(), x.dtype, x.device
+
+
+@functools.lru_cache(maxsize=1024)
+def _view_strides(shape, stride):
+    """Strides of the ffpa_view of a dense tensor whose address allows one, or None (as _view_or_none)."""
+    (B, H, N, _), (sb, sh, sn, sd) = shape, stride
+    if sd != 1 or (sb | sh | sn) & 7 or sb < 0 or sh < 0 or sn < 0:
+        return None
+    if B > 1 and sb == 0 or H > 1 and sh == 0 or N > 1 and sn == 0:
+        return None
+    return sb, sh, sn
+
+
+@functools.lru_cache(maxsize=1024)
+def _like_strides(shape, stride):
+    """Strides that torch.empty_like gives a tensor, where they fit an ffpa_view; else contiguous ones."""
+    like = torch.empty_like(torch.empty_strided(shape, stride, dtype=torch.uint8, device="meta")).stride()
+    return like if _view_strides(shape, like) else torch.empty(shape, dtype=torch.uint8, device="meta").stride()
+
+
+def _in4(x, strides):
+    """(tensor, its ffpa_view) of an input whose _view_strides are known; copied only where no view of it fits."""
+    p = x.data_ptr()
+    if strides is None or p & 15:
+        x = x.clone(memory_format=torch.contiguous_format)
+        return x, _view(x)
+    return x, _ffi.View(p, *strides)
+
+
+def _out4(x, out, like, name: str):
+    """(tensor, its ffpa_view) of an output: new with strides `like`, or `out`, checked against x."""
+    if out is None:
+        out = torch.empty_strided(x.shape, like, dtype=x.dtype, device=x.device)
+        return out, _ffi.View(out.data_ptr(), *like[:3])
+    if out is not x and (out.shape != x.shape or out.dtype != x.dtype or out.device != x.device):
+        raise ValueError(f"{name} must have its input's shape, dtype and device")
+    return out, _out_view(out)
+
+
 def _rope_positions(start, positions, B: int, shape, dev):
-    if start is not None and positions is not None:
-        raise ValueError("give start or positions, not both")
     if positions is not None:
+        if start is not None:
+            raise ValueError("give start or positions, not both")
         if positions.dtype is not torch.int32 or positions.shape != shape or not positions.is_contiguous() \
                 or positions.device != dev:
             raise ValueError(f"positions must be a contiguous int32 {list(shape)} tensor on {dev}")
@@ -805,60 +850,54 @@ def _rope_positions(start, positions, B: int, shape, dev):
 _NO_VIEW = _ffi.View(None, 0, 0, 0)
 
 
-def _rope_out(x, out, name: str):
-    if out is None:
-        out = torch.empty_like(x)
-        w = _view_or_none(out)
-        if w is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            w = _view(out)
-        return out, w
-    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
-        raise ValueError(f"{name} must have its input's shape, dtype and device")
-    return out, _out_view(out)
-
-
-def _rope_pair(q, k, plan: RopePlan, dims: int):
-    """Shared checks; returns the device."""
-    dev = q.device
-    if dev.type != "cuda" or plan.turns.device != dev:
+@functools.lru_cache(maxsize=512)
+def _rope_layout(q, k, plan_device, dims: int):
+    """Checks of a pair's shapes and types; (device, its index, ABI type, strides of the views and of new outputs)."""
+    shape, stride, dtype, dev = q
+    if dev.type != "cuda" or plan_device != dev:
         raise ValueError("q and the plan must be on one CUDA device")
-    if q.dim() != dims:
+    if len(shape) != dims:
         raise ValueError("expected q [B,Hq,N,D]" if dims == 4 else "expected q [T,Hq,D]")
     if k is not None:
-        if k.dim() != dims or k.shape[-1] != q.shape[-1] or k.shape[0] != q.shape[0] or \
-                dims == 4 and k.shape[2] != q.shape[2]:
-            raise ValueError(f"k {tuple(k.shape)} does not match q {tuple(q.shape)}")
-        if k.device != dev:
+        ks = k[0]
+        if len(ks) != dims or ks[-1] != shape[-1] or ks[0] != shape[0] or dims == 4 and ks[2] != shape[2]:
+            raise ValueError(f"k {tuple(ks)} does not match q {tuple(shape)}")
+        if k[3] != dev:
             raise ValueError("q and k are on different devices")
-        if k.dtype != q.dtype:
-            raise ValueError(f"mixed dtypes {q.dtype} and {k.dtype}")
-    return dev
+        if k[2] != dtype:
+            raise ValueError(f"mixed dtypes {dtype} and {k[2]}")
+    if dtype not in _DTYPES:
+        raise NotImplementedError(f"dtype {dtype}: only torch.bfloat16 and torch.float16 are supported")
+    views = ()
+    if dims == 4:
+        views = tuple((_view_strides(*x[:2]), _like_strides(*x[:2])) for x in (q, k) if x is not None)
+    return dev, dev.index, _DTYPES[dtype], views
 
 
 def _rope_dense(q, k, plan, start, positions, inverse, q_out=None, k_out=None):
-    dev = _rope_pair(q, k, plan, 4)
-    if _elsewhere(dev):
+    dev, index, dt, views = _rope_layout(_meta(q), None if k is None else _meta(k), plan.turns.device, 4)
+    if index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _rope_dense(q, k, plan, start, positions, inverse, q_out, k_out)
     B, Hq, N, D = q.shape
     ps, pp = _rope_positions(start, positions, B, (B, N), dev)
-    q, wq = _in_view(q)
-    q_out, woq = _rope_out(q, q_out, "q_out")
+    x, wq = _in4(q, views[0][0])
+    q_out, woq = _out4(q, q_out, views[0][1], "q_out")
     Hk, wk, wok = 0, _NO_VIEW, _NO_VIEW
+    y = None  # (x and y keep copies alive until the call is made)
     if k is not None:
         Hk = k.shape[1]
-        k, wk = _in_view(k)
-        k_out, wok = _rope_out(k, k_out, "k_out")
-    st = _ffi.load().ffpa_rope(_dt(q), wq, wk, woq, wok, plan._c, ps, pp, B, Hq, Hk, N, D, inverse, _raw_stream(dev))
+        y, wk = _in4(k, views[1][0])
+        k_out, wok = _out4(k, k_out, views[1][1], "k_out")
+    st = _ffi.load().ffpa_rope(dt, wq, wk, woq, wok, plan._c, ps, pp, B, Hq, Hk, N, D, inverse, _raw_stream(dev))
     if st:
         _ffi.raise_for(st, "ffpa_rope")
     return q_out, k_out
 
 
 def _rope_packed(q, k, plan, cu, start, positions, inverse, q_out=None, k_out=None):
-    dev = _rope_pair(q, k, plan, 3)
-    if _elsewhere(dev):
+    dev, index, dt, _ = _rope_layout(_meta(q), None if k is None else _meta(k), plan.turns.device, 3)
+    if index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _rope_packed(q, k, plan, cu, start, positions, inverse, q_out, k_out)
     T, Hq, D = q.shape
@@ -871,7 +910,8 @@ def _rope_packed(q, k, plan, cu, start, positions, inverse, q_out=None, k_out=No
             continue
         if out is None:
             # rows of no sequence are not written
-            out = torch.zeros(x.shape, dtype=x.dtype, device=dev) if inverse else torch.empty(x.shape, dtype=x.dtype, device=dev)
+            new = torch.zeros if inverse else torch.empty
+            out = new(x.shape, dtype=x.dtype, device=dev)
         elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
             raise ValueError(f"{name} must be contiguous, with its input's shape, dtype and device")
         outs.append(out)
@@ -879,7 +919,7 @@ def _rope_packed(q, k, plan, cu, start, positions, inverse, q_out=None, k_out=No
     if k is not None:
         Hk, k = k.shape[1], _in_packed(k)
         pk, pok = k.data_ptr(), outs[1].data_ptr()
-    st = _ffi.load().ffpa_varlen_rope(_dt(q), q.data_ptr(), pk, outs[0].data_ptr(), pok, plan._c,
+    st = _ffi.load().ffpa_varlen_rope(dt, q.data_ptr(), pk, outs[0].data_ptr(), pok, plan._c,
                                       _lengths(cu, B + 1, "cu_seqlens", dev), ps, pp, B, T, Hq, Hk, D, inverse,
                                       _raw_stream(dev))
     if st:
@@ -965,35 +1005,31 @@ def decode_weights_workspace(q, k) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
-def _line_checks(q, *caches):
-    shape = q.shape
+@functools.lru_cache(maxsize=512)
+def _line_layout(q, *caches):
+    """Checks of the shapes and types of queries and caches (k, v, batch); (device, its index, ABI type, strides of
+    the views of q and the caches, strides of a new output)."""
+    shape, stride, dtype, dev = q
     if len(shape) != 4:
         raise ValueError("expected q [B,Hq,Nq,D]")
-    dev, dt = q.device, q.dtype
     if dev.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
-    for k, v, batch in caches:
-        ks = k.shape
-        if len(ks) != 4 or v.shape != ks or ks[0] != batch or ks[3] != shape[3] or ks[1] != caches[-1][0].shape[1]:
-            raise ValueError(f"k {tuple(ks)} and v {tuple(v.shape)} do not match q {tuple(shape)}")
-        if k.device != dev or v.device != dev:
+    for k, v, own in caches:
+        ks = k[0]
+        if len(ks) != 4 or v[0] != ks or ks[0] != (shape[0] if own else 1) or ks[3] != shape[3] or \
+                ks[1] != caches[-1][0][0][1]:
+            raise ValueError(f"k {tuple(ks)} and v {tuple(v[0])} do not match q {tuple(shape)}")
+        if k[3] != dev or v[3] != dev:
             raise ValueError("q, k and v must be on one device")
-        if k.dtype != dt or v.dtype != dt:
-            raise ValueError(f"mixed dtypes {dt}, {k.dtype} and {v.dtype}")
-    return shape, dev
+        if k[2] != dtype or v[2] != dtype:
+            raise ValueError(f"mixed dtypes {dtype}, {k[2]} and {v[2]}")
+    if dtype not in _DTYPES:
+        raise NotImplementedError(f"dtype {dtype}: only torch.bfloat16 and torch.float16 are supported")
+    views = [_view_strides(*q[:2])] + [_view_strides(*x[:2]) for c in caches for x in c[:2]]
+    return dev, dev.index, _DTYPES[dtype], views, _like_strides(shape, stride)
 
 
-def _line_outputs(q, shape, dev, out, lse, workspace, workspace_bytes):
-    if out is None:
-        out = torch.empty_like(q)
-        wo = _view_or_none(out)
-        if wo is None:
-            out = torch.empty(shape, dtype=q.dtype, device=dev)
-            wo = _view(out)
-    elif out.shape != shape or out.dtype != q.dtype or out.device != dev:
-        raise ValueError("out must have q's shape, dtype and device")
-    else:
-        wo = _out_view(out)
+def _line_scratch(shape, dev, lse, workspace, workspace_bytes):
     if lse is None:
         lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
     elif not lse.is_contiguous() or lse.dtype != torch.float32 or lse.shape != shape[:3] or lse.device != dev:
@@ -1004,7 +1040,7 @@ def _line_outputs(q, shape, dev, out, lse, workspace, workspace_bytes):
         raise ValueError("workspace must be contiguous and on q's device")
     else:
         workspace_bytes = workspace.numel() * workspace.element_size()
-    return out, wo, lse, workspace, workspace_bytes
+    return lse, workspace, workspace_bytes
 
 
 def decode_fwd_shared(q, k_prefix, v_prefix, k, v, lens=None, causal: bool = False, scale: float | None = None,
@@ -1014,17 +1050,18 @@ def decode_fwd_shared(q, k_prefix, v_prefix, k, v, lens=None, causal: bool = Fal
     lens[b] rows of its own cache (k, v [B, Hkv, N, D]; int32 [B] on the device, None: N each);
     causal is bottom-right over all of them. The prefix is read once for the batch.
     q [B, Hq, Nq, D]; returns (o, lse)."""
-    shape, dev = _line_checks(q, (k_prefix, v_prefix, 1), (k, v, q.shape[0]))
-    if _elsewhere(dev):
+    dev, index, dt, views, like = _line_layout(_meta(q), (_meta(k_prefix), _meta(v_prefix), False),
+                                               (_meta(k), _meta(v), True))
+    if index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return decode_fwd_shared(q, k_prefix, v_prefix, k, v, lens, causal, scale, out, lse, workspace)
-    B, Hq, Nq, D = shape
+    shape = B, Hq, Nq, D = q.shape
     Hkv, N, Np = k.shape[1], k.shape[2], k_prefix.shape[2]
-    dt = _dt(q)
-    q, wq = _in_view(q)
-    (kp, wkp), (vp, wvp), (k, wk), (v, wv) = _in_view(k_prefix), _in_view(v_prefix), _in_view(k), _in_view(v)
-    need = 0 if workspace is not None else _shared_workspace_bytes(dev.index, dt, B, Hq, Hkv, Nq, Np, N, D)
-    out, wo, lse, workspace, n = _line_outputs(q, shape, dev, out, lse, workspace, need)
+    (x, wq), (kp, wkp), (vp, wvp), (k, wk), (v, wv) = (
+        _in4(t, w) for t, w in zip((q, k_prefix, v_prefix, k, v), views))
+    out, wo = _out4(q, out, like, "out")
+    need = 0 if workspace is not None else _shared_workspace_bytes(index, dt, B, Hq, Hkv, Nq, Np, N, D)
+    lse, workspace, n = _line_scratch(shape, dev, lse, workspace, need)
     st = _ffi.load().ffpa_decode_fwd_shared(dt, wq, wkp, wvp, wk, wv, _lengths(lens, B, "lens", dev), wo,
                                             lse.data_ptr(), workspace.data_ptr(), n, B, Hq, Hkv, Nq, Np, N, D,
                                             int(bool(causal)), _scale(scale, D), _raw_stream(dev))
@@ -1047,27 +1084,46 @@ def decode_fwd_weights(q, k, v, weights, lens=None, causal: bool = False, scale:
     N each), and the softmax weight that each gets from the rows of its kv head is added to
     weights [B, Hkv, N] (fp32), in place or into weights_out. q [B, Hq, Nq, D]; returns
     (o, lse, weights_out)."""
-    shape, dev = _line_checks(q, (k, v, q.shape[0]))
-    if _elsewhere(dev):
+    dev, index, dt, views, like = _line_layout(_meta(q), (_meta(k), _meta(v), True))
+    if index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return decode_fwd_weights(q, k, v, weights, lens, causal, scale, out, lse, weights_out, workspace)
-    B, Hq, Nq, D = shape
+    shape = B, Hq, Nq, D = q.shape
     Hkv, N = k.shape[1], k.shape[2]
-    dt = _dt(q)
     if weights_out is None:
         weights_out = weights
     pw = _weights_ptr(weights, (B, Hkv, N), "weights", dev)
     po = _weights_ptr(weights_out, (B, Hkv, N), "weights_out", dev)
-    q, wq = _in_view(q)
-    (k, wk), (v, wv) = _in_view(k), _in_view(v)
-    need = 0 if workspace is not None else _weights_workspace_bytes(dev.index, dt, B, Hq, Hkv, Nq, N, D)
-    out, wo, lse, workspace, n = _line_outputs(q, shape, dev, out, lse, workspace, need)
+    (x, wq), (k, wk), (v, wv) = (_in4(t, w) for t, w in zip((q, k, v), views))
+    out, wo = _out4(q, out, like, "out")
+    need = 0 if workspace is not None else _weights_workspace_bytes(index, dt, B, Hq, Hkv, Nq, N, D)
+    lse, workspace, n = _line_scratch(shape, dev, lse, workspace, need)
     st = _ffi.load().ffpa_decode_fwd_weights(dt, wq, wk, wv, _lengths(lens, B, "lens", dev), pw, po, wo,
                                              lse.data_ptr(), workspace.data_ptr(), n, B, Hq, Hkv, Nq, N, D,
                                              int(bool(causal)), _scale(scale, D), _raw_stream(dev))
     if st:
         _ffi.raise_for(st, "ffpa_decode_fwd_weights")
     return out, lse, weights_out
+
+
+@functools.lru_cache(maxsize=512)
+def _evict_layout(k, v, k_out, v_out):
+    """Checks of the shapes and types of an eviction's caches; (device, its index, ABI type, strides of k's and v's views)."""
+    shape, _, dtype, dev = k
+    if len(shape) != 4 or v[0] != shape:
+        raise ValueError("expected k and v [B,Hkv,N,D]")
+    if dev.type != "cuda" or v[3] != dev:
+        raise ValueError("k and v must be on one CUDA device")
+    if v[2] != dtype:
+        raise ValueError(f"mixed dtypes {dtype} and {v[2]}")
+    if dtype not in _DTYPES:
+        raise NotImplementedError(f"dtype {dtype}: only torch.bfloat16 and torch.float16 are supported")
+    for x, name in ((k_out, "k_out"), (v_out, "v_out")):
+        s = x[0]
+        if len(s) != 4 or (s[0], s[1], s[3]) != (shape[0], shape[1], shape[3]) or s[2] != k_out[0][2] or \
+                x[2] != dtype or x[3] != dev:
+            raise ValueError(f"{name} must be [B, Hkv, N_out, D] of k's dtype on k's device")
+    return dev, dev.index, _DTYPES[dtype], (_view_strides(*k[:2]), _view_strides(*v[:2]))
 
 
 def kv_evict(k, v, weights, lens, keep: int, recent: int = 0, k_out=None, v_out=None, weights_out=None,
@@ -1078,43 +1134,34 @@ def kv_evict(k, v, weights, lens, keep: int, recent: int = 0, k_out=None, v_out=
     v_out [B, Hkv, N_out, D], weights_out [B, Hkv, N_out] and lens_out; rows behind the kept
     ones are left as they are. Returns (k_out, v_out, weights_out, lens_out, kept), kept int32
     [B, Hkv, keep]: where each token was, -1 behind the last."""
-    shape, dev = k.shape, k.device
-    if len(shape) != 4 or v.shape != shape:
-        raise ValueError("expected k and v [B,Hkv,N,D]")
-    if dev.type != "cuda" or v.device != dev:
-        raise ValueError("k and v must be on one CUDA device")
-    if v.dtype != k.dtype:
-        raise ValueError(f"mixed dtypes {k.dtype} and {v.dtype}")
     if (k_out is None) != (v_out is None) or (k_out is None) != (weights_out is None):
         raise ValueError("give k_out, v_out and weights_out together, or none of them")
     if lens is None:
         raise ValueError("lens is required")
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return kv_evict(k, v, weights, lens, keep, recent, k_out, v_out, weights_out, lens_out)
-    B, Hkv, N, D = shape
-    if k_out is None:
+    in_place = k_out is None
+    if in_place:
         k_out, v_out, weights_out = k, v, weights
-        wk, wv = _out_view(k), _out_view(v)  # in place: no copy would do
-        wok, wov, Nout = wk, wv, N
-        if lens_out is None:
-            lens_out = lens
+    dev, index, dt, views = _evict_layout(_meta(k), _meta(v), _meta(k_out), _meta(v_out))
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            if in_place:
+                return kv_evict(k, v, weights, lens, keep, recent, lens_out=lens_out)
+            return kv_evict(k, v, weights, lens, keep, recent, k_out, v_out, weights_out, lens_out)
+    B, Hkv, N, D = k.shape
+    Nout = k_out.shape[2]
+    if in_place:
+        wk, wv = wok, wov = _out_view(k), _out_view(v)  # no copy would do
     else:
-        Nout = k_out.shape[2] if k_out.dim() == 4 else -1
-        for x, name in ((k_out, "k_out"), (v_out, "v_out")):
-            if x.shape != (B, Hkv, Nout, D) or x.dtype != k.dtype or x.device != dev:
-                raise ValueError(f"{name} must be [B, Hkv, N_out, D] of k's dtype on k's device")
-        k, wk = _in_view(k)
-        v, wv = _in_view(v)
+        (k, wk), (v, wv) = _in4(k, views[0]), _in4(v, views[1])
         wok, wov = _out_view(k_out), _out_view(v_out)
-        if lens_out is None:
-            lens_out = torch.empty_like(lens)
+    if lens_out is None:
+        lens_out = lens if in_place else torch.empty_like(lens)
     pw = _weights_ptr(weights, (B, Hkv, N), "weights", dev)
     po = _weights_ptr(weights_out, (B, Hkv, Nout), "weights_out", dev)
     if keep < 1:
         raise ValueError(f"keep={keep} must be positive")
     kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev)
-    st = _ffi.load().ffpa_kv_evict(_dt(k), wk, wv, pw, _lengths(lens, B, "lens", dev), wok, wov, po,
+    st = _ffi.load().ffpa_kv_evict(dt, wk, wv, pw, _lengths(lens, B, "lens", dev), wok, wov, po,
                                    _lengths(lens_out, B, "lens_out", dev), kept.data_ptr(), B, Hkv, N, Nout, D,
                                    int(keep), int(recent), _raw_stream(dev))
     if st:

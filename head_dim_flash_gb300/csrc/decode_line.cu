@@ -122,13 +122,14 @@ __device__ __forceinline__ int clamp_len(const LineArgs& a, int b)
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTileKeys - 1) / kTileKeys; }
 
 // Tiles of the whole line (below 2^31), and those before sequence `b` (by whole warps).
-__device__ __forceinline__ void line_sums(const LineArgs& a, const LineGeo& g, int b, int& total, int& before)
+__device__ __forceinline__ void line_sums(const LineArgs& a, const LineGeo& g, const int* staged, int b, int& total,
+                                          int& before)
 {
     const Problem& pb = a.f.pb;
     int t = 0, p = 0;
 #pragma unroll 4
     for (int i = threadIdx.x & 31; i < pb.B; i += 32) {
-        const int n = tiles_of(clamp_len(a, i));
+        const int n = tiles_of(staged ? staged[i] : clamp_len(a, i));
         t += n;
         if (i < b) p += n;
     }
@@ -253,8 +254,6 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
                 const __grid_constant__ CUtensorMap tKp, const __grid_constant__ CUtensorMap tVp, const LineArgs a,
                 const LineGeo g)
 {
-    pdl_wait();
-    pdl_trigger();
     constexpr int KT = kTileKeys, NT = KT / 8, ROWS = 16 * MT;
     constexpr int SLOTS = MT * NT * 2;  // float2 a lane holds of a tile's scores
     const Problem& pb = a.f.pb;
@@ -264,11 +263,23 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = g.stages;
     if (smem_u32(smem) & 1023u) {
+        pdl_wait();
         if (threadIdx.x == 0) atomicCAS(a.f.ctl.status, 0u, 5u | (0xffu << 8));
         return;
     }
     if (threadIdx.x < g.groups * S) mbar_init(&sh.full[threadIdx.x / S][threadIdx.x % S], 1);
-    if (threadIdx.x == 0) sh.abort_flag = 0;
+    if (threadIdx.x == 0) {
+        sh.abort_flag = 0;
+        prefetch_tmap(&tK);
+        prefetch_tmap(&tV);
+        if (g.rblocks_p) {
+            prefetch_tmap(&tKp);
+            prefetch_tmap(&tVp);
+        }
+    }
+    fence_barrier_init();
+    pdl_wait();  // from here on, what the kernel before wrote
+    pdl_trigger();
     if (a.lens)
         for (int i = threadIdx.x; i < pb.B; i += blockDim.x) {
             const int n = a.lens[i];
@@ -290,11 +301,10 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
                 static_cast<const uint16_t*>(a.f.q) + b * pb.vq.sb + (hk * (pb.Hq / pb.Hkv) + gg) * pb.vq.sh + i * pb.vq.sn + col);
         }
     }
-    fence_barrier_init();
     __syncthreads();
     const Line line{a, g, a.lens && pb.B <= kLens ? s_len : nullptr};
     int total, unused;
-    line_sums(a, g, 0, total, unused);
+    line_sums(a, g, line.lens, 0, total, unused);
     const Cuts cuts(g, total);
     volatile int* abort_p = &sh.abort_flag;
     uint32_t* status = a.f.ctl.status;
@@ -679,6 +689,7 @@ struct Pieces {
 // cheaper than sharing them, and short contexts have few.
 constexpr int kWeighKeys = 1024;
 constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinLoads = 16;  // pieces of a row on their way at once
 
 template <bool BF16, bool SCORE>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, const LineGeo g, const int rows,
@@ -695,22 +706,22 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
     const int slices = (pb.D + 127) >> 7;
     int bh, block = 0, row = 0, slice = 0;  // (sequence, kv head)
     if (is_row) {
-        const long long unit = cta * kJoinWarps + warp;
-        if (unit >= static_cast<long long>(rows) * slices) return;  // warps are on their own
+        const unsigned unit = static_cast<unsigned>(cta) * kJoinWarps + warp;  // below 2^32: line_fits
+        if (unit >= static_cast<unsigned>(rows) * slices) return;  // warps are on their own
         row = static_cast<int>(unit / slices);
-        slice = static_cast<int>(unit - static_cast<long long>(row) * slices);
+        slice = static_cast<int>(unit - static_cast<unsigned>(row) * slices);
         bh = row / R;
     } else {
-        const long long rest = cta - row_ctas;
-        if (!SCORE || rest >= static_cast<long long>(pb.B) * pb.Hkv * key_blocks) return;
+        const unsigned rest = static_cast<unsigned>(cta - row_ctas);
+        if (!SCORE || rest >= static_cast<unsigned>(pb.B) * pb.Hkv * key_blocks) return;
         bh = static_cast<int>(rest / key_blocks);
-        block = static_cast<int>(rest - static_cast<long long>(bh) * key_blocks);
+        block = static_cast<int>(rest - static_cast<unsigned>(bh) * key_blocks);
     }
     const int b = bh / pb.Hkv, hk = bh - b * pb.Hkv;
     const int len = clamp_len(a, b);
     if (!is_row && block * kWeighKeys >= len) return;
     int total, before;
-    line_sums(a, g, b, total, before);
+    line_sums(a, g, nullptr, b, total, before);
     const Cuts cuts(g, total);
     const int tiles = tiles_of(len);
 
@@ -767,18 +778,26 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
             v.y *= scale;
             v.z *= scale;
             v.w *= scale;
+            // sixteen loads in flight; past the last piece, its own again with no weight
             const int n = min(32, pieces - p0);
-#pragma unroll 8
-            for (int k = 0; k < n; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, w, k);
-                const float* ok = reinterpret_cast<const float*>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), k));
-                if (mine) {
-                    const float4 p = *reinterpret_cast<const float4*>(ok + col);
-                    v.x = fmaf(wk, p.x, v.x);
-                    v.y = fmaf(wk, p.y, v.y);
-                    v.z = fmaf(wk, p.z, v.z);
-                    v.w = fmaf(wk, p.w, v.w);
+            for (int k0 = 0; k0 < n; k0 += kJoinLoads) {
+                float4 p[kJoinLoads];
+#pragma unroll
+                for (int k = 0; k < kJoinLoads; ++k) {
+                    const float* ok = reinterpret_cast<const float*>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), min(k0 + k, n - 1)));
+                    if (mine) p[k] = *reinterpret_cast<const float4*>(ok + col);
+                }
+#pragma unroll
+                for (int k = 0; k < kJoinLoads; ++k) {
+                    const float ws = __shfl_sync(0xffffffffu, w, min(k0 + k, n - 1));
+                    const float wk = k0 + k < n ? ws : 0.f;
+                    if (mine) {
+                        v.x = fmaf(wk, p[k].x, v.x);
+                        v.y = fmaf(wk, p[k].y, v.y);
+                        v.z = fmaf(wk, p[k].z, v.z);
+                        v.w = fmaf(wk, p[k].w, v.w);
+                    }
                 }
             }
         }
@@ -793,8 +812,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
     }
     if constexpr (SCORE) {
         constexpr int kBatch = 512, kEach = kWeighKeys / kJoinThreads;
-        float acc[kEach] = {};
+        float acc[kEach], old[kEach];
         const int j0 = block * kWeighKeys;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int j = j0 + k * kJoinThreads + tid;
+            old[k] = j < len ? a.weights[static_cast<size_t>(bh) * pb.Nkv + j] : 0.f;
+            acc[k] = 0.f;
+        }
         for (int rbase = 0; rbase < R; rbase += kBatch) {
             const int nr = min(kBatch, R - rbase);
             __syncthreads();
@@ -808,6 +833,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
                     mx = g.l_whole[static_cast<size_t>(bh) * R + r];
                     sum = 0.125f;  // of eight lanes
                 } else {
+#pragma unroll 4
                     for (int k = lane & 7; k < own.count; k += 8)
                         mx = fmaxf(mx, g.l_cut[static_cast<size_t>(own.slot(k)) * g.rows + ur]);
                 }
@@ -823,13 +849,24 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
             }
             __syncthreads();
             const float* src = g.scores + (static_cast<size_t>(bh) * R + rbase) * g.pitch + j0 + tid;
-#pragma unroll 4
-            for (int q = 0; q < nr; ++q) {
-                const float l2 = row_l[q];
+            // four rows' scores in flight; rows and keys past the last are read again and not added
+            int at[kEach];
 #pragma unroll
-                for (int k = 0; k < kEach; ++k)
-                    if (j0 + k * kJoinThreads + tid < len) acc[k] += exp2f(src[k * kJoinThreads] - l2);
-                src += g.pitch;
+            for (int k = 0; k < kEach; ++k) at[k] = min(k * kJoinThreads, len - 1 - j0 - tid);
+            for (int q0 = 0; q0 < nr; q0 += 4) {
+                float x[4][kEach];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k)
+                        x[q][k] = src[static_cast<size_t>(min(q0 + q, nr - 1)) * g.pitch + at[k]];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (q0 + q < nr) {
+                        const float l2 = row_l[q0 + q];
+#pragma unroll
+                        for (int k = 0; k < kEach; ++k) acc[k] += exp2f(x[q][k] - l2);
+                    }
             }
         }
 #pragma unroll
@@ -837,7 +874,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
             const int j = j0 + k * kJoinThreads + tid;
             if (j < len) {
                 const size_t at = static_cast<size_t>(bh) * pb.Nkv + j;
-                a.oweights[at] = a.weights[at] + acc[k];
+                a.oweights[at] = old[k] + acc[k];
             }
         }
     }
@@ -938,7 +975,7 @@ bool line_fits(const Problem& pb, bool shared, int Np)
     // rows are joined by a CTA each; key tiles of a range are counted in 31 bits
     const long long units = static_cast<long long>(pb.B) * pb.Hkv * ((R + 15) / 16);
     const long long tiles = units * (pb.Nkv / 16 + 1) + (shared ? static_cast<long long>(pb.Hkv) * ((R * pb.B + 15) / 16) * (Np / 16 + 1) : 0);
-    return tiles < 0x7fffffffLL && R * pb.B * pb.Hkv < 0x7fffffffLL;
+    return tiles < 0x7fffffffLL && R * pb.B * pb.Hkv < 0x10000000LL;
 }
 
 size_t line_workspace_bytes(const Problem& pb, bool shared, int Np)

@@ -103,7 +103,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     // the next GEMM kernel of a backward may take SMs as this grid's last CTAs start
     pdl_trigger();
-    if constexpr (SPLIT) pdl_wait();  // the kernel before lays out the queries
     using T = Traits<OP>;
     const Problem& pb = a.pb;
     const int C = gm.C;
@@ -256,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     cluster_sync_all();  // every CTA's barriers exist before any remote arrive
     tc_fence_after();
+    if constexpr (SPLIT) pdl_wait();  // the kernel before lays out the queries
     const uint32_t tmem = sh.tmem_base;
     const uint32_t t_acc = tmem;        // [0, 256): accumulator slab
     const uint32_t t_x0 = tmem + 256;   // X buffers (and Y for the two-product kernels)
