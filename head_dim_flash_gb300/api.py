@@ -812,9 +812,9 @@ def _view_strides(shape, stride):
 
 @functools.lru_cache(maxsize=1024)
 def _like_strides(shape, stride):
-    """Strides that torch.empty_like gives a tensor, where they fit an ffpa_view; else contiguous ones."""
+    """Strides that torch.empty_like gives a tensor, where they fit an ffpa_view; else None."""
     like = torch.empty_like(torch.empty_strided(shape, stride, dtype=torch.uint8, device="meta")).stride()
-    return like if _view_strides(shape, like) else torch.empty(shape, dtype=torch.uint8, device="meta").stride()
+    return like if _view_strides(shape, like) else None
 
 
 def _in4(x, strides):
@@ -829,7 +829,10 @@ def _in4(x, strides):
 def _out4(x, out, like, name: str):
     """(tensor, its ffpa_view) of an output: new with strides `like`, or `out`, checked against x."""
     if out is None:
-        out = torch.empty_strided(x.shape, like, dtype=x.dtype, device=x.device)
+        if like is None:  # empty_like would not fit
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            return out, _view(out)
+        out = torch.empty_like(x)
         return out, _ffi.View(out.data_ptr(), *like[:3])
     if out is not x and (out.shape != x.shape or out.dtype != x.dtype or out.device != x.device):
         raise ValueError(f"{name} must have its input's shape, dtype and device")

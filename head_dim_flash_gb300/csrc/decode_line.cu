@@ -288,19 +288,6 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
                 atomicCAS(a.f.ctl.status, 0u, DEV_INVALID | (VS_LINE << 8) | ((static_cast<uint32_t>(i) & 0xffffu) << 16));
             if (pb.B <= kLens) s_len[i] = good ? n : 0;
         }
-    if (g.splits) {
-        const int nv = pb.D >> 3, each = pb.Hq / pb.Hkv * pb.Nq;
-        const long long vecs = static_cast<long long>(pb.B) * pb.Hq * pb.Nq * nv;
-        for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < vecs;
-             e += static_cast<long long>(gridDim.x) * blockDim.x) {
-            const int row = static_cast<int>(e / nv);  // [Hkv][B][group][Nq], below 2^31
-            const int col = static_cast<int>(e - static_cast<long long>(row) * nv) * 8;
-            const int hk = row / g.Rp, rp = row - hk * g.Rp;
-            const int b = rp / each, r = rp - b * each, gg = r / pb.Nq, i = r - gg * pb.Nq;
-            *reinterpret_cast<uint4*>(g.q_rows + static_cast<size_t>(row) * pb.D + col) = *reinterpret_cast<const uint4*>(
-                static_cast<const uint16_t*>(a.f.q) + b * pb.vq.sb + (hk * (pb.Hq / pb.Hkv) + gg) * pb.vq.sh + i * pb.vq.sn + col);
-        }
-    }
     __syncthreads();
     const Line line{a, g, a.lens && pb.B <= kLens ? s_len : nullptr};
     int total, unused;
@@ -313,9 +300,9 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
     const int group = warp / g.warps, wg = warp - group * g.warps;
     // neighbouring ranges go to different SMs: a line of few tiles does not crowd a few of them
     const int range = group * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-    if (range >= cuts.ranges) return;  // no barrier below spans groups
-    const int n = cuts.begin(range + 1) - cuts.begin(range);
-    const Spot spot = line.find(cuts.begin(range));
+    const bool work = range < cuts.ranges;
+    const int n = work ? cuts.begin(range + 1) - cuts.begin(range) : 0;
+    const Spot spot = line.find(work ? cuts.begin(range) : 0);
     uint8_t* const ring = smem + static_cast<size_t>(group) * S * g.stage_bytes;
     float2* const part = reinterpret_cast<float2*>(smem + static_cast<size_t>(g.groups) * S * g.stage_bytes) +
                          group * (g.warps > 1 ? (g.warps + 1) * SLOTS * 32 : 0);
@@ -348,6 +335,21 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
         sh.ahead[group].stage = 0;
         for (int i = 0; i < S; ++i) issue();
     }
+    // (many rows) the queries as rows of the prefix' kernel, while the first tiles are on their way
+    if (g.splits) {
+        const int warps = blockDim.x >> 5, rows = pb.Hkv * g.Rp;
+        for (int row = blockIdx.x * warps + warp; row < rows; row += gridDim.x * warps) {  // [Hkv][B][group][Nq]
+            const int hk = row / g.Rp;
+            int b, gg, i;
+            row_of(row - hk * g.Rp, -1, pb.Nq, g.R, b, gg, i);
+            const uint16_t* src = static_cast<const uint16_t*>(a.f.q) + b * pb.vq.sb +
+                                  (hk * (pb.Hq / pb.Hkv) + gg) * pb.vq.sh + i * pb.vq.sn;
+            uint16_t* dst = g.q_rows + static_cast<size_t>(row) * pb.D;
+            for (int c = lane * 8; c < pb.D; c += 256)
+                *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
+        }
+    }
+    if (!work) return;  // no barrier below spans groups
 
     // ------------------------------------------------------------ products
     const int my_chunks = CC == 1 ? 1 : (wg < g.chunks) + (wg + 8 < g.chunks);
@@ -398,6 +400,24 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
                                                           q + (wg + 8 * cc) * 64 + ks * 16 + k8 * 8 + cpair)
                                                     : 0u;
             }
+    };
+    // A unit's queries are wanted at once when it begins: they are called into L1
+    // while the unit before it is at work (a row's 64 head dims are one line).
+    auto touch_next = [&](Spot u) {
+        line.next_unit(u);
+        const int r = lane & 15;
+        if (u.b >= pb.B || r >= unit_rows(u)) return;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            if (mt * 16 + r >= unit_rows(u)) break;
+            int bb, gg, i;
+            row_of(u.rb * ROWS + mt * 16 + r, u.b, pb.Nq, R, bb, gg, i);
+            const uint16_t* q = static_cast<const uint16_t*>(a.f.q) + bb * pb.vq.sb + (u.hk * G + gg) * pb.vq.sh +
+                                i * pb.vq.sn + (CC == 1 ? wg : wg + (lane >> 4) * 8) * 64;
+            uint32_t x;
+            if (CC == 1 || wg + (lane >> 4) * 8 < g.chunks)
+                asm volatile("ld.global.ca.b32 %0, [%1];" : "=r"(x) : "l"(q));
+        }
     };
     auto reset = [&] {
 #pragma unroll
@@ -637,6 +657,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
     reset();
     enter_unit(unit);
     int first = unit.tile;      // first tile of the unit in this range
+    if (n > unit.tiles - unit.tile) touch_next(unit);
     scores();
     softmax(unit, false);
     for (int t = 0; t < n; ++t) {
@@ -648,7 +669,10 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
             fresh = more;
         }
         if (more) {
-            if (fresh) enter_unit(unit);
+            if (fresh) {
+                enter_unit(unit);
+                if (n - t - 1 > unit.tiles) touch_next(unit);
+            }
             scores();
         }
         values(cur);
@@ -684,16 +708,19 @@ struct Pieces {
     __device__ int slot(int i) const { return i == 0 ? 2 * first + 1 : 2 * (first + i); }
 };
 
-// A warp per query row and 128 head dims, then, when scoring, a CTA per kWeighKeys
-// tokens of a kv head. The row warps each find their row's pieces again: that is
-// cheaper than sharing them, and short contexts have few.
+// A warp per query row (per row and 128 head dims where rows are few), then, when
+// scoring, a CTA per kWeighKeys tokens of a kv head. Each warp finds its row's
+// pieces by itself: three loads in a row, which many warps per SM hide better
+// than sharing would save. LOADS pieces of a row are on their way at once: few
+// registers, so many warps, where rows are many and their pieces few.
 constexpr int kWeighKeys = 1024;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinLoads = 16;  // pieces of a row on their way at once
 
-template <bool BF16, bool SCORE>
+
+template <bool BF16, bool SCORE, int LOADS>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, const LineGeo g, const int rows,
-                                                            const int row_ctas, const int key_blocks)
+                                                            const int row_ctas, const int key_blocks,
+                                                            const int parts)
 {
     pdl_wait();
     pdl_trigger();
@@ -703,13 +730,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
     const int R = g.R;
     const long long cta = static_cast<long long>(blockIdx.x) + static_cast<long long>(gridDim.x) * blockIdx.y;
     const bool is_row = cta < row_ctas;
-    const int slices = (pb.D + 127) >> 7;
-    int bh, block = 0, row = 0, slice = 0;  // (sequence, kv head)
+    int bh, block = 0, row = 0, part = 0;  // (sequence, kv head)
     if (is_row) {
         const unsigned unit = static_cast<unsigned>(cta) * kJoinWarps + warp;  // below 2^32: line_fits
-        if (unit >= static_cast<unsigned>(rows) * slices) return;  // warps are on their own
-        row = static_cast<int>(unit / slices);
-        slice = static_cast<int>(unit - static_cast<unsigned>(row) * slices);
+        if (unit >= static_cast<unsigned>(rows) * parts) return;  // warps are on their own
+        row = static_cast<int>(unit / parts);
+        part = static_cast<int>(unit - static_cast<unsigned>(row) * parts);
         bh = row / R;
     } else {
         const unsigned rest = static_cast<unsigned>(cta - row_ctas);
@@ -751,63 +777,63 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
             l += at;
             o += at * pb.D;
         };
-        const int col = slice * 128 + lane * 4;
-        const bool mine = col < pb.D;
-        float mx = -INFINITY, sum = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        // 32 pieces at a time, a lane for each; the sums are rescaled when a later 32 hold a larger maximum
-        for (int p0 = 0; p0 < pieces; p0 += 32) {
-            const float *l = nullptr, *o = nullptr;
-            float w = -INFINITY;
-            if (p0 + lane < pieces) {
-                find(p0 + lane, l, o);
-                w = *l;
-            }
-            float top = w;
+        const int gg = r / pb.Nq, qi = r - gg * pb.Nq;
+        uint16_t* out = static_cast<uint16_t*>(a.f.o) + b * pb.vo.sb + (hk * (pb.Hq / pb.Hkv) + gg) * pb.vo.sh + qi * pb.vo.sn;
+        float top = -INFINITY, total_w = 0.f;
+        // Most rows have up to 32 pieces, a lane for each. More are taken in turn:
+        // the largest of all first.
+        for (int i = lane; i < pieces; i += 32) {
+            const float *l, *o;
+            find(i, l, o);
+            top = fmaxf(top, *l);
+        }
 #pragma unroll
-            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            if (top == -INFINITY) continue;
-            const float now = fmaxf(mx, top), scale = mx == -INFINITY ? 0.f : exp2f(mx - now);
-            mx = now;
-            w = w == -INFINITY ? 0.f : exp2f(w - now);
-            float part = w;
-#pragma unroll
-            for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
-            sum = sum * scale + part;
-            v.x *= scale;
-            v.y *= scale;
-            v.z *= scale;
-            v.w *= scale;
-            // sixteen loads in flight; past the last piece, its own again with no weight
-            const int n = min(32, pieces - p0);
-            for (int k0 = 0; k0 < n; k0 += kJoinLoads) {
-                float4 p[kJoinLoads];
-#pragma unroll
-                for (int k = 0; k < kJoinLoads; ++k) {
-                    const float* ok = reinterpret_cast<const float*>(
-                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), min(k0 + k, n - 1)));
-                    if (mine) p[k] = *reinterpret_cast<const float4*>(ok + col);
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        for (int c0 = part * 128; c0 < pb.D; c0 += parts * 128) {
+            const int col = c0 + lane * 4;
+            const bool mine = col < pb.D;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+            for (int p0 = 0; p0 < pieces && top > -INFINITY; p0 += 32) {
+                const float *l = nullptr, *o = nullptr;
+                float w = 0.f;
+                if (p0 + lane < pieces) {
+                    find(p0 + lane, l, o);
+                    w = exp2f(*l - top);
                 }
+                sum += w;
+                // several loads in flight; past the last piece, its own again with no weight
+                const int n = min(32, pieces - p0);
+                for (int k0 = 0; k0 < n; k0 += LOADS) {
+                    float4 p[LOADS];
 #pragma unroll
-                for (int k = 0; k < kJoinLoads; ++k) {
-                    const float ws = __shfl_sync(0xffffffffu, w, min(k0 + k, n - 1));
-                    const float wk = k0 + k < n ? ws : 0.f;
-                    if (mine) {
-                        v.x = fmaf(wk, p[k].x, v.x);
-                        v.y = fmaf(wk, p[k].y, v.y);
-                        v.z = fmaf(wk, p[k].z, v.z);
-                        v.w = fmaf(wk, p[k].w, v.w);
+                    for (int k = 0; k < LOADS; ++k) {
+                        const float* ok = reinterpret_cast<const float*>(
+                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), min(k0 + k, n - 1)));
+                        if (mine) p[k] = *reinterpret_cast<const float4*>(ok + col);
+                    }
+#pragma unroll
+                    for (int k = 0; k < LOADS; ++k) {
+                        const float ws = __shfl_sync(0xffffffffu, w, min(k0 + k, n - 1));
+                        const float wk = k0 + k < n ? ws : 0.f;
+                        if (mine) {
+                            v.x = fmaf(wk, p[k].x, v.x);
+                            v.y = fmaf(wk, p[k].y, v.y);
+                            v.z = fmaf(wk, p[k].z, v.z);
+                            v.w = fmaf(wk, p[k].w, v.w);
+                        }
                     }
                 }
             }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            total_w = sum;
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            if (mine)
+                *reinterpret_cast<uint2*>(out + col) =
+                    make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const int gg = r / pb.Nq, i = r - gg * pb.Nq;
-        uint16_t* out = static_cast<uint16_t*>(a.f.o) + b * pb.vo.sb + (hk * (pb.Hq / pb.Hkv) + gg) * pb.vo.sh + i * pb.vo.sn;
-        if (mine)
-            *reinterpret_cast<uint2*>(out + col) =
-                make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
-        if (slice == 0 && lane == 0) a.f.lse[row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+        if (part == 0 && lane == 0) a.f.lse[row] = total_w > 0.f ? (top + log2f(total_w)) * kLn2 : -INFINITY;
         return;
     }
     if constexpr (SCORE) {
@@ -1048,13 +1074,19 @@ cudaError_t launch_line(const LineArgs& args, void* workspace, cudaStream_t s)
     }
     const int rows = pb.B * pb.Hq * pb.Nq;
     const int key_blocks = a.shared ? 0 : (pb.Nkv + kWeighKeys - 1) / kWeighKeys;
-    const int row_ctas = static_cast<int>((static_cast<long long>(rows) * ((pb.D + 127) >> 7) + kJoinWarps - 1) / kJoinWarps);
+    // a warp per 128 head dims of a row as long as one round of warps holds them
+    const int sms = p.ctas, slices = (pb.D + 127) >> 7;
+    const bool many = static_cast<long long>(rows) * slices > 32LL * sms;
+    const int parts = many ? 1 : slices;
+    const int row_ctas = static_cast<int>((static_cast<long long>(rows) * parts + kJoinWarps - 1) / kJoinWarps);
     const long long ctas = row_ctas + static_cast<long long>(pb.B) * pb.Hkv * key_blocks;
     const long long x = ctas < 0x40000000LL ? ctas : 0x40000000LL;
     const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>((ctas + x - 1) / x));
-    auto join = a.f.bf16 ? (a.shared ? join_kernel<true, false> : join_kernel<true, true>)
-                         : (a.shared ? join_kernel<false, false> : join_kernel<false, true>);
-    return launch_dependent(join, grid, kJoinThreads, 0, s, a, g, rows, row_ctas, key_blocks);
+    auto join = a.f.bf16 ? (a.shared ? (many ? join_kernel<true, false, 4> : join_kernel<true, false, 16>)
+                                     : (many ? join_kernel<true, true, 4> : join_kernel<true, true, 16>))
+                         : (a.shared ? (many ? join_kernel<false, false, 4> : join_kernel<false, false, 16>)
+                                     : (many ? join_kernel<false, true, 4> : join_kernel<false, true, 16>));
+    return launch_dependent(join, grid, kJoinThreads, 0, s, a, g, rows, row_ctas, key_blocks, parts);
 }
 
 }  // namespace ffpa
