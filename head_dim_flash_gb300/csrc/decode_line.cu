@@ -16,10 +16,9 @@
 // per warp (mma.m16n8k16 over its chunks) and summed through shared memory;
 // the online softmax is done by every warp alike; O += P V stays with the
 // chunks, in registers. The scores of tile t + 1 are issued before the values
-// of tile t. A tile is a chain of waits (data, sum, maximum, P), so an SM runs
-// two groups or more, which share nothing. A slot is refilled by the group's last
-// warp, which has little to sum, when all warps have passed the barrier of the
-// sum: a producer warp would cost every thread registers.
+// of tile t. A tile is a chain of waits (data, sum, maximum, P): where its bytes
+// take less time than that, D <= 256, an SM runs two groups or more, which share
+// nothing but the producer warp.
 //
 // The scoring form also stores the scores (fp32, log2 units: 4 bytes per row
 // and key beside 4 D of K and V), and the second kernel turns them into weights
@@ -40,12 +39,17 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kMaxStages = 12;
 constexpr int kMaxGroups = 8;
 constexpr int kLens = 1024;     // lengths staged in shared memory; longer batches read them from L2
-constexpr int kTileKeys = 16;   // keys of a tile: one k16 step of the value product
+constexpr int kLineThreads = 288;  // warps 0..7 compute, warp 8 TMA producer
+// The same with three idle warps: three warpgroups of 168 registers a thread, of
+// which the two that compute take 232 and the producer's keeps 40.
+constexpr int kLineThreadsWide = 384;
+static_assert(2 * 232 + 40 == 3 * 168, "no more registers than the launch gives");
 constexpr int kJoinThreads = 256;
 
-enum LineSite : uint32_t { LS_FULL = 0x58, LS_DRAIN };
+enum LineSite : uint32_t { LS_PROD = 0x58, LS_FULL, LS_DRAIN };
 
 struct LineGeo {
+    int shift;           // keys of a tile: 1 << shift
     int chunks, warps, groups, stages, stage_bytes;
     int rows;            // query rows of a unit (16 or 32)
     int R, rblocks;      // rows of a kv head's group, their blocks
@@ -72,11 +76,7 @@ struct Spot {
 };
 
 struct __align__(1024) LineStatic {
-    uint64_t full[kMaxGroups][kMaxStages];
-    struct {
-        Spot at;              // of the next tile to load
-        int left, stage;      // tiles to load, the slot of the next
-    } ahead[kMaxGroups];
+    uint64_t full[kMaxGroups][kMaxStages], empty[kMaxGroups][kMaxStages];
     int abort_flag;
 };
 static_assert(sizeof(LineStatic) == 2048, "static shared block must be whole KiB");
@@ -119,7 +119,10 @@ __device__ __forceinline__ int clamp_len(const LineArgs& a, int b)
     return n >= 0 && n <= a.f.pb.Nkv ? n : 0;
 }
 
-__device__ __forceinline__ int tiles_of(int keys) { return (keys + kTileKeys - 1) / kTileKeys; }
+__device__ __forceinline__ int tiles_of(const LineGeo& g, int keys)
+{
+    return static_cast<int>((static_cast<unsigned>(keys) + (1u << g.shift) - 1) >> g.shift);
+}
 
 // Tiles of the whole line (below 2^31), and those before sequence `b` (by whole warps).
 __device__ __forceinline__ void line_sums(const LineArgs& a, const LineGeo& g, const int* staged, int b, int& total,
@@ -129,7 +132,7 @@ __device__ __forceinline__ void line_sums(const LineArgs& a, const LineGeo& g, c
     int t = 0, p = 0;
 #pragma unroll 4
     for (int i = threadIdx.x & 31; i < pb.B; i += 32) {
-        const int n = tiles_of(staged ? staged[i] : clamp_len(a, i));
+        const int n = tiles_of(g, staged ? staged[i] : clamp_len(a, i));
         t += n;
         if (i < b) p += n;
     }
@@ -169,7 +172,7 @@ struct Line {
         s.tiles = 0;
         while (s.b < a.f.pb.B) {
             s.keys = len(s.b);
-            s.tiles = tiles_of(s.keys);
+            s.tiles = tiles_of(g, s.keys);
             if (s.tiles > 0) return;
             ++s.b;
         }
@@ -205,7 +208,7 @@ struct Line {
         int run = 0;
         s.b = a.f.pb.B;
         for (int i0 = 0; i0 < a.f.pb.B; i0 += 32) {
-            const int n = i0 + lane < a.f.pb.B ? tiles_of(len(i0 + lane)) : 0;
+            const int n = i0 + lane < a.f.pb.B ? tiles_of(g, len(i0 + lane)) : 0;
             int incl = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -243,10 +246,12 @@ __device__ __forceinline__ void row_of(int r, int b, int Nq, int R, int& bb, int
     i = r - gg * Nq;
 }
 
-// Threads of a variant: sixteen warps of 128 registers a thread where that
-// holds its rows, else eight.
+// Keys of a tile: as many as the registers of a variant's rows and chunks leave room for.
 template <int MT, int CC>
-constexpr int line_threads() { return MT == 1 && CC == 1 ? 512 : 256; }
+__host__ __device__ constexpr int tile_keys() { return MT == 1 && CC == 1 ? 32 : 16; }
+
+template <int MT, int CC>
+__host__ __device__ constexpr int line_threads() { return MT == 1 && CC == 1 ? kLineThreads : kLineThreadsWide; }
 
 template <bool BF16, int MT, int CC, bool SCORE>
 __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
@@ -254,20 +259,23 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
                 const __grid_constant__ CUtensorMap tKp, const __grid_constant__ CUtensorMap tVp, const LineArgs a,
                 const LineGeo g)
 {
-    constexpr int KT = kTileKeys, NT = KT / 8, ROWS = 16 * MT;
+    constexpr int KT = tile_keys<MT, CC>(), NT = KT / 8, ROWS = 16 * MT;
     constexpr int SLOTS = MT * NT * 2;  // float2 a lane holds of a tile's scores
     const Problem& pb = a.f.pb;
     __shared__ LineStatic sh;
     __shared__ int s_len[kLens];
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = g.stages;
+    const int S = g.stages, compute = g.groups * g.warps;  // warps behind these: idle, and the producer
     if (smem_u32(smem) & 1023u) {
         pdl_wait();
         if (threadIdx.x == 0) atomicCAS(a.f.ctl.status, 0u, 5u | (0xffu << 8));
         return;
     }
-    if (threadIdx.x < g.groups * S) mbar_init(&sh.full[threadIdx.x / S][threadIdx.x % S], 1);
+    if (threadIdx.x < g.groups * S) {
+        mbar_init(&sh.full[threadIdx.x / S][threadIdx.x % S], 1);
+        mbar_init(&sh.empty[threadIdx.x / S][threadIdx.x % S], g.warps);
+    }
     if (threadIdx.x == 0) {
         sh.abort_flag = 0;
         prefetch_tmap(&tK);
@@ -297,47 +305,76 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
     uint32_t* status = a.f.ctl.status;
     const uint64_t lim = a.f.ctl.limit_ns;
     const uint32_t half_bytes = static_cast<uint32_t>(g.stage_bytes / 2);
-    const int group = warp / g.warps, wg = warp - group * g.warps;
     // neighbouring ranges go to different SMs: a line of few tiles does not crowd a few of them
-    const int range = group * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    auto range_of = [&](int group) { return group * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x); };
+    auto ring_of = [&](int group) { return smem + static_cast<size_t>(group) * S * g.stage_bytes; };
+
+    constexpr bool kWide = line_threads<MT, CC>() == kLineThreadsWide;
+    if (warp >= 8) {
+        // ------------------------------------------------------ producer
+        if constexpr (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp > 8) return;
+        // lane 2 i loads K of group i, lane 2 i + 1 its V; the groups take turns
+        int n_most = 0, mine = 0;
+        Spot ahead{};
+        for (int i = 0; i < g.groups; ++i) {
+            const int r = range_of(i);
+            if (r >= cuts.ranges) break;
+            const int first = cuts.begin(r), n = cuts.begin(r + 1) - first;
+            const Spot at = line.find(first);
+            n_most = max(n_most, n);
+            if (lane >> 1 == i) {
+                mine = n;
+                ahead = at;
+            }
+        }
+        const int group = min(lane >> 1, g.groups - 1);
+        uint64_t* const full = sh.full[group];
+        uint8_t* const ring = ring_of(group) + (lane & 1) * half_bytes;
+        int st = 0, issued = 0;
+        uint32_t phase = 1;
+        bool go = true;
+        for (int t = 0; t < n_most; ++t) {
+            if (t < mine && go) {
+                go = mbar_wait(&sh.empty[group][st], phase, abort_p, status, lim, LS_PROD);
+                if (go) {
+                    if ((lane & 1) == 0) mbar_arrive_expect_tx(&full[st], g.stage_bytes);
+                    const CUtensorMap* m = ahead.b < 0 ? (lane & 1 ? &tVp : &tKp) : (lane & 1 ? &tV : &tK);
+                    tma_load_5d(ring + st * g.stage_bytes, m, &full[st], 0, ahead.tile * KT, 0, ahead.hk, max(ahead.b, 0));
+                    ++issued;
+                    if (++ahead.tile == ahead.tiles && t + 1 < mine) line.next_unit(ahead);
+                }
+            }
+            if (++st == S) {
+                st = 0;
+                phase ^= 1u;
+            }
+        }
+        // no copy in flight when the CTA leaves. K's and V's lanes may have stopped
+        // apart when a wait ran out: a stage that lacks one of them is not waited for
+        const int both = min(issued, __shfl_xor_sync(0xffffffffu, issued, 1));
+        if ((lane & 1) == 0)
+            for (int t = max(0, both - S); t < both; ++t) {
+                int dummy = 0;
+                if (!mbar_wait(&full[t % S], (t / S) & 1, &dummy, status, lim, LS_DRAIN, false)) break;
+            }
+        return;
+    }
+    if constexpr (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int group = warp / g.warps, wg = warp - group * g.warps;
+    const int range = warp < compute ? range_of(group) : cuts.ranges;
     const bool work = range < cuts.ranges;
     const int n = work ? cuts.begin(range + 1) - cuts.begin(range) : 0;
     const Spot spot = line.find(work ? cuts.begin(range) : 0);
-    uint8_t* const ring = smem + static_cast<size_t>(group) * S * g.stage_bytes;
+    uint8_t* const ring = ring_of(group);
     float2* const part = reinterpret_cast<float2*>(smem + static_cast<size_t>(g.groups) * S * g.stage_bytes) +
                          group * (g.warps > 1 ? (g.warps + 1) * SLOTS * 32 : 0);
     float2* const fin = part + g.warps * SLOTS * 32;
     auto sync_group = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(g.warps * 32) : "memory"); };
 
-    // -------------------------------------------------------------- loads
-    // lane 0 of the group's last warp; its place in the line is ahead of the products'
-    const bool loads = wg == g.warps - 1 && lane == 0;
-    auto issue = [&] {
-        auto& h = sh.ahead[group];
-        if (h.left == 0) return;
-        --h.left;
-        uint8_t* dst = ring + h.stage * g.stage_bytes;
-        uint64_t* bar = &sh.full[group][h.stage];
-        if (++h.stage == S) h.stage = 0;
-        const bool prefix = h.at.b < 0;
-        mbar_arrive_expect_tx(bar, g.stage_bytes);
-        tma_load_5d(dst, prefix ? &tKp : &tK, bar, 0, h.at.tile * KT, 0, h.at.hk, max(h.at.b, 0));
-        tma_load_5d(dst + half_bytes, prefix ? &tVp : &tV, bar, 0, h.at.tile * KT, 0, h.at.hk, max(h.at.b, 0));
-        if (++h.at.tile == h.at.tiles && h.left) {
-            Spot at = h.at;
-            line.next_unit(at);
-            h.at = at;
-        }
-    };
-    if (loads) {
-        sh.ahead[group].at = spot;
-        sh.ahead[group].left = n;
-        sh.ahead[group].stage = 0;
-        for (int i = 0; i < S; ++i) issue();
-    }
     // (many rows) the queries as rows of the prefix' kernel, while the first tiles are on their way
     if (g.splits) {
-        const int warps = blockDim.x >> 5, rows = pb.Hkv * g.Rp;
+        const int warps = 8, rows = pb.Hkv * g.Rp;
         for (int row = blockIdx.x * warps + warp; row < rows; row += gridDim.x * warps) {  // [Hkv][B][group][Nq]
             const int hk = row / g.Rp;
             int b, gg, i;
@@ -350,7 +387,6 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
         }
     }
     if (!work) return;  // no barrier below spans groups
-
     // ------------------------------------------------------------ products
     const int my_chunks = CC == 1 ? 1 : (wg < g.chunks) + (wg + 8 < g.chunks);
     const int r_lo = lane >> 2, cpair = (lane & 3) * 2;
@@ -472,7 +508,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
         }
     };
     // the sum over the group's warps, the mask, and P and the factors of tile t (the unit `u`'s)
-    auto softmax = [&](const Spot& u, bool refill) {
+    auto softmax = [&](const Spot& u) {
         if (g.warps > 1) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -484,8 +520,6 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
         }
         if (g.warps > 1) {
             sync_group();
-            // every warp has left the values of the tile before: its slot is free
-            if (refill && ok && loads) issue();
             for (int sl = wg; sl < SLOTS; sl += g.warps) {
                 float2 p[8];
 #pragma unroll
@@ -495,9 +529,6 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
                                                   ((p[0].y + p[1].y) + (p[2].y + p[3].y)) + ((p[4].y + p[5].y) + (p[6].y + p[7].y)));
             }
             sync_group();
-        } else if (refill && ok) {
-            __syncwarp();
-            if (loads) issue();
         }
         const bool store = wg == turn;
         if (++turn == g.warps) turn = 0;
@@ -596,6 +627,9 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
                     }
                 }
         }
+        // K and V of this stage have been read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[group][v_st]);
         if (++v_st == S) v_st = 0;
     };
     // the piece of unit u that this range holds: its tiles [first, last)
@@ -659,7 +693,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
     int first = unit.tile;      // first tile of the unit in this range
     if (n > unit.tiles - unit.tile) touch_next(unit);
     scores();
-    softmax(unit, false);
+    softmax(unit);
     for (int t = 0; t < n; ++t) {
         const Spot cur = unit;
         const bool more = t + 1 < n;
@@ -681,15 +715,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
             first = 0;
             reset();
         }
-        if (more) softmax(unit, true);
-    }
-    // a range whose wait ran out leaves none of its copies in flight
-    if (!ok && loads) {
-        const int issued = n - sh.ahead[group].left;
-        for (int t = max(0, issued - S); t < issued; ++t) {
-            int dummy = 0;
-            if (!mbar_wait(&sh.full[group][t % S], (t / S) & 1, &dummy, status, lim, LS_DRAIN, false)) break;
-        }
+        if (more) softmax(unit);
     }
 }
 
@@ -749,7 +775,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
     int total, before;
     line_sums(a, g, nullptr, b, total, before);
     const Cuts cuts(g, total);
-    const int tiles = tiles_of(len);
+    const int tiles = tiles_of(g, len);
 
     if (is_row) {
         const int r = row - bh * R;
@@ -930,6 +956,7 @@ LinePlan line_plan(const Problem& pb, bool shared, int Np)
     const int most = shared && !split ? g.Rp : g.R;
     const int mt = g.chunks > 8 || most <= 16 ? 1 : 2;
     g.rows = 16 * mt;
+    g.shift = mt == 1 && g.chunks <= 8 ? 5 : 4;  // as tile_keys
     g.rblocks = (g.R + g.rows - 1) / g.rows;
     if (split) {
         p.prefix = pb;
@@ -943,15 +970,13 @@ LinePlan line_plan(const Problem& pb, bool shared, int Np)
         g.split_keys = (tiles + g.splits - 1) / g.splits * 128;
     } else if (shared) {
         g.rblocks_p = (g.Rp + g.rows - 1) / g.rows;
-        g.tiles_p = (Np + kTileKeys - 1) / kTileKeys;
+        g.tiles_p = (Np + (1 << g.shift) - 1) >> g.shift;
         if (g.tiles_p == 0) g.rblocks_p = 0;
     }
-    // Groups: what sixteen compute warps hold (eight where a thread needs more
-    // than 120 registers), two at least with sixteen, no more than kMaxGroups.
     g.warps = min(g.chunks, 8);
-    g.groups = min(kMaxGroups, (mt == 1 && g.chunks <= 8 ? 16 : 8) / g.warps);
-    g.stage_bytes = 2 * kTileKeys * g.chunks * 128;
-    const int slots = mt * kTileKeys / 8 * 2;
+    g.groups = min(kMaxGroups, 8 / g.warps);
+    g.stage_bytes = 2 * g.chunks * 128 << g.shift;
+    const int slots = mt * 2 << g.shift >> 3;
     const int exchange = g.warps > 1 ? g.groups * (g.warps + 1) * slots * 256 : 0;
     const int budget = kMaxSmem - static_cast<int>(sizeof(LineStatic)) - kLens * 4 - exchange;
     g.stages = min(kMaxStages, budget / (g.groups * g.stage_bytes));
@@ -989,7 +1014,7 @@ cudaError_t launch_variant(const LineArgs& a, const LinePlan& p, const CUtensorM
     auto kern = a.shared ? line_kernel<BF16, MT, CC, false> : line_kernel<BF16, MT, CC, true>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(p.ctas), p.g.groups * p.g.warps * 32, p.smem, s, m[0], m[1], m[2], m[3], a, p.g);
+    return launch_dependent(kern, dim3(p.ctas), line_threads<MT, CC>(), p.smem, s, m[0], m[1], m[2], m[3], a, p.g);
 }
 
 }  // namespace
@@ -1034,11 +1059,11 @@ cudaError_t launch_line(const LineArgs& args, void* workspace, cudaStream_t s)
     pp.B = 1;
     pp.Nkv = a.Np;
     // maps of sides without keys are never read
-    if (pb.Nkv > 0 && (!make_slab_map(&m[0], a.f.k, pb, true, a.f.bf16, kTileKeys, g.chunks, pb.vk) ||
-                       !make_slab_map(&m[1], a.f.v, pb, true, a.f.bf16, kTileKeys, g.chunks, pb.vv)))
+    if (pb.Nkv > 0 && (!make_slab_map(&m[0], a.f.k, pb, true, a.f.bf16, 1 << g.shift, g.chunks, pb.vk) ||
+                       !make_slab_map(&m[1], a.f.v, pb, true, a.f.bf16, 1 << g.shift, g.chunks, pb.vv)))
         return cudaErrorInvalidValue;
-    if (g.rblocks_p && (!make_slab_map(&m[2], a.kp, pp, true, a.f.bf16, kTileKeys, g.chunks, a.vkp) ||
-                        !make_slab_map(&m[3], a.vp, pp, true, a.f.bf16, kTileKeys, g.chunks, a.vvp)))
+    if (g.rblocks_p && (!make_slab_map(&m[2], a.kp, pp, true, a.f.bf16, 1 << g.shift, g.chunks, a.vkp) ||
+                        !make_slab_map(&m[3], a.vp, pp, true, a.f.bf16, 1 << g.shift, g.chunks, a.vvp)))
         return cudaErrorInvalidValue;
     cudaError_t e;
     if (g.chunks > 8)
