@@ -36,6 +36,7 @@ namespace ffpa {
 namespace {
 
 constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kTau = 8.f;       // a score may lie 2^8 above its row's reference
 constexpr int kMaxStages = 12;
 constexpr int kMaxGroups = 8;
 constexpr int kLens = 1024;     // lengths staged in shared memory; longer batches read them from L2
@@ -246,6 +247,12 @@ __device__ __forceinline__ void row_of(int r, int b, int Nq, int R, int& bb, int
     i = r - gg * Nq;
 }
 
+// Shared memory of a group besides its ring: partial scores, P, maxima and sums.
+__host__ __device__ constexpr int exchange_bytes(int warps, int mt, int nt)
+{
+    return warps * (mt * nt * 2) * 256 + mt * (nt / 2) * 512 + (mt * nt * 2) * 32 + warps * mt * 64;
+}
+
 // Keys of a tile: as many as the registers of a variant's rows and chunks leave room for.
 template <int MT, int CC>
 __host__ __device__ constexpr int tile_keys() { return MT == 1 && CC == 1 ? 32 : 16; }
@@ -368,9 +375,30 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
     const Spot spot = line.find(work ? cuts.begin(range) : 0);
     uint8_t* const ring = ring_of(group);
     float2* const part = reinterpret_cast<float2*>(smem + static_cast<size_t>(g.groups) * S * g.stage_bytes) +
-                         group * (g.warps > 1 ? (g.warps + 1) * SLOTS * 32 : 0);
-    float2* const fin = part + g.warps * SLOTS * 32;
-    auto sync_group = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(g.warps * 32) : "memory"); };
+                         group * exchange_bytes(g.warps, MT, NT) / 8;       // [warps][slot][lane] partial scores
+    uint32_t* const p_s = reinterpret_cast<uint32_t*>(part + g.warps * SLOTS * 32);  // [mt][k16][lane][4]: P as A fragments
+    float* const tops = reinterpret_cast<float*>(p_s + MT * (NT / 2) * 128);         // [slot][8 rows]: maxima
+    float* const sums = tops + SLOTS * 8;                                            // [warps][ROWS]
+    auto sync_group = [&] {
+        if (g.warps > 1)
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(g.warps * 32) : "memory");
+        else
+            __syncwarp();
+    };
+    // the same, and whether x holds for any thread of the group
+    auto any_group = [&](bool x) -> bool {
+        if (g.warps == 1) {
+            __syncwarp();
+            return __any_sync(0xffffffffu, x);
+        }
+        uint32_t r;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\tbar.red.or.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(r)
+            : "r"(1 + group), "r"(g.warps * 32), "r"(static_cast<uint32_t>(x))
+            : "memory");
+        return r != 0;
+    };
 
     // (many rows) the queries as rows of the prefix' kernel, while the first tiles are on their way
     if (g.splits) {
@@ -393,7 +421,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
     const int R = g.R, G = pb.Hq / pb.Hkv;
     uint32_t qa[CC][4][MT][4];
     float o_acc[CC][8][MT][4];
-    float m_run[MT][2], l_run[MT][2], alpha[MT][2];
+    float m_run[MT][2], l_run[MT][2];  // references of my rows (every warp's alike), my share of their sums
     int jlim[MT][2];                // legal keys of the score rows: below this
     uint32_t pa[MT][NT / 2][4];
     float s[MT][NT][4];
@@ -462,7 +490,6 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
             for (int hi = 0; hi < 2; ++hi) {
                 m_run[mt][hi] = -INFINITY;
                 l_run[mt][hi] = 0.f;
-                alpha[mt][hi] = 1.f;
             }
 #pragma unroll
             for (int cc = 0; cc < CC; ++cc)
@@ -472,7 +499,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
                     for (int e = 0; e < 4; ++e) o_acc[cc][i][mt][e] = 0.f;
         }
     };
-    int k_st = 0, v_st = 0, turn = 0;   // stages of the next scores and values; the warp that stores scores
+    int k_st = 0, v_st = 0;   // stages of the next scores and values
     uint32_t k_phase = 0;
     auto scores = [&] {
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sh.full[group][k_st], k_phase, abort_p, status, lim, LS_FULL));
@@ -507,85 +534,101 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
                 }
         }
     };
-    // the sum over the group's warps, the mask, and P and the factors of tile t (the unit `u`'s)
-    auto softmax = [&](const Spot& u) {
-        if (g.warps > 1) {
+    // Slot (mt, i, hi) of a tile: rows 16 mt + 8 hi + lane / 4, keys 8 i + 2 (lane % 4)
+    // and the next; the warps take slots in turn.
+    auto slot_mt = [](int sl) { return MT == 1 ? 0 : sl / (NT * 2); };
+    auto slot_i = [](int sl) { return (sl >> 1) & (NT - 1); };
+    auto of_row = [&](const auto& v, int sl) { return MT == 1 || sl < NT * 2 ? (sl & 1 ? v[0][1] : v[0][0]) : (sl & 1 ? v[MT - 1][1] : v[MT - 1][0]); };
+    // its scores: the sum over the group's warps, in log2 units, masked
+    auto slot_scores = [&](int sl, const Spot& u) {
+        float2 p[8];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+        for (int w = 0; w < 8; ++w) p[w] = w < g.warps ? part[(w * SLOTS + sl) * 32 + lane] : make_float2(0.f, 0.f);
+        const float x = ((p[0].x + p[1].x) + (p[2].x + p[3].x)) + ((p[4].x + p[5].x) + (p[6].x + p[7].x));
+        const float y = ((p[0].y + p[1].y) + (p[2].y + p[3].y)) + ((p[4].y + p[5].y) + (p[6].y + p[7].y));
+        const int j = (u.tile * KT) + slot_i(sl) * 8 + cpair, end = of_row(jlim, sl);
+        return make_float2(j < end ? x * pb.scale_log2 : -INFINITY, j + 1 < end ? y * pb.scale_log2 : -INFINITY);
+    };
+    // P of a tile in shared memory, from the references as they are, and its sums added
+    // to `add`; true where a score lies too far above its reference
+    auto exponentials = [&](const Spot& u, float (&add)[MT][2], bool first_try) {
+        bool over = false;
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    part[(wg * SLOTS + (mt * NT + i) * 2) * 32 + lane] = make_float2(s[mt][i][0], s[mt][i][1]);
-                    part[(wg * SLOTS + (mt * NT + i) * 2 + 1) * 32 + lane] = make_float2(s[mt][i][2], s[mt][i][3]);
-                }
-        }
-        if (g.warps > 1) {
-            sync_group();
-            for (int sl = wg; sl < SLOTS; sl += g.warps) {
-                float2 p[8];
-#pragma unroll
-                for (int w = 0; w < 8; ++w)
-                    p[w] = w < g.warps ? part[(w * SLOTS + sl) * 32 + lane] : make_float2(0.f, 0.f);
-                fin[sl * 32 + lane] = make_float2(((p[0].x + p[1].x) + (p[2].x + p[3].x)) + ((p[4].x + p[5].x) + (p[6].x + p[7].x)),
-                                                  ((p[0].y + p[1].y) + (p[2].y + p[3].y)) + ((p[4].y + p[5].y) + (p[6].y + p[7].y)));
+        for (int mt = 0; mt < MT; ++mt) add[mt][0] = add[mt][1] = 0.f;
+        for (int sl = wg; sl < SLOTS; sl += g.warps) {
+            const float2 x = slot_scores(sl, u);
+            const int mt = slot_mt(sl), i = slot_i(sl), hi = sl & 1;
+            if (SCORE && first_try) {
+                const int r = u.rb * ROWS + mt * 16 + hi * 8 + r_lo, j = u.tile * KT + i * 8 + cpair;
+                if (r < R && j < u.keys)
+                    *reinterpret_cast<float2*>(g.scores + ((static_cast<size_t>(u.b) * pb.Hkv + u.hk) * R + r) * g.pitch + j) = x;
             }
-            sync_group();
-        }
-        const bool store = wg == turn;
-        if (++turn == g.warps) turn = 0;
-        const float c2 = pb.scale_log2;
+            const float ref = of_row(m_run, sl), mu = ref == -INFINITY ? 0.f : ref;
+            over = over || fmaxf(x.x, x.y) > ref + kTau;
+            const float p0 = ex2_approx(x.x - mu), p1 = ex2_approx(x.y - mu);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            float x[NT][4];
-            float top[2] = {-INFINITY, -INFINITY};
+            for (int m = 0; m < MT; ++m)
+                if (m == mt) {
+                    add[m][0] += hi ? 0.f : p0 + p1;
+                    add[m][1] += hi ? p0 + p1 : 0.f;
+                }
+            p_s[((mt * (NT / 2) + (i >> 1)) * 32 + lane) * 4 + (i & 1) * 2 + hi] = pack2<BF16>(p0, p1);
+        }
+        return over;
+    };
+    auto softmax = [&](const Spot& u) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                float2 v[2] = {make_float2(s[mt][i][0], s[mt][i][1]), make_float2(s[mt][i][2], s[mt][i][3])};
-                if (g.warps > 1) {
-                    v[0] = fin[((mt * NT + i) * 2) * 32 + lane];
-                    v[1] = fin[((mt * NT + i) * 2 + 1) * 32 + lane];
-                }
-                const int j = u.tile * KT + i * 8 + cpair;
+                part[(wg * SLOTS + (mt * NT + i) * 2) * 32 + lane] = make_float2(s[mt][i][0], s[mt][i][1]);
+                part[(wg * SLOTS + (mt * NT + i) * 2 + 1) * 32 + lane] = make_float2(s[mt][i][2], s[mt][i][3]);
+            }
+        sync_group();
+        float add[MT][2];
+        if (any_group(exponentials(u, add, true))) {
+            // new references: the rows' maxima so far (a unit's first tile comes here)
+            for (int sl = wg; sl < SLOTS; sl += g.warps) {
+                const float2 x = slot_scores(sl, u);
+                float top = fmaxf(x.x, x.y);
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                if ((lane & 3) == 0) tops[sl * 8 + r_lo] = top;
+            }
+            sync_group();
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float alpha[2];
 #pragma unroll
                 for (int hi = 0; hi < 2; ++hi) {
-                    x[i][2 * hi] = j < jlim[mt][hi] ? v[hi].x * c2 : -INFINITY;
-                    x[i][2 * hi + 1] = j + 1 < jlim[mt][hi] ? v[hi].y * c2 : -INFINITY;
-                    top[hi] = fmaxf(top[hi], fmaxf(x[i][2 * hi], x[i][2 * hi + 1]));
+                    float top = m_run[mt][hi];
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) top = fmaxf(top, tops[((mt * NT + i) * 2 + hi) * 8 + r_lo]);
+                    alpha[hi] = top == -INFINITY ? 1.f : ex2_approx(m_run[mt][hi] - top);
+                    m_run[mt][hi] = top;
+                    l_run[mt][hi] *= alpha[hi];
                 }
+#pragma unroll
+                for (int cc = 0; cc < CC; ++cc)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o_acc[cc][i][mt][e] *= alpha[e >> 1];
             }
-            if constexpr (SCORE) {
-                // one warp of the group stores the tile's scores, each in turn
-                if (store) {
+            exponentials(u, add, false);
+            sync_group();
+        }
 #pragma unroll
-                    for (int hi = 0; hi < 2; ++hi) {
-                        const int r = u.rb * ROWS + mt * 16 + hi * 8 + r_lo;
-                        if (r < R) {
-                            float* dst = g.scores +
-                                         ((static_cast<size_t>(u.b) * pb.Hkv + u.hk) * R + r) * g.pitch + u.tile * KT + cpair;
+        for (int mt = 0; mt < MT; ++mt) {
+            l_run[mt][0] += add[mt][0];
+            l_run[mt][1] += add[mt][1];
 #pragma unroll
-                            for (int i = 0; i < NT; ++i)
-                                if (u.tile * KT + i * 8 + cpair < u.keys)
-                                    *reinterpret_cast<float2*>(dst + i * 8) = make_float2(x[i][2 * hi], x[i][2 * hi + 1]);
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int hi = 0; hi < 2; ++hi) {
-                float tm = top[hi];
-                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
-                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
-                const float mn = fmaxf(m_run[mt][hi], tm);
-                alpha[mt][hi] = mn == -INFINITY ? 1.f : ex2_approx(m_run[mt][hi] - mn);
-                m_run[mt][hi] = mn;
-                const float mu = mn == -INFINITY ? 0.f : mn;
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const float p0 = ex2_approx(x[i][2 * hi] - mu), p1 = ex2_approx(x[i][2 * hi + 1] - mu);
-                    sum += p0 + p1;
-                    pa[mt][i >> 1][(i & 1) * 2 + hi] = pack2<BF16>(p0, p1);
-                }
-                l_run[mt][hi] = l_run[mt][hi] * alpha[mt][hi] + sum;
+            for (int kp = 0; kp < NT / 2; ++kp) {
+                const uint4 v = *reinterpret_cast<const uint4*>(p_s + ((mt * (NT / 2) + kp) * 32 + lane) * 4);
+                pa[mt][kp][0] = v.x;
+                pa[mt][kp][1] = v.y;
+                pa[mt][kp][2] = v.z;
+                pa[mt][kp][3] = v.w;
             }
         }
     };
@@ -595,16 +638,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
 #pragma unroll
         for (int cc = 0; cc < CC; ++cc) {
             if (cc >= my_chunks) break;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    o_acc[cc][i][mt][0] *= alpha[mt][0];
-                    o_acc[cc][i][mt][1] *= alpha[mt][0];
-                    o_acc[cc][i][mt][2] *= alpha[mt][1];
-                    o_acc[cc][i][mt][3] *= alpha[mt][1];
-                }
-            if (!ok) continue;
+            if (!ok) break;
             const uint32_t blk = vbase + (wg + 8 * cc) * KT * 128;
             if (valid < KT) {
                 // rows behind the last key: zero (what lies there may be NaN)
@@ -637,6 +671,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
         const bool whole = first == 0 && last == u.tiles;
         const int rows = unit_rows(u);
         const size_t cut = static_cast<size_t>(2 * range + (first == 0 ? 1 : 0)) * ROWS;
+        // the rows' sums: four lanes of each warp hold a share
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -644,8 +679,17 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
                 float l = l_run[mt][hi];
                 l += __shfl_xor_sync(0xffffffffu, l, 1);
                 l += __shfl_xor_sync(0xffffffffu, l, 2);
+                if ((lane & 3) == 0) sums[wg * ROWS + mt * 16 + hi * 8 + r_lo] = l;
+            }
+        sync_group();
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
                 const int r = mt * 16 + hi * 8 + r_lo;
                 if (r >= rows) continue;
+                float l = 0.f;
+                for (int w = 0; w < g.warps; ++w) l += sums[w * ROWS + r];
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 const float l2 = l > 0.f ? m_run[mt][hi] + log2f(l) : -INFINITY;
                 const int ur = u.rb * ROWS + r;  // row of the kv head's group
@@ -976,8 +1020,7 @@ LinePlan line_plan(const Problem& pb, bool shared, int Np)
     g.warps = min(g.chunks, 8);
     g.groups = min(kMaxGroups, 8 / g.warps);
     g.stage_bytes = 2 * g.chunks * 128 << g.shift;
-    const int slots = mt * 2 << g.shift >> 3;
-    const int exchange = g.warps > 1 ? g.groups * (g.warps + 1) * slots * 256 : 0;
+    const int exchange = g.groups * exchange_bytes(g.warps, mt, (1 << g.shift) / 8);
     const int budget = kMaxSmem - static_cast<int>(sizeof(LineStatic)) - kLens * 4 - exchange;
     g.stages = min(kMaxStages, budget / (g.groups * g.stage_bytes));
     p.smem = g.groups * g.stages * g.stage_bytes + exchange;
