@@ -38,10 +38,12 @@ namespace {
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kTau = 8.f;       // a score may lie 2^8 above its row's reference
 constexpr int kMaxStages = 12;
-constexpr int kMaxGroups = 8;
+constexpr int kMaxGroups = 15;
 constexpr int kLens = 1024;     // lengths staged in shared memory; longer batches read them from L2
 constexpr int kLineThreads = 288;  // warps 0..7 compute, warp 8 TMA producer
-// The same with three idle warps: three warpgroups of 168 registers a thread, of
+// Fifteen compute warps and the producer, 128 registers a thread.
+constexpr int kLineThreadsMany = 512;
+// The first with three idle warps: three warpgroups of 168 registers a thread, of
 // which the two that compute take 232 and the producer's keeps 40.
 constexpr int kLineThreadsWide = 384;
 static_assert(2 * 232 + 40 == 3 * 168, "no more registers than the launch gives");
@@ -50,6 +52,7 @@ constexpr int kJoinThreads = 256;
 enum LineSite : uint32_t { LS_PROD = 0x58, LS_FULL, LS_DRAIN };
 
 struct LineGeo {
+    int many;            // the variant with many warps
     int shift;           // keys of a tile: 1 << shift
     int chunks, warps, groups, stages, stage_bytes;
     int rows;            // query rows of a unit (16 or 32)
@@ -80,7 +83,7 @@ struct __align__(1024) LineStatic {
     uint64_t full[kMaxGroups][kMaxStages], empty[kMaxGroups][kMaxStages];
     int abort_flag;
 };
-static_assert(sizeof(LineStatic) == 2048, "static shared block must be whole KiB");
+static_assert(sizeof(LineStatic) == 3072, "static shared block must be whole KiB");
 
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -254,19 +257,22 @@ __host__ __device__ constexpr int exchange_bytes(int warps, int mt, int nt)
 }
 
 // Keys of a tile: as many as the registers of a variant's rows and chunks leave room for.
-template <int MT, int CC>
-__host__ __device__ constexpr int tile_keys() { return MT == 1 && CC == 1 ? 32 : 16; }
+template <int MT, int CC, bool MANY>
+__host__ __device__ constexpr int tile_keys() { return CC == 1 && !MANY ? 32 : 16; }
 
-template <int MT, int CC>
-__host__ __device__ constexpr int line_threads() { return MT == 1 && CC == 1 ? kLineThreads : kLineThreadsWide; }
+template <int MT, int CC, bool MANY>
+__host__ __device__ constexpr int line_threads()
+{
+    return MANY ? kLineThreadsMany : MT == 1 && CC == 1 ? kLineThreads : kLineThreadsWide;
+}
 
-template <bool BF16, int MT, int CC, bool SCORE>
-__global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
+template <bool BF16, int MT, int CC, bool MANY, bool SCORE>
+__global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
     line_kernel(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CUtensorMap tV,
                 const __grid_constant__ CUtensorMap tKp, const __grid_constant__ CUtensorMap tVp, const LineArgs a,
                 const LineGeo g)
 {
-    constexpr int KT = tile_keys<MT, CC>(), NT = KT / 8, ROWS = 16 * MT;
+    constexpr int KT = tile_keys<MT, CC, MANY>(), NT = KT / 8, ROWS = 16 * MT;
     constexpr int SLOTS = MT * NT * 2;  // float2 a lane holds of a tile's scores
     const Problem& pb = a.f.pb;
     __shared__ LineStatic sh;
@@ -316,11 +322,12 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
     auto range_of = [&](int group) { return group * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x); };
     auto ring_of = [&](int group) { return smem + static_cast<size_t>(group) * S * g.stage_bytes; };
 
-    constexpr bool kWide = line_threads<MT, CC>() == kLineThreadsWide;
-    if (warp >= 8) {
+    constexpr bool kWide = line_threads<MT, CC, MANY>() == kLineThreadsWide;
+    constexpr int kProducer = MANY ? 15 : 8;
+    if (warp >= kProducer) {
         // ------------------------------------------------------ producer
         if constexpr (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp > 8) return;
+        if (warp > kProducer) return;
         // lane 2 i loads K of group i, lane 2 i + 1 its V; the groups take turns
         int n_most = 0, mine = 0;
         Spot ahead{};
@@ -402,7 +409,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
 
     // (many rows) the queries as rows of the prefix' kernel, while the first tiles are on their way
     if (g.splits) {
-        const int warps = 8, rows = pb.Hkv * g.Rp;
+        const int warps = kProducer, rows = pb.Hkv * g.Rp;
         for (int row = blockIdx.x * warps + warp; row < rows; row += gridDim.x * warps) {  // [Hkv][B][group][Nq]
             const int hk = row / g.Rp;
             int b, gg, i;
@@ -542,10 +549,17 @@ __global__ void __launch_bounds__(line_threads<MT, CC>(), 1)
     // its scores: the sum over the group's warps, in log2 units, masked
     auto slot_scores = [&](int sl, const Spot& u) {
         float2 p[8];
+        const float2* src = part + sl * 32 + lane;
+        auto fetch = [&](int w) { p[w] = w < g.warps ? src[w * SLOTS * 32] : make_float2(0.f, 0.f); };
+        fetch(0);
+        fetch(1);
+        float x = p[0].x + p[1].x, y = p[0].y + p[1].y;
+        if (g.warps > 2) {
 #pragma unroll
-        for (int w = 0; w < 8; ++w) p[w] = w < g.warps ? part[(w * SLOTS + sl) * 32 + lane] : make_float2(0.f, 0.f);
-        const float x = ((p[0].x + p[1].x) + (p[2].x + p[3].x)) + ((p[4].x + p[5].x) + (p[6].x + p[7].x));
-        const float y = ((p[0].y + p[1].y) + (p[2].y + p[3].y)) + ((p[4].y + p[5].y) + (p[6].y + p[7].y));
+            for (int w = 2; w < 8; ++w) fetch(w);
+            x += (p[2].x + p[3].x) + ((p[4].x + p[5].x) + (p[6].x + p[7].x));
+            y += (p[2].y + p[3].y) + ((p[4].y + p[5].y) + (p[6].y + p[7].y));
+        }
         const int j = (u.tile * KT) + slot_i(sl) * 8 + cpair, end = of_row(jlim, sl);
         return make_float2(j < end ? x * pb.scale_log2 : -INFINITY, j + 1 < end ? y * pb.scale_log2 : -INFINITY);
     };
@@ -907,15 +921,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
         return;
     }
     if constexpr (SCORE) {
-        constexpr int kBatch = 512, kEach = kWeighKeys / kJoinThreads;
-        float acc[kEach], old[kEach];
-        const int j0 = block * kWeighKeys;
+        constexpr int kBatch = 512;
+        static_assert(kWeighKeys == 4 * kJoinThreads, "four keys per thread");
+        const int j = block * kWeighKeys + 4 * tid;
+        float acc[4] = {}, old[4];
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const int j = j0 + k * kJoinThreads + tid;
-            old[k] = j < len ? a.weights[static_cast<size_t>(bh) * pb.Nkv + j] : 0.f;
-            acc[k] = 0.f;
-        }
+        for (int k = 0; k < 4; ++k) old[k] = j + k < len ? a.weights[static_cast<size_t>(bh) * pb.Nkv + j + k] : 0.f;
         for (int rbase = 0; rbase < R; rbase += kBatch) {
             const int nr = min(kBatch, R - rbase);
             __syncthreads();
@@ -944,35 +955,28 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
                 if ((lane & 7) == 0 && q < nr) row_l[q] = mx == -INFINITY ? 0.f : mx + log2f(sum);
             }
             __syncthreads();
-            const float* src = g.scores + (static_cast<size_t>(bh) * R + rbase) * g.pitch + j0 + tid;
-            // four rows' scores in flight; rows and keys past the last are read again and not added
-            int at[kEach];
+            // eight rows' scores in flight; rows past the last are read again and not added
+            const float* src = g.scores + (static_cast<size_t>(bh) * R + rbase) * g.pitch + j;
+            for (int q0 = 0; q0 < nr && j < len; q0 += 8) {
+                float4 x[8];
 #pragma unroll
-            for (int k = 0; k < kEach; ++k) at[k] = min(k * kJoinThreads, len - 1 - j0 - tid);
-            for (int q0 = 0; q0 < nr; q0 += 4) {
-                float x[4][kEach];
+                for (int q = 0; q < 8; ++q)
+                    x[q] = *reinterpret_cast<const float4*>(src + static_cast<size_t>(min(q0 + q, nr - 1)) * g.pitch);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int k = 0; k < kEach; ++k)
-                        x[q][k] = src[static_cast<size_t>(min(q0 + q, nr - 1)) * g.pitch + at[k]];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < 8; ++q)
                     if (q0 + q < nr) {
                         const float l2 = row_l[q0 + q];
-#pragma unroll
-                        for (int k = 0; k < kEach; ++k) acc[k] += exp2f(x[q][k] - l2);
+                        acc[0] += exp2f(x[q].x - l2);
+                        acc[1] += exp2f(x[q].y - l2);
+                        acc[2] += exp2f(x[q].z - l2);
+                        acc[3] += exp2f(x[q].w - l2);
                     }
             }
         }
+        // (entries behind the last token are not touched: what the scores hold there is not added either)
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const int j = j0 + k * kJoinThreads + tid;
-            if (j < len) {
-                const size_t at = static_cast<size_t>(bh) * pb.Nkv + j;
-                a.oweights[at] = old[k] + acc[k];
-            }
-        }
+        for (int k = 0; k < 4; ++k)
+            if (j + k < len) a.oweights[static_cast<size_t>(bh) * pb.Nkv + j + k] = old[k] + acc[k];
     }
 }
 
@@ -993,15 +997,23 @@ LinePlan line_plan(const Problem& pb, bool shared, int Np)
     g.chunks = pb.D / 64;
     g.R = pb.Hq / pb.Hkv * pb.Nq;
     g.Rp = pb.B * g.R;
-    // Rows that a unit's registers hold serve the prefix as well; more rows than
-    // that are the tensor cores'.
-    const int held = g.chunks > 8 ? 16 : 32;
-    const bool split = shared && Np > 0 && g.Rp > held;
-    const int most = shared && !split ? g.Rp : g.R;
+    const int sms = num_sms() > 0 ? num_sms() : 152;
+    // The prefix of sixteen rows is read by this kernel at HBM's rate; with more,
+    // it passes once per sixteen and the tensor cores are faster (D = 512, eight
+    // heads of 16384 keys: 64 rows 74 us), but for prefixes so short that their
+    // launch costs more than eight tiles per SM do.
+    const bool split = shared && Np > 0 && g.Rp > 16 &&
+                       static_cast<long long>(pb.Hkv) * ((g.Rp + 15) / 16) * ((Np + 31) / 32) > 8LL * sms;
+    const int most = shared && !split ? max(g.R, min(g.Rp, 32)) : g.R;
     const int mt = g.chunks > 8 || most <= 16 ? 1 : 2;
     g.rows = 16 * mt;
-    g.shift = mt == 1 && g.chunks <= 8 ? 5 : 4;  // as tile_keys
     g.rblocks = (g.R + g.rows - 1) / g.rows;
+    // Eight compute warps and tiles of 32 keys where they make one or two groups
+    // without rest; else fifteen and tiles of 16 (tile_keys).
+    g.warps = min(g.chunks, 8);
+    g.many = mt == 1 && (g.warps < 4 || 8 % g.warps != 0);
+    g.groups = min(kMaxGroups, (g.many ? 15 : 8) / g.warps);
+    g.shift = g.chunks <= 8 && !g.many ? 5 : 4;
     if (split) {
         p.prefix = pb;
         p.prefix.B = 1;
@@ -1017,14 +1029,12 @@ LinePlan line_plan(const Problem& pb, bool shared, int Np)
         g.tiles_p = (Np + (1 << g.shift) - 1) >> g.shift;
         if (g.tiles_p == 0) g.rblocks_p = 0;
     }
-    g.warps = min(g.chunks, 8);
-    g.groups = min(kMaxGroups, 8 / g.warps);
     g.stage_bytes = 2 * g.chunks * 128 << g.shift;
     const int exchange = g.groups * exchange_bytes(g.warps, mt, (1 << g.shift) / 8);
     const int budget = kMaxSmem - static_cast<int>(sizeof(LineStatic)) - kLens * 4 - exchange;
     g.stages = min(kMaxStages, budget / (g.groups * g.stage_bytes));
     p.smem = g.groups * g.stages * g.stage_bytes + exchange;
-    p.ctas = num_sms() > 0 ? num_sms() : 152;
+    p.ctas = sms;
     g.ranges = p.ctas * g.groups;
     g.pitch = (pb.Nkv + 3) & ~3;
     const size_t rows_all = static_cast<size_t>(pb.B) * pb.Hq * pb.Nq, D = pb.D;
@@ -1051,13 +1061,13 @@ LinePlan line_plan(const Problem& pb, bool shared, int Np)
     return p;
 }
 
-template <bool BF16, int MT, int CC>
+template <bool BF16, int MT, int CC, bool MANY = false>
 cudaError_t launch_variant(const LineArgs& a, const LinePlan& p, const CUtensorMap* m, cudaStream_t s)
 {
-    auto kern = a.shared ? line_kernel<BF16, MT, CC, false> : line_kernel<BF16, MT, CC, true>;
+    auto kern = a.shared ? line_kernel<BF16, MT, CC, MANY, false> : line_kernel<BF16, MT, CC, MANY, true>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(p.ctas), line_threads<MT, CC>(), p.smem, s, m[0], m[1], m[2], m[3], a, p.g);
+    return launch_dependent(kern, dim3(p.ctas), line_threads<MT, CC, MANY>(), p.smem, s, m[0], m[1], m[2], m[3], a, p.g);
 }
 
 }  // namespace
@@ -1111,6 +1121,8 @@ cudaError_t launch_line(const LineArgs& args, void* workspace, cudaStream_t s)
     cudaError_t e;
     if (g.chunks > 8)
         e = a.f.bf16 ? launch_variant<true, 1, 2>(a, p, m, s) : launch_variant<false, 1, 2>(a, p, m, s);
+    else if (g.many)
+        e = a.f.bf16 ? launch_variant<true, 1, 1, true>(a, p, m, s) : launch_variant<false, 1, 1, true>(a, p, m, s);
     else if (g.rows == 16)
         e = a.f.bf16 ? launch_variant<true, 1, 1>(a, p, m, s) : launch_variant<false, 1, 1>(a, p, m, s);
     else
@@ -1143,8 +1155,8 @@ cudaError_t launch_line(const LineArgs& args, void* workspace, cudaStream_t s)
     const int rows = pb.B * pb.Hq * pb.Nq;
     const int key_blocks = a.shared ? 0 : (pb.Nkv + kWeighKeys - 1) / kWeighKeys;
     // a warp per 128 head dims of a row as long as one round of warps holds them
-    const int sms = p.ctas, slices = (pb.D + 127) >> 7;
-    const bool many = static_cast<long long>(rows) * slices > 32LL * sms;
+    const int slices = (pb.D + 127) >> 7;
+    const bool many = static_cast<long long>(rows) * slices > 32LL * p.ctas;
     const int parts = many ? 1 : slices;
     const int row_ctas = static_cast<int>((static_cast<long long>(rows) * parts + kJoinWarps - 1) / kJoinWarps);
     const long long ctas = row_ctas + static_cast<long long>(pb.B) * pb.Hkv * key_blocks;
