@@ -867,13 +867,18 @@ ffpa_status check_line(ffpa_dtype dt, const ffpa_view& q, const ffpa_view& k, co
 
 ffpa_status run_line(ffpa::LineArgs& a, void* workspace, size_t workspace_bytes, ffpa_stream_t stream)
 {
-    const size_t need = ffpa::line_workspace_bytes(a.f.pb, a.shared, a.Np);
+    if (workspace_bytes > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return fail(FFPA_ERR_INVALID_VALUE, "decode workspace must be non-NULL and 256-byte aligned");
+    ffpa_status st = device_ctl(&a.f.ctl);
+    size_t need = 0;
+    cudaError_t e = cudaSuccess;
+    if (st == FFPA_OK)
+        e = ffpa::launch_line(a, workspace, workspace_bytes, &need, reinterpret_cast<cudaStream_t>(stream));
+    else
+        need = ffpa::line_workspace_bytes(a.f.pb, a.shared, a.Np);
     if (workspace_bytes < need)
         return fail(FFPA_ERR_INVALID_VALUE, "decode workspace too small: %zu < %zu bytes", workspace_bytes, need);
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
-        return fail(FFPA_ERR_INVALID_VALUE, "decode workspace must be non-NULL and 256-byte aligned");
-    FFPA_TRY(device_ctl(&a.f.ctl));
-    return launch_result(ffpa::launch_line(a, workspace, reinterpret_cast<cudaStream_t>(stream)), "decode launch");
+    return st == FFPA_OK ? launch_result(e, "decode launch") : st;
 }
 
 // Workspace queries answer 0 for sizes outside the operation.

@@ -62,6 +62,7 @@ struct LineArgs {
 };
 size_t line_workspace_bytes(const Problem& pb, bool shared, int Np);
 bool line_fits(const Problem& pb, bool shared, int Np);  // its tiles can be numbered
-cudaError_t launch_line(const LineArgs& a, void* workspace, cudaStream_t s);
+// Launches nothing where the workspace is smaller than `need`, which it tells.
+cudaError_t launch_line(const LineArgs& a, void* workspace, size_t workspace_bytes, size_t* need, cudaStream_t s);
 
 }  // namespace ffpa

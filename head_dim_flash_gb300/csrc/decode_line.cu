@@ -5,8 +5,10 @@
 // With few query rows the work is reading K and V once. The key tiles of all
 // units (sequence, kv head, block of rows) form one line, the shared prefix's
 // units at its front, and the line is cut into equal ranges, one per group of
-// warps: ragged lengths keep every SM busy to the end. The cut is made on the
-// device, from the lengths there. A range's first and last unit may reach
+// warps: ragged lengths keep every SM busy to the end. Each unit takes two tiles
+// more of the line than it has, for its start and end (a batch of short contexts
+// behind a prefix would otherwise fall to a few ranges: 106 us against 68). The cut
+// is made on the device, from the lengths there. A range's first and last unit may reach
 // into its neighbours': such a piece leaves a normalised O (fp32) and the log2
 // of its sum in the workspace, and a second kernel joins them:
 //   L = log2 sum_s 2^L_s,  O = sum_s 2^(L_s - L) O_s.
@@ -27,6 +29,7 @@
 //
 // Rows behind a sequence's length hold anything: their scores are replaced,
 // not multiplied, and their V rows are zeroed in shared memory.
+#include <atomic>
 #include <cstring>
 
 #include "cache_ops.h"
@@ -36,6 +39,7 @@ namespace ffpa {
 namespace {
 
 constexpr float kLn2 = 0.693147180559945309f;
+constexpr int kUnitPlaces = 2;    // of a unit in the line besides its tiles
 constexpr float kTau = 8.f;       // a score may lie 2^8 above its row's reference
 constexpr int kMaxStages = 12;
 constexpr int kMaxGroups = 15;
@@ -85,6 +89,8 @@ struct __align__(1024) LineStatic {
 };
 static_assert(sizeof(LineStatic) == 3072, "static shared block must be whole KiB");
 
+constexpr int kLineSmem = kMaxSmem - static_cast<int>(sizeof(LineStatic)) - kLens * 4;  // dynamic
+
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -128,27 +134,33 @@ __device__ __forceinline__ int tiles_of(const LineGeo& g, int keys)
     return static_cast<int>((static_cast<unsigned>(keys) + (1u << g.shift) - 1) >> g.shift);
 }
 
-// Tiles of the whole line (below 2^31), and those before sequence `b` (by whole warps).
+// Places that a unit of so many tiles takes in the line: its start's, then a tile each.
+__device__ __forceinline__ int places_of(int tiles) { return tiles > 0 ? tiles + kUnitPlaces : 0; }
+
+// Places of the whole line (below 2^31), those before sequence `b`, and the units that have tiles (by whole warps).
 __device__ __forceinline__ void line_sums(const LineArgs& a, const LineGeo& g, const int* staged, int b, int& total,
-                                          int& before)
+                                          int& before, int& units)
 {
     const Problem& pb = a.f.pb;
-    int t = 0, p = 0;
+    int t = 0, p = 0, u = 0;
 #pragma unroll 4
     for (int i = threadIdx.x & 31; i < pb.B; i += 32) {
-        const int n = tiles_of(g, staged ? staged[i] : clamp_len(a, i));
+        const int n = places_of(tiles_of(g, staged ? staged[i] : clamp_len(a, i)));
         t += n;
+        u += n > 0;
         if (i < b) p += n;
     }
     t = __reduce_add_sync(0xffffffffu, t);
     p = __reduce_add_sync(0xffffffffu, p);
-    const int per = pb.Hkv * g.rblocks, prefix = pb.Hkv * g.rblocks_p * g.tiles_p;
+    u = __reduce_add_sync(0xffffffffu, u);
+    const int per = pb.Hkv * g.rblocks, prefix = pb.Hkv * g.rblocks_p * places_of(g.tiles_p);
     total = prefix + t * per;
     before = prefix + p * per;
+    units = pb.Hkv * g.rblocks_p + u * per;
 }
 
-// The line cut into ranges, no more than it has tiles, so that none is empty:
-// the first `longer` hold one tile more than the others.
+// The line cut into ranges, no more than it has places: the first `longer` hold
+// one more than the others.
 struct Cuts {
     int ranges, each, longer;
     __device__ Cuts(const LineGeo& g, int total)
@@ -158,7 +170,7 @@ struct Cuts {
         longer = total - each * ranges;
     }
     __device__ int begin(int r) const { return r * each + min(r, longer); }
-    __device__ int holding(int t) const  // the range that holds tile t
+    __device__ int holding(int t) const  // the range that holds place t
     {
         const int head = longer * (each + 1);
         return t < head ? t / (each + 1) : longer + (t - head) / each;
@@ -191,28 +203,30 @@ struct Line {
         ++s.b;
         enter(s);
     }
-    // The place of tile t of the line (called by whole warps).
-    __device__ Spot find(int t) const
+    // The first tile at or behind place t of the line, which lies before its end, and
+    // how many tiles lie before it (called by whole warps).
+    __device__ Spot find(int t, int& done) const
     {
         Spot s{};
         const int H = a.f.pb.Hkv;
-        const int prefix = H * g.rblocks_p * g.tiles_p;
+        const int prefix_places = places_of(g.tiles_p), prefix = H * g.rblocks_p * prefix_places;
         if (t < prefix) {
-            const int unit = t / g.tiles_p;
+            const int unit = t / prefix_places;
             s.b = -1;
             s.hk = unit / g.rblocks_p;
             s.rb = unit - s.hk * g.rblocks_p;
-            s.tile = t - unit * g.tiles_p;
+            s.tile = max(0, t - unit * prefix_places - kUnitPlaces);
             s.tiles = g.tiles_p;
             s.keys = a.Np;
+            done = unit * g.tiles_p + s.tile;
             return s;
         }
         t -= prefix;
+        done = H * g.rblocks_p * g.tiles_p;
         const int per = H * g.rblocks, lane = threadIdx.x & 31;
-        int run = 0;
         s.b = a.f.pb.B;
-        for (int i0 = 0; i0 < a.f.pb.B; i0 += 32) {
-            const int n = i0 + lane < a.f.pb.B ? tiles_of(g, len(i0 + lane)) : 0;
+        for (int i0 = 0, run = 0, units = 0; i0 < a.f.pb.B; i0 += 32) {
+            const int tiles = i0 + lane < a.f.pb.B ? tiles_of(g, len(i0 + lane)) : 0, n = places_of(tiles);
             int incl = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -220,20 +234,34 @@ struct Line {
                 if (lane >= d) incl += o;
             }
             const uint32_t past = __ballot_sync(0xffffffffu, (run + incl) * per > t);
+            const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
             if (past) {
                 const int at = __ffs(past) - 1;
-                const int rest = t - __shfl_sync(0xffffffffu, (run + incl - n) * per, at);
+                const int first = run + __shfl_sync(0xffffffffu, incl - n, at);
+                units += __popc(some & ((1u << at) - 1));
                 s.b = i0 + at;
-                s.tiles = __shfl_sync(0xffffffffu, n, at);
-                const int unit = rest / s.tiles;
-                s.tile = rest - unit * s.tiles;
+                s.tiles = __shfl_sync(0xffffffffu, tiles, at);
+                const int rest = t - first * per, places = places_of(s.tiles);
+                const int unit = rest / places;
+                s.tile = max(0, rest - unit * places - kUnitPlaces);
                 s.hk = unit / g.rblocks;
                 s.rb = unit - s.hk * g.rblocks;
                 s.keys = len(s.b);
+                done += (first - units * kUnitPlaces) * per + unit * s.tiles + s.tile;
                 return s;
             }
             run += __shfl_sync(0xffffffffu, incl, 31);
+            units += __popc(some);
         }
+        return s;
+    }
+    // The tiles of a range: where they begin, and how many.
+    __device__ Spot range(const Cuts& c, int r, int total, int units, int& n) const
+    {
+        int from = 0, to = total - units * kUnitPlaces;
+        const Spot s = find(c.begin(r), from);
+        if (r + 1 < c.ranges) find(c.begin(r + 1), to);
+        n = to - from;
         return s;
     }
 };
@@ -311,8 +339,8 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
         }
     __syncthreads();
     const Line line{a, g, a.lens && pb.B <= kLens ? s_len : nullptr};
-    int total, unused;
-    line_sums(a, g, line.lens, 0, total, unused);
+    int total, unused, units;
+    line_sums(a, g, line.lens, 0, total, unused, units);
     const Cuts cuts(g, total);
     volatile int* abort_p = &sh.abort_flag;
     uint32_t* status = a.f.ctl.status;
@@ -334,8 +362,8 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
         for (int i = 0; i < g.groups; ++i) {
             const int r = range_of(i);
             if (r >= cuts.ranges) break;
-            const int first = cuts.begin(r), n = cuts.begin(r + 1) - first;
-            const Spot at = line.find(first);
+            int n;
+            const Spot at = line.range(cuts, r, total, units, n);
             n_most = max(n_most, n);
             if (lane >> 1 == i) {
                 mine = n;
@@ -377,9 +405,9 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
     if constexpr (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int group = warp / g.warps, wg = warp - group * g.warps;
     const int range = warp < compute ? range_of(group) : cuts.ranges;
-    const bool work = range < cuts.ranges;
-    const int n = work ? cuts.begin(range + 1) - cuts.begin(range) : 0;
-    const Spot spot = line.find(work ? cuts.begin(range) : 0);
+    int n = 0;
+    Spot spot{};
+    if (range < cuts.ranges) spot = line.range(cuts, range, total, units, n);
     uint8_t* const ring = ring_of(group);
     float2* const part = reinterpret_cast<float2*>(smem + static_cast<size_t>(g.groups) * S * g.stage_bytes) +
                          group * exchange_bytes(g.warps, MT, NT) / 8;       // [warps][slot][lane] partial scores
@@ -421,7 +449,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
                 *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
         }
     }
-    if (!work) return;  // no barrier below spans groups
+    if (n == 0) return;  // no barrier below spans groups
     // ------------------------------------------------------------ products
     const int my_chunks = CC == 1 ? 1 : (wg < g.chunks) + (wg + 8 < g.chunks);
     const int r_lo = lane >> 2, cpair = (lane & 3) * 2;
@@ -778,15 +806,15 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
 }
 
 // ------------------------------------------------------------------ joining
-// The pieces of a unit's tiles [s0, s0 + tiles): one per range that holds some.
+// The pieces of a unit that begins at place s0: one per range that holds tiles of it.
 // The first begins inside its range (cut slot 1 there), later ones at theirs (slot 0).
 struct Pieces {
     int first, count;
     bool whole;  // one range holds it all: not in the cut slots
     __device__ Pieces(const Cuts& c, int s0, int tiles)
     {
-        first = tiles > 0 ? c.holding(s0) : 0;
-        count = tiles > 0 ? c.holding(s0 + tiles - 1) - first + 1 : 0;
+        first = tiles > 0 ? c.holding(s0 + kUnitPlaces) : 0;
+        count = tiles > 0 ? c.holding(s0 + kUnitPlaces + tiles - 1) - first + 1 : 0;
         whole = count == 1;
     }
     __device__ int slot(int i) const { return i == 0 ? 2 * first + 1 : 2 * (first + i); }
@@ -830,18 +858,18 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
     const int b = bh / pb.Hkv, hk = bh - b * pb.Hkv;
     const int len = clamp_len(a, b);
     if (!is_row && block * kWeighKeys >= len) return;
-    int total, before;
-    line_sums(a, g, nullptr, b, total, before);
+    int total, before, units;
+    line_sums(a, g, nullptr, b, total, before, units);
     const Cuts cuts(g, total);
     const int tiles = tiles_of(g, len);
 
     if (is_row) {
         const int r = row - bh * R;
         const int rb = r / g.rows, ur = r - rb * g.rows;
-        const Pieces own(cuts, before + (hk * g.rblocks + rb) * tiles, tiles);
+        const Pieces own(cuts, before + (hk * g.rblocks + rb) * places_of(tiles), tiles);
         if (!a.shared && own.whole) return;  // written by the first kernel
         const int rp = b * R + r, rbp = rp / g.rows, urp = rp - rbp * g.rows;
-        const Pieces pre(cuts, (hk * g.rblocks_p + rbp) * g.tiles_p, g.rblocks_p ? g.tiles_p : 0);
+        const Pieces pre(cuts, (hk * g.rblocks_p + rbp) * places_of(g.tiles_p), g.rblocks_p ? g.tiles_p : 0);
         const int np = g.splits ? g.splits : pre.count, pieces = np + own.count;
         auto find = [&](int i, const float*& l, const float*& o) {
             size_t at;
@@ -934,7 +962,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
             for (int q0 = warp * 4; q0 < nr; q0 += kJoinThreads / 8) {
                 const int q = q0 + (lane >> 3), r = rbase + min(q, nr - 1);
                 const int rb = r / g.rows, ur = r - rb * g.rows;
-                const Pieces own(cuts, before + (hk * g.rblocks + rb) * tiles, tiles);
+                const Pieces own(cuts, before + (hk * g.rblocks + rb) * places_of(tiles), tiles);
                 float mx = -INFINITY, sum = 0.f;
                 if (own.whole) {
                     mx = g.l_whole[static_cast<size_t>(bh) * R + r];
@@ -1031,7 +1059,7 @@ LinePlan line_plan(const Problem& pb, bool shared, int Np)
     }
     g.stage_bytes = 2 * g.chunks * 128 << g.shift;
     const int exchange = g.groups * exchange_bytes(g.warps, mt, (1 << g.shift) / 8);
-    const int budget = kMaxSmem - static_cast<int>(sizeof(LineStatic)) - kLens * 4 - exchange;
+    const int budget = kLineSmem - exchange;
     g.stages = min(kMaxStages, budget / (g.groups * g.stage_bytes));
     p.smem = g.groups * g.stages * g.stage_bytes + exchange;
     p.ctas = sms;
@@ -1065,8 +1093,17 @@ template <bool BF16, int MT, int CC, bool MANY = false>
 cudaError_t launch_variant(const LineArgs& a, const LinePlan& p, const CUtensorMap* m, cudaStream_t s)
 {
     auto kern = a.shared ? line_kernel<BF16, MT, CC, MANY, false> : line_kernel<BF16, MT, CC, MANY, true>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+    // the kernel's allowance of shared memory: once per device
+    static std::atomic<uint64_t> allowed[2];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(allowed[a.shared].load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLineSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) allowed[a.shared].fetch_or(bit, std::memory_order_relaxed);
+    }
     return launch_dependent(kern, dim3(p.ctas), line_threads<MT, CC, MANY>(), p.smem, s, m[0], m[1], m[2], m[3], a, p.g);
 }
 
@@ -1078,7 +1115,8 @@ bool line_fits(const Problem& pb, bool shared, int Np)
     if (R * pb.B > 0x7fffffffLL) return false;
     // rows are joined by a CTA each; key tiles of a range are counted in 31 bits
     const long long units = static_cast<long long>(pb.B) * pb.Hkv * ((R + 15) / 16);
-    const long long tiles = units * (pb.Nkv / 16 + 1) + (shared ? static_cast<long long>(pb.Hkv) * ((R * pb.B + 15) / 16) * (Np / 16 + 1) : 0);
+    const long long tiles = units * (pb.Nkv / 16 + 1 + kUnitPlaces) +
+        (shared ? static_cast<long long>(pb.Hkv) * ((R * pb.B + 15) / 16) * (Np / 16 + 1 + kUnitPlaces) : 0);
     return tiles < 0x7fffffffLL && R * pb.B * pb.Hkv < 0x10000000LL;
 }
 
@@ -1088,12 +1126,14 @@ size_t line_workspace_bytes(const Problem& pb, bool shared, int Np)
     return line_plan(pb, shared, Np).total;
 }
 
-cudaError_t launch_line(const LineArgs& args, void* workspace, cudaStream_t s)
+cudaError_t launch_line(const LineArgs& args, void* workspace, size_t workspace_bytes, size_t* need, cudaStream_t s)
 {
     LineArgs a = args;
     const Problem& pb = a.f.pb;
     LinePlan p = line_plan(pb, a.shared, a.Np);
     LineGeo& g = p.g;
+    *need = p.total;
+    if (workspace_bytes < p.total) return cudaErrorInvalidValue;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
     g.o_cut = at(p.o_cut);

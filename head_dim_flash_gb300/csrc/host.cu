@@ -2,6 +2,7 @@
 // maps over strided dense views and the packed varlen layout, device queries.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "kernels.h"
@@ -142,9 +143,13 @@ bool unit_grid(unsigned x, long long n_units, dim3* grid)
 
 int num_sms()
 {
+    // asked several times per call: looked up once per device
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

@@ -1120,13 +1120,12 @@ int xchg_splits(const Problem& pb)
     // time in super-steps of C tiles: the waves' steps and a start and end worth
     // four of them; a split's parts are written and read again (fp32), which is
     // worth half a step of every cluster
-    double best = 0;
+    long long best = 0;
     int splits = 1;
     for (int n = 1; n <= std::min(tiles, kDecodeMaxSplits); ++n) {
         const int per = (tiles + n - 1) / n;
         if ((tiles + per - 1) / per != n) continue;
-        const double cost = static_cast<double>((units * n + at_once - 1) / at_once) * ((per + C - 1) / C + 4) +
-                            0.5 * static_cast<double>(units * n) / at_once;
+        const long long cost = 8 * ((units * n + at_once - 1) / at_once) * ((per + C - 1) / C + 4) + 4 * units * n / at_once;
         if (best == 0 || cost < best) {
             best = cost;
             splits = n;
