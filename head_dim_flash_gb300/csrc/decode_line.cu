@@ -85,9 +85,13 @@ struct Spot {
 
 struct __align__(1024) LineStatic {
     uint64_t full[kMaxGroups][kMaxStages], empty[kMaxGroups][kMaxStages];
+    struct {
+        Spot at;         // first tile of the group's range
+        int from, to;    // tiles of the line before its first and behind its last
+    } start[kMaxGroups];
     int abort_flag;
 };
-static_assert(sizeof(LineStatic) == 3072, "static shared block must be whole KiB");
+static_assert(sizeof(LineStatic) == 4096, "static shared block must be whole KiB");
 
 constexpr int kLineSmem = kMaxSmem - static_cast<int>(sizeof(LineStatic)) - kLens * 4;  // dynamic
 
@@ -255,15 +259,6 @@ struct Line {
         }
         return s;
     }
-    // The tiles of a range: where they begin, and how many.
-    __device__ Spot range(const Cuts& c, int r, int total, int units, int& n) const
-    {
-        int from = 0, to = total - units * kUnitPlaces;
-        const Spot s = find(c.begin(r), from);
-        if (r + 1 < c.ranges) find(c.begin(r + 1), to);
-        n = to - from;
-        return s;
-    }
 };
 
 // Row r of a unit: its (sequence, query head within the group, query).
@@ -349,6 +344,24 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
     // neighbouring ranges go to different SMs: a line of few tiles does not crowd a few of them
     auto range_of = [&](int group) { return group * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x); };
     auto ring_of = [&](int group) { return smem + static_cast<size_t>(group) * S * g.stage_bytes; };
+    // where the groups' ranges begin and end: a warp for each
+    for (int job = warp; job < 2 * g.groups; job += blockDim.x >> 5) {
+        auto& start = sh.start[job >> 1];
+        const int r = range_of(job >> 1) + (job & 1);
+        int done = total - units * kUnitPlaces;
+        Spot at{};
+        if (r < cuts.ranges) at = line.find(cuts.begin(r), done);
+        if (lane == 0) {
+            if (job & 1) {
+                start.to = done;
+            } else {
+                start.at = at;
+                start.from = done;
+            }
+        }
+    }
+    __syncthreads();
+    auto tiles_in = [&](int group) { return max(0, sh.start[group].to - sh.start[group].from); };  // 0: no range
 
     constexpr bool kWide = line_threads<MT, CC, MANY>() == kLineThreadsWide;
     constexpr int kProducer = MANY ? 15 : 8;
@@ -357,20 +370,10 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
         if constexpr (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp > kProducer) return;
         // lane 2 i loads K of group i, lane 2 i + 1 its V; the groups take turns
-        int n_most = 0, mine = 0;
-        Spot ahead{};
-        for (int i = 0; i < g.groups; ++i) {
-            const int r = range_of(i);
-            if (r >= cuts.ranges) break;
-            int n;
-            const Spot at = line.range(cuts, r, total, units, n);
-            n_most = max(n_most, n);
-            if (lane >> 1 == i) {
-                mine = n;
-                ahead = at;
-            }
-        }
         const int group = min(lane >> 1, g.groups - 1);
+        const int mine = lane >> 1 < g.groups ? tiles_in(group) : 0;
+        const int n_most = __reduce_max_sync(0xffffffffu, mine);
+        Spot ahead = sh.start[group].at;
         uint64_t* const full = sh.full[group];
         uint8_t* const ring = ring_of(group) + (lane & 1) * half_bytes;
         int st = 0, issued = 0;
@@ -404,10 +407,8 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
     }
     if constexpr (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int group = warp / g.warps, wg = warp - group * g.warps;
-    const int range = warp < compute ? range_of(group) : cuts.ranges;
-    int n = 0;
-    Spot spot{};
-    if (range < cuts.ranges) spot = line.range(cuts, range, total, units, n);
+    const int range = range_of(group);
+    const int n = warp < compute ? tiles_in(group) : 0;
     uint8_t* const ring = ring_of(group);
     float2* const part = reinterpret_cast<float2*>(smem + static_cast<size_t>(g.groups) * S * g.stage_bytes) +
                          group * exchange_bytes(g.warps, MT, NT) / 8;       // [warps][slot][lane] partial scores
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
     uint32_t pa[MT][NT / 2][4];
     float s[MT][NT][4];
     bool ok = true;
-    Spot unit = spot;               // the unit whose scores are computed
+    Spot unit = sh.start[group].at;  // the unit whose scores are computed
 
     auto unit_rows = [&](const Spot& u) { return (u.b < 0 ? g.Rp : R) - u.rb * ROWS; };
     // queries and key limits of a unit
