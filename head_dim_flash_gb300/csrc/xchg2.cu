@@ -1184,13 +1184,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 32; ++e) v[e] = 0u;
                 }
                 if constexpr (SPLIT) {
-                    if (row_ok) {
-                        float4* d4 = reinterpret_cast<float4*>(part + cc);
+                    // 32 rows x 32 columns of fp32 through the idle ring, so that a store
+                    // writes whole 128-byte lines (one row per lane would touch 32 of them)
+                    float* stage = reinterpret_cast<float*>(sRing + 1024) + (warp - 2) * 32 * 36;
+                    const int lane = static_cast<int>(lane_id());
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            d4[e] = make_float4(__uint_as_float(v[4 * e]) * mul, __uint_as_float(v[4 * e + 1]) * mul,
-                                                __uint_as_float(v[4 * e + 2]) * mul, __uint_as_float(v[4 * e + 3]) * mul);
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4*>(stage + lane * 36 + 4 * e) =
+                            make_float4(__uint_as_float(v[4 * e]) * mul, __uint_as_float(v[4 * e + 1]) * mul,
+                                        __uint_as_float(v[4 * e + 2]) * mul, __uint_as_float(v[4 * e + 3]) * mul);
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int rr = 4 * e + (lane >> 3);  // row of the warp's 32
+                        const float4 x = *reinterpret_cast<const float4*>(stage + rr * 36 + (lane & 7) * 4);
+                        if (row - r + quarter * 32 + rr < row_len)
+                            *reinterpret_cast<float4*>(part + static_cast<long long>(rr - lane) * pb.D + cc +
+                                                       (lane & 7) * 4) = x;
                     }
+                    __syncwarp();
                     continue;
                 }
                 uint32_t w[16];
