@@ -28,6 +28,7 @@
 // Warp roles: warp 0 TMA producer, warp 1 MMA issuer (and TMEM owner),
 // warps 2..5 elementwise (one tile row per thread) and epilogue.
 #include <algorithm>
+#include <atomic>
 #include <cstdlib>
 #include <cstring>
 
@@ -1113,9 +1114,40 @@ bool xchg_uses_pair(const Problem& pb)
 
 namespace {
 
-// A split forward takes pairs where the forward does and its rows fill more
-// than one CTA's 128.
-bool split_uses_pair(const Problem& pb) { return xchg_uses_pair(pb) && pb.Nq > 128; }
+// A split forward takes pairs where its rows fill more than one CTA's 128 and
+// the slabs are whole (16384 keys of eight heads, 512 rows: D = 512 179 us against
+// 198; D = 384 152 against 153, 640 158 against 156, 768 with 256 rows 306 against 289).
+bool split_uses_pair(const Problem& pb) { return xchg_uses_pair(pb) && pb.Nq > 128 && pb.D == 512; }
+
+// Clusters of `size` one-CTA-per-SM CTAs that run at once on the current device:
+// sizes above 2 do not reach every SM (46 of 3, 36 of 4, 23 of 6, 15 of 8).
+int clusters_at_once(int size)
+{
+    static std::atomic<int> known[64][9];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    if ((n = known[dev][size].load(std::memory_order_relaxed)) > 0) return n;
+    auto kern = xchg_kernel<XOP_FWD, true, false, true>;
+    const int smem = kMaxSmem - static_cast<int>(sizeof(StaticSmem));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size, 1000);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        return 144 / size;  // no device: any number does
+    }
+    known[dev][size].store(n, std::memory_order_relaxed);
+    return n;
+}
 
 }  // namespace
 
@@ -1123,10 +1155,7 @@ int xchg_splits(const Problem& pb)
 {
     const bool pair = split_uses_pair(pb);
     const int C = pair ? ((pb.D + 127) / 128 * 128 + 255) / 256 : ((pb.D + 63) / 64 + 3) / 4;
-    const int cluster = pair ? 2 * C : C;
-    const int sms = num_sms() > 0 ? num_sms() : 152;
-    // clusters that run at once: cluster sizes above 2 do not reach every SM
-    const long long at_once = std::max(1, (cluster <= 2 ? sms : sms - 8) / cluster);
+    const long long at_once = clusters_at_once(pair ? 2 * C : C);
     const long long units = static_cast<long long>(pb.Hq) * ((pb.Nq + (pair ? 255 : 127)) / (pair ? 256 : 128));
     const int tiles = (pb.Nkv + 127) / 128;
     // time in super-steps of C tiles: the waves' steps and a start and end worth
