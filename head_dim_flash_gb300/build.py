@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libffpa.so")
 SOURCES = ("api.cu", "host.cu", "bwd.cu", "xchg.cu", "xchg2.cu", "decode.cu", "fp8.cu", "dsq.cu", "noalloc.cu",
-           "kv4.cu", "decode_kv4.cu", "rope.cu", "decode_line.cu", "evict.cu")
+           "kv4.cu", "decode_kv4.cu", "rope.cu", "evict.cu", "decode_line.cu",
+           "decode_line_bf16.cu", "decode_line_fp16.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1203,16 +1203,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                        (lane & 7) * 4) = x;
                     }
                     __syncwarp();
-                    continue;
-                }
-                uint32_t w[16];
+                } else {
+                    uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    w[e] = pack2<BF16>(__uint_as_float(v[2 * e]) * mul, __uint_as_float(v[2 * e + 1]) * mul);
-                if (row_ok) {
-                    uint4* d4 = reinterpret_cast<uint4*>(dst + cc);
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack2<BF16>(__uint_as_float(v[2 * e]) * mul, __uint_as_float(v[2 * e + 1]) * mul);
+                    if (row_ok) {
+                        uint4* d4 = reinterpret_cast<uint4*>(dst + cc);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) d4[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                        for (int e = 0; e < 4; ++e) d4[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    }
                 }
             }
             if (OP == XOP_FWD && c == 0 && half == 0 && row_ok) {
