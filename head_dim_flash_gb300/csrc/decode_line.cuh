@@ -840,7 +840,7 @@ constexpr int kJoinWarps = kJoinThreads / 32;
 
 
 template <bool BF16, bool SCORE, int LOADS>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, const LineGeo g, const int rows,
+__global__ void __launch_bounds__(kJoinThreads, LOADS > 8 ? 2 : SCORE ? 4 : 3) join_kernel(const LineArgs a, const LineGeo g, const int rows,
                                                             const int row_ctas, const int key_blocks,
                                                             const int parts)
 {
@@ -901,29 +901,37 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
         };
         const int gg = r / pb.Nq, qi = r - gg * pb.Nq;
         uint16_t* out = static_cast<uint16_t*>(a.f.o) + b * pb.vo.sb + (hk * (pb.Hq / pb.Hkv) + gg) * pb.vo.sh + qi * pb.vo.sn;
-        float top = -INFINITY, total_w = 0.f;
-        // Most rows have up to 32 pieces, a lane for each. More are taken in turn:
-        // the largest of all first.
-        for (int i = lane; i < pieces; i += 32) {
-            const float *l, *o;
+        // Most rows have up to 32 pieces, a lane for each; more are taken in turn.
+        float top = -INFINITY, sum = 0.f, w0 = 0.f;
+        const float *l = nullptr, *o0 = nullptr;
+        if (lane < pieces) {
+            find(lane, l, o0);
+            top = w0 = *l;
+        }
+        for (int i = 32 + lane; i < pieces; i += 32) {
+            const float* o;
             find(i, l, o);
             top = fmaxf(top, *l);
         }
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        w0 = lane < pieces && top > -INFINITY ? exp2f(w0 - top) : 0.f;
         for (int c0 = part * 128; c0 < pb.D; c0 += parts * 128) {
             const int col = c0 + lane * 4;
             const bool mine = col < pb.D;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            float sum = 0.f;
+            sum = w0;
             for (int p0 = 0; p0 < pieces && top > -INFINITY; p0 += 32) {
-                const float *l = nullptr, *o = nullptr;
-                float w = 0.f;
-                if (p0 + lane < pieces) {
-                    find(p0 + lane, l, o);
-                    w = exp2f(*l - top);
+                const float* o = o0;
+                float w = w0;
+                if (p0) {
+                    w = 0.f;
+                    if (p0 + lane < pieces) {
+                        find(p0 + lane, l, o);
+                        w = exp2f(*l - top);
+                    }
+                    sum += w;
                 }
-                sum += w;
                 // several loads in flight; past the last piece, its own again with no weight
                 const int n = min(32, pieces - p0);
                 for (int k0 = 0; k0 < n; k0 += LOADS) {
@@ -949,13 +957,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LineArgs a, co
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            total_w = sum;
             const float inv = sum > 0.f ? 1.f / sum : 0.f;
             if (mine)
                 *reinterpret_cast<uint2*>(out + col) =
                     make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
         }
-        if (part == 0 && lane == 0) a.f.lse[row] = total_w > 0.f ? (top + log2f(total_w)) * kLn2 : -INFINITY;
+        if (part == 0 && lane == 0) a.f.lse[row] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
         return;
     }
     if constexpr (SCORE) {
@@ -1078,7 +1085,7 @@ cudaError_t run_join(const LineArgs& a, const LinePlan& p, cudaStream_t s)
     const long long x = ctas < 0x40000000LL ? ctas : 0x40000000LL;
     const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>((ctas + x - 1) / x));
     auto join = a.shared ? (many ? join_kernel<BF16, false, 4> : join_kernel<BF16, false, 16>)
-                         : (many ? join_kernel<BF16, true, 4> : join_kernel<BF16, true, 16>);
+                         : (ctas > 2 * p.ctas ? join_kernel<BF16, true, 8> : join_kernel<BF16, true, 16>);
     return launch_dependent(join, grid, kJoinThreads, 0, s, a, p.g, rows, row_ctas, key_blocks, parts);
 }
 

@@ -24,8 +24,8 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelEach = 4;       // keys per thread and tile of the ordered pass
-constexpr int kHeld = 16;         // keys per thread kept in registers over the passes
 constexpr int kBins = 2048;
+constexpr int kCopies = 4;        // of the histogram: scores crowd a few bins
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 8;     // 16-byte pieces that a thread has in flight
 
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 {
     pdl_wait();
     pdl_trigger();
-    __shared__ int hist[kBins];
+    __shared__ int hist[kCopies][kBins];
     __shared__ int warp_sum[32];
     __shared__ int found[2];
     const unsigned unit = static_cast<unsigned>(unit_id());
@@ -102,29 +102,25 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     uint32_t known = 0, bits = 0;
     int left = places;
     if (places > 0) {
-        // the first 16384 keys stay in registers; the others are read again (L2)
-        uint32_t held[kHeld];
-#pragma unroll
-        for (int j = 0; j < kHeld; ++j) {
-            const int i = j * kSelThreads + tid;
-            held[j] = i < early ? score_key(w[i]) : 0u;
-        }
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             const int width = pass < 2 ? 11 : 10, shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+            for (int i = tid; i < kCopies * kBins; i += kSelThreads) hist[0][i] = 0;
             __syncthreads();
-            auto count = [&](uint32_t key) {
-                if ((key & bits) == known) atomicAdd(&hist[(key >> shift) & ((1u << width) - 1)], 1);
-            };
-#pragma unroll
-            for (int j = 0; j < kHeld; ++j)
-                if (j * kSelThreads + tid < early) count(held[j]);
-            for (int i = kHeld * kSelThreads + tid; i < early; i += kSelThreads) count(score_key(w[i]));
+            int* mine = hist[(tid >> 5) & (kCopies - 1)];
+            for (int i = tid; i < early; i += kSelThreads) {
+                const uint32_t key = score_key(w[i]);
+                if ((key & bits) == known) atomicAdd(&mine[(key >> shift) & ((1u << width) - 1)], 1);
+            }
             __syncthreads();
             // bins from the largest down, two per thread
             const int hi = kBins - 1 - 2 * tid;
-            const int c0 = hist[hi], c1 = hist[hi - 1];
+            int c0 = 0, c1 = 0;
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c) {
+                c0 += hist[c][hi];
+                c1 += hist[c][hi - 1];
+            }
             const int above = block_scan(c0 + c1, warp_sum).x;
             if (above < left && above + c0 + c1 >= left) {
                 const bool first = above + c0 >= left;
