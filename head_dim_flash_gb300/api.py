@@ -935,17 +935,26 @@ class _Rope(torch.autograd.Function):
     def forward(ctx, q, k, plan, cu, start, positions):
         ctx.save_for_backward(cu, start, positions)
         ctx.plan = plan
+        ctx.set_materialize_grads(False)
         if cu is None:
             return _rope_dense(q, k, plan, start, positions, 0)
         return _rope_packed(q, k, plan, cu, start, positions, 0)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dq, dk):
         cu, start, positions = ctx.saved_tensors
-        if cu is None:
-            dq, dk = _rope_dense(dq, dk, ctx.plan, start, positions, 1)
-        else:
-            dq, dk = _rope_packed(dq, dk, ctx.plan, cu, start, positions, 1)
+        # the gradients that there are, in one call
+        grads = [x for x, wanted in zip((dq, dk), ctx.needs_input_grad) if wanted and x is not None]
+        if grads:
+            pair = (grads[0], grads[1] if len(grads) > 1 else None)
+            if cu is None:
+                turned = _rope_dense(*pair, ctx.plan, start, positions, 1)
+            else:
+                turned = _rope_packed(*pair, ctx.plan, cu, start, positions, 1)
+            turned = iter(turned)
+            dq, dk = (next(turned) if wanted and x is not None else None
+                      for x, wanted in zip((dq, dk), ctx.needs_input_grad))
         return dq, dk, None, None, None, None
 
 

@@ -205,14 +205,14 @@ __device__ __forceinline__ bool find_move(const EvictArgs& a, Move& m)
     return true;
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictArgs a, const int rows)
+__global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictArgs a, const int most, const int rows)
 {
     pdl_wait();
     pdl_trigger();
     Move m;
     if (!find_move(a, m)) return;
     const int nv = a.D >> 3;  // 16-byte pieces of a row
-    const int r0 = blockIdx.x * rows, r1 = min(r0 + rows, a.keep);
+    const int r0 = blockIdx.x * rows, r1 = min(r0 + rows, most);
     const int total = (r1 - r0) * nv;
     for (int i0 = threadIdx.x; i0 < total; i0 += kMoveThreads * kMoveBatch) {
         uint4 x[kMoveBatch];
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictArg
 }
 
 // In place: columns [64 x, 64 x + 64) of the head dim (32 where D % 64 leaves them), tokens in order.
-__global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const EvictArgs a)
+__global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const EvictArgs a, const int most)
 {
     pdl_wait();
     pdl_trigger();
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const EvictAr
 #pragma unroll
         for (int j = 0; j < kMoveBatch; ++j) {
             const int r = r0 + j * (kMoveThreads / 8) + (threadIdx.x >> 3);
-            const int from = r < a.keep ? __ldg(m.kept + r) : -1;
+            const int from = r < most ? __ldg(m.kept + r) : -1;
             if (mine && from > r) {
                 v[j] = __ldcs(reinterpret_cast<const uint4*>(m.src + from * m.sn + col));
                 moves |= 1u << j;
@@ -261,10 +261,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const EvictAr
     };
     uint32_t moves;
     load(0, x, moves);
-    for (int r0 = 0; r0 < a.keep; r0 += kRows) {
+    for (int r0 = 0; r0 < most; r0 += kRows) {
         uint4 y[kMoveBatch];
         uint32_t next = 0;
-        if (r0 + kRows < a.keep) load(r0 + kRows, y, next);
+        if (r0 + kRows < most) load(r0 + kRows, y, next);
         __syncthreads();  // this batch has been read (the loads above wait only in the next round)
 #pragma unroll
         for (int j = 0; j < kMoveBatch; ++j) {
@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const EvictAr
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s)
 {
+    const int most = a.keep < a.N ? a.keep : a.N;  // tokens that a kv head can keep
     dim3 grid;
     const long long units = static_cast<long long>(a.B) * a.Hkv;
     if (!unit_grid(1, units, &grid)) return cudaErrorInvalidConfiguration;
@@ -287,14 +288,14 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     if (a.in_place) {
         if (!unit_grid((a.D + 63) / 64, 2 * units, &grid)) return cudaErrorInvalidConfiguration;
-        return launch_dependent(evict_shift_kernel, grid, kMoveThreads, 0, s, a);
+        return launch_dependent(evict_shift_kernel, grid, kMoveThreads, 0, s, a, most);
     }
     // pieces of 64 KiB, smaller where that leaves SMs idle
     int rows = 32768 / a.D;
     const long long sms = num_sms() > 0 ? num_sms() : 152;
-    while (rows > 4 && (a.keep + rows - 1) / rows * 2 * units < 4 * sms) rows >>= 1;
-    if (!unit_grid((a.keep + rows - 1) / rows, 2 * units, &grid)) return cudaErrorInvalidConfiguration;
-    return launch_dependent(evict_copy_kernel, grid, kMoveThreads, 0, s, a, rows);
+    while (rows > 4 && (most + rows - 1) / rows * 2 * units < 4 * sms) rows >>= 1;
+    if (!unit_grid(most > 0 ? (most + rows - 1) / rows : 1, 2 * units, &grid)) return cudaErrorInvalidConfiguration;
+    return launch_dependent(evict_copy_kernel, grid, kMoveThreads, 0, s, a, most, rows);
 }
 
 }  // namespace ffpa

@@ -213,6 +213,24 @@ def test_varlen_attention_takes_a_plan():
     assert torch.equal(s, t)
 
 
+def test_rope_gradient_of_one_input():
+    g = gen(7)
+    plan = ffpa.rope_plan(64)
+    q = randn(g, 2, 4, 9, 64, dtype=torch.bfloat16)
+    k = randn(g, 2, 2, 9, 64, dtype=torch.bfloat16).requires_grad_()
+    pos = torch.arange(9, device="cuda")
+    yq, yk = ffpa.rope(q, k, plan)
+    dy = randn(g, *yk.shape, dtype=torch.bfloat16)
+    (dk,) = torch.autograd.grad((yq, yk), (k,), (torch.ones_like(yq), dy), retain_graph=True)
+    check_turned(dk, dy, pos, thetas(64), False, sign=-1.0)
+    (dk,) = torch.autograd.grad(yk, (k,), dy)
+    check_turned(dk, dy, pos, thetas(64), False, sign=-1.0)
+    x = q.clone().requires_grad_()
+    (g1,) = torch.autograd.grad(ffpa.rope(x, None, plan)[0].float().pow(2).sum(), (x,), create_graph=True)
+    with pytest.raises(RuntimeError):  # not silently without its second derivative
+        g1.sum().backward()
+
+
 # ----------------------------------------------------------------- decode
 def reference(q, k, v, end, kp=None, vp=None):
     """Rows of one sequence in 64 bits: q [Hq, Nq, D], k, v [Hkv, n, D], end [Nq]: first key not seen.
@@ -551,6 +569,70 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for x, y in got:
         assert all(torch.equal(a, b) for a, b in zip(x, y))
+
+
+def test_caches_beyond_32_bits():
+    """The second sequence begins more than 2^31 elements behind the first."""
+    g = gen(34)
+    N, D, lens = 17_000_000, 128, (7, 300)
+    k, v = (torch.empty((2, 1, N, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert k.stride(0) > 2 ** 31
+    for b, n in enumerate(lens):
+        k[b, :, :n], v[b, :, :n] = randn(g, 1, n, D), randn(g, 1, n, D)
+        k[b, :, n:n + 64], v[b, :, n:n + 64] = math.nan, math.nan
+    q = randn(g, 2, 4, 1, D, dtype=torch.bfloat16)
+    w = torch.zeros((2, 1, N), device="cuda")
+    n = ints(*lens)
+    o, lse, _ = ffpa.decode_fwd_weights(q, k, v, w, n)
+    o2, lse2 = ffpa.decode_fwd_shared(q, k[1:, :, :50], v[1:, :, :50], k, v, n)
+    api.get_status()
+    for b, m in enumerate(lens):
+        ref = reference(q[b], k[b, :, :m], v[b, :, :m], row_ends(m, 1, False))
+        check_decode(o[b], lse[b], ref, f"sequence {b}")
+        within(w[b, :, :m], ref[2], (2 * ref[4] + 2.0 ** -18) * ref[2] + 2.0 ** -23, "weights")
+        ref = reference(q[b], k[b, :, :m], v[b, :, :m], row_ends(50 + m, 1, False), k[1, :, :50], v[1, :, :50])
+        check_decode(o2[b], lse2[b], ref, f"behind a prefix {b}")
+    assert float(w.sum()) == pytest.approx(8, abs=1e-4)
+    last, row = k[1, 0, 299].clone(), kept_rows(w[1, 0, :300].cpu().tolist(), 300, 100, 10)
+    before = k[1, 0, :300].clone()
+    *_, kept = ffpa.kv_evict(k, v, w, n, 100, 10)
+    api.get_status()
+    assert kept[1, 0].tolist() == row and n.tolist() == [7, 100]
+    assert torch.equal(k[1, 0, :100], before[row]) and torch.equal(k[1, 0, 99], last)
+    x = k[:, :, -5:]  # rows at the far end of the storage
+    x.copy_(randn(g, 2, 1, 5, D))
+    y, _ = ffpa.rope(x, None, ffpa.rope_plan(D), start=ints(3, 1 << 30))
+    check_turned(y, x, torch.tensor([[3], [1 << 30]], device="cuda")[:, None] + torch.arange(5, device="cuda"), thetas(D), False)
+
+
+def test_calls_follow_the_current_stream():
+    """On a side stream, behind work that makes their inputs there."""
+    g = gen(35)
+    plan = ffpa.rope_plan(128)
+    q, k, v = (randn(g, 4, h, 2000, 128, dtype=torch.bfloat16) for h in (8, 2, 2))
+    lens = ints(2000, 100, 0, 1999)
+    w = torch.rand((4, 2, 2000), generator=g, device="cuda")
+    s = torch.cuda.Stream()
+
+    def calls(q, k, v, w, lens):
+        rq, rk = ffpa.rope(q, k, plan)
+        o = ffpa.decode_fwd_weights(rq[:, :, :1], rk, v, w, lens, weights_out=torch.zeros_like(w))
+        p = ffpa.decode_fwd_shared(rq[:, :, :3], rk[:1], v[:1], rk, v, lens, causal=True)
+        e = ffpa.kv_evict(rk, v, o[2], lens, 64, 8, k_out=torch.zeros_like(k), v_out=torch.zeros_like(v),
+                          weights_out=torch.zeros_like(w))
+        return [rq, rk, *o, *p, *e]
+
+    want = calls(q, k, v, w, lens)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        late = [torch.zeros_like(x) for x in (q, k, v, w, lens)]
+        for _ in range(20):  # the inputs arrive late
+            for x, y in zip(late, (q, k, v, w, lens)):
+                x.copy_(y)
+        got = calls(*late)
+    s.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
 
 
 @pytest.mark.parametrize("bad", [-1, 51])
