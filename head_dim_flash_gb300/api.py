@@ -1069,8 +1069,11 @@ def decode_fwd_shared(q, k_prefix, v_prefix, k, v, lens=None, causal: bool = Fal
             return decode_fwd_shared(q, k_prefix, v_prefix, k, v, lens, causal, scale, out, lse, workspace)
     shape = B, Hq, Nq, D = q.shape
     Hkv, N, Np = k.shape[1], k.shape[2], k_prefix.shape[2]
-    (x, wq), (kp, wkp), (vp, wvp), (k, wk), (v, wv) = (
-        _in4(t, w) for t, w in zip((q, k_prefix, v_prefix, k, v), views))
+    x, wq = _in4(q, views[0])  # (x keeps a copy alive until the call is made)
+    k_prefix, wkp = _in4(k_prefix, views[1])
+    v_prefix, wvp = _in4(v_prefix, views[2])
+    k, wk = _in4(k, views[3])
+    v, wv = _in4(v, views[4])
     out, wo = _out4(q, out, like, "out")
     need = 0 if workspace is not None else _shared_workspace_bytes(index, dt, B, Hq, Hkv, Nq, Np, N, D)
     lse, workspace, n = _line_scratch(shape, dev, lse, workspace, need)
@@ -1106,7 +1109,9 @@ def decode_fwd_weights(q, k, v, weights, lens=None, causal: bool = False, scale:
         weights_out = weights
     pw = _weights_ptr(weights, (B, Hkv, N), "weights", dev)
     po = _weights_ptr(weights_out, (B, Hkv, N), "weights_out", dev)
-    (x, wq), (k, wk), (v, wv) = (_in4(t, w) for t, w in zip((q, k, v), views))
+    x, wq = _in4(q, views[0])  # (x keeps a copy alive until the call is made)
+    k, wk = _in4(k, views[1])
+    v, wv = _in4(v, views[2])
     out, wo = _out4(q, out, like, "out")
     need = 0 if workspace is not None else _weights_workspace_bytes(index, dt, B, Hq, Hkv, Nq, N, D)
     lse, workspace, n = _line_scratch(shape, dev, lse, workspace, need)

@@ -598,16 +598,22 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
         const int j = (u.tile * KT) + slot_i(sl) * 8 + cpair, end = of_row(jlim, sl);
         return make_float2(j < end ? x * pb.scale_log2 : -INFINITY, j + 1 < end ? y * pb.scale_log2 : -INFINITY);
     };
+    // A unit of up to eight rows leaves the matrix product's other eight idle: they
+    // take the rows again with what P's rounding left over, so that P counts 16 bits
+    // (bf16) or 22 and O's error is its own rounding's.
+    auto is_fine = [&](const Spot& u) { return MT == 1 && unit_rows(u) <= 8; };
     // P of a tile in shared memory, from the references as they are, and its sums added
     // to `add`; true where a score lies too far above its reference
     auto exponentials = [&](const Spot& u, float (&add)[MT][2], bool first_try) {
         bool over = false;
+        const bool fine = is_fine(u);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) add[mt][0] = add[mt][1] = 0.f;
 #pragma unroll(W ? kTurns : 1)
         for (int j0 = 0; j0 < kTurns; ++j0) {
             const int sl = wg + j0 * warps;
             if (!kEven && sl >= SLOTS) break;
+            if (fine && (sl & 1)) continue;
             const float2 x = slot_scores(sl, u);
             const int mt = slot_mt(sl), i = slot_i(sl), hi = sl & 1;
             if (SCORE && first_try) {
@@ -624,7 +630,13 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
                     add[m][0] += hi ? 0.f : p0 + p1;
                     add[m][1] += hi ? p0 + p1 : 0.f;
                 }
-            p_s[((mt * (NT / 2) + (i >> 1)) * 32 + lane) * 4 + (i & 1) * 2 + hi] = pack2<BF16>(p0, p1);
+            uint32_t* to = p_s + ((mt * (NT / 2) + (i >> 1)) * 32 + lane) * 4 + (i & 1) * 2 + hi;
+            const uint32_t packed = pack2<BF16>(p0, p1);
+            *to = packed;
+            if (fine) {
+                const float2 back = unpack2<BF16>(packed);
+                to[1] = pack2<BF16>(p0 - back.x, p1 - back.y);
+            }
         }
         return over;
     };
@@ -660,6 +672,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
                     m_run[mt][hi] = top;
                     l_run[mt][hi] *= alpha[hi];
                 }
+                if (is_fine(u)) alpha[1] = alpha[0];
 #pragma unroll
                 for (int cc = 0; cc < CC; ++cc)
 #pragma unroll
@@ -740,6 +753,7 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
             for (int hi = 0; hi < 2; ++hi) {
                 const int r = mt * 16 + hi * 8 + r_lo;
                 if (r >= rows) continue;
+                const bool fine = is_fine(u);
                 float l = 0.f;
                 for (int w = 0; w < warps; ++w) l += sums[w * ROWS + r];
                 const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -765,7 +779,13 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int col = (wg + 8 * cc) * 64 + i * 8 + cpair;
-                        const float v0 = o_acc[cc][i][mt][2 * hi] * inv, v1 = o_acc[cc][i][mt][2 * hi + 1] * inv;
+                        float v0 = o_acc[cc][i][mt][2 * hi], v1 = o_acc[cc][i][mt][2 * hi + 1];
+                        if (hi == 0 && fine) {
+                            v0 += o_acc[cc][i][mt][2];
+                            v1 += o_acc[cc][i][mt][3];
+                        }
+                        v0 *= inv;
+                        v1 *= inv;
                         if (out)
                             *reinterpret_cast<uint32_t*>(out + col) = pack2<BF16>(v0, v1);
                         else

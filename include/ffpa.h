@@ -348,7 +348,9 @@ FFPA_API ffpa_status ffpa_varlen_rope(ffpa_dtype dt, const void* q, const void* 
  *   workspace: device scratch of at least ffpa_decode_shared_workspace_bytes()
  *   bytes, 256-byte aligned, sized on the current device; one call at a time
  *   per workspace. The query returns 0 for sizes outside the operation.
- * P is rounded to the input type, sums and O up to its final rounding are fp32.
+ * P is rounded to the input type (with up to eight rows per kv head, Hq / Hkv * Nq,
+ * the rounding's remainder is kept, too, for the sequences' own keys, and for
+ * the prefix if the whole batch has as few); sums and O up to its final rounding are fp32.
  * A length below 0 or above N records FFPA_ERR_INVALID_VALUE in the device
  * status word (ffpa_get_status) and the outputs of the call are undefined.
  */
