@@ -72,6 +72,7 @@ line::LinePlan line_plan(const Problem& pb, bool shared, int Np)
     p.o_cut = take(2 * static_cast<size_t>(g.ranges) * g.rows * D);
     p.l_cut = take(2 * static_cast<size_t>(g.ranges) * g.rows);
     p.l_whole = take(rows_all);
+    p.before = take(static_cast<size_t>(pb.B) + 1);  // (as wide as a float)
     if (shared) {
         p.o_whole = take(rows_all * D);
         p.o_whole_p = take(g.rblocks_p ? rows_all * D : 0);
@@ -121,6 +122,7 @@ cudaError_t launch_line(const LineArgs& args, void* workspace, size_t workspace_
     g.l_whole = at(p.l_whole);
     g.o_whole_p = at(p.o_whole_p);
     g.l_whole_p = at(p.l_whole_p);
+    g.before = reinterpret_cast<int*>(ws + p.before);
     g.scores = at(p.scores);
     g.o_split = at(p.o_split);
     g.l_split = at(p.l_split);

@@ -69,6 +69,7 @@ struct LineGeo {
     float *o_cut, *l_cut;      // [2 * ranges][rows][D], [2 * ranges][rows]
     float *o_whole, *l_whole;  // [B * Hq * Nq][D] (shared), [B * Hq * Nq]: units inside one range
     float *o_whole_p, *l_whole_p;  // [Hkv * Rp][D], [Hkv * Rp]
+    int* before;         // [B + 1]: places of the line before each sequence's units; of the whole line
     float* scores;       // [B * Hq * Nq][pitch]
     int pitch;
     // many rows: the prefix is the tensor cores' (launch_xchg, split over the keys)
@@ -143,26 +144,44 @@ __device__ __forceinline__ int tiles_of(const LineGeo& g, int keys)
 // Places that a unit of so many tiles takes in the line: its start's, then a tile each.
 __device__ __forceinline__ int places_of(int tiles) { return tiles > 0 ? tiles + kUnitPlaces : 0; }
 
-// Places of the whole line (below 2^31), those before sequence `b`, and the units that have tiles (by whole warps).
-__device__ __forceinline__ void line_sums(const LineArgs& a, const LineGeo& g, const int* staged, int b, int& total,
-                                          int& before, int& units)
+// Places of the whole line (below 2^31), and the units that have tiles (by whole warps).
+__device__ __forceinline__ void line_sums(const LineArgs& a, const LineGeo& g, const int* staged, int& total, int& units)
 {
     const Problem& pb = a.f.pb;
-    int t = 0, p = 0, u = 0;
+    int t = 0, u = 0;
 #pragma unroll 4
     for (int i = threadIdx.x & 31; i < pb.B; i += 32) {
         const int n = places_of(tiles_of(g, staged ? staged[i] : clamp_len(a, i)));
         t += n;
         u += n > 0;
-        if (i < b) p += n;
     }
     t = __reduce_add_sync(0xffffffffu, t);
-    p = __reduce_add_sync(0xffffffffu, p);
     u = __reduce_add_sync(0xffffffffu, u);
-    const int per = pb.Hkv * g.rblocks, prefix = pb.Hkv * g.rblocks_p * places_of(g.tiles_p);
-    total = prefix + t * per;
-    before = prefix + p * per;
+    const int per = pb.Hkv * g.rblocks;
+    total = pb.Hkv * g.rblocks_p * places_of(g.tiles_p) + t * per;
     units = pb.Hkv * g.rblocks_p + u * per;
+}
+
+// What the joining kernel asks of the line (by a whole warp).
+__device__ __forceinline__ void store_befores(const LineArgs& a, const LineGeo& g, const int* staged)
+{
+    const Problem& pb = a.f.pb;
+    const int lane = threadIdx.x & 31, per = pb.Hkv * g.rblocks;
+    int run = 0;
+    const int prefix = pb.Hkv * g.rblocks_p * places_of(g.tiles_p);
+    for (int i0 = 0; i0 < pb.B; i0 += 32) {
+        const int i = i0 + lane;
+        const int n = i < pb.B ? places_of(tiles_of(g, staged ? staged[i] : clamp_len(a, i))) : 0;
+        int incl = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (i < pb.B) g.before[i] = prefix + (run + incl - n) * per;
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) g.before[pb.B] = prefix + run * per;
 }
 
 // The line cut into ranges, no more than it has places: the first `longer` hold
@@ -338,8 +357,8 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
         }
     __syncthreads();
     const Line line{a, g, a.lens && pb.B <= kLens ? s_len : nullptr};
-    int total, unused, units;
-    line_sums(a, g, line.lens, 0, total, unused, units);
+    int total, units;
+    line_sums(a, g, line.lens, total, units);
     const Cuts cuts(g, total);
     volatile int* abort_p = &sh.abort_flag;
     uint32_t* status = a.f.ctl.status;
@@ -407,6 +426,8 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
                 int dummy = 0;
                 if (!mbar_wait(&full[t % S], (t / S) & 1, &dummy, status, lim, LS_DRAIN, false)) break;
             }
+        __syncwarp();
+        if (blockIdx.x == 0) store_befores(a, g, line.lens);  // with nothing left to load
         return;
     }
     if constexpr (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
@@ -888,9 +909,8 @@ __global__ void __launch_bounds__(kJoinThreads, LOADS > 8 ? 2 : SCORE ? 4 : 3) j
     const int b = bh / pb.Hkv, hk = bh - b * pb.Hkv;
     const int len = clamp_len(a, b);
     if (!is_row && block * kWeighKeys >= len) return;
-    int total, before, units;
-    line_sums(a, g, nullptr, b, total, before, units);
-    const Cuts cuts(g, total);
+    const int before = g.before[b];
+    const Cuts cuts(g, g.before[pb.B]);
     const int tiles = tiles_of(g, len);
 
     if (is_row) {
@@ -1049,7 +1069,7 @@ struct LinePlan {
     LineGeo g;
     int ctas;
     int smem;
-    size_t o_cut, l_cut, o_whole, l_whole, o_whole_p, l_whole_p, scores, o_split, l_split, q_rows, total;  // byte offsets
+    size_t o_cut, l_cut, o_whole, l_whole, o_whole_p, l_whole_p, before, scores, o_split, l_split, q_rows, total;  // byte offsets
     Problem prefix;  // the prefix as one batch entry of Rp queries per kv head
 };
 
