@@ -40,6 +40,9 @@
 // or barrier forwarder (odd rank), warps 2..9 elementwise (two threads per
 // TMEM row) and epilogue, warp 10 ships the own Z tile to the other pairs.
 //
+// SPLIT (the forward alone): a batch's rows against a shared prefix, split over
+// the keys, as in the one-CTA form (csrc/xchg.cu).
+//
 // Every per-step barrier is indexed by buffer and every waiter observes each
 // of its phases in order, at most one phase away from the barrier's state,
 // so that the parity waits are exact.
