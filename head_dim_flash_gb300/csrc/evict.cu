@@ -8,9 +8,13 @@
 // known, find the smallest key that stays and how many that equal it do. A last
 // pass in index order writes where each kept token was, and its score. The keys
 // are a 512th of the cache's bytes at D = 512 and are read from L2 after the
-// first pass; what bounds the kernel is the latency of its passes.
+// first pass; what bounds the kernel is the latency of its passes: 16384 tokens
+// 19 us, 900 tokens 8. (The keys in registers over the passes: 22; one addition per
+// bin and warp, by matching lanes: 31.)
 //
-// The second moves the rows, each read and written once: bound by memory. Out of
+// The second moves the rows, each read and written once: bound by memory (64 kv
+// heads cut from 16384 to 8192 tokens, D = 512, 2.1 GB: 312 us, 6.7 TB/s, a copy's
+// rate). Out of
 // place its CTAs take pieces of the kept tokens. In place a row moves to where
 // an earlier one was: a CTA owns 64 head dims of one tensor's kv head and takes
 // all its tokens in order, a batch read whole before it is written. A batch's

@@ -13,6 +13,12 @@
 // once into shared memory, while the first values are on their way, and serve
 // every head. A thread owns 16 head dims of a row, two 16-byte accesses: 8
 // pairs, or a piece of the head dims behind `rot`, which are copied.
+//
+// Measured on a GB300 against a copy of the same tensors (us): 8192 tokens of 40
+// heads of D = 512 108 against 100, 16000 of 20 of D = 320 with interleaved pairs on 128
+// dims 64 against 63, 32768 of 40 of D = 128 100 against 100; 32 tokens 2.8, a
+// launch. Four CTAs per SM instead of three (64 registers, streaming loads and
+// stores): no difference.
 #include "cache_ops.h"
 #include "kv4.cuh"
 
