@@ -24,13 +24,13 @@
 //
 // A tile is a chain of waits (data, sum, P), about 400 instructions a warp at six
 // cycles each. A tile of 32 keys at D = 512 takes as long to arrive (64 KiB at the
-// SM's share of HBM: 1.4 us). Head dims that divide into two groups of warps run
-// two (D <= 256); the others run fifteen warps in groups of their chunks over
-// tiles of 16 keys (D = 320, 500 MB, 16 rows: 102 us against 105 with one number of
-// warps for all, 131 with one group of five). Sixteen compute warps and a
-// producer do not fit: registers come in fours of warps. Issuing the loads from a
-// compute warp instead of a producer costs the chain 300 cycles a tile (D = 512,
-// 8 x 16384 tokens: 345 us against 326).
+// SM's share of HBM: 1.4 us). Head dims that divide into two groups of four warps
+// run two (D = 256); the others run fifteen warps in groups of their chunks over
+// tiles of 16 keys (16 ragged sequences at D = 320, 16 rows: 87 us against 102 with
+// one group of five). Sixteen compute warps and a producer do not fit: the register
+// file is dealt out to warps by fours. Two groups of eight at D = 512 whose own
+// warps issued the loads took 343 us for 8 x 16384 tokens, one group and a producer
+// 326.
 //
 // Measured on a GB300 (bf16, this kernel alone): 8 sequences of 16384 tokens, 8 kv
 // heads of D = 512, 4 rows, 2.15 GB: 317 us, 6.8 TB/s with the scores' 17 MB; 16
