@@ -14,12 +14,11 @@
 //
 // The second moves the rows, each read and written once: bound by memory (64 kv
 // heads cut from 16384 to 8192 tokens, D = 512, 2.1 GB: 312 us, 6.7 TB/s, a copy's
-// rate). Out of
-// place its CTAs take pieces of the kept tokens. In place a row moves to where
-// an earlier one was: a CTA owns 64 head dims of one tensor's kv head and takes
-// all its tokens in order, a batch read whole before it is written. A batch's
-// targets lie at or below its own first source and below every later one's, so
-// the next batch may already be on its way.
+// rate). Out of place its CTAs take pieces of the kept tokens. In place a row moves
+// to where an earlier one was: a CTA owns 64 to 256 head dims of one tensor's kv
+// head and takes all its tokens in order, a batch read whole before it is written.
+// A batch's targets lie at or below its own first source and below every later
+// one's, so the next batch may already be on its way.
 #include "cache_ops.h"
 #include "kv4.cuh"
 
@@ -239,23 +238,24 @@ __global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictArg
     }
 }
 
-// In place: columns [64 x, 64 x + 64) of the head dim (32 where D % 64 leaves them), tokens in order.
-__global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const EvictArgs a, const int most)
+// In place: COLS head dims (as many as D leaves), tokens in order.
+template <int THREADS, int COLS>
+__global__ void __launch_bounds__(THREADS) evict_shift_kernel(const EvictArgs a, const int most)
 {
     pdl_wait();
     pdl_trigger();
     Move m;
     if (!find_move(a, m)) return;
-    const int col = blockIdx.x * 64 + (threadIdx.x & 7) * 8;
-    constexpr int kRows = kMoveThreads / 8 * kMoveBatch;
+    const int col = blockIdx.x * COLS + threadIdx.x % (COLS / 8) * 8;
+    constexpr int kStep = THREADS / (COLS / 8), kRows = kStep * kMoveBatch;
     const bool mine = col < a.D;
     uint4 x[kMoveBatch];
-    // row r0 + 32 j + tid / 8 of a batch: a token that stays where it is does not move
+    // my rows of a batch; a token that stays where it is does not move
     auto load = [&](int r0, uint4 (&v)[kMoveBatch], uint32_t& moves) {
         moves = 0;
 #pragma unroll
         for (int j = 0; j < kMoveBatch; ++j) {
-            const int r = r0 + j * (kMoveThreads / 8) + (threadIdx.x >> 3);
+            const int r = r0 + j * kStep + threadIdx.x / (COLS / 8);
             const int from = r < most ? __ldg(m.kept + r) : -1;
             if (mine && from > r) {
                 v[j] = __ldcs(reinterpret_cast<const uint4*>(m.src + from * m.sn + col));
@@ -263,20 +263,24 @@ __global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const EvictAr
             }
         }
     };
-    uint32_t moves;
-    load(0, x, moves);
-    for (int r0 = 0; r0 < most; r0 += kRows) {
-        uint4 y[kMoveBatch];
-        uint32_t next = 0;
-        if (r0 + kRows < most) load(r0 + kRows, y, next);
-        __syncthreads();  // this batch has been read (the loads above wait only in the next round)
+    auto store = [&](int r0, const uint4 (&v)[kMoveBatch], uint32_t moves) {
 #pragma unroll
         for (int j = 0; j < kMoveBatch; ++j) {
-            const int r = r0 + j * (kMoveThreads / 8) + (threadIdx.x >> 3);
-            if (moves >> j & 1) __stcs(reinterpret_cast<uint4*>(m.dst + r * m.on + col), x[j]);
-            x[j] = y[j];
+            const int r = r0 + j * kStep + threadIdx.x / (COLS / 8);
+            if (moves >> j & 1) __stcs(reinterpret_cast<uint4*>(m.dst + r * m.on + col), v[j]);
         }
-        moves = next;
+    };
+    // two batches in turn: a copy of one to the other would wait for its loads
+    uint4 y[kMoveBatch];
+    uint32_t mx, my;
+    load(0, x, mx);
+    for (int r0 = 0; r0 < most; r0 += 2 * kRows) {
+        load(r0 + kRows, y, my);  // (nothing past the last row)
+        __syncthreads();          // the first batch has been read
+        store(r0, x, mx);
+        load(r0 + 2 * kRows, x, mx);
+        __syncthreads();
+        store(r0 + kRows, y, my);
     }
 }
 
@@ -291,8 +295,20 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s)
     cudaError_t e = launch_dependent(evict_select_kernel, grid, kSelThreads, 0, s, a);
     if (e != cudaSuccess) return e;
     if (a.in_place) {
-        if (!unit_grid((a.D + 63) / 64, 2 * units, &grid)) return cudaErrorInvalidConfiguration;
-        return launch_dependent(evict_shift_kernel, grid, kMoveThreads, 0, s, a, most);
+        // As wide as leaves a CTA for most places on the SMs, two each (64 kv heads of 16384 tokens, D = 512: 256
+        // head dims 477 us, 128 512, 64 628); what a narrow CTA has in flight is what its threads hold: 512 of them
+        // where CTAs are few (8 kv heads of 131072: 756 us, 256 threads 1200).
+        const long long sms = num_sms() > 0 ? num_sms() : 152;
+        auto fits = [&](int c) { return a.D >= c && 2 * units * ((a.D + c - 1) / c) >= 3 * sms / 2; };
+        const int cols = fits(256) ? 256 : fits(128) ? 128 : 64;
+        const long long ctas = (a.D + cols - 1) / cols;
+        if (!unit_grid(static_cast<unsigned>(ctas), 2 * units, &grid)) return cudaErrorInvalidConfiguration;
+        const bool few = 2 * units * ctas <= sms;
+        auto kern = cols == 256   ? evict_shift_kernel<kMoveThreads, 256>
+                    : cols == 128 ? evict_shift_kernel<kMoveThreads, 128>
+                    : few         ? evict_shift_kernel<2 * kMoveThreads, 64>
+                                  : evict_shift_kernel<kMoveThreads, 64>;
+        return launch_dependent(kern, grid, few ? 2 * kMoveThreads : kMoveThreads, 0, s, a, most);
     }
     // pieces of 64 KiB, smaller where that leaves SMs idle
     int rows = 32768 / a.D;
