@@ -287,6 +287,8 @@ WEIGH = [  # Hkv, G, Nq, D, N, lens
     (1, 7, 3, 832, 333, (333, 64, 2)),
     (2, 2, 1, 1024, 97, (97, 96)),
     (4, 2, 1, 64, 5000, (5000, 4999)),
+    (2, 3, 3, 384, 700, (700, 13, 350)),
+    (2, 8, 3, 64, 400, (400, 399)),
 ]
 
 
@@ -410,7 +412,10 @@ EVICT = [  # Hkv, N, D, lens, keep, recent
     (1, 1, 64, (1,), 1, 0), (2, 40, 64, (40, 0, 39, 20), 20, 0), (1, 300, 320, (300, 299, 128), 128, 128),
     (3, 513, 96, (513, 1, 512), 511, 7), (2, 5000, 512, (5000, 4096, 2049), 2048, 100),
     (1, 9000, 64, (9000, 8999), 8998, 0), (2, 130, 1024, (130, 77), 1, 0), (2, 130, 1024, (130, 77), 1, 1),
-    (1, 20000, 128, (20000,), 333, 32), (2, 50, 128, (50, 3), 64, 10)]
+    (1, 20000, 128, (20000,), 333, 32), (2, 50, 128, (50, 3), 64, 10),
+    # many kv heads: in place, CTAs of 128 and of 256 head dims
+    (8, 700, 160, tuple(700 - 41 * i for i in range(16)), 300, 20),
+    (8, 700, 320, tuple(700 - 41 * i for i in range(16)), 300, 20)]
 
 
 @pytest.mark.parametrize("kind", ["plain", "ties", "equal", "odd"])
