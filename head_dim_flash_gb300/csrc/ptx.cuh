@@ -369,6 +369,9 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool a
            ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Its bit that turns the signs of A (kind::f16, kind::f8f6f4).
+constexpr uint32_t kIdescNegateA = 1u << 13;
+
 // D(tmem) (+)= A(smem desc) x B(smem desc); issued by a single thread.
 __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate)

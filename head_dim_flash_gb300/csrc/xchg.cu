@@ -381,7 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer
         if (elect_one()) {
-            const uint32_t idesc_s = idesc_f16(128, 128, BF16, false, false);
+            const uint32_t idesc_s =
+                idesc_f16(128, 128, BF16, false, false) | (OP == XOP_FWD && a.turn_q ? kIdescNegateA : 0u);
             const uint32_t idesc_v = idesc_f16(128, sw, BF16, false, true);
             RingPos rp;
             bool ok = true;
@@ -1011,9 +1012,14 @@ cudaError_t dispatch(const XArgs& a, const CUtensorMap* maps, const Geo& gm, int
 
 }  // namespace
 
-cudaError_t launch_single(int op, const XArgs& a, cudaStream_t s)
+cudaError_t launch_single(int op, const XArgs& args, cudaStream_t s)
 {
+    XArgs a = args;
     const Problem& pb = a.pb;
+    if (op == XOP_FWD && pb.scale_log2 < 0.f) {
+        a.turn_q = 1;
+        a.pb.scale_log2 = -a.pb.scale_log2;
+    }
     const bool q_empty = q_side_empty(pb), kv_empty = kv_side_empty(pb);
     const bool rows_q = (op == XOP_FWD || op == XOP_DQ);
     if (rows_q ? q_empty : kv_empty) return cudaSuccess;  // no output rows

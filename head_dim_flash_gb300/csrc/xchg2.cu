@@ -444,7 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------- MMA issuer (pair)
             if (elect_one()) {
                 // (F8: format code 0 = e4m3 in both operand fields; V^T is K-major)
-                const uint32_t idesc_s = idesc_f16(256, 128, F8 ? false : BF16, false, false);
+                const uint32_t idesc_s =
+                    idesc_f16(256, 128, F8 ? false : BF16, false, false) | (OP == XOP_FWD && a.turn_q ? kIdescNegateA : 0u);
                 const uint32_t idesc_v = idesc_f16(256, sw, F8 ? false : BF16, false, !F8);
                 auto mma = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
                     if constexpr (F8)
@@ -1281,9 +1282,14 @@ cudaError_t dispatch(const XArgs& a, const CUtensorMap* maps, const PGeo& gm, in
 
 }  // namespace
 
-cudaError_t launch_pair(int op, const XArgs& a, cudaStream_t s)
+cudaError_t launch_pair(int op, const XArgs& args, cudaStream_t s)
 {
+    XArgs a = args;
     const Problem& pb = a.pb;
+    if (op == XOP_FWD && pb.scale_log2 < 0.f) {
+        a.turn_q = 1;
+        a.pb.scale_log2 = -a.pb.scale_log2;
+    }
     const bool q_empty = q_side_empty(pb), kv_empty = kv_side_empty(pb);
     const bool rows_q = (op == XOP_FWD || op == XOP_DQ);
     if (rows_q ? q_empty : kv_empty) return cudaSuccess;  // no output rows

@@ -1,0 +1,94 @@
+"""The cache operators at their edges: the prefix on the tensor cores in each of its forms, scales below zero, rows that
+are not numbers, packed batches with rows of no sequence, forward-mode differentiation, narrow eviction in place.
+References and tolerances are those of test_gpu_cache_ops."""
+import math
+
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+import head_dim_flash_gb300 as ffpa
+from head_dim_flash_gb300 import api
+from tests.test_gpu_cache_ops import DT, caches, check_decode, gen, ints, kept_rows, randn, reference, row_ends, within
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------- scales below zero
+# softmax(-s q k) is softmax(s (-q) k); products, sums and roundings are the same but for their signs
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B,H,G,Nq,D,Np,N,lens", [
+    (3, 1, 2, 2, 320, 700, 9, (9, 0, 1)), (30, 2, 2, 3, 128, 1665, 9, (0, 1, 2, 3, 9) * 6),
+    (20, 2, 4, 4, 320, 1025, 6, (0, 1, 2, 3, 4) * 4), (8, 4, 4, 4, 512, 1281, 5, (0, 1, 2, 3, 5, 4, 0, 1)),
+    (11, 2, 4, 3, 512, 2177, 4, (0, 1, 2, 4, 3, 0, 1, 2, 4, 3, 0)), (12, 2, 4, 3, 1024, 2177, 4, (0, 1, 2, 4) * 3)])
+def test_shared_with_a_negative_scale(dt, causal, B, H, G, Nq, D, Np, N, lens):
+    g = gen(41)
+    q = randn(g, B, H * G, Nq, D, dtype=DT[dt]) * 3  # scores far from each other
+    k, v = caches(g, B, H, N, D, DT[dt], lens)
+    kp, vp = (randn(g, 1, H, Np, D, dtype=DT[dt]) for _ in range(2))
+    s = 1 / math.sqrt(D)
+    o, lse = ffpa.decode_fwd_shared(q, kp, vp, k, v, ints(*lens), causal=causal, scale=-s)
+    api.get_status()
+    for b, n in enumerate(lens):
+        ref = reference(-q[b], k[b, :, :n], v[b, :, :n], row_ends(Np + n, Nq, causal), kp[0], vp[0])
+        check_decode(o[b], lse[b], ref, f"sequence {b}")
+    o2, lse2 = ffpa.decode_fwd_shared(-q, kp, vp, k, v, ints(*lens), causal=causal, scale=s)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_weights_with_a_negative_scale(dt):
+    g = gen(42)
+    lens = (2001, 16, 0, 1000)
+    q = randn(g, 4, 8, 2, 320, dtype=DT[dt])
+    k, v = caches(g, 4, 2, 2001, 320, DT[dt], lens)
+    w = [torch.zeros((4, 2, 2001), device="cuda") for _ in range(2)]
+    a = ffpa.decode_fwd_weights(q, k, v, w[0], ints(*lens), causal=True, scale=-0.07)
+    b = ffpa.decode_fwd_weights(-q, k, v, w[1], ints(*lens), causal=True, scale=0.07)
+    api.get_status()
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and float(w[0].sum()) == pytest.approx(3 * 16, abs=1e-3)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B,H,G,Nq,Nkv,D", [
+    (1, 2, 2, 300, 300, 64), (1, 2, 1, 130, 257, 320), (1, 1, 2, 200, 70, 512), (2, 1, 1, 257, 390, 640),
+    (1, 1, 1, 140, 129, 992), (1, 2, 1, 260, 700, 1024), (2, 2, 4, 3, 500, 512)])
+def test_attention_with_a_negative_scale(dt, causal, B, H, G, Nq, Nkv, D):
+    g = gen(43)
+    q = (randn(g, B, H * G, Nq, D, dtype=DT[dt]) * 3).requires_grad_()
+    k, v = (randn(g, B, H, Nkv, D, dtype=DT[dt]).requires_grad_() for _ in range(2))
+    do = randn(g, *q.shape, dtype=DT[dt])
+    s = 1 / math.sqrt(D)
+    out = []
+    for x, scale in ((q, -s), (-q, s)):
+        o, lse = ffpa.attention(x, k, v, causal=causal, scale=scale, return_lse=True)
+        out.append((o, lse, *torch.autograd.grad(o, (q, k, v), do)))
+    api.get_status()
+    for b in range(B):
+        ref = reference(-q[b], k[b], v[b], row_ends(Nkv, Nq, causal))
+        check_decode(out[0][0][b], out[0][1][b], ref, f"entry {b}")
+    for x, y, what in zip(*out, ("o", "lse", "dq", "dk", "dv")):
+        assert torch.equal(x, y), what
+
+
+def test_varlen_attention_with_a_negative_scale():
+    g = gen(44)
+    cu = ints(0, 10, 300, 700)
+    q = randn(g, 700, 4, 320, dtype=torch.float16) * 3
+    k, v = (randn(g, 700, 2, 320, dtype=torch.float16) for _ in range(2))
+    a = ffpa.varlen_attention(q, k, v, cu, causal=True, scale=-0.05, return_lse=True)
+    b = ffpa.varlen_attention(-q, k, v, cu, causal=True, scale=0.05, return_lse=True)
+    api.get_status()
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and bool(torch.isfinite(a[1]).all())
+
+
+@pytest.mark.parametrize("D", [128, 512])
+def test_fp8_with_a_negative_scale(D):
+    g = gen(45)
+    q = randn(g, 1, 2, 300, D, dtype=torch.bfloat16) * 3
+    k, v = (randn(g, 1, 2, 390, D, dtype=torch.bfloat16) for _ in range(2))
+    a, b = (ffpa.fwd_fp8(x, k, v, False, s)[:2] for x, s in ((q, -0.05), (-q, 0.05)))
+    api.get_status()
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and bool(torch.isfinite(a[1]).all())
