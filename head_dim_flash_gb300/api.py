@@ -907,14 +907,14 @@ def _rope_packed(q, k, plan, cu, start, positions, inverse, q_out=None, k_out=No
     B = cu.numel() - 1
     ps, pp = _rope_positions(start, positions, B, (T,), dev)
     Hk, pk, pok = 0, None, None
+    # rows of no sequence become zero in new outputs and stay as they are in given ones
+    zero = q_out is None and (k is None or k_out is None)
     outs = []
     for x, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
         if x is None:
             continue
         if out is None:
-            # rows of no sequence are not written
-            new = torch.zeros if inverse else torch.empty
-            out = new(x.shape, dtype=x.dtype, device=dev)
+            out = (torch.empty if zero else torch.zeros)(x.shape, dtype=x.dtype, device=dev)
         elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
             raise ValueError(f"{name} must be contiguous, with its input's shape, dtype and device")
         outs.append(out)
@@ -923,8 +923,8 @@ def _rope_packed(q, k, plan, cu, start, positions, inverse, q_out=None, k_out=No
         Hk, k = k.shape[1], _in_packed(k)
         pk, pok = k.data_ptr(), outs[1].data_ptr()
     st = _ffi.load().ffpa_varlen_rope(dt, q.data_ptr(), pk, outs[0].data_ptr(), pok, plan._c,
-                                      _lengths(cu, B + 1, "cu_seqlens", dev), ps, pp, B, T, Hq, Hk, D, inverse,
-                                      _raw_stream(dev))
+                                      _lengths(cu, B + 1, "cu_seqlens", dev), ps, pp, B, T, Hq, Hk, D,
+                                      inverse | 2 * zero, _raw_stream(dev))
     if st:
         _ffi.raise_for(st, "ffpa_varlen_rope")
     return outs[0], outs[1] if k is not None else None
@@ -980,7 +980,7 @@ _rope_apply = rope  # attention() has a parameter of that name
 def varlen_rope(q, k, plan: RopePlan, cu_seqlens, start=None, positions=None, q_out=None, k_out=None):
     """As rope, for a packed batch: q [T, Hq, D], k [T, Hkv, D] (or None), sequence b's tokens the
     rows [cu_seqlens[b], cu_seqlens[b + 1]) (int32 on the device); positions: int32 [T]. Rows of no
-    sequence are not written; their gradient is zero."""
+    sequence stay as they are in q_out and k_out and are zero in new outputs; their gradient is zero."""
     if _needs_grad(q, k):
         if q_out is not None or k_out is not None:
             raise ValueError("q_out and k_out are for inputs that need no gradient")

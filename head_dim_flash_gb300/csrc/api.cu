@@ -774,7 +774,8 @@ namespace {
 
 ffpa_status run_rope(ffpa_dtype dt, const ffpa_view& q, const ffpa_view& k, const ffpa_view& q_out,
                      const ffpa_view& k_out, const ffpa_rope_plan& plan, const int* start, const int* positions,
-                     const int* cu, int B, int total, int Hq, int Hkv, int N, int D, int inverse, ffpa_stream_t stream)
+                     const int* cu, int B, int total, int Hq, int Hkv, int N, int D, int inverse, int zero_rest,
+                     ffpa_stream_t stream)
 {
     FFPA_TRY(check_common(dt, 0, 0, D, 1.f));
     if (B < 0 || N < 0 || total < 0 || Hq < 0 || Hkv < 0)
@@ -786,7 +787,7 @@ ffpa_status run_rope(ffpa_dtype dt, const ffpa_view& q, const ffpa_view& k, cons
         return fail(FFPA_ERR_NOT_SUPPORTED, "Hq + Hkv = %lld heads exceed %d", static_cast<long long>(Hq) + Hkv, INT_MAX / 64);
     const long long tokens = cu ? total : static_cast<long long>(B) * N;
     if (tokens > INT_MAX) return fail(FFPA_ERR_NOT_SUPPORTED, "%lld tokens exceed 2^31 - 1", tokens);
-    const bool any = tokens > 0 && B > 0 && Hq + Hkv > 0;
+    const bool any = tokens > 0 && (B > 0 || zero_rest) && Hq + Hkv > 0;
     if (any && !plan.turns) return fail(FFPA_ERR_INVALID_VALUE, "the plan's turns are NULL");
     if (reinterpret_cast<uintptr_t>(plan.turns) & 7u) return fail(FFPA_ERR_INVALID_VALUE, "turns must be 8-byte aligned");
     if ((reinterpret_cast<uintptr_t>(start) & 3u) || (reinterpret_cast<uintptr_t>(positions) & 3u) ||
@@ -816,6 +817,7 @@ ffpa_status run_rope(ffpa_dtype dt, const ffpa_view& q, const ffpa_view& k, cons
     a.interleaved = plan.interleaved != 0;
     a.mscale = plan.mscale;
     a.sign = inverse ? -1.f : 1.f;
+    a.zero_rest = zero_rest;
     a.start = start;
     a.pos = positions;
     a.cu = cu;
@@ -896,18 +898,20 @@ ffpa_status ffpa_rope(ffpa_dtype dt, ffpa_view q, ffpa_view k, ffpa_view q_out, 
                       const int* start, const int* positions, int B, int Hq, int Hkv, int N, int D, int inverse,
                       ffpa_stream_t stream)
 {
-    return run_rope(dt, q, k, q_out, k_out, plan, start, positions, nullptr, B, 0, Hq, Hkv, N, D, inverse, stream);
+    return run_rope(dt, q, k, q_out, k_out, plan, start, positions, nullptr, B, 0, Hq, Hkv, N, D, inverse, 0, stream);
 }
 
 ffpa_status ffpa_varlen_rope(ffpa_dtype dt, const void* q, const void* k, void* q_out, void* k_out,
                              ffpa_rope_plan plan, const int* cu_seqlens, const int* start, const int* positions,
-                             int batch, int total, int Hq, int Hkv, int D, int inverse, ffpa_stream_t stream)
+                             int batch, int total, int Hq, int Hkv, int D, int flags, ffpa_stream_t stream)
 {
     if (!cu_seqlens) return fail(FFPA_ERR_INVALID_VALUE, "cu_seqlens is NULL");
+    if (flags & ~(FFPA_ROPE_INVERSE | FFPA_ROPE_ZERO_REST))
+        return fail(FFPA_ERR_INVALID_VALUE, "flags=%d: FFPA_ROPE_INVERSE and FFPA_ROPE_ZERO_REST are known", flags);
     const int hq = Hq > 0 ? Hq : 1, hk = Hkv > 0 ? Hkv : 1;
     return run_rope(dt, packed_rows(const_cast<void*>(q), hq, D), packed_rows(const_cast<void*>(k), hk, D),
                     packed_rows(q_out, hq, D), packed_rows(k_out, hk, D), plan, start, positions, cu_seqlens, batch,
-                    total, Hq, Hkv, total, D, inverse, stream);
+                    total, Hq, Hkv, total, D, flags & FFPA_ROPE_INVERSE, flags & FFPA_ROPE_ZERO_REST, stream);
 }
 
 size_t ffpa_decode_shared_workspace_bytes(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int Np, int N, int D)

@@ -19,6 +19,7 @@ struct RopeArgs {
     const unsigned long long* turns;  // device [rot / 2]: turns per position, in units of 2^-64
     int rot, interleaved;
     float mscale, sign;           // sign: -1 turns back (the gradient)
+    int zero_rest;                // packed: rows of no sequence become zero, instead of staying as they are
     const int* start;             // device [B]: position of each sequence's first token (null: 0)
     const int* pos;               // device [B, N] / [total]: every position, or null
     const int* cu;                // device [B + 1]: packed token offsets, or null

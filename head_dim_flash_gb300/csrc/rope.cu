@@ -83,6 +83,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a)
                 if (a.cu[e] <= t) b = max(b, e);
 #pragma unroll
             for (int d = 8; d; d >>= 1) b = max(b, __shfl_xor_sync(0xffffu << (tid & 16), b, d));
+            if (a.zero_rest && (b < 0 || b >= a.B))  // here, where it costs the other rows nothing
+                for (int e = tid & 15; e < heads * (a.D >> 3); e += 16) {
+                    const int h = h0 + e / (a.D >> 3);
+                    uint16_t* row = h < a.Hq ? static_cast<uint16_t*>(a.oq) + t * a.voq.sn + h * a.voq.sh
+                                             : static_cast<uint16_t*>(a.ok) + t * a.vok.sn + (h - a.Hq) * a.vok.sh;
+                    reinterpret_cast<uint4*>(row)[e % (a.D >> 3)] = make_uint4(0u, 0u, 0u, 0u);
+                }
             if ((tid & 15) == 0) {
                 RopeToken k{};
                 k.there = b >= 0 && b < a.B;

@@ -329,10 +329,13 @@ FFPA_API ffpa_status ffpa_rope(ffpa_dtype dt, ffpa_view q, ffpa_view k, ffpa_vie
                                int N, int D, int inverse, ffpa_stream_t stream);
 /* The same for a packed batch: [total, H, D] contiguous, sequence b's tokens the
  * rows [cu_seqlens[b], cu_seqlens[b + 1]) (device int32 [batch + 1], nondecreasing);
- * positions: device int32 [total]. Rows of no sequence are left as they are. */
+ * positions: device int32 [total]. Rows of no sequence are left as they are, or
+ * become zero with FFPA_ROPE_ZERO_REST (attention reads whole tiles past a
+ * sequence's end: what lies there has to be finite). */
+enum { FFPA_ROPE_INVERSE = 1, FFPA_ROPE_ZERO_REST = 2 };
 FFPA_API ffpa_status ffpa_varlen_rope(ffpa_dtype dt, const void* q, const void* k, void* q_out, void* k_out,
                                       ffpa_rope_plan plan, const int* cu_seqlens, const int* start,
-                                      const int* positions, int batch, int total, int Hq, int Hkv, int D, int inverse,
+                                      const int* positions, int batch, int total, int Hq, int Hkv, int D, int flags,
                                       ffpa_stream_t stream);
 
 /*

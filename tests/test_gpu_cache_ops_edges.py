@@ -92,3 +92,58 @@ def test_fp8_with_a_negative_scale(D):
     a, b = (ffpa.fwd_fp8(x, k, v, False, s)[:2] for x, s in ((q, -0.05), (-q, 0.05)))
     api.get_status()
     assert all(torch.equal(x, y) for x, y in zip(a, b)) and bool(torch.isfinite(a[1]).all())
+
+
+# ----------------------------------------------------------------- rotary positions
+def left_behind(shape, dtype):
+    """The allocator's next block of this size holds NaN."""
+    for _ in range(4):
+        torch.full(shape, math.nan, dtype=dtype, device="cuda")
+
+
+@pytest.mark.parametrize("rot", [64, 128])
+def test_new_packed_outputs_have_no_rows_left_as_they_were(rot):
+    g = gen(48)
+    plan = ffpa.rope_plan(rot)
+    T, D = 900, 128
+    q, k = randn(g, T, 4, D, dtype=torch.bfloat16), randn(g, T, 2, D, dtype=torch.bfloat16)
+    for cu, there in ((ints(0, 300, 700), range(0, 700)), (ints(100, 300), range(100, 300)), (ints(0), range(0, 0)),
+                      (ints(0, 0, 0), range(0, 0))):
+        left_behind(q.shape, q.dtype)
+        left_behind(k.shape, k.dtype)
+        yq, yk = ffpa.varlen_rope(q, k, plan, cu)
+        api.get_status()
+        rows = torch.zeros(T, dtype=torch.bool, device="cuda")
+        rows[there.start:there.stop] = True
+        for x, y in ((q, yq), (k, yk)):
+            assert bool((y[~rows] == 0).all()) and not bool(torch.isnan(y).any())
+            given = torch.full_like(x, 3.0)
+            r, _ = ffpa.varlen_rope(x, None, plan, cu, q_out=given)
+            assert torch.equal(r[rows], y[rows]) and bool((r[~rows] == 3).all())
+    # the gradient, too
+    x = q.clone().requires_grad_()
+    y, _ = ffpa.varlen_rope(x, None, plan, ints(0, 300, 700))
+    left_behind(q.shape, q.dtype)
+    (dx,) = torch.autograd.grad(y, x, torch.ones_like(y))
+    assert bool((dx[700:] == 0).all()) and not bool(torch.isnan(dx).any())
+
+
+@pytest.mark.parametrize("D", [64, 320, 512])
+def test_packed_attention_with_a_plan_and_padding(D):
+    """Rows behind the last sequence reach none of its results or gradients."""
+    g = gen(49)
+    plan = ffpa.rope_plan(64)
+    T, pad = 437, 90
+    cu = ints(0, 130, T)
+    q, k, v = (randn(g, T + pad, h, D, dtype=torch.bfloat16) for h in (4, 2, 2))
+    do = randn(g, T + pad, 4, D, dtype=torch.bfloat16)
+    out = []
+    for n in (T, T + pad):
+        x = [t[:n].clone().requires_grad_() for t in (q, k, v)]
+        for t in x:
+            left_behind(t.shape, t.dtype)
+        o = ffpa.varlen_attention(*x, cu, causal=True, rope=plan)
+        out.append([t[:T] for t in (o, *torch.autograd.grad(o, x, do[:n]))])
+    api.get_status()
+    for x, y, what in zip(*out, ("o", "dq", "dk", "dv")):
+        assert bool(torch.isfinite(y).all()) and torch.equal(x, y), what
