@@ -792,8 +792,9 @@ __global__ void __launch_bounds__(line_threads<MT, CC, MANY>(), 1)
                 const bool fine = is_fine(u);
                 float l = 0.f;
                 for (int w = 0; w < warps; ++w) l += sums[w * ROWS + r];
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                const float l2 = l > 0.f ? m_run[mt][hi] + log2f(l) : -INFINITY;
+                // (a row that is not a number stays one: its sum is neither above 0 nor 0)
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float l2 = l == 0.f ? -INFINITY : m_run[mt][hi] + log2f(l);
                 const int ur = u.rb * ROWS + r;  // row of the kv head's group
                 const size_t row = (static_cast<size_t>(max(u.b, 0)) * pb.Hkv + u.hk) * (u.b < 0 ? g.Rp : R) + ur;
                 float* dst = nullptr;
@@ -957,26 +958,33 @@ __global__ void __launch_bounds__(kJoinThreads, LOADS > 8 ? 2 : SCORE ? 4 : 3) j
         const int gg = r / pb.Nq, qi = r - gg * pb.Nq;
         uint16_t* out = static_cast<uint16_t*>(a.f.o) + b * pb.vo.sb + (hk * (pb.Hq / pb.Hkv) + gg) * pb.vo.sh + qi * pb.vo.sn;
         // Most rows have up to 32 pieces, a lane for each; more are taken in turn.
+        // A piece that is not a number counts in no maximum, but makes the sum one that is none.
         float top = -INFINITY, sum = 0.f, w0 = 0.f;
+        bool live = false;  // a piece has keys
         const float *l = nullptr, *o0 = nullptr;
         if (lane < pieces) {
             find(lane, l, o0);
-            top = w0 = *l;
+            w0 = *l;
+            top = fmaxf(top, w0);
+            live = w0 != -INFINITY;
         }
         for (int i = 32 + lane; i < pieces; i += 32) {
             const float* o;
             find(i, l, o);
             top = fmaxf(top, *l);
+            live = live || *l != -INFINITY;
         }
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        w0 = lane < pieces && top > -INFINITY ? exp2f(w0 - top) : 0.f;
+        live = __any_sync(0xffffffffu, live);
+        if (top == -INFINITY) top = 0.f;
+        w0 = lane < pieces ? exp2f(w0 - top) : 0.f;
         for (int c0 = part * 128; c0 < pb.D; c0 += parts * 128) {
             const int col = c0 + lane * 4;
             const bool mine = col < pb.D;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             sum = w0;
-            for (int p0 = 0; p0 < pieces && top > -INFINITY; p0 += 32) {
+            for (int p0 = 0; p0 < pieces && live; p0 += 32) {
                 const float* o = o0;
                 float w = w0;
                 if (p0) {
@@ -1012,12 +1020,12 @@ __global__ void __launch_bounds__(kJoinThreads, LOADS > 8 ? 2 : SCORE ? 4 : 3) j
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
             if (mine)
                 *reinterpret_cast<uint2*>(out + col) =
                     make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
         }
-        if (part == 0 && lane == 0) a.f.lse[row] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        if (part == 0 && lane == 0) a.f.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         return;
     }
     if constexpr (SCORE) {
@@ -1046,13 +1054,16 @@ __global__ void __launch_bounds__(kJoinThreads, LOADS > 8 ? 2 : SCORE ? 4 : 3) j
                 }
 #pragma unroll
                 for (int d = 4; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                if (!own.whole && mx > -INFINITY)
+                // (a piece that is not a number is in no maximum, and in the sum)
+                if (!own.whole) {
+                    if (mx == -INFINITY) mx = 0.f;
                     for (int k = lane & 7; k < own.count; k += 8)
                         sum += exp2f(g.l_cut[static_cast<size_t>(own.slot(k)) * g.rows + ur] - mx);
+                }
 #pragma unroll
                 for (int d = 4; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 // a row that saw no key adds nothing: all its scores are -inf
-                if ((lane & 7) == 0 && q < nr) row_l[q] = mx == -INFINITY ? 0.f : mx + log2f(sum);
+                if ((lane & 7) == 0 && q < nr) row_l[q] = mx == -INFINITY || sum == 0.f ? 0.f : mx + log2f(sum);
             }
             __syncthreads();
             // eight rows' scores in flight; rows past the last are read again and not added

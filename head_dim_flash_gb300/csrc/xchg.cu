@@ -852,7 +852,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             void* out;
             View ov;
             if (OP == XOP_FWD) {
-                mul = l_tot > 0.f ? 1.f / l_tot : 0.f;
+                // (a split's row that is not a number has to reach the join as one)
+                mul = l_tot > 0.f || (SPLIT && l_tot != 0.f) ? 1.f / l_tot : 0.f;
                 out = a.o;
                 ov = pb.vo;
             } else if (OP == XOP_DQ) {
@@ -951,7 +952,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (OP == XOP_FWD && c == 0 && half == 0 && row_ok) {
-                const float lse = l_tot > 0.f ? (m_ref + log2f(l_tot)) * (SPLIT ? 1.f : kLn2) : -INFINITY;
+                const float lse = l_tot > 0.f || (SPLIT && l_tot != 0.f)
+                                      ? (m_ref + log2f(l_tot)) * (SPLIT ? 1.f : kLn2)
+                                      : -INFINITY;
                 const size_t li = VARLEN ? static_cast<size_t>(h) * pb.total_q + tq0 + row
                                          : (static_cast<size_t>(b) * pb.Hq + h) * pb.Nq + row;
                 (SPLIT ? a.l_part : a.lse)[li] = lse;

@@ -354,6 +354,8 @@ FFPA_API ffpa_status ffpa_varlen_rope(ffpa_dtype dt, const void* q, const void* 
  * P is rounded to the input type (with up to eight rows per kv head, Hq / Hkv * Nq,
  * the rounding's remainder is kept, too, for the sequences' own keys, and for
  * the prefix if the whole batch has as few); sums and O up to its final rounding are fp32.
+ * A row with a score of NaN or +inf has NaN for its O, its LSE and the weights
+ * that it gives (ffpa_decode_fwd_weights); a row without keys has O = 0, LSE = -inf.
  * A length below 0 or above N records FFPA_ERR_INVALID_VALUE in the device
  * status word (ffpa_get_status) and the outputs of the call are undefined.
  */

@@ -94,6 +94,92 @@ def test_fp8_with_a_negative_scale(D):
     assert all(torch.equal(x, y) for x, y in zip(a, b)) and bool(torch.isfinite(a[1]).all())
 
 
+# ----------------------------------------------------------------- rows that are not numbers
+def is_nan(x):
+    return bool(torch.isnan(x).all())
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("B,H,G,Nq,D,Np,N", [
+    (2, 2, 4, 1, 512, 0, 60),       # whole units
+    (2, 2, 4, 1, 512, 40, 5000),    # units that ranges cut
+    (2, 1, 8, 4, 320, 40, 5000),
+    (1, 1, 4, 1, 512, 40000, 5),    # more pieces of a row than a warp has lanes
+    (5, 8, 4, 1, 512, 3000, 30),    # the tensor cores: one CTA per slab
+    (11, 2, 4, 3, 512, 2177, 4),    # pairs
+    (30, 2, 2, 3, 128, 1665, 9)])
+def test_shared_rows_that_are_not_numbers(bad, B, H, G, Nq, D, Np, N):
+    """A query that is not a number, then one key of the prefix or of a cache."""
+    g = gen(46)
+    q = randn(g, B, H * G, Nq, D, dtype=torch.bfloat16)
+    k, v = (randn(g, B, H, N, D, dtype=torch.bfloat16) for _ in range(2))
+    kp, vp = (randn(g, 1, H, Np, D, dtype=torch.bfloat16) for _ in range(2))
+    q0 = q.clone()
+    q0[B - 1, 1, 0, 5] = bad
+    if math.isinf(bad):  # +inf against keys of both signs: some scores are +inf
+        q0[B - 1, 1, 0, 5:7] = bad
+    o, lse = ffpa.decode_fwd_shared(q0, kp, vp, k, v)
+    api.get_status()
+    assert is_nan(o[B - 1, 1, 0]) and is_nan(lse[B - 1, 1, 0])
+    ref = [reference(q[b], k[b], v[b], row_ends(Np + N, Nq, False), kp[0], vp[0]) for b in range(B)]
+
+    def others(o, lse, there):
+        for b in range(B):
+            at = there[b]
+            x = [y.clone() for y in (o[b], lse[b])]
+            for y, z in zip(x, ref[b]):
+                y[at] = z[at].to(y.dtype)  # (not compared)
+            check_decode(*x, ref[b], f"sequence {b}")
+
+    hit = torch.zeros((B, H * G, Nq), dtype=torch.bool, device="cuda")
+    hit[B - 1, 1, 0] = True
+    others(o, lse, hit)
+    # one key of the prefix: every row of its head; one of a sequence's own: its rows
+    for own in (False, True):
+        if not own and Np == 0:
+            continue
+        k1, kp1 = k.clone(), kp.clone()
+        hit = torch.zeros((B, H * G, Nq), dtype=torch.bool, device="cuda")
+        if own:
+            k1[0, H - 1, N // 2, 9] = math.nan
+            hit[0, (H - 1) * G:] = True
+        else:
+            kp1[0, H - 1, Np // 2, 9] = math.nan
+            hit[:, (H - 1) * G:] = True
+        o, lse = ffpa.decode_fwd_shared(q, kp1, vp, k1, v)
+        api.get_status()
+        assert is_nan(o[hit]) and is_nan(lse[hit])
+        others(o, lse, hit)
+
+
+@pytest.mark.parametrize("G,Nq,D,N", [(4, 1, 512, 60), (4, 1, 512, 9000), (8, 3, 320, 60), (8, 3, 320, 9000),
+                                      (4, 4, 64, 9000)])
+def test_weights_of_rows_that_are_not_numbers(G, Nq, D, N):
+    g = gen(47)
+    q = randn(g, 2, 2 * G, Nq, D, dtype=torch.float16)
+    k, v = (randn(g, 2, 2, N, D, dtype=torch.float16) for _ in range(2))
+    for what in ("query", "key"):
+        q0, k0 = q.clone(), k.clone()
+        if what == "query":
+            q0[1, 0, 0, 3] = math.nan
+        else:
+            k0[1, 0, N - 2, 3] = math.nan
+        w = torch.zeros((2, 2, N), device="cuda")
+        o, lse, _ = ffpa.decode_fwd_weights(q0, k0, v, w)
+        api.get_status()
+        hit = torch.zeros((2, 2 * G, Nq), dtype=torch.bool, device="cuda")
+        if what == "query":
+            hit[1, 0, 0] = True
+        else:
+            hit[1, :G] = True
+        assert is_nan(o[hit]) and is_nan(lse[hit]) and is_nan(w[1, 0])
+        assert not bool(torch.isnan(o[~hit]).any()) and bool(torch.isfinite(lse[~hit]).all())
+        for b, h in ((0, 0), (0, 1), (1, 1)):
+            ref = reference(q[b, h * G:(h + 1) * G], k[b, h:h + 1], v[b, h:h + 1], row_ends(N, Nq, False))
+            check_decode(o[b, h * G:(h + 1) * G], lse[b, h * G:(h + 1) * G], ref, f"{what} {b} {h}")
+            within(w[b, h], ref[2][0], (2 * ref[4] + 2.0 ** -18) * ref[2][0] + 2.0 ** -23 * ref[2][0], f"weights {b} {h}")
+
+
 # ----------------------------------------------------------------- rotary positions
 def left_behind(shape, dtype):
     """The allocator's next block of this size holds NaN."""
