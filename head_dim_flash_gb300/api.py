@@ -25,6 +25,7 @@ import functools
 import math
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _ffi
 
@@ -959,6 +960,11 @@ class _Rope(torch.autograd.Function):
 
 
 def _needs_grad(q, k) -> bool:
+    # a tensor with a forward-mode tangent need not require a gradient (the level is -1 outside of that mode;
+    # without that private name the tensors are asked)
+    if getattr(forward_ad, "_current_level", 0) >= 0 and \
+            any(x is not None and forward_ad.unpack_dual(x).tangent is not None for x in (q, k)):
+        raise NotImplementedError("rotary positions have no forward-mode derivative")
     return torch.is_grad_enabled() and (q.requires_grad or k is not None and k.requires_grad)
 
 

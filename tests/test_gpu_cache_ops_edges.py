@@ -233,3 +233,20 @@ def test_packed_attention_with_a_plan_and_padding(D):
     api.get_status()
     for x, y, what in zip(*out, ("o", "dq", "dk", "dv")):
         assert bool(torch.isfinite(y).all()) and torch.equal(x, y), what
+
+
+def test_forward_mode_is_refused():
+    g = gen(50)
+    plan = ffpa.rope_plan(64)
+    q, k = randn(g, 1, 4, 9, 64, dtype=torch.bfloat16), randn(g, 1, 2, 9, 64, dtype=torch.bfloat16)
+    plain = ffpa.rope(q, k, plan)
+    with forward_ad.dual_level():
+        dual = [forward_ad.make_dual(x, torch.ones_like(x)) for x in (q, k)]
+        for call in (lambda: ffpa.rope(dual[0], k, plan), lambda: ffpa.rope(q, dual[1], plan),
+                     lambda: ffpa.rope(dual[0], None, plan), lambda: ffpa.attention(dual[0], k, k, rope=plan),
+                     lambda: ffpa.varlen_rope(q[0], dual[1][0], plan, ints(0, 4)),
+                     lambda: ffpa.varlen_attention(dual[0][0], dual[1][0], k[0], ints(0, 4), rope=plan)):
+            with pytest.raises(RuntimeError):
+                call()
+        y = ffpa.rope(q, k, plan)  # tensors without a tangent
+    assert all(torch.equal(a, b) for a, b in zip(y, plain))
