@@ -1181,8 +1181,10 @@ def kv_evict(k, v, weights, lens, keep: int, recent: int = 0, k_out=None, v_out=
         lens_out = lens if in_place else torch.empty_like(lens)
     pw = _weights_ptr(weights, (B, Hkv, N), "weights", dev)
     po = _weights_ptr(weights_out, (B, Hkv, Nout), "weights_out", dev)
-    if keep < 1:
-        raise ValueError(f"keep={keep} must be positive")
+    if keep < 1 or not 0 <= recent <= keep:
+        raise ValueError(f"keep={keep} must be positive and recent={recent} in [0, keep]")
+    if keep > 0x7fffffff - 4096:
+        raise NotImplementedError(f"keep={keep} is limited to {0x7fffffff - 4096} tokens")
     kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev)
     st = _ffi.load().ffpa_kv_evict(dt, wk, wv, pw, _lengths(lens, B, "lens", dev), wok, wov, po,
                                    _lengths(lens_out, B, "lens_out", dev), kept.data_ptr(), B, Hkv, N, Nout, D,

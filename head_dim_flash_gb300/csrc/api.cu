@@ -839,8 +839,9 @@ ffpa_status check_line(ffpa_dtype dt, const ffpa_view& q, const ffpa_view& k, co
     FFPA_TRY(check_dense_sizes(B, Hq, Nq, N));
     if (D % 64 != 0) return fail(FFPA_ERR_NOT_SUPPORTED, "decode path: D=%d must be a multiple of 64", D);
     if (Np < 0) return fail(FFPA_ERR_INVALID_VALUE, "negative prefix length %d", Np);
-    if (static_cast<long long>(Np) + N > INT_MAX)
-        return fail(FFPA_ERR_NOT_SUPPORTED, "prefix and cache hold %lld keys, above 2^31 - 1", static_cast<long long>(Np) + N);
+    if (static_cast<long long>(Np) + N > ffpa::kMaxTokens)
+        return fail(FFPA_ERR_NOT_SUPPORTED, "prefix and cache hold %lld keys, above %d", static_cast<long long>(Np) + N,
+                    ffpa::kMaxTokens);
     const long q_rows = static_cast<long>(B) * Hq * Nq;
     a->f.pb = dense_problem(B, Hq, Hkv, Nq, N, D, causal, scale);
     if (q_rows > 0 && !ffpa::line_fits(a->f.pb, shared, Np))
@@ -887,7 +888,7 @@ ffpa_status run_line(ffpa::LineArgs& a, void* workspace, size_t workspace_bytes,
 bool line_sizes_ok(ffpa_dtype dt, int B, int Hq, int Hkv, int Nq, int N, int D, int Np)
 {
     return (dt == FFPA_BF16 || dt == FFPA_FP16) && B > 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && Nq > 0 && N >= 0 &&
-           Np >= 0 && D >= 64 && D <= 1024 && D % 64 == 0;
+           Np >= 0 && static_cast<long long>(Np) + N <= ffpa::kMaxTokens && D >= 64 && D <= 1024 && D % 64 == 0;
 }
 
 }  // namespace
@@ -970,6 +971,8 @@ ffpa_status ffpa_kv_evict(ffpa_dtype dt, ffpa_view k, ffpa_view v, const float* 
     if (B < 0 || N < 0 || N_out < 0) return fail(FFPA_ERR_INVALID_VALUE, "negative size B=%d N=%d N_out=%d", B, N, N_out);
     if (keep < 1 || recent < 0 || recent > keep)
         return fail(FFPA_ERR_INVALID_VALUE, "keep=%d must be positive and recent=%d in [0, keep]", keep, recent);
+    if (N > ffpa::kMaxTokens || keep > ffpa::kMaxTokens)
+        return fail(FFPA_ERR_NOT_SUPPORTED, "N=%d and keep=%d are limited to %d tokens", N, keep, ffpa::kMaxTokens);
     if (N_out < (keep < N ? keep : N))
         return fail(FFPA_ERR_INVALID_VALUE, "N_out=%d does not hold min(keep=%d, N=%d) tokens", N_out, keep, N);
     if (static_cast<long long>(B) * Hkv > INT_MAX / 2)

@@ -10,6 +10,10 @@ namespace ffpa {
 // Sites of a sequence whose length lies outside its cache, in the device status word.
 enum : uint32_t { VS_LINE = 0x7b, VS_EVICT = 0x7c };
 
+// Tokens that a cache and its prefix may hold, or an eviction keep: the kernels'
+// indexes, up to a block of 4096 past the last token, stay within 31 bits.
+constexpr int kMaxTokens = 0x7fffffff - 4096;
+
 // Rotary positions of q and k (k absent: Hk = 0), or their inverse.
 struct RopeArgs {
     int bf16;

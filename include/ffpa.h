@@ -347,7 +347,7 @@ FFPA_API ffpa_status ffpa_varlen_rope(ffpa_dtype dt, const void* q, const void* 
  *   q, o: [B, Hq, Nq, D] views (o may be q's own); k_prefix, v_prefix:
  *   [1, Hkv, Np, D] views (stride_b unused); k, v: [B, Hkv, N, D] views, whose
  *   rows at and past lens[b] may hold anything; lse: contiguous fp32 [B, Hq, Nq].
- *   D: a multiple of 64 in [64, 1024].
+ *   D: a multiple of 64 in [64, 1024]; Np + N at most 2^31 - 4097.
  *   workspace: device scratch of at least ffpa_decode_shared_workspace_bytes()
  *   bytes, 256-byte aligned, sized on the current device; one call at a time
  *   per workspace. The query returns 0 for sizes outside the operation.
@@ -394,7 +394,8 @@ FFPA_API ffpa_status ffpa_decode_fwd_weights(ffpa_dtype dt, ffpa_view q, ffpa_vi
  *   inputs' own (in place) or none overlaps any input.
  *   lens_out: device int32 [B], min(lens[b], keep); may be lens.
  *   kept: device int32 [B, Hkv, keep], where each kept token was; -1 behind the last.
- *   D: a multiple of 32 in [64, 1024]; keep >= 1; 0 <= recent <= keep.
+ *   D: a multiple of 32 in [64, 1024]; keep >= 1; 0 <= recent <= keep; N and
+ *   keep at most 2^31 - 4097.
  * A length below 0 or above N records FFPA_ERR_INVALID_VALUE in the device
  * status word; the outputs of that sequence are undefined.
  */

@@ -20,6 +20,35 @@ def test_unknown_flags_of_packed_positions(lib):  # noqa: F811
         assert call(flags, 0) == 0  # no tokens
 
 
+def test_token_counts_near_31_bits(lib):  # noqa: F811
+    """Indexes run a block past the last token: 2^31 - 4097 tokens are the most."""
+    most = 2 ** 31 - 4097
+    for fn in (shared, weigh):
+        assert fn(lib, N=2 ** 31 - 1, **(dict(Np=0) if fn is shared else {})) == 2
+        assert "keys" in lib.ffpa_last_error().decode()
+    for N, Np in ((most, 1), (1, most), (2 ** 30, 2 ** 30)):
+        assert shared(lib, N=N, Np=Np) == 2 and "keys" in lib.ffpa_last_error().decode()
+        assert lib.ffpa_decode_shared_workspace_bytes(0, 1, 1, 1, 1, Np, N, 64) == 0
+    assert lib.ffpa_decode_weights_workspace_bytes(0, 1, 1, 1, 1, most + 1, 64) == 0
+    assert lib.ffpa_decode_weights_workspace_bytes(0, 1, 1, 1, 1, most, 64) >= 4 * most
+    for kw in (dict(N=2 ** 31 - 1, Nout=2 ** 31 - 1), dict(N=most + 1), dict(keep=2 ** 31 - 1), dict(keep=most + 1)):
+        assert evict(lib, **kw) == 2 and "tokens" in lib.ffpa_last_error().decode()
+    # within them, the next check speaks
+    assert evict(lib, N=most, Nout=10, keep=most) == 1 and "N_out" in lib.ffpa_last_error().decode()
+
+
+def test_what_an_eviction_keeps_is_checked_before_it_is_allocated(monkeypatch):
+    k, w, n = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16), torch.zeros(1, 2, 4), torch.zeros(1).int()
+    monkeypatch.setattr(api, "_evict_layout", lambda *a: (torch.device("cpu"), 0, 0, ((512, 256, 64),) * 2))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for keep, recent in ((0, 0), (4, 5), (4, -1), (4, 2 ** 32), (-3, 0)):
+        with pytest.raises(ValueError, match="keep"):
+            api.kv_evict(k, k.clone(), w, n, keep, recent)
+    for keep in (2 ** 31 - 1, 2 ** 31 - 4096, 2 ** 33):
+        with pytest.raises(NotImplementedError, match="keep"):
+            api.kv_evict(k, k.clone(), w, n, keep)
+
+
 def test_forward_mode_is_refused(monkeypatch):
     """A tangent is not dropped, whether or not a gradient is wanted."""
     def launched(*args):
