@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a)
 {
     pdl_wait();
     pdl_trigger();
-    __shared__ float2 table[kRopePairs];  // [token][pair % 8 / 2][unit][pair % 2]
+    __shared__ __align__(16) float2 table[kRopePairs];  // [token][pair % 8 / 2][unit][pair % 2], read by two
     __shared__ RopeToken tok[kRopeTokens];
     const int tid = threadIdx.x;
     const long long T = a.cu ? a.total : static_cast<long long>(a.B) * a.N;
