@@ -14,6 +14,61 @@ from tests.test_gpu_cache_ops import DT, caches, check_decode, gen, ints, kept_r
 pytestmark = pytest.mark.gpu
 
 
+# ----------------------------------------------------------------- the prefix on the tensor cores
+SPLIT = [  # B, Hkv, G, Nq, D, Np, N, lens
+    # one CTA per row tile
+    (40, 2, 2, 1, 64, 4225, 5, (0, 5, 1, 2) * 10),
+    (30, 2, 2, 3, 128, 1665, 9, (0, 1, 2, 3, 9) * 6),
+    (1, 1, 1, 1500, 192, 1100, 0, (0,)),
+    # clusters of two, whole and unequal slabs, 128 rows and fewer of them
+    (20, 2, 4, 4, 320, 1025, 6, (0, 1, 2, 3, 4) * 4),
+    (3, 1, 2, 300, 320, 1153, 40, (0, 40, 7)),
+    (1, 1, 2, 1300, 320, 1200, 3, (3,)),
+    (9, 4, 4, 2, 448, 1985, 3, (0, 1, 3) * 3),
+    (8, 4, 4, 4, 512, 1281, 5, (0, 1, 2, 3, 5, 4, 0, 1)),
+    (5, 8, 4, 1, 512, 3000, 30, (0, 30, 1, 16, 17)),
+    # pairs
+    (11, 2, 4, 3, 512, 2177, 4, (0, 1, 2, 4, 3, 0, 1, 2, 4, 3, 0)),
+    (26, 2, 4, 3, 512, 1281, 2, (0, 1) * 13),
+    (1, 1, 2, 1300, 512, 1200, 3, (3,)),
+    # clusters of three and four
+    (12, 2, 4, 3, 576, 2177, 4, (0, 1, 2, 4) * 3),
+    (17, 2, 4, 3, 640, 1537, 3, (3,) + (0, 1, 2, 3) * 4),
+    (17, 2, 4, 3, 768, 1537, 3, (3,) + (0, 1, 2, 3) * 4),
+    (1, 1, 1, 700, 768, 1025, 0, (0,)),
+    (12, 2, 4, 3, 832, 2177, 4, (0, 1, 2, 4) * 3),
+    (12, 2, 4, 3, 1024, 2177, 4, (0, 1, 2, 4) * 3),
+    (1, 1, 1, 700, 1024, 1025, 2, (2,)),
+]
+
+
+def split_taken(B, H, G, Nq, D, Np, N):
+    """The scratch of a prefix in the line does not depend on its length; the tensor cores' parts need their own."""
+    from head_dim_flash_gb300 import _ffi
+
+    return _ffi.load().ffpa_decode_shared_workspace_bytes(0, B, H * G, H, Nq, Np, N, D) != \
+        _ffi.load().ffpa_decode_shared_workspace_bytes(0, B, H * G, H, Nq, 1, N, D)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B,H,G,Nq,D,Np,N,lens", SPLIT)
+def test_shared_prefix_on_the_tensor_cores(dt, causal, B, H, G, Nq, D, Np, N, lens):
+    """Causal limits inside the prefix, on both sides of a tile's border, before whole splits, at no key at all."""
+    assert split_taken(B, H, G, Nq, D, Np, N) and len(lens) == B
+    g = gen(40)
+    q = randn(g, B, Nq, H * G, D, dtype=DT[dt]).transpose(1, 2)
+    k, v = caches(g, B, H, N, D, DT[dt], lens)
+    kp, vp = (randn(g, 1, Np, H, D, dtype=DT[dt]).transpose(1, 2) for _ in range(2))
+    o, lse = ffpa.decode_fwd_shared(q, kp, vp, k, v, ints(*lens), causal=causal)
+    api.get_status()
+    for b, n in enumerate(lens):
+        ref = reference(q[b], k[b, :, :n], v[b, :, :n], row_ends(Np + n, Nq, causal), kp[0], vp[0])
+        check_decode(o[b], lse[b], ref, f"sequence {b}")
+    again = ffpa.decode_fwd_shared(q, kp, vp, k, v, ints(*lens), causal=causal, out=q)
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
 # ----------------------------------------------------------------- scales below zero
 # softmax(-s q k) is softmax(s (-q) k); products, sums and roundings are the same but for their signs
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
@@ -67,7 +122,7 @@ def test_attention_with_a_negative_scale(dt, causal, B, H, G, Nq, Nkv, D):
         out.append((o, lse, *torch.autograd.grad(o, (q, k, v), do)))
     api.get_status()
     for b in range(B):
-        ref = reference(-q[b], k[b], v[b], row_ends(Nkv, Nq, causal))
+        ref = reference(-q.detach()[b], k.detach()[b], v.detach()[b], row_ends(Nkv, Nq, causal))
         check_decode(out[0][0][b], out[0][1][b], ref, f"entry {b}")
     for x, y, what in zip(*out, ("o", "lse", "dq", "dk", "dv")):
         assert torch.equal(x, y), what
@@ -250,3 +305,25 @@ def test_forward_mode_is_refused():
                 call()
         y = ffpa.rope(q, k, plan)  # tensors without a tangent
     assert all(torch.equal(a, b) for a, b in zip(y, plain))
+
+
+# ----------------------------------------------------------------- eviction
+@pytest.mark.parametrize("D", [64, 96])
+def test_evict_in_place_of_narrow_heads(D):
+    """More kv heads than SMs: slices of 64 head dims, 256 rows a batch and several batches."""
+    g = gen(51)
+    B, H, N, keep, recent = 16, 8, 1500, 701, 30
+    lens = [1500 - 53 * i for i in range(B)]
+    k, v = (randn(g, B, N, H, D, dtype=torch.bfloat16).transpose(1, 2) for _ in range(2))
+    w = torch.rand((B, H, N), generator=g, device="cuda")
+    k0, v0, w0 = k.clone(), v.clone(), w.cpu()
+    n = ints(*lens)
+    *_, kept = ffpa.kv_evict(k, v, w, n, keep, recent)
+    api.get_status()
+    assert n.tolist() == [min(x, keep) for x in lens]
+    for b in range(B):
+        for h in range(H):
+            rows = kept_rows(w0[b, h].tolist(), lens[b], keep, recent)
+            assert kept[b, h].tolist() == rows
+            for x, x0 in ((k, k0), (v, v0)):
+                assert torch.equal(x[b, h, :keep], x0[b, h, rows]) and torch.equal(x[b, h, keep:], x0[b, h, keep:])
