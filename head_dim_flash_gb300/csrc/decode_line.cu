@@ -93,7 +93,7 @@ bool line_fits(const Problem& pb, bool shared, int Np)
 {
     const long long R = static_cast<long long>(pb.Hq / pb.Hkv) * pb.Nq;
     if (R * pb.B > 0x7fffffffLL) return false;
-    // rows are joined by a CTA each; key tiles of a range are counted in 31 bits
+    // a row is joined by up to eight warps, numbered in 32 bits; key tiles of a range are counted in 31
     const long long units = static_cast<long long>(pb.B) * pb.Hkv * ((R + 15) / 16);
     const long long tiles = units * (pb.Nkv / 16 + 1 + kUnitPlaces) +
         (shared ? static_cast<long long>(pb.Hkv) * ((R * pb.B + 15) / 16) * (Np / 16 + 1 + kUnitPlaces) : 0);

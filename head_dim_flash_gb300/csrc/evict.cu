@@ -16,9 +16,10 @@
 // heads cut from 16384 to 8192 tokens, D = 512, 2.1 GB: 312 us, 6.7 TB/s, a copy's
 // rate). Out of place its CTAs take pieces of the kept tokens. In place a row moves
 // to where an earlier one was: a CTA owns 64 to 256 head dims of one tensor's kv
-// head and takes all its tokens in order, a batch read whole before it is written.
-// A batch's targets lie at or below its own first source and below every later
-// one's, so the next batch may already be on its way.
+// head and takes all its tokens in order. Sources ascend and none lies below its
+// target, so a batch's targets may be sources of its own, and are no later batch's:
+// a barrier stands between a batch's reads and its writes, and the next batch may
+// already be on its way.
 #include "cache_ops.h"
 #include "kv4.cuh"
 

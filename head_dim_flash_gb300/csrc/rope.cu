@@ -4,9 +4,10 @@
 // by position * theta_p: (x, y) -> m (x cos - y sin, x sin + y cos). A turn is
 // all that matters, so theta_p is kept as turns per position in 64-bit
 // fixed point (units of 2^-64): position * turns, wrapped, is the angle's
-// fraction of a turn, exact to 2^-33 for every 32-bit position, where an fp32
-// product at position 10^6 is off by a thirtieth of a radian. sin and cos of
-// the fraction are fp32, so are the products; one rounding at the end.
+// fraction of a turn within 2^-33 for every 32-bit position, where an fp32
+// product at position 10^6 is off by a thirtieth of a radian. Its upper 32 bits
+// become an fp32 (within 2^-26 turns); sin, cos and the products are fp32, too;
+// one rounding at the end.
 //
 // One pass, bound by memory: each value is read and written once. A CTA takes
 // a few tokens and the heads of both tensors; their cos and sin are computed

@@ -307,8 +307,9 @@ FFPA_API ffpa_status ffpa_decode_fwd_kv4(ffpa_dtype dt, ffpa_view q, ffpa_kv4_ca
  *   (x, y) -> mscale * (x cos - y sin, x sin + y cos);
  * pairs are (p, p + rot_dim / 2), or (2p, 2p + 1) when interleaved; the other
  * dims are copied. theta_p is given as turns[p] = round(theta_p / 2 pi * 2^64)
- * (mod 2^64; device memory, rot_dim / 2 entries), so that the angle of every
- * 32-bit position is exact to 2^-33 turns. sin, cos and the products are fp32.
+ * (mod 2^64; device memory, rot_dim / 2 entries), so that position * theta_p less
+ * whole turns is within 2^-33 turns for every 32-bit position; the angle is then
+ * an fp32 (within 2^-25 turns in all), as are sin, cos and the products.
  * rot_dim: a multiple of 16 in [16, D]; D: a multiple of 32 in [64, 1024].
  */
 typedef struct ffpa_rope_plan {
