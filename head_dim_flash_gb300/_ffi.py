@@ -312,34 +312,6 @@ def ffpa_decode_fwd_kv4(*args):
     return load().ffpa_decode_fwd_kv4(*args)
 
 
-def ffpa_rope(*args):
-    return load().ffpa_rope(*args)
-
-
-def ffpa_varlen_rope(*args):
-    return load().ffpa_varlen_rope(*args)
-
-
-def ffpa_decode_shared_workspace_bytes(*args):
-    return load().ffpa_decode_shared_workspace_bytes(*args)
-
-
-def ffpa_decode_fwd_shared(*args):
-    return load().ffpa_decode_fwd_shared(*args)
-
-
-def ffpa_decode_weights_workspace_bytes(*args):
-    return load().ffpa_decode_weights_workspace_bytes(*args)
-
-
-def ffpa_decode_fwd_weights(*args):
-    return load().ffpa_decode_fwd_weights(*args)
-
-
-def ffpa_kv_evict(*args):
-    return load().ffpa_kv_evict(*args)
-
-
 def ffpa_bwd_workspace_bytes(*args):
     return load().ffpa_bwd_workspace_bytes(*args)
 
