@@ -1103,7 +1103,8 @@ def decode_fwd_weights(q, k, v, weights, lens=None, causal: bool = False, scale:
     """Decode / short-query forward that scores its cache, through ffpa_decode_fwd_weights: the keys
     of sequence b are the first lens[b] rows of k, v [B, Hkv, N, D] (int32 [B] on the device, None:
     N each), and the softmax weight that each gets from the rows of its kv head is added to
-    weights [B, Hkv, N] (fp32), in place or into weights_out. q [B, Hq, Nq, D]; returns
+    weights [B, Hkv, N] (fp32), in place or into weights_out. The caller sets a new token's entry
+    (to zero) when it enters the cache: kv_evict leaves old weights behind the kept tokens. q [B, Hq, Nq, D]; returns
     (o, lse, weights_out)."""
     dev, index, dt, views, like = _line_layout(_meta(q), (_meta(k), _meta(v), True))
     if index != torch.cuda.current_device():

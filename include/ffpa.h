@@ -373,7 +373,9 @@ FFPA_API ffpa_status ffpa_decode_fwd_shared(ffpa_dtype dt, ffpa_view q, ffpa_vie
  *   weights_out[b, h, j] = weights[b, h, j] + sum over the rows of kv head h's
  *                          group of softmax weight (row, j),  j < lens[b]
  * (fp32 [B, Hkv, N] contiguous, 16-byte aligned; weights_out may be weights).
- * Entries at and past lens[b] keep what they hold. The order of the sum is
+ * Entries at and past lens[b] keep what they hold: a token that enters the cache
+ * needs its entry set (to zero), above all behind an eviction in place, which
+ * leaves old weights behind the kept tokens. The order of the sum is
  * fixed. Other arguments and the checks as for ffpa_decode_fwd_shared. The
  * workspace holds the scores: 4 bytes per query row and cached token.
  */
