@@ -111,10 +111,10 @@ struct XArgs {
     int splits, split_keys, split_rows, split_nq, split_causal, split_most;
     const int* split_lens;             // device, null: split_most each
     float *o_part, *l_part;
-    // Set by the launch of a forward with a negative scale: Q's signs are turned in
-    // Q K^T, and the kernel has the scale's magnitude, so that the largest X of a row
-    // has the largest score.
-    int turn_q;
+    // Set by the launch of a forward with a negative scale: the instruction
+    // descriptor's bit that turns Q's signs in Q K^T. The kernel has the scale's
+    // magnitude, so that the largest X of a row has the largest score.
+    uint32_t turn_q;
 };
 
 // The GEMMs over the tiles the dK kernel stored (dense, D a multiple of 64 up to 1024;

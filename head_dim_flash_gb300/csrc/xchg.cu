@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------ MMA issuer
         if (elect_one()) {
             const uint32_t idesc_s =
-                idesc_f16(128, 128, BF16, false, false) | (OP == XOP_FWD && a.turn_q ? kIdescNegateA : 0u);
+                idesc_f16(128, 128, BF16, false, false) | (OP == XOP_FWD ? a.turn_q : 0u);
             const uint32_t idesc_v = idesc_f16(128, sw, BF16, false, true);
             RingPos rp;
             bool ok = true;
@@ -1020,7 +1020,7 @@ cudaError_t launch_single(int op, const XArgs& args, cudaStream_t s)
     XArgs a = args;
     const Problem& pb = a.pb;
     if (op == XOP_FWD && pb.scale_log2 < 0.f) {
-        a.turn_q = 1;
+        a.turn_q = kIdescNegateA;
         a.pb.scale_log2 = -a.pb.scale_log2;
     }
     const bool q_empty = q_side_empty(pb), kv_empty = kv_side_empty(pb);

@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) {
                 // (F8: format code 0 = e4m3 in both operand fields; V^T is K-major)
                 const uint32_t idesc_s =
-                    idesc_f16(256, 128, F8 ? false : BF16, false, false) | (OP == XOP_FWD && a.turn_q ? kIdescNegateA : 0u);
+                    idesc_f16(256, 128, F8 ? false : BF16, false, false) | (OP == XOP_FWD ? a.turn_q : 0u);
                 const uint32_t idesc_v = idesc_f16(256, sw, F8 ? false : BF16, false, !F8);
                 auto mma = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
                     if constexpr (F8)
@@ -1290,7 +1290,7 @@ cudaError_t launch_pair(int op, const XArgs& args, cudaStream_t s)
     XArgs a = args;
     const Problem& pb = a.pb;
     if (op == XOP_FWD && pb.scale_log2 < 0.f) {
-        a.turn_q = 1;
+        a.turn_q = kIdescNegateA;
         a.pb.scale_log2 = -a.pb.scale_log2;
     }
     const bool q_empty = q_side_empty(pb), kv_empty = kv_side_empty(pb);
